@@ -164,9 +164,9 @@ def _encode(v, keep_sign=False):
     blocks = -(-d // BLOCK)
     padded = torch.nn.functional.pad(v, (0, blocks * BLOCK - d)).view(m, blocks, BLOCK)
     top = padded.abs().amax(2, keepdim=True)
-    scale = (((top.view(torch.int32) + 0x10000) >> 23) - 6).clamp(min=0)
+    scale = (((top.view(torch.int32) + 0x10000) >> 23) - 6).clamp(0, 248)
     bad = ~torch.isfinite(top)
-    q = torch.round(padded * ((254 - scale) << 23).view(torch.float32))
+    q = torch.round(padded * ((254 - scale) << 23).view(torch.float32)).clamp(-127, 127)
     if keep_sign:
         q = torch.where(padded > 0, q.clamp(min=1), q)
     q = torch.where(bad, torch.zeros_like(q), q)
@@ -378,9 +378,9 @@ def _round_to_block(v, keep_sign=False):
     top = b.abs().max(2, keepdim=True).values
     # top = f 2^e with f in [1/2, 1): f 2^7 < 128 is the first candidate's largest code
     f, e = torch.frexp(top)
-    k = torch.where(f * 128 >= 127.5, e - 6, e - 7).clamp(min=-127)
+    k = torch.where(f * 128 >= 127.5, e - 6, e - 7).clamp(-127, 121)
     step = _power(k)
-    q = (b / step).round()
+    q = (b / step).round().clamp(-127, 127)
     if keep_sign:
         q = torch.where((b > 0) & (q < 1), torch.ones_like(q), q)
     return (q * step).view(m, blocks * BLOCK)[:, :d]
