@@ -129,11 +129,15 @@ def _code_only(text: str) -> str:
     return re.sub(r"\s+", "", text)
 
 
+# what the step's kernels are compiled from
+STEP_SOURCES = ("api.cu", "common.cuh", "elementwise.cu", "gelu_and_mul_sparse.cu")
+
+
 def kernel_sources_hash() -> str:
-    """Hash of the library's CUDA/C++ code (comments and whitespace ignored)."""
+    """Hash of the step's CUDA/C++ code (comments and whitespace ignored)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "gated_activation_gb300", "csrc")
-    for f in sorted(os.listdir(csrc)):
+    for f in STEP_SOURCES:
         with open(os.path.join(csrc, f)) as fh:
             h.update(f.encode() + _code_only(fh.read()).encode())
     return h.hexdigest()[:16]

@@ -42,6 +42,11 @@ EXPORTED = (
     "squared_relu", "gelu_and_mul_sparse_workspace_bytes", "gelu_and_mul_sparse_ws",
     "gelu_and_mul_sparse_ws_static", "gated_act_selftest_wait_timeout_ws",
     "gated_act_selftest_wait_timeout_ex", "gelu_and_mul_sparse_native_plan",
+    "gated_act_checkpoint_scales", "silu_and_mul_checkpoint", "gelu_and_mul_checkpoint",
+    "gelu_and_mul_sparse_checkpoint", "silu_and_mul_backward", "gelu_and_mul_backward",
+    "gelu_and_mul_sparse_backward", "gated_act_checkpoint_values", "layer_norm",
+    "layer_norm_backward", "layer_norm_backward_workspace_bytes", "moe_balance_loss",
+    "moe_balance_loss_backward", "moe_balance_loss_workspace_bytes",
 )
 
 
@@ -137,6 +142,33 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.gelu_and_mul_sparse_ws_static.argtypes = [vp, cvp, i64, i64, i64, ctypes.c_double,
                                                   ctypes.c_int, ctypes.c_int, ctypes.c_int, vp]
     lib.gelu_and_mul_sparse_ws_static.restype = ctypes.c_int
+    # the training operators (gated_act_training.h)
+    c_int, f64, size = ctypes.c_int, ctypes.c_double, ctypes.c_size_t
+    for fn, restype, argtypes in (
+            ("gated_act_checkpoint_scales", i64, [i64]),
+            ("silu_and_mul_checkpoint", c_int, [vp, vp, vp, cvp, i64, i64, i64, c_int, cvp, vp]),
+            ("gelu_and_mul_checkpoint", c_int, [vp, vp, vp, cvp, i64, i64, i64, c_int, cvp, vp]),
+            ("gelu_and_mul_sparse_checkpoint", c_int,
+             [vp, vp, vp, vp, cvp, i64, i64, i64, f64, c_int, vp]),
+            ("silu_and_mul_backward", c_int,
+             [vp, vp, cvp, cvp, cvp, i64, i64, i64, c_int, cvp, vp]),
+            ("gelu_and_mul_backward", c_int,
+             [vp, vp, cvp, cvp, cvp, i64, i64, i64, c_int, cvp, vp]),
+            ("gelu_and_mul_sparse_backward", c_int,
+             [vp, vp, cvp, cvp, cvp, cvp, i64, i64, i64, f64, c_int, vp]),
+            ("gated_act_checkpoint_values", c_int, [vp, cvp, cvp, i64, i64, c_int, vp]),
+            ("layer_norm", c_int,
+             [vp, vp, vp, cvp, cvp, cvp, i64, i64, i64, f64, c_int, c_int, vp]),
+            ("layer_norm_backward_workspace_bytes", size, [i64, i64]),
+            ("layer_norm_backward", c_int,
+             [vp, vp, vp, cvp, cvp, cvp, cvp, cvp, i64, i64, i64, i64, c_int, c_int, vp, size, vp]),
+            ("moe_balance_loss_workspace_bytes", size, [i64, i64]),
+            ("moe_balance_loss", c_int,
+             [vp, vp, vp, vp, cvp, cvp, cvp, i64, i64, i64, i64, c_int, c_int, f64, vp, size, vp]),
+            ("moe_balance_loss_backward", c_int,
+             [vp, cvp, cvp, cvp, cvp, cvp, i64, i64, i64, i64, c_int, f64, vp])):
+        getattr(lib, fn).restype = restype
+        getattr(lib, fn).argtypes = argtypes
     if path is None:
         _lib = lib
     return lib
@@ -384,7 +416,10 @@ def squared_relu(x: torch.Tensor, out: torch.Tensor | None = None,
     return out
 
 
+from .training import *  # noqa: E402,F401,F403
+from .training import __all__ as _training_all  # noqa: E402
+
 __all__ = ["gelu_and_mul_sparse_native", "gelu_and_mul_sparse_native_plan", "silu_and_mul_bounded", "gelu_and_mul", "squared_relu", "gelu_and_mul_sparse", "gelu_and_mul_sparse_plan", "silu_and_mul", "device_status", "noop",
            "load_library",
            "status_string", "GatedActError", "Plan", "EXPORTED", "LIB_PATH", "workspace_bytes",
-           "new_workspace"]
+           "new_workspace"] + _training_all

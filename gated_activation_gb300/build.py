@@ -21,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libgated_act.so")
-SOURCES = ("api.cu", "gelu_and_mul_sparse.cu", "elementwise.cu")
+SOURCES = ("api.cu", "gelu_and_mul_sparse.cu", "elementwise.cu",
+           "training.cu", "checkpoint.cu", "layer_norm.cu", "balance.cu")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

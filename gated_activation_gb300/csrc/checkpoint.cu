@@ -1,0 +1,391 @@
+// 8-bit checkpoints of the gated activations, and the backward passes that
+// read them (definitions in gated_act_training.h).
+//
+// Each op reads and writes every byte once and computes a few dozen
+// instructions per element: HBM bandwidth bounds it.  Per gate/up pair of a
+// 16-bit type the forward pass moves 4 + 2 bytes of rows and 2 + 1/16 of
+// checkpoint, the backward pass 2 (+ 2 with the recomputed output) + 4 and
+// the same 2 + 1/16.
+//
+// Blocks: a block of the 8-bit format is 32 elements of one half.  The
+// any-layout kernels give a block of the gate half and the block of the up
+// half beside it to one warp, one element per lane, so every access of a warp
+// is one contiguous run whatever the alignment, and the block's largest
+// magnitude is one redux.
+#include <algorithm>
+
+#include "training.cuh"
+
+namespace gact {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+__device__ __forceinline__ int64_t live_rows(int64_t M, const int32_t *n_rows) {
+    if (!n_rows)
+        return M;
+    const int64_t n = *n_rows;
+    return n < 0 ? 0 : n > M ? M : n;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// One block of a half, one element per lane (`in`: the lane holds one): writes
+// its code and, from lane 0, the scale.
+template <bool KEEP_SIGN>
+__device__ __forceinline__ void put_block(int8_t *codes, uint8_t *scale, float v, bool in, int lane) {
+    const uint32_t s = scale_of(__reduce_max_sync(0xFFFFFFFFu, in ? abs_bits(v) : 0u));
+    if (s == kTopScale)
+        v = clamp_top(v);
+    int q = code_of(v, code_factor(s));
+    if (KEEP_SIGN && v > 0.f)
+        q = max(q, 1);
+    if (in)
+        *codes = static_cast<int8_t>(s == kBadScale ? 0 : q);
+    if (lane == 0)
+        *scale = static_cast<uint8_t>(s);
+}
+
+// ------------------------------------------------- elementwise, any layout
+
+template <class T, class Act>
+__global__ void __launch_bounds__(kThreads)
+ckpt_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
+                 const T *__restrict__ in, int64_t M, int64_t d, int64_t rs, int64_t B,
+                 const int32_t *n_rows) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t total = live_rows(M, n_rows) * B;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < total;
+         i += step) {
+        const int64_t r = i / B, b = i - r * B, c = b * kBlock + lane;
+        const bool ok = c < d;
+        const float g = ok ? to_float(in[r * rs + c]) : 0.f;
+        const float u = ok ? to_float(in[r * rs + d + c]) : 0.f;
+        if (ok)
+            out[r * d + c] = from_float<T>(act_mul<Act>(g, u));
+        put_block<false>(codes + r * 2 * d + c, scales + r * 2 * B + b, g, ok, lane);
+        put_block<false>(codes + r * 2 * d + d + c, scales + r * 2 * B + B + b, u, ok, lane);
+    }
+}
+
+template <class T, class Act>
+__global__ void __launch_bounds__(kThreads)
+ckpt_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
+                  const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t M,
+                  int64_t d, int64_t gs, int64_t B, const int32_t *n_rows) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t total = live_rows(M, n_rows) * B;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < total;
+         i += step) {
+        const int64_t r = i / B, b = i - r * B, c = b * kBlock + lane;
+        if (c >= d)
+            continue;
+        const float g = codes[r * 2 * d + c] * code_step(scales[r * 2 * B + b]);
+        const float u = codes[r * 2 * d + d + c] * code_step(scales[r * 2 * B + B + b]);
+        const float dy = to_float(grad[r * gs + c]);
+        const GateGrad m = act_grad<Act>(g, u, dy);
+        grad_in[r * 2 * d + c] = from_float<T>(m.gate);
+        grad_in[r * 2 * d + d + c] = from_float<T>(m.up);
+        if (out)
+            out[r * d + c] = from_float<T>(m.out);
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+ckpt_values_any(T *__restrict__ values, const int8_t *__restrict__ codes,
+                const uint8_t *__restrict__ scales, int64_t M, int64_t d, int64_t B) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t total = M * 2 * d, step = static_cast<int64_t>(gridDim.x) * kThreads;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
+         i += step) {
+        const int64_t h = i / d, c = i - h * d;   // h: half-row
+        values[i] = from_float<T>(codes[i] * code_step(scales[h * B + c / kBlock]));
+    }
+}
+
+// ------------------------------------------------------ sparse, any layout
+
+// Sum over the CTA, the same bits in every thread; red holds kWarps floats
+// and may be used again after the next barrier.
+__device__ __forceinline__ float cta_sum(float v, float *red) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float t = red[threadIdx.x & (kWarps - 1)];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1)
+        t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    return t;
+}
+
+// One CTA per row; the gate is read again (from L1/L2) for each pass.
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+sparse_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
+                   float *__restrict__ std_out, const T *__restrict__ in, int64_t rows, int64_t d,
+                   int64_t rs, int64_t B, float z) {
+    __shared__ float red[2][kWarps];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const T *g = in + r * rs;
+        float acc = 0.f;
+        for (int64_t c = threadIdx.x; c < d; c += kThreads)
+            acc += to_float(g[c]);
+        const float mean = cta_sum(acc, red[0]) / static_cast<float>(d);
+        acc = 0.f;
+        for (int64_t c = threadIdx.x; c < d; c += kThreads) {
+            const float e = to_float(g[c]) - mean;
+            acc = fmaf(e, e, acc);
+        }
+        const float std = __fsqrt_rn(cta_sum(acc, red[1]) / static_cast<float>(d));
+        const float cutoff = fmaf(std, z, mean);
+        if (threadIdx.x == 0)
+            std_out[r] = std;
+        for (int64_t b = warp; b < B; b += kWarps) {
+            const int64_t c = b * kBlock + lane;
+            const bool ok = c < d;
+            const float v = ok ? to_float(g[c]) - cutoff : 0.f;
+            const float u = ok ? to_float(g[d + c]) : 0.f;
+            if (ok)
+                out[r * d + c] = from_float<T>(gelu_mul(max_nan(v, 0.f), u));
+            put_block<true>(codes + r * 2 * d + c, scales + r * 2 * B + b, v, ok, lane);
+            put_block<false>(codes + r * 2 * d + d + c, scales + r * 2 * B + B + b, u, ok, lane);
+        }
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+sparse_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
+                    const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
+                    const float *__restrict__ std_in, int64_t rows, int64_t d, int64_t gs,
+                    int64_t B, float z) {
+    __shared__ float red[2][kWarps];
+    pdl_wait();
+    pdl_trigger();
+    int k = 0;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, k ^= 1) {
+        const float std = std_in[r];
+        const float inv = std == 0.f ? 0.f : z / std;
+        const int8_t *q = codes + r * 2 * d;
+        const uint8_t *sc = scales + r * 2 * B;
+        T *gi = grad_in + r * 2 * d;
+        float acc = 0.f;
+        for (int64_t c = threadIdx.x; c < d; c += kThreads) {
+            const float v = q[c] * code_step(sc[c / kBlock]);
+            const float u = q[d + c] * code_step(sc[B + c / kBlock]);
+            const float dy = to_float(grad[r * gs + c]);
+            const GateGrad m = sparse_grad(v, u, dy);
+            acc += m.gate;
+            gi[d + c] = from_float<T>(m.up);
+            if (out)
+                out[r * d + c] = from_float<T>(m.out);
+        }
+        const float mean_h = cta_sum(acc, red[k]) / static_cast<float>(d);
+        for (int64_t c = threadIdx.x; c < d; c += kThreads) {
+            const float v = q[c] * code_step(sc[c / kBlock]);
+            const float u = q[d + c] * code_step(sc[B + c / kBlock]);
+            const float dy = to_float(grad[r * gs + c]);
+            const float h = sparse_grad(v, u, dy).gate;
+            gi[c] = from_float<T>(fmaf(-mean_h, fmaf(inv, fmaf(z, std, v), 1.f), h));
+        }
+    }
+}
+
+// -------------------------------------------------------------- host side
+
+constexpr int64_t kMaxWidth = int64_t(1) << 30, kMaxRows = int64_t(1) << 40;
+
+int check_sizes(int64_t M, int64_t d, int64_t stride, int64_t width, int dtype) {
+    if (M < 0 || d <= 0)
+        return GATED_ACT_ERR_SIZE;
+    if (stride < width)
+        return GATED_ACT_ERR_STRIDE;
+    if (!elem_size(dtype))
+        return GATED_ACT_ERR_DTYPE;
+    if (d > kMaxWidth || M > kMaxRows || stride > kMaxRows ||
+        (M > 0 && std::max(stride, 2 * d) > (int64_t(1) << 60) / M))
+        return GATED_ACT_ERR_TOO_LARGE;
+    return GATED_ACT_OK;
+}
+
+dim3 grid_of(int64_t units, int64_t per_cta) {
+    // grid-stride kernels: at most 64 CTAs per SM
+    return dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div64(units, per_cta),
+                                                        int64_t(device_sm_count()) * 64)));
+}
+
+template <class Act>
+int forward(void *out, int8_t *codes, uint8_t *scales, const void *in, int64_t M, int64_t d,
+            int64_t rs, int dtype, const int32_t *n_rows, cudaStream_t stream) {
+    int rc = check_sizes(M, d, rs, 2 * d, dtype);
+    if (rc != GATED_ACT_OK || M == 0)
+        return rc;
+    const int64_t B = ceil_div64(d, kBlock), size = elem_size(dtype);
+    Region r[5] = {{out, static_cast<uint64_t>(M * d * size), uintptr_t(size), true},
+                   {codes, static_cast<uint64_t>(M * 2 * d), 1, true},
+                   {scales, static_cast<uint64_t>(M * 2 * B), 1, true},
+                   {in, span_bytes(M, rs, 2 * d, size), uintptr_t(size), false},
+                   {n_rows, n_rows ? 4u : 0u, 4, false}};
+    if ((rc = check_regions(r, 5)) != GATED_ACT_OK)
+        return rc;
+    return with_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        return launched(launch_kernel(ckpt_forward_any<T, Act>, grid_of(M * B, kWarps),
+                                      dim3(kThreads), 0, stream, 1, as<T>(r[0]), as<int8_t>(r[1]),
+                                      as<uint8_t>(r[2]), as<const T>(r[3]), M, d, rs, B,
+                                      as<const int32_t>(r[4])));
+    });
+}
+
+template <class Act>
+int backward(void *grad_in, void *out, const void *grad, const int8_t *codes,
+             const uint8_t *scales, int64_t M, int64_t d, int64_t gs, int dtype,
+             const int32_t *n_rows, cudaStream_t stream) {
+    int rc = check_sizes(M, d, gs, d, dtype);
+    if (rc != GATED_ACT_OK || M == 0)
+        return rc;
+    const int64_t B = ceil_div64(d, kBlock), size = elem_size(dtype);
+    Region r[6] = {{grad_in, static_cast<uint64_t>(M * 2 * d * size), uintptr_t(size), true},
+                   {out, out ? static_cast<uint64_t>(M * d * size) : 0, uintptr_t(size), true},
+                   {grad, span_bytes(M, gs, d, size), uintptr_t(size), false},
+                   {codes, static_cast<uint64_t>(M * 2 * d), 1, false},
+                   {scales, static_cast<uint64_t>(M * 2 * B), 1, false},
+                   {n_rows, n_rows ? 4u : 0u, 4, false}};
+    if ((rc = check_regions(r, 6)) != GATED_ACT_OK)
+        return rc;
+    return with_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        return launched(launch_kernel(ckpt_backward_any<T, Act>, grid_of(M * B, kWarps),
+                                      dim3(kThreads), 0, stream, 1, as<T>(r[0]), as<T>(r[1]),
+                                      as<const T>(r[2]), as<const int8_t>(r[3]),
+                                      as<const uint8_t>(r[4]), M, d, gs, B,
+                                      as<const int32_t>(r[5])));
+    });
+}
+
+}  // namespace
+}  // namespace gact
+
+extern "C" int64_t gated_act_checkpoint_scales(int64_t d) {
+    return d <= 0 ? 0 : 2 * ((d - 1) / gact::kBlock + 1);
+}
+
+extern "C" int silu_and_mul_checkpoint(void *out, int8_t *codes, uint8_t *scales, const void *in,
+                                       int64_t M, int64_t d, int64_t row_stride, int dtype,
+                                       const int32_t *n_rows, cudaStream_t stream) {
+    return gact::forward<gact::Silu>(out, codes, scales, in, M, d, row_stride, dtype, n_rows,
+                                     stream);
+}
+
+extern "C" int gelu_and_mul_checkpoint(void *out, int8_t *codes, uint8_t *scales, const void *in,
+                                       int64_t M, int64_t d, int64_t row_stride, int dtype,
+                                       const int32_t *n_rows, cudaStream_t stream) {
+    return gact::forward<gact::Gelu>(out, codes, scales, in, M, d, row_stride, dtype, n_rows,
+                                     stream);
+}
+
+extern "C" int silu_and_mul_backward(void *grad_in, void *out, const void *grad_out,
+                                     const int8_t *codes, const uint8_t *scales, int64_t M,
+                                     int64_t d, int64_t grad_stride, int dtype,
+                                     const int32_t *n_rows, cudaStream_t stream) {
+    return gact::backward<gact::Silu>(grad_in, out, grad_out, codes, scales, M, d, grad_stride,
+                                      dtype, n_rows, stream);
+}
+
+extern "C" int gelu_and_mul_backward(void *grad_in, void *out, const void *grad_out,
+                                     const int8_t *codes, const uint8_t *scales, int64_t M,
+                                     int64_t d, int64_t grad_stride, int dtype,
+                                     const int32_t *n_rows, cudaStream_t stream) {
+    return gact::backward<gact::Gelu>(grad_in, out, grad_out, codes, scales, M, d, grad_stride,
+                                      dtype, n_rows, stream);
+}
+
+extern "C" int gelu_and_mul_sparse_checkpoint(void *out, int8_t *codes, uint8_t *scales,
+                                              float *std, const void *in, int64_t T, int64_t d,
+                                              int64_t row_stride, double z, int dtype,
+                                              cudaStream_t stream) {
+    using namespace gact;
+    int rc = check_sizes(T, d, row_stride, 2 * d, dtype);
+    if (rc != GATED_ACT_OK || T == 0)
+        return rc;
+    const int64_t B = ceil_div64(d, kBlock), size = elem_size(dtype);
+    Region r[5] = {{out, static_cast<uint64_t>(T * d * size), uintptr_t(size), true},
+                   {codes, static_cast<uint64_t>(T * 2 * d), 1, true},
+                   {scales, static_cast<uint64_t>(T * 2 * B), 1, true},
+                   {std, static_cast<uint64_t>(T * 4), 4, true},
+                   {in, span_bytes(T, row_stride, 2 * d, size), uintptr_t(size), false}};
+    if ((rc = check_regions(r, 5)) != GATED_ACT_OK)
+        return rc;
+    return with_type(dtype, [&](auto t) {
+        using E = decltype(t);
+        return launched(launch_kernel(sparse_forward_any<E>, grid_of(T, 1), dim3(kThreads), 0,
+                                      stream, 1, as<E>(r[0]), as<int8_t>(r[1]), as<uint8_t>(r[2]),
+                                      as<float>(r[3]), as<const E>(r[4]), T, d, row_stride, B,
+                                      static_cast<float>(z)));
+    });
+}
+
+extern "C" int gelu_and_mul_sparse_backward(void *grad_in, void *out, const void *grad_out,
+                                            const int8_t *codes, const uint8_t *scales,
+                                            const float *std, int64_t T, int64_t d,
+                                            int64_t grad_stride, double z, int dtype,
+                                            cudaStream_t stream) {
+    using namespace gact;
+    int rc = check_sizes(T, d, grad_stride, d, dtype);
+    if (rc != GATED_ACT_OK || T == 0)
+        return rc;
+    const int64_t B = ceil_div64(d, kBlock), size = elem_size(dtype);
+    Region r[6] = {{grad_in, static_cast<uint64_t>(T * 2 * d * size), uintptr_t(size), true},
+                   {out, out ? static_cast<uint64_t>(T * d * size) : 0, uintptr_t(size), true},
+                   {grad_out, span_bytes(T, grad_stride, d, size), uintptr_t(size), false},
+                   {codes, static_cast<uint64_t>(T * 2 * d), 1, false},
+                   {scales, static_cast<uint64_t>(T * 2 * B), 1, false},
+                   {std, static_cast<uint64_t>(T * 4), 4, false}};
+    if ((rc = check_regions(r, 6)) != GATED_ACT_OK)
+        return rc;
+    return with_type(dtype, [&](auto t) {
+        using E = decltype(t);
+        return launched(launch_kernel(sparse_backward_any<E>, grid_of(T, 1), dim3(kThreads), 0,
+                                      stream, 1, as<E>(r[0]), as<E>(r[1]), as<const E>(r[2]),
+                                      as<const int8_t>(r[3]), as<const uint8_t>(r[4]),
+                                      as<const float>(r[5]), T, d, grad_stride, B,
+                                      static_cast<float>(z)));
+    });
+}
+
+extern "C" int gated_act_checkpoint_values(void *values, const int8_t *codes,
+                                           const uint8_t *scales, int64_t M, int64_t d, int dtype,
+                                           cudaStream_t stream) {
+    using namespace gact;
+    if (dtype == GATED_ACT_F16)
+        return GATED_ACT_ERR_DTYPE;
+    int rc = check_sizes(M, d, 2 * d, 2 * d, dtype);
+    if (rc != GATED_ACT_OK || M == 0)
+        return rc;
+    const int64_t B = ceil_div64(d, kBlock), size = elem_size(dtype);
+    Region r[3] = {{values, static_cast<uint64_t>(M * 2 * d * size), uintptr_t(size), true},
+                   {codes, static_cast<uint64_t>(M * 2 * d), 1, false},
+                   {scales, static_cast<uint64_t>(M * 2 * B), 1, false}};
+    if ((rc = check_regions(r, 3)) != GATED_ACT_OK)
+        return rc;
+    return with_type(dtype, [&](auto t) {
+        using E = decltype(t);
+        return launched(launch_kernel(ckpt_values_any<E>, grid_of(M * 2 * d, kThreads),
+                                      dim3(kThreads), 0, stream, 1, as<E>(r[0]),
+                                      as<const int8_t>(r[1]), as<const uint8_t>(r[2]), M, d, B));
+    });
+}

@@ -1,0 +1,183 @@
+// Internal helpers of the training operators (checkpoint.cu, layer_norm.cu,
+// balance.cu): element types, the activations with their derivatives, the
+// 8-bit block format, and the host side's argument checks.
+#pragma once
+
+#include "common.cuh"
+#include "gated_act_training.h"
+
+namespace gact {
+
+// ---------------------------------------------------------------- elements
+
+using bf16 = __nv_bfloat16;
+using f16 = __half;
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(bf16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(f16 x) { return __half2float(x); }
+
+template <class T> __device__ __forceinline__ T from_float(float x);
+template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <> __device__ __forceinline__ bf16 from_float<bf16>(float x) { return __float2bfloat16_rn(x); }
+template <> __device__ __forceinline__ f16 from_float<f16>(float x) { return __float2half_rn(x); }
+
+// ------------------------------------------------------------- activations
+
+// Both activations are g sigma(a) with a = a(g), and their slope is
+// sigma (1 + g (1 - sigma) a').  With t = e^{-|a|}, sigma and 1 - sigma are
+// 1 / (1 + t) and t / (1 + t) in one order or the other: no cancellation.  t is
+// the square of h = 2^{-|a| log2(e) / 2}, which the flushing hardware
+// exponential (PTX ISA ex2.approx.ftz.f32, relative error about 2^-22) keeps
+// normal for |a| < 174; 1 + t lies in [1, 2], where the hardware reciprocal
+// is within one ulp.  sigma is handed on as the product s1 s2 (h / (1 + t)
+// and h for a < 0), s2 to be multiplied last: then nothing but a result itself
+// can fall below fp32's normal range.
+struct Gate {
+    float s1, s2;   // sigma = s1 s2
+    float w;        // slope = sigma w
+};
+__device__ __forceinline__ Gate gate_of(float a, float g_slope) {
+    float h, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(fabsf(a) * (-0.5f * 1.4426950408889634f)));
+    const float t = h * h;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+    const bool up = a >= 0.f;
+    Gate m;
+    m.s2 = up ? 1.f : h;
+    m.s1 = r * m.s2;
+    m.w = fmaf(g_slope, up ? t * r : r, 1.f);
+    return m;
+}
+
+struct Silu {
+    __device__ static Gate gate(float g) { return gate_of(g, g); }
+};
+
+// a = 2 sqrt(2/pi) (g + 0.044715 g^3).  g a' is taken at most at |g| = 16,
+// where it cannot overflow: past |g| = 11, t is 0 and so is its factor (a > 0)
+// or sigma (a < 0).
+struct Gelu {
+    static constexpr float k2 = 2.0f * 0.7978845608028654f;
+    static constexpr float k2c = 2.0f * 0.7978845608028654f * 0.044715f;
+    __device__ static Gate gate(float g) {
+        const float b = fminf(fmaxf(g, -16.f), 16.f);
+        return gate_of(g * fmaf(k2c, g * g, k2), b * fmaf(3.f * k2c, b * b, k2));
+    }
+};
+
+// gelu_tanh(s) u for s >= 0 or NaN.
+__device__ __forceinline__ float gelu_mul(float s, float u) {
+    const Gate m = Gelu::gate(s);
+    return s * m.s1 * u;
+}
+
+// act(g) u
+template <class Act> __device__ __forceinline__ float act_mul(float g, float u) {
+    const Gate m = Act::gate(g);
+    return g * m.s1 * u * m.s2;
+}
+
+// The gradients of act(g) u, and act(g) u itself.
+struct GateGrad {
+    float gate, up, out;
+};
+template <class Act> __device__ __forceinline__ GateGrad act_grad(float g, float u, float dy) {
+    const Gate m = Act::gate(g);
+    const float p = g * m.s1;
+    return {dy * u * m.s1 * m.w * m.s2, p * dy * m.s2, p * u * m.s2};
+}
+// The same of gelu_tanh at s = max(delta, 0); gate is 0 where delta <= 0.
+__device__ __forceinline__ GateGrad sparse_grad(float delta, float u, float dy) {
+    float s;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(s) : "f"(delta));
+    const Gate m = Gelu::gate(s);
+    const float p = s * m.s1;
+    return {delta <= 0.f ? 0.f : dy * u * m.s1 * m.w, p * dy, p * u};
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// ------------------------------------------------------- 8-bit block format
+
+constexpr int kBlock = 32;   // elements that share a scale
+constexpr uint32_t kBadScale = 255u;
+constexpr uint32_t kTopScale = 248u;   // 2^121: the next one's codes would reach 2^128
+
+// Scale byte of a block from the bits of its largest magnitude, m 2^E with
+// m in [1, 2): the codes of k = E - 6 reach 64 m, which rounds past 127 from
+// m = 127.5 / 64 on; adding 2^23 - 0x7F0000 to the bits carries into the
+// exponent exactly then.  NaN and infinity give 255.  At kTopScale the largest
+// magnitudes round to 128: clamp_top limits the values of such a block first.
+__device__ __forceinline__ uint32_t scale_of(uint32_t top_bits) {
+    if (top_bits >= 0x7F800000u)
+        return kBadScale;
+    const int e = static_cast<int>((top_bits + 0x10000u) >> 23) - 6;
+    return static_cast<uint32_t>(min(max(e, 0), static_cast<int>(kTopScale)));
+}
+__device__ __forceinline__ float clamp_top(float v) {
+    constexpr float top = 127.f * 0x1p121f;
+    return fminf(fmaxf(v, -top), top);
+}
+// 2^-k, the factor from value to code (0 for a bad block), and 2^k, the step
+// from code to value (NaN for a bad block, subnormal for scale 0).
+__device__ __forceinline__ float code_factor(uint32_t scale) {
+    return scale == kBadScale ? 0.f : __uint_as_float((254u - scale) << 23);
+}
+__device__ __forceinline__ float code_step(uint32_t scale) {
+    return __uint_as_float(scale == kBadScale ? 0x7FC00000u : scale == 0 ? 0x00400000u : scale << 23);
+}
+// rint(v 2^-k): the product is exact, so the fused add of 1.5 2^23 rounds once,
+// to nearest even, and leaves the code in the low byte.  v = NaN or infinity
+// (only with factor 0) gives NaN bits; the caller masks bad blocks.
+__device__ __forceinline__ int code_of(float v, float factor) {
+    return __float_as_int(fmaf(v, factor, 12582912.f)) - 0x4B400000;
+}
+
+// ---------------------------------------------------------------- host side
+
+// One buffer of a call: its checks, then the address kernels use for it.
+struct Region {
+    const void *p;
+    uint64_t bytes;
+    uintptr_t align;
+    bool write;
+    const void *dev = nullptr;
+};
+
+// Null, alignment, overlap (of two buffers of which one is written) and
+// residence of every buffer; empty buffers (bytes = 0) are skipped.
+int check_regions(Region *r, int n);
+
+inline int64_t elem_size(int dtype) {
+    return dtype == GATED_ACT_F32 ? 4 : dtype == GATED_ACT_BF16 || dtype == GATED_ACT_F16 ? 2 : 0;
+}
+inline int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Bytes spanned by `rows` rows of `width` elements, `stride` elements apart.
+inline uint64_t span_bytes(int64_t rows, int64_t stride, int64_t width, int64_t size) {
+    return rows <= 0 ? 0 : static_cast<uint64_t>(((rows - 1) * stride + width) * size);
+}
+
+template <class T> inline T *as(const Region &r) {
+    return static_cast<T *>(const_cast<void *>(r.dev));
+}
+
+// Calls f(T{}) with the element type of a checked dtype code.
+template <class F> inline int with_type(int dtype, F f) {
+    switch (dtype) {
+    case GATED_ACT_BF16: return f(bf16{});
+    case GATED_ACT_F16: return f(f16{});
+    default: return f(float{});
+    }
+}
+
+inline int launched(cudaError_t e) {
+    return cuda_status(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+}  // namespace gact
