@@ -113,6 +113,160 @@ ckpt_values_any(T *__restrict__ values, const int8_t *__restrict__ codes,
     }
 }
 
+// --------------------------------------------------- elementwise, vectors
+//
+// Rows in 16-byte vectors (pointers and strides allow it, d a multiple of 8):
+// a thread takes 8 elements of the gate and the 8 of the up half beside them;
+// four neighbouring lanes hold a block of each.  A row is 4 B slots of 8
+// elements, B blocks, so that lane groups and blocks coincide in every row;
+// the slots past d (a ragged last block) are empty.
+
+// Largest magnitude over the four lanes of a block, of both halves at once.
+template <class T>
+__device__ __forceinline__ void block_tops(uint32_t *g, uint32_t *u) {
+    if constexpr (sizeof(T) == 2) {
+        uint32_t w = *g | (*u << 16);
+        w = max_u16x2(w, __shfl_xor_sync(0xFFFFFFFFu, w, 1));
+        w = max_u16x2(w, __shfl_xor_sync(0xFFFFFFFFu, w, 2));
+        *g = w & 0xFFFFu;
+        *u = w >> 16;
+    } else {
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+            *g = max(*g, __shfl_xor_sync(0xFFFFFFFFu, *g, o));
+            *u = max(*u, __shfl_xor_sync(0xFFFFFFFFu, *u, o));
+        }
+    }
+}
+
+template <class T, class Act, int VPT, class I>
+__global__ void __launch_bounds__(kThreads)
+ckpt_forward_vec(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
+                 const T *__restrict__ in, int64_t M, I d, int64_t rs, I B,
+                 const int32_t *n_rows) {
+    pdl_wait();
+    pdl_trigger();
+    const I slots = 4 * B;
+    const I live = static_cast<I>(live_rows(M, n_rows));
+    const I first = static_cast<I>(blockIdx.x) * (VPT * kThreads) + threadIdx.x;
+    I row[VPT], col[VPT];
+    Vec8<T> g[VPT], u[VPT];
+    bool ok[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const I s = first + i * kThreads;
+        row[i] = s / slots;
+        col[i] = (s - row[i] * slots) * 8;
+        ok[i] = row[i] < live && col[i] < d;
+        g[i] = u[i] = Vec8<T>::zero();
+        if (ok[i]) {
+            const T *p = in + static_cast<int64_t>(row[i]) * rs + col[i];
+            g[i] = Vec8<T>::load(p);
+            u[i] = Vec8<T>::load(p + d);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        uint32_t tg = g[i].top(), tu = u[i].top();
+        block_tops<T>(&tg, &tu);
+        if (!ok[i])
+            continue;
+        const uint32_t sg = scale_of(top_as_float<T>(tg)), su = scale_of(top_as_float<T>(tu));
+        float2 gf[4], uf[4];
+        Vec8<T> o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            gf[j] = g[i].pair(j);
+            uf[j] = u[i].pair(j);
+            o.put(j, make_float2(act_mul<Act>(gf[j].x, uf[j].x), act_mul<Act>(gf[j].y, uf[j].y)));
+        }
+        const int64_t r = row[i];
+        o.store(out + r * d + col[i]);
+        int8_t *c = codes + r * 2 * d + col[i];
+        st_u2(c, codes_of<false>(gf, sg));
+        st_u2(c + d, codes_of<false>(uf, su));
+        if (col[i] % kBlock == 0) {
+            uint8_t *s = scales + r * 2 * B + col[i] / kBlock;
+            s[0] = static_cast<uint8_t>(sg);
+            s[B] = static_cast<uint8_t>(su);
+        }
+    }
+}
+
+template <class T, class Act, int VPT, class I>
+__global__ void __launch_bounds__(kThreads)
+ckpt_backward_vec(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
+                  const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t M,
+                  I d, int64_t gs, I B, const int32_t *n_rows) {
+    pdl_wait();
+    pdl_trigger();
+    const I nv = d / 8;
+    const I live = static_cast<I>(live_rows(M, n_rows));
+    const I first = static_cast<I>(blockIdx.x) * (VPT * kThreads) + threadIdx.x;
+    I row[VPT], col[VPT];
+    Vec8<T> dy[VPT];
+    uint2 cg[VPT], cu[VPT];
+    uint32_t sg[VPT], su[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const I s = first + i * kThreads;
+        row[i] = s / nv;
+        col[i] = (s - row[i] * nv) * 8;
+        if (row[i] < live) {
+            const int64_t r = row[i];
+            dy[i] = Vec8<T>::load(grad + r * gs + col[i]);
+            const int8_t *c = codes + r * 2 * d + col[i];
+            cg[i] = ld_stream_u2(c);
+            cu[i] = ld_stream_u2(c + d);
+            const uint8_t *q = scales + r * 2 * B + col[i] / kBlock;
+            sg[i] = __ldg(q);
+            su[i] = __ldg(q + B);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        if (row[i] >= live)
+            continue;
+        const uint2 bg = bias_codes(cg[i]), bu = bias_codes(cu[i]);
+        const float stg = code_step(sg[i]), stu = code_step(su[i]);
+        Vec8<T> og, ou, oo;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 g = decode_pair(bg, j, stg), u = decode_pair(bu, j, stu);
+            const float2 y = dy[i].pair(j);
+            const GateGrad a = act_grad<Act>(g.x, u.x, y.x), b = act_grad<Act>(g.y, u.y, y.y);
+            og.put(j, make_float2(a.gate, b.gate));
+            ou.put(j, make_float2(a.up, b.up));
+            oo.put(j, make_float2(a.out, b.out));
+        }
+        const int64_t r = row[i];
+        T *p = grad_in + r * 2 * d + col[i];
+        og.store(p);
+        ou.store(p + d);
+        if (out)
+            oo.store(out + r * d + col[i]);
+    }
+}
+
+template <class T, class I>
+__global__ void __launch_bounds__(kThreads)
+ckpt_values_vec(T *__restrict__ values, const int8_t *__restrict__ codes,
+                const uint8_t *__restrict__ scales, I total, I nv, I B) {
+    pdl_wait();
+    pdl_trigger();
+    const I s = static_cast<I>(blockIdx.x) * kThreads + threadIdx.x;
+    if (s >= total)
+        return;
+    const I h = s / nv, v = s - h * nv;                // half-row, vector
+    const float step = code_step(__ldg(scales + static_cast<int64_t>(h) * B + v / 4));
+    const uint2 b = bias_codes(ld_stream_u2(codes + static_cast<int64_t>(s) * 8));
+    Vec8<T> o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        o.put(j, decode_pair(b, j, step));
+    o.store(values + static_cast<int64_t>(s) * 8);
+}
+
 // ------------------------------------------------------ sparse, any layout
 
 // Sum over the CTA, the same bits in every thread; red holds kWarps floats
@@ -228,6 +382,18 @@ dim3 grid_of(int64_t units, int64_t per_cta) {
                                                         int64_t(device_sm_count()) * 64)));
 }
 
+// Calls f(I{}, grid) for `slots` slots, VPT per thread, with I the type that
+// their indexes take: 32 bits where they fit.
+template <class F> int with_index(int64_t slots, int vpt, F f) {
+    const int64_t per = int64_t(kThreads) * vpt, grid = ceil_div64(slots, per);
+    if (grid > 0x7FFFFFFF)
+        return GATED_ACT_ERR_TOO_LARGE;
+    const dim3 g(static_cast<unsigned>(grid));
+    return slots + per < (int64_t(1) << 31) ? f(uint32_t{}, g) : f(int64_t{}, g);
+}
+
+constexpr int kForwardVpt = 1, kBackwardVpt = 1;
+
 template <class Act>
 int forward(void *out, int8_t *codes, uint8_t *scales, const void *in, int64_t M, int64_t d,
             int64_t rs, int dtype, const int32_t *n_rows, cudaStream_t stream) {
@@ -242,8 +408,20 @@ int forward(void *out, int8_t *codes, uint8_t *scales, const void *in, int64_t M
                    {n_rows, n_rows ? 4u : 0u, 4, false}};
     if ((rc = check_regions(r, 5)) != GATED_ACT_OK)
         return rc;
+    const bool vec = d % 8 == 0 && rs % 8 == 0 && aligned(r[0].dev, 16) && aligned(r[1].dev, 8) &&
+                     aligned(r[3].dev, 16);
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
+        if (vec) {
+            constexpr int VPT = kForwardVpt;
+            return with_index(M * 4 * B, VPT, [&](auto idx, dim3 grid) {
+                using I = decltype(idx);
+                return launched(launch_kernel(
+                    ckpt_forward_vec<T, Act, VPT, I>, grid, dim3(kThreads), 0, stream, 1,
+                    as<T>(r[0]), as<int8_t>(r[1]), as<uint8_t>(r[2]), as<const T>(r[3]), M,
+                    static_cast<I>(d), rs, static_cast<I>(B), as<const int32_t>(r[4])));
+            });
+        }
         return launched(launch_kernel(ckpt_forward_any<T, Act>, grid_of(M * B, kWarps),
                                       dim3(kThreads), 0, stream, 1, as<T>(r[0]), as<int8_t>(r[1]),
                                       as<uint8_t>(r[2]), as<const T>(r[3]), M, d, rs, B,
@@ -267,8 +445,21 @@ int backward(void *grad_in, void *out, const void *grad, const int8_t *codes,
                    {n_rows, n_rows ? 4u : 0u, 4, false}};
     if ((rc = check_regions(r, 6)) != GATED_ACT_OK)
         return rc;
+    const bool vec = d % 8 == 0 && gs % 8 == 0 && aligned(r[0].dev, 16) && aligned(r[1].dev, 16) &&
+                     aligned(r[2].dev, 16) && aligned(r[3].dev, 8);
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
+        if (vec) {
+            constexpr int VPT = kBackwardVpt;
+            return with_index(M * (d / 8), VPT, [&](auto idx, dim3 grid) {
+                using I = decltype(idx);
+                return launched(launch_kernel(
+                    ckpt_backward_vec<T, Act, VPT, I>, grid, dim3(kThreads), 0, stream, 1,
+                    as<T>(r[0]), as<T>(r[1]), as<const T>(r[2]), as<const int8_t>(r[3]),
+                    as<const uint8_t>(r[4]), M, static_cast<I>(d), gs, static_cast<I>(B),
+                    as<const int32_t>(r[5])));
+            });
+        }
         return launched(launch_kernel(ckpt_backward_any<T, Act>, grid_of(M * B, kWarps),
                                       dim3(kThreads), 0, stream, 1, as<T>(r[0]), as<T>(r[1]),
                                       as<const T>(r[2]), as<const int8_t>(r[3]),
@@ -384,6 +575,14 @@ extern "C" int gated_act_checkpoint_values(void *values, const int8_t *codes,
         return rc;
     return with_type(dtype, [&](auto t) {
         using E = decltype(t);
+        if (d % 8 == 0 && aligned(r[0].dev, 16) && aligned(r[1].dev, 8))
+            return with_index(M * 2 * (d / 8), 1, [&](auto idx, dim3 grid) {
+                using I = decltype(idx);
+                return launched(launch_kernel(
+                    ckpt_values_vec<E, I>, grid, dim3(kThreads), 0, stream, 1, as<E>(r[0]),
+                    as<const int8_t>(r[1]), as<const uint8_t>(r[2]), static_cast<I>(M * 2 * (d / 8)),
+                    static_cast<I>(d / 8), static_cast<I>(B)));
+            });
         return launched(launch_kernel(ckpt_values_any<E>, grid_of(M * 2 * d, kThreads),
                                       dim3(kThreads), 0, stream, 1, as<E>(r[0]),
                                       as<const int8_t>(r[1]), as<const uint8_t>(r[2]), M, d, B));

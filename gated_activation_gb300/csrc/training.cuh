@@ -3,6 +3,8 @@
 // 8-bit block format, and the host side's argument checks.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "gated_act_training.h"
 
@@ -102,6 +104,92 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// ------------------------------------------------------------ 8 elements
+
+__device__ __forceinline__ uint2 ld_stream_u2(const void *p) {
+    uint2 r;
+    asm("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ void st_u2(void *p, uint2 v) {
+    asm volatile("st.global.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(v.x), "r"(v.y));
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// 8 consecutive elements of a row, as loaded: four words of two 16-bit
+// elements, or eight of one.  pair(i) is elements 2i and 2i + 1.
+template <class T> struct Vec8 {
+    static_assert(sizeof(T) == 2, "16-bit elements");
+    uint4 q;
+    __device__ static Vec8 zero() { return {make_uint4(0u, 0u, 0u, 0u)}; }
+    __device__ static Vec8 load(const T *p) { return {ld_stream(p)}; }
+    __device__ void store(T *p) const { st_vec_out(p, q); }
+    __device__ float2 pair(int i) const {
+        const uint32_t w = (&q.x)[i];
+        if constexpr (std::is_same_v<T, bf16>)
+            return make_float2(bf16_lo(w), bf16_hi(w));
+        else
+            return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    }
+    __device__ void put(int i, float2 f) {
+        if constexpr (std::is_same_v<T, bf16>) {
+            (&q.x)[i] = pack_bf16x2(f.x, f.y);
+        } else {
+            const __half2 h = __floats2half2_rn(f.x, f.y);
+            (&q.x)[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+    // Largest magnitude, as the bits of the element type: for values of one
+    // type these order as the magnitudes do, infinity and NaN above all.
+    __device__ uint32_t top() const {
+        constexpr uint32_t m = 0x7FFF7FFFu;
+        const uint32_t w = max_u16x2(max_u16x2(q.x & m, q.y & m), max_u16x2(q.z & m, q.w & m));
+        return max(w >> 16, w & 0xFFFFu);
+    }
+};
+template <> struct Vec8<float> {
+    uint4 q[2];
+    __device__ static Vec8 zero() {
+        return {{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}};
+    }
+    __device__ static Vec8 load(const float *p) { return {{ld_stream(p), ld_stream(p + 4)}}; }
+    __device__ void store(float *p) const {
+        st_vec_out(p, q[0]);
+        st_vec_out(p + 4, q[1]);
+    }
+    __device__ float2 pair(int i) const {
+        const uint32_t *w = &q[i / 2].x + 2 * (i & 1);
+        return make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    }
+    __device__ void put(int i, float2 f) {
+        uint32_t *w = &q[i / 2].x + 2 * (i & 1);
+        w[0] = __float_as_uint(f.x);
+        w[1] = __float_as_uint(f.y);
+    }
+    __device__ uint32_t top() const {
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            t = max(t, max(max(q[i].x & 0x7FFFFFFFu, q[i].y & 0x7FFFFFFFu),
+                           max(q[i].z & 0x7FFFFFFFu, q[i].w & 0x7FFFFFFFu)));
+        return t;
+    }
+};
+
+// Bits of a largest magnitude (Vec8::top) as those of the fp32 value.
+template <class T> __device__ __forceinline__ uint32_t top_as_float(uint32_t t) {
+    if constexpr (std::is_same_v<T, float>)
+        return t;
+    else if constexpr (std::is_same_v<T, bf16>)
+        return t << 16;
+    else
+        return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(t))));
+}
+
 // ------------------------------------------------------- 8-bit block format
 
 constexpr int kBlock = 32;   // elements that share a scale
@@ -136,6 +224,46 @@ __device__ __forceinline__ float code_step(uint32_t scale) {
 // (only with factor 0) gives NaN bits; the caller masks bad blocks.
 __device__ __forceinline__ int code_of(float v, float factor) {
     return __float_as_int(fmaf(v, factor, 12582912.f)) - 0x4B400000;
+}
+
+// The codes of 8 values of one block, for the block's scale.
+template <bool KEEP_SIGN>
+__device__ __forceinline__ uint2 codes_of(const float2 (&v)[4], uint32_t scale) {
+    const float f = code_factor(scale);
+    const float2 f2 = make_float2(f, f), magic = make_float2(12582912.f, 12582912.f);
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 x = v[i];
+        if (scale == kTopScale)
+            x = make_float2(clamp_top(x.x), clamp_top(x.y));
+        const float2 q = fma2(x, f2, magic);
+        w[2 * i] = __float_as_uint(q.x);
+        w[2 * i + 1] = __float_as_uint(q.y);
+        if (KEEP_SIGN) {   // 12582912 + 1, the bits of code 1
+            if (x.x > 0.f)
+                w[2 * i] = max(w[2 * i], 0x4B400001u);
+            if (x.y > 0.f)
+                w[2 * i + 1] = max(w[2 * i + 1], 0x4B400001u);
+        }
+    }
+    uint2 c;
+    c.x = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+    c.y = __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410);
+    return scale == kBadScale ? make_uint2(0u, 0u) : c;
+}
+
+// Codes 2i and 2i + 1 of 8 (biased: codes ^ 0x80808080) as values: the byte
+// becomes the low bits of 2^23 + 128 + code; both steps are exact.
+__device__ __forceinline__ float2 decode_pair(uint2 biased, int i, float step) {
+    const uint32_t w = i < 2 ? biased.x : biased.y;
+    const float2 f = make_float2(
+        __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + 2 * (i & 1))),
+        __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7541 + 2 * (i & 1))));
+    return mul2(sub2(f, make_float2(8388736.f, 8388736.f)), make_float2(step, step));
+}
+__device__ __forceinline__ uint2 bias_codes(uint2 c) {
+    return make_uint2(c.x ^ 0x80808080u, c.y ^ 0x80808080u);
 }
 
 // ---------------------------------------------------------------- host side

@@ -36,21 +36,38 @@ class BalanceLoss(NamedTuple):
     coef: float
 
 
+# The current stream's handle without a Stream object around it: these calls
+# are a few microseconds long on the host, and that object is two of them.
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _handle(x: torch.Tensor, stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return _current_stream(x.get_device() if x.is_cuda else torch.cuda.current_device())
+
+
+def _lib():
+    return _ga._lib or _ga.load_library()
+
+
 def _new(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """An uninitialised tensor where ``like`` lives, owned by ``stream``."""
+    if stream is None and like.is_cuda:
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if not like.is_cuda:
         return torch.empty(shape, dtype=dtype, pin_memory=True)
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _scratch(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
     """Device memory for one call, owned by ``stream``."""
-    with torch.cuda.stream(stream):          # None: the current stream stays
-        return torch.empty(nbytes, dtype=torch.uint8,
-                           device=like.device if like.is_cuda else "cuda")
+    device = like.device if like.is_cuda else torch.device("cuda", torch.cuda.current_device())
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _reachable(x: torch.Tensor, what: str) -> None:
@@ -116,9 +133,9 @@ def _checkpoint_rows(x, d, out, stream):
 
 def _checkpointed(fn, x, n_rows, d, out, stream):
     m, d, stride, code, out, (codes, scales) = _checkpoint_rows(x, d, out, stream)
-    rc = getattr(_ga.load_library(), fn)(
+    rc = getattr(_lib(), fn)(
         out.data_ptr(), codes.data_ptr(), scales.data_ptr(), x.data_ptr(), m, d, stride, code,
-        _count(n_rows), _ga._stream_handle(stream))
+        _count(n_rows), _handle(x, stream))
     _ga._check(fn, rc)
     return out, Checkpoint(codes, scales)
 
@@ -152,9 +169,9 @@ def gelu_and_mul_sparse_checkpoint(x: torch.Tensor, z: float, d: int | None = No
     """
     m, d, stride, code, out, (codes, scales) = _checkpoint_rows(x, d, out, stream)
     std = _new((m,), torch.float32, x, stream)
-    rc = _ga.load_library().gelu_and_mul_sparse_checkpoint(
+    rc = _lib().gelu_and_mul_sparse_checkpoint(
         out.data_ptr(), codes.data_ptr(), scales.data_ptr(), std.data_ptr(), x.data_ptr(), m, d,
-        stride, float(z), code, _ga._stream_handle(stream))
+        stride, float(z), code, _handle(x, stream))
     _ga._check("gelu_and_mul_sparse_checkpoint", rc)
     return out, Checkpoint(codes, scales, std)
 
@@ -175,9 +192,9 @@ def _backward_rows(grad_out, kept, recompute, stream):
 def _activation_backward(fn, grad_out, kept, n_rows, recompute, stream):
     m, d, stride, code, codes, scales, grad_in, out = _backward_rows(grad_out, kept, recompute,
                                                                      stream)
-    rc = getattr(_ga.load_library(), fn)(
+    rc = getattr(_lib(), fn)(
         grad_in.data_ptr(), out.data_ptr() if recompute else 0, grad_out.data_ptr(), codes, scales,
-        m, d, stride, code, _count(n_rows), _ga._stream_handle(stream))
+        m, d, stride, code, _count(n_rows), _handle(grad_out, stream))
     _ga._check(fn, rc)
     return (grad_in, out) if recompute else grad_in
 
@@ -210,9 +227,9 @@ def gelu_and_mul_sparse_backward(grad_out: torch.Tensor, kept: Checkpoint, z: fl
     m, d, stride, code, codes, scales, grad_in, out = _backward_rows(grad_out, kept, recompute,
                                                                      stream)
     std = _flat(kept.std, "std", torch.float32, (m,))
-    rc = _ga.load_library().gelu_and_mul_sparse_backward(
+    rc = _lib().gelu_and_mul_sparse_backward(
         grad_in.data_ptr(), out.data_ptr() if recompute else 0, grad_out.data_ptr(), codes, scales,
-        std, m, d, stride, float(z), code, _ga._stream_handle(stream))
+        std, m, d, stride, float(z), code, _handle(grad_out, stream))
     _ga._check("gelu_and_mul_sparse_backward", rc)
     return (grad_in, out) if recompute else grad_in
 
@@ -227,8 +244,9 @@ def checkpoint_values(kept: Checkpoint, dtype: torch.dtype = torch.bfloat16,
     m, d = kept.codes.shape[0], kept.codes.shape[1] // 2
     codes, scales = _kept(kept, m, d)
     values = _new((m, 2 * d), dtype, kept.codes, stream)
-    rc = _ga.load_library().gated_act_checkpoint_values(
-        values.data_ptr(), codes, scales, m, d, _ga._DTYPE_CODE[dtype], _ga._stream_handle(stream))
+    rc = _lib().gated_act_checkpoint_values(
+        values.data_ptr(), codes, scales, m, d, _ga._DTYPE_CODE[dtype],
+        _handle(kept.codes, stream))
     _ga._check("gated_act_checkpoint_values", rc)
     return values
 
@@ -255,10 +273,10 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     t, d, stride, code = _rows(x, "input")
     w, b, wcode = _params(weight, bias, x, d)
     out = _output(out, (t, d), x, stream)
-    mean, rstd = _new((2, t), torch.float32, x, stream).unbind()
-    rc = _ga.load_library().layer_norm(
+    mean, rstd = (_new((t,), torch.float32, x, stream) for _ in range(2))
+    rc = _lib().layer_norm(
         out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), x.data_ptr(), w, b, t, d, stride,
-        float(eps), code, wcode, _ga._stream_handle(stream))
+        float(eps), code, wcode, _handle(x, stream))
     _ga._check("layer_norm", rc)
     return out, mean, rstd
 
@@ -275,17 +293,18 @@ def layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.T
     w, _, wcode = _params(weight, None, x, d)
     mean_p = _flat(mean, "mean", torch.float32, (t,))
     rstd_p = _flat(rstd, "rstd", torch.float32, (t,))
-    lib = _ga.load_library()
+    lib = _lib()
     grad_in = _new((t, d), x.dtype, x, stream)
-    grads = _new((2 if bias else 1, d), torch.float32, x, stream).unbind()
+    grad_weight = _new((d,), torch.float32, x, stream)
+    grad_bias = _new((d,), torch.float32, x, stream) if bias else None
     need = lib.layer_norm_backward_workspace_bytes(t, d)
     ws = _scratch(need, x, stream)
     rc = lib.layer_norm_backward(
-        grad_in.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr() if bias else 0,
+        grad_in.data_ptr(), grad_weight.data_ptr(), grad_bias.data_ptr() if bias else 0,
         grad_out.data_ptr(), x.data_ptr(), w, mean_p, rstd_p, t, d, stride, gstride, code, wcode,
-        ws.data_ptr(), need, _ga._stream_handle(stream))
+        ws.data_ptr(), need, _handle(x, stream))
     _ga._check("layer_norm_backward", rc)
-    return grad_in, grads[0], grads[1] if bias else None
+    return grad_in, grad_weight, grad_bias
 
 
 # ------------------------------------------------------------ balance loss
@@ -313,15 +332,15 @@ def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float,
     k = ids.shape[1]
     ids_p = _flat(ids, "ids", ids.dtype, (t, k))
     live_p = _live(live, t)
-    lib = _ga.load_library()
-    loss, mean_p = _new((1 + e,), torch.float32, logits, stream).split((1, e))
-    tokens, counts = _new((1 + e,), torch.int32, logits, stream).split((1, e))
+    lib = _lib()
+    loss, mean_p = (_new((n,), torch.float32, logits, stream) for n in (1, e))
+    tokens, counts = (_new((n,), torch.int32, logits, stream) for n in (1, e))
     need = lib.moe_balance_loss_workspace_bytes(t, e)
     ws = _scratch(need, logits, stream)
     rc = lib.moe_balance_loss(
         loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(), mean_p.data_ptr(),
         logits.data_ptr(), ids_p, live_p, t, e, k, stride, code, int(ids.dtype == torch.int64),
-        float(coef), ws.data_ptr(), need, _ga._stream_handle(stream))
+        float(coef), ws.data_ptr(), need, _handle(logits, stream))
     _ga._check("moe_balance_loss", rc)
     return BalanceLoss(loss, counts, tokens, mean_p, k, float(coef))
 
@@ -339,9 +358,9 @@ def moe_balance_loss_backward(grad_loss: torch.Tensor, logits: torch.Tensor, kep
     tokens = _flat(kept.tokens, "tokens", torch.int32, (1,))
     live_p = _live(live, t)
     grad = _new((t, e), logits.dtype, logits, stream)
-    rc = _ga.load_library().moe_balance_loss_backward(
+    rc = _lib().moe_balance_loss_backward(
         grad.data_ptr(), grad_loss.data_ptr(), logits.data_ptr(), counts, tokens, live_p, t, e,
-        kept.k, stride, code, kept.coef, _ga._stream_handle(stream))
+        kept.k, stride, code, kept.coef, _handle(logits, stream))
     _ga._check("moe_balance_loss_backward", rc)
     return grad
 
