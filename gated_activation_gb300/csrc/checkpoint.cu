@@ -359,6 +359,173 @@ sparse_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__res
     }
 }
 
+// -------------------------------------------------------- sparse, vectors
+//
+// One CTA per row, the row in registers: thread t holds the 8-element vectors
+// t, t + NT, ... (V of them) of both halves, so the gate is read once for its
+// statistics and its codes, and four neighbouring lanes hold a block.  All
+// loads are issued before the first sum.
+
+template <int NT>
+__device__ __forceinline__ float row_sum(float v, float *red) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    constexpr int NW = NT / 32;
+    float t = red[threadIdx.x & (NW - 1)];
+#pragma unroll
+    for (int o = NW / 2; o > 0; o >>= 1)
+        t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    return t;
+}
+
+template <class T, int NT, int V>
+__global__ void __launch_bounds__(NT)
+sparse_forward_vec(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
+                   float *__restrict__ std_out, const T *__restrict__ in, int d, int64_t rs,
+                   int B, float z) {
+    __shared__ float red[2][NT / 32];
+    pdl_wait();
+    pdl_trigger();
+    const int64_t r = blockIdx.x;
+    const T *p = in + r * rs;
+    Vec8<T> g[V], u[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (threadIdx.x + NT * i);
+        g[i] = c < d ? Vec8<T>::load(p + c) : Vec8<T>::zero();
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (threadIdx.x + NT * i);
+        u[i] = c < d ? Vec8<T>::load(p + d + c) : Vec8<T>::zero();
+    }
+    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc = add2(acc, g[i].pair(j));
+    const float n = static_cast<float>(d);
+    const float mean = row_sum<NT>(acc.x + acc.y, red[0]) / n;
+    acc = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (8 * (threadIdx.x + NT * i) < d)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 e = sub2(g[i].pair(j), make_float2(mean, mean));
+                acc = fma2(e, e, acc);
+            }
+    const float std = __fsqrt_rn(row_sum<NT>(acc.x + acc.y, red[1]) / n);
+    const float cutoff = fmaf(std, z, mean);
+    if (threadIdx.x == 0)
+        std_out[r] = std;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (threadIdx.x + NT * i);
+        float2 v[4], w[4];
+        Vec8<T> o;
+        uint32_t tg = 0, tu = u[i].top();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = sub2(g[i].pair(j), make_float2(cutoff, cutoff));
+            w[j] = u[i].pair(j);
+            tg = max(tg, max(abs_bits(v[j].x), abs_bits(v[j].y)));
+            o.put(j, make_float2(gelu_mul(max_nan(v[j].x, 0.f), w[j].x),
+                                 gelu_mul(max_nan(v[j].y, 0.f), w[j].y)));
+        }
+        if (c >= d)
+            tg = 0;
+        block_tops<float>(&tg, &tu);   // 32-bit keys; u's own order is that of its type
+        if (c >= d)
+            continue;
+        const uint32_t sg = scale_of(tg), su = scale_of(top_as_float<T>(tu));
+        o.store(out + r * d + c);
+        int8_t *q = codes + r * 2 * d + c;
+        st_u2(q, codes_of<true>(v, sg));
+        st_u2(q + d, codes_of<false>(w, su));
+        if (c % kBlock == 0) {
+            uint8_t *s = scales + r * 2 * B + c / kBlock;
+            s[0] = static_cast<uint8_t>(sg);
+            s[B] = static_cast<uint8_t>(su);
+        }
+    }
+}
+
+template <class T, int NT, int V>
+__global__ void __launch_bounds__(NT)
+sparse_backward_vec(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
+                    const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
+                    const float *__restrict__ std_in, int d, int64_t gs, int B, float z) {
+    __shared__ float red[NT / 32];
+    pdl_wait();
+    pdl_trigger();
+    const int64_t r = blockIdx.x;
+    const float std = std_in[r];
+    const T *y = grad + r * gs;
+    const int8_t *q = codes + r * 2 * d;
+    const uint8_t *sc = scales + r * 2 * B;
+    T *gi = grad_in + r * 2 * d;
+    Vec8<T> dy[V];
+    uint2 cg[V], cu[V];
+    uint32_t sg[V], su[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (threadIdx.x + NT * i);
+        if (c < d) {
+            cg[i] = ld_stream_u2(q + c);
+            cu[i] = ld_stream_u2(q + d + c);
+            dy[i] = Vec8<T>::load(y + c);
+            sg[i] = __ldg(sc + c / kBlock);
+            su[i] = __ldg(sc + B + c / kBlock);
+        }
+    }
+    // h, and the two outputs that do not wait for its sum
+    float2 h[V][4], acc = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (threadIdx.x + NT * i);
+        if (c >= d)
+            continue;
+        const uint2 bg = bias_codes(cg[i]), bu = bias_codes(cu[i]);
+        const float stg = code_step(sg[i]), stu = code_step(su[i]);
+        Vec8<T> ou, oo;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 v = decode_pair(bg, j, stg), u = decode_pair(bu, j, stu);
+            const float2 t = dy[i].pair(j);
+            const GateGrad a = sparse_grad(v.x, u.x, t.x), b = sparse_grad(v.y, u.y, t.y);
+            h[i][j] = make_float2(a.gate, b.gate);
+            acc = add2(acc, h[i][j]);
+            ou.put(j, make_float2(a.up, b.up));
+            oo.put(j, make_float2(a.out, b.out));
+        }
+        ou.store(gi + d + c);
+        if (out)
+            oo.store(out + r * d + c);
+    }
+    // grad = h - m (1 + inv (delta + z std)), m the mean of h, inv = z / std
+    const float m = row_sum<NT>(acc.x + acc.y, red) / static_cast<float>(d);
+    const float inv = std == 0.f ? 0.f : z / std;
+    const float2 zs = make_float2(z * std, z * std), inv2 = make_float2(inv, inv),
+                 one = make_float2(1.f, 1.f), m2 = make_float2(-m, -m);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (threadIdx.x + NT * i);
+        if (c >= d)
+            continue;
+        const uint2 bg = bias_codes(cg[i]);
+        const float stg = code_step(sg[i]);
+        Vec8<T> og;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            og.put(j, fma2(m2, fma2(inv2, add2(decode_pair(bg, j, stg), zs), one), h[i][j]));
+        og.store(gi + c);
+    }
+}
+
 // -------------------------------------------------------------- host side
 
 constexpr int64_t kMaxWidth = int64_t(1) << 30, kMaxRows = int64_t(1) << 40;
@@ -390,6 +557,27 @@ template <class F> int with_index(int64_t slots, int vpt, F f) {
         return GATED_ACT_ERR_TOO_LARGE;
     const dim3 g(static_cast<unsigned>(grid));
     return slots + per < (int64_t(1) << 31) ? f(uint32_t{}, g) : f(int64_t{}, g);
+}
+
+// Calls f(integral constants NT, V) for rows of nv 8-element vectors held by
+// one CTA; false when no such CTA holds them.
+template <int N> using Const = std::integral_constant<int, N>;
+template <class F> bool with_row_cta(int64_t nv, int *rc, F f) {
+    if (nv <= 128)
+        *rc = f(Const<128>{}, Const<1>{});
+    else if (nv <= 256)
+        *rc = f(Const<256>{}, Const<1>{});
+    else if (nv <= 512)
+        *rc = f(Const<256>{}, Const<2>{});
+    else if (nv <= 1024)
+        *rc = f(Const<512>{}, Const<2>{});
+    else if (nv <= 2048)
+        *rc = f(Const<1024>{}, Const<2>{});
+    else if (nv <= 4096)
+        *rc = f(Const<1024>{}, Const<4>{});
+    else
+        return false;
+    return true;
 }
 
 constexpr int kForwardVpt = 1, kBackwardVpt = 1;
@@ -521,8 +709,20 @@ extern "C" int gelu_and_mul_sparse_checkpoint(void *out, int8_t *codes, uint8_t 
                    {in, span_bytes(T, row_stride, 2 * d, size), uintptr_t(size), false}};
     if ((rc = check_regions(r, 5)) != GATED_ACT_OK)
         return rc;
+    const bool vec = d % 8 == 0 && row_stride % 8 == 0 && aligned(r[0].dev, 16) &&
+                     aligned(r[1].dev, 8) && aligned(r[4].dev, 16) && T <= 0x7FFFFFFF;
     return with_type(dtype, [&](auto t) {
         using E = decltype(t);
+        const auto go = [&](auto nt, auto v) {
+            return launched(launch_kernel(
+                sparse_forward_vec<E, nt(), v()>, dim3(static_cast<unsigned>(T)), dim3(nt()), 0,
+                stream, 1, as<E>(r[0]), as<int8_t>(r[1]), as<uint8_t>(r[2]), as<float>(r[3]),
+                as<const E>(r[4]), static_cast<int>(d), row_stride, static_cast<int>(B),
+                static_cast<float>(z)));
+        };
+        int done;
+        if (vec && with_row_cta(d / 8, &done, go))
+            return done;
         return launched(launch_kernel(sparse_forward_any<E>, grid_of(T, 1), dim3(kThreads), 0,
                                       stream, 1, as<E>(r[0]), as<int8_t>(r[1]), as<uint8_t>(r[2]),
                                       as<float>(r[3]), as<const E>(r[4]), T, d, row_stride, B,
@@ -548,8 +748,21 @@ extern "C" int gelu_and_mul_sparse_backward(void *grad_in, void *out, const void
                    {std, static_cast<uint64_t>(T * 4), 4, false}};
     if ((rc = check_regions(r, 6)) != GATED_ACT_OK)
         return rc;
+    const bool vec = d % 8 == 0 && grad_stride % 8 == 0 && aligned(r[0].dev, 16) &&
+                     aligned(r[1].dev, 16) && aligned(r[2].dev, 16) && aligned(r[3].dev, 8) &&
+                     T <= 0x7FFFFFFF;
     return with_type(dtype, [&](auto t) {
         using E = decltype(t);
+        const auto go = [&](auto nt, auto v) {
+            return launched(launch_kernel(
+                sparse_backward_vec<E, nt(), v()>, dim3(static_cast<unsigned>(T)), dim3(nt()), 0,
+                stream, 1, as<E>(r[0]), as<E>(r[1]), as<const E>(r[2]), as<const int8_t>(r[3]),
+                as<const uint8_t>(r[4]), as<const float>(r[5]), static_cast<int>(d), grad_stride,
+                static_cast<int>(B), static_cast<float>(z)));
+        };
+        int done;
+        if (vec && with_row_cta(d / 8, &done, go))
+            return done;
         return launched(launch_kernel(sparse_backward_any<E>, grid_of(T, 1), dim3(kThreads), 0,
                                       stream, 1, as<E>(r[0]), as<E>(r[1]), as<const E>(r[2]),
                                       as<const int8_t>(r[3]), as<const uint8_t>(r[4]),
