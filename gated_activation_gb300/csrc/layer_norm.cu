@@ -116,33 +116,280 @@ ln_backward_columns_any(float *__restrict__ part, const T *__restrict__ grad,
 
 // Adds the n shares of every column: thread x a column, the kReduceY threads y
 // of a column every kReduceY-th share.
-constexpr int kReduceX = 32, kReduceY = 8;
+constexpr int kReduceX = 32, kReduceY = 32;
 __global__ void __launch_bounds__(kReduceX *kReduceY)
 ln_backward_reduce(float *__restrict__ grad_weight, float *__restrict__ grad_bias,
                    const float *__restrict__ part, int64_t n, int64_t d) {
-    __shared__ float sum[2][kReduceY][kReduceX];
+    __shared__ float sum[2][kReduceY][kReduceX + 1];
     pdl_wait();
     pdl_trigger();
     const int x = threadIdx.x % kReduceX, y = threadIdx.x / kReduceX;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * kReduceX + x;
     float w = 0.f, b = 0.f;
-    if (c < d)
-        for (int64_t i = y; i < n; i += kReduceY) {
+    if (c < d) {
+#pragma unroll 4
+        for (int64_t i = y; i < n; i += kReduceY)
             w += part[i * d + c];
-            if (grad_bias)
+        if (grad_bias)
+#pragma unroll 4
+            for (int64_t i = y; i < n; i += kReduceY)
                 b += part[(n + i) * d + c];
-        }
+    }
     sum[0][y][x] = w;
     sum[1][y][x] = b;
     __syncthreads();
-    if (y == 0 && c < d) {
-        for (int i = 1; i < kReduceY; ++i) {
-            w += sum[0][i][x];
-            b += sum[1][i][x];
-        }
-        grad_weight[c] = w;
+    // warp y joins column y's shares
+    w = warp_sum(sum[0][x][y]);
+    b = warp_sum(sum[1][x][y]);
+    const int64_t to = static_cast<int64_t>(blockIdx.x) * kReduceX + y;
+    if (x == 0 && to < d) {
+        grad_weight[to] = w;
         if (grad_bias)
-            grad_bias[c] = b;
+            grad_bias[to] = b;
+    }
+}
+
+// ------------------------------------------------------- forward, vectors
+//
+// The row in registers: TPR threads hold it, thread t the 8-element vectors
+// t, t + TPR, ..., V of them; a CTA of max(TPR, 128) threads takes 128 / TPR
+// rows where a row needs one warp only.  The row's loads bypass L1, so that
+// the parameters, read by every CTA, stay in it.
+
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *red) {
+    v = warp_sum(v);
+    if constexpr (TPR > 32) {
+        if ((threadIdx.x & 31) == 0)
+            red[threadIdx.x >> 5] = v;
+        __syncthreads();
+        constexpr int NW = TPR / 32;
+        v = red[threadIdx.x & (NW - 1)];
+#pragma unroll
+        for (int o = NW / 2; o > 0; o >>= 1)
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    }
+    return v;
+}
+
+// 8 parameters through L1.
+template <class W> __device__ __forceinline__ Vec8<W> load_params(const W *p) {
+    Vec8<W> v;
+    uint4 *q = reinterpret_cast<uint4 *>(&v);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(v) / 16); ++i)
+        q[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    return v;
+}
+
+template <class T, class W, int TPR, int V>
+__global__ void __launch_bounds__(TPR > 128 ? TPR : 128)
+ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restrict__ rstd_out,
+               const T *__restrict__ in, const W *__restrict__ weight, const W *__restrict__ bias,
+               int64_t rows, int d, int64_t rs, float eps) {
+    constexpr int kRows = TPR > 128 ? 1 : 128 / TPR;
+    __shared__ float red[2][TPR > 32 ? TPR / 32 : 1];
+    pdl_wait();
+    pdl_trigger();
+    const int t = threadIdx.x % TPR;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
+    if (kRows > 1 && r >= rows)      // whole warps: a row of several warps has its CTA alone
+        return;
+    const T *p = in + r * rs;
+    Vec8<T> x[V];
+    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (t + TPR * i);
+        x[i] = c < d ? Vec8<T>::load(p + c) : Vec8<T>::zero();
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc = add2(acc, x[i].pair(j));
+    const float n = static_cast<float>(d);
+    const float mean = row_sum<TPR>(acc.x + acc.y, red[0]) / n;
+    const float2 m2 = make_float2(mean, mean);
+    acc = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (8 * (t + TPR * i) < d)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 e = sub2(x[i].pair(j), m2);
+                acc = fma2(e, e, acc);
+            }
+    const float var = row_sum<TPR>(acc.x + acc.y, red[1]) / n;
+    const float rstd = 1.0f / __fsqrt_rn(var + eps);
+    const float2 r2 = make_float2(rstd, rstd);
+    if (t == 0) {
+        mean_out[r] = mean;
+        rstd_out[r] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (t + TPR * i);
+        if (c >= d)
+            continue;
+        const Vec8<W> w = load_params(weight + c);
+        Vec8<T> o;
+        if (bias) {
+            const Vec8<W> b = load_params(bias + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o.put(j, fma2(mul2(sub2(x[i].pair(j), m2), r2), w.pair(j), b.pair(j)));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o.put(j, mul2(mul2(sub2(x[i].pair(j), m2), r2), w.pair(j)));
+        }
+        o.store(out + r * d + c);
+    }
+}
+
+// ------------------------------------------------------ backward, vectors
+//
+// Persistent CTAs: a CTA takes the rows b, b + G, ... and holds its columns'
+// shares of the parameters' gradients, and the weight, in registers; thread
+// t the 8-element vectors t, t + NT, ....  Rows reach it through a ring of S
+// shared-memory slots that cp.async fills S - 1 rows ahead.  A thread copies
+// just the vectors it will read itself, so the ring needs no barrier: its own
+// wait_group is all.  The row's two sums are the only barrier.
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <class T, class W, int NT, int V, int S>
+__global__ void __launch_bounds__(NT, 512 / NT)
+ln_backward_vec(T *__restrict__ grad_in, float *__restrict__ part, const T *__restrict__ grad,
+                const T *__restrict__ in, const W *__restrict__ weight,
+                const float *__restrict__ mean_in, const float *__restrict__ rstd_in, int64_t rows,
+                int d, int64_t rs, int64_t gs) {
+    constexpr int P = sizeof(T) / 2;           // 16-byte pieces of a vector
+    constexpr int NW = NT / 32;
+    extern __shared__ __align__(16) uint4 ring[];   // [S][2][V][P][NT]
+    __shared__ float2 red[2][NW];
+    const int t = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t G = gridDim.x;
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16u * t;
+    const auto fetch = [&](int64_t r, int slot) {
+        if (r < rows) {
+            const T *x = in + r * rs, *y = grad + r * gs;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = 8 * (t + NT * i);
+                if (c < d)
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        const uint32_t at = base + 16u * NT * ((slot * 2 * V + i) * P + p);
+                        copy16(at, x + c + 16 / sizeof(T) * p);
+                        copy16(at + 16u * NT * V * P, y + c + 16 / sizeof(T) * p);
+                    }
+            }
+        }
+        copy_commit();
+    };
+    const auto held = [&](int slot, int which, int i) {
+        Vec8<T> v;
+        uint4 *q = reinterpret_cast<uint4 *>(&v);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            q[p] = ring[(((slot * 2 + which) * V + i) * P + p) * NT + t];
+        return v;
+    };
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k)
+        fetch(blockIdx.x + k * G, k);
+    Vec8<W> w[V];
+    float2 dw[V][4], db[V][4];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (t + NT * i);
+        w[i] = c < d ? load_params(weight + c) : Vec8<W>::zero();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            dw[i][j] = db[i][j] = make_float2(0.f, 0.f);
+    }
+    int slot = 0, k = 0;
+    float mean = mean_in[blockIdx.x], rstd = rstd_in[blockIdx.x];
+    for (int64_t r = blockIdx.x; r < rows; r += G, k ^= 1) {
+        // the slot read in the round before: this thread is done with it
+        fetch(r + (S - 1) * G, slot == 0 ? S - 1 : slot - 1);
+        const float2 m2 = make_float2(mean, mean), r2 = make_float2(rstd, rstd);
+        if (r + G < rows) {
+            mean = mean_in[r + G];
+            rstd = rstd_in[r + G];
+        }
+        copy_wait<S - 1>();
+        float2 a2 = make_float2(0.f, 0.f), b2 = a2;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (8 * (t + NT * i) >= d)
+                continue;
+            const Vec8<T> x = held(slot, 0, i), y = held(slot, 1, i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 dy = y.pair(j), h = mul2(sub2(x.pair(j), m2), r2);
+                db[i][j] = add2(db[i][j], dy);
+                dw[i][j] = fma2(dy, h, dw[i][j]);
+                const float2 g = mul2(dy, w[i].pair(j));
+                a2 = add2(a2, g);
+                b2 = fma2(g, h, b2);
+            }
+        }
+        float a = warp_sum(a2.x + a2.y), b = warp_sum(b2.x + b2.y);
+        if constexpr (NW > 1) {
+            if ((t & 31) == 0)
+                red[k][t >> 5] = make_float2(a, b);
+            __syncthreads();
+            const float2 s = red[k][t & (NW - 1)];
+            a = s.x;
+            b = s.y;
+#pragma unroll
+            for (int o = NW / 2; o > 0; o >>= 1) {
+                a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+                b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            }
+        }
+        const float n = static_cast<float>(d);
+        const float2 ma = make_float2(-a / n, -a / n), mb = make_float2(-b / n, -b / n);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = 8 * (t + NT * i);
+            if (c >= d)
+                continue;
+            const Vec8<T> x = held(slot, 0, i), y = held(slot, 1, i);
+            Vec8<T> o;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 h = mul2(sub2(x.pair(j), m2), r2);
+                o.put(j, mul2(r2, fma2(h, mb, fma2(y.pair(j), w[i].pair(j), ma))));
+            }
+            o.store(grad_in + r * d + c);
+        }
+        slot = slot == S - 1 ? 0 : slot + 1;
+    }
+    float *pw = part + static_cast<int64_t>(blockIdx.x) * d, *pb = pw + G * d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (t + NT * i);
+        if (c >= d)
+            continue;
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            *reinterpret_cast<float4 *>(pw + c + 2 * j) =
+                make_float4(dw[i][j].x, dw[i][j].y, dw[i][j + 1].x, dw[i][j + 1].y);
+            *reinterpret_cast<float4 *>(pb + c + 2 * j) =
+                make_float4(db[i][j].x, db[i][j].y, db[i][j + 1].x, db[i][j + 1].y);
+        }
     }
 }
 
@@ -169,10 +416,61 @@ template <class F> int with_types(int dtype, int param_dtype, F f) {
     });
 }
 
-// Rows whose shares are added up apart before the second kernel joins them.
+// CTAs whose shares of the parameters' gradients the second kernel joins: as
+// many as run at once (512 threads per SM).
 int64_t shares(int64_t T, int64_t d) {
-    (void)d;
-    return std::min<int64_t>(T, int64_t(device_sm_count()) * 2);
+    const int64_t per_sm = d <= 1024 ? 8 : d <= 2048 ? 4 : d <= 4096 ? 2 : 1;
+    return std::min<int64_t>(T, device_sm_count() * per_sm);
+}
+
+template <int N> using Const = std::integral_constant<int, N>;
+
+// Calls f(integral constants TPR, V) for the forward pass over rows of nv
+// vectors; false when no CTA holds such a row.
+template <class F> bool with_forward(int64_t nv, int *rc, F f) {
+    if (nv <= 32)
+        *rc = f(Const<32>{}, Const<1>{});
+    else if (nv <= 64)
+        *rc = f(Const<32>{}, Const<2>{});
+    else if (nv <= 128)
+        *rc = f(Const<32>{}, Const<4>{});
+    else if (nv <= 256)
+        *rc = f(Const<128>{}, Const<2>{});
+    else if (nv <= 512)
+        *rc = f(Const<256>{}, Const<2>{});
+    else if (nv <= 1024)
+        *rc = f(Const<512>{}, Const<2>{});
+    else if (nv <= 2048)
+        *rc = f(Const<512>{}, Const<4>{});
+    else if (nv <= 4096)
+        *rc = f(Const<1024>{}, Const<4>{});
+    else
+        return false;
+    return true;
+}
+
+// The same of the backward pass, with S ring slots: the CTAs of one SM, 512
+// threads, share its shared memory.
+template <int SIZE, class F> bool with_backward(int64_t nv, int *rc, F f) {
+    if (nv <= 64)
+        *rc = f(Const<64>{}, Const<1>{}, Const<4>{});
+    else if (nv <= 128)
+        *rc = f(Const<64>{}, Const<2>{}, Const<SIZE == 2 ? 5 : 3>{});
+    else if (nv <= 256)
+        *rc = f(Const<128>{}, Const<2>{}, Const<SIZE == 2 ? 6 : 3>{});
+    else if (nv <= 512)
+        *rc = f(Const<256>{}, Const<2>{}, Const<SIZE == 2 ? 6 : 3>{});
+    else if (nv <= 1024)
+        *rc = f(Const<512>{}, Const<2>{}, Const<SIZE == 2 ? 6 : 3>{});
+    else {
+        if constexpr (SIZE == 2)
+            if (nv <= 2048) {
+                *rc = f(Const<512>{}, Const<4>{}, Const<3>{});
+                return true;
+            }
+        return false;
+    }
+    return true;
 }
 
 }  // namespace
@@ -197,9 +495,24 @@ extern "C" int layer_norm(void *out, float *mean, float *rstd, const void *in, c
     if ((rc = check_regions(r, 6)) != GATED_ACT_OK)
         return rc;
     const int64_t grid = std::min<int64_t>(T, int64_t(device_sm_count()) * 64);
+    const bool vec = d % 8 == 0 && row_stride % 8 == 0 && aligned(r[0].dev, 16) &&
+                     aligned(r[3].dev, 16) && aligned(r[4].dev, 16) && aligned(r[5].dev, 16) &&
+                     T <= 0x7FFFFFFF;
     return with_types(dtype, param_dtype, [&](auto t, auto w) {
         using E = decltype(t);
         using W = decltype(w);
+        const auto go = [&](auto tpr, auto v) {
+            constexpr int NT = tpr() > 128 ? tpr() : 128;
+            return launched(launch_kernel(
+                ln_forward_vec<E, W, tpr(), v()>,
+                dim3(static_cast<unsigned>(ceil_div64(T, NT / tpr()))), dim3(NT), 0, stream, 1,
+                as<E>(r[0]), as<float>(r[1]), as<float>(r[2]), as<const E>(r[3]),
+                as<const W>(r[4]), as<const W>(r[5]), T, static_cast<int>(d), row_stride,
+                static_cast<float>(eps)));
+        };
+        int done;
+        if (vec && with_forward(d / 8, &done, go))
+            return done;
         return launched(launch_kernel(ln_forward_any<E, W>, dim3(static_cast<unsigned>(grid)),
                                       dim3(kThreads), 0, stream, 1, as<E>(r[0]), as<float>(r[1]),
                                       as<float>(r[2]), as<const E>(r[3]), as<const W>(r[4]),
@@ -242,21 +555,37 @@ extern "C" int layer_norm_backward(void *grad_in, float *grad_weight, float *gra
     float *part = as<float>(r[3]);
     int64_t n = 0;
     if (T > 0) {
-        const int64_t per = ceil_div64(T, shares(T, d));
-        n = ceil_div64(T, per);
-        const int64_t grid = std::min<int64_t>(T, int64_t(device_sm_count()) * 64);
+        const bool vec = d % 8 == 0 && row_stride % 8 == 0 && grad_stride % 8 == 0 &&
+                         aligned(r[0].dev, 16) && aligned(r[4].dev, 16) && aligned(r[5].dev, 16) &&
+                         aligned(r[6].dev, 16);
         rc = with_types(dtype, param_dtype, [&](auto t, auto w) {
             using E = decltype(t);
             using W = decltype(w);
-            return launched(launch_kernel(
+            const auto go = [&](auto nt, auto v, auto slots) {
+                constexpr size_t smem = 2 * slots() * v() * nt() * 8 * sizeof(E);
+                const auto kernel = ln_backward_vec<E, W, nt(), v(), slots()>;
+                const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
+                if (e != cudaSuccess)
+                    return cuda_status(e);
+                n = shares(T, d);
+                return launched(launch_kernel(
+                    kernel, dim3(static_cast<unsigned>(n)), dim3(nt()), smem, stream, 1,
+                    as<E>(r[0]), part, as<const E>(r[4]), as<const E>(r[5]), as<const W>(r[6]),
+                    as<const float>(r[7]), as<const float>(r[8]), T, static_cast<int>(d),
+                    row_stride, grad_stride));
+            };
+            int done;
+            if (vec && with_backward<sizeof(E)>(d / 8, &done, go))
+                return done;
+            const int64_t grid = std::min<int64_t>(T, int64_t(device_sm_count()) * 64);
+            done = launched(launch_kernel(
                 ln_backward_rows_any<E, W>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
                 stream, 1, as<E>(r[0]), as<const E>(r[4]), as<const E>(r[5]), as<const W>(r[6]),
                 as<const float>(r[7]), as<const float>(r[8]), T, d, row_stride, grad_stride));
-        });
-        if (rc != GATED_ACT_OK)
-            return rc;
-        rc = with_type(dtype, [&](auto t) {
-            using E = decltype(t);
+            if (done != GATED_ACT_OK)
+                return done;
+            const int64_t per = ceil_div64(T, shares(T, d));
+            n = ceil_div64(T, per);
             return launched(launch_kernel(
                 ln_backward_columns_any<E>,
                 dim3(static_cast<unsigned>(ceil_div64(d, kThreads)), static_cast<unsigned>(n)),

@@ -304,6 +304,17 @@ template <class F> inline int with_type(int dtype, F f) {
     }
 }
 
+// Lets `kernel` launch with `bytes` of dynamic shared memory (and up to 1 KB
+// of static).  Above the default 48 KB that takes an attribute of the kernel,
+// set before each launch: a host-side call, with nothing kept per device or
+// context.
+inline cudaError_t allow_smem(const void *kernel, size_t bytes) {
+    if (bytes <= 47 * 1024)
+        return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(bytes));
+}
+
 inline int launched(cudaError_t e) {
     return cuda_status(e != cudaSuccess ? e : cudaGetLastError());
 }
