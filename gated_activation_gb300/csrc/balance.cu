@@ -4,12 +4,19 @@
 // The forward pass reads the logits and the chosen ids once, the backward
 // pass reads the logits again (a softmax is recomputed in registers rather
 // than stored) and writes their gradient: HBM or L2 bandwidth bounds long
-// batches, launch latency short ones.  One warp takes a token: lane l holds
-// the logits l, l + 32, ... so any row start is one contiguous run per
-// access.  The sums over tokens are kept per lane in registers, joined per CTA
-// in shared memory in warp order, and over the CTAs by a second kernel in
-// CTA order; the counts are integers, so their atomics give the same result
-// in any order.
+// batches, launch latency short ones.
+//
+// Tokens: L lanes share a token, each holding V groups of kLane elements of
+// its logits (rows in 16-byte vectors: 8 consecutive elements per group; any
+// other layout: one, and L = 32, so that every access of a warp is one
+// contiguous run).  The probabilities are summed over tokens per lane in
+// registers, over the lanes and warps of a CTA in shared memory, and over the
+// CTAs in CTA order; the counts are integers, whose atomics give the same
+// result in any order.
+//
+// Up to kClusterTokens tokens take one launch, a cluster of 8 CTAs that joins its
+// sums through distributed shared memory; longer batches write each CTA's
+// sums to the workspace, and a second kernel, one such cluster, joins them.
 #include <algorithm>
 
 #include "training.cuh"
@@ -20,189 +27,359 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxExperts = 1024;
+constexpr int kCluster = 8;
 
-// Softmax of one token's logits, held V per lane; a row with no finite
-// maximum above -infinity gives 0 everywhere.
-template <int V>
-__device__ __forceinline__ void softmax_row(float (&p)[V]) {
-    float top = p[0];
+// ------------------------------------------------------------------- tokens
+
+// The logits of one token held by one lane, V groups of N: group i starts at
+// element (i * L + lane) * N.
+template <class T, int L, int V, int N> struct Row {
+    float x[V * N];
+
+    __device__ static int column(int lane, int i) { return (i / N * L + lane) * N + i % N; }
+
+    __device__ void load(const T *row, int E, int lane) {
 #pragma unroll
-    for (int i = 1; i < V; ++i)
-        top = fmaxf(top, p[i]);
+        for (int i = 0; i < V; ++i) {
+            const int c = (i * L + lane) * N;
+            if constexpr (N == 8) {
+                if (c < E) {
+                    const Vec8<T> v = Vec8<T>::load(row + c);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    // fmaxf skips NaN; exp of a NaN logit stays NaN and reaches the sum
-    const float shift = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = v.pair(j);
+                        x[8 * i + 2 * j] = f.x;
+                        x[8 * i + 2 * j + 1] = f.y;
+                    }
+                } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        p[i] = __expf(p[i] - shift);
-        sum += p[i];
+                    for (int j = 0; j < 8; ++j)
+                        x[8 * i + j] = -INFINITY;
+                }
+            } else {
+                x[i] = c < E ? to_float(row[c]) : -INFINITY;
+            }
+        }
     }
-    sum = warp_sum(sum);
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        p[i] *= inv;
-}
 
-template <class T, int V>
-__device__ __forceinline__ void load_row(float (&p)[V], const T *row, int E, int lane) {
+    // In place; a token whose logits are all -infinity gets 0 everywhere.
+    __device__ void softmax() {
+        float top = x[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane + 32 * i;
-        p[i] = e < E ? to_float(row[e]) : -INFINITY;
+        for (int i = 1; i < V * N; ++i)
+            top = fmaxf(top, x[i]);
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        // fmaxf skips a NaN; the exponential of a NaN logit brings it back
+        const float shift = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V * N; ++i) {
+            x[i] = __expf(x[i] - shift);
+            sum += x[i];
+        }
+        sum = total(sum);
+        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll
+        for (int i = 0; i < V * N; ++i)
+            x[i] *= inv;
     }
-}
 
-// CTA b takes the tokens [b * per, (b + 1) * per).  part_p [G][E] fp32,
-// part_c [G][E + 1] int32 (the last: live tokens).
-template <class T, class I, int V>
-__global__ void __launch_bounds__(kThreads)
-balance_rows(float *__restrict__ part_p, int32_t *__restrict__ part_c,
-             const T *__restrict__ logits, const I *__restrict__ ids,
-             const uint8_t *__restrict__ live, int64_t tokens, int64_t per, int E, int64_t k,
-             int64_t ls) {
-    extern __shared__ float sums[];                              // [kWarps][E]
-    int *hist = reinterpret_cast<int *>(sums + kWarps * E);      // [E + 1]
+    __device__ static float total(float v) {
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1)
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        return v;
+    }
+
+    __device__ void store(T *row, int E, int lane) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = (i * L + lane) * N;
+            if (c >= E)
+                continue;
+            if constexpr (N == 8) {
+                Vec8<T> v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v.put(j, make_float2(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]));
+                v.store(row + c);
+            } else {
+                row[c] = from_float<T>(x[i]);
+            }
+        }
+    }
+};
+
+// The chosen ids, int32 or int64.
+struct Ids {
+    const void *p;
+    int wide;
+    __device__ int64_t at(int64_t i) const {
+        return wide ? __ldg(static_cast<const long long *>(p) + i)
+                    : static_cast<int64_t>(__ldg(static_cast<const int *>(p) + i));
+    }
+};
+
+// Sums of the tokens [t0, t1) into shared memory: sums [kWarps][E] (a row per
+// warp), hist [E + 1] counts and live tokens.  Ends with a barrier.
+template <class T, int L, int V, int N>
+__device__ __forceinline__ void sum_tokens(float *sums, int *hist, const T *logits, Ids ids,
+                                           const uint8_t *live, int64_t t0, int64_t t1, int E,
+                                           int k, int64_t ls) {
+    constexpr int kTokens = 32 / L;       // tokens of a warp at a time
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int part = lane / L, sub = lane % L;
+    float acc[V * N];
+#pragma unroll
+    for (int i = 0; i < V * N; ++i)
+        acc[i] = 0.f;
+    int mine = 0;
+    // every lane takes part in the shuffles of every round
+    for (int64_t t = t0 + warp * kTokens; t < t1; t += kWarps * kTokens) {
+        const bool on = t + part < t1 && (!live || live[t + part]);
+        Row<T, L, V, N> p;
+        p.load(logits + (t + part) * ls, on ? E : 0, sub);
+        p.softmax();
+        if (on) {
+            mine += sub == 0;
+#pragma unroll
+            for (int i = 0; i < V * N; ++i)
+                acc[i] += p.x[i];
+        }
+    }
+    const int64_t first = t0 * k, n = (t1 - t0) * k;
+    for (int64_t j = threadIdx.x; j < n; j += kThreads) {
+        const int64_t e = ids.at(first + j);
+        if (e >= 0 && e < E && (!live || live[t0 + static_cast<uint32_t>(j) / static_cast<uint32_t>(k)]))
+            atomicAdd(hist + e, 1);
+    }
+    mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+    if (lane == 0 && mine)
+        atomicAdd(hist + E, mine);
+#pragma unroll
+    for (int i = 0; i < V * N; ++i) {
+        float a = acc[i];
+#pragma unroll
+        for (int o = L; o < 32; o <<= 1)
+            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        const int c = Row<T, L, V, N>::column(sub, i);
+        if (part == 0 && c < E)
+            sums[warp * E + c] = a;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ float warps_sum(const float *sums, int E, int e) {
+    float s = sums[e];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w)
+        s += sums[w * E + e];
+    return s;
+}
+
+// ------------------------------------------------------------- the cluster
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of the same shared-memory variable in another CTA of the cluster.
+__device__ __forceinline__ uint32_t peer(const void *p, uint32_t rank) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), v;
+    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// The CTA's share of sum_e c_e p_e, joined over the cluster: rank 0 writes
+// the loss.  `mine`: the thread's term.
+__device__ __forceinline__ void write_loss(float *loss, float *share, float *red, float mine,
+                                           float scale, uint32_t rank) {
+    mine = warp_sum(mine);
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = mine;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float s = 0.f;
+        for (int w = 0; w < kWarps; ++w)
+            s += red[w];
+        *share = s;
+    }
+    cluster_sync();
+    if (rank == 0 && threadIdx.x == 0) {
+        float s = 0.f;
+        for (int c = 0; c < kCluster; ++c)
+            s += __uint_as_float(peer(share, c));
+        loss[0] = s * scale;
+    }
+    cluster_sync();   // no CTA leaves while its share is read
+}
+
+// One launch: the cluster's CTAs take `per` tokens each, then E / 8 experts.
+template <class T, int L, int V, int N>
+__global__ void __launch_bounds__(kThreads)
+balance_cluster(float *__restrict__ loss, int32_t *__restrict__ counts,
+                int32_t *__restrict__ tokens, float *__restrict__ mean_p,
+                const T *__restrict__ logits, Ids ids,
+                const uint8_t *__restrict__ live, int64_t T_, int64_t per, int E, int k,
+                int64_t ls, float coef) {
+    extern __shared__ float sums[];                            // [kWarps][E]
+    int *hist = reinterpret_cast<int *>(sums + kWarps * E);    // [E + 1]
+    __shared__ float share, red[kWarps];
     for (int e = threadIdx.x; e <= E; e += kThreads)
         hist[e] = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    const int64_t t0 = blockIdx.x * per, t1 = min(tokens, t0 + per);
-    float acc[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        acc[i] = 0.f;
-    int mine = 0;
-    for (int64_t t = t0 + warp; t < t1; t += kWarps) {
-        if (live && !live[t])
-            continue;
-        ++mine;
-        float p[V];
-        load_row<T, V>(p, logits + t * ls, E, lane);
-        softmax_row<V>(p);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            acc[i] += p[i];
-        for (int64_t j = lane; j < k; j += 32) {
-            const int64_t e = static_cast<int64_t>(ids[t * k + j]);
-            if (e >= 0 && e < E)
-                atomicAdd(hist + e, 1);
+    const uint32_t rank = cluster_rank();
+    const int64_t t0 = min(T_, rank * per), t1 = min(T_, t0 + per);
+    sum_tokens<T, L, V, N>(sums, hist, logits, ids, live, t0, t1, E, k, ls);
+    for (int e = threadIdx.x; e < E; e += kThreads)
+        sums[e] = warps_sum(sums, E, e);                       // only this thread reads column e
+    cluster_sync();
+    int n = 0;
+    for (int c = 0; c < kCluster; ++c)
+        n += static_cast<int>(peer(hist + E, c));
+    const float nf = static_cast<float>(n > 0 ? n : 1);
+    float mine = 0.f;
+    for (int e = rank + kCluster * threadIdx.x; e < E; e += kCluster * kThreads) {
+        float p = 0.f;
+        int c = 0;
+        for (int r = 0; r < kCluster; ++r) {
+            p += __uint_as_float(peer(sums + e, r));
+            c += static_cast<int>(peer(hist + e, r));
         }
+        p /= nf;
+        counts[e] = c;
+        mean_p[e] = p;
+        mine = fmaf(static_cast<float>(c), p, mine);
     }
-    if (lane == 0)
-        atomicAdd(hist + E, mine);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (lane + 32 * i < E)
-            sums[warp * E + lane + 32 * i] = acc[i];
+    if (rank == 0 && threadIdx.x == 0)
+        tokens[0] = n;
+    write_loss(loss, &share, red, mine,
+               coef * static_cast<float>(E) / (nf * static_cast<float>(k)), rank);
+}
+
+// Long batches: CTA b of G takes the tokens [b * per, (b + 1) * per) and leaves
+// its sums in the workspace, an expert's G of them side by side:
+// part_p [E][G] fp32, part_c [E + 1][G] int32 (the last: live tokens).
+template <class T, int L, int V, int N>
+__global__ void __launch_bounds__(kThreads)
+balance_tokens(float *__restrict__ part_p, int32_t *__restrict__ part_c,
+               const T *__restrict__ logits, Ids ids,
+               const uint8_t *__restrict__ live, int64_t T_, int64_t per, int E, int k,
+               int64_t ls) {
+    extern __shared__ float sums[];
+    int *hist = reinterpret_cast<int *>(sums + kWarps * E);
+    for (int e = threadIdx.x; e <= E; e += kThreads)
+        hist[e] = 0;
     __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const int64_t t0 = min(T_, blockIdx.x * per), t1 = min(T_, t0 + per);
+    sum_tokens<T, L, V, N>(sums, hist, logits, ids, live, t0, t1, E, k, ls);
+    const int64_t G = gridDim.x;
     for (int e = threadIdx.x; e <= E; e += kThreads) {
-        part_c[static_cast<int64_t>(blockIdx.x) * (E + 1) + e] = hist[e];
-        if (e < E) {
-            float s = 0.f;
-            for (int w = 0; w < kWarps; ++w)
-                s += sums[w * E + e];
-            part_p[static_cast<int64_t>(blockIdx.x) * E + e] = s;
-        }
+        part_c[e * G + blockIdx.x] = hist[e];
+        if (e < E)
+            part_p[e * G + blockIdx.x] = warps_sum(sums, E, e);
     }
 }
 
-// Joins the G partial sums: one CTA, thread e the expert e.
-__global__ void __launch_bounds__(kMaxExperts)
+// Joins the G sums of every expert: a warp takes an expert.
+__global__ void __launch_bounds__(kThreads)
 balance_join(float *__restrict__ loss, int32_t *__restrict__ counts, int32_t *__restrict__ tokens,
              float *__restrict__ mean_p, const float *__restrict__ part_p,
              const int32_t *__restrict__ part_c, int G, int E, float k, float coef) {
-    __shared__ float red[32];
-    __shared__ int live;
+    __shared__ float share, red[kWarps];
     pdl_wait();
     pdl_trigger();
-    const int e = threadIdx.x, lane = e & 31;
-    if (e == 0)
-        live = 0;
-    __syncthreads();
+    const uint32_t rank = cluster_rank();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int n = 0;
-    for (int g = e; g < G; g += blockDim.x)
-        n += part_c[static_cast<int64_t>(g) * (E + 1) + E];
-    if (n)
-        atomicAdd(&live, n);
-    float p = 0.f;
-    int c = 0;
-    if (e < E)
-        for (int g = 0; g < G; ++g) {
-            p += part_p[static_cast<int64_t>(g) * E + e];
-            c += part_c[static_cast<int64_t>(g) * (E + 1) + e];
-        }
-    __syncthreads();
-    n = live;
+    for (int g = lane; g < G; g += 32)
+        n += part_c[static_cast<int64_t>(E) * G + g];
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
     const float nf = static_cast<float>(n > 0 ? n : 1);
-    p /= nf;
-    if (e < E) {
-        counts[e] = c;
-        mean_p[e] = p;
-    }
-    float s = warp_sum(e < E ? static_cast<float>(c) / (nf * k) * p : 0.f);
-    if (lane == 0)
-        red[e >> 5] = s;
-    __syncthreads();
-    if (e < 32) {
-        s = warp_sum(e < static_cast<int>(blockDim.x) / 32 ? red[e] : 0.f);
-        if (e == 0) {
-            loss[0] = coef * static_cast<float>(E) * s;
-            tokens[0] = n;
+    float mine = 0.f;
+    for (int e = rank * kWarps + warp; e < E; e += kCluster * kWarps) {
+        float p = 0.f;
+        int c = 0;
+#pragma unroll 4
+        for (int g = lane; g < G; g += 32) {
+            p += part_p[static_cast<int64_t>(e) * G + g];
+            c += part_c[static_cast<int64_t>(e) * G + g];
+        }
+        p = warp_sum(p) / nf;
+        c = __reduce_add_sync(0xFFFFFFFFu, c);
+        if (lane == 0) {
+            counts[e] = c;
+            mean_p[e] = p;
+            mine = fmaf(static_cast<float>(c), p, mine);
         }
     }
+    if (rank == 0 && threadIdx.x == 0)
+        tokens[0] = n;
+    write_loss(loss, &share, red, mine, coef * static_cast<float>(E) / (nf * k), rank);
 }
 
-// Counts enter as c_j - C/E, C their sum: the same gradient, since p sums to
-// 1, without the cancellation of nearly equal counts.
-template <class T, int V>
+// Counts enter as c_j - C / E, C their sum, rounded to an integer: the same
+// gradient, since p sums to 1, without the cancellation of nearly equal counts.
+template <class T, int L, int V, int N>
 __global__ void __launch_bounds__(kThreads)
 balance_backward(T *__restrict__ grad, const float *__restrict__ grad_loss,
                  const T *__restrict__ logits, const int32_t *__restrict__ counts,
-                 const int32_t *__restrict__ tokens_live, const uint8_t *__restrict__ live,
-                 int64_t tokens, int E, float k, int64_t ls, float coef) {
+                 const int32_t *__restrict__ tokens, const uint8_t *__restrict__ live, int64_t T_,
+                 int E, float k, int64_t ls, float coef) {
+    using R = Row<T, L, V, N>;
+    constexpr int kTokens = 32 / L;
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    float c[V], total = 0.f;
+    const int lane = threadIdx.x & 31, part = lane / L, sub = lane % L;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kTokens;
+    int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kTokens + part;
+    float c[V * N], sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane + 32 * i;
-        c[i] = e < E ? static_cast<float>(counts[e]) : 0.f;
-        total += c[i];
+    for (int i = 0; i < V * N; ++i) {
+        const int e = R::column(sub, i);
+        c[i] = e < E ? static_cast<float>(__ldg(counts + e)) : 0.f;
+        sum += c[i];
     }
-    const float mid = rintf(warp_sum(total) / static_cast<float>(E));
+    const float mid = rintf(R::total(sum) / static_cast<float>(E));
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V * N; ++i)
         c[i] -= mid;
-    const int n = *tokens_live;
+    const int n = *tokens;
     const float nf = static_cast<float>(n > 0 ? n : 1);
     const float scale = *grad_loss * (coef * static_cast<float>(E) / (nf * nf * k));
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < tokens;
-         t += step) {
-        const bool on = !live || live[t];
-        float p[V], mixed = 0.f;
-        if (on) {
-            load_row<T, V>(p, logits + t * ls, E, lane);
-            softmax_row<V>(p);
+    // every lane takes part in the shuffles of every round
+    for (; t - part < T_; t += step) {
+        const bool in = t < T_, on = in && (!live || live[t]);
+        R p;
+        p.load(logits + t * ls, on ? E : 0, sub);
+        p.softmax();
+        float mixed = 0.f;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                mixed = fmaf(p[i], c[i], mixed);
-            mixed = warp_sum(mixed);
-        }
+        for (int i = 0; i < V * N; ++i)
+            mixed = fmaf(p.x[i], c[i], mixed);
+        mixed = R::total(mixed);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (lane + 32 * i < E)
-                grad[t * E + lane + 32 * i] =
-                    from_float<T>(on ? scale * p[i] * (c[i] - mixed) : 0.f);
+        for (int i = 0; i < V * N; ++i)
+            p.x[i] = on ? scale * p.x[i] * (c[i] - mixed) : 0.f;
+        if (in)
+            p.store(grad + t * E, E, sub);
     }
 }
+
+// -------------------------------------------------------------- host side
 
 int check_sizes(int64_t T, int64_t E, int64_t k, int64_t ls, int dtype) {
     if (T < 0 || E <= 0 || k <= 0)
@@ -217,30 +394,42 @@ int check_sizes(int64_t T, int64_t E, int64_t k, int64_t ls, int dtype) {
     return GATED_ACT_OK;
 }
 
-// Calls f(integral_constant<V>) with the smallest V in 1, 2, 4, .. for which
-// 32 V >= E.
-template <int V> struct Lanes {
-    static constexpr int value = V;
-};
-template <class F> int with_lanes(int64_t E, F f) {
-    return E <= 32    ? f(Lanes<1>{})
-           : E <= 64  ? f(Lanes<2>{})
-           : E <= 128 ? f(Lanes<4>{})
-           : E <= 256 ? f(Lanes<8>{})
-           : E <= 512 ? f(Lanes<16>{})
-                      : f(Lanes<32>{});
+template <int N> using Const = std::integral_constant<int, N>;
+
+// Calls f(integral constants L, V, N) for E experts: vectors of 8 with the
+// fewest lanes that hold a row, or single elements.
+template <class F> int with_lanes(int64_t E, bool vec, F f) {
+    if (vec)
+        return E <= 8     ? f(Const<1>{}, Const<1>{}, Const<8>{})
+               : E <= 16  ? f(Const<2>{}, Const<1>{}, Const<8>{})
+               : E <= 32  ? f(Const<4>{}, Const<1>{}, Const<8>{})
+               : E <= 64  ? f(Const<8>{}, Const<1>{}, Const<8>{})
+               : E <= 128 ? f(Const<16>{}, Const<1>{}, Const<8>{})
+               : E <= 256 ? f(Const<32>{}, Const<1>{}, Const<8>{})
+               : E <= 512 ? f(Const<32>{}, Const<2>{}, Const<8>{})
+                          : f(Const<32>{}, Const<4>{}, Const<8>{});
+    return E <= 32    ? f(Const<32>{}, Const<1>{}, Const<1>{})
+           : E <= 64  ? f(Const<32>{}, Const<2>{}, Const<1>{})
+           : E <= 128 ? f(Const<32>{}, Const<4>{}, Const<1>{})
+           : E <= 256 ? f(Const<32>{}, Const<8>{}, Const<1>{})
+           : E <= 512 ? f(Const<32>{}, Const<16>{}, Const<1>{})
+                      : f(Const<32>{}, Const<32>{}, Const<1>{});
 }
 
+// Batches of up to this many tokens take the one-launch cluster.
+constexpr int64_t kClusterTokens = 512;
+
+// CTAs that a longer batch's tokens are split over: two per SM, at least 32
+// tokens each.
 int64_t parts(int64_t T) {
-    return std::max<int64_t>(1, std::min<int64_t>(ceil_div64(T, kWarps * 4),
-                                                  device_sm_count()));
+    return std::max<int64_t>(1, std::min<int64_t>(ceil_div64(T, 32), device_sm_count() * 2));
 }
 
 }  // namespace
 }  // namespace gact
 
 extern "C" size_t moe_balance_loss_workspace_bytes(int64_t T, int64_t E) {
-    if (T < 0 || E <= 0 || E > gact::kMaxExperts)
+    if (T <= gact::kClusterTokens || E <= 0 || E > gact::kMaxExperts)
         return 16;
     return static_cast<size_t>((gact::parts(T) * (2 * E + 1) * 4 + 15) / 16 * 16);
 }
@@ -268,35 +457,36 @@ extern "C" int moe_balance_loss(float *loss, int32_t *counts, int32_t *tokens, f
                    {live, live ? static_cast<uint64_t>(T) : 0, 1, false}};
     if ((rc = check_regions(r, 8)) != GATED_ACT_OK)
         return rc;
-    const int64_t per = std::max<int64_t>(1, ceil_div64(T, parts(T)));
-    const int64_t G = ceil_div64(T, per);
+    const bool vec = E % 8 == 0 && logits_stride % 8 == 0 && aligned(r[5].dev, 16);
+    const bool cluster = T <= kClusterTokens;
+    const int64_t G = cluster ? kCluster : parts(T), per = ceil_div64(T, G);
     float *part_p = as<float>(r[4]);
     int32_t *part_c = reinterpret_cast<int32_t *>(part_p + G * E);
-    if (G > 0) {
-        rc = with_type(dtype, [&](auto t) {
-            return with_lanes(E, [&](auto lanes) {
-                using Elem = decltype(t);
-                constexpr int V = decltype(lanes)::value;
-                const size_t smem = (kWarps * E + E + 1) * 4;
-                const auto go = [&](auto id) {
-                    using I = decltype(id);
-                    return launched(launch_kernel(
-                        balance_rows<Elem, I, V>, dim3(static_cast<unsigned>(G)), dim3(kThreads),
-                        smem, stream, 1, part_p, part_c, as<const Elem>(r[5]), as<const I>(r[6]),
-                        as<const uint8_t>(r[7]), T, per, static_cast<int>(E), k, logits_stride));
-                };
-                return ids64 ? go(int64_t{}) : go(int32_t{});
-            });
+    const int Ei = static_cast<int>(E), ki = static_cast<int>(k);
+    const float c = static_cast<float>(coef);
+    const Ids chosen = {r[6].dev, ids64};
+    rc = with_type(dtype, [&](auto t) {
+        return with_lanes(E, vec, [&](auto l, auto v, auto n) {
+            using Elem = decltype(t);
+            const size_t smem = (kWarps * E + E + 1) * 4;
+            if (cluster)
+                return launched(launch_kernel(
+                    balance_cluster<Elem, l(), v(), n()>, dim3(kCluster), dim3(kThreads), smem,
+                    stream, kCluster, as<float>(r[0]), as<int32_t>(r[1]), as<int32_t>(r[2]),
+                    as<float>(r[3]), as<const Elem>(r[5]), chosen, as<const uint8_t>(r[7]), T,
+                    per, Ei, ki, logits_stride, c));
+            return launched(launch_kernel(
+                balance_tokens<Elem, l(), v(), n()>, dim3(static_cast<unsigned>(G)),
+                dim3(kThreads), smem, stream, 1, part_p, part_c, as<const Elem>(r[5]), chosen,
+                as<const uint8_t>(r[7]), T, per, Ei, ki, logits_stride));
         });
-        if (rc != GATED_ACT_OK)
-            return rc;
-    }
+    });
+    if (rc != GATED_ACT_OK || cluster)
+        return rc;
     return launched(launch_kernel(
-        balance_join, dim3(1), dim3(static_cast<unsigned>(ceil_div64(E, 32) * 32)), 0, stream, 1,
-        as<float>(r[0]), as<int32_t>(r[1]), as<int32_t>(r[2]), as<float>(r[3]),
-        static_cast<const float *>(part_p), static_cast<const int32_t *>(part_c),
-        static_cast<int>(G), static_cast<int>(E), static_cast<float>(k),
-        static_cast<float>(coef)));
+        balance_join, dim3(kCluster), dim3(kThreads), 0, stream, kCluster, as<float>(r[0]),
+        as<int32_t>(r[1]), as<int32_t>(r[2]), as<float>(r[3]), static_cast<const float *>(part_p),
+        static_cast<const int32_t *>(part_c), static_cast<int>(G), Ei, static_cast<float>(k), c));
 }
 
 extern "C" int moe_balance_loss_backward(void *grad_logits, const float *grad_loss,
@@ -317,17 +507,19 @@ extern "C" int moe_balance_loss_backward(void *grad_logits, const float *grad_lo
                    {live, live ? static_cast<uint64_t>(T) : 0, 1, false}};
     if ((rc = check_regions(r, 6)) != GATED_ACT_OK)
         return rc;
-    const int64_t grid = std::min<int64_t>(ceil_div64(T, kWarps), int64_t(device_sm_count()) * 8);
+    const bool vec = E % 8 == 0 && logits_stride % 8 == 0 && aligned(r[0].dev, 16) &&
+                     aligned(r[2].dev, 16);
     return with_type(dtype, [&](auto t) {
-        return with_lanes(E, [&](auto lanes) {
+        return with_lanes(E, vec, [&](auto l, auto v, auto n) {
             using Elem = decltype(t);
-            constexpr int V = decltype(lanes)::value;
+            const int64_t grid = std::min<int64_t>(ceil_div64(T, kWarps * (32 / l())),
+                                                   int64_t(device_sm_count()) * 8);
             return launched(launch_kernel(
-                balance_backward<Elem, V>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
-                stream, 1, as<Elem>(r[0]), as<const float>(r[1]), as<const Elem>(r[2]),
-                as<const int32_t>(r[3]), as<const int32_t>(r[4]), as<const uint8_t>(r[5]), T,
-                static_cast<int>(E), static_cast<float>(k), logits_stride,
-                static_cast<float>(coef)));
+                balance_backward<Elem, l(), v(), n()>, dim3(static_cast<unsigned>(grid)),
+                dim3(kThreads), 0, stream, 1, as<Elem>(r[0]), as<const float>(r[1]),
+                as<const Elem>(r[2]), as<const int32_t>(r[3]), as<const int32_t>(r[4]),
+                as<const uint8_t>(r[5]), T, static_cast<int>(E), static_cast<float>(k),
+                logits_stride, static_cast<float>(coef)));
         });
     });
 }
