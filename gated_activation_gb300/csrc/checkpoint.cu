@@ -48,68 +48,158 @@ __device__ __forceinline__ void put_block(int8_t *codes, uint8_t *scale, float v
         *scale = static_cast<uint8_t>(s);
 }
 
-// ------------------------------------------------- elementwise, any layout
+// n / d; a 32-bit n takes the multiplication.
+template <class I> __device__ __forceinline__ I quotient(I n, I d, const FastDiv &by) {
+    if constexpr (sizeof(I) == 4)
+        return by(n);
+    else
+        return n / d;
+}
 
-template <class T, class Act>
+// ------------------------------------------------- elementwise, any layout
+//
+// A warp takes kAnyBlocks consecutive blocks of a row, one element of each per
+// lane; J = ceil(B / kAnyBlocks) such jobs make a row.
+
+constexpr int kAnyBlocks = 4;
+
+// Steps of the blocks b0, b0 + 1, ... of both halves, one per lane: lane i
+// that of block i of the gate half, lane kAnyBlocks + i of the up half.
+__device__ __forceinline__ float lane_step(const uint8_t *scales, int64_t b0, int64_t B, int lane) {
+    const int i = lane % kAnyBlocks, up = lane / kAnyBlocks;
+    return up < 2 && b0 + i < B ? code_step(__ldg(scales + up * B + b0 + i)) : 0.f;
+}
+
+template <class T, class Act, class I>
 __global__ void __launch_bounds__(kThreads)
 ckpt_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
-                 const T *__restrict__ in, int64_t M, int64_t d, int64_t rs, int64_t B,
-                 const int32_t *n_rows) {
+                 const T *__restrict__ in, int64_t M, int64_t d, int64_t rs, int64_t B, I J,
+                 FastDiv by_J, const int32_t *n_rows) {
     pdl_wait();
     pdl_trigger();
+    constexpr int U = kAnyBlocks;
     const int lane = threadIdx.x & 31;
-    const int64_t total = live_rows(M, n_rows) * B;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < total;
-         i += step) {
-        const int64_t r = i / B, b = i - r * B, c = b * kBlock + lane;
-        const bool ok = c < d;
-        const float g = ok ? to_float(in[r * rs + c]) : 0.f;
-        const float u = ok ? to_float(in[r * rs + d + c]) : 0.f;
-        if (ok)
-            out[r * d + c] = from_float<T>(act_mul<Act>(g, u));
-        put_block<false>(codes + r * 2 * d + c, scales + r * 2 * B + b, g, ok, lane);
-        put_block<false>(codes + r * 2 * d + d + c, scales + r * 2 * B + B + b, u, ok, lane);
+    const I job = static_cast<I>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const I row = quotient(job, J, by_J);
+    if (row >= live_rows(M, n_rows))      // the warp as a whole
+        return;
+    const int64_t r = row, b0 = static_cast<int64_t>(job - row * J) * U, c0 = b0 * kBlock + lane;
+    const T *p = in + r * rs + c0;
+    T graw[U], uraw[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+        if (c0 + kBlock * i < d) {
+            graw[i] = __ldg(p + kBlock * i);
+            uraw[i] = __ldg(p + d + kBlock * i);
+        }
+    T *o = out + r * d + c0;
+    int8_t *q = codes + r * 2 * d + c0;
+    uint8_t *s = scales + r * 2 * B + b0;
+#pragma unroll
+    for (int i = 0; i < U; i += 2) {
+        const bool in0 = c0 + kBlock * i < d, in1 = c0 + kBlock * (i + 1) < d;
+        const float2 g = make_float2(in0 ? to_float(graw[i]) : 0.f, in1 ? to_float(graw[i + 1]) : 0.f);
+        const float2 u = make_float2(in0 ? to_float(uraw[i]) : 0.f, in1 ? to_float(uraw[i + 1]) : 0.f);
+        const float2 y = act_mul<Act>(g, u);
+        if (b0 + i < B) {
+            if (in0)
+                o[kBlock * i] = from_float<T>(y.x);
+            put_block<false>(q + kBlock * i, s + i, g.x, in0, lane);
+            put_block<false>(q + d + kBlock * i, s + B + i, u.x, in0, lane);
+        }
+        if (b0 + i + 1 < B) {
+            if (in1)
+                o[kBlock * (i + 1)] = from_float<T>(y.y);
+            put_block<false>(q + kBlock * (i + 1), s + i + 1, g.y, in1, lane);
+            put_block<false>(q + d + kBlock * (i + 1), s + B + i + 1, u.y, in1, lane);
+        }
     }
 }
 
-template <class T, class Act>
+template <class T, class Act, class I>
 __global__ void __launch_bounds__(kThreads)
 ckpt_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
                   const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t M,
-                  int64_t d, int64_t gs, int64_t B, const int32_t *n_rows) {
+                  int64_t d, int64_t gs, int64_t B, I J, FastDiv by_J, const int32_t *n_rows) {
     pdl_wait();
     pdl_trigger();
+    constexpr int U = kAnyBlocks;
     const int lane = threadIdx.x & 31;
-    const int64_t total = live_rows(M, n_rows) * B;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < total;
-         i += step) {
-        const int64_t r = i / B, b = i - r * B, c = b * kBlock + lane;
-        if (c >= d)
-            continue;
-        const float g = codes[r * 2 * d + c] * code_step(scales[r * 2 * B + b]);
-        const float u = codes[r * 2 * d + d + c] * code_step(scales[r * 2 * B + B + b]);
-        const float dy = to_float(grad[r * gs + c]);
-        const GateGrad m = act_grad<Act>(g, u, dy);
-        grad_in[r * 2 * d + c] = from_float<T>(m.gate);
-        grad_in[r * 2 * d + d + c] = from_float<T>(m.up);
-        if (out)
-            out[r * d + c] = from_float<T>(m.out);
+    const I job = static_cast<I>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const I row = quotient(job, J, by_J);
+    if (row >= live_rows(M, n_rows))
+        return;
+    const int64_t r = row, b0 = static_cast<int64_t>(job - row * J) * U, c0 = b0 * kBlock + lane;
+    const T *dy = grad + r * gs + c0;
+    const int8_t *q = codes + r * 2 * d + c0;
+    T yraw[U];
+    int8_t qg[U], qu[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+        if (c0 + kBlock * i < d) {
+            yraw[i] = __ldg(dy + kBlock * i);
+            qg[i] = __ldg(q + kBlock * i);
+            qu[i] = __ldg(q + d + kBlock * i);
+        }
+    const float step = lane_step(scales + r * 2 * B, b0, B, lane);
+    T *gi = grad_in + r * 2 * d + c0, *o = out + r * d + c0;
+#pragma unroll
+    for (int i = 0; i < U; i += 2) {
+        const bool in0 = c0 + kBlock * i < d, in1 = c0 + kBlock * (i + 1) < d;
+        const float2 sg = make_float2(__shfl_sync(0xFFFFFFFFu, step, i),
+                                      __shfl_sync(0xFFFFFFFFu, step, i + 1));
+        const float2 su = make_float2(__shfl_sync(0xFFFFFFFFu, step, U + i),
+                                      __shfl_sync(0xFFFFFFFFu, step, U + i + 1));
+        const float2 g = mul2(make_float2(in0 ? qg[i] : 0, in1 ? qg[i + 1] : 0), sg);
+        const float2 u = mul2(make_float2(in0 ? qu[i] : 0, in1 ? qu[i + 1] : 0), su);
+        const float2 y = make_float2(in0 ? to_float(yraw[i]) : 0.f, in1 ? to_float(yraw[i + 1]) : 0.f);
+        const GateGrad2 m = act_grad<Act>(g, u, y);
+        if (in0) {
+            gi[kBlock * i] = from_float<T>(m.gate.x);
+            gi[d + kBlock * i] = from_float<T>(m.up.x);
+            if (out)
+                o[kBlock * i] = from_float<T>(m.out.x);
+        }
+        if (in1) {
+            gi[kBlock * (i + 1)] = from_float<T>(m.gate.y);
+            gi[d + kBlock * (i + 1)] = from_float<T>(m.up.y);
+            if (out)
+                o[kBlock * (i + 1)] = from_float<T>(m.out.y);
+        }
     }
 }
 
-template <class T>
+template <class T, class I>
 __global__ void __launch_bounds__(kThreads)
 ckpt_values_any(T *__restrict__ values, const int8_t *__restrict__ codes,
-                const uint8_t *__restrict__ scales, int64_t M, int64_t d, int64_t B) {
+                const uint8_t *__restrict__ scales, int64_t M, int64_t d, int64_t B, I J,
+                FastDiv by_J) {
     pdl_wait();
     pdl_trigger();
-    const int64_t total = M * 2 * d, step = static_cast<int64_t>(gridDim.x) * kThreads;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-         i += step) {
-        const int64_t h = i / d, c = i - h * d;   // h: half-row
-        values[i] = from_float<T>(codes[i] * code_step(scales[h * B + c / kBlock]));
+    constexpr int U = kAnyBlocks;
+    const int lane = threadIdx.x & 31;
+    const I job = static_cast<I>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const I row = quotient(job, J, by_J);
+    if (row >= M)
+        return;
+    const int64_t r = row, b0 = static_cast<int64_t>(job - row * J) * U, c0 = b0 * kBlock + lane;
+    const int8_t *q = codes + r * 2 * d + c0;
+    T *v = values + r * 2 * d + c0;
+    int8_t qg[U], qu[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+        if (c0 + kBlock * i < d) {
+            qg[i] = __ldg(q + kBlock * i);
+            qu[i] = __ldg(q + d + kBlock * i);
+        }
+    const float step = lane_step(scales + r * 2 * B, b0, B, lane);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const float sg = __shfl_sync(0xFFFFFFFFu, step, i), su = __shfl_sync(0xFFFFFFFFu, step, U + i);
+        if (c0 + kBlock * i < d) {
+            v[kBlock * i] = from_float<T>(qg[i] * sg);
+            v[d + kBlock * i] = from_float<T>(qu[i] * su);
+        }
     }
 }
 
@@ -142,7 +232,7 @@ __device__ __forceinline__ void block_tops(uint32_t *g, uint32_t *u) {
 template <class T, class Act, int VPT, class I>
 __global__ void __launch_bounds__(kThreads)
 ckpt_forward_vec(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
-                 const T *__restrict__ in, int64_t M, I d, int64_t rs, I B,
+                 const T *__restrict__ in, int64_t M, I d, int64_t rs, I B, FastDiv by_slots,
                  const int32_t *n_rows) {
     pdl_wait();
     pdl_trigger();
@@ -155,7 +245,7 @@ ckpt_forward_vec(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__res
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const I s = first + i * kThreads;
-        row[i] = s / slots;
+        row[i] = quotient(s, slots, by_slots);
         col[i] = (s - row[i] * slots) * 8;
         ok[i] = row[i] < live && col[i] < d;
         g[i] = u[i] = Vec8<T>::zero();
@@ -178,7 +268,7 @@ ckpt_forward_vec(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__res
         for (int j = 0; j < 4; ++j) {
             gf[j] = g[i].pair(j);
             uf[j] = u[i].pair(j);
-            o.put(j, make_float2(act_mul<Act>(gf[j].x, uf[j].x), act_mul<Act>(gf[j].y, uf[j].y)));
+            o.put(j, act_mul<Act>(gf[j], uf[j]));
         }
         const int64_t r = row[i];
         o.store(out + r * d + col[i]);
@@ -197,7 +287,7 @@ template <class T, class Act, int VPT, class I>
 __global__ void __launch_bounds__(kThreads)
 ckpt_backward_vec(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
                   const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t M,
-                  I d, int64_t gs, I B, const int32_t *n_rows) {
+                  I d, int64_t gs, I B, FastDiv by_nv, const int32_t *n_rows) {
     pdl_wait();
     pdl_trigger();
     const I nv = d / 8;
@@ -210,7 +300,7 @@ ckpt_backward_vec(T *__restrict__ grad_in, T *__restrict__ out, const T *__restr
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const I s = first + i * kThreads;
-        row[i] = s / nv;
+        row[i] = quotient(s, nv, by_nv);
         col[i] = (s - row[i] * nv) * 8;
         if (row[i] < live) {
             const int64_t r = row[i];
@@ -234,10 +324,10 @@ ckpt_backward_vec(T *__restrict__ grad_in, T *__restrict__ out, const T *__restr
         for (int j = 0; j < 4; ++j) {
             const float2 g = decode_pair(bg, j, stg), u = decode_pair(bu, j, stu);
             const float2 y = dy[i].pair(j);
-            const GateGrad a = act_grad<Act>(g.x, u.x, y.x), b = act_grad<Act>(g.y, u.y, y.y);
-            og.put(j, make_float2(a.gate, b.gate));
-            ou.put(j, make_float2(a.up, b.up));
-            oo.put(j, make_float2(a.out, b.out));
+            const GateGrad2 m = act_grad<Act>(g, u, y);
+            og.put(j, m.gate);
+            ou.put(j, m.up);
+            oo.put(j, m.out);
         }
         const int64_t r = row[i];
         T *p = grad_in + r * 2 * d + col[i];
@@ -248,26 +338,169 @@ ckpt_backward_vec(T *__restrict__ grad_in, T *__restrict__ out, const T *__restr
     }
 }
 
-template <class T, class I>
+template <class T, int VPT, class I>
 __global__ void __launch_bounds__(kThreads)
 ckpt_values_vec(T *__restrict__ values, const int8_t *__restrict__ codes,
-                const uint8_t *__restrict__ scales, I total, I nv, I B) {
+                const uint8_t *__restrict__ scales, I total, I nv, I B, FastDiv by_nv) {
     pdl_wait();
     pdl_trigger();
-    const I s = static_cast<I>(blockIdx.x) * kThreads + threadIdx.x;
-    if (s >= total)
-        return;
-    const I h = s / nv, v = s - h * nv;                // half-row, vector
-    const float step = code_step(__ldg(scales + static_cast<int64_t>(h) * B + v / 4));
-    const uint2 b = bias_codes(ld_stream_u2(codes + static_cast<int64_t>(s) * 8));
-    Vec8<T> o;
+    const I first = static_cast<I>(blockIdx.x) * (VPT * kThreads) + threadIdx.x;
+    uint2 c[VPT];
+    uint32_t e[VPT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        o.put(j, decode_pair(b, j, step));
-    o.store(values + static_cast<int64_t>(s) * 8);
+    for (int i = 0; i < VPT; ++i) {
+        const I s = first + i * kThreads;
+        if (s < total) {
+            const I h = quotient(s, nv, by_nv), v = s - h * nv;        // half-row, vector
+            c[i] = ld_stream_u2(codes + static_cast<int64_t>(s) * 8);
+            e[i] = __ldg(scales + static_cast<int64_t>(h) * B + v / 4);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const I s = first + i * kThreads;
+        if (s >= total)
+            continue;
+        const float step = code_step(e[i]);
+        const uint2 b = bias_codes(c[i]);
+        Vec8<T> o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            o.put(j, decode_pair(b, j, step));
+        o.store(values + static_cast<int64_t>(s) * 8);
+    }
+}
+
+// Sum over a CTA of NT threads, the same bits in every thread; red holds NT / 32
+// floats.
+template <int NT>
+__device__ __forceinline__ float row_sum(float v, float *red) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    constexpr int NW = NT / 32;
+    float t = red[threadIdx.x & (NW - 1)];
+#pragma unroll
+    for (int o = NW / 2; o > 0; o >>= 1)
+        t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    return t;
 }
 
 // ------------------------------------------------------ sparse, any layout
+//
+// One CTA per row, one element per lane: warp w holds the blocks w, w + NT / 32,
+// ..., V of them, in registers.
+
+template <class T, int NT, int V>
+__global__ void __launch_bounds__(NT)
+sparse_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
+                   float *__restrict__ std_out, const T *__restrict__ in, int d, int64_t rs,
+                   int B, float z) {
+    __shared__ float red[2][NT / 32];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t r = blockIdx.x;
+    const T *p = in + r * rs + threadIdx.x;
+    float g[V], acc = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        g[i] = static_cast<int>(threadIdx.x) + NT * i < d ? to_float(__ldg(p + NT * i)) : 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        acc += g[i];
+    const float n = static_cast<float>(d);
+    const float mean = row_sum<NT>(acc, red[0]) / n;
+    acc = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float e = static_cast<int>(threadIdx.x) + NT * i < d ? g[i] - mean : 0.f;
+        acc = fmaf(e, e, acc);
+    }
+    const float std = __fsqrt_rn(row_sum<NT>(acc, red[1]) / n);
+    const float cutoff = fmaf(std, z, mean);
+    if (threadIdx.x == 0)
+        std_out[r] = std;
+    T *o = out + r * d + threadIdx.x;
+    int8_t *q = codes + r * 2 * d + threadIdx.x;
+    uint8_t *s = scales + r * 2 * B + (threadIdx.x >> 5);
+#pragma unroll
+    for (int i0 = 0; i0 < V; i0 += 4) {
+        T raw[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (static_cast<int>(threadIdx.x) + NT * (i0 + j) < d)
+                raw[j] = __ldg(p + d + NT * (i0 + j));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = threadIdx.x + NT * (i0 + j);
+            if (c - lane >= d)       // the warp's block as a whole
+                continue;
+            const bool ok = c < d;
+            const float v = ok ? g[i0 + j] - cutoff : 0.f, u = ok ? to_float(raw[j]) : 0.f;
+            if (ok)
+                o[NT * (i0 + j)] = from_float<T>(act_mul<Gelu>(relu_nan2(both(v)), both(u)).x);
+            put_block<true>(q + NT * (i0 + j), s + NT / 32 * (i0 + j), v, ok, lane);
+            put_block<false>(q + d + NT * (i0 + j), s + B + NT / 32 * (i0 + j), u, ok, lane);
+        }
+    }
+}
+
+template <class T, int NT, int V>
+__global__ void __launch_bounds__(NT)
+sparse_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
+                    const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
+                    const float *__restrict__ std_in, int d, int64_t gs, int B, float z) {
+    __shared__ float red[NT / 32];
+    pdl_wait();
+    pdl_trigger();
+    const int64_t r = blockIdx.x;
+    const float std = std_in[r];
+    const T *y = grad + r * gs + threadIdx.x;
+    const int8_t *q = codes + r * 2 * d + threadIdx.x;
+    const uint8_t *s = scales + r * 2 * B + (threadIdx.x >> 5);
+    T *gi = grad_in + r * 2 * d + threadIdx.x, *o = out + r * d + threadIdx.x;
+    float h[V], acc = 0.f;
+#pragma unroll
+    for (int i0 = 0; i0 < V; i0 += 4) {
+        T dy[4];
+        int8_t cg[4], cu[4];
+        uint8_t sg[4], su[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (static_cast<int>(threadIdx.x) + NT * (i0 + j) < d) {
+                dy[j] = __ldg(y + NT * (i0 + j));
+                cg[j] = __ldg(q + NT * (i0 + j));
+                cu[j] = __ldg(q + d + NT * (i0 + j));
+                sg[j] = __ldg(s + NT / 32 * (i0 + j));
+                su[j] = __ldg(s + B + NT / 32 * (i0 + j));
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            h[i0 + j] = 0.f;
+            if (static_cast<int>(threadIdx.x) + NT * (i0 + j) >= d)
+                continue;
+            const GateGrad2 m = sparse_grad(both(cg[j] * code_step(sg[j])),
+                                            both(cu[j] * code_step(su[j])), both(to_float(dy[j])));
+            h[i0 + j] = m.gate.x;
+            acc += m.gate.x;
+            gi[d + NT * (i0 + j)] = from_float<T>(m.up.x);
+            if (out)
+                o[NT * (i0 + j)] = from_float<T>(m.out.x);
+        }
+    }
+    const float m = row_sum<NT>(acc, red) / static_cast<float>(d);
+    const float inv = std == 0.f ? 0.f : z / std;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (static_cast<int>(threadIdx.x) + NT * i < d) {      // the codes again, from L1 or L2
+            const float v = __ldg(q + NT * i) * code_step(__ldg(s + NT / 32 * i));
+            gi[NT * i] = from_float<T>(fmaf(-m, fmaf(inv, fmaf(z, std, v), 1.f), h[i]));
+        }
+}
+
+// ----------------------------------------- sparse, rows that no CTA holds
 
 // Sum over the CTA, the same bits in every thread; red holds kWarps floats
 // and may be used again after the next barrier.
@@ -286,7 +519,7 @@ __device__ __forceinline__ float cta_sum(float v, float *red) {
 // One CTA per row; the gate is read again (from L1/L2) for each pass.
 template <class T>
 __global__ void __launch_bounds__(kThreads)
-sparse_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
+sparse_forward_wide(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                    float *__restrict__ std_out, const T *__restrict__ in, int64_t rows, int64_t d,
                    int64_t rs, int64_t B, float z) {
     __shared__ float red[2][kWarps];
@@ -314,7 +547,7 @@ sparse_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__r
             const float v = ok ? to_float(g[c]) - cutoff : 0.f;
             const float u = ok ? to_float(g[d + c]) : 0.f;
             if (ok)
-                out[r * d + c] = from_float<T>(gelu_mul(max_nan(v, 0.f), u));
+                out[r * d + c] = from_float<T>(act_mul<Gelu>(relu_nan2(both(v)), both(u)).x);
             put_block<true>(codes + r * 2 * d + c, scales + r * 2 * B + b, v, ok, lane);
             put_block<false>(codes + r * 2 * d + d + c, scales + r * 2 * B + B + b, u, ok, lane);
         }
@@ -323,7 +556,7 @@ sparse_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__r
 
 template <class T>
 __global__ void __launch_bounds__(kThreads)
-sparse_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
+sparse_backward_wide(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
                     const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                     const float *__restrict__ std_in, int64_t rows, int64_t d, int64_t gs,
                     int64_t B, float z) {
@@ -342,18 +575,18 @@ sparse_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__res
             const float v = q[c] * code_step(sc[c / kBlock]);
             const float u = q[d + c] * code_step(sc[B + c / kBlock]);
             const float dy = to_float(grad[r * gs + c]);
-            const GateGrad m = sparse_grad(v, u, dy);
-            acc += m.gate;
-            gi[d + c] = from_float<T>(m.up);
+            const GateGrad2 m = sparse_grad(both(v), both(u), both(dy));
+            acc += m.gate.x;
+            gi[d + c] = from_float<T>(m.up.x);
             if (out)
-                out[r * d + c] = from_float<T>(m.out);
+                out[r * d + c] = from_float<T>(m.out.x);
         }
         const float mean_h = cta_sum(acc, red[k]) / static_cast<float>(d);
         for (int64_t c = threadIdx.x; c < d; c += kThreads) {
             const float v = q[c] * code_step(sc[c / kBlock]);
             const float u = q[d + c] * code_step(sc[B + c / kBlock]);
             const float dy = to_float(grad[r * gs + c]);
-            const float h = sparse_grad(v, u, dy).gate;
+            const float h = sparse_grad(both(v), both(u), both(dy)).gate.x;
             gi[c] = from_float<T>(fmaf(-mean_h, fmaf(inv, fmaf(z, std, v), 1.f), h));
         }
     }
@@ -365,20 +598,6 @@ sparse_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__res
 // t, t + NT, ... (V of them) of both halves, so the gate is read once for its
 // statistics and its codes, and four neighbouring lanes hold a block.  All
 // loads are issued before the first sum.
-
-template <int NT>
-__device__ __forceinline__ float row_sum(float v, float *red) {
-    v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0)
-        red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    constexpr int NW = NT / 32;
-    float t = red[threadIdx.x & (NW - 1)];
-#pragma unroll
-    for (int o = NW / 2; o > 0; o >>= 1)
-        t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    return t;
-}
 
 template <class T, int NT, int V>
 __global__ void __launch_bounds__(NT)
@@ -433,8 +652,7 @@ sparse_forward_vec(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__r
             v[j] = sub2(g[i].pair(j), make_float2(cutoff, cutoff));
             w[j] = u[i].pair(j);
             tg = max(tg, max(abs_bits(v[j].x), abs_bits(v[j].y)));
-            o.put(j, make_float2(gelu_mul(max_nan(v[j].x, 0.f), w[j].x),
-                                 gelu_mul(max_nan(v[j].y, 0.f), w[j].y)));
+            o.put(j, act_mul<Gelu>(relu_nan2(v[j]), w[j]));
         }
         if (c >= d)
             tg = 0;
@@ -496,11 +714,11 @@ sparse_backward_vec(T *__restrict__ grad_in, T *__restrict__ out, const T *__res
         for (int j = 0; j < 4; ++j) {
             const float2 v = decode_pair(bg, j, stg), u = decode_pair(bu, j, stu);
             const float2 t = dy[i].pair(j);
-            const GateGrad a = sparse_grad(v.x, u.x, t.x), b = sparse_grad(v.y, u.y, t.y);
-            h[i][j] = make_float2(a.gate, b.gate);
-            acc = add2(acc, h[i][j]);
-            ou.put(j, make_float2(a.up, b.up));
-            oo.put(j, make_float2(a.out, b.out));
+            const GateGrad2 m = sparse_grad(v, u, t);
+            h[i][j] = m.gate;
+            acc = add2(acc, m.gate);
+            ou.put(j, m.up);
+            oo.put(j, m.out);
         }
         ou.store(gi + d + c);
         if (out)
@@ -559,9 +777,37 @@ template <class F> int with_index(int64_t slots, int vpt, F f) {
     return slots + per < (int64_t(1) << 31) ? f(uint32_t{}, g) : f(int64_t{}, g);
 }
 
+// Calls f(I{}, grid) for `jobs` jobs of a warp each, as with_index.
+template <class F> int with_jobs(int64_t jobs, F f) {
+    const int64_t grid = ceil_div64(jobs, kWarps);
+    if (grid > 0x7FFFFFFF)
+        return GATED_ACT_ERR_TOO_LARGE;
+    const dim3 g(static_cast<unsigned>(grid));
+    return jobs + kWarps < (int64_t(1) << 31) ? f(uint32_t{}, g) : f(int64_t{}, g);
+}
+
+// The CTA that holds a row of d elements one by one, as with_row_cta.
+template <int N> using Const = std::integral_constant<int, N>;
+template <class F> bool with_any_cta(int64_t d, int *rc, F f) {
+    if (d <= 1024)
+        *rc = f(Const<256>{}, Const<4>{});
+    else if (d <= 2048)
+        *rc = f(Const<256>{}, Const<8>{});
+    else if (d <= 4096)
+        *rc = f(Const<512>{}, Const<8>{});
+    else if (d <= 8192)
+        *rc = f(Const<512>{}, Const<16>{});
+    else if (d <= 16384)
+        *rc = f(Const<1024>{}, Const<16>{});
+    else if (d <= 32768)
+        *rc = f(Const<1024>{}, Const<32>{});
+    else
+        return false;
+    return true;
+}
+
 // Calls f(integral constants NT, V) for rows of nv 8-element vectors held by
 // one CTA; false when no such CTA holds them.
-template <int N> using Const = std::integral_constant<int, N>;
 template <class F> bool with_row_cta(int64_t nv, int *rc, F f) {
     if (nv <= 128)
         *rc = f(Const<128>{}, Const<1>{});
@@ -580,7 +826,7 @@ template <class F> bool with_row_cta(int64_t nv, int *rc, F f) {
     return true;
 }
 
-constexpr int kForwardVpt = 1, kBackwardVpt = 1;
+constexpr int kForwardVpt = 1, kBackwardVpt = 1, kValuesVpt = 4;
 
 template <class Act>
 int forward(void *out, int8_t *codes, uint8_t *scales, const void *in, int64_t M, int64_t d,
@@ -607,13 +853,18 @@ int forward(void *out, int8_t *codes, uint8_t *scales, const void *in, int64_t M
                 return launched(launch_kernel(
                     ckpt_forward_vec<T, Act, VPT, I>, grid, dim3(kThreads), 0, stream, 1,
                     as<T>(r[0]), as<int8_t>(r[1]), as<uint8_t>(r[2]), as<const T>(r[3]), M,
-                    static_cast<I>(d), rs, static_cast<I>(B), as<const int32_t>(r[4])));
+                    static_cast<I>(d), rs, static_cast<I>(B), FastDiv(static_cast<uint32_t>(4 * B)),
+                    as<const int32_t>(r[4])));
             });
         }
-        return launched(launch_kernel(ckpt_forward_any<T, Act>, grid_of(M * B, kWarps),
-                                      dim3(kThreads), 0, stream, 1, as<T>(r[0]), as<int8_t>(r[1]),
-                                      as<uint8_t>(r[2]), as<const T>(r[3]), M, d, rs, B,
-                                      as<const int32_t>(r[4])));
+        const int64_t J = ceil_div64(B, kAnyBlocks);
+        return with_jobs(M * J, [&](auto idx, dim3 grid) {
+            using I = decltype(idx);
+            return launched(launch_kernel(
+                ckpt_forward_any<T, Act, I>, grid, dim3(kThreads), 0, stream, 1, as<T>(r[0]),
+                as<int8_t>(r[1]), as<uint8_t>(r[2]), as<const T>(r[3]), M, d, rs, B,
+                static_cast<I>(J), FastDiv(static_cast<uint32_t>(J)), as<const int32_t>(r[4])));
+        });
     });
 }
 
@@ -645,14 +896,18 @@ int backward(void *grad_in, void *out, const void *grad, const int8_t *codes,
                     ckpt_backward_vec<T, Act, VPT, I>, grid, dim3(kThreads), 0, stream, 1,
                     as<T>(r[0]), as<T>(r[1]), as<const T>(r[2]), as<const int8_t>(r[3]),
                     as<const uint8_t>(r[4]), M, static_cast<I>(d), gs, static_cast<I>(B),
-                    as<const int32_t>(r[5])));
+                    FastDiv(static_cast<uint32_t>(d / 8)), as<const int32_t>(r[5])));
             });
         }
-        return launched(launch_kernel(ckpt_backward_any<T, Act>, grid_of(M * B, kWarps),
-                                      dim3(kThreads), 0, stream, 1, as<T>(r[0]), as<T>(r[1]),
-                                      as<const T>(r[2]), as<const int8_t>(r[3]),
-                                      as<const uint8_t>(r[4]), M, d, gs, B,
-                                      as<const int32_t>(r[5])));
+        const int64_t J = ceil_div64(B, kAnyBlocks);
+        return with_jobs(M * J, [&](auto idx, dim3 grid) {
+            using I = decltype(idx);
+            return launched(launch_kernel(
+                ckpt_backward_any<T, Act, I>, grid, dim3(kThreads), 0, stream, 1, as<T>(r[0]),
+                as<T>(r[1]), as<const T>(r[2]), as<const int8_t>(r[3]), as<const uint8_t>(r[4]), M,
+                d, gs, B, static_cast<I>(J), FastDiv(static_cast<uint32_t>(J)),
+                as<const int32_t>(r[5])));
+        });
     });
 }
 
@@ -723,7 +978,16 @@ extern "C" int gelu_and_mul_sparse_checkpoint(void *out, int8_t *codes, uint8_t 
         int done;
         if (vec && with_row_cta(d / 8, &done, go))
             return done;
-        return launched(launch_kernel(sparse_forward_any<E>, grid_of(T, 1), dim3(kThreads), 0,
+        const auto any = [&](auto nt, auto v) {
+            return launched(launch_kernel(
+                sparse_forward_any<E, nt(), v()>, dim3(static_cast<unsigned>(T)), dim3(nt()), 0,
+                stream, 1, as<E>(r[0]), as<int8_t>(r[1]), as<uint8_t>(r[2]), as<float>(r[3]),
+                as<const E>(r[4]), static_cast<int>(d), row_stride, static_cast<int>(B),
+                static_cast<float>(z)));
+        };
+        if (T <= 0x7FFFFFFF && with_any_cta(d, &done, any))
+            return done;
+        return launched(launch_kernel(sparse_forward_wide<E>, grid_of(T, 1), dim3(kThreads), 0,
                                       stream, 1, as<E>(r[0]), as<int8_t>(r[1]), as<uint8_t>(r[2]),
                                       as<float>(r[3]), as<const E>(r[4]), T, d, row_stride, B,
                                       static_cast<float>(z)));
@@ -763,7 +1027,16 @@ extern "C" int gelu_and_mul_sparse_backward(void *grad_in, void *out, const void
         int done;
         if (vec && with_row_cta(d / 8, &done, go))
             return done;
-        return launched(launch_kernel(sparse_backward_any<E>, grid_of(T, 1), dim3(kThreads), 0,
+        const auto any = [&](auto nt, auto v) {
+            return launched(launch_kernel(
+                sparse_backward_any<E, nt(), v()>, dim3(static_cast<unsigned>(T)), dim3(nt()), 0,
+                stream, 1, as<E>(r[0]), as<E>(r[1]), as<const E>(r[2]),
+                as<const int8_t>(r[3]), as<const uint8_t>(r[4]), as<const float>(r[5]),
+                static_cast<int>(d), grad_stride, static_cast<int>(B), static_cast<float>(z)));
+        };
+        if (T <= 0x7FFFFFFF && with_any_cta(d, &done, any))
+            return done;
+        return launched(launch_kernel(sparse_backward_wide<E>, grid_of(T, 1), dim3(kThreads), 0,
                                       stream, 1, as<E>(r[0]), as<E>(r[1]), as<const E>(r[2]),
                                       as<const int8_t>(r[3]), as<const uint8_t>(r[4]),
                                       as<const float>(r[5]), T, d, grad_stride, B,
@@ -789,15 +1062,20 @@ extern "C" int gated_act_checkpoint_values(void *values, const int8_t *codes,
     return with_type(dtype, [&](auto t) {
         using E = decltype(t);
         if (d % 8 == 0 && aligned(r[0].dev, 16) && aligned(r[1].dev, 8))
-            return with_index(M * 2 * (d / 8), 1, [&](auto idx, dim3 grid) {
+            return with_index(M * 2 * (d / 8), kValuesVpt, [&](auto idx, dim3 grid) {
                 using I = decltype(idx);
                 return launched(launch_kernel(
-                    ckpt_values_vec<E, I>, grid, dim3(kThreads), 0, stream, 1, as<E>(r[0]),
+                    ckpt_values_vec<E, kValuesVpt, I>, grid, dim3(kThreads), 0, stream, 1, as<E>(r[0]),
                     as<const int8_t>(r[1]), as<const uint8_t>(r[2]), static_cast<I>(M * 2 * (d / 8)),
-                    static_cast<I>(d / 8), static_cast<I>(B)));
+                    static_cast<I>(d / 8), static_cast<I>(B), FastDiv(static_cast<uint32_t>(d / 8))));
             });
-        return launched(launch_kernel(ckpt_values_any<E>, grid_of(M * 2 * d, kThreads),
-                                      dim3(kThreads), 0, stream, 1, as<E>(r[0]),
-                                      as<const int8_t>(r[1]), as<const uint8_t>(r[2]), M, d, B));
+        const int64_t J = ceil_div64(B, kAnyBlocks);
+        return with_jobs(M * J, [&](auto idx, dim3 grid) {
+            using I = decltype(idx);
+            return launched(launch_kernel(
+                ckpt_values_any<E, I>, grid, dim3(kThreads), 0, stream, 1, as<E>(r[0]),
+                as<const int8_t>(r[1]), as<const uint8_t>(r[2]), M, d, B, static_cast<I>(J),
+                FastDiv(static_cast<uint32_t>(J))));
+        });
     });
 }

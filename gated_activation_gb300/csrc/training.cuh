@@ -27,81 +27,86 @@ template <> __device__ __forceinline__ f16 from_float<f16>(float x) { return __f
 // ------------------------------------------------------------- activations
 
 // Both activations are g sigma(a) with a = a(g), and their slope is
-// sigma (1 + g (1 - sigma) a').  With t = e^{-|a|}, sigma and 1 - sigma are
-// 1 / (1 + t) and t / (1 + t) in one order or the other: no cancellation.  t is
-// the square of h = 2^{-|a| log2(e) / 2}, which the flushing hardware
-// exponential (PTX ISA ex2.approx.ftz.f32, relative error about 2^-22) keeps
-// normal for |a| < 174; 1 + t lies in [1, 2], where the hardware reciprocal
-// is within one ulp.  sigma is handed on as the product s1 s2 (h / (1 + t)
-// and h for a < 0), s2 to be multiplied last: then nothing but a result itself
-// can fall below fp32's normal range.
-struct Gate {
-    float s1, s2;   // sigma = s1 s2
-    float w;        // slope = sigma w
+// sigma (1 + g a' (1 - sigma)).  With y = a log2(e) / 2, k = 2^y and h = 2^-y,
+//   sigma = k r,  r = 1 / (k + h):
+// no cancellation and no case by sign.  k, h and r come from the flushing
+// hardware exponential and reciprocal (PTX ISA ex2.approx.ftz.f32, rcp.approx.
+// ftz.f32, relative error about 2^-22); k and r stay normal down to a = -174,
+// and k is multiplied last, so nothing but a result itself can fall below
+// fp32's normal range.  y is taken at most at 16, where 1 - sigma is 2^-32.
+// Two elements at a time: the paired fp32 instructions halve the issue slots.
+struct Gate2 {
+    float2 r, k;   // sigma = r k
 };
-__device__ __forceinline__ Gate gate_of(float a, float g_slope) {
-    float h, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(fabsf(a) * (-0.5f * 1.4426950408889634f)));
-    const float t = h * h;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
-    const bool up = a >= 0.f;
-    Gate m;
-    m.s2 = up ? 1.f : h;
-    m.s1 = r * m.s2;
-    m.w = fmaf(g_slope, up ? t * r : r, 1.f);
+__device__ __forceinline__ Gate2 gate_of(float2 y) {
+    Gate2 m;
+    float2 h;
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(y.x) : "f"(16.f));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(y.y) : "f"(16.f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(m.k.x) : "f"(y.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(m.k.y) : "f"(y.y));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h.x) : "f"(-y.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h.y) : "f"(-y.y));
+    h = add2(m.k, h);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(m.r.x) : "f"(h.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(m.r.y) : "f"(h.y));
     return m;
 }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// exponent(g) = y, lean(g) = g a'.
 struct Silu {
-    __device__ static Gate gate(float g) { return gate_of(g, g); }
+    __device__ static float2 exponent(float2 g) { return mul2(g, both(0.5f * 1.4426950408889634f)); }
+    __device__ static float2 lean(float2 g) { return g; }
 };
 
 // a = 2 sqrt(2/pi) (g + 0.044715 g^3).  g a' is taken at most at |g| = 16,
-// where it cannot overflow: past |g| = 11, t is 0 and so is its factor (a > 0)
-// or sigma (a < 0).
+// where it cannot overflow: past |g| = 11, sigma or 1 - sigma is 0 beside it.
 struct Gelu {
     static constexpr float k2 = 2.0f * 0.7978845608028654f;
     static constexpr float k2c = 2.0f * 0.7978845608028654f * 0.044715f;
-    __device__ static Gate gate(float g) {
-        const float b = fminf(fmaxf(g, -16.f), 16.f);
-        return gate_of(g * fmaf(k2c, g * g, k2), b * fmaf(3.f * k2c, b * b, k2));
+    static constexpr float e = 0.5f * 1.4426950408889634f;
+    __device__ static float2 exponent(float2 g) {
+        return mul2(g, fma2(mul2(g, g), both(e * k2c), both(e * k2)));
+    }
+    __device__ static float2 lean(float2 g) {
+        float2 b;
+        asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(b.x) : "f"(g.x), "f"(16.f));
+        asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(b.y) : "f"(g.y), "f"(16.f));
+        return mul2(b, fma2(mul2(b, b), both(3.f * k2c), both(k2)));
     }
 };
 
-// gelu_tanh(s) u for s >= 0 or NaN.
-__device__ __forceinline__ float gelu_mul(float s, float u) {
-    const Gate m = Gelu::gate(s);
-    return s * m.s1 * u;
-}
-
 // act(g) u
-template <class Act> __device__ __forceinline__ float act_mul(float g, float u) {
-    const Gate m = Act::gate(g);
-    return g * m.s1 * u * m.s2;
+template <class Act> __device__ __forceinline__ float2 act_mul(float2 g, float2 u) {
+    const Gate2 m = gate_of(Act::exponent(g));
+    return mul2(mul2(mul2(g, m.r), u), m.k);
 }
 
 // The gradients of act(g) u, and act(g) u itself.
-struct GateGrad {
-    float gate, up, out;
+struct GateGrad2 {
+    float2 gate, up, out;
 };
-template <class Act> __device__ __forceinline__ GateGrad act_grad(float g, float u, float dy) {
-    const Gate m = Act::gate(g);
-    const float p = g * m.s1;
-    return {dy * u * m.s1 * m.w * m.s2, p * dy * m.s2, p * u * m.s2};
+template <class Act>
+__device__ __forceinline__ GateGrad2 act_grad(float2 g, float2 u, float2 dy) {
+    const Gate2 m = gate_of(Act::exponent(g));
+    const float2 p = mul2(g, m.r), q = mul2(dy, m.k);
+    const float2 off = fma2(make_float2(-m.r.x, -m.r.y), m.k, both(1.f));   // 1 - sigma
+    const float2 w = fma2(Act::lean(g), off, both(1.f));
+    return {mul2(mul2(mul2(u, m.r), w), q), mul2(p, q), mul2(mul2(p, u), m.k)};
+}
+__device__ __forceinline__ float2 relu_nan2(float2 x) {
+    float2 s;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(s.x) : "f"(x.x));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(s.y) : "f"(x.y));
+    return s;
 }
 // The same of gelu_tanh at s = max(delta, 0); gate is 0 where delta <= 0.
-__device__ __forceinline__ GateGrad sparse_grad(float delta, float u, float dy) {
-    float s;
-    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(s) : "f"(delta));
-    const Gate m = Gelu::gate(s);
-    const float p = s * m.s1;
-    return {delta <= 0.f ? 0.f : dy * u * m.s1 * m.w, p * dy, p * u};
-}
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
+__device__ __forceinline__ GateGrad2 sparse_grad(float2 delta, float2 u, float2 dy) {
+    GateGrad2 m = act_grad<Gelu>(relu_nan2(delta), u, dy);
+    m.gate.x = delta.x <= 0.f ? 0.f : m.gate.x;
+    m.gate.y = delta.y <= 0.f ? 0.f : m.gate.y;
+    return m;
 }
 
 // ------------------------------------------------------------ 8 elements
@@ -146,8 +151,11 @@ template <class T> struct Vec8 {
     // Largest magnitude, as the bits of the element type: for values of one
     // type these order as the magnitudes do, infinity and NaN above all.
     __device__ uint32_t top() const {
-        constexpr uint32_t m = 0x7FFF7FFFu;
-        const uint32_t w = max_u16x2(max_u16x2(q.x & m, q.y & m), max_u16x2(q.z & m, q.w & m));
+        using T2 = std::conditional_t<std::is_same_v<T, bf16>, __nv_bfloat162, __half2>;
+        const T2 *h = reinterpret_cast<const T2 *>(&q);
+        const T2 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])),
+                                 __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(&m);
         return max(w >> 16, w & 0xFFFFu);
     }
 };
@@ -314,6 +322,19 @@ inline cudaError_t allow_smem(const void *kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(bytes));
 }
+
+// n / d for n < 2^31 by a multiplication (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", 1994): with 2^(s-1) < d <= 2^s and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(m, n) + n) >> s.
+struct FastDiv {
+    uint32_t m, s;
+    explicit FastDiv(uint32_t d) : s(0) {
+        while (s < 32 && (uint64_t(1) << s) < d)
+            ++s;
+        m = static_cast<uint32_t>((((uint64_t(1) << s) - d) << 32) / d + 1);
+    }
+    __device__ uint32_t operator()(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
+};
 
 inline int launched(cudaError_t e) {
     return cuda_status(e != cudaSuccess ? e : cudaGetLastError());

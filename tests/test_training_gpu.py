@@ -18,7 +18,8 @@ DTYPES = [BF16, F16, F32]
 # with and without a ragged last block, an expert's width, several vectors per thread, wider
 # than a row that one CTA holds
 SHAPES = [(1, 1), (3, 7), (5, 32), (2, 33), (4, 40), (3, 96), (64, 257), (33, 768), (7, 4099),
-          (5, 8192), (2, 16392), (2, 32768), (1, 40000)]
+          (5, 8192), (2, 16392), (2, 32768), (1, 40000), (3, 1500), (2, 8001), (2, 16001),
+          (1, 32761), (1, 40001)]
 
 
 @pytest.fixture(scope="module")
