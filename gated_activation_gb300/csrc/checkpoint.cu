@@ -230,7 +230,7 @@ __device__ __forceinline__ void block_tops(uint32_t *g, uint32_t *u) {
 }
 
 template <class T, class Act, int VPT, class I>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && sizeof(I) == 4 ? 8 : 6)
 ckpt_forward_vec(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                  const T *__restrict__ in, int64_t M, I d, int64_t rs, I B, FastDiv by_slots,
                  const int32_t *n_rows) {
@@ -284,7 +284,7 @@ ckpt_forward_vec(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__res
 }
 
 template <class T, class Act, int VPT, class I>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && sizeof(I) == 4 ? 8 : 6)
 ckpt_backward_vec(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
                   const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t M,
                   I d, int64_t gs, I B, FastDiv by_nv, const int32_t *n_rows) {
@@ -440,7 +440,7 @@ sparse_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__r
             const bool ok = c < d;
             const float v = ok ? g[i0 + j] - cutoff : 0.f, u = ok ? to_float(raw[j]) : 0.f;
             if (ok)
-                o[NT * (i0 + j)] = from_float<T>(act_mul<Gelu>(relu_nan2(both(v)), both(u)).x);
+                o[NT * (i0 + j)] = from_float<T>(sparse_mul(both(v), both(u)).x);
             put_block<true>(q + NT * (i0 + j), s + NT / 32 * (i0 + j), v, ok, lane);
             put_block<false>(q + d + NT * (i0 + j), s + B + NT / 32 * (i0 + j), u, ok, lane);
         }
@@ -547,7 +547,7 @@ sparse_forward_wide(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__
             const float v = ok ? to_float(g[c]) - cutoff : 0.f;
             const float u = ok ? to_float(g[d + c]) : 0.f;
             if (ok)
-                out[r * d + c] = from_float<T>(act_mul<Gelu>(relu_nan2(both(v)), both(u)).x);
+                out[r * d + c] = from_float<T>(sparse_mul(both(v), both(u)).x);
             put_block<true>(codes + r * 2 * d + c, scales + r * 2 * B + b, v, ok, lane);
             put_block<false>(codes + r * 2 * d + d + c, scales + r * 2 * B + B + b, u, ok, lane);
         }
@@ -599,6 +599,36 @@ sparse_backward_wide(T *__restrict__ grad_in, T *__restrict__ out, const T *__re
 // statistics and its codes, and four neighbouring lanes hold a block.  All
 // loads are issued before the first sum.
 
+// The output and the codes of the 8 elements at column c of a row (nothing for
+// c >= d, but the lane takes part in its block's largest magnitudes).
+template <class T>
+__device__ __forceinline__ void finish_vec(const Vec8<T> &g, const Vec8<T> &u, float cutoff, int c,
+                                           int d, T *out, int8_t *codes, uint8_t *scales, int B) {
+    float2 v[4], w[4];
+    Vec8<T> o;
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[j] = sub2(g.pair(j), both(cutoff));
+        w[j] = u.pair(j);
+        top = max_abs(top, v[j]);
+        o.put(j, sparse_mul(v[j], w[j]));
+    }
+    uint32_t tg = c < d ? __float_as_uint(top) : 0u, tu = c < d ? u.top() : 0u;
+    block_tops<float>(&tg, &tu);   // 32-bit keys; u's own order is that of its type
+    if (c >= d)
+        return;
+    const uint32_t sg = scale_of(tg), su = scale_of(top_as_float<T>(tu));
+    o.store(out + c);
+    st_u2(codes + c, codes_of<true>(v, sg));
+    st_u2(codes + d + c, codes_of<false>(w, su));
+    if (c % kBlock == 0) {
+        uint8_t *s = scales + c / kBlock;
+        s[0] = static_cast<uint8_t>(sg);
+        s[B] = static_cast<uint8_t>(su);
+    }
+}
+
 template <class T, int NT, int V>
 __global__ void __launch_bounds__(NT)
 sparse_forward_vec(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
@@ -644,31 +674,7 @@ sparse_forward_vec(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__r
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = 8 * (threadIdx.x + NT * i);
-        float2 v[4], w[4];
-        Vec8<T> o;
-        uint32_t tg = 0, tu = u[i].top();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = sub2(g[i].pair(j), make_float2(cutoff, cutoff));
-            w[j] = u[i].pair(j);
-            tg = max(tg, max(abs_bits(v[j].x), abs_bits(v[j].y)));
-            o.put(j, act_mul<Gelu>(relu_nan2(v[j]), w[j]));
-        }
-        if (c >= d)
-            tg = 0;
-        block_tops<float>(&tg, &tu);   // 32-bit keys; u's own order is that of its type
-        if (c >= d)
-            continue;
-        const uint32_t sg = scale_of(tg), su = scale_of(top_as_float<T>(tu));
-        o.store(out + r * d + c);
-        int8_t *q = codes + r * 2 * d + c;
-        st_u2(q, codes_of<true>(v, sg));
-        st_u2(q + d, codes_of<false>(w, su));
-        if (c % kBlock == 0) {
-            uint8_t *s = scales + r * 2 * B + c / kBlock;
-            s[0] = static_cast<uint8_t>(sg);
-            s[B] = static_cast<uint8_t>(su);
-        }
+        finish_vec(g[i], u[i], cutoff, c, d, out + r * d, codes + r * 2 * d, scales + r * 2 * B, B);
     }
 }
 
@@ -741,6 +747,200 @@ sparse_backward_vec(T *__restrict__ grad_in, T *__restrict__ out, const T *__res
         for (int j = 0; j < 4; ++j)
             og.put(j, fma2(m2, fma2(inv2, add2(decode_pair(bg, j, stg), zs), one), h[i][j]));
         og.store(gi + c);
+    }
+}
+
+// ----------------------------------------------------------- sparse, a ring
+//
+// The same with persistent CTAs: CTA b takes the rows b, b + G, ..., which
+// reach it through a ring of S shared-memory slots that cp.async fills S - 1
+// rows ahead, so that HBM keeps streaming while a row is summed and written.  A
+// thread copies just the vectors it will read itself: its own wait_group is
+// all the synchronization that the ring needs.
+
+template <class T, int NT, int V, int S>
+__global__ void __launch_bounds__(NT, 1024 / NT)
+sparse_forward_ring(T *__restrict__ out, int8_t *__restrict__ codes,
+                    uint8_t *__restrict__ scales, float *__restrict__ std_out,
+                    const T *__restrict__ in, int64_t rows, int d, int64_t rs, int B, float z) {
+    constexpr int P = sizeof(T) / 2;                // 16-byte pieces of a vector
+    extern __shared__ __align__(16) uint4 ring[];   // [S][2][V][P][NT]
+    __shared__ float red[2][NT / 32];
+    const int t = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t G = gridDim.x;
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16u * t;
+    const auto fetch = [&](int64_t r, int slot) {
+        if (r < rows) {
+            const T *p = in + r * rs + 8 * t;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (8 * (t + NT * i) < d)
+#pragma unroll
+                        for (int k = 0; k < P; ++k)
+                            copy16(base + 16u * NT * (((slot * 2 + h) * V + i) * P + k),
+                                   p + h * d + 8 * NT * i + 16 / sizeof(T) * k);
+        }
+        copy_commit();
+    };
+    const auto held = [&](int slot, int h, int i) {
+        Vec8<T> v = Vec8<T>::zero();
+        if (8 * (t + NT * i) < d) {
+            uint4 *q = reinterpret_cast<uint4 *>(&v);
+#pragma unroll
+            for (int k = 0; k < P; ++k)
+                q[k] = ring[(((slot * 2 + h) * V + i) * P + k) * NT + t];
+        }
+        return v;
+    };
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k)
+        fetch(blockIdx.x + k * G, k);
+    int slot = 0;
+    const float n = static_cast<float>(d);
+    for (int64_t r = blockIdx.x; r < rows; r += G) {
+        // the slot read in the round before: this thread is done with it
+        fetch(r + (S - 1) * G, slot == 0 ? S - 1 : slot - 1);
+        copy_wait<S - 1>();
+        Vec8<T> g[V];
+        float2 acc = both(0.f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            g[i] = held(slot, 0, i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc = add2(acc, g[i].pair(j));
+        }
+        const float mean = row_sum<NT>(acc.x + acc.y, red[0]) / n;
+        acc = both(0.f);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (8 * (t + NT * i) < d)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 e = sub2(g[i].pair(j), both(mean));
+                    acc = fma2(e, e, acc);
+                }
+        const float std = __fsqrt_rn(row_sum<NT>(acc.x + acc.y, red[1]) / n);
+        const float cutoff = fmaf(std, z, mean);
+        if (t == 0)
+            std_out[r] = std;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            finish_vec(g[i], held(slot, 1, i), cutoff, 8 * (t + NT * i), d, out + r * d,
+                       codes + r * 2 * d, scales + r * 2 * B, B);
+        slot = slot == S - 1 ? 0 : slot + 1;
+    }
+}
+
+template <class T, int NT, int V, int S>
+__global__ void __launch_bounds__(NT, 1024 / NT)
+sparse_backward_ring(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
+                     const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
+                     const float *__restrict__ std_in, int64_t rows, int d, int64_t gs, int B,
+                     float z) {
+    constexpr int P = sizeof(T) / 2;
+    extern __shared__ __align__(16) uint4 ring[];          // [S][V][P][NT], then the codes:
+    uint2 *const ring8 = reinterpret_cast<uint2 *>(ring + S * V * P * NT);   // [S][2][V][NT]
+    __shared__ float red[2][NT / 32];
+    const int t = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t G = gridDim.x;
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16u * t;
+    const uint32_t base8 = static_cast<uint32_t>(__cvta_generic_to_shared(ring8)) + 8u * t;
+    const auto fetch = [&](int64_t r, int slot) {
+        if (r < rows) {
+            const T *y = grad + r * gs + 8 * t;
+            const int8_t *q = codes + r * 2 * d + 8 * t;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (8 * (t + NT * i) < d) {
+                    copy8(base8 + 8u * NT * ((slot * 2) * V + i), q + 8 * NT * i);
+                    copy8(base8 + 8u * NT * ((slot * 2 + 1) * V + i), q + d + 8 * NT * i);
+#pragma unroll
+                    for (int k = 0; k < P; ++k)
+                        copy16(base + 16u * NT * ((slot * V + i) * P + k),
+                               y + 8 * NT * i + 16 / sizeof(T) * k);
+                }
+        }
+        copy_commit();
+    };
+    // the scales are read a row ahead too, into registers: bytes have no cp.async
+    uint32_t sg[V], su[V];
+    float std = 0.f;
+    const auto fetch_scales = [&](int64_t r) {
+        if (r >= rows)
+            return;
+        const uint8_t *sc = scales + r * 2 * B + t / 4;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (8 * (t + NT * i) < d) {
+                sg[i] = __ldg(sc + NT / 4 * i);
+                su[i] = __ldg(sc + B + NT / 4 * i);
+            }
+        std = __ldg(std_in + r);
+    };
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k)
+        fetch(blockIdx.x + k * G, k);
+    fetch_scales(blockIdx.x);
+    int slot = 0, k = 0;
+    for (int64_t r = blockIdx.x; r < rows; r += G, k ^= 1) {
+        fetch(r + (S - 1) * G, slot == 0 ? S - 1 : slot - 1);
+        copy_wait<S - 1>();
+        T *gi = grad_in + r * 2 * d;
+        float2 h[V][4], acc = both(0.f);
+        float step[V];
+        const float dev = std;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = 8 * (t + NT * i);
+            if (c >= d)
+                continue;
+            step[i] = code_step(sg[i]);
+            const float stu = code_step(su[i]);
+            const uint2 bg = bias_codes(ring8[((slot * 2) * V + i) * NT + t]);
+            const uint2 bu = bias_codes(ring8[((slot * 2 + 1) * V + i) * NT + t]);
+            Vec8<T> dy, ou, oo;
+            uint4 *q = reinterpret_cast<uint4 *>(&dy);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                q[p] = ring[((slot * V + i) * P + p) * NT + t];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const GateGrad2 m = sparse_grad(decode_pair(bg, j, step[i]), decode_pair(bu, j, stu),
+                                                dy.pair(j));
+                h[i][j] = m.gate;
+                acc = add2(acc, m.gate);
+                ou.put(j, m.up);
+                oo.put(j, m.out);
+            }
+            ou.store(gi + d + c);
+            if (out)
+                oo.store(out + r * d + c);
+        }
+        fetch_scales(r + G);
+        // grad = h - m (1 + inv (delta + z std)), m the mean of h, inv = z / std
+        const float m = row_sum<NT>(acc.x + acc.y, red[k]) / static_cast<float>(d);
+        const float inv = dev == 0.f ? 0.f : z / dev;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = 8 * (t + NT * i);
+            if (c >= d)
+                continue;
+            const uint2 bg = bias_codes(ring8[((slot * 2) * V + i) * NT + t]);
+            Vec8<T> og;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                og.put(j, fma2(both(-m), fma2(both(inv), add2(decode_pair(bg, j, step[i]), both(z * dev)),
+                                              both(1.f)), h[i][j]));
+            og.store(gi + c);
+        }
+        slot = slot == S - 1 ? 0 : slot + 1;
     }
 }
 
@@ -824,6 +1024,14 @@ template <class F> bool with_row_cta(int64_t nv, int *rc, F f) {
     else
         return false;
     return true;
+}
+
+// Rows of which one CTA of 1024 threads holds a single one, more of them than
+// SMs, take the ring.  Measured on GB300 at 2048 x 16384 bf16: forward 74.6 -> 60.5
+// us, backward 79.7 -> 69.1 us; narrower rows, of which an SM runs several
+// CTAs, are faster without it (2000 x 4096 fp16: forward 14.8 against 17.6 us).
+bool takes_ring(int64_t T, int64_t nv, int64_t size) {
+    return size == 2 && nv > 1024 && nv <= 2048 && T > device_sm_count();
 }
 
 constexpr int kForwardVpt = 1, kBackwardVpt = 1, kValuesVpt = 4;
@@ -976,6 +1184,19 @@ extern "C" int gelu_and_mul_sparse_checkpoint(void *out, int8_t *codes, uint8_t 
                 static_cast<float>(z)));
         };
         int done;
+        if constexpr (sizeof(E) == 2)
+            if (vec && takes_ring(T, d / 8, sizeof(E))) {
+                constexpr int kSlots = 3;
+                constexpr size_t smem = kSlots * 2 * 1024 * 16 * sizeof(E);
+                const auto kernel = sparse_forward_ring<E, 1024, 2, kSlots>;
+                const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
+                if (e != cudaSuccess)
+                    return cuda_status(e);
+                return launched(launch_kernel(
+                    kernel, dim3(device_sm_count()), dim3(1024), smem, stream, 1, as<E>(r[0]), as<int8_t>(r[1]), as<uint8_t>(r[2]),
+                    as<float>(r[3]), as<const E>(r[4]), T, static_cast<int>(d), row_stride,
+                    static_cast<int>(B), static_cast<float>(z)));
+            }
         if (vec && with_row_cta(d / 8, &done, go))
             return done;
         const auto any = [&](auto nt, auto v) {
@@ -1025,6 +1246,19 @@ extern "C" int gelu_and_mul_sparse_backward(void *grad_in, void *out, const void
                 static_cast<int>(B), static_cast<float>(z)));
         };
         int done;
+        if constexpr (sizeof(E) == 2)
+            if (vec && takes_ring(T, d / 8, sizeof(E))) {
+                constexpr int kSlots = 3;
+                constexpr size_t smem = kSlots * 2 * 1024 * (8 * sizeof(E) + 16);
+                const auto kernel = sparse_backward_ring<E, 1024, 2, kSlots>;
+                const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
+                if (e != cudaSuccess)
+                    return cuda_status(e);
+                return launched(launch_kernel(
+                    kernel, dim3(device_sm_count()), dim3(1024), smem, stream, 1, as<E>(r[0]), as<E>(r[1]), as<const E>(r[2]),
+                    as<const int8_t>(r[3]), as<const uint8_t>(r[4]), as<const float>(r[5]), T,
+                    static_cast<int>(d), grad_stride, static_cast<int>(B), static_cast<float>(z)));
+            }
         if (vec && with_row_cta(d / 8, &done, go))
             return done;
         const auto any = [&](auto nt, auto v) {

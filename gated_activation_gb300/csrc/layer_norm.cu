@@ -257,14 +257,6 @@ ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restr
 // just the vectors it will read itself, so the ring needs no barrier: its own
 // wait_group is all.  The row's two sums are the only barrier.
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <class T, class W, int NT, int V, int S>
 __global__ void __launch_bounds__(NT, 512 / NT)
 ln_backward_vec(T *__restrict__ grad_in, float *__restrict__ part, const T *__restrict__ grad,

@@ -101,12 +101,41 @@ __device__ __forceinline__ float2 relu_nan2(float2 x) {
     asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(s.y) : "f"(x.y));
     return s;
 }
-// The same of gelu_tanh at s = max(delta, 0); gate is 0 where delta <= 0.
+
+// gelu_tanh at s >= 0 (or NaN), where sigma = 1 / (1 + e) with e = 2^{-2 y} <= 1
+// takes one exponential less and no limit; 1 - sigma = e r.
+__device__ __forceinline__ void gate_of_positive(float2 s, float2 *e, float2 *r) {
+    const float2 y2 = mul2(s, fma2(mul2(s, s), both(-2.f * Gelu::e * Gelu::k2c),
+                                   both(-2.f * Gelu::e * Gelu::k2)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e->x) : "f"(y2.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e->y) : "f"(y2.y));
+    const float2 n = add2(*e, both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r->x) : "f"(n.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r->y) : "f"(n.y));
+}
+// gelu_tanh(max(delta, 0)) u, and its gradients; gate is 0 where delta <= 0.
+__device__ __forceinline__ float2 sparse_mul(float2 delta, float2 u) {
+    const float2 s = relu_nan2(delta);
+    float2 e, r;
+    gate_of_positive(s, &e, &r);
+    return mul2(mul2(s, r), u);
+}
 __device__ __forceinline__ GateGrad2 sparse_grad(float2 delta, float2 u, float2 dy) {
-    GateGrad2 m = act_grad<Gelu>(relu_nan2(delta), u, dy);
+    const float2 s = relu_nan2(delta);
+    float2 e, r;
+    gate_of_positive(s, &e, &r);
+    const float2 p = mul2(s, r), w = fma2(Gelu::lean(s), mul2(e, r), both(1.f));
+    GateGrad2 m = {mul2(mul2(mul2(u, r), w), dy), mul2(p, dy), mul2(p, u)};
     m.gate.x = delta.x <= 0.f ? 0.f : m.gate.x;
     m.gate.y = delta.y <= 0.f ? 0.f : m.gate.y;
     return m;
+}
+
+// max(t, |a|, |b|), NaN if one is NaN.
+__device__ __forceinline__ float max_abs(float t, float2 v) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(t), "f"(v.x), "f"(v.y));
+    return r;
 }
 
 // ------------------------------------------------------------ 8 elements
@@ -179,14 +208,25 @@ template <> struct Vec8<float> {
         w[1] = __float_as_uint(f.y);
     }
     __device__ uint32_t top() const {
-        uint32_t t = 0;
+        float t = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            t = max(t, max(max(q[i].x & 0x7FFFFFFFu, q[i].y & 0x7FFFFFFFu),
-                           max(q[i].z & 0x7FFFFFFFu, q[i].w & 0x7FFFFFFFu)));
-        return t;
+        for (int i = 0; i < 4; ++i)
+            t = max_abs(t, pair(i));
+        return __float_as_uint(t);
     }
 };
+
+// Asynchronous copies to shared memory, by the thread that will read them.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Bits of a largest magnitude (Vec8::top) as those of the fp32 value.
 template <class T> __device__ __forceinline__ uint32_t top_as_float(uint32_t t) {
@@ -236,29 +276,36 @@ __device__ __forceinline__ int code_of(float v, float factor) {
 
 // The codes of 8 values of one block, for the block's scale.
 template <bool KEEP_SIGN>
-__device__ __forceinline__ uint2 codes_of(const float2 (&v)[4], uint32_t scale) {
-    const float f = code_factor(scale);
-    const float2 f2 = make_float2(f, f), magic = make_float2(12582912.f, 12582912.f);
+__device__ __forceinline__ uint2 pack_codes(const float2 (&v)[4], float factor) {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float2 x = v[i];
-        if (scale == kTopScale)
-            x = make_float2(clamp_top(x.x), clamp_top(x.y));
-        const float2 q = fma2(x, f2, magic);
+        const float2 q = fma2(v[i], both(factor), both(12582912.f));
         w[2 * i] = __float_as_uint(q.x);
         w[2 * i + 1] = __float_as_uint(q.y);
         if (KEEP_SIGN) {   // 12582912 + 1, the bits of code 1
-            if (x.x > 0.f)
+            if (v[i].x > 0.f)
                 w[2 * i] = max(w[2 * i], 0x4B400001u);
-            if (x.y > 0.f)
+            if (v[i].y > 0.f)
                 w[2 * i + 1] = max(w[2 * i + 1], 0x4B400001u);
         }
     }
-    uint2 c;
-    c.x = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
-    c.y = __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410);
-    return scale == kBadScale ? make_uint2(0u, 0u) : c;
+    return make_uint2(
+        __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410),
+        __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410));
+}
+template <bool KEEP_SIGN>
+__device__ __forceinline__ uint2 codes_of(const float2 (&v)[4], uint32_t scale) {
+    if (scale >= kTopScale) {   // a block at the very end of the range, or a bad one
+        if (scale == kBadScale)
+            return make_uint2(0u, 0u);
+        float2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = make_float2(clamp_top(v[i].x), clamp_top(v[i].y));
+        return pack_codes<KEEP_SIGN>(x, __uint_as_float((254u - kTopScale) << 23));
+    }
+    return pack_codes<KEEP_SIGN>(v, __uint_as_float((254u - scale) << 23));
 }
 
 // Codes 2i and 2i + 1 of 8 (biased: codes ^ 0x80808080) as values: the byte
