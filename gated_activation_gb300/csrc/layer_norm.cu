@@ -149,30 +149,59 @@ ln_backward_reduce(float *__restrict__ grad_weight, float *__restrict__ grad_bia
     }
 }
 
-// ------------------------------------------------------- forward, vectors
+// ------------------------------------------------------- vectors, a ring
 //
-// The row in registers: TPR threads hold it, thread t the 8-element vectors
-// t, t + TPR, ..., V of them; a CTA of max(TPR, 128) threads takes 128 / TPR
-// rows where a row needs one warp only.  The row's loads bypass L1, so that
-// the parameters, read by every CTA, stay in it.
+// Persistent CTAs, each row held by TPR threads, thread t with the 8-element
+// vectors t, t + TPR, ..., V of them; the parameters stay in registers.  Rows
+// reach their threads through a ring of S shared-memory slots that cp.async
+// fills S - 1 rows ahead, so that HBM keeps streaming while a row is summed
+// and written.  A thread copies just the vectors it will read itself: its own
+// wait_group is all the synchronization that the ring needs.
 
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float *red) {
-    v = warp_sum(v);
-    if constexpr (TPR > 32) {
-        if ((threadIdx.x & 31) == 0)
-            red[threadIdx.x >> 5] = v;
-        __syncthreads();
-        constexpr int NW = TPR / 32;
-        v = red[threadIdx.x & (NW - 1)];
-#pragma unroll
-        for (int o = NW / 2; o > 0; o >>= 1)
-            v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+// This thread's part of the ring: `which` counts the rows of a slot (the
+// input, and in the backward pass the gradient).
+template <class T, int NT, int TPR, int V, int ROWS> struct Ring {
+    static constexpr int P = sizeof(T) / 2;    // 16-byte pieces of a vector
+    uint4 *mine;                               // [S][ROWS][V][P][NT]
+    uint32_t at;
+    int t, d;
+    __device__ Ring(uint4 *ring, int t_, int d_)
+        : mine(ring + threadIdx.x),
+          at(static_cast<uint32_t>(__cvta_generic_to_shared(ring + threadIdx.x))), t(t_), d(d_) {}
+    __device__ static int index(int slot, int which, int i, int p) {
+        return (((slot * ROWS + which) * V + i) * P + p) * NT;
     }
-    return v;
+    __device__ void fetch(int slot, int which, const T *row) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (8 * (t + TPR * i) < d)
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    copy16(at + 16u * index(slot, which, i, p),
+                           row + 8 * (t + TPR * i) + 16 / sizeof(T) * p);
+    }
+    // Zero past the row's end.
+    __device__ Vec8<T> held(int slot, int which, int i) const {
+        Vec8<T> v = Vec8<T>::zero();
+        if (8 * (t + TPR * i) < d) {
+            uint4 *q = reinterpret_cast<uint4 *>(&v);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                q[p] = mine[index(slot, which, i, p)];
+        }
+        return v;
+    }
+};
+
+// Barrier of the TPR threads of one row: the CTA's, or one of its named ones.
+template <int NT, int TPR> __device__ __forceinline__ void row_barrier() {
+    if constexpr (TPR == NT)
+        __syncthreads();
+    else if constexpr (TPR > 32)
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / TPR), "n"(TPR) : "memory");
 }
 
-// 8 parameters through L1.
+// 8 parameters.
 template <class W> __device__ __forceinline__ Vec8<W> load_params(const W *p) {
     Vec8<W> v;
     uint4 *q = reinterpret_cast<uint4 *>(&v);
@@ -182,25 +211,120 @@ template <class W> __device__ __forceinline__ Vec8<W> load_params(const W *p) {
     return v;
 }
 
-template <class T, class W, int TPR, int V>
-__global__ void __launch_bounds__(TPR > 128 ? TPR : 128)
-ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restrict__ rstd_out,
-               const T *__restrict__ in, const W *__restrict__ weight, const W *__restrict__ bias,
-               int64_t rows, int d, int64_t rs, float eps) {
-    constexpr int kRows = TPR > 128 ? 1 : 128 / TPR;
-    __shared__ float red[2][TPR > 32 ? TPR / 32 : 1];
+// Sum over the NT threads of a CTA that holds one row; red holds NT / 32 floats.
+template <int NT> __device__ __forceinline__ float row_sum(float v, float *red) {
+    v = warp_sum(v);
+    if constexpr (NT > 32) {
+        if ((threadIdx.x & 31) == 0)
+            red[threadIdx.x >> 5] = v;
+        __syncthreads();
+        constexpr int NW = NT / 32;
+        v = red[threadIdx.x & (NW - 1)];
+#pragma unroll
+        for (int o = NW / 2; o > 0; o >>= 1)
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    }
+    return v;
+}
+
+template <class T, class W, int NT, int V, int S>
+__global__ void __launch_bounds__(NT, 1024 / NT)
+ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__restrict__ rstd_out,
+                const T *__restrict__ in, const W *__restrict__ weight, const W *__restrict__ bias,
+                int64_t rows, int d, int64_t rs, float eps) {
+    extern __shared__ __align__(16) uint4 slots[];
+    __shared__ float red[2][NT / 32];
+    const int t = threadIdx.x;
     pdl_wait();
     pdl_trigger();
-    const int t = threadIdx.x % TPR;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
-    if (kRows > 1 && r >= rows)      // whole warps: a row of several warps has its CTA alone
-        return;
+    const int64_t G = gridDim.x;
+    const Ring<T, NT, NT, V, 1> ring(slots, t, d);
+    const auto fetch = [&](int64_t r, int slot) {
+        if (r < rows)
+            ring.fetch(slot, 0, in + r * rs);
+        copy_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k)
+        fetch(blockIdx.x + k * G, k);
+    Vec8<W> w[V], b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (t + NT * i);
+        w[i] = c < d ? load_params(weight + c) : Vec8<W>::zero();
+        b[i] = c < d && bias ? load_params(bias + c) : Vec8<W>::zero();
+    }
+    int slot = 0;
+    const float n = static_cast<float>(d);
+    for (int64_t r = blockIdx.x; r < rows; r += G) {
+        // the slot read in the round before: this thread is done with it
+        fetch(r + (S - 1) * G, slot == 0 ? S - 1 : slot - 1);
+        copy_wait<S - 1>();
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const Vec8<T> x = ring.held(slot, 0, i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc = add2(acc, x.pair(j));
+        }
+        const float mean = row_sum<NT>(acc.x + acc.y, red[0]) / n;
+        const float2 m2 = make_float2(mean, mean);
+        acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (8 * (t + NT * i) < d) {
+                const Vec8<T> x = ring.held(slot, 0, i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 e = sub2(x.pair(j), m2);
+                    acc = fma2(e, e, acc);
+                }
+            }
+        const float var = row_sum<NT>(acc.x + acc.y, red[1]) / n;
+        const float rstd = 1.0f / __fsqrt_rn(var + eps);
+        const float2 r2 = make_float2(rstd, rstd);
+        if (t == 0) {
+            mean_out[r] = mean;
+            rstd_out[r] = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = 8 * (t + NT * i);
+            if (c >= d)
+                continue;
+            const Vec8<T> x = ring.held(slot, 0, i);
+            Vec8<T> o;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o.put(j, fma2(mul2(sub2(x.pair(j), m2), r2), w[i].pair(j), b[i].pair(j)));
+            o.store(out + r * d + c);
+        }
+        slot = slot == S - 1 ? 0 : slot + 1;
+    }
+}
+
+// ------------------------------------------------- forward, wider rows
+//
+// One CTA per row, which its registers hold; the parameters through L1, which
+// the row's loads bypass.
+
+template <class T, class W, int NT, int V>
+__global__ void __launch_bounds__(NT)
+ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restrict__ rstd_out,
+               const T *__restrict__ in, const W *__restrict__ weight, const W *__restrict__ bias,
+               int d, int64_t rs, float eps) {
+    __shared__ float red[2][NT / 32];
+    pdl_wait();
+    pdl_trigger();
+    const int t = threadIdx.x;
+    const int64_t r = blockIdx.x;
     const T *p = in + r * rs;
     Vec8<T> x[V];
     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = 8 * (t + TPR * i);
+        const int c = 8 * (t + NT * i);
         x[i] = c < d ? Vec8<T>::load(p + c) : Vec8<T>::zero();
     }
 #pragma unroll
@@ -209,18 +333,18 @@ ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restr
         for (int j = 0; j < 4; ++j)
             acc = add2(acc, x[i].pair(j));
     const float n = static_cast<float>(d);
-    const float mean = row_sum<TPR>(acc.x + acc.y, red[0]) / n;
+    const float mean = row_sum<NT>(acc.x + acc.y, red[0]) / n;
     const float2 m2 = make_float2(mean, mean);
     acc = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        if (8 * (t + TPR * i) < d)
+        if (8 * (t + NT * i) < d)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 e = sub2(x[i].pair(j), m2);
                 acc = fma2(e, e, acc);
             }
-    const float var = row_sum<TPR>(acc.x + acc.y, red[1]) / n;
+    const float var = row_sum<NT>(acc.x + acc.y, red[1]) / n;
     const float rstd = 1.0f / __fsqrt_rn(var + eps);
     const float2 r2 = make_float2(rstd, rstd);
     if (t == 0) {
@@ -229,7 +353,7 @@ ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restr
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = 8 * (t + TPR * i);
+        const int c = 8 * (t + NT * i);
         if (c >= d)
             continue;
         const Vec8<W> w = load_params(weight + c);
@@ -248,74 +372,60 @@ ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restr
     }
 }
 
-// ------------------------------------------------------ backward, vectors
+// ------------------------------------------------------ backward, a ring
 //
-// Persistent CTAs: a CTA takes the rows b, b + G, ... and holds its columns'
-// shares of the parameters' gradients, and the weight, in registers; thread
-// t the 8-element vectors t, t + NT, ....  Rows reach it through a ring of S
-// shared-memory slots that cp.async fills S - 1 rows ahead.  A thread copies
-// just the vectors it will read itself, so the ring needs no barrier: its own
-// wait_group is all.  The row's two sums are the only barrier.
+// CTAs of NT threads, NT / TPR rows at a time, each row's TPR threads with a
+// barrier of their own.  A thread holds its columns' shares of the
+// parameters' gradients, and the weight, in registers; at the end the CTA
+// joins its rows' shares in shared memory and writes one share per column.
+// With h = (x - mean) rstd = x rstd + c and g = dy w, the gradient is
+//   rstd (g - A - h B) = dy (w rstd) + x (-B rstd^2) + (-A - c B) rstd.
 
-template <class T, class W, int NT, int V, int S>
-__global__ void __launch_bounds__(NT, 512 / NT)
-ln_backward_vec(T *__restrict__ grad_in, float *__restrict__ part, const T *__restrict__ grad,
-                const T *__restrict__ in, const W *__restrict__ weight,
-                const float *__restrict__ mean_in, const float *__restrict__ rstd_in, int64_t rows,
-                int d, int64_t rs, int64_t gs) {
-    constexpr int P = sizeof(T) / 2;           // 16-byte pieces of a vector
-    constexpr int NW = NT / 32;
-    extern __shared__ __align__(16) uint4 ring[];   // [S][2][V][P][NT]
-    __shared__ float2 red[2][NW];
-    const int t = threadIdx.x;
+constexpr int kBackThreads = 512;
+
+template <class T, class W, int TPR, int V, int S>
+__global__ void __launch_bounds__(kBackThreads, 1)
+ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__restrict__ grad,
+                 const T *__restrict__ in, const W *__restrict__ weight,
+                 const float *__restrict__ mean_in, const float *__restrict__ rstd_in,
+                 int64_t rows, int d, int64_t rs, int64_t gs) {
+    constexpr int NT = kBackThreads, R = NT / TPR, NW = TPR / 32;
+    extern __shared__ __align__(16) uint4 slots[];
+    __shared__ float2 red[2][NT / 32];
+    const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
     pdl_wait();
     pdl_trigger();
-    const int64_t G = gridDim.x;
-    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16u * t;
+    const int64_t G = static_cast<int64_t>(gridDim.x) * R;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * R + group;
+    const Ring<T, NT, TPR, V, 2> ring(slots, t, d);
     const auto fetch = [&](int64_t r, int slot) {
         if (r < rows) {
-            const T *x = in + r * rs, *y = grad + r * gs;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = 8 * (t + NT * i);
-                if (c < d)
-#pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        const uint32_t at = base + 16u * NT * ((slot * 2 * V + i) * P + p);
-                        copy16(at, x + c + 16 / sizeof(T) * p);
-                        copy16(at + 16u * NT * V * P, y + c + 16 / sizeof(T) * p);
-                    }
-            }
+            ring.fetch(slot, 0, in + r * rs);
+            ring.fetch(slot, 1, grad + r * gs);
         }
         copy_commit();
     };
-    const auto held = [&](int slot, int which, int i) {
-        Vec8<T> v;
-        uint4 *q = reinterpret_cast<uint4 *>(&v);
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-            q[p] = ring[(((slot * 2 + which) * V + i) * P + p) * NT + t];
-        return v;
-    };
 #pragma unroll
     for (int k = 0; k < S - 1; ++k)
-        fetch(blockIdx.x + k * G, k);
+        fetch(first + k * G, k);
     Vec8<W> w[V];
     float2 dw[V][4], db[V][4];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = 8 * (t + NT * i);
+        const int c = 8 * (t + TPR * i);
         w[i] = c < d ? load_params(weight + c) : Vec8<W>::zero();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             dw[i][j] = db[i][j] = make_float2(0.f, 0.f);
     }
     int slot = 0, k = 0;
-    float mean = mean_in[blockIdx.x], rstd = rstd_in[blockIdx.x];
-    for (int64_t r = blockIdx.x; r < rows; r += G, k ^= 1) {
+    float mean = first < rows ? mean_in[first] : 0.f, rstd = first < rows ? rstd_in[first] : 0.f;
+    const float n = static_cast<float>(d);
+    for (int64_t r = first; r < rows; r += G, k ^= 1) {
         // the slot read in the round before: this thread is done with it
         fetch(r + (S - 1) * G, slot == 0 ? S - 1 : slot - 1);
-        const float2 m2 = make_float2(mean, mean), r2 = make_float2(rstd, rstd);
+        const float r1 = rstd, c1 = -mean * rstd;
+        const float2 r2 = make_float2(r1, r1), c2 = make_float2(c1, c1);
         if (r + G < rows) {
             mean = mean_in[r + G];
             rstd = rstd_in[r + G];
@@ -324,12 +434,10 @@ ln_backward_vec(T *__restrict__ grad_in, float *__restrict__ part, const T *__re
         float2 a2 = make_float2(0.f, 0.f), b2 = a2;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (8 * (t + NT * i) >= d)
-                continue;
-            const Vec8<T> x = held(slot, 0, i), y = held(slot, 1, i);
+            const Vec8<T> x = ring.held(slot, 0, i), y = ring.held(slot, 1, i);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 dy = y.pair(j), h = mul2(sub2(x.pair(j), m2), r2);
+                const float2 dy = y.pair(j), h = fma2(x.pair(j), r2, c2);
                 db[i][j] = add2(db[i][j], dy);
                 dw[i][j] = fma2(dy, h, dw[i][j]);
                 const float2 g = mul2(dy, w[i].pair(j));
@@ -340,9 +448,9 @@ ln_backward_vec(T *__restrict__ grad_in, float *__restrict__ part, const T *__re
         float a = warp_sum(a2.x + a2.y), b = warp_sum(b2.x + b2.y);
         if constexpr (NW > 1) {
             if ((t & 31) == 0)
-                red[k][t >> 5] = make_float2(a, b);
-            __syncthreads();
-            const float2 s = red[k][t & (NW - 1)];
+                red[k][threadIdx.x >> 5] = make_float2(a, b);
+            row_barrier<NT, TPR>();
+            const float2 s = red[k][group * NW + (t & (NW - 1))];
             a = s.x;
             b = s.y;
 #pragma unroll
@@ -351,36 +459,64 @@ ln_backward_vec(T *__restrict__ grad_in, float *__restrict__ part, const T *__re
                 b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
             }
         }
-        const float n = static_cast<float>(d);
-        const float2 ma = make_float2(-a / n, -a / n), mb = make_float2(-b / n, -b / n);
+        a /= n;
+        b /= n;
+        const float xs = -b * r1 * r1, off = fmaf(-c1, b, -a) * r1;
+        const float2 xs2 = make_float2(xs, xs), off2 = make_float2(off, off);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (t + NT * i);
+            const int c = 8 * (t + TPR * i);
             if (c >= d)
                 continue;
-            const Vec8<T> x = held(slot, 0, i), y = held(slot, 1, i);
+            const Vec8<T> x = ring.held(slot, 0, i), y = ring.held(slot, 1, i);
             Vec8<T> o;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 h = mul2(sub2(x.pair(j), m2), r2);
-                o.put(j, mul2(r2, fma2(h, mb, fma2(y.pair(j), w[i].pair(j), ma))));
-            }
+            for (int j = 0; j < 4; ++j)
+                o.put(j, fma2(y.pair(j), mul2(w[i].pair(j), r2), fma2(x.pair(j), xs2, off2)));
             o.store(grad_in + r * d + c);
         }
         slot = slot == S - 1 ? 0 : slot + 1;
     }
-    float *pw = part + static_cast<int64_t>(blockIdx.x) * d, *pb = pw + G * d;
+    // columns' shares: over the CTA's rows in shared memory, group by group
+    float *pw = part + static_cast<int64_t>(blockIdx.x) * d;
+    float *pb = pw + static_cast<int64_t>(gridDim.x) * d;
+    if constexpr (R == 1) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = 8 * (t + NT * i);
-        if (c >= d)
-            continue;
+        for (int i = 0; i < V; ++i) {
+            const int c = 8 * (t + TPR * i);
+            if (c >= d)
+                continue;
 #pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-            *reinterpret_cast<float4 *>(pw + c + 2 * j) =
-                make_float4(dw[i][j].x, dw[i][j].y, dw[i][j + 1].x, dw[i][j + 1].y);
-            *reinterpret_cast<float4 *>(pb + c + 2 * j) =
-                make_float4(db[i][j].x, db[i][j].y, db[i][j + 1].x, db[i][j + 1].y);
+            for (int j = 0; j < 4; j += 2) {
+                *reinterpret_cast<float4 *>(pw + c + 2 * j) =
+                    make_float4(dw[i][j].x, dw[i][j].y, dw[i][j + 1].x, dw[i][j + 1].y);
+                *reinterpret_cast<float4 *>(pb + c + 2 * j) =
+                    make_float4(db[i][j].x, db[i][j].y, db[i][j + 1].x, db[i][j + 1].y);
+            }
+        }
+    } else {
+        // [R][8 V TPR] for the weight, then, once read, for the bias
+        constexpr int kCols = 8 * V * TPR;
+        float *sum = reinterpret_cast<float *>(slots);
+        copy_wait<0>();
+        __syncthreads();      // every group is done with the ring
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<float2 *>(sum + group * kCols + 8 * (t + TPR * i) + 2 * j) =
+                        which ? db[i][j] : dw[i][j];
+            __syncthreads();
+            for (int c = threadIdx.x; c < d; c += NT) {
+                float s = sum[c];
+#pragma unroll
+                for (int q = 1; q < R; ++q)
+                    s += sum[q * kCols + c];
+                (which ? pb : pw)[c] = s;
+            }
+            __syncthreads();
         }
     }
 }
@@ -408,52 +544,51 @@ template <class F> int with_types(int dtype, int param_dtype, F f) {
     });
 }
 
-// CTAs whose shares of the parameters' gradients the second kernel joins: as
-// many as run at once (512 threads per SM).
-int64_t shares(int64_t T, int64_t d) {
-    const int64_t per_sm = d <= 1024 ? 8 : d <= 2048 ? 4 : d <= 4096 ? 2 : 1;
-    return std::min<int64_t>(T, device_sm_count() * per_sm);
-}
+// Shares of the parameters' gradients that the second kernel joins: one per
+// SM, or per row where there are fewer rows.
+int64_t shares(int64_t T) { return std::min<int64_t>(T, device_sm_count()); }
 
 template <int N> using Const = std::integral_constant<int, N>;
 
-// Calls f(integral constants TPR, V) for the forward pass over rows of nv
-// vectors; false when no CTA holds such a row.
-template <class F> bool with_forward(int64_t nv, int *rc, F f) {
+// Calls f(integral constants NT, V, S) for the forward ring over rows of nv
+// vectors, 1024 threads per SM; false when it holds no such row.
+template <int SIZE, class F> bool with_forward_ring(int64_t nv, int *rc, F f) {
+    constexpr int S = SIZE == 2 ? 4 : 3;
     if (nv <= 32)
-        *rc = f(Const<32>{}, Const<1>{});
+        *rc = f(Const<32>{}, Const<1>{}, Const<S>{});
     else if (nv <= 64)
-        *rc = f(Const<32>{}, Const<2>{});
+        *rc = f(Const<32>{}, Const<2>{}, Const<S>{});
     else if (nv <= 128)
-        *rc = f(Const<32>{}, Const<4>{});
+        *rc = f(Const<64>{}, Const<2>{}, Const<S>{});
     else if (nv <= 256)
-        *rc = f(Const<128>{}, Const<2>{});
+        *rc = f(Const<128>{}, Const<2>{}, Const<S>{});
     else if (nv <= 512)
-        *rc = f(Const<256>{}, Const<2>{});
+        *rc = f(Const<256>{}, Const<2>{}, Const<S>{});
     else if (nv <= 1024)
-        *rc = f(Const<512>{}, Const<2>{});
+        *rc = f(Const<512>{}, Const<2>{}, Const<S>{});
     else if (nv <= 2048)
-        *rc = f(Const<512>{}, Const<4>{});
-    else if (nv <= 4096)
-        *rc = f(Const<1024>{}, Const<4>{});
+        *rc = f(Const<1024>{}, Const<2>{}, Const<S>{});
     else
         return false;
     return true;
 }
 
-// The same of the backward pass, with S ring slots: the CTAs of one SM, 512
-// threads, share its shared memory.
-template <int SIZE, class F> bool with_backward(int64_t nv, int *rc, F f) {
-    if (nv <= 64)
-        *rc = f(Const<64>{}, Const<1>{}, Const<4>{});
+// Calls f(integral constants TPR, V, S) for the backward ring: the slots of
+// the 512 threads of an SM take up to 192 KB of shared memory.
+template <int SIZE, class F> bool with_backward_ring(int64_t nv, int *rc, F f) {
+    constexpr int S2 = SIZE == 2 ? 6 : 3;    // slots at two vectors per thread
+    if (nv <= 32)
+        *rc = f(Const<32>{}, Const<1>{}, Const<S2>{});
+    else if (nv <= 64)
+        *rc = f(Const<32>{}, Const<2>{}, Const<S2>{});
     else if (nv <= 128)
-        *rc = f(Const<64>{}, Const<2>{}, Const<SIZE == 2 ? 5 : 3>{});
+        *rc = f(Const<64>{}, Const<2>{}, Const<S2>{});
     else if (nv <= 256)
-        *rc = f(Const<128>{}, Const<2>{}, Const<SIZE == 2 ? 6 : 3>{});
+        *rc = f(Const<128>{}, Const<2>{}, Const<S2>{});
     else if (nv <= 512)
-        *rc = f(Const<256>{}, Const<2>{}, Const<SIZE == 2 ? 6 : 3>{});
+        *rc = f(Const<256>{}, Const<2>{}, Const<S2>{});
     else if (nv <= 1024)
-        *rc = f(Const<512>{}, Const<2>{}, Const<SIZE == 2 ? 6 : 3>{});
+        *rc = f(Const<512>{}, Const<2>{}, Const<S2>{});
     else {
         if constexpr (SIZE == 2)
             if (nv <= 2048) {
@@ -493,18 +628,28 @@ extern "C" int layer_norm(void *out, float *mean, float *rstd, const void *in, c
     return with_types(dtype, param_dtype, [&](auto t, auto w) {
         using E = decltype(t);
         using W = decltype(w);
-        const auto go = [&](auto tpr, auto v) {
-            constexpr int NT = tpr() > 128 ? tpr() : 128;
+        const auto go = [&](auto nt, auto v, auto slots) {
+            constexpr size_t smem = slots() * v() * nt() * 8 * sizeof(E);
+            const auto kernel = ln_forward_ring<E, W, nt(), v(), slots()>;
+            const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
+            if (e != cudaSuccess)
+                return cuda_status(e);
+            const int64_t ctas = std::min<int64_t>(T, device_sm_count() * (1024 / nt()));
             return launched(launch_kernel(
-                ln_forward_vec<E, W, tpr(), v()>,
-                dim3(static_cast<unsigned>(ceil_div64(T, NT / tpr()))), dim3(NT), 0, stream, 1,
+                kernel, dim3(static_cast<unsigned>(ctas)), dim3(nt()), smem, stream, 1,
                 as<E>(r[0]), as<float>(r[1]), as<float>(r[2]), as<const E>(r[3]),
                 as<const W>(r[4]), as<const W>(r[5]), T, static_cast<int>(d), row_stride,
                 static_cast<float>(eps)));
         };
         int done;
-        if (vec && with_forward(d / 8, &done, go))
+        if (vec && with_forward_ring<sizeof(E)>(d / 8, &done, go))
             return done;
+        if (vec && d / 8 <= 4096)
+            return launched(launch_kernel(
+                ln_forward_vec<E, W, 1024, 4>, dim3(static_cast<unsigned>(T)), dim3(1024), 0,
+                stream, 1, as<E>(r[0]), as<float>(r[1]), as<float>(r[2]), as<const E>(r[3]),
+                as<const W>(r[4]), as<const W>(r[5]), static_cast<int>(d), row_stride,
+                static_cast<float>(eps)));
         return launched(launch_kernel(ln_forward_any<E, W>, dim3(static_cast<unsigned>(grid)),
                                       dim3(kThreads), 0, stream, 1, as<E>(r[0]), as<float>(r[1]),
                                       as<float>(r[2]), as<const E>(r[3]), as<const W>(r[4]),
@@ -516,7 +661,7 @@ extern "C" int layer_norm(void *out, float *mean, float *rstd, const void *in, c
 extern "C" size_t layer_norm_backward_workspace_bytes(int64_t T, int64_t d) {
     if (T <= 0 || d <= 0 || d > gact::kMaxWidth)
         return 16;
-    return static_cast<size_t>(std::max<int64_t>(16, gact::shares(T, d) * d * 8));
+    return static_cast<size_t>(std::max<int64_t>(16, gact::shares(T) * d * 8));
 }
 
 extern "C" int layer_norm_backward(void *grad_in, float *grad_weight, float *grad_bias,
@@ -553,21 +698,21 @@ extern "C" int layer_norm_backward(void *grad_in, float *grad_weight, float *gra
         rc = with_types(dtype, param_dtype, [&](auto t, auto w) {
             using E = decltype(t);
             using W = decltype(w);
-            const auto go = [&](auto nt, auto v, auto slots) {
-                constexpr size_t smem = 2 * slots() * v() * nt() * 8 * sizeof(E);
-                const auto kernel = ln_backward_vec<E, W, nt(), v(), slots()>;
+            const auto go = [&](auto tpr, auto v, auto slots) {
+                constexpr size_t smem = 2 * slots() * v() * kBackThreads * 8 * sizeof(E);
+                const auto kernel = ln_backward_ring<E, W, tpr(), v(), slots()>;
                 const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
                 if (e != cudaSuccess)
                     return cuda_status(e);
-                n = shares(T, d);
+                n = std::min<int64_t>(shares(T), ceil_div64(T, kBackThreads / tpr()));
                 return launched(launch_kernel(
-                    kernel, dim3(static_cast<unsigned>(n)), dim3(nt()), smem, stream, 1,
+                    kernel, dim3(static_cast<unsigned>(n)), dim3(kBackThreads), smem, stream, 1,
                     as<E>(r[0]), part, as<const E>(r[4]), as<const E>(r[5]), as<const W>(r[6]),
                     as<const float>(r[7]), as<const float>(r[8]), T, static_cast<int>(d),
                     row_stride, grad_stride));
             };
             int done;
-            if (vec && with_backward<sizeof(E)>(d / 8, &done, go))
+            if (vec && with_backward_ring<sizeof(E)>(d / 8, &done, go))
                 return done;
             const int64_t grid = std::min<int64_t>(T, int64_t(device_sm_count()) * 64);
             done = launched(launch_kernel(
@@ -576,7 +721,7 @@ extern "C" int layer_norm_backward(void *grad_in, float *grad_weight, float *gra
                 as<const float>(r[7]), as<const float>(r[8]), T, d, row_stride, grad_stride));
             if (done != GATED_ACT_OK)
                 return done;
-            const int64_t per = ceil_div64(T, shares(T, d));
+            const int64_t per = ceil_div64(T, shares(T));
             n = ceil_div64(T, per);
             return launched(launch_kernel(
                 ln_backward_columns_any<E>,
