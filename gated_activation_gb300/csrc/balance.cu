@@ -24,40 +24,51 @@
 namespace gact {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kThreads = 256;             // of the cluster, and of the backward pass
 constexpr int kMaxExperts = 1024;
+constexpr int kSumRows = 8;               // rows of the shared sums, each for every 8th warp
 constexpr int kCluster = 8;
 
 // ------------------------------------------------------------------- tokens
 
 // The logits of one token held by one lane, V groups of N: group i starts at
-// element (i * L + lane) * N.
+// element (i * L + lane) * N.  Raw: as loaded, so that the next token's can be
+// on their way while this one is computed.
+template <class T, int L, int V, int N> struct Raw {
+    std::conditional_t<N == 8, Vec8<T>, T> v[V];
+    __device__ void load(const T *row, int E, int lane) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = (i * L + lane) * N;
+            if (c < E) {
+                if constexpr (N == 8)
+                    v[i] = Vec8<T>::load(row + c);
+                else
+                    v[i] = __ldg(row + c);
+            }
+        }
+    }
+};
+
 template <class T, int L, int V, int N> struct Row {
     float x[V * N];
 
     __device__ static int column(int lane, int i) { return (i / N * L + lane) * N + i % N; }
 
-    __device__ void load(const T *row, int E, int lane) {
+    // E = 0: a row of -infinity.
+    __device__ void expand(const Raw<T, L, V, N> &raw, int E, int lane) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = (i * L + lane) * N;
+            const bool in = (i * L + lane) * N < E;
             if constexpr (N == 8) {
-                if (c < E) {
-                    const Vec8<T> v = Vec8<T>::load(row + c);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = v.pair(j);
-                        x[8 * i + 2 * j] = f.x;
-                        x[8 * i + 2 * j + 1] = f.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        x[8 * i + j] = -INFINITY;
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = raw.v[i].pair(j);
+                    x[8 * i + 2 * j] = in ? f.x : -INFINITY;
+                    x[8 * i + 2 * j + 1] = in ? f.y : -INFINITY;
                 }
             } else {
-                x[i] = c < E ? to_float(row[c]) : -INFINITY;
+                x[i] = in ? to_float(raw.v[i]) : -INFINITY;
             }
         }
     }
@@ -122,59 +133,90 @@ struct Ids {
     }
 };
 
-// Sums of the tokens [t0, t1) into shared memory: sums [kWarps][E] (a row per
-// warp), hist [E + 1] counts and live tokens.  Ends with a barrier.
-template <class T, int L, int V, int N>
+// Sums of the tokens [t0, t1) into shared memory: sums [kSumRows][E], of which
+// row r holds every kSumRows-th warp's, hist [E + 1] counts and live tokens.
+// NT threads; ends with a barrier.
+template <class T, int NT, int L, int V, int N>
 __device__ __forceinline__ void sum_tokens(float *sums, int *hist, const T *logits, Ids ids,
                                            const uint8_t *live, int64_t t0, int64_t t1, int E,
                                            int k, int64_t ls) {
     constexpr int kTokens = 32 / L;       // tokens of a warp at a time
+    constexpr int kWarps = NT / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int part = lane / L, sub = lane % L;
+    using R = Row<T, L, V, N>;
+    // two tokens on their way
+    Raw<T, L, V, N> raw[2];
+    bool on[2];
+    const auto fetch = [&](int64_t t, int slot) {
+        on[slot] = t + part < t1 && (!live || live[t + part]);
+        raw[slot].load(logits + (t + part) * ls, on[slot] ? E : 0, sub);
+    };
+    const int64_t step = kWarps * kTokens;
+    int64_t t = t0 + warp * kTokens;
+    fetch(t, 0);
+    fetch(t + step, 1);
+    // the counts, while the first tokens arrive
+    const int64_t first = t0 * k, n = (t1 - t0) * k;
+#pragma unroll 4
+    for (int64_t j = threadIdx.x; j < n; j += NT) {
+        const int64_t e = ids.at(first + j);
+        if (e >= 0 && e < E && (!live || live[t0 + static_cast<uint32_t>(j) / static_cast<uint32_t>(k)]))
+            atomicAdd(hist + e, 1);
+    }
     float acc[V * N];
 #pragma unroll
     for (int i = 0; i < V * N; ++i)
         acc[i] = 0.f;
     int mine = 0;
     // every lane takes part in the shuffles of every round
-    for (int64_t t = t0 + warp * kTokens; t < t1; t += kWarps * kTokens) {
-        const bool on = t + part < t1 && (!live || live[t + part]);
-        Row<T, L, V, N> p;
-        p.load(logits + (t + part) * ls, on ? E : 0, sub);
+    const auto take = [&](int slot) {
+        R p;
+        p.expand(raw[slot], on[slot] ? E : 0, sub);
+        const bool ok = on[slot];
+        fetch(t + 2 * step, slot);
         p.softmax();
-        if (on) {
+        if (ok) {
             mine += sub == 0;
 #pragma unroll
             for (int i = 0; i < V * N; ++i)
                 acc[i] += p.x[i];
         }
-    }
-    const int64_t first = t0 * k, n = (t1 - t0) * k;
-    for (int64_t j = threadIdx.x; j < n; j += kThreads) {
-        const int64_t e = ids.at(first + j);
-        if (e >= 0 && e < E && (!live || live[t0 + static_cast<uint32_t>(j) / static_cast<uint32_t>(k)]))
-            atomicAdd(hist + e, 1);
+        t += step;
+    };
+    while (t < t1) {
+        take(0);
+        if (t < t1)
+            take(1);
     }
     mine = __reduce_add_sync(0xFFFFFFFFu, mine);
     if (lane == 0 && mine)
         atomicAdd(hist + E, mine);
 #pragma unroll
-    for (int i = 0; i < V * N; ++i) {
-        float a = acc[i];
+    for (int i = 0; i < V * N; ++i)
 #pragma unroll
         for (int o = L; o < 32; o <<= 1)
-            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        const int c = Row<T, L, V, N>::column(sub, i);
-        if (part == 0 && c < E)
-            sums[warp * E + c] = a;
+            acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], o);
+    // the rows of sums take the warps in turn: a fixed order
+#pragma unroll
+    for (int w = 0; w < kWarps; w += kSumRows) {
+        if (part == 0 && warp >= w && warp < w + kSumRows) {
+            float *row = sums + (warp - w) * E;
+#pragma unroll
+            for (int i = 0; i < V * N; ++i) {
+                const int c = R::column(sub, i);
+                if (c < E)
+                    row[c] = w == 0 ? acc[i] : row[c] + acc[i];
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
 }
 
-__device__ __forceinline__ float warps_sum(const float *sums, int E, int e) {
+__device__ __forceinline__ float rows_sum(const float *sums, int E, int e) {
     float s = sums[e];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w)
+    for (int w = 1; w < kSumRows; ++w)
         s += sums[w * E + e];
     return s;
 }
@@ -200,7 +242,8 @@ __device__ __forceinline__ uint32_t peer(const void *p, uint32_t rank) {
 }
 
 // The CTA's share of sum_e c_e p_e, joined over the cluster: rank 0 writes
-// the loss.  `mine`: the thread's term.
+// the loss.  `mine`: the thread's term; red: a float per warp.
+template <int NT>
 __device__ __forceinline__ void write_loss(float *loss, float *share, float *red, float mine,
                                            float scale, uint32_t rank) {
     mine = warp_sum(mine);
@@ -209,7 +252,8 @@ __device__ __forceinline__ void write_loss(float *loss, float *share, float *red
     __syncthreads();
     if (threadIdx.x == 0) {
         float s = 0.f;
-        for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w)
             s += red[w];
         *share = s;
     }
@@ -231,9 +275,9 @@ balance_cluster(float *__restrict__ loss, int32_t *__restrict__ counts,
                 const T *__restrict__ logits, Ids ids,
                 const uint8_t *__restrict__ live, int64_t T_, int64_t per, int E, int k,
                 int64_t ls, float coef) {
-    extern __shared__ float sums[];                            // [kWarps][E]
-    int *hist = reinterpret_cast<int *>(sums + kWarps * E);    // [E + 1]
-    __shared__ float share, red[kWarps];
+    extern __shared__ float sums[];                              // [kSumRows][E]
+    int *hist = reinterpret_cast<int *>(sums + kSumRows * E);    // [E + 1]
+    __shared__ float share, red[kThreads / 32];
     for (int e = threadIdx.x; e <= E; e += kThreads)
         hist[e] = 0;
     __syncthreads();
@@ -241,9 +285,9 @@ balance_cluster(float *__restrict__ loss, int32_t *__restrict__ counts,
     pdl_trigger();
     const uint32_t rank = cluster_rank();
     const int64_t t0 = min(T_, rank * per), t1 = min(T_, t0 + per);
-    sum_tokens<T, L, V, N>(sums, hist, logits, ids, live, t0, t1, E, k, ls);
+    sum_tokens<T, kThreads, L, V, N>(sums, hist, logits, ids, live, t0, t1, E, k, ls);
     for (int e = threadIdx.x; e < E; e += kThreads)
-        sums[e] = warps_sum(sums, E, e);                       // only this thread reads column e
+        sums[e] = rows_sum(sums, E, e);                       // only this thread reads column e
     cluster_sync();
     int n = 0;
     for (int c = 0; c < kCluster; ++c)
@@ -264,71 +308,89 @@ balance_cluster(float *__restrict__ loss, int32_t *__restrict__ counts,
     }
     if (rank == 0 && threadIdx.x == 0)
         tokens[0] = n;
-    write_loss(loss, &share, red, mine,
+    write_loss<kThreads>(loss, &share, red, mine,
                coef * static_cast<float>(E) / (nf * static_cast<float>(k)), rank);
 }
 
 // Long batches: CTA b of G takes the tokens [b * per, (b + 1) * per) and leaves
 // its sums in the workspace, an expert's G of them side by side:
 // part_p [E][G] fp32, part_c [E + 1][G] int32 (the last: live tokens).
-template <class T, int L, int V, int N>
-__global__ void __launch_bounds__(kThreads)
+template <class T, int NT, int L, int V, int N>
+__global__ void __launch_bounds__(NT)
 balance_tokens(float *__restrict__ part_p, int32_t *__restrict__ part_c,
                const T *__restrict__ logits, Ids ids,
                const uint8_t *__restrict__ live, int64_t T_, int64_t per, int E, int k,
                int64_t ls) {
     extern __shared__ float sums[];
-    int *hist = reinterpret_cast<int *>(sums + kWarps * E);
-    for (int e = threadIdx.x; e <= E; e += kThreads)
+    int *hist = reinterpret_cast<int *>(sums + kSumRows * E);
+    for (int e = threadIdx.x; e <= E; e += NT)
         hist[e] = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
     const int64_t t0 = min(T_, blockIdx.x * per), t1 = min(T_, t0 + per);
-    sum_tokens<T, L, V, N>(sums, hist, logits, ids, live, t0, t1, E, k, ls);
+    sum_tokens<T, NT, L, V, N>(sums, hist, logits, ids, live, t0, t1, E, k, ls);
     const int64_t G = gridDim.x;
-    for (int e = threadIdx.x; e <= E; e += kThreads) {
+    for (int e = threadIdx.x; e <= E; e += NT) {
         part_c[e * G + blockIdx.x] = hist[e];
         if (e < E)
-            part_p[e * G + blockIdx.x] = warps_sum(sums, E, e);
+            part_p[e * G + blockIdx.x] = rows_sum(sums, E, e);
     }
 }
 
-// Joins the G sums of every expert: a warp takes an expert.
-__global__ void __launch_bounds__(kThreads)
+// Joins the G sums of every expert, G <= 32 kJoinLoads: a warp takes an expert.
+constexpr int kJoinThreads = 512;
+constexpr int kJoinLoads = 8;
+__global__ void __launch_bounds__(kJoinThreads)
 balance_join(float *__restrict__ loss, int32_t *__restrict__ counts, int32_t *__restrict__ tokens,
              float *__restrict__ mean_p, const float *__restrict__ part_p,
              const int32_t *__restrict__ part_c, int G, int E, float k, float coef) {
+    constexpr int kWarps = kJoinThreads / 32;
     __shared__ float share, red[kWarps];
     pdl_wait();
     pdl_trigger();
     const uint32_t rank = cluster_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int n = 0;
-    for (int g = lane; g < G; g += 32)
-        n += part_c[static_cast<int64_t>(E) * G + g];
+    int e = rank * kWarps + warp;
+    float p[kJoinLoads];
+    int c[kJoinLoads], n = 0;
+    const auto fetch = [&] {
+#pragma unroll
+        for (int i = 0; i < kJoinLoads; ++i) {
+            const bool in = e < E && lane + 32 * i < G;
+            p[i] = in ? part_p[e * G + lane + 32 * i] : 0.f;
+            c[i] = in ? part_c[e * G + lane + 32 * i] : 0;
+        }
+    };
+    fetch();
+#pragma unroll
+    for (int i = 0; i < kJoinLoads; ++i)
+        n += lane + 32 * i < G ? part_c[E * G + lane + 32 * i] : 0;
     n = __reduce_add_sync(0xFFFFFFFFu, n);
     const float nf = static_cast<float>(n > 0 ? n : 1);
     float mine = 0.f;
-    for (int e = rank * kWarps + warp; e < E; e += kCluster * kWarps) {
-        float p = 0.f;
-        int c = 0;
-#pragma unroll 4
-        for (int g = lane; g < G; g += 32) {
-            p += part_p[static_cast<int64_t>(e) * G + g];
-            c += part_c[static_cast<int64_t>(e) * G + g];
+    while (e < E) {
+        float ps = 0.f;
+        int cs = 0;
+#pragma unroll
+        for (int i = 0; i < kJoinLoads; ++i) {
+            ps += p[i];
+            cs += c[i];
         }
-        p = warp_sum(p) / nf;
-        c = __reduce_add_sync(0xFFFFFFFFu, c);
+        const int at = e;
+        e += kCluster * kWarps;
+        fetch();
+        ps = warp_sum(ps) / nf;
+        cs = __reduce_add_sync(0xFFFFFFFFu, cs);
         if (lane == 0) {
-            counts[e] = c;
-            mean_p[e] = p;
-            mine = fmaf(static_cast<float>(c), p, mine);
+            counts[at] = cs;
+            mean_p[at] = ps;
+            mine = fmaf(static_cast<float>(cs), ps, mine);
         }
     }
     if (rank == 0 && threadIdx.x == 0)
         tokens[0] = n;
-    write_loss(loss, &share, red, mine, coef * static_cast<float>(E) / (nf * k), rank);
+    write_loss<kJoinThreads>(loss, &share, red, mine, coef * static_cast<float>(E) / (nf * k), rank);
 }
 
 // Counts enter as c_j - C / E, C their sum, rounded to an integer: the same
@@ -340,12 +402,19 @@ balance_backward(T *__restrict__ grad, const float *__restrict__ grad_loss,
                  const int32_t *__restrict__ tokens, const uint8_t *__restrict__ live, int64_t T_,
                  int E, float k, int64_t ls, float coef) {
     using R = Row<T, L, V, N>;
-    constexpr int kTokens = 32 / L;
+    constexpr int kTokens = 32 / L, kWarps = kThreads / 32;
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, part = lane / L, sub = lane % L;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kTokens;
     int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kTokens + part;
+    Raw<T, L, V, N> raw;
+    bool on;
+    const auto fetch = [&](int64_t at) {
+        on = at < T_ && (!live || live[at]);
+        raw.load(logits + at * ls, on ? E : 0, sub);
+    };
+    fetch(t);
     float c[V * N], sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V * N; ++i) {
@@ -353,18 +422,20 @@ balance_backward(T *__restrict__ grad, const float *__restrict__ grad_loss,
         c[i] = e < E ? static_cast<float>(__ldg(counts + e)) : 0.f;
         sum += c[i];
     }
+    const int n = *tokens;
+    const float up = *grad_loss;
     const float mid = rintf(R::total(sum) / static_cast<float>(E));
 #pragma unroll
     for (int i = 0; i < V * N; ++i)
         c[i] -= mid;
-    const int n = *tokens;
     const float nf = static_cast<float>(n > 0 ? n : 1);
-    const float scale = *grad_loss * (coef * static_cast<float>(E) / (nf * nf * k));
+    const float scale = up * (coef * static_cast<float>(E) / (nf * nf * k));
     // every lane takes part in the shuffles of every round
     for (; t - part < T_; t += step) {
-        const bool in = t < T_, on = in && (!live || live[t]);
+        const bool in = t < T_, now = on;
         R p;
-        p.load(logits + t * ls, on ? E : 0, sub);
+        p.expand(raw, now ? E : 0, sub);
+        fetch(t + step);
         p.softmax();
         float mixed = 0.f;
 #pragma unroll
@@ -373,7 +444,7 @@ balance_backward(T *__restrict__ grad, const float *__restrict__ grad_loss,
         mixed = R::total(mixed);
 #pragma unroll
         for (int i = 0; i < V * N; ++i)
-            p.x[i] = on ? scale * p.x[i] * (c[i] - mixed) : 0.f;
+            p.x[i] = now ? scale * p.x[i] * (c[i] - mixed) : 0.f;
         if (in)
             p.store(grad + t * E, E, sub);
     }
@@ -419,10 +490,11 @@ template <class F> int with_lanes(int64_t E, bool vec, F f) {
 // Batches of up to this many tokens take the one-launch cluster.
 constexpr int64_t kClusterTokens = 512;
 
-// CTAs that a longer batch's tokens are split over: two per SM, at least 32
-// tokens each.
+// CTAs that a longer batch's tokens are split over: one per SM, of at least 32
+// tokens each.  The join reads up to 32 kJoinLoads of them.
 int64_t parts(int64_t T) {
-    return std::max<int64_t>(1, std::min<int64_t>(ceil_div64(T, 32), device_sm_count() * 2));
+    return std::max<int64_t>(1, std::min<int64_t>({ceil_div64(T, 32), device_sm_count(),
+                                                   int64_t(32) * kJoinLoads}));
 }
 
 }  // namespace
@@ -468,23 +540,25 @@ extern "C" int moe_balance_loss(float *loss, int32_t *counts, int32_t *tokens, f
     rc = with_type(dtype, [&](auto t) {
         return with_lanes(E, vec, [&](auto l, auto v, auto n) {
             using Elem = decltype(t);
-            const size_t smem = (kWarps * E + E + 1) * 4;
+            const size_t smem = (kSumRows * E + E + 1) * 4;
             if (cluster)
                 return launched(launch_kernel(
                     balance_cluster<Elem, l(), v(), n()>, dim3(kCluster), dim3(kThreads), smem,
                     stream, kCluster, as<float>(r[0]), as<int32_t>(r[1]), as<int32_t>(r[2]),
                     as<float>(r[3]), as<const Elem>(r[5]), chosen, as<const uint8_t>(r[7]), T,
                     per, Ei, ki, logits_stride, c));
+            // 32 warps per SM, 16 where a lane holds more than 8 logits
+            constexpr int NT = v() * n() > 8 ? 512 : 1024;
             return launched(launch_kernel(
-                balance_tokens<Elem, l(), v(), n()>, dim3(static_cast<unsigned>(G)),
-                dim3(kThreads), smem, stream, 1, part_p, part_c, as<const Elem>(r[5]), chosen,
+                balance_tokens<Elem, NT, l(), v(), n()>, dim3(static_cast<unsigned>(G)),
+                dim3(NT), smem, stream, 1, part_p, part_c, as<const Elem>(r[5]), chosen,
                 as<const uint8_t>(r[7]), T, per, Ei, ki, logits_stride));
         });
     });
     if (rc != GATED_ACT_OK || cluster)
         return rc;
     return launched(launch_kernel(
-        balance_join, dim3(kCluster), dim3(kThreads), 0, stream, kCluster, as<float>(r[0]),
+        balance_join, dim3(kCluster), dim3(kJoinThreads), 0, stream, kCluster, as<float>(r[0]),
         as<int32_t>(r[1]), as<int32_t>(r[2]), as<float>(r[3]), static_cast<const float *>(part_p),
         static_cast<const int32_t *>(part_c), static_cast<int>(G), Ei, static_cast<float>(k), c));
 }
@@ -512,8 +586,9 @@ extern "C" int moe_balance_loss_backward(void *grad_logits, const float *grad_lo
     return with_type(dtype, [&](auto t) {
         return with_lanes(E, vec, [&](auto l, auto v, auto n) {
             using Elem = decltype(t);
-            const int64_t grid = std::min<int64_t>(ceil_div64(T, kWarps * (32 / l())),
-                                                   int64_t(device_sm_count()) * 8);
+            // up to 8 CTAs per SM, all with the same number of rounds
+            const int64_t rounds = ceil_div64(T, kThreads / l());
+            const int64_t grid = ceil_div64(rounds, ceil_div64(rounds, device_sm_count() * 8));
             return launched(launch_kernel(
                 balance_backward<Elem, l(), v(), n()>, dim3(static_cast<unsigned>(grid)),
                 dim3(kThreads), 0, stream, 1, as<Elem>(r[0]), as<const float>(r[1]),

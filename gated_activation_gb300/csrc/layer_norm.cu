@@ -114,38 +114,45 @@ ln_backward_columns_any(float *__restrict__ part, const T *__restrict__ grad,
     part[(gridDim.y + blockIdx.y) * d + c] = b;
 }
 
-// Adds the n shares of every column: thread x a column, the kReduceY threads y
-// of a column every kReduceY-th share.
-constexpr int kReduceX = 32, kReduceY = 32;
-__global__ void __launch_bounds__(kReduceX *kReduceY)
+// Adds the n shares of every column, of the weight (blockIdx.y = 0) or the bias:
+// a warp reads 128 columns of every kReduceWarps-th share, four per lane.
+constexpr int kReduceWarps = 16, kReduceColumns = 128;
+__global__ void __launch_bounds__(32 * kReduceWarps)
 ln_backward_reduce(float *__restrict__ grad_weight, float *__restrict__ grad_bias,
                    const float *__restrict__ part, int64_t n, int64_t d) {
-    __shared__ float sum[2][kReduceY][kReduceX + 1];
+    __shared__ float4 sum[kReduceWarps][32];
     pdl_wait();
     pdl_trigger();
-    const int x = threadIdx.x % kReduceX, y = threadIdx.x / kReduceX;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * kReduceX + x;
-    float w = 0.f, b = 0.f;
-    if (c < d) {
-#pragma unroll 4
-        for (int64_t i = y; i < n; i += kReduceY)
-            w += part[i * d + c];
-        if (grad_bias)
-#pragma unroll 4
-            for (int64_t i = y; i < n; i += kReduceY)
-                b += part[(n + i) * d + c];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * kReduceColumns + 4 * lane;
+    const float *p = part + blockIdx.y * n * d;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (d % 4 == 0) {
+        if (c < d)
+#pragma unroll 10
+            for (int64_t i = warp; i < n; i += kReduceWarps) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + i * d + c));
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+                s.w += v.w;
+            }
+    } else {
+        for (int64_t i = warp; i < n; i += kReduceWarps)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < d)
+                    (&s.x)[j] += __ldcg(p + i * d + c + j);
     }
-    sum[0][y][x] = w;
-    sum[1][y][x] = b;
+    sum[warp][lane] = s;
     __syncthreads();
-    // warp y joins column y's shares
-    w = warp_sum(sum[0][x][y]);
-    b = warp_sum(sum[1][x][y]);
-    const int64_t to = static_cast<int64_t>(blockIdx.x) * kReduceX + y;
-    if (x == 0 && to < d) {
-        grad_weight[to] = w;
-        if (grad_bias)
-            grad_bias[to] = b;
+    const int64_t to = static_cast<int64_t>(blockIdx.x) * kReduceColumns + threadIdx.x;
+    if (threadIdx.x < kReduceColumns && to < d) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kReduceWarps; ++w)
+            t += reinterpret_cast<const float *>(sum[w])[threadIdx.x];
+        (blockIdx.y ? grad_bias : grad_weight)[to] = t;
     }
 }
 
@@ -255,7 +262,7 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
         b[i] = c < d && bias ? load_params(bias + c) : Vec8<W>::zero();
     }
     int slot = 0;
-    const float n = static_cast<float>(d);
+    const float inv = 1.0f / static_cast<float>(d);
     for (int64_t r = blockIdx.x; r < rows; r += G) {
         // the slot read in the round before: this thread is done with it
         fetch(r + (S - 1) * G, slot == 0 ? S - 1 : slot - 1);
@@ -268,7 +275,10 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
             for (int j = 0; j < 4; ++j)
                 acc = add2(acc, x.pair(j));
         }
-        const float mean = row_sum<NT>(acc.x + acc.y, red[0]) / n;
+        const float sum = row_sum<NT>(acc.x + acc.y, red[0]);
+        // the quotient by a product and its residual: exact for constant rows
+        float mean = sum * inv;
+        mean = fmaf(fmaf(-mean, static_cast<float>(d), sum), inv, mean);
         const float2 m2 = make_float2(mean, mean);
         acc = make_float2(0.f, 0.f);
 #pragma unroll
@@ -281,8 +291,8 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
                     acc = fma2(e, e, acc);
                 }
             }
-        const float var = row_sum<NT>(acc.x + acc.y, red[1]) / n;
-        const float rstd = 1.0f / __fsqrt_rn(var + eps);
+        const float var = row_sum<NT>(acc.x + acc.y, red[1]) * inv;
+        const float rstd = rsqrtf(var + eps);
         const float2 r2 = make_float2(rstd, rstd);
         if (t == 0) {
             mean_out[r] = mean;
@@ -378,8 +388,8 @@ ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restr
 // barrier of their own.  A thread holds its columns' shares of the
 // parameters' gradients, and the weight, in registers; at the end the CTA
 // joins its rows' shares in shared memory and writes one share per column.
-// With h = (x - mean) rstd = x rstd + c and g = dy w, the gradient is
-//   rstd (g - A - h B) = dy (w rstd) + x (-B rstd^2) + (-A - c B) rstd.
+// With h = (x - mean) rstd and g = dy w, the gradient is
+//   rstd (g - A - h B) = dy (w rstd) + (x - mean) (-B rstd^2) - A rstd.
 
 constexpr int kBackThreads = 512;
 
@@ -420,12 +430,12 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
     }
     int slot = 0, k = 0;
     float mean = first < rows ? mean_in[first] : 0.f, rstd = first < rows ? rstd_in[first] : 0.f;
-    const float n = static_cast<float>(d);
+    const float inv = 1.0f / static_cast<float>(d);
     for (int64_t r = first; r < rows; r += G, k ^= 1) {
         // the slot read in the round before: this thread is done with it
         fetch(r + (S - 1) * G, slot == 0 ? S - 1 : slot - 1);
-        const float r1 = rstd, c1 = -mean * rstd;
-        const float2 r2 = make_float2(r1, r1), c2 = make_float2(c1, c1);
+        const float r1 = rstd;
+        const float2 r2 = make_float2(r1, r1), m2 = make_float2(mean, mean);
         if (r + G < rows) {
             mean = mean_in[r + G];
             rstd = rstd_in[r + G];
@@ -437,7 +447,7 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
             const Vec8<T> x = ring.held(slot, 0, i), y = ring.held(slot, 1, i);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 dy = y.pair(j), h = fma2(x.pair(j), r2, c2);
+                const float2 dy = y.pair(j), h = mul2(sub2(x.pair(j), m2), r2);
                 db[i][j] = add2(db[i][j], dy);
                 dw[i][j] = fma2(dy, h, dw[i][j]);
                 const float2 g = mul2(dy, w[i].pair(j));
@@ -459,9 +469,9 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
                 b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
             }
         }
-        a /= n;
-        b /= n;
-        const float xs = -b * r1 * r1, off = fmaf(-c1, b, -a) * r1;
+        a *= inv;
+        b *= inv;
+        const float xs = -b * r1 * r1, off = -a * r1;
         const float2 xs2 = make_float2(xs, xs), off2 = make_float2(off, off);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -472,7 +482,8 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
             Vec8<T> o;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                o.put(j, fma2(y.pair(j), mul2(w[i].pair(j), r2), fma2(x.pair(j), xs2, off2)));
+                o.put(j, fma2(y.pair(j), mul2(w[i].pair(j), r2),
+                              fma2(sub2(x.pair(j), m2), xs2, off2)));
             o.store(grad_in + r * d + c);
         }
         slot = slot == S - 1 ? 0 : slot + 1;
@@ -733,7 +744,8 @@ extern "C" int layer_norm_backward(void *grad_in, float *grad_weight, float *gra
             return rc;
     }
     return launched(launch_kernel(ln_backward_reduce,
-                                  dim3(static_cast<unsigned>(ceil_div64(d, kReduceX))),
-                                  dim3(kReduceX * kReduceY), 0, stream, 1, as<float>(r[1]),
+                                  dim3(static_cast<unsigned>(ceil_div64(d, kReduceColumns)),
+                                       grad_bias ? 2 : 1),
+                                  dim3(32 * kReduceWarps), 0, stream, 1, as<float>(r[1]),
                                   as<float>(r[2]), static_cast<const float *>(part), n, d));
 }
