@@ -32,71 +32,30 @@ constexpr int kCluster = 8;
 // ------------------------------------------------------------------- tokens
 
 // The logits of one token held by one lane, V groups of N: group i starts at
-// element (i * L + lane) * N.  Raw: as loaded, so that the next token's can be
-// on their way while this one is computed.
+// element (i * L + lane) * N.  As loaded, so that the next token's can be on
+// their way while this one is computed; 0 past the row's end.
 template <class T, int L, int V, int N> struct Raw {
     std::conditional_t<N == 8, Vec8<T>, T> v[V];
     __device__ void load(const T *row, int E, int lane) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = (i * L + lane) * N;
-            if (c < E) {
-                if constexpr (N == 8)
-                    v[i] = Vec8<T>::load(row + c);
-                else
-                    v[i] = __ldg(row + c);
-            }
+            if constexpr (N == 8)
+                v[i] = c < E ? Vec8<T>::load(row + c) : Vec8<T>::zero();
+            else
+                v[i] = c < E ? __ldg(row + c) : from_float<T>(0.f);
         }
     }
 };
 
+// A token's softmax, e * inv: e = exp(logit - largest).  A token whose logits
+// are all -infinity, and one with E = 0, has e = 0 and inv = 0.
 template <class T, int L, int V, int N> struct Row {
-    float x[V * N];
+    static constexpr int M = V * N, P = (M + 1) / 2;
+    float2 e[P];      // M = 1: the second half is 0
+    float inv;
 
     __device__ static int column(int lane, int i) { return (i / N * L + lane) * N + i % N; }
-
-    // E = 0: a row of -infinity.
-    __device__ void expand(const Raw<T, L, V, N> &raw, int E, int lane) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const bool in = (i * L + lane) * N < E;
-            if constexpr (N == 8) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = raw.v[i].pair(j);
-                    x[8 * i + 2 * j] = in ? f.x : -INFINITY;
-                    x[8 * i + 2 * j + 1] = in ? f.y : -INFINITY;
-                }
-            } else {
-                x[i] = in ? to_float(raw.v[i]) : -INFINITY;
-            }
-        }
-    }
-
-    // In place; a token whose logits are all -infinity gets 0 everywhere.
-    __device__ void softmax() {
-        float top = x[0];
-#pragma unroll
-        for (int i = 1; i < V * N; ++i)
-            top = fmaxf(top, x[i]);
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        // fmaxf skips a NaN; the exponential of a NaN logit brings it back
-        const float shift = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < V * N; ++i) {
-            x[i] = __expf(x[i] - shift);
-            sum += x[i];
-        }
-        sum = total(sum);
-        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-#pragma unroll
-        for (int i = 0; i < V * N; ++i)
-            x[i] *= inv;
-    }
-
     __device__ static float total(float v) {
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1)
@@ -104,22 +63,50 @@ template <class T, int L, int V, int N> struct Row {
         return v;
     }
 
-    __device__ void store(T *row, int E, int lane) const {
+    __device__ Row(const Raw<T, L, V, N> &raw, int E, int lane) {
+        float top = -INFINITY;
+        if constexpr (N == 8) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (i * L + lane) * N;
-            if (c >= E)
-                continue;
-            if constexpr (N == 8) {
-                Vec8<T> v;
+            for (int i = 0; i < V; ++i) {
+                float m = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v.put(j, make_float2(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]));
-                v.store(row + c);
-            } else {
-                row[c] = from_float<T>(x[i]);
+                for (int j = 0; j < 4; ++j) {
+                    e[4 * i + j] = raw.v[i].pair(j);
+                    m = fmaxf(m, fmaxf(e[4 * i + j].x, e[4 * i + j].y));
+                }
+                top = fmaxf(top, (i * L + lane) * N < E ? m : -INFINITY);
+            }
+        } else {
+            e[P - 1].y = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float x = to_float(raw.v[i]);
+                (i & 1 ? e[i / 2].y : e[i / 2].x) = x;
+                top = fmaxf(top, i * L + lane < E ? x : -INFINITY);
             }
         }
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        // e = (2^y)^2, y = (logit - top) log2(e) / 2: the square carries e down to
+        // the subnormal numbers that the flushing exponential would drop.  fmaxf
+        // skips a NaN; the exponential of a NaN logit brings it back.
+        constexpr float half = 0.5f * 1.4426950408889634f;
+        const float shift = top == -INFINITY ? 0.f : -top * half;
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            // past the row's end 2^-infinity
+            const float sx = column(lane, 2 * i) < E ? shift : -INFINITY;
+            const float sy = N == 8 ? sx : column(lane, 2 * i + 1) < E && 2 * i + 1 < M ? shift : -INFINITY;
+            float2 y = fma2(e[i], both(half), make_float2(sx, sy));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(y.x));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(y.y));
+            e[i] = mul2(y, y);
+            sum = add2(sum, e[i]);
+        }
+        const float s = total(sum.x + sum.y);
+        inv = s == 0.f ? 0.f : 1.0f / s;
     }
 };
 
@@ -164,24 +151,20 @@ __device__ __forceinline__ void sum_tokens(float *sums, int *hist, const T *logi
         if (e >= 0 && e < E && (!live || live[t0 + static_cast<uint32_t>(j) / static_cast<uint32_t>(k)]))
             atomicAdd(hist + e, 1);
     }
-    float acc[V * N];
+    float2 acc2[R::P];
 #pragma unroll
-    for (int i = 0; i < V * N; ++i)
-        acc[i] = 0.f;
+    for (int i = 0; i < R::P; ++i)
+        acc2[i] = make_float2(0.f, 0.f);
     int mine = 0;
-    // every lane takes part in the shuffles of every round
+    // every lane takes part in the shuffles of every round; a token that is not
+    // live adds zeros
     const auto take = [&](int slot) {
-        R p;
-        p.expand(raw[slot], on[slot] ? E : 0, sub);
-        const bool ok = on[slot];
+        const R p(raw[slot], on[slot] ? E : 0, sub);
+        mine += on[slot] && sub == 0;
         fetch(t + 2 * step, slot);
-        p.softmax();
-        if (ok) {
-            mine += sub == 0;
 #pragma unroll
-            for (int i = 0; i < V * N; ++i)
-                acc[i] += p.x[i];
-        }
+        for (int i = 0; i < R::P; ++i)
+            acc2[i] = fma2(p.e[i], both(p.inv), acc2[i]);
         t += step;
     };
     while (t < t1) {
@@ -192,6 +175,10 @@ __device__ __forceinline__ void sum_tokens(float *sums, int *hist, const T *logi
     mine = __reduce_add_sync(0xFFFFFFFFu, mine);
     if (lane == 0 && mine)
         atomicAdd(hist + E, mine);
+    float acc[V * N];
+#pragma unroll
+    for (int i = 0; i < V * N; ++i)
+        acc[i] = i & 1 ? acc2[i / 2].y : acc2[i / 2].x;
 #pragma unroll
     for (int i = 0; i < V * N; ++i)
 #pragma unroll
@@ -415,38 +402,51 @@ balance_backward(T *__restrict__ grad, const float *__restrict__ grad_loss,
         raw.load(logits + at * ls, on ? E : 0, sub);
     };
     fetch(t);
-    float c[V * N], sum = 0.f;
+    float2 c[R::P];
+    float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < V * N; ++i) {
-        const int e = R::column(sub, i);
-        c[i] = e < E ? static_cast<float>(__ldg(counts + e)) : 0.f;
-        sum += c[i];
+    for (int i = 0; i < R::P; ++i) {
+        const int e0 = R::column(sub, 2 * i), e1 = R::column(sub, 2 * i + 1);
+        c[i].x = e0 < E ? static_cast<float>(__ldg(counts + e0)) : 0.f;
+        c[i].y = 2 * i + 1 < R::M && e1 < E ? static_cast<float>(__ldg(counts + e1)) : 0.f;
+        sum += c[i].x + c[i].y;
     }
     const int n = *tokens;
     const float up = *grad_loss;
     const float mid = rintf(R::total(sum) / static_cast<float>(E));
 #pragma unroll
-    for (int i = 0; i < V * N; ++i)
-        c[i] -= mid;
+    for (int i = 0; i < R::P; ++i)
+        c[i] = sub2(c[i], both(mid));
     const float nf = static_cast<float>(n > 0 ? n : 1);
     const float scale = up * (coef * static_cast<float>(E) / (nf * nf * k));
     // every lane takes part in the shuffles of every round
     for (; t - part < T_; t += step) {
-        const bool in = t < T_, now = on;
-        R p;
-        p.expand(raw, now ? E : 0, sub);
+        const R p(raw, on ? E : 0, sub);
         fetch(t + step);
-        p.softmax();
-        float mixed = 0.f;
+        float2 mix = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < V * N; ++i)
-            mixed = fmaf(p.x[i], c[i], mixed);
-        mixed = R::total(mixed);
+        for (int i = 0; i < R::P; ++i)
+            mix = fma2(p.e[i], c[i], mix);
+        const float mixed = R::total(mix.x + mix.y) * p.inv, s = scale * p.inv;
+        if (t >= T_)
+            continue;
+        T *row = grad + t * E;
 #pragma unroll
-        for (int i = 0; i < V * N; ++i)
-            p.x[i] = now ? scale * p.x[i] * (c[i] - mixed) : 0.f;
-        if (in)
-            p.store(grad + t * E, E, sub);
+        for (int i = 0; i < V; ++i) {
+            const int at = (i * L + sub) * N;
+            if (at >= E)
+                continue;
+            if constexpr (N == 8) {
+                Vec8<T> o;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    o.put(j, mul2(mul2(p.e[4 * i + j], both(s)), sub2(c[4 * i + j], both(mixed))));
+                o.store(row + at);
+            } else {
+                const float e = i & 1 ? p.e[i / 2].y : p.e[i / 2].x;
+                row[at] = from_float<T>(e * s * ((i & 1 ? c[i / 2].y : c[i / 2].x) - mixed));
+            }
+        }
     }
 }
 
@@ -467,16 +467,16 @@ int check_sizes(int64_t T, int64_t E, int64_t k, int64_t ls, int dtype) {
 
 template <int N> using Const = std::integral_constant<int, N>;
 
-// Calls f(integral constants L, V, N) for E experts: vectors of 8 with the
-// fewest lanes that hold a row, or single elements.
+// Calls f(integral constants L, V, N) for E experts: two vectors of 8 per lane
+// (fewer shuffles per element than one), or single elements.
 template <class F> int with_lanes(int64_t E, bool vec, F f) {
     if (vec)
         return E <= 8     ? f(Const<1>{}, Const<1>{}, Const<8>{})
-               : E <= 16  ? f(Const<2>{}, Const<1>{}, Const<8>{})
-               : E <= 32  ? f(Const<4>{}, Const<1>{}, Const<8>{})
-               : E <= 64  ? f(Const<8>{}, Const<1>{}, Const<8>{})
-               : E <= 128 ? f(Const<16>{}, Const<1>{}, Const<8>{})
-               : E <= 256 ? f(Const<32>{}, Const<1>{}, Const<8>{})
+               : E <= 16  ? f(Const<1>{}, Const<2>{}, Const<8>{})
+               : E <= 32  ? f(Const<2>{}, Const<2>{}, Const<8>{})
+               : E <= 64  ? f(Const<4>{}, Const<2>{}, Const<8>{})
+               : E <= 128 ? f(Const<8>{}, Const<2>{}, Const<8>{})
+               : E <= 256 ? f(Const<16>{}, Const<2>{}, Const<8>{})
                : E <= 512 ? f(Const<32>{}, Const<2>{}, Const<8>{})
                           : f(Const<32>{}, Const<4>{}, Const<8>{});
     return E <= 32    ? f(Const<32>{}, Const<1>{}, Const<1>{})
@@ -547,8 +547,8 @@ extern "C" int moe_balance_loss(float *loss, int32_t *counts, int32_t *tokens, f
                     stream, kCluster, as<float>(r[0]), as<int32_t>(r[1]), as<int32_t>(r[2]),
                     as<float>(r[3]), as<const Elem>(r[5]), chosen, as<const uint8_t>(r[7]), T,
                     per, Ei, ki, logits_stride, c));
-            // 32 warps per SM, 16 where a lane holds more than 8 logits
-            constexpr int NT = v() * n() > 8 ? 512 : 1024;
+            // 32 warps per SM, 16 where the registers of a lane's logits forbid it
+            constexpr int NT = v() * n() > 16 || sizeof(Elem) * v() * n() > 32 ? 512 : 1024;
             return launched(launch_kernel(
                 balance_tokens<Elem, NT, l(), v(), n()>, dim3(static_cast<unsigned>(G)),
                 dim3(NT), smem, stream, 1, part_p, part_c, as<const Elem>(r[5]), chosen,
