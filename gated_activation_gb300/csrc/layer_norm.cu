@@ -13,27 +13,35 @@ namespace gact {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 
+// -------------------------------------------------- rows that no CTA holds
+
+// Sum over the CTA, the same bits in every thread; red holds 32 values.
 __device__ __forceinline__ float cta_sum(float v, float *red) {
     v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0)
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0)
         red[threadIdx.x >> 5] = v;
     __syncthreads();
-    float t = red[threadIdx.x & (kWarps - 1)];
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1)
-        t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    return t;
+    return warp_sum(lane < warps ? red[lane] : 0.f);
+}
+__device__ __forceinline__ float2 cta_sum2(float2 v, float2 *red) {
+    v = make_float2(warp_sum(v.x), warp_sum(v.y));
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0)
+        red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < warps ? red[lane] : make_float2(0.f, 0.f);
+    return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
-// Any layout: one CTA per row, the row read again (from L1/L2) for each pass.
+// One CTA per row, the row read again (from L1/L2) for each pass.
 template <class T, class W>
 __global__ void __launch_bounds__(kThreads)
-ln_forward_any(T *__restrict__ out, float *__restrict__ mean_out, float *__restrict__ rstd_out,
-               const T *__restrict__ in, const W *__restrict__ weight, const W *__restrict__ bias,
-               int64_t rows, int64_t d, int64_t rs, float eps) {
-    __shared__ float red[2][kWarps];
+ln_forward_wide(T *__restrict__ out, float *__restrict__ mean_out, float *__restrict__ rstd_out,
+                const T *__restrict__ in, const W *__restrict__ weight, const W *__restrict__ bias,
+                int64_t rows, int64_t d, int64_t rs, float eps) {
+    __shared__ float red[2][32];
     pdl_wait();
     pdl_trigger();
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
@@ -63,25 +71,25 @@ ln_forward_any(T *__restrict__ out, float *__restrict__ mean_out, float *__restr
 
 template <class T, class W>
 __global__ void __launch_bounds__(kThreads)
-ln_backward_rows_any(T *__restrict__ grad_in, const T *__restrict__ grad, const T *__restrict__ in,
-                     const W *__restrict__ weight, const float *__restrict__ mean_in,
-                     const float *__restrict__ rstd_in, int64_t rows, int64_t d, int64_t rs,
-                     int64_t gs) {
-    __shared__ float red[2][2][kWarps];
+ln_backward_rows(T *__restrict__ grad_in, const T *__restrict__ grad, const T *__restrict__ in,
+                 const W *__restrict__ weight, const float *__restrict__ mean_in,
+                 const float *__restrict__ rstd_in, int64_t rows, int64_t d, int64_t rs,
+                 int64_t gs) {
+    __shared__ float2 red[2][32];
     pdl_wait();
     pdl_trigger();
     int k = 0;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, k ^= 1) {
         const T *x = in + r * rs, *dy = grad + r * gs;
         const float mean = mean_in[r], rstd = rstd_in[r];
-        float a = 0.f, b = 0.f;
+        float2 s = make_float2(0.f, 0.f);
         for (int64_t c = threadIdx.x; c < d; c += kThreads) {
             const float g = to_float(dy[c]) * to_float(weight[c]);
-            a += g;
-            b = fmaf(g, (to_float(x[c]) - mean) * rstd, b);
+            s.x += g;
+            s.y = fmaf(g, (to_float(x[c]) - mean) * rstd, s.y);
         }
-        const float ma = cta_sum(a, red[k][0]) / static_cast<float>(d);
-        const float mb = cta_sum(b, red[k][1]) / static_cast<float>(d);
+        s = cta_sum2(s, red[k]);
+        const float ma = s.x / static_cast<float>(d), mb = s.y / static_cast<float>(d);
         for (int64_t c = threadIdx.x; c < d; c += kThreads) {
             const float g = to_float(dy[c]) * to_float(weight[c]);
             const float h = (to_float(x[c]) - mean) * rstd;
@@ -94,7 +102,7 @@ ln_backward_rows_any(T *__restrict__ grad_in, const T *__restrict__ grad, const 
 // column per thread.  part: [2][gridDim.y][d].
 template <class T>
 __global__ void __launch_bounds__(kThreads)
-ln_backward_columns_any(float *__restrict__ part, const T *__restrict__ grad,
+ln_backward_columns(float *__restrict__ part, const T *__restrict__ grad,
                         const T *__restrict__ in, const float *__restrict__ mean_in,
                         const float *__restrict__ rstd_in, int64_t rows, int64_t per, int64_t d,
                         int64_t rs, int64_t gs) {
@@ -156,6 +164,16 @@ ln_backward_reduce(float *__restrict__ grad_weight, float *__restrict__ grad_bia
     }
 }
 
+// 8 parameters.
+template <class W> __device__ __forceinline__ Vec8<W> load_params(const W *p) {
+    Vec8<W> v;
+    uint4 *q = reinterpret_cast<uint4 *>(&v);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(v) / 16); ++i)
+        q[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    return v;
+}
+
 // ------------------------------------------------------- vectors, a ring
 //
 // Persistent CTAs, each row held by TPR threads, thread t with the 8-element
@@ -164,12 +182,41 @@ ln_backward_reduce(float *__restrict__ grad_weight, float *__restrict__ grad_bia
 // fills S - 1 rows ahead, so that HBM keeps streaming while a row is summed
 // and written.  A thread copies just the vectors it will read itself: its own
 // wait_group is all the synchronization that the ring needs.
+//
+// EDGES: rows that start or end off a 16-byte boundary.  The ring holds the
+// vectors of the row that lie on it; the up to 7 elements before and after them
+// are `edges`, one per thread of the row's first warp, read a row ahead into a
+// register.  Rows of one kind of offset go to one CTA (its rows are a multiple
+// of kKinds apart), so that its threads keep their columns.
+
+constexpr int kKinds = 8;      // rows this far apart have the same offset
+
+// Where the vectors of a row of d elements begin, and how many elements they hold.
+struct Span8 {
+    int head, width;
+};
+template <class T, bool EDGES> __device__ __forceinline__ Span8 span_of(const T *row, int d) {
+    if constexpr (!EDGES)
+        return {0, d};
+    const int head = min(d, static_cast<int>((-reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T)));
+    return {head, (d - head) / 8 * 8};
+}
+// The column of thread t's edge, or -1.
+template <bool EDGES> __device__ __forceinline__ int edge_of(const Span8 &s, int d, int t) {
+    if constexpr (!EDGES)
+        return -1;
+    if (t < 8)
+        return t < s.head ? t : -1;
+    const int c = s.head + s.width + t - 8;
+    return t < 16 && c < d ? c : -1;
+}
 
 // This thread's part of the ring: `which` counts the rows of a slot (the
-// input, and in the backward pass the gradient).
+// input, and in the backward pass the gradient).  Columns from the span's head.
 template <class T, int NT, int TPR, int V, int ROWS> struct Ring {
-    static constexpr int P = sizeof(T) / 2;    // 16-byte pieces of a vector
-    uint4 *mine;                               // [S][ROWS][V][P][NT]
+    static constexpr int P = sizeof(T) / 2;           // 16-byte pieces of a vector
+    static constexpr int kPiece = 16 / sizeof(T);     // their elements
+    uint4 *mine;                                      // [S][ROWS][V][P][NT]
     uint32_t at;
     int t, d;
     __device__ Ring(uint4 *ring, int t_, int d_)
@@ -178,19 +225,20 @@ template <class T, int NT, int TPR, int V, int ROWS> struct Ring {
     __device__ static int index(int slot, int which, int i, int p) {
         return (((slot * ROWS + which) * V + i) * P + p) * NT;
     }
+    __device__ int column(int i) const { return 8 * (t + TPR * i); }
+    __device__ bool in(int i) const { return column(i) < d; }
     __device__ void fetch(int slot, int which, const T *row) const {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (8 * (t + TPR * i) < d)
+            if (in(i))
 #pragma unroll
                 for (int p = 0; p < P; ++p)
-                    copy16(at + 16u * index(slot, which, i, p),
-                           row + 8 * (t + TPR * i) + 16 / sizeof(T) * p);
+                    copy16(at + 16u * index(slot, which, i, p), row + column(i) + kPiece * p);
     }
-    // Zero past the row's end.
+    // Zero past the span's end.
     __device__ Vec8<T> held(int slot, int which, int i) const {
         Vec8<T> v = Vec8<T>::zero();
-        if (8 * (t + TPR * i) < d) {
+        if (in(i)) {
             uint4 *q = reinterpret_cast<uint4 *>(&v);
 #pragma unroll
             for (int p = 0; p < P; ++p)
@@ -200,22 +248,28 @@ template <class T, int NT, int TPR, int V, int ROWS> struct Ring {
     }
 };
 
+// The parameters of 8 columns at p; one by one where they are not aligned.
+template <bool EDGES, class W> __device__ __forceinline__ Vec8<W> params8(const W *p, bool in) {
+    Vec8<W> v = Vec8<W>::zero();
+    if (in) {
+        if constexpr (EDGES) {
+            W *e = reinterpret_cast<W *>(&v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                e[j] = __ldg(p + j);
+        } else {
+            v = load_params(p);
+        }
+    }
+    return v;
+}
+
 // Barrier of the TPR threads of one row: the CTA's, or one of its named ones.
 template <int NT, int TPR> __device__ __forceinline__ void row_barrier() {
     if constexpr (TPR == NT)
         __syncthreads();
     else if constexpr (TPR > 32)
         asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / TPR), "n"(TPR) : "memory");
-}
-
-// 8 parameters.
-template <class W> __device__ __forceinline__ Vec8<W> load_params(const W *p) {
-    Vec8<W> v;
-    uint4 *q = reinterpret_cast<uint4 *>(&v);
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(v) / 16); ++i)
-        q[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-    return v;
 }
 
 // Sum over the NT threads of a CTA that holds one row; red holds NT / 32 floats.
@@ -234,7 +288,7 @@ template <int NT> __device__ __forceinline__ float row_sum(float v, float *red) 
     return v;
 }
 
-template <class T, class W, int NT, int V, int S>
+template <class T, class W, int NT, int V, int S, bool EDGES>
 __global__ void __launch_bounds__(NT, 1024 / NT)
 ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__restrict__ rstd_out,
                 const T *__restrict__ in, const W *__restrict__ weight, const W *__restrict__ bias,
@@ -245,10 +299,12 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
     pdl_wait();
     pdl_trigger();
     const int64_t G = gridDim.x;
-    const Ring<T, NT, NT, V, 1> ring(slots, t, d);
+    const Span8 span = span_of<T, EDGES>(in + blockIdx.x * rs, d);
+    const int edge = edge_of<EDGES>(span, d, t);
+    const Ring<T, NT, NT, V, 1> ring(slots, t, span.width);
     const auto fetch = [&](int64_t r, int slot) {
         if (r < rows)
-            ring.fetch(slot, 0, in + r * rs);
+            ring.fetch(slot, 0, in + r * rs + span.head);
         copy_commit();
     };
 #pragma unroll
@@ -257,17 +313,25 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
     Vec8<W> w[V], b[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = 8 * (t + NT * i);
-        w[i] = c < d ? load_params(weight + c) : Vec8<W>::zero();
-        b[i] = c < d && bias ? load_params(bias + c) : Vec8<W>::zero();
+        w[i] = params8<EDGES>(weight + span.head + ring.column(i), ring.in(i));
+        b[i] = params8<EDGES>(bias + span.head + ring.column(i), ring.in(i) && bias);
+    }
+    float we = 0.f, be = 0.f, next = 0.f;
+    if (EDGES && edge >= 0) {
+        we = to_float(__ldg(weight + edge));
+        be = bias ? to_float(__ldg(bias + edge)) : 0.f;
+        next = to_float(__ldg(in + blockIdx.x * rs + edge));
     }
     int slot = 0;
     const float inv = 1.0f / static_cast<float>(d);
     for (int64_t r = blockIdx.x; r < rows; r += G) {
         // the slot read in the round before: this thread is done with it
         fetch(r + (S - 1) * G, slot == 0 ? S - 1 : slot - 1);
+        const float xe = next;
+        if (EDGES && edge >= 0 && r + G < rows)
+            next = to_float(__ldg(in + (r + G) * rs + edge));
         copy_wait<S - 1>();
-        float2 acc = make_float2(0.f, 0.f);
+        float2 acc = make_float2(xe, 0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const Vec8<T> x = ring.held(slot, 0, i);
@@ -281,9 +345,11 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
         mean = fmaf(fmaf(-mean, static_cast<float>(d), sum), inv, mean);
         const float2 m2 = make_float2(mean, mean);
         acc = make_float2(0.f, 0.f);
+        if (EDGES && edge >= 0)
+            acc.x = (xe - mean) * (xe - mean);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (8 * (t + NT * i) < d) {
+            if (ring.in(i)) {
                 const Vec8<T> x = ring.held(slot, 0, i);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -300,16 +366,17 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (t + NT * i);
-            if (c >= d)
+            if (!ring.in(i))
                 continue;
             const Vec8<T> x = ring.held(slot, 0, i);
             Vec8<T> o;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 o.put(j, fma2(mul2(sub2(x.pair(j), m2), r2), w[i].pair(j), b[i].pair(j)));
-            o.store(out + r * d + c);
+            o.store(out + r * d + span.head + ring.column(i));
         }
+        if (EDGES && edge >= 0)
+            out[r * d + edge] = from_float<T>(fmaf((xe - mean) * rstd, we, be));
         slot = slot == S - 1 ? 0 : slot + 1;
     }
 }
@@ -390,28 +457,54 @@ ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restr
 // joins its rows' shares in shared memory and writes one share per column.
 // With h = (x - mean) rstd and g = dy w, the gradient is
 //   rstd (g - A - h B) = dy (w rstd) + (x - mean) (-B rstd^2) - A rstd.
+// Rows that one CTA's registers and ring cannot hold are split over a cluster
+// of CL CTAs, `chunk` columns each; the row's two sums are then joined through
+// distributed shared memory.
 
 constexpr int kBackThreads = 512;
 
-template <class T, class W, int TPR, int V, int S>
+// A float2 into the same shared-memory variable of another CTA of the cluster.
+__device__ __forceinline__ void put_peer(float2 *p, uint32_t rank, float2 v) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(rank));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <class T, class W, int TPR, int V, int S, int CL, bool EDGES>
 __global__ void __launch_bounds__(kBackThreads, 1)
 ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__restrict__ grad,
                  const T *__restrict__ in, const W *__restrict__ weight,
                  const float *__restrict__ mean_in, const float *__restrict__ rstd_in,
-                 int64_t rows, int d, int64_t rs, int64_t gs) {
+                 int64_t rows, int width, int chunk, int64_t rs, int64_t gs) {
     constexpr int NT = kBackThreads, R = NT / TPR, NW = TPR / 32;
+    static_assert(CL == 1 || (R == 1 && !EDGES), "a cluster takes one row at a time");
     extern __shared__ __align__(16) uint4 slots[];
     __shared__ float2 red[2][NT / 32];
+    __shared__ float2 peers[2][CL];
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    // this CTA's columns: d of them from `from` on
+    const int rank = CL == 1 ? 0 : blockIdx.x % CL, from = rank * chunk;
+    const int d = CL == 1 ? width : max(0, min(chunk, width - from));
+    in += from;
+    grad += from;
+    weight += from;
+    grad_in += from;
+    part += from;
     pdl_wait();
     pdl_trigger();
-    const int64_t G = static_cast<int64_t>(gridDim.x) * R;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * R + group;
-    const Ring<T, NT, TPR, V, 2> ring(slots, t, d);
+    const int64_t share = blockIdx.x / CL, count = gridDim.x / CL;
+    const int64_t G = count * R, first = share * R + group;
+    const Span8 span = span_of<T, EDGES>(in + first * rs, d);
+    const int edge = edge_of<EDGES>(span, d, t);
+    const Ring<T, NT, TPR, V, 2> ring(slots, t, span.width);
     const auto fetch = [&](int64_t r, int slot) {
         if (r < rows) {
-            ring.fetch(slot, 0, in + r * rs);
-            ring.fetch(slot, 1, grad + r * gs);
+            ring.fetch(slot, 0, in + r * rs + span.head);
+            ring.fetch(slot, 1, grad + r * gs + span.head);
         }
         copy_commit();
     };
@@ -422,15 +515,24 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
     float2 dw[V][4], db[V][4];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = 8 * (t + TPR * i);
-        w[i] = c < d ? load_params(weight + c) : Vec8<W>::zero();
+        w[i] = params8<EDGES>(weight + span.head + ring.column(i), ring.in(i));
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             dw[i][j] = db[i][j] = make_float2(0.f, 0.f);
     }
+    float we = 0.f, dwe = 0.f, dbe = 0.f, next_x = 0.f, next_y = 0.f;
+    const auto fetch_edge = [&](int64_t r) {
+        if (EDGES && edge >= 0 && r < rows) {
+            next_x = to_float(__ldg(in + r * rs + edge));
+            next_y = to_float(__ldg(grad + r * gs + edge));
+        }
+    };
+    if (EDGES && edge >= 0)
+        we = to_float(__ldg(weight + edge));
+    fetch_edge(first);
     int slot = 0, k = 0;
     float mean = first < rows ? mean_in[first] : 0.f, rstd = first < rows ? rstd_in[first] : 0.f;
-    const float inv = 1.0f / static_cast<float>(d);
+    const float inv = 1.0f / static_cast<float>(width);
     for (int64_t r = first; r < rows; r += G, k ^= 1) {
         // the slot read in the round before: this thread is done with it
         fetch(r + (S - 1) * G, slot == 0 ? S - 1 : slot - 1);
@@ -440,8 +542,16 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
             mean = mean_in[r + G];
             rstd = rstd_in[r + G];
         }
+        const float xe = (next_x - m2.x) * r1, ye = next_y;   // an edge's h and gradient
+        fetch_edge(r + G);
         copy_wait<S - 1>();
         float2 a2 = make_float2(0.f, 0.f), b2 = a2;
+        if (EDGES && edge >= 0) {
+            dbe += ye;
+            dwe = fmaf(ye, xe, dwe);
+            a2.x = ye * we;
+            b2.x = ye * we * xe;
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const Vec8<T> x = ring.held(slot, 0, i), y = ring.held(slot, 1, i);
@@ -469,14 +579,25 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
                 b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
             }
         }
+        if constexpr (CL > 1) {
+            if (threadIdx.x < CL)
+                put_peer(&peers[k][rank], threadIdx.x, make_float2(a, b));
+            __syncwarp();
+            cluster_barrier();
+            a = b = 0.f;
+#pragma unroll
+            for (int q = 0; q < CL; ++q) {
+                a += peers[k][q].x;
+                b += peers[k][q].y;
+            }
+        }
         a *= inv;
         b *= inv;
         const float xs = -b * r1 * r1, off = -a * r1;
         const float2 xs2 = make_float2(xs, xs), off2 = make_float2(off, off);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (t + TPR * i);
-            if (c >= d)
+            if (!ring.in(i))
                 continue;
             const Vec8<T> x = ring.held(slot, 0, i), y = ring.held(slot, 1, i);
             Vec8<T> o;
@@ -484,14 +605,17 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
             for (int j = 0; j < 4; ++j)
                 o.put(j, fma2(y.pair(j), mul2(w[i].pair(j), r2),
                               fma2(sub2(x.pair(j), m2), xs2, off2)));
-            o.store(grad_in + r * d + c);
+            o.store(grad_in + r * width + span.head + ring.column(i));
         }
+        if (EDGES && edge >= 0)
+            grad_in[r * width + edge] = from_float<T>(r1 * (ye * we - a - xe * b));
         slot = slot == S - 1 ? 0 : slot + 1;
     }
+    if constexpr (CL > 1)
+        cluster_barrier();      // no CTA leaves while another writes to it
     // columns' shares: over the CTA's rows in shared memory, group by group
-    float *pw = part + static_cast<int64_t>(blockIdx.x) * d;
-    float *pb = pw + static_cast<int64_t>(gridDim.x) * d;
-    if constexpr (R == 1) {
+    float *pw = part + share * width, *pb = pw + count * width;
+    if constexpr (R == 1 && !EDGES) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = 8 * (t + TPR * i);
@@ -506,26 +630,35 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
             }
         }
     } else {
-        // [R][8 V TPR] for the weight, then, once read, for the bias
-        constexpr int kCols = 8 * V * TPR;
+        // [R][kCols] for the weight, then, once read, for the bias
+        constexpr int kCols = 8 * V * TPR + 16;
         float *sum = reinterpret_cast<float *>(slots);
         copy_wait<0>();
         __syncthreads();      // every group is done with the ring
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
+            float *to = sum + group * kCols;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < V; ++i) {
+                if (!ring.in(i))
+                    continue;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<float2 *>(sum + group * kCols + 8 * (t + TPR * i) + 2 * j) =
-                        which ? db[i][j] : dw[i][j];
+                for (int j = 0; j < 4; ++j) {
+                    const float2 v = which ? db[i][j] : dw[i][j];
+                    const int c = span.head + ring.column(i) + 2 * j;
+                    to[c] = v.x;
+                    to[c + 1] = v.y;
+                }
+            }
+            if (EDGES && edge >= 0)
+                to[edge] = which ? dbe : dwe;
             __syncthreads();
             for (int c = threadIdx.x; c < d; c += NT) {
-                float s = sum[c];
+                float v = sum[c];
 #pragma unroll
                 for (int q = 1; q < R; ++q)
-                    s += sum[q * kCols + c];
-                (which ? pb : pw)[c] = s;
+                    v += sum[q * kCols + c];
+                (which ? pb : pw)[c] = v;
             }
             __syncthreads();
         }
@@ -556,8 +689,10 @@ template <class F> int with_types(int dtype, int param_dtype, F f) {
 }
 
 // Shares of the parameters' gradients that the second kernel joins: one per
-// SM, or per row where there are fewer rows.
-int64_t shares(int64_t T) { return std::min<int64_t>(T, device_sm_count()); }
+// SM, or per row where there are fewer rows; a multiple of kKinds of them.
+int64_t shares(int64_t T) {
+    return std::min<int64_t>(ceil_div64(T, kKinds), std::max(1, device_sm_count() / kKinds)) * kKinds;
+}
 
 template <int N> using Const = std::integral_constant<int, N>;
 
@@ -584,32 +719,49 @@ template <int SIZE, class F> bool with_forward_ring(int64_t nv, int *rc, F f) {
     return true;
 }
 
-// Calls f(integral constants TPR, V, S) for the backward ring: the slots of
+// Calls f(integral constants TPR, V, S, CL) for the backward ring: the slots of
 // the 512 threads of an SM take up to 192 KB of shared memory.
 template <int SIZE, class F> bool with_backward_ring(int64_t nv, int *rc, F f) {
     constexpr int S2 = SIZE == 2 ? 6 : 3;    // slots at two vectors per thread
+    constexpr Const<1> one{};
     if (nv <= 32)
-        *rc = f(Const<32>{}, Const<1>{}, Const<S2>{});
+        *rc = f(Const<32>{}, Const<1>{}, Const<S2>{}, one);
     else if (nv <= 64)
-        *rc = f(Const<32>{}, Const<2>{}, Const<S2>{});
+        *rc = f(Const<32>{}, Const<2>{}, Const<S2>{}, one);
     else if (nv <= 128)
-        *rc = f(Const<64>{}, Const<2>{}, Const<S2>{});
+        *rc = f(Const<64>{}, Const<2>{}, Const<S2>{}, one);
     else if (nv <= 256)
-        *rc = f(Const<128>{}, Const<2>{}, Const<S2>{});
+        *rc = f(Const<128>{}, Const<2>{}, Const<S2>{}, one);
     else if (nv <= 512)
-        *rc = f(Const<256>{}, Const<2>{}, Const<S2>{});
+        *rc = f(Const<256>{}, Const<2>{}, Const<S2>{}, one);
     else if (nv <= 1024)
-        *rc = f(Const<512>{}, Const<2>{}, Const<S2>{});
-    else {
-        if constexpr (SIZE == 2)
-            if (nv <= 2048) {
-                *rc = f(Const<512>{}, Const<4>{}, Const<3>{});
-                return true;
-            }
-        return false;
+        *rc = f(Const<512>{}, Const<2>{}, Const<S2>{}, one);
+    else if constexpr (SIZE == 2) {
+        if (nv <= 2048)
+            *rc = f(Const<512>{}, Const<4>{}, Const<3>{}, one);
+        else if (nv <= 4096)
+            *rc = f(Const<512>{}, Const<4>{}, Const<3>{}, Const<2>{});
+        else
+            return false;
+    } else {
+        if (nv <= 2048)
+            *rc = f(Const<512>{}, Const<2>{}, Const<S2>{}, Const<2>{});
+        else if (nv <= 4096)
+            *rc = f(Const<512>{}, Const<2>{}, Const<S2>{}, Const<4>{});
+        else
+            return false;
     }
     return true;
 }
+
+// Whether the rows of two buffers, a and b elements apart, start at the same
+// offset from a 16-byte boundary, and rows kKinds apart at the same one.
+inline bool same_offsets(const Region &x, int64_t a, const Region &y, int64_t b, int64_t size) {
+    return (reinterpret_cast<uintptr_t>(x.dev) - reinterpret_cast<uintptr_t>(y.dev)) % 16 == 0 &&
+           ((a - b) * size) % 16 == 0;
+}
+// Vectors of 8 elements that a row of d elements off a boundary holds at most.
+inline int64_t vectors_of(int64_t d) { return std::max<int64_t>(1, d / 8); }
 
 }  // namespace
 }  // namespace gact
@@ -632,28 +784,30 @@ extern "C" int layer_norm(void *out, float *mean, float *rstd, const void *in, c
                    {bias, bias ? static_cast<uint64_t>(d * wsize) : 0, uintptr_t(wsize), false}};
     if ((rc = check_regions(r, 6)) != GATED_ACT_OK)
         return rc;
-    const int64_t grid = std::min<int64_t>(T, int64_t(device_sm_count()) * 64);
     const bool vec = d % 8 == 0 && row_stride % 8 == 0 && aligned(r[0].dev, 16) &&
                      aligned(r[3].dev, 16) && aligned(r[4].dev, 16) && aligned(r[5].dev, 16) &&
                      T <= 0x7FFFFFFF;
     return with_types(dtype, param_dtype, [&](auto t, auto w) {
         using E = decltype(t);
         using W = decltype(w);
-        const auto go = [&](auto nt, auto v, auto slots) {
-            constexpr size_t smem = slots() * v() * nt() * 8 * sizeof(E);
-            const auto kernel = ln_forward_ring<E, W, nt(), v(), slots()>;
-            const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
-            if (e != cudaSuccess)
-                return cuda_status(e);
-            const int64_t ctas = std::min<int64_t>(T, device_sm_count() * (1024 / nt()));
-            return launched(launch_kernel(
-                kernel, dim3(static_cast<unsigned>(ctas)), dim3(nt()), smem, stream, 1,
-                as<E>(r[0]), as<float>(r[1]), as<float>(r[2]), as<const E>(r[3]),
-                as<const W>(r[4]), as<const W>(r[5]), T, static_cast<int>(d), row_stride,
-                static_cast<float>(eps)));
+        const auto ring = [&](auto edges) {
+            return [&](auto nt, auto v, auto slots) {
+                constexpr size_t smem = slots() * v() * nt() * 8 * sizeof(E);
+                const auto kernel = ln_forward_ring<E, W, nt(), v(), slots(), edges()>;
+                const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
+                if (e != cudaSuccess)
+                    return cuda_status(e);
+                const int64_t most = std::max(1, device_sm_count() / kKinds) * (1024 / nt());
+                const int64_t ctas = std::min<int64_t>(ceil_div64(T, kKinds), most) * kKinds;
+                return launched(launch_kernel(
+                    kernel, dim3(static_cast<unsigned>(edges() ? ctas : std::min(T, ctas))),
+                    dim3(nt()), smem, stream, 1, as<E>(r[0]), as<float>(r[1]), as<float>(r[2]),
+                    as<const E>(r[3]), as<const W>(r[4]), as<const W>(r[5]), T,
+                    static_cast<int>(d), row_stride, static_cast<float>(eps)));
+            };
         };
         int done;
-        if (vec && with_forward_ring<sizeof(E)>(d / 8, &done, go))
+        if (vec && with_forward_ring<sizeof(E)>(d / 8, &done, ring(std::false_type{})))
             return done;
         if (vec && d / 8 <= 4096)
             return launched(launch_kernel(
@@ -661,7 +815,11 @@ extern "C" int layer_norm(void *out, float *mean, float *rstd, const void *in, c
                 stream, 1, as<E>(r[0]), as<float>(r[1]), as<float>(r[2]), as<const E>(r[3]),
                 as<const W>(r[4]), as<const W>(r[5]), static_cast<int>(d), row_stride,
                 static_cast<float>(eps)));
-        return launched(launch_kernel(ln_forward_any<E, W>, dim3(static_cast<unsigned>(grid)),
+        if (!vec && same_offsets(r[0], d, r[3], row_stride, size) &&
+            with_forward_ring<sizeof(E)>(vectors_of(d), &done, ring(std::true_type{})))
+            return done;
+        const int64_t grid = std::min<int64_t>(T, int64_t(device_sm_count()) * 64);
+        return launched(launch_kernel(ln_forward_wide<E, W>, dim3(static_cast<unsigned>(grid)),
                                       dim3(kThreads), 0, stream, 1, as<E>(r[0]), as<float>(r[1]),
                                       as<float>(r[2]), as<const E>(r[3]), as<const W>(r[4]),
                                       as<const W>(r[5]), T, d, row_stride,
@@ -709,25 +867,39 @@ extern "C" int layer_norm_backward(void *grad_in, float *grad_weight, float *gra
         rc = with_types(dtype, param_dtype, [&](auto t, auto w) {
             using E = decltype(t);
             using W = decltype(w);
-            const auto go = [&](auto tpr, auto v, auto slots) {
-                constexpr size_t smem = 2 * slots() * v() * kBackThreads * 8 * sizeof(E);
-                const auto kernel = ln_backward_ring<E, W, tpr(), v(), slots()>;
-                const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
-                if (e != cudaSuccess)
-                    return cuda_status(e);
-                n = std::min<int64_t>(shares(T), ceil_div64(T, kBackThreads / tpr()));
-                return launched(launch_kernel(
-                    kernel, dim3(static_cast<unsigned>(n)), dim3(kBackThreads), smem, stream, 1,
-                    as<E>(r[0]), part, as<const E>(r[4]), as<const E>(r[5]), as<const W>(r[6]),
-                    as<const float>(r[7]), as<const float>(r[8]), T, static_cast<int>(d),
-                    row_stride, grad_stride));
+            const auto ring = [&](auto edges) {
+                return [&](auto tpr, auto v, auto slots, auto cl) {
+                    constexpr bool kEdges = edges() && cl() == 1;
+                    if (edges() && !kEdges)      // rows that wide are not sent here
+                        return static_cast<int>(GATED_ACT_ERR_VARIANT);
+                    constexpr size_t smem = 2 * slots() * v() * kBackThreads * 8 * sizeof(E);
+                    const auto kernel = ln_backward_ring<E, W, tpr(), v(), slots(), cl(), kEdges>;
+                    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
+                    if (e != cudaSuccess)
+                        return cuda_status(e);
+                    const int64_t chunk = ceil_div64(d / 8, cl()) * 8;
+                    n = std::min<int64_t>(ceil_div64(T, kBackThreads / tpr()),
+                                          std::max<int64_t>(1, shares(T) / cl()));
+                    if (kEdges)
+                        n = std::min(ceil_div64(n, kKinds) * kKinds, shares(T));
+                    return launched(launch_kernel(
+                        kernel, dim3(static_cast<unsigned>(n * cl())), dim3(kBackThreads), smem,
+                        stream, cl(), as<E>(r[0]), part, as<const E>(r[4]), as<const E>(r[5]),
+                        as<const W>(r[6]), as<const float>(r[7]), as<const float>(r[8]), T,
+                        static_cast<int>(d), static_cast<int>(chunk), row_stride, grad_stride));
+                };
             };
             int done;
-            if (vec && with_backward_ring<sizeof(E)>(d / 8, &done, go))
+            if (vec && with_backward_ring<sizeof(E)>(d / 8, &done, ring(std::false_type{})))
+                return done;
+            if (!vec && same_offsets(r[0], d, r[5], row_stride, size) &&
+                same_offsets(r[0], d, r[4], grad_stride, size) &&
+                vectors_of(d) <= (size == 2 ? 2048 : 1024) &&
+                with_backward_ring<sizeof(E)>(vectors_of(d), &done, ring(std::true_type{})))
                 return done;
             const int64_t grid = std::min<int64_t>(T, int64_t(device_sm_count()) * 64);
             done = launched(launch_kernel(
-                ln_backward_rows_any<E, W>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
+                ln_backward_rows<E, W>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
                 stream, 1, as<E>(r[0]), as<const E>(r[4]), as<const E>(r[5]), as<const W>(r[6]),
                 as<const float>(r[7]), as<const float>(r[8]), T, d, row_stride, grad_stride));
             if (done != GATED_ACT_OK)
@@ -735,7 +907,7 @@ extern "C" int layer_norm_backward(void *grad_in, float *grad_weight, float *gra
             const int64_t per = ceil_div64(T, shares(T));
             n = ceil_div64(T, per);
             return launched(launch_kernel(
-                ln_backward_columns_any<E>,
+                ln_backward_columns<E>,
                 dim3(static_cast<unsigned>(ceil_div64(d, kThreads)), static_cast<unsigned>(n)),
                 dim3(kThreads), 0, stream, 1, part, as<const E>(r[4]), as<const E>(r[5]),
                 as<const float>(r[7]), as<const float>(r[8]), T, per, d, row_stride, grad_stride));
