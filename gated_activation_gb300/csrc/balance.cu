@@ -529,7 +529,7 @@ extern "C" int moe_balance_loss(float *loss, int32_t *counts, int32_t *tokens, f
                    {live, live ? static_cast<uint64_t>(T) : 0, 1, false}};
     if ((rc = check_regions(r, 8)) != GATED_ACT_OK)
         return rc;
-    const bool vec = E % 8 == 0 && logits_stride % 8 == 0 && aligned(r[5].dev, 16);
+    const bool vec = E % 8 == 0 && logits_stride % 8 == 0 && aligned(r[5].dev, 8 * size);
     const bool cluster = T <= kClusterTokens;
     const int64_t G = cluster ? kCluster : parts(T), per = ceil_div64(T, G);
     float *part_p = as<float>(r[4]);
@@ -581,8 +581,8 @@ extern "C" int moe_balance_loss_backward(void *grad_logits, const float *grad_lo
                    {live, live ? static_cast<uint64_t>(T) : 0, 1, false}};
     if ((rc = check_regions(r, 6)) != GATED_ACT_OK)
         return rc;
-    const bool vec = E % 8 == 0 && logits_stride % 8 == 0 && aligned(r[0].dev, 16) &&
-                     aligned(r[2].dev, 16);
+    const bool vec = E % 8 == 0 && logits_stride % 8 == 0 && aligned(r[0].dev, 8 * size) &&
+                     aligned(r[2].dev, 8 * size);
     return with_type(dtype, [&](auto t) {
         return with_lanes(E, vec, [&](auto l, auto v, auto n) {
             using Elem = decltype(t);

@@ -1050,8 +1050,8 @@ int forward(void *out, int8_t *codes, uint8_t *scales, const void *in, int64_t M
                    {n_rows, n_rows ? 4u : 0u, 4, false}};
     if ((rc = check_regions(r, 5)) != GATED_ACT_OK)
         return rc;
-    const bool vec = d % 8 == 0 && rs % 8 == 0 && aligned(r[0].dev, 16) && aligned(r[1].dev, 8) &&
-                     aligned(r[3].dev, 16);
+    const bool vec = d % 8 == 0 && rs % 8 == 0 && aligned(r[0].dev, 8 * size) && aligned(r[1].dev, 8) &&
+                     aligned(r[3].dev, 8 * size);
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
         if (vec) {
@@ -1092,8 +1092,8 @@ int backward(void *grad_in, void *out, const void *grad, const int8_t *codes,
                    {n_rows, n_rows ? 4u : 0u, 4, false}};
     if ((rc = check_regions(r, 6)) != GATED_ACT_OK)
         return rc;
-    const bool vec = d % 8 == 0 && gs % 8 == 0 && aligned(r[0].dev, 16) && aligned(r[1].dev, 16) &&
-                     aligned(r[2].dev, 16) && aligned(r[3].dev, 8);
+    const bool vec = d % 8 == 0 && gs % 8 == 0 && aligned(r[0].dev, 8 * size) && aligned(r[1].dev, 8 * size) &&
+                     aligned(r[2].dev, 8 * size) && aligned(r[3].dev, 8);
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
         if (vec) {
@@ -1172,8 +1172,8 @@ extern "C" int gelu_and_mul_sparse_checkpoint(void *out, int8_t *codes, uint8_t 
                    {in, span_bytes(T, row_stride, 2 * d, size), uintptr_t(size), false}};
     if ((rc = check_regions(r, 5)) != GATED_ACT_OK)
         return rc;
-    const bool vec = d % 8 == 0 && row_stride % 8 == 0 && aligned(r[0].dev, 16) &&
-                     aligned(r[1].dev, 8) && aligned(r[4].dev, 16) && T <= 0x7FFFFFFF;
+    const bool vec = d % 8 == 0 && row_stride % 8 == 0 && aligned(r[0].dev, 8 * size) &&
+                     aligned(r[1].dev, 8) && aligned(r[4].dev, 8 * size) && T <= 0x7FFFFFFF;
     return with_type(dtype, [&](auto t) {
         using E = decltype(t);
         const auto go = [&](auto nt, auto v) {
@@ -1233,8 +1233,8 @@ extern "C" int gelu_and_mul_sparse_backward(void *grad_in, void *out, const void
                    {std, static_cast<uint64_t>(T * 4), 4, false}};
     if ((rc = check_regions(r, 6)) != GATED_ACT_OK)
         return rc;
-    const bool vec = d % 8 == 0 && grad_stride % 8 == 0 && aligned(r[0].dev, 16) &&
-                     aligned(r[1].dev, 16) && aligned(r[2].dev, 16) && aligned(r[3].dev, 8) &&
+    const bool vec = d % 8 == 0 && grad_stride % 8 == 0 && aligned(r[0].dev, 8 * size) &&
+                     aligned(r[1].dev, 8 * size) && aligned(r[2].dev, 8 * size) && aligned(r[3].dev, 8) &&
                      T <= 0x7FFFFFFF;
     return with_type(dtype, [&](auto t) {
         using E = decltype(t);
@@ -1295,7 +1295,7 @@ extern "C" int gated_act_checkpoint_values(void *values, const int8_t *codes,
         return rc;
     return with_type(dtype, [&](auto t) {
         using E = decltype(t);
-        if (d % 8 == 0 && aligned(r[0].dev, 16) && aligned(r[1].dev, 8))
+        if (d % 8 == 0 && aligned(r[0].dev, 8 * size) && aligned(r[1].dev, 8))
             return with_index(M * 2 * (d / 8), kValuesVpt, [&](auto idx, dim3 grid) {
                 using I = decltype(idx);
                 return launched(launch_kernel(

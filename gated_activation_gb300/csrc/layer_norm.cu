@@ -213,9 +213,13 @@ template <bool EDGES> __device__ __forceinline__ int edge_of(const Span8 &s, int
 
 // This thread's part of the ring: `which` counts the rows of a slot (the
 // input, and in the backward pass the gradient).  Columns from the span's head.
+// A vector is P pieces of 16 bytes, and neighbouring lanes have neighbouring
+// pieces: of 16-bit elements a vector is 8 consecutive columns, of 32-bit ones
+// twice 4 of them, 4 TPR apart (two pieces side by side would have each access
+// of a warp fetch half of every sector that it touches).
 template <class T, int NT, int TPR, int V, int ROWS> struct Ring {
-    static constexpr int P = sizeof(T) / 2;           // 16-byte pieces of a vector
-    static constexpr int kPiece = 16 / sizeof(T);     // their elements
+    static constexpr int P = sizeof(T) / 2;
+    static constexpr int kPiece = 16 / sizeof(T);     // elements of a piece
     uint4 *mine;                                      // [S][ROWS][V][P][NT]
     uint32_t at;
     int t, d;
@@ -225,44 +229,58 @@ template <class T, int NT, int TPR, int V, int ROWS> struct Ring {
     __device__ static int index(int slot, int which, int i, int p) {
         return (((slot * ROWS + which) * V + i) * P + p) * NT;
     }
-    __device__ int column(int i) const { return 8 * (t + TPR * i); }
-    __device__ bool in(int i) const { return column(i) < d; }
+    // Column of element e (0 to 7) of vector i.
+    __device__ int column(int i, int e) const {
+        return kPiece * (t + TPR * (P * i + e / kPiece)) + e % kPiece;
+    }
+    __device__ bool in(int i, int e = 0) const { return column(i, e) < d; }
     __device__ void fetch(int slot, int which, const T *row) const {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (in(i))
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    copy16(at + 16u * index(slot, which, i, p), row + column(i) + kPiece * p);
+            for (int p = 0; p < P; ++p)
+                if (in(i, kPiece * p))
+                    copy16(at + 16u * index(slot, which, i, p), row + column(i, kPiece * p));
     }
     // Zero past the span's end.
     __device__ Vec8<T> held(int slot, int which, int i) const {
         Vec8<T> v = Vec8<T>::zero();
-        if (in(i)) {
-            uint4 *q = reinterpret_cast<uint4 *>(&v);
+        uint4 *q = reinterpret_cast<uint4 *>(&v);
 #pragma unroll
-            for (int p = 0; p < P; ++p)
+        for (int p = 0; p < P; ++p)
+            if (in(i, kPiece * p))
                 q[p] = mine[index(slot, which, i, p)];
-        }
+        return v;
+    }
+    __device__ void store(const Vec8<T> &v, T *row, int i) const {
+        const uint4 *q = reinterpret_cast<const uint4 *>(&v);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            if (in(i, kPiece * p))
+                st_vec_out(row + column(i, kPiece * p), q[p]);
+    }
+    // The parameters of vector i; one by one where they are not aligned.
+    template <bool EDGES, class W> __device__ Vec8<W> params(const W *w, int i) const {
+        Vec8<W> v = Vec8<W>::zero();
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            if (in(i, kPiece * p)) {
+                const W *from = w + column(i, kPiece * p);
+                W *to = reinterpret_cast<W *>(&v) + kPiece * p;
+                if constexpr (EDGES) {
+#pragma unroll
+                    for (int j = 0; j < kPiece; ++j)
+                        to[j] = __ldg(from + j);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kPiece * static_cast<int>(sizeof(W)) / 16; ++j)
+                        reinterpret_cast<uint4 *>(to)[j] =
+                            __ldg(reinterpret_cast<const uint4 *>(from) + j);
+                }
+            }
         return v;
     }
 };
-
-// The parameters of 8 columns at p; one by one where they are not aligned.
-template <bool EDGES, class W> __device__ __forceinline__ Vec8<W> params8(const W *p, bool in) {
-    Vec8<W> v = Vec8<W>::zero();
-    if (in) {
-        if constexpr (EDGES) {
-            W *e = reinterpret_cast<W *>(&v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                e[j] = __ldg(p + j);
-        } else {
-            v = load_params(p);
-        }
-    }
-    return v;
-}
 
 // Barrier of the TPR threads of one row: the CTA's, or one of its named ones.
 template <int NT, int TPR> __device__ __forceinline__ void row_barrier() {
@@ -313,8 +331,8 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
     Vec8<W> w[V], b[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        w[i] = params8<EDGES>(weight + span.head + ring.column(i), ring.in(i));
-        b[i] = params8<EDGES>(bias + span.head + ring.column(i), ring.in(i) && bias);
+        w[i] = ring.template params<EDGES>(weight + span.head, i);
+        b[i] = bias ? ring.template params<EDGES>(bias + span.head, i) : Vec8<W>::zero();
     }
     float we = 0.f, be = 0.f, next = 0.f;
     if (EDGES && edge >= 0) {
@@ -352,10 +370,11 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
             if (ring.in(i)) {
                 const Vec8<T> x = ring.held(slot, 0, i);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 e = sub2(x.pair(j), m2);
-                    acc = fma2(e, e, acc);
-                }
+                for (int j = 0; j < 4; ++j)
+                    if (ring.in(i, 2 * j)) {
+                        const float2 e = sub2(x.pair(j), m2);
+                        acc = fma2(e, e, acc);
+                    }
             }
         const float var = row_sum<NT>(acc.x + acc.y, red[1]) * inv;
         const float rstd = rsqrtf(var + eps);
@@ -373,7 +392,7 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 o.put(j, fma2(mul2(sub2(x.pair(j), m2), r2), w[i].pair(j), b[i].pair(j)));
-            o.store(out + r * d + span.head + ring.column(i));
+            ring.store(o, out + r * d + span.head, i);
         }
         if (EDGES && edge >= 0)
             out[r * d + edge] = from_float<T>(fmaf((xe - mean) * rstd, we, be));
@@ -515,7 +534,7 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
     float2 dw[V][4], db[V][4];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        w[i] = params8<EDGES>(weight + span.head + ring.column(i), ring.in(i));
+        w[i] = ring.template params<EDGES>(weight + span.head, i);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             dw[i][j] = db[i][j] = make_float2(0.f, 0.f);
@@ -605,7 +624,7 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
             for (int j = 0; j < 4; ++j)
                 o.put(j, fma2(y.pair(j), mul2(w[i].pair(j), r2),
                               fma2(sub2(x.pair(j), m2), xs2, off2)));
-            o.store(grad_in + r * width + span.head + ring.column(i));
+            ring.store(o, grad_in + r * width + span.head, i);
         }
         if (EDGES && edge >= 0)
             grad_in[r * width + edge] = from_float<T>(r1 * (ye * we - a - xe * b));
@@ -617,18 +636,16 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
     float *pw = part + share * width, *pb = pw + count * width;
     if constexpr (R == 1 && !EDGES) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = 8 * (t + TPR * i);
-            if (c >= d)
-                continue;
+        for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                *reinterpret_cast<float4 *>(pw + c + 2 * j) =
-                    make_float4(dw[i][j].x, dw[i][j].y, dw[i][j + 1].x, dw[i][j + 1].y);
-                *reinterpret_cast<float4 *>(pb + c + 2 * j) =
-                    make_float4(db[i][j].x, db[i][j].y, db[i][j + 1].x, db[i][j + 1].y);
-            }
-        }
+            for (int j = 0; j < 4; j += 2)
+                if (ring.in(i, 2 * j)) {
+                    const int c = ring.column(i, 2 * j);
+                    *reinterpret_cast<float4 *>(pw + c) =
+                        make_float4(dw[i][j].x, dw[i][j].y, dw[i][j + 1].x, dw[i][j + 1].y);
+                    *reinterpret_cast<float4 *>(pb + c) =
+                        make_float4(db[i][j].x, db[i][j].y, db[i][j + 1].x, db[i][j + 1].y);
+                }
     } else {
         // [R][kCols] for the weight, then, once read, for the bias
         constexpr int kCols = 8 * V * TPR + 16;
@@ -639,17 +656,15 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
         for (int which = 0; which < 2; ++which) {
             float *to = sum + group * kCols;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (!ring.in(i))
-                    continue;
+            for (int i = 0; i < V; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 v = which ? db[i][j] : dw[i][j];
-                    const int c = span.head + ring.column(i) + 2 * j;
-                    to[c] = v.x;
-                    to[c + 1] = v.y;
-                }
-            }
+                for (int j = 0; j < 4; ++j)
+                    if (ring.in(i, 2 * j)) {
+                        const float2 v = which ? db[i][j] : dw[i][j];
+                        const int c = span.head + ring.column(i, 2 * j);
+                        to[c] = v.x;
+                        to[c + 1] = v.y;
+                    }
             if (EDGES && edge >= 0)
                 to[edge] = which ? dbe : dwe;
             __syncthreads();
@@ -809,7 +824,7 @@ extern "C" int layer_norm(void *out, float *mean, float *rstd, const void *in, c
         int done;
         if (vec && with_forward_ring<sizeof(E)>(d / 8, &done, ring(std::false_type{})))
             return done;
-        if (vec && d / 8 <= 4096)
+        if (vec && d / 8 <= 4096 && aligned(r[0].dev, 8 * size) && aligned(r[3].dev, 8 * size))
             return launched(launch_kernel(
                 ln_forward_vec<E, W, 1024, 4>, dim3(static_cast<unsigned>(T)), dim3(1024), 0,
                 stream, 1, as<E>(r[0]), as<float>(r[1]), as<float>(r[2]), as<const E>(r[3]),

@@ -154,7 +154,7 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// 8 consecutive elements of a row, as loaded: four words of two 16-bit
+// 8 consecutive elements of a row, aligned to their size, as loaded: four words of two 16-bit
 // elements, or eight of one.  pair(i) is elements 2i and 2i + 1.
 template <class T> struct Vec8 {
     static_assert(sizeof(T) == 2, "16-bit elements");
@@ -188,15 +188,25 @@ template <class T> struct Vec8 {
         return max(w >> 16, w & 0xFFFFu);
     }
 };
+// Of fp32, 32 bytes in one access (PTX ISA ld/st.global.v8.b32, sm_100 and
+// later): two 16-byte accesses of a warp would each touch every sector.
 template <> struct Vec8<float> {
     uint4 q[2];
     __device__ static Vec8 zero() {
         return {{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}};
     }
-    __device__ static Vec8 load(const float *p) { return {{ld_stream(p), ld_stream(p + 4)}}; }
+    __device__ static Vec8 load(const float *p) {
+        Vec8 v;
+        asm("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(v.q[0].x), "=r"(v.q[0].y), "=r"(v.q[0].z), "=r"(v.q[0].w), "=r"(v.q[1].x),
+              "=r"(v.q[1].y), "=r"(v.q[1].z), "=r"(v.q[1].w)
+            : "l"(p));
+        return v;
+    }
     __device__ void store(float *p) const {
-        st_vec_out(p, q[0]);
-        st_vec_out(p + 4, q[1]);
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+                     "r"(q[0].x), "r"(q[0].y), "r"(q[0].z), "r"(q[0].w), "r"(q[1].x), "r"(q[1].y),
+                     "r"(q[1].z), "r"(q[1].w));
     }
     __device__ float2 pair(int i) const {
         const uint32_t *w = &q[i / 2].x + 2 * (i & 1);
