@@ -48,6 +48,50 @@ __device__ __forceinline__ void put_block(int8_t *codes, uint8_t *scale, float v
         *scale = static_cast<uint8_t>(s);
 }
 
+// Four blocks of each half, whole, one element of each per lane: their codes at
+// codes + i * es and codes + d + i * es, their scales at scales + i * ss and
+// scales + B + i * ss.  The eight largest magnitudes are found together, halving
+// the values at every exchange, so that lane 4 k ends with the k-th and each
+// scale is computed once, not by every lane.
+template <bool KEEP_SIGN>
+__device__ __forceinline__ void put_blocks(int8_t *codes, int64_t d, int es, uint8_t *scales,
+                                           int64_t B, int ss, const float (&g)[4],
+                                           const float (&u)[4], int lane) {
+    uint32_t t[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        t[i] = abs_bits(g[i]);
+        t[4 + i] = abs_bits(u[i]);
+    }
+#pragma unroll
+    for (int n = 4; n >= 1; n >>= 1) {
+        const bool up = lane & (4 * n);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const uint32_t keep = up ? t[i + n] : t[i], give = up ? t[i] : t[i + n];
+            t[i] = max(keep, __shfl_xor_sync(0xFFFFFFFFu, give, 4 * n));
+        }
+    }
+    t[0] = max(t[0], __shfl_xor_sync(0xFFFFFFFFu, t[0], 2));
+    t[0] = max(t[0], __shfl_xor_sync(0xFFFFFFFFu, t[0], 1));
+    const uint32_t s = scale_of(t[0]);
+    const int k = lane >> 2;
+    if ((lane & 3) == 0)
+        scales[(k < 4 ? k * ss : B + (k - 4) * ss)] = static_cast<uint8_t>(s);
+    const bool odd = __any_sync(0xFFFFFFFFu, s >= kTopScale);
+    const float f = code_factor(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float v = i < 4 ? g[i & 3] : u[i & 3];
+        if (odd && __shfl_sync(0xFFFFFFFFu, s, 4 * i) >= kTopScale)
+            v = __shfl_sync(0xFFFFFFFFu, s, 4 * i) == kBadScale ? 0.f : clamp_top(v);
+        int q = code_of(v, __shfl_sync(0xFFFFFFFFu, f, 4 * i));
+        if (KEEP_SIGN && i < 4 && v > 0.f)
+            q = max(q, 1);
+        codes[(i < 4 ? 0 : d) + (i & 3) * es] = static_cast<int8_t>(q);
+    }
+}
+
 // n / d; a 32-bit n takes the multiplication.
 template <class I> __device__ __forceinline__ I quotient(I n, I d, const FastDiv &by) {
     if constexpr (sizeof(I) == 4)
@@ -85,34 +129,43 @@ ckpt_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__res
         return;
     const int64_t r = row, b0 = static_cast<int64_t>(job - row * J) * U, c0 = b0 * kBlock + lane;
     const T *p = in + r * rs + c0;
-    T graw[U], uraw[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-        if (c0 + kBlock * i < d) {
-            graw[i] = __ldg(p + kBlock * i);
-            uraw[i] = __ldg(p + d + kBlock * i);
-        }
     T *o = out + r * d + c0;
     int8_t *q = codes + r * 2 * d + c0;
     uint8_t *s = scales + r * 2 * B + b0;
+    T graw[U], uraw[U];
+    if (c0 - lane + kBlock * U <= d) {
 #pragma unroll
-    for (int i = 0; i < U; i += 2) {
-        const bool in0 = c0 + kBlock * i < d, in1 = c0 + kBlock * (i + 1) < d;
-        const float2 g = make_float2(in0 ? to_float(graw[i]) : 0.f, in1 ? to_float(graw[i + 1]) : 0.f);
-        const float2 u = make_float2(in0 ? to_float(uraw[i]) : 0.f, in1 ? to_float(uraw[i + 1]) : 0.f);
-        const float2 y = act_mul<Act>(g, u);
-        if (b0 + i < B) {
-            if (in0)
-                o[kBlock * i] = from_float<T>(y.x);
-            put_block<false>(q + kBlock * i, s + i, g.x, in0, lane);
-            put_block<false>(q + d + kBlock * i, s + B + i, u.x, in0, lane);
+        for (int i = 0; i < U; ++i) {
+            graw[i] = __ldg(p + kBlock * i);
+            uraw[i] = __ldg(p + d + kBlock * i);
         }
-        if (b0 + i + 1 < B) {
-            if (in1)
-                o[kBlock * (i + 1)] = from_float<T>(y.y);
-            put_block<false>(q + kBlock * (i + 1), s + i + 1, g.y, in1, lane);
-            put_block<false>(q + d + kBlock * (i + 1), s + B + i + 1, u.y, in1, lane);
+        float g[U], u[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            g[i] = to_float(graw[i]);
+            u[i] = to_float(uraw[i]);
         }
+#pragma unroll
+        for (int i = 0; i < U; i += 2) {
+            const float2 y = act_mul<Act>(make_float2(g[i], g[i + 1]), make_float2(u[i], u[i + 1]));
+            o[kBlock * i] = from_float<T>(y.x);
+            o[kBlock * (i + 1)] = from_float<T>(y.y);
+        }
+        put_blocks<false>(q, d, kBlock, s, B, 1, g, u, lane);
+        return;
+    }
+    // the row's end
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        if (b0 + i >= B)
+            break;
+        const bool ok = c0 + kBlock * i < d;
+        const float g = ok ? to_float(__ldg(p + kBlock * i)) : 0.f;
+        const float u = ok ? to_float(__ldg(p + d + kBlock * i)) : 0.f;
+        if (ok)
+            o[kBlock * i] = from_float<T>(act_mul<Act>(both(g), both(u)).x);
+        put_block<false>(q + kBlock * i, s + i, g, ok, lane);
+        put_block<false>(q + d + kBlock * i, s + B + i, u, ok, lane);
     }
 }
 
@@ -402,49 +455,63 @@ sparse_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__r
     pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int64_t r = blockIdx.x;
-    const T *p = in + r * rs + threadIdx.x;
+    const int t = threadIdx.x;
+    const T *p = in + r * rs + t;
     float g[V], acc = 0.f;
+    for_groups<NT, V>(t, d, [&](int i, bool full) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        g[i] = static_cast<int>(threadIdx.x) + NT * i < d ? to_float(__ldg(p + NT * i)) : 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        acc += g[i];
+        for (int j = i; j < i + 4; ++j)
+            g[j] = full || t + NT * j < d ? to_float(__ldg(p + NT * j)) : 0.f;
+    });
+    for_groups<NT, V>(t, d, [&](int i, bool) { acc += (g[i] + g[i + 1]) + (g[i + 2] + g[i + 3]); });
     const float n = static_cast<float>(d);
     const float mean = row_sum<NT>(acc, red[0]) / n;
     acc = 0.f;
+    for_groups<NT, V>(t, d, [&](int i, bool full) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float e = static_cast<int>(threadIdx.x) + NT * i < d ? g[i] - mean : 0.f;
-        acc = fmaf(e, e, acc);
-    }
+        for (int j = i; j < i + 4; ++j) {
+            const float e = full || t + NT * j < d ? g[j] - mean : 0.f;
+            acc = fmaf(e, e, acc);
+        }
+    });
     const float std = __fsqrt_rn(row_sum<NT>(acc, red[1]) / n);
     const float cutoff = fmaf(std, z, mean);
-    if (threadIdx.x == 0)
+    if (t == 0)
         std_out[r] = std;
-    T *o = out + r * d + threadIdx.x;
-    int8_t *q = codes + r * 2 * d + threadIdx.x;
-    uint8_t *s = scales + r * 2 * B + (threadIdx.x >> 5);
+    T *o = out + r * d + t;
+    int8_t *q = codes + r * 2 * d + t;
+    uint8_t *s = scales + r * 2 * B + (t >> 5);
+    for_groups<NT, V>(t, d, [&](int i, bool full) {
+        float v[4], u[4];
+        if (full) {
 #pragma unroll
-    for (int i0 = 0; i0 < V; i0 += 4) {
-        T raw[4];
+            for (int j = 0; j < 4; ++j) {
+                v[j] = g[i + j] - cutoff;
+                u[j] = to_float(__ldg(p + d + NT * (i + j)));
+            }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (static_cast<int>(threadIdx.x) + NT * (i0 + j) < d)
-                raw[j] = __ldg(p + d + NT * (i0 + j));
+            for (int j = 0; j < 4; j += 2) {
+                const float2 y = sparse_mul(make_float2(v[j], v[j + 1]), make_float2(u[j], u[j + 1]));
+                o[NT * (i + j)] = from_float<T>(y.x);
+                o[NT * (i + j + 1)] = from_float<T>(y.y);
+            }
+            put_blocks<true>(q + NT * i, d, NT, s + NT / 32 * i, B, NT / 32, v, u, lane);
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int c = threadIdx.x + NT * (i0 + j);
+            const int c = t + NT * (i + j);
             if (c - lane >= d)       // the warp's block as a whole
                 continue;
             const bool ok = c < d;
-            const float v = ok ? g[i0 + j] - cutoff : 0.f, u = ok ? to_float(raw[j]) : 0.f;
+            v[j] = ok ? g[i + j] - cutoff : 0.f;
+            u[j] = ok ? to_float(__ldg(p + d + NT * (i + j))) : 0.f;
             if (ok)
-                o[NT * (i0 + j)] = from_float<T>(sparse_mul(both(v), both(u)).x);
-            put_block<true>(q + NT * (i0 + j), s + NT / 32 * (i0 + j), v, ok, lane);
-            put_block<false>(q + d + NT * (i0 + j), s + B + NT / 32 * (i0 + j), u, ok, lane);
+                o[NT * (i + j)] = from_float<T>(sparse_mul(both(v[j]), both(u[j])).x);
+            put_block<true>(q + NT * (i + j), s + NT / 32 * (i + j), v[j], ok, lane);
+            put_block<false>(q + d + NT * (i + j), s + B + NT / 32 * (i + j), u[j], ok, lane);
         }
-    }
+    });
 }
 
 template <class T, int NT, int V>
@@ -457,47 +524,58 @@ sparse_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__res
     pdl_trigger();
     const int64_t r = blockIdx.x;
     const float std = std_in[r];
-    const T *y = grad + r * gs + threadIdx.x;
-    const int8_t *q = codes + r * 2 * d + threadIdx.x;
-    const uint8_t *s = scales + r * 2 * B + (threadIdx.x >> 5);
-    T *gi = grad_in + r * 2 * d + threadIdx.x, *o = out + r * d + threadIdx.x;
+    const int t = threadIdx.x;
+    const T *y = grad + r * gs + t;
+    const int8_t *q = codes + r * 2 * d + t;
+    const uint8_t *s = scales + r * 2 * B + (t >> 5);
+    T *gi = grad_in + r * 2 * d + t, *o = out + r * d + t;
     float h[V], acc = 0.f;
-#pragma unroll
-    for (int i0 = 0; i0 < V; i0 += 4) {
+    for_groups<NT, V>(t, d, [&](int i, bool full) {
         T dy[4];
         int8_t cg[4], cu[4];
         uint8_t sg[4], su[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (static_cast<int>(threadIdx.x) + NT * (i0 + j) < d) {
-                dy[j] = __ldg(y + NT * (i0 + j));
-                cg[j] = __ldg(q + NT * (i0 + j));
-                cu[j] = __ldg(q + d + NT * (i0 + j));
-                sg[j] = __ldg(s + NT / 32 * (i0 + j));
-                su[j] = __ldg(s + B + NT / 32 * (i0 + j));
+            if (full || t + NT * (i + j) < d) {
+                dy[j] = __ldg(y + NT * (i + j));
+                cg[j] = __ldg(q + NT * (i + j));
+                cu[j] = __ldg(q + d + NT * (i + j));
+                sg[j] = __ldg(s + NT / 32 * (i + j));
+                su[j] = __ldg(s + B + NT / 32 * (i + j));
+            } else {
+                dy[j] = from_float<T>(0.f);
+                cg[j] = cu[j] = 0;
+                sg[j] = su[j] = 0;
             }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            h[i0 + j] = 0.f;
-            if (static_cast<int>(threadIdx.x) + NT * (i0 + j) >= d)
-                continue;
-            const GateGrad2 m = sparse_grad(both(cg[j] * code_step(sg[j])),
-                                            both(cu[j] * code_step(su[j])), both(to_float(dy[j])));
-            h[i0 + j] = m.gate.x;
-            acc += m.gate.x;
-            gi[d + NT * (i0 + j)] = from_float<T>(m.up.x);
-            if (out)
-                o[NT * (i0 + j)] = from_float<T>(m.out.x);
+        for (int j = 0; j < 4; j += 2) {
+            const GateGrad2 m = sparse_grad(
+                make_float2(cg[j] * code_step(sg[j]), cg[j + 1] * code_step(sg[j + 1])),
+                make_float2(cu[j] * code_step(su[j]), cu[j + 1] * code_step(su[j + 1])),
+                make_float2(to_float(dy[j]), to_float(dy[j + 1])));
+            h[i + j] = m.gate.x;
+            h[i + j + 1] = m.gate.y;
+            acc += m.gate.x + m.gate.y;
+            const float up[2] = {m.up.x, m.up.y}, again[2] = {m.out.x, m.out.y};
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (full || t + NT * (i + j + k) < d) {
+                    gi[d + NT * (i + j + k)] = from_float<T>(up[k]);
+                    if (out)
+                        o[NT * (i + j + k)] = from_float<T>(again[k]);
+                }
         }
-    }
+    });
     const float m = row_sum<NT>(acc, red) / static_cast<float>(d);
     const float inv = std == 0.f ? 0.f : z / std;
+    for_groups<NT, V>(t, d, [&](int i, bool full) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (static_cast<int>(threadIdx.x) + NT * i < d) {      // the codes again, from L1 or L2
-            const float v = __ldg(q + NT * i) * code_step(__ldg(s + NT / 32 * i));
-            gi[NT * i] = from_float<T>(fmaf(-m, fmaf(inv, fmaf(z, std, v), 1.f), h[i]));
-        }
+        for (int j = i; j < i + 4; ++j)
+            if (full || t + NT * j < d) {      // the codes again, from L1 or L2
+                const float v = __ldg(q + NT * j) * code_step(__ldg(s + NT / 32 * j));
+                gi[NT * j] = from_float<T>(fmaf(-m, fmaf(inv, fmaf(z, std, v), 1.f), h[j]));
+            }
+    });
 }
 
 // ----------------------------------------- sparse, rows that no CTA holds
@@ -989,12 +1067,14 @@ template <class F> int with_jobs(int64_t jobs, F f) {
 // The CTA that holds a row of d elements one by one, as with_row_cta.
 template <int N> using Const = std::integral_constant<int, N>;
 template <class F> bool with_any_cta(int64_t d, int *rc, F f) {
-    if (d <= 1024)
-        *rc = f(Const<256>{}, Const<4>{});
+    if (d <= 512)
+        *rc = f(Const<64>{}, Const<8>{});
+    else if (d <= 1024)
+        *rc = f(Const<64>{}, Const<16>{});
     else if (d <= 2048)
-        *rc = f(Const<256>{}, Const<8>{});
+        *rc = f(Const<128>{}, Const<16>{});
     else if (d <= 4096)
-        *rc = f(Const<512>{}, Const<8>{});
+        *rc = f(Const<256>{}, Const<16>{});
     else if (d <= 8192)
         *rc = f(Const<512>{}, Const<16>{});
     else if (d <= 16384)

@@ -248,6 +248,16 @@ template <class T> __device__ __forceinline__ uint32_t top_as_float(uint32_t t) 
         return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(t))));
 }
 
+// f(i0, full) for the groups i0, i0 + 4, ... < V of four columns t + NT i each that
+// hold any; full: all of the group's columns are below d in the whole warp.
+template <int NT, int V, class F> __device__ __forceinline__ void for_groups(int t, int d, F f) {
+    const int last = t | 31;
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+        if (NT * i + t - (t & 31) < d)
+            f(i, last + NT * (i + 3) < d);
+}
+
 // ------------------------------------------------------- 8-bit block format
 
 constexpr int kBlock = 32;   // elements that share a scale
