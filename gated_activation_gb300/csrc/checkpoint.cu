@@ -169,6 +169,14 @@ ckpt_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__res
     }
 }
 
+// A code as the low byte of 2^23 + 128 + code, and two such as values.
+__device__ __forceinline__ uint32_t load_code(const int8_t *p) {
+    return (__ldg(reinterpret_cast<const uint8_t *>(p)) ^ 0x80u) | 0x4B000000u;
+}
+__device__ __forceinline__ float2 code_pair(uint32_t a, uint32_t b) {
+    return sub2(make_float2(__uint_as_float(a), __uint_as_float(b)), both(8388736.f));
+}
+
 template <class T, class Act, class I>
 __global__ void __launch_bounds__(kThreads)
 ckpt_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
@@ -185,6 +193,37 @@ ckpt_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__restr
     const int64_t r = row, b0 = static_cast<int64_t>(job - row * J) * U, c0 = b0 * kBlock + lane;
     const T *dy = grad + r * gs + c0;
     const int8_t *q = codes + r * 2 * d + c0;
+    if (c0 - lane + kBlock * U <= d) {
+        T y[U];
+        uint32_t g[U], u[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            y[i] = __ldg(dy + kBlock * i);
+            g[i] = load_code(q + kBlock * i);
+            u[i] = load_code(q + d + kBlock * i);
+        }
+        const float step = lane_step(scales + r * 2 * B, b0, B, lane);
+        T *gi = grad_in + r * 2 * d + c0, *o = out + r * d + c0;
+#pragma unroll
+        for (int i = 0; i < U; i += 2) {
+            const float2 sg = make_float2(__shfl_sync(0xFFFFFFFFu, step, i),
+                                          __shfl_sync(0xFFFFFFFFu, step, i + 1));
+            const float2 su = make_float2(__shfl_sync(0xFFFFFFFFu, step, U + i),
+                                          __shfl_sync(0xFFFFFFFFu, step, U + i + 1));
+            const GateGrad2 m = act_grad<Act>(mul2(code_pair(g[i], g[i + 1]), sg),
+                                              mul2(code_pair(u[i], u[i + 1]), su),
+                                              make_float2(to_float(y[i]), to_float(y[i + 1])));
+            gi[kBlock * i] = from_float<T>(m.gate.x);
+            gi[kBlock * (i + 1)] = from_float<T>(m.gate.y);
+            gi[d + kBlock * i] = from_float<T>(m.up.x);
+            gi[d + kBlock * (i + 1)] = from_float<T>(m.up.y);
+            if (out) {
+                o[kBlock * i] = from_float<T>(m.out.x);
+                o[kBlock * (i + 1)] = from_float<T>(m.out.y);
+            }
+        }
+        return;
+    }
     T yraw[U];
     int8_t qg[U], qu[U];
 #pragma unroll
@@ -446,7 +485,7 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
 // ..., V of them, in registers.
 
 template <class T, int NT, int V>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 1024 / NT)
 sparse_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                    float *__restrict__ std_out, const T *__restrict__ in, int d, int64_t rs,
                    int B, float z) {
@@ -457,6 +496,10 @@ sparse_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__r
     const int64_t r = blockIdx.x;
     const int t = threadIdx.x;
     const T *p = in + r * rs + t;
+    // the up half is read last: to L2 meanwhile
+    constexpr int kLine = 128 / sizeof(T);
+    for (int c = kLine * t; c < d; c += kLine * NT)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(in + r * rs + d + c));
     float g[V], acc = 0.f;
     for_groups<NT, V>(t, d, [&](int i, bool full) {
 #pragma unroll
@@ -515,7 +558,7 @@ sparse_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__r
 }
 
 template <class T, int NT, int V>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 1024 / NT)
 sparse_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
                     const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                     const float *__restrict__ std_in, int d, int64_t gs, int B, float z) {
