@@ -338,7 +338,8 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
     if (EDGES && edge >= 0) {
         we = to_float(__ldg(weight + edge));
         be = bias ? to_float(__ldg(bias + edge)) : 0.f;
-        next = to_float(__ldg(in + blockIdx.x * rs + edge));
+        if (blockIdx.x < rows)
+            next = to_float(__ldg(in + blockIdx.x * rs + edge));
     }
     int slot = 0;
     const float inv = 1.0f / static_cast<float>(d);
@@ -734,10 +735,10 @@ template <int SIZE, class F> bool with_forward_ring(int64_t nv, int *rc, F f) {
     return true;
 }
 
-// Calls f(integral constants TPR, V, S, CL) for the backward ring: the slots of
-// the 512 threads of an SM take up to 192 KB of shared memory.
+// Calls f(integral constants TPR, V, S, CL) for the backward ring.  Four slots are
+// enough: with six, 192 KB, 16384 x 2048 bf16 takes 42.1 us against 40.8.
 template <int SIZE, class F> bool with_backward_ring(int64_t nv, int *rc, F f) {
-    constexpr int S2 = SIZE == 2 ? 6 : 3;    // slots at two vectors per thread
+    constexpr int S2 = SIZE == 2 ? 4 : 3;    // slots at two vectors per thread
     constexpr Const<1> one{};
     if (nv <= 32)
         *rc = f(Const<32>{}, Const<1>{}, Const<S2>{}, one);

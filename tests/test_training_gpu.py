@@ -292,7 +292,10 @@ def _norm_case(t, d, dtype, wtype, seed, bias=True):
     return x, w, b, _randn(t, d, seed=seed + 5).to(dtype)
 
 
-NORM_SHAPES = SHAPES + [(700, 2048), (1000, 40), (320, 8192), (300, 1)]
+# and many rows: aligned and off a boundary, through every number of rows per CTA, and rows
+# that a cluster shares
+NORM_SHAPES = SHAPES + [(700, 2048), (1000, 40), (320, 8192), (300, 1), (5000, 301), (3000, 520),
+                        (1300, 2047), (1000, 4099), (650, 1036), (170, 20000), (170, 12345)]
 
 
 def _check_norm(ga, x, w, b, dy, dtype, eps=1e-5, xd=None, dyd=None):
@@ -464,15 +467,15 @@ def _everything(ga, x, z, nx, w, logits, ids, stream=None):
     for name in ("silu", "gelu"):
         forward, backward = _ops(ga, name)
         out, kept = forward(x, stream=stream)
-        got += [out, *kept[:2], *backward(dy.contiguous() if stream is None else dy, kept,
-                                          recompute=True, stream=stream)]
+        flat = dy.contiguous() if stream is None and dy.is_cuda else dy
+        got += [out, *kept[:2], *backward(flat, kept, recompute=True, stream=stream)]
     out, kept = ga.gelu_and_mul_sparse_checkpoint(x, z, stream=stream)
     got += [out, *kept, *ga.gelu_and_mul_sparse_backward(dy, kept, z, recompute=True, stream=stream),
             ga.checkpoint_values(kept, stream=stream)]
     norm = ga.layer_norm(nx, w, w, stream=stream)
     got += [*norm, *ga.layer_norm_backward(nx, nx, w, norm[1], norm[2], stream=stream)]
     kept = ga.moe_balance_loss(logits, ids, 0.5, stream=stream)
-    one = logits.new_ones(1, dtype=F32)
+    one = torch.ones(1, dtype=F32, device="cuda")
     return got + [*kept[:4], ga.moe_balance_loss_backward(one, logits, kept, stream=stream)]
 
 
@@ -521,6 +524,33 @@ def test_host_rows_in_place(ga):
     torch.cuda.synchronize()
     assert not out.is_cuda and torch.equal(out, want.cpu())
     assert torch.equal(kept.codes, wkept.codes.cpu())
+
+
+def test_everything_on_host_rows(ga):
+    # page-locked rows are read and written in place, to the same bits
+    args = _inputs(7)
+    want = _everything(ga, *args)
+    host = [a.cpu().pin_memory() if isinstance(a, torch.Tensor) else a for a in args]
+    got = _everything(ga, *host)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert not b.is_cuda and torch.equal(a.cpu(), b)
+
+
+def test_more_than_2_to_31_vectors(ga):
+    # rows of one vector, more of them than 32-bit indexes hold
+    m, d = (1 << 30) // 2 + 5, 8
+    x = torch.zeros((m, 2 * d), dtype=BF16, device="cuda")
+    x[-3:] = _gated(3, d, BF16, 8)
+    tail = x[-3:].clone()
+    out, kept = ga.silu_and_mul_checkpoint(x)
+    want, wkept = ga.silu_and_mul_checkpoint(tail)
+    assert torch.equal(out[-3:], want) and (out[:-3:1 << 20] == 0).all()
+    assert torch.equal(kept.codes[-3:], wkept.codes) and torch.equal(kept.scales[-3:], wkept.scales)
+    del x
+    assert torch.equal(ga.silu_and_mul_backward(out, kept)[-3:],
+                       ga.silu_and_mul_backward(out[-3:].clone(), wkept))
+    assert torch.equal(ga.checkpoint_values(kept)[-3:], ga.checkpoint_values(wkept))
 
 
 @pytest.mark.parametrize("d", [16384, 16385])
