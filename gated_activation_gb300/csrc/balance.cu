@@ -586,9 +586,11 @@ extern "C" int moe_balance_loss_backward(void *grad_logits, const float *grad_lo
     return with_type(dtype, [&](auto t) {
         return with_lanes(E, vec, [&](auto l, auto v, auto n) {
             using Elem = decltype(t);
-            // up to 4 CTAs per SM (its registers allow), all with the same number of rounds
+            // up to 4 CTAs per SM, as the registers of 16 logits per lane allow, or 8, all
+            // with the same number of rounds
             const int64_t rounds = ceil_div64(T, kThreads / l());
-            const int64_t grid = ceil_div64(rounds, ceil_div64(rounds, device_sm_count() * 4));
+            const int64_t most = device_sm_count() * (v() * n() > 8 ? 4 : 8);
+            const int64_t grid = ceil_div64(rounds, ceil_div64(rounds, most));
             return launched(launch_kernel(
                 balance_backward<Elem, l(), v(), n()>, dim3(static_cast<unsigned>(grid)),
                 dim3(kThreads), 0, stream, 1, as<Elem>(r[0]), as<const float>(r[1]),
