@@ -5,13 +5,13 @@
 // instructions per element: HBM bandwidth bounds it.  Per gate/up pair of a
 // 16-bit type the forward pass moves 4 + 2 bytes of rows and 2 + 1/16 of
 // checkpoint, the backward pass 2 (+ 2 with the recomputed output) + 4 and
-// the same 2 + 1/16.
+// the same 2 + 1/16.  Rates below are of GB300 and, in percent, of its copy
+// rate, 6.79 TB/s; inputs larger than L2 in turn, backward passes with the
+// recomputed output.
 //
-// Blocks: a block of the 8-bit format is 32 elements of one half.  The
-// any-layout kernels give a block of the gate half and the block of the up
-// half beside it to one warp, one element per lane, so every access of a warp
-// is one contiguous run whatever the alignment, and the block's largest
-// magnitude is one redux.
+// A block of the 8-bit format is 32 elements of one half.  Its largest
+// magnitude m = 1.f 2^E fixes k = E - 6 (or the next one, where 1.f would round
+// to 128), a code is v 2^-k rounded, and both powers of two are exact.
 #include <algorithm>
 
 #include "training.cuh"
@@ -102,8 +102,14 @@ template <class I> __device__ __forceinline__ I quotient(I n, I d, const FastDiv
 
 // ------------------------------------------------- elementwise, any layout
 //
-// A warp takes kAnyBlocks consecutive blocks of a row, one element of each per
-// lane; J = ceil(B / kAnyBlocks) such jobs make a row.
+// A warp takes kAnyBlocks consecutive blocks of a row of both halves, one element
+// of each per lane, so that every access of a warp is one contiguous run
+// whatever the alignment; J = ceil(B / kAnyBlocks) such jobs make a row.  Four
+// blocks of two halves are the eight largest magnitudes that one exchange of
+// lanes finds together (put_blocks).  The single bytes and half words that a
+// lane moves make instructions the bound: 16384 x 767 bf16 takes 28.4 us forward
+// (53%) and 30.5 us backward (61%), against 25.2 and 28.7 us at 768, where the
+// vectors below take 17.2 and 20.7.
 
 constexpr int kAnyBlocks = 4;
 
@@ -302,6 +308,14 @@ ckpt_values_any(T *__restrict__ values, const int8_t *__restrict__ codes,
 // four neighbouring lanes hold a block of each.  A row is 4 B slots of 8
 // elements, B blocks, so that lane groups and blocks coincide in every row;
 // the slots past d (a ragged last block) are empty.
+//
+// HBM bounds it: silu of 16384 x 768 bf16 takes 17.2 us forward (87%) and 20.7 us
+// backward (90%), of 4000 x 2048 fp32 18.4 us (92%) and 23.4 us (93%).  One slot
+// per thread and full occupancy hide the loads better than two per thread (20.8
+// and 24.6 us); the values, with nothing to compute, take four (2048 x 16384:
+// 31.5 us, 95%; one: 36.5 us).  Slots are found by a 32-bit multiplication while
+// they number fewer than 2^31: by a 64-bit division the two passes take 18.5
+// and 21.9 us.
 
 // Largest magnitude over the four lanes of a block, of both halves at once.
 template <class T>
@@ -482,10 +496,14 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
 // ------------------------------------------------------ sparse, any layout
 //
 // One CTA per row, one element per lane: warp w holds the blocks w, w + NT / 32,
-// ..., V of them, in registers.
+// ..., V of them, in registers.  Instructions and the row's two barriers bound
+// it: 2000 x 4097 bf16 takes 30.9 us forward (31%; 35.2 with registers for 1024
+// threads per SM instead of 1536) and 37.8 us backward (32%; with 1536: 46.2), 43.3 and
+// 76.6 us with the row read again for each pass, as the next section does.  Rows in
+// vectors take a third: 2000 x 4096 fp16 13.3 and 18.3 us.
 
 template <class T, int NT, int V>
-__global__ void __launch_bounds__(NT, 1024 / NT)
+__global__ void __launch_bounds__(NT, 1536 / NT)
 sparse_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                    float *__restrict__ std_out, const T *__restrict__ in, int d, int64_t rs,
                    int B, float z) {
@@ -623,46 +641,38 @@ sparse_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__res
 
 // ----------------------------------------- sparse, rows that no CTA holds
 
-// Sum over the CTA, the same bits in every thread; red holds kWarps floats
-// and may be used again after the next barrier.
-__device__ __forceinline__ float cta_sum(float v, float *red) {
-    v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0)
-        red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = red[threadIdx.x & (kWarps - 1)];
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1)
-        t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    return t;
-}
+constexpr int kWideThreads = 1024, kWideWarps = kWideThreads / 32;
 
-// One CTA per row; the gate is read again (from L1/L2) for each pass.
+// One CTA per row; the gate is read again (from L1/L2) for each pass.  100 x 40000
+// bf16: 40.1 us forward, 50.7 us backward (256 threads: 115.6 and 166.9): a row's
+// latency bounds so few of them.
 template <class T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kWideThreads)
 sparse_forward_wide(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                    float *__restrict__ std_out, const T *__restrict__ in, int64_t rows, int64_t d,
                    int64_t rs, int64_t B, float z) {
-    __shared__ float red[2][kWarps];
+    __shared__ float red[2][kWideWarps];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const T *g = in + r * rs;
         float acc = 0.f;
-        for (int64_t c = threadIdx.x; c < d; c += kThreads)
+#pragma unroll 4
+        for (int64_t c = threadIdx.x; c < d; c += kWideThreads)
             acc += to_float(g[c]);
-        const float mean = cta_sum(acc, red[0]) / static_cast<float>(d);
+        const float mean = row_sum<kWideThreads>(acc, red[0]) / static_cast<float>(d);
         acc = 0.f;
-        for (int64_t c = threadIdx.x; c < d; c += kThreads) {
+#pragma unroll 4
+        for (int64_t c = threadIdx.x; c < d; c += kWideThreads) {
             const float e = to_float(g[c]) - mean;
             acc = fmaf(e, e, acc);
         }
-        const float std = __fsqrt_rn(cta_sum(acc, red[1]) / static_cast<float>(d));
+        const float std = __fsqrt_rn(row_sum<kWideThreads>(acc, red[1]) / static_cast<float>(d));
         const float cutoff = fmaf(std, z, mean);
         if (threadIdx.x == 0)
             std_out[r] = std;
-        for (int64_t b = warp; b < B; b += kWarps) {
+        for (int64_t b = warp; b < B; b += kWideWarps) {
             const int64_t c = b * kBlock + lane;
             const bool ok = c < d;
             const float v = ok ? to_float(g[c]) - cutoff : 0.f;
@@ -676,12 +686,12 @@ sparse_forward_wide(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kWideThreads)
 sparse_backward_wide(T *__restrict__ grad_in, T *__restrict__ out, const T *__restrict__ grad,
                     const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                     const float *__restrict__ std_in, int64_t rows, int64_t d, int64_t gs,
                     int64_t B, float z) {
-    __shared__ float red[2][kWarps];
+    __shared__ float red[2][kWideWarps];
     pdl_wait();
     pdl_trigger();
     int k = 0;
@@ -692,7 +702,8 @@ sparse_backward_wide(T *__restrict__ grad_in, T *__restrict__ out, const T *__re
         const uint8_t *sc = scales + r * 2 * B;
         T *gi = grad_in + r * 2 * d;
         float acc = 0.f;
-        for (int64_t c = threadIdx.x; c < d; c += kThreads) {
+#pragma unroll 4
+        for (int64_t c = threadIdx.x; c < d; c += kWideThreads) {
             const float v = q[c] * code_step(sc[c / kBlock]);
             const float u = q[d + c] * code_step(sc[B + c / kBlock]);
             const float dy = to_float(grad[r * gs + c]);
@@ -702,8 +713,9 @@ sparse_backward_wide(T *__restrict__ grad_in, T *__restrict__ out, const T *__re
             if (out)
                 out[r * d + c] = from_float<T>(m.out.x);
         }
-        const float mean_h = cta_sum(acc, red[k]) / static_cast<float>(d);
-        for (int64_t c = threadIdx.x; c < d; c += kThreads) {
+        const float mean_h = row_sum<kWideThreads>(acc, red[k]) / static_cast<float>(d);
+#pragma unroll 4
+        for (int64_t c = threadIdx.x; c < d; c += kWideThreads) {
             const float v = q[c] * code_step(sc[c / kBlock]);
             const float u = q[d + c] * code_step(sc[B + c / kBlock]);
             const float dy = to_float(grad[r * gs + c]);
@@ -718,7 +730,10 @@ sparse_backward_wide(T *__restrict__ grad_in, T *__restrict__ out, const T *__re
 // One CTA per row, the row in registers: thread t holds the 8-element vectors
 // t, t + NT, ... (V of them) of both halves, so the gate is read once for its
 // statistics and its codes, and four neighbouring lanes hold a block.  All
-// loads are issued before the first sum.
+// loads are issued before the first sum.  The barriers of the statistics, at
+// which a CTA neither reads nor writes, keep it from the copy rate: 4000 x 4096 bf16
+// takes 22.6 us forward (86%) and 32.9 us backward (74%), 500 x 32768 31.9 and
+// 43.2 us, 8 x 8192 fp32 2.7 and 3.9 us (launch and latency).
 
 // The output and the codes of the 8 elements at column c of a row (nothing for
 // c >= d, but the lane takes part in its block's largest magnitudes).
@@ -877,7 +892,8 @@ sparse_backward_vec(T *__restrict__ grad_in, T *__restrict__ out, const T *__res
 // reach it through a ring of S shared-memory slots that cp.async fills S - 1
 // rows ahead, so that HBM keeps streaming while a row is summed and written.  A
 // thread copies just the vectors it will read itself: its own wait_group is
-// all the synchronization that the ring needs.
+// all the synchronization that the ring needs.  2048 x 16384 bf16: forward 49.5 us
+// (81%), backward 56.3 us (88%); takes_ring has the figures without it.
 
 template <class T, int NT, int V, int S>
 __global__ void __launch_bounds__(NT, 1024 / NT)
@@ -1151,15 +1167,17 @@ template <int MAX, class F> bool with_row_cta(int64_t nv, int *rc, F f) {
     return true;
 }
 
-// Rows of which one CTA of 1024 threads holds a single one, more of them than
-// SMs, take the ring.  Measured on GB300 at 2048 x 16384 bf16: forward 74.6 -> 60.5
-// us, backward 79.7 -> 69.1 us; narrower rows, of which an SM runs several
-// CTAs, are faster without it (2000 x 4096 fp16: forward 14.8 against 17.6 us).
+// Rows that fill a CTA of 1024 threads, the one that an SM then holds, take the
+// ring if there are more of them than SMs: 2048 x 16384 bf16 forward 49.5 against
+// 62.4 us, backward 56.3 against 76.3.  Of narrower rows an SM runs several CTAs,
+// which hide each other's barriers: 4000 x 8192 bf16 takes 75.3 us forward in the
+// ring and 50.2 without, backward 63.8 and 64.7.  The vectors of fp32 rows that
+// wide would not leave room for slots to fill ahead, and reach 91 to 94% without.
 bool takes_ring(int64_t T, int64_t nv, int64_t size) {
     return size == 2 && nv > 1024 && nv <= 2048 && T > device_sm_count();
 }
 
-constexpr int kForwardVpt = 1, kBackwardVpt = 1, kValuesVpt = 4;
+constexpr int kForwardVpt = 1, kBackwardVpt = 1, kValuesVpt = 4;   // slots per thread
 
 template <class Act>
 int forward(void *out, int8_t *codes, uint8_t *scales, const void *in, int64_t M, int64_t d,
@@ -1333,7 +1351,7 @@ extern "C" int gelu_and_mul_sparse_checkpoint(void *out, int8_t *codes, uint8_t 
         };
         if (T <= 0x7FFFFFFF && with_any_cta(d, &done, any))
             return done;
-        return launched(launch_kernel(sparse_forward_wide<E>, grid_of(T, 1), dim3(kThreads), 0,
+        return launched(launch_kernel(sparse_forward_wide<E>, grid_of(T, 1), dim3(kWideThreads), 0,
                                       stream, 1, as<E>(r[0]), as<int8_t>(r[1]), as<uint8_t>(r[2]),
                                       as<float>(r[3]), as<const E>(r[4]), T, d, row_stride, B,
                                       static_cast<float>(z)));
@@ -1397,7 +1415,7 @@ extern "C" int gelu_and_mul_sparse_backward(void *grad_in, void *out, const void
         };
         if (T <= 0x7FFFFFFF && with_any_cta(d, &done, any))
             return done;
-        return launched(launch_kernel(sparse_backward_wide<E>, grid_of(T, 1), dim3(kThreads), 0,
+        return launched(launch_kernel(sparse_backward_wide<E>, grid_of(T, 1), dim3(kWideThreads), 0,
                                       stream, 1, as<E>(r[0]), as<E>(r[1]), as<const E>(r[2]),
                                       as<const int8_t>(r[3]), as<const uint8_t>(r[4]),
                                       as<const float>(r[5]), T, d, grad_stride, B,

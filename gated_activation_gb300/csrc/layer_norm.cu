@@ -4,7 +4,8 @@
 // the backward pass reads two and writes one.  The parameters' gradients are
 // sums over the rows: each CTA adds up its own rows' share of every column,
 // and a second kernel adds the CTAs' shares in a fixed order, so results do
-// not depend on how the blocks were scheduled.
+// not depend on how the blocks were scheduled.  Rates below are of GB300 and, in
+// percent, of its copy rate, 6.79 TB/s; inputs larger than L2 in turn.
 #include <algorithm>
 
 #include "training.cuh"
@@ -35,9 +36,12 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2 *red) {
     return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
-// One CTA per row, the row read again (from L1/L2) for each pass.
-template <class T, class W>
-__global__ void __launch_bounds__(kThreads)
+// One CTA per row, the row read again (from L1/L2) for each pass, one element per
+// access: rows wider than the rings hold, and rows whose buffers lie at different
+// offsets.  1000 x 12345 fp16 takes 27.8 us forward and 53.1 us backward (rings:
+// 16.8 and 36.2), 100 x 40000 bf16 19.9 and 49.4 us (with 256 threads 59.1 and 103.8).
+template <class T, class W, int NT>
+__global__ void __launch_bounds__(NT)
 ln_forward_wide(T *__restrict__ out, float *__restrict__ mean_out, float *__restrict__ rstd_out,
                 const T *__restrict__ in, const W *__restrict__ weight, const W *__restrict__ bias,
                 int64_t rows, int64_t d, int64_t rs, float eps) {
@@ -47,11 +51,11 @@ ln_forward_wide(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const T *x = in + r * rs;
         float acc = 0.f;
-        for (int64_t c = threadIdx.x; c < d; c += kThreads)
+        for (int64_t c = threadIdx.x; c < d; c += NT)
             acc += to_float(x[c]);
         const float mean = cta_sum(acc, red[0]) / static_cast<float>(d);
         acc = 0.f;
-        for (int64_t c = threadIdx.x; c < d; c += kThreads) {
+        for (int64_t c = threadIdx.x; c < d; c += NT) {
             const float e = to_float(x[c]) - mean;
             acc = fmaf(e, e, acc);
         }
@@ -61,7 +65,7 @@ ln_forward_wide(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
             mean_out[r] = mean;
             rstd_out[r] = rstd;
         }
-        for (int64_t c = threadIdx.x; c < d; c += kThreads) {
+        for (int64_t c = threadIdx.x; c < d; c += NT) {
             const float h = (to_float(x[c]) - mean) * rstd;
             const float w = to_float(weight[c]);
             out[r * d + c] = from_float<T>(bias ? fmaf(h, w, to_float(bias[c])) : h * w);
@@ -69,8 +73,8 @@ ln_forward_wide(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
     }
 }
 
-template <class T, class W>
-__global__ void __launch_bounds__(kThreads)
+template <class T, class W, int NT>
+__global__ void __launch_bounds__(NT)
 ln_backward_rows(T *__restrict__ grad_in, const T *__restrict__ grad, const T *__restrict__ in,
                  const W *__restrict__ weight, const float *__restrict__ mean_in,
                  const float *__restrict__ rstd_in, int64_t rows, int64_t d, int64_t rs,
@@ -83,14 +87,14 @@ ln_backward_rows(T *__restrict__ grad_in, const T *__restrict__ grad, const T *_
         const T *x = in + r * rs, *dy = grad + r * gs;
         const float mean = mean_in[r], rstd = rstd_in[r];
         float2 s = make_float2(0.f, 0.f);
-        for (int64_t c = threadIdx.x; c < d; c += kThreads) {
+        for (int64_t c = threadIdx.x; c < d; c += NT) {
             const float g = to_float(dy[c]) * to_float(weight[c]);
             s.x += g;
             s.y = fmaf(g, (to_float(x[c]) - mean) * rstd, s.y);
         }
         s = cta_sum2(s, red[k]);
         const float ma = s.x / static_cast<float>(d), mb = s.y / static_cast<float>(d);
-        for (int64_t c = threadIdx.x; c < d; c += kThreads) {
+        for (int64_t c = threadIdx.x; c < d; c += NT) {
             const float g = to_float(dy[c]) * to_float(weight[c]);
             const float h = (to_float(x[c]) - mean) * rstd;
             grad_in[r * d + c] = from_float<T>(rstd * (g - ma - h * mb));
@@ -188,6 +192,11 @@ template <class W> __device__ __forceinline__ Vec8<W> load_params(const W *p) {
 // are `edges`, one per thread of the row's first warp, read a row ahead into a
 // register.  Rows of one kind of offset go to one CTA (its rows are a multiple
 // of kKinds apart), so that its threads keep their columns.
+//
+// 16384 x 2048 bf16 with fp32 parameters takes 22.7 us (87%), 4004 x 4096 fp32 22.4 us
+// (86%), 2048 x 16384 bf16 26.6 us (74%: the two barriers of a row that fills the
+// CTA).  EDGES costs tests and a dependent load per row: aligned rows through it
+// take 29.6 us at 16384 x 2048; 5000 x 2047 bf16 takes 13.1 us (46%).
 
 constexpr int kKinds = 8;      // rows this far apart have the same offset
 
@@ -404,7 +413,8 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
 // ------------------------------------------------- forward, wider rows
 //
 // One CTA per row, which its registers hold; the parameters through L1, which
-// the row's loads bypass.
+// the row's loads bypass.  800 x 32768 bf16: 29.7 us (52%), against 65.0 with the row
+// read again for each pass.
 
 template <class T, class W, int NT, int V>
 __global__ void __launch_bounds__(NT)
@@ -480,6 +490,12 @@ ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restr
 // Rows that one CTA's registers and ring cannot hold are split over a cluster
 // of CL CTAs, `chunk` columns each; the row's two sums are then joined through
 // distributed shared memory.
+//
+// With the second kernel, 16384 x 2048 bf16 with fp32 parameters takes 39.6 us (75%),
+// 4004 x 4096 fp32 35.5 us (82%), 2048 x 16384 bf16 44.0 us (67%), 800 x 32768 bf16
+// 49.7 us over clusters of two (140.0 with the row read again for each pass); 5000 x
+// 2047 bf16 24.7 us.  The shares, one per SM and column, are written and read
+// again: with few rows they are the larger part (16 x 2048: 4.8 us, two launches).
 
 constexpr int kBackThreads = 512;
 
@@ -704,18 +720,27 @@ template <class F> int with_types(int dtype, int param_dtype, F f) {
     });
 }
 
+template <int N> using Const = std::integral_constant<int, N>;
+
+// Calls f(integral constant NT): the threads of a row that no ring takes.  1024
+// for wide ones: 100 x 12345 fp16 forward 7.9 us against 19.2 with 256, 1000 of them 27.8
+// against 25.1, backward 53.1 against 57.2.
+template <class F> int with_threads(int64_t d, F f) {
+    return d > 8192 ? f(Const<1024>{}) : f(Const<kThreads>{});
+}
+
 // Shares of the parameters' gradients that the second kernel joins: one per
 // SM, or per row where there are fewer rows; a multiple of kKinds of them.
 int64_t shares(int64_t T) {
     return std::min<int64_t>(ceil_div64(T, kKinds), std::max(1, device_sm_count() / kKinds)) * kKinds;
 }
 
-template <int N> using Const = std::integral_constant<int, N>;
-
 // Calls f(integral constants NT, V, S) for the forward ring over rows of nv
-// vectors, 1024 threads per SM; false when it holds no such row.
+// vectors, 1024 threads per SM; false when it holds no such row.  Two slots, one
+// row ahead, are enough: with four 16384 x 2048 bf16 takes 23.5 us against 22.7,
+// 16384 x 512 7.85 against 7.12 (the first rows reach the SM as one burst).
 template <int SIZE, class F> bool with_forward_ring(int64_t nv, int *rc, F f) {
-    constexpr int S = SIZE == 2 ? 4 : 3;
+    constexpr int S = 2;
     if (nv <= 32)
         *rc = f(Const<32>{}, Const<1>{}, Const<S>{});
     else if (nv <= 64)
@@ -735,10 +760,12 @@ template <int SIZE, class F> bool with_forward_ring(int64_t nv, int *rc, F f) {
     return true;
 }
 
-// Calls f(integral constants TPR, V, S, CL) for the backward ring.  Four slots are
-// enough: with six, 192 KB, 16384 x 2048 bf16 takes 42.1 us against 40.8.
+// Calls f(integral constants TPR, V, S, CL) for the backward ring.  Two slots are
+// enough here, too: with six, 192 KB, 16384 x 2048 bf16 takes 42.1 us, with four 40.5,
+// with two 39.6.  At four vectors per thread the CTA holds one row, and three are
+// better: 2048 x 16384 bf16 44.0 us against 44.5.
 template <int SIZE, class F> bool with_backward_ring(int64_t nv, int *rc, F f) {
-    constexpr int S2 = SIZE == 2 ? 4 : 3;    // slots at two vectors per thread
+    constexpr int S2 = 2;    // slots at two vectors per thread
     constexpr Const<1> one{};
     if (nv <= 32)
         *rc = f(Const<32>{}, Const<1>{}, Const<S2>{}, one);
@@ -835,11 +862,12 @@ extern "C" int layer_norm(void *out, float *mean, float *rstd, const void *in, c
             with_forward_ring<sizeof(E)>(vectors_of(d), &done, ring(std::true_type{})))
             return done;
         const int64_t grid = std::min<int64_t>(T, int64_t(device_sm_count()) * 64);
-        return launched(launch_kernel(ln_forward_wide<E, W>, dim3(static_cast<unsigned>(grid)),
-                                      dim3(kThreads), 0, stream, 1, as<E>(r[0]), as<float>(r[1]),
-                                      as<float>(r[2]), as<const E>(r[3]), as<const W>(r[4]),
-                                      as<const W>(r[5]), T, d, row_stride,
-                                      static_cast<float>(eps)));
+        return with_threads(d, [&](auto nt) {
+            return launched(launch_kernel(
+                ln_forward_wide<E, W, nt()>, dim3(static_cast<unsigned>(grid)), dim3(nt()), 0,
+                stream, 1, as<E>(r[0]), as<float>(r[1]), as<float>(r[2]), as<const E>(r[3]),
+                as<const W>(r[4]), as<const W>(r[5]), T, d, row_stride, static_cast<float>(eps)));
+        });
     });
 }
 
@@ -914,10 +942,13 @@ extern "C" int layer_norm_backward(void *grad_in, float *grad_weight, float *gra
                 with_backward_ring<sizeof(E)>(vectors_of(d), &done, ring(std::true_type{})))
                 return done;
             const int64_t grid = std::min<int64_t>(T, int64_t(device_sm_count()) * 64);
-            done = launched(launch_kernel(
-                ln_backward_rows<E, W>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
-                stream, 1, as<E>(r[0]), as<const E>(r[4]), as<const E>(r[5]), as<const W>(r[6]),
-                as<const float>(r[7]), as<const float>(r[8]), T, d, row_stride, grad_stride));
+            done = with_threads(d, [&](auto nt) {
+                return launched(launch_kernel(
+                    ln_backward_rows<E, W, nt()>, dim3(static_cast<unsigned>(grid)), dim3(nt()),
+                    0, stream, 1, as<E>(r[0]), as<const E>(r[4]), as<const E>(r[5]),
+                    as<const W>(r[6]), as<const float>(r[7]), as<const float>(r[8]), T, d,
+                    row_stride, grad_stride));
+            });
             if (done != GATED_ACT_OK)
                 return done;
             const int64_t per = ceil_div64(T, shares(T));
