@@ -124,36 +124,55 @@ struct Ids {
     }
 };
 
+// Nonzero for a live token t of those before `end`.
+__device__ __forceinline__ uint8_t live_at(const uint8_t *live, uint32_t t, uint32_t end) {
+    return t >= end ? uint8_t(0) : live ? __ldg(live + t) : uint8_t(1);
+}
+
+constexpr int kIdLoads = 4;               // ids of a thread on their way together
+
 // Sums of the tokens [t0, t1) into shared memory: sums [kSumRows][E], of which
 // row r holds every kSumRows-th warp's, hist [E + 1] counts and live tokens.
 // NT threads; ends with a barrier.
 template <class T, int NT, int L, int V, int N>
 __device__ __forceinline__ void sum_tokens(float *sums, int *hist, const T *logits, Ids ids,
-                                           const uint8_t *live, int64_t t0, int64_t t1, int E,
+                                           const uint8_t *live, uint32_t t0, uint32_t t1, int E,
                                            int k, int64_t ls) {
     constexpr int kTokens = 32 / L;       // tokens of a warp at a time
     constexpr int kWarps = NT / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int part = lane / L, sub = lane % L;
     using R = Row<T, L, V, N>;
-    // two tokens on their way
+    // two tokens on their way, and whether the two after them are live
     Raw<T, L, V, N> raw[2];
-    bool on[2];
-    const auto fetch = [&](int64_t t, int slot) {
-        on[slot] = t + part < t1 && (!live || live[t + part]);
+    uint8_t on[2], next[2];
+    constexpr uint32_t step = kWarps * kTokens;
+    const auto fetch = [&](uint32_t t, int slot) {
+        on[slot] = next[slot];
         raw[slot].load(logits + (t + part) * ls, on[slot] ? E : 0, sub);
+        next[slot] = live_at(live, t + part + 2 * step, t1);
     };
-    const int64_t step = kWarps * kTokens;
-    int64_t t = t0 + warp * kTokens;
+    uint32_t t = t0 + warp * kTokens;
+    next[0] = live_at(live, t + part, t1);
+    next[1] = live_at(live, t + part + step, t1);
     fetch(t, 0);
     fetch(t + step, 1);
     // the counts, while the first tokens arrive
-    const int64_t first = t0 * k, n = (t1 - t0) * k;
-#pragma unroll 4
-    for (int64_t j = threadIdx.x; j < n; j += NT) {
-        const int64_t e = ids.at(first + j);
-        if (e >= 0 && e < E && (!live || live[t0 + static_cast<uint32_t>(j) / static_cast<uint32_t>(k)]))
-            atomicAdd(hist + e, 1);
+    const uint32_t kn = static_cast<uint32_t>(k), n = (t1 - t0) * kn;
+    const int64_t first = static_cast<int64_t>(t0) * k;
+    for (uint32_t j = threadIdx.x; j < n; j += NT * kIdLoads) {
+        int64_t e[kIdLoads];
+        uint8_t in[kIdLoads];
+#pragma unroll
+        for (int i = 0; i < kIdLoads; ++i) {
+            const uint32_t at = j + i * NT;
+            e[i] = at < n ? ids.at(first + at) : -1;
+            in[i] = at < n ? live_at(live, t0 + at / kn, t1) : uint8_t(0);
+        }
+#pragma unroll
+        for (int i = 0; i < kIdLoads; ++i)
+            if (in[i] && e[i] >= 0 && e[i] < E)
+                atomicAdd(hist + e[i], 1);
     }
     float2 acc2[R::P];
 #pragma unroll
@@ -164,7 +183,7 @@ __device__ __forceinline__ void sum_tokens(float *sums, int *hist, const T *logi
     // live adds zeros
     const auto take = [&](int slot) {
         const R p(raw[slot], on[slot] ? E : 0, sub);
-        mine += on[slot] && sub == 0;
+        mine += on[slot] != 0 && sub == 0;
         fetch(t + 2 * step, slot);
 #pragma unroll
         for (int i = 0; i < R::P; ++i)
@@ -275,7 +294,7 @@ balance_cluster(float *__restrict__ loss, int32_t *__restrict__ counts,
     pdl_wait();
     pdl_trigger();
     const uint32_t rank = cluster_rank();
-    const int64_t t0 = min(T_, rank * per), t1 = min(T_, t0 + per);
+    const uint32_t t0 = min(T_, rank * per), t1 = min(T_, t0 + per);
     sum_tokens<T, kThreads, L, V, N>(sums, hist, logits, ids, live, t0, t1, E, k, ls);
     for (int e = threadIdx.x; e < E; e += kThreads)
         sums[e] = rows_sum(sums, E, e);                       // only this thread reads column e
@@ -319,7 +338,7 @@ balance_tokens(float *__restrict__ part_p, int32_t *__restrict__ part_c,
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    const int64_t t0 = min(T_, blockIdx.x * per), t1 = min(T_, t0 + per);
+    const uint32_t t0 = min(T_, blockIdx.x * per), t1 = min(T_, t0 + per);
     sum_tokens<T, NT, L, V, N>(sums, hist, logits, ids, live, t0, t1, E, k, ls);
     const int64_t G = gridDim.x;
     for (int e = threadIdx.x; e <= E; e += NT) {
@@ -332,7 +351,7 @@ balance_tokens(float *__restrict__ part_p, int32_t *__restrict__ part_c,
 // Joins the G sums of every expert, G <= 32 kJoinLoads: a warp takes an expert.
 constexpr int kJoinThreads = 512;
 constexpr int kJoinLoads = 8;
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 1)
 balance_join(float *__restrict__ loss, int32_t *__restrict__ counts, int32_t *__restrict__ tokens,
              float *__restrict__ mean_p, const float *__restrict__ part_p,
              const int32_t *__restrict__ part_c, int G, int E, float k, float coef) {

@@ -102,8 +102,12 @@ ln_backward_rows(T *__restrict__ grad_in, const T *__restrict__ grad, const T *_
     }
 }
 
+// Floats from one share of the d columns to the next: whole 16-byte vectors.
+// What lies past column d is not written, and summed into no result.
+__host__ __device__ constexpr int64_t share_width(int64_t d) { return (d + 3) / 4 * 4; }
+
 // Columns' shares of the rows [y * per, (y + 1) * per), y = blockIdx.y: one
-// column per thread.  part: [2][gridDim.y][d].
+// column per thread.  part: [2][gridDim.y][share_width(d)].
 template <class T>
 __global__ void __launch_bounds__(kThreads)
 ln_backward_columns(float *__restrict__ part, const T *__restrict__ grad,
@@ -122,14 +126,14 @@ ln_backward_columns(float *__restrict__ part, const T *__restrict__ grad,
         w = fmaf(dy, (to_float(in[r * rs + c]) - mean_in[r]) * rstd_in[r], w);
         b += dy;
     }
-    part[blockIdx.y * d + c] = w;
-    part[(gridDim.y + blockIdx.y) * d + c] = b;
+    part[blockIdx.y * share_width(d) + c] = w;
+    part[(gridDim.y + blockIdx.y) * share_width(d) + c] = b;
 }
 
 // Adds the n shares of every column, of the weight (blockIdx.y = 0) or the bias:
 // a warp reads 128 columns of every kReduceWarps-th share, four per lane.
-constexpr int kReduceWarps = 16, kReduceColumns = 128;
-__global__ void __launch_bounds__(32 * kReduceWarps)
+constexpr int kReduceWarps = 16, kReduceLoads = 10, kReduceColumns = 128;
+__global__ void __launch_bounds__(32 * kReduceWarps, 1)
 ln_backward_reduce(float *__restrict__ grad_weight, float *__restrict__ grad_bias,
                    const float *__restrict__ part, int64_t n, int64_t d) {
     __shared__ float4 sum[kReduceWarps][32];
@@ -137,25 +141,25 @@ ln_backward_reduce(float *__restrict__ grad_weight, float *__restrict__ grad_bia
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * kReduceColumns + 4 * lane;
-    const float *p = part + blockIdx.y * n * d;
+    const int64_t ps = share_width(d);
+    const float *p = part + blockIdx.y * n * ps;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (d % 4 == 0) {
-        if (c < d)
-#pragma unroll 10
-            for (int64_t i = warp; i < n; i += kReduceWarps) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + i * d + c));
-                s.x += v.x;
-                s.y += v.y;
-                s.z += v.z;
-                s.w += v.w;
-            }
-    } else {
-        for (int64_t i = warp; i < n; i += kReduceWarps)
+    if (c < d)
+        for (int64_t i = warp; i < n; i += kReduceWarps * kReduceLoads) {
+            float4 v[kReduceLoads];       // on their way together; past the last, that one
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c + j < d)
-                    (&s.x)[j] += __ldcg(p + i * d + c + j);
-    }
+            for (int j = 0; j < kReduceLoads; ++j)
+                v[j] = __ldcg(reinterpret_cast<const float4 *>(
+                    p + min(i + j * kReduceWarps, n - 1) * ps + c));
+#pragma unroll
+            for (int j = 0; j < kReduceLoads; ++j)
+                if (i + j * kReduceWarps < n) {
+                    s.x += v[j].x;
+                    s.y += v[j].y;
+                    s.z += v[j].z;
+                    s.w += v[j].w;
+                }
+        }
     sum[warp][lane] = s;
     __syncthreads();
     const int64_t to = static_cast<int64_t>(blockIdx.x) * kReduceColumns + threadIdx.x;
@@ -650,7 +654,7 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
     if constexpr (CL > 1)
         cluster_barrier();      // no CTA leaves while another writes to it
     // columns' shares: over the CTA's rows in shared memory, group by group
-    float *pw = part + share * width, *pb = pw + count * width;
+    float *pw = part + share * share_width(width), *pb = pw + count * share_width(width);
     if constexpr (R == 1 && !EDGES) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -874,7 +878,7 @@ extern "C" int layer_norm(void *out, float *mean, float *rstd, const void *in, c
 extern "C" size_t layer_norm_backward_workspace_bytes(int64_t T, int64_t d) {
     if (T <= 0 || d <= 0 || d > gact::kMaxWidth)
         return 16;
-    return static_cast<size_t>(std::max<int64_t>(16, gact::shares(T) * d * 8));
+    return static_cast<size_t>(std::max<int64_t>(16, gact::shares(T) * gact::share_width(d) * 8));
 }
 
 extern "C" int layer_norm_backward(void *grad_in, float *grad_weight, float *grad_bias,
