@@ -892,8 +892,8 @@ sparse_backward_vec(T *__restrict__ grad_in, T *__restrict__ out, const T *__res
 // reach it through a ring of S shared-memory slots that cp.async fills S - 1
 // rows ahead, so that HBM keeps streaming while a row is summed and written.  A
 // thread copies just the vectors it will read itself: its own wait_group is
-// all the synchronization that the ring needs.  2048 x 16384 bf16: forward 49.5 us
-// (81%), backward 56.3 us (88%); takes_ring has the figures without it.
+// all the synchronization that the ring needs.  2048 x 16384 bf16: forward 48.5 us
+// (82%), backward 56.3 us (88%); with_ring_cta has the figures without it.
 
 template <class T, int NT, int V, int S>
 __global__ void __launch_bounds__(NT, 1024 / NT)
@@ -1167,14 +1167,35 @@ template <int MAX, class F> bool with_row_cta(int64_t nv, int *rc, F f) {
     return true;
 }
 
-// Rows that fill a CTA of 1024 threads, the one that an SM then holds, take the
-// ring if there are more of them than SMs: 2048 x 16384 bf16 forward 49.5 against
-// 62.4 us, backward 56.3 against 76.3.  Of narrower rows an SM runs several CTAs,
-// which hide each other's barriers: 4000 x 8192 bf16 takes 75.3 us forward in the
-// ring and 50.2 without, backward 63.8 and 64.7.  The vectors of fp32 rows that
-// wide would not leave room for slots to fill ahead, and reach 91 to 94% without.
-bool takes_ring(int64_t T, int64_t nv, int64_t size) {
-    return size == 2 && nv > 1024 && nv <= 2048 && T > device_sm_count();
+// Persistent CTAs, 1024 threads per SM.
+dim3 ring_grid(int nt) { return dim3(static_cast<unsigned>(device_sm_count() * (1024 / nt))); }
+
+// Calls f(integral constant NT) for the ring over T rows of nv vectors, two per
+// thread; false for rows that do not take it: those of more or fewer vectors, and
+// batches of no more than two rows per CTA, where filling the ring costs what it
+// hides (608 x 8192 bf16 forward 10.6 us in the ring and 9.9 without, 450 x 8192 backward
+// 10.6 and 9.7; 1216 x 8192 16.6 and 17.7, 19.8 and 21.7).  In the ring and without, bf16:
+//                  8000 x 2048   4000 x 4096   4000 x 8192   2048 x 16384
+//   forward, us    22.8  25.1    23.2  22.5    44.8  50.2    48.5  62.4
+//   backward, us   29.7  31.0    29.9  32.7    55.3  64.4    56.4  76.3
+// The forward pass leaves out its one loss.  It has two slots, with three 2048 x 16384
+// takes 49.0 us; the backward pass three, with two 65.3.  fp32 rows that wide would not
+// leave room for slots to fill ahead, and reach 91 to 94% of the copy rate without.
+template <bool FORWARD, class F> bool with_ring_cta(int64_t T, int64_t nv, int *rc, F f) {
+    if (nv <= 128 || nv > 2048 || (FORWARD && nv > 256 && nv <= 512))
+        return false;
+    const int nt = nv <= 256 ? 128 : nv <= 512 ? 256 : nv <= 1024 ? 512 : 1024;
+    if (T <= int64_t(2) * device_sm_count() * (1024 / nt))
+        return false;
+    if (nt == 128)
+        *rc = f(Const<128>{});
+    else if (nt == 512)
+        *rc = f(Const<512>{});
+    else if (nt == 1024)
+        *rc = f(Const<1024>{});
+    else if constexpr (!FORWARD)
+        *rc = f(Const<256>{});
+    return true;
 }
 
 constexpr int kForwardVpt = 1, kBackwardVpt = 1, kValuesVpt = 4;   // slots per thread
@@ -1327,19 +1348,22 @@ extern "C" int gelu_and_mul_sparse_checkpoint(void *out, int8_t *codes, uint8_t 
                 static_cast<float>(z)));
         };
         int done;
-        if constexpr (sizeof(E) == 2)
-            if (vec && takes_ring(T, d / 8, sizeof(E))) {
-                constexpr int kSlots = 3;
-                constexpr size_t smem = kSlots * 2 * 1024 * 16 * sizeof(E);
-                const auto kernel = sparse_forward_ring<E, 1024, 2, kSlots>;
+        if constexpr (sizeof(E) == 2) {
+            const auto ring = [&](auto nt) {
+                constexpr int kSlots = 2;
+                constexpr size_t smem = kSlots * 2 * nt() * 16 * sizeof(E);
+                const auto kernel = sparse_forward_ring<E, nt(), 2, kSlots>;
                 const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
                 if (e != cudaSuccess)
                     return cuda_status(e);
                 return launched(launch_kernel(
-                    kernel, dim3(device_sm_count()), dim3(1024), smem, stream, 1, as<E>(r[0]), as<int8_t>(r[1]), as<uint8_t>(r[2]),
-                    as<float>(r[3]), as<const E>(r[4]), T, static_cast<int>(d), row_stride,
-                    static_cast<int>(B), static_cast<float>(z)));
-            }
+                    kernel, ring_grid(nt()), dim3(nt()), smem, stream, 1, as<E>(r[0]),
+                    as<int8_t>(r[1]), as<uint8_t>(r[2]), as<float>(r[3]), as<const E>(r[4]), T,
+                    static_cast<int>(d), row_stride, static_cast<int>(B), static_cast<float>(z)));
+            };
+            if (vec && with_ring_cta<true>(T, d / 8, &done, ring))
+                return done;
+        }
         if (vec && with_row_cta<4>(d / 8, &done, go))
             return done;
         const auto any = [&](auto nt, auto v) {
@@ -1389,19 +1413,23 @@ extern "C" int gelu_and_mul_sparse_backward(void *grad_in, void *out, const void
                 static_cast<int>(B), static_cast<float>(z)));
         };
         int done;
-        if constexpr (sizeof(E) == 2)
-            if (vec && takes_ring(T, d / 8, sizeof(E))) {
+        if constexpr (sizeof(E) == 2) {
+            const auto ring = [&](auto nt) {
                 constexpr int kSlots = 3;
-                constexpr size_t smem = kSlots * 2 * 1024 * (8 * sizeof(E) + 16);
-                const auto kernel = sparse_backward_ring<E, 1024, 2, kSlots>;
+                constexpr size_t smem = kSlots * 2 * nt() * (8 * sizeof(E) + 16);
+                const auto kernel = sparse_backward_ring<E, nt(), 2, kSlots>;
                 const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
                 if (e != cudaSuccess)
                     return cuda_status(e);
                 return launched(launch_kernel(
-                    kernel, dim3(device_sm_count()), dim3(1024), smem, stream, 1, as<E>(r[0]), as<E>(r[1]), as<const E>(r[2]),
-                    as<const int8_t>(r[3]), as<const uint8_t>(r[4]), as<const float>(r[5]), T,
-                    static_cast<int>(d), grad_stride, static_cast<int>(B), static_cast<float>(z)));
-            }
+                    kernel, ring_grid(nt()), dim3(nt()), smem, stream, 1, as<E>(r[0]),
+                    as<E>(r[1]), as<const E>(r[2]), as<const int8_t>(r[3]), as<const uint8_t>(r[4]),
+                    as<const float>(r[5]), T, static_cast<int>(d), grad_stride,
+                    static_cast<int>(B), static_cast<float>(z)));
+            };
+            if (vec && with_ring_cta<false>(T, d / 8, &done, ring))
+                return done;
+        }
         // fp32 rows of more than 16384 elements would spill: element by element they take
         // 49.8 us at 300 x 32768 against 69.4, at 2048 x 16384 the vectors 94.5 against 141.4
         if (vec && with_row_cta<sizeof(E) == 2 ? 4 : 2>(d / 8, &done, go))

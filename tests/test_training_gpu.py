@@ -214,6 +214,27 @@ def test_sparse_step(ga, m, d, z, dtype):
     assert torch.equal(ga.gelu_and_mul_sparse_backward(dy.cuda(), kept, z), grad)
 
 
+# more rows of each width than two per CTA of the GPU, and not a multiple of its CTAs
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("m,d", [(2437, 1032), (2501, 2048), (1219, 2056), (1243, 4096),
+                                 (613, 4104), (611, 8192), (307, 8200), (311, 16384)])
+def test_sparse_long_batches(ga, m, d, dtype):
+    x = _gated(m, d, dtype, d + m, pad=8)[:, :2 * d]
+    out, kept = ga.gelu_and_mul_sparse_checkpoint(x, W.Z95)
+    _check_sparse_forward(x.double().cpu(), d, W.Z95, dtype, out, kept)
+    dy = _randn(m, d, seed=m).to(dtype)
+    want = R.sparse_backward(R.values(kept.codes, kept.scales), dy.double(),
+                             kept.std.double().cpu(), W.Z95)
+    grad, again = ga.gelu_and_mul_sparse_backward(_strided(dy, 8, 0), kept, W.Z95, recompute=True)
+    R.check(grad, *want["grad"], dtype, "grad")
+    R.check(again, *want["out"], dtype, "recomputed out")
+    # a row's results are its own, whichever CTA takes it
+    for rows in (slice(0, 1), slice(m - 1, m), slice(m // 2, m // 2 + 1)):
+        part = type(kept)(*(t[rows] for t in kept))
+        alone = ga.gelu_and_mul_sparse_backward(dy[rows].cuda(), part, W.Z95)
+        R.check(alone, *(t[rows] for t in want["grad"]), dtype, "grad of a row")
+
+
 @pytest.mark.parametrize("d", [64, 45, 2048])
 def test_sparse_constant_and_masked_rows(ga, d):
     # constant gates (std = 0): nothing passes, gradients are 0; gradients that are not finite
