@@ -3,12 +3,12 @@
 //
 // The forward pass reads the logits and the chosen ids once, the backward
 // pass reads the logits again (a softmax is recomputed in registers rather
-// than stored) and writes their gradient.  65536 x 128 bf16, k = 8, takes 12.0 us
-// forward and 9.0 us backward on GB300 (26% and 55% of the copy rate, 6.79 TB/s):
+// than stored) and writes their gradient.  65536 x 128 bf16, k = 8, takes 11.2 us
+// forward and 8.9 us backward on GB300 (28% and 55% of the copy rate, 6.79 TB/s):
 // per pair of logits two exponentials and about thirty instructions, and of a
 // token the two exchanges between its lanes, bound it before HBM does, and the
-// second launch of the forward pass adds 2 us.  Of 64 tokens both take the latency
-// of a launch, 3.3 and 1.8 us.
+// second launch of the forward pass adds 2.5 us, the counts 1 us.  Of 64 tokens both
+// take the latency of a launch, 3.4 and 1.9 us.
 //
 // Tokens: L lanes share a token, each holding V groups of kLane elements of
 // its logits (rows in 16-byte vectors: 8 consecutive elements per group; any

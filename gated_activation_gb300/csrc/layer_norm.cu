@@ -38,8 +38,8 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2 *red) {
 
 // One CTA per row, the row read again (from L1/L2) for each pass, one element per
 // access: rows wider than the rings hold, and rows whose buffers lie at different
-// offsets.  1000 x 12345 fp16 takes 27.8 us forward and 53.1 us backward (rings:
-// 16.8 and 36.2), 100 x 40000 bf16 19.9 and 49.4 us (with 256 threads 59.1 and 103.8).
+// offsets.  1000 x 12345 fp16 takes 27.8 us forward and 53.1 us backward (rings: 16.8
+// and 33.0), 100 x 40000 bf16 19.9 and 49 us (with 256 threads 59.1 and 104).
 template <class T, class W, int NT>
 __global__ void __launch_bounds__(NT)
 ln_forward_wide(T *__restrict__ out, float *__restrict__ mean_out, float *__restrict__ rstd_out,
@@ -499,11 +499,11 @@ ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restr
 // of CL CTAs, `chunk` columns each; the row's two sums are then joined through
 // distributed shared memory.
 //
-// With the second kernel, 16384 x 2048 bf16 with fp32 parameters takes 39.6 us (75%),
-// 4004 x 4096 fp32 35.5 us (82%), 2048 x 16384 bf16 44.0 us (67%), 800 x 32768 bf16
-// 49.7 us over clusters of two (140.0 with the row read again for each pass); 5000 x
-// 2047 bf16 24.7 us.  The shares, one per SM and column, are written and read
-// again: with few rows they are the larger part (16 x 2048: 4.8 us, two launches).
+// With the second kernel, 16384 x 2048 bf16 with fp32 parameters takes 37.7 us (79%),
+// 4004 x 4096 fp32 33.6 us (86%), 2048 x 16384 bf16 42.9 us (69%), 800 x 32768 bf16
+// 49.5 us over clusters of two (140.0 with the row read again for each pass); 5000 x
+// 2047 bf16 22.8 us.  The shares, one per SM and column, are written and read
+// again: with few rows they are the larger part (16 x 2048: 4.9 us, two launches).
 
 constexpr int kBackThreads = 512;
 
@@ -770,8 +770,8 @@ template <int SIZE, class F> bool with_forward_ring(int64_t nv, int *rc, F f) {
 
 // Calls f(integral constants TPR, V, S, CL) for the backward ring.  Two slots are
 // enough here, too: with six, 192 KB, 16384 x 2048 bf16 takes 42.1 us, with four 40.5,
-// with two 39.6.  At four vectors per thread the CTA holds one row, and three are
-// better: 2048 x 16384 bf16 44.0 us against 44.5.
+// with two 39.6 (the second kernel took 2 us more then than now).  At four vectors per thread the CTA holds one row, and three are
+// better: 2048 x 16384 bf16 44.0 us against 44.5 (likewise).
 template <int SIZE, class F> bool with_backward_ring(int64_t nv, int *rc, F f) {
     constexpr int S2 = 2;    // slots at two vectors per thread
     constexpr Const<1> one{};
