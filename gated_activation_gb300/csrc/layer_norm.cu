@@ -497,7 +497,7 @@ ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restr
 //   rstd (g - A - h B) = dy (w rstd) + (x - mean) (-B rstd^2) - A rstd.
 // Rows that one CTA's registers and ring cannot hold are split over a cluster
 // of CL CTAs, `chunk` columns each; the row's two sums are then joined through
-// distributed shared memory.
+// distributed shared memory, after a barrier that every CTA has started.
 //
 // With the second kernel, 16384 x 2048 bf16 with fp32 parameters takes 37.7 us (79%),
 // 4004 x 4096 fp32 33.6 us (86%), 2048 x 16384 bf16 42.9 us (69%), 800 x 32768 bf16
@@ -517,6 +517,14 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// A CTA's shared memory may be written by its peers once it has started: each says so on
+// entry, and waits for the others before it first writes to them.
+__device__ __forceinline__ void cluster_started() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 template <class T, class W, int TPR, int V, int S, int CL, bool EDGES>
 __global__ void __launch_bounds__(kBackThreads, 1)
@@ -529,6 +537,8 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
     extern __shared__ __align__(16) uint4 slots[];
     __shared__ float2 red[2][NT / 32];
     __shared__ float2 peers[2][CL];
+    if constexpr (CL > 1)
+        cluster_started();
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
     // this CTA's columns: d of them from `from` on
     const int rank = CL == 1 ? 0 : blockIdx.x % CL, from = rank * chunk;
@@ -577,6 +587,10 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
     int slot = 0, k = 0;
     float mean = first < rows ? mean_in[first] : 0.f, rstd = first < rows ? rstd_in[first] : 0.f;
     const float inv = 1.0f / static_cast<float>(width);
+    if constexpr (CL > 1) {
+        __syncwarp();
+        cluster_wait_started();      // the first rows are on their way
+    }
     for (int64_t r = first; r < rows; r += G, k ^= 1) {
         // the slot read in the round before: this thread is done with it
         fetch(r + (S - 1) * G, slot == 0 ? S - 1 : slot - 1);

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from tests.gpu_util import require_gpu
-from tests.test_training_gpu import DTYPES, _check_balance, _randn
+from tests.test_training_gpu import (BF16, DTYPES, F32, _check_balance, _check_norm, _norm_case,
+                                     _randn)
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +30,25 @@ def test_balance_equal_counts_have_no_gradient(ga, t, e, dtype):
     assert (grad == 0).all()
     kept, grad = _check_balance(ga, logits, ids, None, coef=0.25)
     assert (grad == 0).all() and abs(kept.loss.item() - 0.25) < 1e-5
+
+
+# ---------------------------------------------------------------- layer norm
+
+# rows that clusters of two and four share: fewer and more of them than clusters on the GPU
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("t,d", [(1, 8200), (3, 16384), (200, 9000), (90, 16400), (1, 24576),
+                                 (170, 32768)])
+def test_layer_norm_rows_that_a_cluster_shares(ga, t, d, dtype):
+    for wtype, bias in ((dtype, True), (F32, False)):
+        _check_norm(ga, *_norm_case(t, d, dtype, wtype, t + d, bias), dtype)
+
+
+def test_layer_norm_rows_that_a_cluster_shares_again(ga):
+    # the same bits every time, one call behind the other
+    x, w, _, dy = _norm_case(300, 20480, BF16, F32, 5)
+    x, w, dy = x.cuda(), w.cuda(), dy.cuda()
+    _, mean, rstd = ga.layer_norm(x, w)
+    first = ga.layer_norm_backward(dy, x, w, mean, rstd)
+    for got in [ga.layer_norm_backward(dy, x, w, mean, rstd) for _ in range(20)]:
+        for a, b in zip(first, got):
+            assert torch.equal(a, b)
