@@ -93,17 +93,19 @@ template <class T, int L, int V, int N> struct Row {
         for (int o = L / 2; o > 0; o >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
         // e = (2^y)^2, y = (logit - top) log2(e) / 2: the square carries e down to
-        // the subnormal numbers that the flushing exponential would drop.  fmaxf
+        // the subnormal numbers that the flushing exponential would drop.  The
+        // difference comes first: it is 0 at the largest logit however far that is
+        // from 0, where a product of each alone would leave its rounding.  fmaxf
         // skips a NaN; the exponential of a NaN logit brings it back.
         constexpr float half = 0.5f * 1.4426950408889634f;
-        const float shift = top == -INFINITY ? 0.f : -top * half;
+        const float from = top == -INFINITY ? 0.f : top;
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             // past the row's end 2^-infinity
-            const float sx = column(lane, 2 * i) < E ? shift : -INFINITY;
-            const float sy = N == 8 ? sx : column(lane, 2 * i + 1) < E && 2 * i + 1 < M ? shift : -INFINITY;
-            float2 y = fma2(e[i], both(half), make_float2(sx, sy));
+            const float fx = column(lane, 2 * i) < E ? from : INFINITY;
+            const float fy = N == 8 ? fx : column(lane, 2 * i + 1) < E && 2 * i + 1 < M ? from : INFINITY;
+            float2 y = mul2(sub2(e[i], make_float2(fx, fy)), both(half));
             asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(y.x));
             asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(y.y));
             e[i] = mul2(y, y);

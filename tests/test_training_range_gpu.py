@@ -5,8 +5,8 @@ import pytest
 import torch
 
 from tests.gpu_util import require_gpu
-from tests.test_training_gpu import (BF16, DTYPES, F32, _check_balance, _check_norm, _norm_case,
-                                     _randn)
+from tests.test_training_gpu import (BF16, DTYPES, F16, F32, _check_balance, _check_norm,
+                                     _norm_case, _randn)
 
 pytestmark = pytest.mark.gpu
 
@@ -14,6 +14,10 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module")
 def ga():
     return require_gpu()
+
+
+def _chosen(t, e, k, seed):
+    return torch.randint(0, e, (t, k), generator=torch.Generator().manual_seed(seed))
 
 
 # -------------------------------------------------------------- balance loss
@@ -30,6 +34,38 @@ def test_balance_equal_counts_have_no_gradient(ga, t, e, dtype):
     assert (grad == 0).all()
     kept, grad = _check_balance(ga, logits, ids, None, coef=0.25)
     assert (grad == 0).all() and abs(kept.loss.item() - 0.25) < 1e-5
+
+
+# rows: the one-launch cluster, and the two launches of a longer batch
+LARGE = {F16: [-65504.0, 65504.0, -3e4], BF16: [torch.finfo(BF16).min, torch.finfo(BF16).max,
+                                                -1e30, 1e30, -1e10, 1e10],
+         F32: [torch.finfo(F32).min, torch.finfo(F32).max, -1e30, 1e30, -1e10, 1e10, 12345678.0]}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("t", [7, 901])
+@pytest.mark.parametrize("e", [1, 8, 24, 60, 128, 512, 1000])
+def test_balance_large_logits(ga, t, e, dtype):
+    # a row of one value, the type's lowest (a mask's) or another far from 0: every expert's
+    # probability is 1 / E
+    value = torch.tensor([LARGE[dtype][i % len(LARGE[dtype])] for i in range(t)])
+    logits = value[:, None].expand(t, e).to(dtype).contiguous()
+    kept, _ = _check_balance(ga, logits, _chosen(t, e, 2, t), None)
+    assert torch.allclose(kept.mean_p.cpu(), torch.full((e,), 1 / e), rtol=1e-5)
+    # some experts at the lowest value beside ordinary ones: those have probability 0
+    logits = _randn(t, e, seed=e).to(dtype)
+    logits[:, 1::3] = torch.finfo(dtype).min
+    _, grad = _check_balance(ga, logits, _chosen(t, e, 2, t), None)
+    assert (grad[:, 1::3] == 0).all()
+
+
+@pytest.mark.parametrize("t", [7, 901])
+@pytest.mark.parametrize("e", [8, 60, 128])
+def test_balance_logits_around_a_large_value(ga, t, e):
+    # differences that fp32 holds exactly, far from 0
+    steps = torch.randint(-12, 1, (t, e), generator=torch.Generator().manual_seed(e)).float()
+    for base in (-2.0 ** 23, 2.0 ** 23, 2.0 ** 22 + 0.5):
+        _check_balance(ga, steps + base, _chosen(t, e, 2, t), None)
 
 
 # ---------------------------------------------------------------- layer norm
