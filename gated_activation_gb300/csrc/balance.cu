@@ -447,12 +447,13 @@ balance_backward(T *__restrict__ grad, const float *__restrict__ grad_loss,
     // every lane takes part in the shuffles of every round
     for (; t - part < T_; t += step) {
         const R p(raw, on ? E : 0, sub);
+        const float up_row = on ? scale : 0.f;      // no product of 0 and a scale that overflowed
         fetch(t + step);
         float2 mix = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < R::P; ++i)
             mix = fma2(p.e[i], c[i], mix);
-        const float mixed = R::total(mix.x + mix.y) * p.inv, s = scale * p.inv;
+        const float mixed = R::total(mix.x + mix.y) * p.inv, s = up_row * p.inv;
         if (t >= T_)
             continue;
         T *row = grad + t * E;

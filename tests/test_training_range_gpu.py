@@ -68,6 +68,18 @@ def test_balance_logits_around_a_large_value(ga, t, e):
         _check_balance(ga, steps + base, _chosen(t, e, 2, t), None)
 
 
+@pytest.mark.parametrize("up", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("t,e", [(40, 8), (40, 60), (901, 128), (901, 33)])
+def test_balance_rows_that_are_not_live_with_a_loss_gradient_that_is_not_finite(ga, t, e, up):
+    # the gradient of a loss scale that overflowed: 0 in rows that are not live all the same
+    logits = _randn(t, e, seed=t).cuda()
+    live = torch.arange(t, device="cuda") % 3 != 1
+    kept = ga.moe_balance_loss(logits, _chosen(t, e, 1, t).cuda(), 0.5, live=live)
+    for on in (live, torch.zeros_like(live)):
+        grad = ga.moe_balance_loss_backward(torch.full((1,), up, device="cuda"), logits, kept, live=on)
+        assert (grad[~on] == 0).all() and not torch.isfinite(grad[on]).any()
+
+
 # ---------------------------------------------------------------- layer norm
 
 # rows that clusters of two and four share: fewer and more of them than clusters on the GPU
