@@ -494,7 +494,9 @@ ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restr
 // parameters' gradients, and the weight, in registers; at the end the CTA
 // joins its rows' shares in shared memory and writes one share per column.
 // With h = (x - mean) rstd and g = dy w, the gradient is
-//   rstd (g - A - h B) = dy (w rstd) + (x - mean) (-B rstd^2) - A rstd.
+//   rstd (g - A - h B) = dy (w rstd) + h (-B rstd) - A rstd;
+// (x - mean) (-B rstd^2) would be one product less, but rstd^2 leaves fp32's
+// range where the deviation is below 1e-19 or above 1e19.
 // Rows that one CTA's registers and ring cannot hold are split over a cluster
 // of CL CTAs, `chunk` columns each; the row's two sums are then joined through
 // distributed shared memory, after a barrier that every CTA has started.
@@ -651,8 +653,8 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
         }
         a *= inv;
         b *= inv;
-        const float xs = -b * r1 * r1, off = -a * r1;
-        const float2 xs2 = make_float2(xs, xs), off2 = make_float2(off, off);
+        const float hs = -b * r1, off = -a * r1;
+        const float2 hs2 = make_float2(hs, hs), off2 = make_float2(off, off);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             if (!ring.in(i))
@@ -662,7 +664,7 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 o.put(j, fma2(y.pair(j), mul2(w[i].pair(j), r2),
-                              fma2(sub2(x.pair(j), m2), xs2, off2)));
+                              fma2(mul2(sub2(x.pair(j), m2), r2), hs2, off2)));
             ring.store(o, grad_in + r * width + span.head, i);
         }
         if (EDGES && edge >= 0)

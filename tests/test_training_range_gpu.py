@@ -4,6 +4,7 @@ tests/training_ref.py (which derives the bounds)."""
 import pytest
 import torch
 
+from tests import training_ref as R
 from tests.gpu_util import require_gpu
 from tests.test_training_gpu import (BF16, DTYPES, F16, F32, _check_balance, _check_norm,
                                      _norm_case, _randn)
@@ -100,3 +101,22 @@ def test_layer_norm_rows_that_a_cluster_shares_again(ga):
     for got in [ga.layer_norm_backward(dy, x, w, mean, rstd) for _ in range(20)]:
         for a, b in zip(first, got):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("scale", [1e-20, 1e-15, 1e15, 1e20])
+@pytest.mark.parametrize("t,d", [(5, 64), (40, 2048), (3, 8192), (5, 301), (9, 2047), (2, 16384),
+                                 (2, 20000), (2, 40001)])
+def test_layer_norm_backward_of_small_and_large_deviations(ga, t, d, scale, dtype):
+    # 1 / std whose square fp32 does not hold; gradients that follow the row, so that the mean of
+    # g hat is about 1
+    x = (scale * _randn(t, d, seed=d)).to(dtype)
+    dy = (x.float() / scale + 0.5 * _randn(t, d, seed=d + 1)).to(dtype)
+    w = 1 + 0.2 * _randn(d, seed=d + 2)
+    want = R.layer_norm(x.double(), w.double(), None, 0.0)
+    mean, rstd = (want[k][0].to(F32).cuda() for k in ("mean", "rstd"))
+    grad, gw, gb = ga.layer_norm_backward(dy.cuda(), x.cuda(), w.cuda(), mean, rstd)
+    want = R.layer_norm_backward(x.double(), dy.double(), w.double(), 0.0)
+    R.check(grad, *want["grad"], dtype, "grad")
+    R.check(gw, *want["weight"], F32, "grad_weight")
+    R.check(gb, *want["bias"], F32, "grad_bias")
