@@ -493,6 +493,26 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
     return t;
 }
 
+// The mean of a row of n elements, its sum from all threads as row_sum.  `other` is
+// nonzero in a thread that holds an element with other bits than the row's first:
+// where none does, that element is the mean.  The deviation of such a row is 0 and no
+// gate lies above the cutoff, but a rounded sum would give it a deviation of its
+// rounding and, at z < 1, pass the whole row or none of it.  One logic instruction per
+// word; the barrier carries the answer.
+template <int NT>
+__device__ __forceinline__ float row_mean(float v, float *red, uint32_t other, float first, float n) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = v;
+    const bool same = !__syncthreads_or(other != 0u);
+    constexpr int NW = NT / 32;
+    float t = red[threadIdx.x & (NW - 1)];
+#pragma unroll
+    for (int o = NW / 2; o > 0; o >>= 1)
+        t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    return same ? first : t / n;
+}
+
 // ------------------------------------------------------ sparse, any layout
 //
 // One CTA per row, one element per lane: warp w holds the blocks w, w + NT / 32,
@@ -518,15 +538,23 @@ sparse_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__r
     constexpr int kLine = 128 / sizeof(T);
     for (int c = kLine * t; c < d; c += kLine * NT)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(in + r * rs + d + c));
+    const float first = to_float(__ldg(in + r * rs));
+    uint32_t other = 0u;
     float g[V], acc = 0.f;
     for_groups<NT, V>(t, d, [&](int i, bool full) {
 #pragma unroll
         for (int j = i; j < i + 4; ++j)
             g[j] = full || t + NT * j < d ? to_float(__ldg(p + NT * j)) : 0.f;
     });
-    for_groups<NT, V>(t, d, [&](int i, bool) { acc += (g[i] + g[i + 1]) + (g[i + 2] + g[i + 3]); });
+    for_groups<NT, V>(t, d, [&](int i, bool full) {
+        acc += (g[i] + g[i + 1]) + (g[i + 2] + g[i + 3]);
+#pragma unroll
+        for (int j = i; j < i + 4; ++j)
+            if (full || t + NT * j < d)
+                other |= __float_as_uint(g[j]) ^ __float_as_uint(first);
+    });
     const float n = static_cast<float>(d);
-    const float mean = row_sum<NT>(acc, red[0]) / n;
+    const float mean = row_mean<NT>(acc, red[0], other, first, n);
     acc = 0.f;
     for_groups<NT, V>(t, d, [&](int i, bool full) {
 #pragma unroll
@@ -657,11 +685,17 @@ sparse_forward_wide(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const T *g = in + r * rs;
+        const float first = to_float(g[0]);
+        uint32_t other = 0u;
         float acc = 0.f;
 #pragma unroll 4
-        for (int64_t c = threadIdx.x; c < d; c += kWideThreads)
-            acc += to_float(g[c]);
-        const float mean = row_sum<kWideThreads>(acc, red[0]) / static_cast<float>(d);
+        for (int64_t c = threadIdx.x; c < d; c += kWideThreads) {
+            const float x = to_float(g[c]);
+            acc += x;
+            other |= __float_as_uint(x) ^ __float_as_uint(first);
+        }
+        const float mean =
+            row_mean<kWideThreads>(acc, red[0], other, first, static_cast<float>(d));
         acc = 0.f;
 #pragma unroll 4
         for (int64_t c = threadIdx.x; c < d; c += kWideThreads) {
@@ -775,6 +809,7 @@ sparse_forward_vec(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__r
     pdl_trigger();
     const int64_t r = blockIdx.x;
     const T *p = in + r * rs;
+    const T first = __ldg(p);
     Vec8<T> g[V], u[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -787,13 +822,17 @@ sparse_forward_vec(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__r
         u[i] = c < d ? Vec8<T>::load(p + d + c) : Vec8<T>::zero();
     }
     float2 acc = make_float2(0.f, 0.f);
+    uint32_t other = 0u;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             acc = add2(acc, g[i].pair(j));
+        if (8 * (threadIdx.x + NT * i) < d)
+            other |= g[i].other(Vec8<T>::pattern(first));
+    }
     const float n = static_cast<float>(d);
-    const float mean = row_sum<NT>(acc.x + acc.y, red[0]) / n;
+    const float mean = row_mean<NT>(acc.x + acc.y, red[0], other, to_float(first), n);
     acc = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -936,22 +975,29 @@ sparse_forward_ring(T *__restrict__ out, int8_t *__restrict__ codes,
 #pragma unroll
     for (int k = 0; k < S - 1; ++k)
         fetch(blockIdx.x + k * G, k);
+    T next = __ldg(in + blockIdx.x * rs);      // the first element of the next row; every CTA has one
     int slot = 0;
     const float n = static_cast<float>(d);
     for (int64_t r = blockIdx.x; r < rows; r += G) {
         // the slot read in the round before: this thread is done with it
         fetch(r + (S - 1) * G, slot == 0 ? S - 1 : slot - 1);
+        const T first = next;
+        if (r + G < rows)
+            next = __ldg(in + (r + G) * rs);
         copy_wait<S - 1>();
         Vec8<T> g[V];
         float2 acc = both(0.f);
+        uint32_t other = 0u;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             g[i] = held(slot, 0, i);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 acc = add2(acc, g[i].pair(j));
+            if (8 * (t + NT * i) < d)
+                other |= g[i].other(Vec8<T>::pattern(first));
         }
-        const float mean = row_sum<NT>(acc.x + acc.y, red[0]) / n;
+        const float mean = row_mean<NT>(acc.x + acc.y, red[0], other, to_float(first), n);
         acc = both(0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i)

@@ -177,6 +177,13 @@ template <class T> struct Vec8 {
             (&q.x)[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
     }
+    // Nonzero where an element has other bits than those of pattern(first).
+    __device__ static uint32_t pattern(T first) {
+        return 0x10001u * *reinterpret_cast<const unsigned short *>(&first);
+    }
+    __device__ uint32_t other(uint32_t of) const {
+        return (q.x ^ of) | (q.y ^ of) | (q.z ^ of) | (q.w ^ of);
+    }
     // Largest magnitude, as the bits of the element type: for values of one
     // type these order as the magnitudes do, infinity and NaN above all.
     __device__ uint32_t top() const {
@@ -216,6 +223,14 @@ template <> struct Vec8<float> {
         uint32_t *w = &q[i / 2].x + 2 * (i & 1);
         w[0] = __float_as_uint(f.x);
         w[1] = __float_as_uint(f.y);
+    }
+    __device__ static uint32_t pattern(float first) { return __float_as_uint(first); }
+    __device__ uint32_t other(uint32_t of) const {
+        uint32_t r = 0u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            r |= (q[i].x ^ of) | (q[i].y ^ of) | (q[i].z ^ of) | (q[i].w ^ of);
+        return r;
     }
     __device__ uint32_t top() const {
         float t = 0.f;

@@ -4,10 +4,11 @@ tests/training_ref.py (which derives the bounds)."""
 import pytest
 import torch
 
+import workloads as W
 from tests import training_ref as R
 from tests.gpu_util import require_gpu
 from tests.test_training_gpu import (BF16, DTYPES, F16, F32, _check_balance, _check_norm,
-                                     _norm_case, _randn)
+                                     _check_sparse_forward, _gated, _norm_case, _randn)
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +121,38 @@ def test_layer_norm_backward_of_small_and_large_deviations(ga, t, d, scale, dtyp
     R.check(grad, *want["grad"], dtype, "grad")
     R.check(gw, *want["weight"], F32, "grad_weight")
     R.check(gb, *want["bias"], F32, "grad_bias")
+
+
+# --------------------------------------------------------------- checkpoints
+
+# one per lane and in vectors, of every kernel: rows in registers, in the ring, read again
+@pytest.mark.parametrize("dtype,m,d", [(F32, 3, 257), (F32, 3, 1000), (F32, 2, 1001), (F32, 2, 2048),
+                                       (F32, 2, 4096), (F32, 2, 8193), (F32, 2, 16384),
+                                       (F32, 2, 20001), (F32, 2, 40000), (F16, 2, 32760),
+                                       (F16, 2437, 1032), (F16, 613, 4104), (F16, 311, 16376)])
+def test_sparse_constant_rows(ga, m, d, dtype):
+    # constants of many digits, whose sums are rounded: the deviation is 0 all the same, nothing
+    # passes, and the gradients are 0
+    value = torch.tensor([2.5841505, 2.71828, -0.1, 1 / 3, 77.7, 1e-3, 12345.678])
+    gate = value[torch.arange(m) % len(value)][:, None].expand(m, d)
+    x = torch.cat([gate, _randn(m, d, seed=d)], 1).to(dtype).cuda()
+    dy = torch.ones(m, d, dtype=dtype, device="cuda")
+    for z in (0.0, W.Z95, -1.0):
+        out, kept = ga.gelu_and_mul_sparse_checkpoint(x, z)
+        assert (kept.std == 0).all() and (kept.codes[:, :d] == 0).all() and (out == 0).all()
+        assert (ga.gelu_and_mul_sparse_backward(dy, kept, z) == 0).all()
+
+
+@pytest.mark.parametrize("dtype,m,d", [(F32, 7, 257), (F32, 6, 1000), (F32, 6, 16384),
+                                       (F16, 2437, 1032), (F16, 2, 40000)])
+def test_sparse_rows_constant_but_for_one_element(ga, m, d, dtype):
+    # the one element may be the first, the last or any other
+    x = _gated(m, d, dtype, 7)
+    x[:, :d] = 0.7
+    at = torch.tensor([0, d - 1, d // 2, 1, 8, 33])[torch.arange(m) % 6].cuda()
+    x[torch.arange(m, device="cuda"), at] = 0.9
+    for z in (0.0, 1.0):
+        out, kept = ga.gelu_and_mul_sparse_checkpoint(x, z)
+        _check_sparse_forward(x.double().cpu(), d, z, dtype, out, kept)
+        assert (kept.std > 0).all()
+        assert (kept.codes[:, :d] > 0).sum(1).eq(1).all()
