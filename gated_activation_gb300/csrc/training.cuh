@@ -177,13 +177,6 @@ template <class T> struct Vec8 {
             (&q.x)[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
     }
-    // Nonzero where an element has other bits than those of pattern(first).
-    __device__ static uint32_t pattern(T first) {
-        return 0x10001u * *reinterpret_cast<const unsigned short *>(&first);
-    }
-    __device__ uint32_t other(uint32_t of) const {
-        return (q.x ^ of) | (q.y ^ of) | (q.z ^ of) | (q.w ^ of);
-    }
     // Largest magnitude, as the bits of the element type: for values of one
     // type these order as the magnitudes do, infinity and NaN above all.
     __device__ uint32_t top() const {
@@ -224,8 +217,9 @@ template <> struct Vec8<float> {
         w[0] = __float_as_uint(f.x);
         w[1] = __float_as_uint(f.y);
     }
-    __device__ static uint32_t pattern(float first) { return __float_as_uint(first); }
-    __device__ uint32_t other(uint32_t of) const {
+    // Nonzero where an element has other bits than `first`.
+    __device__ uint32_t other(float first) const {
+        const uint32_t of = __float_as_uint(first);
         uint32_t r = 0u;
 #pragma unroll
         for (int i = 0; i < 2; ++i)

@@ -128,7 +128,8 @@ def test_layer_norm_backward_of_small_and_large_deviations(ga, t, d, scale, dtyp
 # one per lane and in vectors, of every kernel: rows in registers, in the ring, read again
 @pytest.mark.parametrize("dtype,m,d", [(F32, 3, 257), (F32, 3, 1000), (F32, 2, 1001), (F32, 2, 2048),
                                        (F32, 2, 4096), (F32, 2, 8193), (F32, 2, 16384),
-                                       (F32, 2, 20001), (F32, 2, 40000), (F16, 2, 32760),
+                                       (F32, 2, 20001), (F32, 2, 40000), (F16, 2, 32760), (F16, 3, 12001),
+                                       (F16, 2, 32761), (F16, 2, 40000), (BF16, 2, 70000),
                                        (F16, 2437, 1032), (F16, 613, 4104), (F16, 311, 16376)])
 def test_sparse_constant_rows(ga, m, d, dtype):
     # constants of many digits, whose sums are rounded: the deviation is 0 all the same, nothing
