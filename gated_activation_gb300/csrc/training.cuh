@@ -27,29 +27,29 @@ template <> __device__ __forceinline__ f16 from_float<f16>(float x) { return __f
 // ------------------------------------------------------------- activations
 
 // Both activations are g sigma(a) with a = a(g), and their slope is
-// sigma (1 + g a' (1 - sigma)).  With y = a log2(e) / 2, k = 2^y and h = 2^-y,
-//   sigma = k r,  r = 1 / (k + h):
-// no cancellation and no case by sign.  k, h and r come from the flushing
-// hardware exponential and reciprocal (PTX ISA ex2.approx.ftz.f32, rcp.approx.
-// ftz.f32, relative error about 2^-22); k and r stay normal down to a = -174,
-// and k is multiplied last, so nothing but a result itself can fall below
-// fp32's normal range.  y is taken at most at 16, where 1 - sigma is 2^-32.
-// Two elements at a time: the paired fp32 instructions halve the issue slots.
+// sigma (1 + g a' (1 - sigma)).  With y = a log2(e) / 2 and e = 2^-|y|,
+//   sigma = r k,  r = 1 / (1 + e^2), k = 1 for y >= 0;  r = e / (1 + e^2), k = e for y < 0:
+// no cancellation and no limit on y.  e and the reciprocal come from the flushing
+// hardware functions (PTX ISA ex2.approx.ftz.f32, rcp.approx.ftz.f32, relative error
+// about 2^-22); e stays normal down to a = -174, where sigma is 2^-251, and is 0 below.
+// Neither factor is above 1, and k is multiplied last, so that a product with them
+// falls below fp32's normal range only where the result does, or where what it
+// multiplies is there already.  (The gate's gradient is the product of u r and dy k:
+// one of these may lose bits below the normal range while the other is large.)  Two
+// elements at a time: the paired fp32 instructions halve the issue slots.
 struct Gate2 {
     float2 r, k;   // sigma = r k
 };
 __device__ __forceinline__ Gate2 gate_of(float2 y) {
     Gate2 m;
-    float2 h;
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(y.x) : "f"(16.f));
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(y.y) : "f"(16.f));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(m.k.x) : "f"(y.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(m.k.y) : "f"(y.y));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h.x) : "f"(-y.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h.y) : "f"(-y.y));
-    h = add2(m.k, h);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(m.r.x) : "f"(h.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(m.r.y) : "f"(h.y));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(-fabsf(y.x)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(-fabsf(y.y)));
+    m.k = make_float2(y.x < 0.f ? e.x : 1.f, y.y < 0.f ? e.y : 1.f);
+    e = fma2(e, e, make_float2(1.f, 1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(m.r.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(m.r.y) : "f"(e.y));
+    m.r = mul2(m.r, m.k);
     return m;
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }

@@ -8,7 +8,7 @@ import workloads as W
 from tests import training_ref as R
 from tests.gpu_util import require_gpu
 from tests.test_training_gpu import (BF16, DTYPES, F16, F32, _check_balance, _check_norm,
-                                     _check_sparse_forward, _gated, _norm_case, _randn)
+                                     _check_sparse_forward, _gated, _norm_case, _ops, _randn)
 
 pytestmark = pytest.mark.gpu
 
@@ -157,3 +157,25 @@ def test_sparse_rows_constant_but_for_one_element(ga, m, d, dtype):
         _check_sparse_forward(x.double().cpu(), d, z, dtype, out, kept)
         assert (kept.std > 0).all()
         assert (kept.codes[:, :d] > 0).sum(1).eq(1).all()
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 37])
+def test_small_up_values_beside_large_gates(ga, d, dtype, name):
+    # an up half at the lower end of the normal range, whose products with the gate are normal:
+    # no factor on the way may take them below it
+    gates = torch.tensor([0.5, 3.0, 8.0, 13.0, 22.5, 30.0, 60.0, 500.0, -0.5, -3.0, -20.0, -70.0])
+    gate = gates[:, None].expand(len(gates), d)
+    up = 1.2e-38 * (1 + _randn(len(gates), d, seed=1).abs())
+    x = torch.cat([gate, up], 1).to(dtype)
+    forward, backward = _ops(ga, name)
+    out, kept = forward(x.cuda())
+    xr = x.double()
+    a, _, _, grow = R.act(name, xr[:, :d])
+    R.check(out, a * xr[:, d:], (a * xr[:, d:]).abs() * grow, dtype, "out")
+    dy = _randn(len(gates), d, seed=2).to(dtype)
+    want = R.act_backward(name, R.values(kept.codes, kept.scales), dy.double())
+    grad, again = backward(dy.cuda(), kept, recompute=True)
+    R.check(grad, *want["grad"], dtype, "grad")
+    R.check(again, *want["out"], dtype, "recomputed out")
