@@ -216,7 +216,7 @@ int64_t gated_width(const Rows &x, PyObject *d_) {
         d = integer(d_);
     else if (x.n % 2)
         value_error("odd row length: pass d explicitly");
-    if (d < 1 || x.n < 2 * d)
+    if (d < 1 || d > x.n / 2)
         value_error("rows are shorter than 2d");
     return d;
 }

@@ -179,3 +179,12 @@ def test_small_up_values_beside_large_gates(ga, d, dtype, name):
     grad, again = backward(dy.cuda(), kept, recompute=True)
     R.check(grad, *want["grad"], dtype, "grad")
     R.check(again, *want["out"], dtype, "recomputed out")
+
+
+@pytest.mark.parametrize("d", [0, -1, 9, 1 << 40, 1 << 62, (1 << 63) - 1])
+def test_widths_that_the_rows_do_not_hold(ga, d):
+    x = torch.zeros(0, 16, dtype=BF16, device="cuda")
+    for call in (lambda: ga.silu_and_mul_checkpoint(x, d=d),
+                 lambda: ga.gelu_and_mul_sparse_checkpoint(x, 1.0, d=d)):
+        with pytest.raises(ValueError):
+            call()
