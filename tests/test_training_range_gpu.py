@@ -1,6 +1,8 @@
 """The training operators at the ends of their ranges: what their formulas give where the
 arithmetic could lose it, and every kernel that the sizes choose, against the 64-bit forms of
 tests/training_ref.py (which derives the bounds)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -188,3 +190,128 @@ def test_widths_that_the_rows_do_not_hold(ga, d):
                  lambda: ga.gelu_and_mul_sparse_checkpoint(x, 1.0, d=d)):
         with pytest.raises(ValueError):
             call()
+
+
+# ----------------------------------- the kernels of every class of widths and batches
+
+# widths in whole vectors between those of the other tests: a few rows, more than the shares
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("t,d", [(3, 2056), (3, 4096), (700, 4096), (320, 3000), (2, 6144), (170, 4104),
+                                 (2, 8208), (170, 12288), (160, 16384)])
+def test_layer_norm_widths(ga, t, d, dtype):
+    for wtype, bias in ((dtype, True), (F32, False)):
+        _check_norm(ga, *_norm_case(t, d, dtype, wtype, t + d, bias), dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("t,d", [(33, 4095), (170, 10001), (160, 16383)])
+def test_layer_norm_widths_off_a_boundary(ga, t, d, dtype):
+    _check_norm(ga, *_norm_case(t, d, dtype, F32, t + d, True), dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,d", [(3, 1032), (5, 2048), (3, 2056), (700, 4096), (2, 4104), (3, 8200),
+                                 (40, 12288), (160, 16384), (3, 24576)])
+def test_sparse_widths(ga, m, d, dtype):
+    for z in (0.0, W.Z95):
+        x = _gated(m, d, dtype, d + m)
+        out, kept = ga.gelu_and_mul_sparse_checkpoint(x, z)
+        _check_sparse_forward(x.double().cpu(), d, z, dtype, out, kept)
+        dy = _randn(m, d, seed=d + 1).to(dtype)
+        want = R.sparse_backward(R.values(kept.codes, kept.scales), dy.double(),
+                                 kept.std.double().cpu(), z)
+        grad, again = ga.gelu_and_mul_sparse_backward(dy.cuda(), kept, z, recompute=True)
+        R.check(grad, *want["grad"], dtype, "grad")
+        R.check(again, *want["out"], dtype, "recomputed out")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("t,e,k", [(769, 1, 1), (900, 8, 2), (1100, 24, 2), (1300, 32, 4), (1000, 64, 4),
+                                   (1000, 128, 8), (20000, 128, 8), (1200, 160, 6), (800, 256, 8),
+                                   (2000, 384, 6), (900, 1000, 2), (900, 1024, 8), (800, 5, 2),
+                                   (900, 100, 4), (800, 250, 3), (850, 500, 2), (850, 1001, 2)])
+def test_balance_long_batches(ga, t, e, k, dtype):
+    logits = (1.5 * _randn(t, e, seed=t) + 0.5 * _randn(1, e, seed=e)).to(dtype)
+    ids = _chosen(t, e, k, t + k)
+    _check_balance(ga, logits, ids, None)
+    _check_balance(ga, logits, ids.int(), _randn(t, seed=3) > -0.5)
+
+
+# ------------------------------------------------------ what the outputs end at
+
+class _Guarded:
+    """Output buffers with bands around them that must stay as they are."""
+
+    def __init__(self, off, **sizes):
+        self.off, self.sizes = off, sizes
+        self.buf = {k: torch.full((n + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+                    for k, n in sizes.items()}
+
+    def __getitem__(self, k):
+        return ctypes.c_void_p(self.buf[k].data_ptr() + 256 + self.off)
+
+    def check(self, what):
+        for k, b in self.buf.items():
+            end = 256 + self.off + self.sizes[k]
+            assert (b[:256 + self.off] == 0xA5).all() and (b[end:] == 0xA5).all(), (k, *what)
+
+
+@pytest.mark.parametrize("dtype,m,d", [(BF16, 3, 37), (BF16, 2, 1000), (BF16, 2, 4099), (F32, 3, 1001),
+                                       (F32, 3, 8192), (BF16, 2437, 1032), (BF16, 311, 16376),
+                                       (F16, 2, 40001)])
+def test_guard_bands_sparse(ga, m, d, dtype):
+    lib, s = ga.load_library(), torch.cuda.current_stream().cuda_stream
+    x, dy, nb = _gated(m, d, dtype, 9), _randn(m, d, seed=1).to(dtype).cuda(), -(-d // 32)
+    size, code = x.element_size(), {BF16: ga.BF16, F16: ga.F16, F32: ga.F32}[dtype]
+    for off in (0, size, 32):
+        g = _Guarded(off, out=size * m * d, codes=2 * m * d, scales=2 * m * nb, grad=2 * size * m * d,
+                     again=size * m * d)
+        f = _Guarded(0, std=4 * m, values=8 * m * d)
+        assert lib.gelu_and_mul_sparse_checkpoint(g["out"], g["codes"], g["scales"], f["std"],
+                                                  x.data_ptr(), m, d, 2 * d, 1.0, code, s) == 0
+        assert lib.gelu_and_mul_sparse_backward(g["grad"], g["again"], dy.data_ptr(), g["codes"],
+                                                g["scales"], f["std"], m, d, d, 1.0, code, s) == 0
+        assert lib.gated_act_checkpoint_values(f["values"], g["codes"], g["scales"], m, d, ga.F32,
+                                               s) == 0
+        g.check((m, d, off))
+        f.check((m, d, off))
+
+
+@pytest.mark.parametrize("dtype,t,d", [(BF16, 3, 37), (BF16, 5, 301), (BF16, 700, 2047), (F32, 9, 1001),
+                                       (F32, 3, 4096), (BF16, 3, 12345), (BF16, 2, 20000),
+                                       (F16, 2, 40001)])
+def test_guard_bands_layer_norm(ga, t, d, dtype):
+    lib, s = ga.load_library(), torch.cuda.current_stream().cuda_stream
+    x, w, b, dy = (v.cuda() for v in _norm_case(t, d, dtype, F32, 3))
+    size, code = x.element_size(), {BF16: ga.BF16, F16: ga.F16, F32: ga.F32}[dtype]
+    need = lib.layer_norm_backward_workspace_bytes(t, d)
+    for off in (0, size, 16):
+        g = _Guarded(off, out=size * t * d, grad=size * t * d)
+        f = _Guarded(0, mean=4 * t, rstd=4 * t, gw=4 * d, gb=4 * d, ws=need)
+        assert lib.layer_norm(g["out"], f["mean"], f["rstd"], x.data_ptr(), w.data_ptr(), b.data_ptr(),
+                              t, d, d, 1e-5, code, ga.F32, s) == 0
+        assert lib.layer_norm_backward(g["grad"], f["gw"], f["gb"], dy.data_ptr(), x.data_ptr(),
+                                       w.data_ptr(), f["mean"], f["rstd"], t, d, d, d, code, ga.F32,
+                                       f["ws"], need, s) == 0
+        g.check((t, d, off))
+        f.check((t, d, off))
+
+
+@pytest.mark.parametrize("dtype,t,e", [(BF16, 3, 8), (BF16, 40, 60), (F32, 901, 33), (F32, 900, 128),
+                                       (F16, 900, 1000), (BF16, 5000, 5)])
+def test_guard_bands_balance(ga, t, e, dtype):
+    lib, s = ga.load_library(), torch.cuda.current_stream().cuda_stream
+    x, ids = _randn(t, e, seed=1).to(dtype).cuda(), _chosen(t, e, 2, 1).cuda()
+    size, code = x.element_size(), {BF16: ga.BF16, F16: ga.F16, F32: ga.F32}[dtype]
+    need = lib.moe_balance_loss_workspace_bytes(t, e)
+    one = torch.ones(1, device="cuda")
+    for off in (0, size, 32):
+        g = _Guarded(off, grad=size * t * e)
+        f = _Guarded(0, loss=4, counts=4 * e, tokens=4, p=4 * e, ws=need)
+        assert lib.moe_balance_loss(f["loss"], f["counts"], f["tokens"], f["p"], x.data_ptr(),
+                                    ids.data_ptr(), None, t, e, 2, e, code, 1, 0.5, f["ws"], need,
+                                    s) == 0
+        assert lib.moe_balance_loss_backward(g["grad"], one.data_ptr(), x.data_ptr(), f["counts"],
+                                             f["tokens"], None, t, e, 2, e, code, 0.5, s) == 0
+        g.check((t, e, off))
+        f.check((t, e, off))
