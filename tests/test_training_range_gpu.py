@@ -315,3 +315,63 @@ def test_guard_bands_balance(ga, t, e, dtype):
                                              f["tokens"], None, t, e, 2, e, code, 0.5, s) == 0
         g.check((t, e, off))
         f.check((t, e, off))
+
+
+# -------------------------------------------- indexes past 32 bits, kernel by kernel
+
+def _room(gb):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gb << 30:
+        pytest.skip(f"needs {gb} GB of device memory")
+
+
+def _tail_kept(ga, d):
+    x = _gated(3, d, BF16, 8)
+    return x, *ga.silu_and_mul_checkpoint(x)
+
+
+def test_more_than_2_to_31_vectors_of_values(ga):
+    # 2 d / 8 vectors per row: 2^31 and more in 2^30 rows of d = 8
+    _room(80)
+    m, d = (1 << 30) + 5, 8
+    _, _, tail = _tail_kept(ga, d)
+    codes = torch.zeros((m, 2 * d), dtype=torch.int8, device="cuda")
+    scales = torch.zeros((m, 2), dtype=torch.uint8, device="cuda")
+    codes[-3:], scales[-3:] = tail.codes, tail.scales
+    got = ga.checkpoint_values(ga.Checkpoint(codes, scales))
+    assert torch.equal(got[-3:], ga.checkpoint_values(tail)) and (got[:-3:1 << 20] == 0).all()
+
+
+def test_more_than_2_to_31_vectors_of_gradients(ga):
+    # d / 8 vectors per row: 2^31 rows and more of d = 8
+    _room(180)
+    m, d = (1 << 31) + 5, 8
+    _, _, tail = _tail_kept(ga, d)
+    codes = torch.zeros((m, 2 * d), dtype=torch.int8, device="cuda")
+    scales = torch.zeros((m, 2), dtype=torch.uint8, device="cuda")
+    codes[-3:], scales[-3:] = tail.codes, tail.scales
+    dy = torch.zeros((m, d), dtype=BF16, device="cuda")
+    dy[-3:] = _randn(3, d, seed=7).to(BF16).cuda()
+    short = ga.silu_and_mul_backward(dy[-3:].clone(), tail)
+    got = ga.silu_and_mul_backward(dy, ga.Checkpoint(codes, scales))
+    assert torch.equal(got[-3:], short) and (got[:-3:1 << 20] == 0).all()
+    del got, dy, codes, scales
+    torch.cuda.empty_cache()
+
+
+def test_more_than_2_to_31_blocks_element_by_element(ga):
+    # one block per row: 2^31 rows and more of d = 1
+    _room(60)
+    m, d = (1 << 31) + 5, 1
+    tail, want, wkept = _tail_kept(ga, d)
+    x = torch.zeros((m, 2 * d), dtype=BF16, device="cuda")
+    x[-3:] = tail
+    out, kept = ga.silu_and_mul_checkpoint(x)
+    del x
+    assert torch.equal(out[-3:], want) and (out[:-3:1 << 20] == 0).all()
+    assert torch.equal(kept.codes[-3:], wkept.codes) and torch.equal(kept.scales[-3:], wkept.scales)
+    short, again = ga.silu_and_mul_backward(want, wkept, recompute=True)
+    got, gagain = ga.silu_and_mul_backward(out, kept, recompute=True)
+    assert torch.equal(got[-3:], short) and torch.equal(gagain[-3:], again)
+    del got, gagain, out
+    assert torch.equal(ga.checkpoint_values(kept)[-3:], ga.checkpoint_values(wkept))
