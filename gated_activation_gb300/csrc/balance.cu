@@ -235,16 +235,6 @@ __device__ __forceinline__ float rows_sum(const float *sums, int E, int e) {
 
 // ------------------------------------------------------------- the cluster
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // A word of the same shared-memory variable in another CTA of the cluster.
 __device__ __forceinline__ uint32_t peer(const void *p, uint32_t rank) {
     uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), v;
@@ -269,14 +259,14 @@ __device__ __forceinline__ void write_loss(float *loss, float *share, float *red
             s += red[w];
         *share = s;
     }
-    cluster_sync();
+    cluster_barrier();
     if (rank == 0 && threadIdx.x == 0) {
         float s = 0.f;
         for (int c = 0; c < kCluster; ++c)
             s += __uint_as_float(peer(share, c));
         loss[0] = s * scale;
     }
-    cluster_sync();   // no CTA leaves while its share is read
+    cluster_barrier();   // no CTA leaves while its share is read
 }
 
 // One launch: the cluster's CTAs take `per` tokens each, then E / 8 experts.
@@ -300,7 +290,7 @@ balance_cluster(float *__restrict__ loss, int32_t *__restrict__ counts,
     sum_tokens<T, kThreads, L, V, N>(sums, hist, logits, ids, live, t0, t1, E, k, ls);
     for (int e = threadIdx.x; e < E; e += kThreads)
         sums[e] = rows_sum(sums, E, e);                       // only this thread reads column e
-    cluster_sync();
+    cluster_barrier();
     int n = 0;
     for (int c = 0; c < kCluster; ++c)
         n += static_cast<int>(peer(hist + E, c));
@@ -490,8 +480,6 @@ int check_sizes(int64_t T, int64_t E, int64_t k, int64_t ls, int dtype) {
         return GATED_ACT_ERR_TOO_LARGE;
     return GATED_ACT_OK;
 }
-
-template <int N> using Const = std::integral_constant<int, N>;
 
 // Calls f(integral constants L, V, N) for E experts: two vectors of 8 per lane, or
 // single elements.  One vector per lane exchanges more (65536 x 128 bf16 backward

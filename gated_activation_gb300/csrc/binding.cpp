@@ -203,9 +203,6 @@ template <class... A> PyObject *pack(PyObject *cls, A... a) {
     return r;
 }
 
-constexpr int64_t kBlock = 32;
-int64_t scale_bytes(int64_t d) { return 2 * ((d + kBlock - 1) / kBlock); }
-
 template <class T> T *ptr(const Tensor &x) { return static_cast<T *>(x.data_ptr()); }
 
 // --------------------------------------------------------------- checkpoints
@@ -229,7 +226,7 @@ template <class F> PyObject *checkpoint(const char *fn, F f, PyObject *const *a)
     const Launch go(a[4], x.x);
     const Tensor out = go.output(a[3], {x.m, d}, x.x.scalar_type());
     const Tensor codes = go.empty({x.m, 2 * d}, at::kChar);
-    const Tensor scales = go.empty({x.m, scale_bytes(d)}, at::kByte);
+    const Tensor scales = go.empty({x.m, gated_act_checkpoint_scales(d)}, at::kByte);
     check(fn, f(out.data_ptr(), ptr<int8_t>(codes), ptr<uint8_t>(scales), x.data(), x.m, d,
                 x.stride, x.code, n_rows, go.stream));
     return pack(nullptr, wrap(out), pack(g_checkpoint, wrap(codes), wrap(scales), none()));
@@ -249,7 +246,7 @@ PyObject *sparse_checkpoint(PyObject *const *a) {
     const Launch go(a[4], x.x);
     const Tensor out = go.output(a[3], {x.m, d}, x.x.scalar_type());
     const Tensor codes = go.empty({x.m, 2 * d}, at::kChar);
-    const Tensor scales = go.empty({x.m, scale_bytes(d)}, at::kByte);
+    const Tensor scales = go.empty({x.m, gated_act_checkpoint_scales(d)}, at::kByte);
     const Tensor std = go.empty({x.m}, at::kFloat);
     check("gelu_and_mul_sparse_checkpoint",
           gelu_and_mul_sparse_checkpoint(out.data_ptr(), ptr<int8_t>(codes), ptr<uint8_t>(scales),
@@ -273,7 +270,7 @@ struct Kept {
     void expect(PyObject *o, int64_t m, int64_t d) {
         codes = static_cast<const int8_t *>(flat(x, "codes", at::kChar, {m, 2 * d}));
         scales = static_cast<const uint8_t *>(
-            flat(tensor(item(o, 1), "scales"), "scales", at::kByte, {m, scale_bytes(d)}));
+            flat(tensor(item(o, 1), "scales"), "scales", at::kByte, {m, gated_act_checkpoint_scales(d)}));
         std = item(o, 2);
     }
 };

@@ -477,22 +477,6 @@ ckpt_values_vec(T *__restrict__ values, const int8_t *__restrict__ codes,
     }
 }
 
-// Sum over a CTA of NT threads, the same bits in every thread; red holds NT / 32
-// floats.
-template <int NT>
-__device__ __forceinline__ float row_sum(float v, float *red) {
-    v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0)
-        red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    constexpr int NW = NT / 32;
-    float t = red[threadIdx.x & (NW - 1)];
-#pragma unroll
-    for (int o = NW / 2; o > 0; o >>= 1)
-        t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    return t;
-}
-
 // The mean of a row of n elements, its sum from all threads as row_sum.  `other` is
 // nonzero in a thread that holds an element with other bits than the row's first:
 // where none does, that element is the mean.  The deviation of such a row is 0 and no
@@ -1143,8 +1127,6 @@ sparse_backward_ring(T *__restrict__ grad_in, T *__restrict__ out, const T *__re
 
 // -------------------------------------------------------------- host side
 
-constexpr int64_t kMaxWidth = int64_t(1) << 30, kMaxRows = int64_t(1) << 40;
-
 int check_sizes(int64_t M, int64_t d, int64_t stride, int64_t width, int dtype) {
     if (M < 0 || d <= 0)
         return GATED_ACT_ERR_SIZE;
@@ -1184,7 +1166,6 @@ template <class F> int with_jobs(int64_t jobs, F f) {
 }
 
 // The CTA that holds a row of d elements one by one, as with_row_cta.
-template <int N> using Const = std::integral_constant<int, N>;
 template <class F> bool with_any_cta(int64_t d, int *rc, F f) {
     if (d <= 512)
         *rc = f(Const<64>{}, Const<8>{});

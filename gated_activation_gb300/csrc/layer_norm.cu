@@ -307,22 +307,6 @@ template <int NT, int TPR> __device__ __forceinline__ void row_barrier() {
         asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / TPR), "n"(TPR) : "memory");
 }
 
-// Sum over the NT threads of a CTA that holds one row; red holds NT / 32 floats.
-template <int NT> __device__ __forceinline__ float row_sum(float v, float *red) {
-    v = warp_sum(v);
-    if constexpr (NT > 32) {
-        if ((threadIdx.x & 31) == 0)
-            red[threadIdx.x >> 5] = v;
-        __syncthreads();
-        constexpr int NW = NT / 32;
-        v = red[threadIdx.x & (NW - 1)];
-#pragma unroll
-        for (int o = NW / 2; o > 0; o >>= 1)
-            v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    }
-    return v;
-}
-
 template <class T, class W, int NT, int V, int S, bool EDGES>
 __global__ void __launch_bounds__(NT, 1024 / NT)
 ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__restrict__ rstd_out,
@@ -515,18 +499,6 @@ __device__ __forceinline__ void put_peer(float2 *p, uint32_t rank, float2 v) {
     asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(rank));
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A CTA's shared memory may be written by its peers once it has started: each says so on
-// entry, and waits for the others before it first writes to them.
-__device__ __forceinline__ void cluster_started() {
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait_started() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 template <class T, class W, int TPR, int V, int S, int CL, bool EDGES>
 __global__ void __launch_bounds__(kBackThreads, 1)
@@ -590,7 +562,6 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
     float mean = first < rows ? mean_in[first] : 0.f, rstd = first < rows ? rstd_in[first] : 0.f;
     const float inv = 1.0f / static_cast<float>(width);
     if constexpr (CL > 1) {
-        __syncwarp();
         cluster_wait_started();      // the first rows are on their way
     }
     for (int64_t r = first; r < rows; r += G, k ^= 1) {
@@ -642,7 +613,6 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
         if constexpr (CL > 1) {
             if (threadIdx.x < CL)
                 put_peer(&peers[k][rank], threadIdx.x, make_float2(a, b));
-            __syncwarp();
             cluster_barrier();
             a = b = 0.f;
 #pragma unroll
@@ -721,8 +691,6 @@ ln_backward_ring(T *__restrict__ grad_in, float *__restrict__ part, const T *__r
     }
 }
 
-constexpr int64_t kMaxWidth = int64_t(1) << 30, kMaxRows = int64_t(1) << 40;
-
 int check_sizes(int64_t T, int64_t d, int64_t rs, int64_t gs, int dtype, int param_dtype) {
     if (T < 0 || d <= 0)
         return GATED_ACT_ERR_SIZE;
@@ -744,8 +712,6 @@ template <class F> int with_types(int dtype, int param_dtype, F f) {
     });
 }
 
-template <int N> using Const = std::integral_constant<int, N>;
-
 // Calls f(integral constant NT): the threads of a row that no ring takes.  1024
 // for wide ones: 100 x 12345 fp16 forward 7.9 us against 19.2 with 256, 1000 of them 27.8
 // against 25.1, backward 53.1 against 57.2.
@@ -763,7 +729,7 @@ int64_t shares(int64_t T) {
 // vectors, 1024 threads per SM; false when it holds no such row.  Two slots, one
 // row ahead, are enough: with four 16384 x 2048 bf16 takes 23.5 us against 22.7,
 // 16384 x 512 7.85 against 7.12 (the first rows reach the SM as one burst).
-template <int SIZE, class F> bool with_forward_ring(int64_t nv, int *rc, F f) {
+template <class F> bool with_forward_ring(int64_t nv, int *rc, F f) {
     constexpr int S = 2;
     if (nv <= 32)
         *rc = f(Const<32>{}, Const<1>{}, Const<S>{});
@@ -874,7 +840,7 @@ extern "C" int layer_norm(void *out, float *mean, float *rstd, const void *in, c
             };
         };
         int done;
-        if (vec && with_forward_ring<sizeof(E)>(d / 8, &done, ring(std::false_type{})))
+        if (vec && with_forward_ring(d / 8, &done, ring(std::false_type{})))
             return done;
         if (vec && d / 8 <= 4096 && aligned(r[0].dev, 8 * size) && aligned(r[3].dev, 8 * size))
             return launched(launch_kernel(
@@ -883,7 +849,7 @@ extern "C" int layer_norm(void *out, float *mean, float *rstd, const void *in, c
                 as<const W>(r[4]), as<const W>(r[5]), static_cast<int>(d), row_stride,
                 static_cast<float>(eps)));
         if (!vec && same_offsets(r[0], d, r[3], row_stride, size) &&
-            with_forward_ring<sizeof(E)>(vectors_of(d), &done, ring(std::true_type{})))
+            with_forward_ring(vectors_of(d), &done, ring(std::true_type{})))
             return done;
         const int64_t grid = std::min<int64_t>(T, int64_t(device_sm_count()) * 64);
         return with_threads(d, [&](auto nt) {

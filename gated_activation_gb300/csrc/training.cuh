@@ -350,6 +350,46 @@ __device__ __forceinline__ uint2 bias_codes(uint2 c) {
     return make_uint2(c.x ^ 0x80808080u, c.y ^ 0x80808080u);
 }
 
+// ------------------------------------------------------- CTAs and clusters
+
+// Sum over the NT threads of a CTA that holds one row, the same bits in every thread;
+// red holds NT / 32 floats.
+template <int NT> __device__ __forceinline__ float row_sum(float v, float *red) {
+    v = warp_sum(v);
+    if constexpr (NT > 32) {
+        if ((threadIdx.x & 31) == 0)
+            red[threadIdx.x >> 5] = v;
+        __syncthreads();
+        constexpr int NW = NT / 32;
+        v = red[threadIdx.x & (NW - 1)];
+#pragma unroll
+        for (int o = NW / 2; o > 0; o >>= 1)
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    }
+    return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Barrier of the cluster's threads: what each wrote before is seen by all after it.
+__device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A CTA's shared memory may be written by its peers once it has started: each says so on
+// entry, and waits for the others before it first writes to them.
+__device__ __forceinline__ void cluster_started() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- host side
 
 // One buffer of a call: its checks, then the address kernels use for it.
@@ -364,6 +404,10 @@ struct Region {
 // Null, alignment, overlap (of two buffers of which one is written) and
 // residence of every buffer; empty buffers (bytes = 0) are skipped.
 int check_regions(Region *r, int n);
+
+constexpr int64_t kMaxWidth = int64_t(1) << 30, kMaxRows = int64_t(1) << 40;
+
+template <int N> using Const = std::integral_constant<int, N>;
 
 inline int64_t elem_size(int dtype) {
     return dtype == GATED_ACT_F32 ? 4 : dtype == GATED_ACT_BF16 || dtype == GATED_ACT_F16 ? 2 : 0;
