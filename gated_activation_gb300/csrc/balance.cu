@@ -396,7 +396,8 @@ balance_join(float *__restrict__ loss, int32_t *__restrict__ counts, int32_t *__
 }
 
 // Counts enter as c_j - C / E, C their sum, rounded to an integer: the same
-// gradient, since p sums to 1, without the cancellation of nearly equal counts.
+// gradient, since p sums to 1, without the cancellation of nearly equal counts.  The
+// difference is one of integers: fp32 does not hold a count past 2^24.
 template <class T, int L, int V, int N>
 __global__ void __launch_bounds__(kThreads)
 balance_backward(T *__restrict__ grad, const float *__restrict__ grad_loss,
@@ -417,21 +418,22 @@ balance_backward(T *__restrict__ grad, const float *__restrict__ grad_loss,
         raw.load(logits + at * ls, on ? E : 0, sub);
     };
     fetch(t);
-    float2 c[R::P];
+    int chosen[2 * R::P];
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < R::P; ++i) {
-        const int e0 = R::column(sub, 2 * i), e1 = R::column(sub, 2 * i + 1);
-        c[i].x = e0 < E ? static_cast<float>(__ldg(counts + e0)) : 0.f;
-        c[i].y = 2 * i + 1 < R::M && e1 < E ? static_cast<float>(__ldg(counts + e1)) : 0.f;
-        sum += c[i].x + c[i].y;
+    for (int i = 0; i < 2 * R::P; ++i) {
+        const int e = R::column(sub, i);
+        chosen[i] = i < R::M && e < E ? __ldg(counts + e) : 0;
+        sum += static_cast<float>(chosen[i]);
     }
     const int n = *tokens;
     const float up = *grad_loss;
-    const float mid = rintf(R::total(sum) / static_cast<float>(E));
+    const int mid = static_cast<int>(rintf(R::total(sum) / static_cast<float>(E)));
+    float2 c[R::P];
 #pragma unroll
     for (int i = 0; i < R::P; ++i)
-        c[i] = sub2(c[i], both(mid));
+        c[i] = make_float2(static_cast<float>(chosen[2 * i] - mid),
+                           static_cast<float>(chosen[2 * i + 1] - mid));
     const float nf = static_cast<float>(n > 0 ? n : 1);
     const float scale = up * (coef * static_cast<float>(E) / (nf * nf * k));
     // every lane takes part in the shuffles of every round

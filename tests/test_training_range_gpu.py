@@ -84,6 +84,23 @@ def test_balance_rows_that_are_not_live_with_a_loss_gradient_that_is_not_finite(
         assert (grad[~on] == 0).all() and not torch.isfinite(grad[on]).any()
 
 
+@pytest.mark.parametrize("e", [8, 24, 60])
+def test_balance_gradient_of_counts_past_2_to_24(ga, e):
+    # counts that fp32 does not hold, a few choices apart
+    t, k, up = 5, 4, 2.0 ** 40
+    logits = _randn(t, e, seed=e)
+    counts = (1 << 31) // e - 64 + torch.randint(-3, 4, (e,), generator=torch.Generator().manual_seed(e))
+    n = int(counts.sum()) // k
+    kept = ga.BalanceLoss(torch.zeros(1).cuda(), counts.int().cuda(),
+                          torch.tensor([n], dtype=torch.int32).cuda(), torch.zeros(e).cuda(), k, 1.0)
+    grad = ga.moe_balance_loss_backward(torch.full((1,), up).cuda(), logits.cuda(), kept)
+    p = torch.softmax(logits.double(), 1)
+    c = counts.double() - counts.double().mean()
+    scale = up * e / (n * n * k)
+    mag = scale * p * (c.abs() + 1 + (p * (c.abs() + 1)).sum(1, keepdim=True))
+    R.check(grad, scale * p * (c - (p * c).sum(1, keepdim=True)), 6 * mag, F32, "grad")
+
+
 # ---------------------------------------------------------------- layer norm
 
 # rows that clusters of two and four share: fewer and more of them than clusters on the GPU
