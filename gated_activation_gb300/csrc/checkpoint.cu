@@ -477,33 +477,13 @@ ckpt_values_vec(T *__restrict__ values, const int8_t *__restrict__ codes,
     }
 }
 
-// The mean of a row of n elements, its sum from all threads as row_sum.  `other` is
-// nonzero in a thread that holds an element with other bits than the row's first:
-// where none does, that element is the mean.  The deviation of such a row is 0 and no
-// gate lies above the cutoff, but a rounded sum would give it a deviation of its
-// rounding and, at z < 1, pass the whole row or none of it.  One logic instruction per
-// element; the barrier carries the answer.
+// The mean of a row of n elements: `first` where all have its bits.
 template <int NT>
 __device__ __forceinline__ float row_mean(float v, float *red, uint32_t other, float first, float n) {
-    v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0)
-        red[threadIdx.x >> 5] = v;
-    const bool same = !__syncthreads_or(other != 0u);
-    constexpr int NW = NT / 32;
-    float t = red[threadIdx.x & (NW - 1)];
-#pragma unroll
-    for (int o = NW / 2; o > 0; o >>= 1)
-        t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    return same ? first : t / n;
+    bool same;
+    const float sum = row_sum<NT>(v, red, other, &same);
+    return same ? first : sum / n;
 }
-// Whether sums of up to N equal elements can be rounded: fp32 holds the multiples up to
-// 2^13 of an fp16 number and up to 2^16 of a bf16 one (11 and 8 bits).  Rows whose sums
-// are exact need no such test, which costs them 2 to 4% (2048 x 16384 bf16 forward 49.7
-// us against 48.5, 4000 x 8192 46.3 against 44.7).
-template <class T, int N>
-constexpr bool kSumsRound = N > (std::is_same_v<T, float> ? 1
-                                 : std::is_same_v<T, f16> ? 1 << 13
-                                                          : 1 << 16);
 
 // ------------------------------------------------------ sparse, any layout
 //
@@ -545,7 +525,7 @@ sparse_forward_any(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__r
 #pragma unroll
             for (int j = i; j < i + 4; ++j)
                 if (full || t + NT * j < d)
-                    other |= __float_as_uint(g[j]) ^ __float_as_uint(first);
+                    other |= unlike(g[j], first);
     });
     const float n = static_cast<float>(d);
     float mean;
@@ -690,7 +670,7 @@ sparse_forward_wide(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__
         for (int64_t c = threadIdx.x; c < d; c += kWideThreads) {
             const float x = to_float(g[c]);
             acc += x;
-            other |= __float_as_uint(x) ^ __float_as_uint(first);
+            other |= unlike(x, first);
         }
         const float mean =
             row_mean<kWideThreads>(acc, red[0], other, first, static_cast<float>(d));
@@ -829,7 +809,7 @@ sparse_forward_vec(T *__restrict__ out, int8_t *__restrict__ codes, uint8_t *__r
             acc = add2(acc, g[i].pair(j));
         if constexpr (kRound)
             if (8 * (threadIdx.x + NT * i) < d)
-                other |= g[i].other(first);
+                other |= unlike(g[i], first);
     }
     const float n = static_cast<float>(d);
     float mean;

@@ -17,15 +17,7 @@ constexpr int kThreads = 256;
 
 // -------------------------------------------------- rows that no CTA holds
 
-// Sum over the CTA, the same bits in every thread; red holds 32 values.
-__device__ __forceinline__ float cta_sum(float v, float *red) {
-    v = warp_sum(v);
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    if (lane == 0)
-        red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return warp_sum(lane < warps ? red[lane] : 0.f);
-}
+// Sums over the CTA, the same bits in every thread; red holds 32 values.
 __device__ __forceinline__ float2 cta_sum2(float2 v, float2 *red) {
     v = make_float2(warp_sum(v.x), warp_sum(v.y));
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -50,16 +42,23 @@ ln_forward_wide(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
     pdl_trigger();
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const T *x = in + r * rs;
+        const float first = to_float(x[0]);
+        uint32_t other = 0u;
+        bool same;
         float acc = 0.f;
-        for (int64_t c = threadIdx.x; c < d; c += NT)
-            acc += to_float(x[c]);
-        const float mean = cta_sum(acc, red[0]) / static_cast<float>(d);
+        for (int64_t c = threadIdx.x; c < d; c += NT) {
+            const float v = to_float(x[c]);
+            acc += v;
+            other |= unlike(v, first);
+        }
+        const float sum = row_sum<NT>(acc, red[0], other, &same);
+        const float mean = same ? first : sum / static_cast<float>(d);
         acc = 0.f;
         for (int64_t c = threadIdx.x; c < d; c += NT) {
             const float e = to_float(x[c]) - mean;
             acc = fmaf(e, e, acc);
         }
-        const float var = cta_sum(acc, red[1]) / static_cast<float>(d);
+        const float var = row_sum<NT>(acc, red[1]) / static_cast<float>(d);
         const float rstd = 1.0f / __fsqrt_rn(var + eps);
         if (threadIdx.x == 0) {
             mean_out[r] = mean;
@@ -269,6 +268,16 @@ template <class T, int NT, int TPR, int V, int ROWS> struct Ring {
                 q[p] = mine[index(slot, which, i, p)];
         return v;
     }
+    // Nonzero where an element of vector i has other bits than `first`.
+    __device__ uint32_t unlike(const Vec8<T> &v, int i, T first) const {
+        const uint4 *q = reinterpret_cast<const uint4 *>(&v);
+        uint32_t r = 0u;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            if (in(i, kPiece * p))
+                r |= gact::unlike(q[p], repeated(first));
+        return r;
+    }
     __device__ void store(const Vec8<T> &v, T *row, int i) const {
         const uint4 *q = reinterpret_cast<const uint4 *>(&v);
 #pragma unroll
@@ -335,22 +344,30 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
         w[i] = ring.template params<EDGES>(weight + span.head, i);
         b[i] = bias ? ring.template params<EDGES>(bias + span.head, i) : Vec8<W>::zero();
     }
-    float we = 0.f, be = 0.f, next = 0.f;
+    float we = 0.f, be = 0.f;
+    T next = from_float<T>(0.f);      // as loaded: its conversion would wait for it
     if (EDGES && edge >= 0) {
         we = to_float(__ldg(weight + edge));
         be = bias ? to_float(__ldg(bias + edge)) : 0.f;
         if (blockIdx.x < rows)
-            next = to_float(__ldg(in + blockIdx.x * rs + edge));
+            next = __ldg(in + blockIdx.x * rs + edge);
     }
+    // the sums are of whole vectors, or of any number of elements with EDGES
+    constexpr bool kRound = EDGES ? kSumsRound<T, 8 * NT * V + 7> : kSumsRound<T, NT * V>;
+    T next_first = kRound && blockIdx.x < rows ? __ldg(in + blockIdx.x * rs) : T{};
     int slot = 0;
     const float inv = 1.0f / static_cast<float>(d);
     for (int64_t r = blockIdx.x; r < rows; r += G) {
         // the slot read in the round before: this thread is done with it
         fetch(r + (S - 1) * G, slot == 0 ? S - 1 : slot - 1);
-        const float xe = next;
+        const T first = next_first;
+        if (kRound && r + G < rows)
+            next_first = __ldg(in + (r + G) * rs);
+        const float xe = to_float(next);
         if (EDGES && edge >= 0 && r + G < rows)
-            next = to_float(__ldg(in + (r + G) * rs + edge));
+            next = __ldg(in + (r + G) * rs + edge);
         copy_wait<S - 1>();
+        uint32_t other = kRound && EDGES && edge >= 0 ? unlike(xe, to_float(first)) : 0u;
         float2 acc = make_float2(xe, 0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -358,11 +375,21 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 acc = add2(acc, x.pair(j));
+            if constexpr (kRound)
+                other |= ring.unlike(x, i, first);
         }
-        const float sum = row_sum<NT>(acc.x + acc.y, red[0]);
-        // the quotient by a product and its residual: exact for constant rows
+        bool same = false;
+        float sum;
+        if constexpr (kRound)
+            sum = row_sum<NT>(acc.x + acc.y, red[0], other, &same);
+        else
+            sum = row_sum<NT>(acc.x + acc.y, red[0]);
+        // the quotient by a product and its residual, which gives the value of a row of one
+        // where the sum is exact
         float mean = sum * inv;
         mean = fmaf(fmaf(-mean, static_cast<float>(d), sum), inv, mean);
+        if (kRound && same)
+            mean = to_float(first);
         const float2 m2 = make_float2(mean, mean);
         acc = make_float2(0.f, 0.f);
         if (EDGES && edge >= 0)
@@ -419,20 +446,34 @@ ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restr
     const int t = threadIdx.x;
     const int64_t r = blockIdx.x;
     const T *p = in + r * rs;
+    constexpr bool kRound = kSumsRound<T, NT * V>;    // sums of whole vectors
+    const T first = kRound ? __ldg(p) : T{};
     Vec8<T> x[V];
     float2 acc = make_float2(0.f, 0.f);
+    uint32_t other = 0u;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = 8 * (t + NT * i);
         x[i] = c < d ? Vec8<T>::load(p + c) : Vec8<T>::zero();
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             acc = add2(acc, x[i].pair(j));
+        if constexpr (kRound)
+            if (8 * (t + NT * i) < d)
+                other |= unlike(x[i], first);
+    }
     const float n = static_cast<float>(d);
-    const float mean = row_sum<NT>(acc.x + acc.y, red[0]) / n;
+    bool same = false;
+    float mean;
+    if constexpr (kRound) {
+        mean = row_sum<NT>(acc.x + acc.y, red[0], other, &same) / n;
+        mean = same ? to_float(first) : mean;
+    } else {
+        mean = row_sum<NT>(acc.x + acc.y, red[0]) / n;
+    }
     const float2 m2 = make_float2(mean, mean);
     acc = make_float2(0.f, 0.f);
 #pragma unroll

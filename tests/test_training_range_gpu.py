@@ -142,6 +142,30 @@ def test_layer_norm_backward_of_small_and_large_deviations(ga, t, d, scale, dtyp
     R.check(gb, *want["bias"], F32, "grad_bias")
 
 
+@pytest.mark.parametrize("dtype,t,d", [(F32, 7, 64), (F32, 7, 200), (F32, 7, 1000), (F32, 7, 2048),
+                                       (F32, 7, 2047), (F32, 7, 4097), (F32, 7, 16384), (F32, 7, 20000),
+                                       (F32, 7, 40001), (F16, 7, 1001), (F16, 9, 12345), (F16, 7, 16383),
+                                       (F16, 7, 40000), (BF16, 7, 16383), (BF16, 7, 70000)])
+def test_layer_norm_rows_of_one_value(ga, t, d, dtype):
+    # values of many digits, whose sums are rounded: the mean is the value, the deviation 0 and
+    # the output the bias, with eps far below the value's rounding too
+    value = torch.tensor([2.5841505, 2.71828, -0.1, 1 / 3, 77.7, 1e-3, 12345.678])
+    x = value[torch.arange(t) % 7][:, None].expand(t, d).to(dtype).cuda()
+    w, b = 1 + _randn(d, seed=1).cuda(), _randn(d, seed=2).cuda()
+    out, mean, rstd = ga.layer_norm(x.contiguous(), w, b, eps=1e-5)
+    assert torch.equal(mean, x[:, 0].float())
+    assert torch.equal(out, b.to(dtype).expand(t, d))
+    assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5), rtol=1e-6)
+
+
+@pytest.mark.parametrize("dtype,t,d", [(F32, 6, 64), (F32, 6, 2047), (F32, 6, 16384), (F32, 6, 20000),
+                                       (F16, 6, 16383), (F32, 6, 40001)])
+def test_layer_norm_rows_of_one_value_but_for_one_element(ga, t, d, dtype):
+    x = torch.full((t, d), 0.7)
+    x[torch.arange(t), torch.tensor([0, d - 1, d // 2, 1, 8, 33])] = 0.9
+    _check_norm(ga, x.to(dtype), *_norm_case(t, d, dtype, F32, 3)[1:], dtype)
+
+
 # --------------------------------------------------------------- checkpoints
 
 # one per lane and in vectors, of every kernel: rows in registers, in the ring, read again
