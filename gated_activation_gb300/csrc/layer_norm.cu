@@ -345,7 +345,7 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
         b[i] = bias ? ring.template params<EDGES>(bias + span.head, i) : Vec8<W>::zero();
     }
     float we = 0.f, be = 0.f;
-    T next = from_float<T>(0.f);      // as loaded: its conversion would wait for it
+    T next{};      // as loaded: its conversion would wait for it
     if (EDGES && edge >= 0) {
         we = to_float(__ldg(weight + edge));
         be = bias ? to_float(__ldg(bias + edge)) : 0.f;
@@ -363,7 +363,7 @@ ln_forward_ring(T *__restrict__ out, float *__restrict__ mean_out, float *__rest
         const T first = next_first;
         if (kRound && r + G < rows)
             next_first = __ldg(in + (r + G) * rs);
-        const float xe = to_float(next);
+        const float xe = EDGES ? to_float(next) : 0.f;
         if (EDGES && edge >= 0 && r + G < rows)
             next = __ldg(in + (r + G) * rs + edge);
         copy_wait<S - 1>();
