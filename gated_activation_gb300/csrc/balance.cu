@@ -3,12 +3,13 @@
 //
 // The forward pass reads the logits and the chosen ids once, the backward
 // pass reads the logits again (a softmax is recomputed in registers rather
-// than stored) and writes their gradient.  65536 x 128 bf16, k = 8, takes 11.2 us
-// forward and 8.9 us backward on GB300 (28% and 55% of the copy rate, 6.79 TB/s):
-// per pair of logits two exponentials and about thirty instructions, and of a
-// token the two exchanges between its lanes, bound it before HBM does, and the
-// second launch of the forward pass adds 2.5 us, the counts 1 us.  Of 64 tokens both
-// take the latency of a launch, 3.4 and 1.9 us.
+// than stored) and writes their gradient.  65536 x 128 bf16, k = 8, takes 11.3 us
+// forward and 8.7 us backward on GB300 (27% and 57% of the copy rate, 6.79 TB/s).
+// Latency bounds both: with 22.8 and 19.2 instructions per logit the issue slots are
+// 57% busy while a CTA runs (40 and 34% of the whole launch), and a warp waits for its
+// next tokens, the exchanges between a token's lanes and, forward, the CTA's barriers
+// while the warps' sums are added.  The forward pass's second launch is 2.5 us of it, the counts
+// 1 us.  Of 64 tokens both take the latency of a launch, 3.3 and 1.8 us.
 //
 // Tokens: L lanes share a token, each holding V groups of kLane elements of
 // its logits (rows in 16-byte vectors: 8 consecutive elements per group; any
@@ -484,9 +485,10 @@ int check_sizes(int64_t T, int64_t E, int64_t k, int64_t ls, int dtype) {
 }
 
 // Calls f(integral constants L, V, N) for E experts: two vectors of 8 per lane, or
-// single elements.  One vector per lane exchanges more (65536 x 128 bf16 backward
-// 11.2 us against 8.9, forward 12.0 in both), four keep too few tokens on their way
-// (12.4 and 9.3 us; 32768 x 64 fp32 forward 9.3 against 8.3).
+// single elements.  One vector per lane exchanges more in the backward pass, four keep
+// fewer tokens on their way.  Forward and backward, us, with one, two and four:
+//   65536 x 128 bf16   11.0 11.6    11.2  8.7    10.7  9.2
+//   32768 x 64 fp32     7.7  5.2     7.4  5.2     8.4  4.5
 template <class F> int with_lanes(int64_t E, bool vec, F f) {
     if (vec)
         return E <= 8     ? f(Const<1>{}, Const<1>{}, Const<8>{})
@@ -569,7 +571,8 @@ extern "C" int moe_balance_loss(float *loss, int32_t *counts, int32_t *tokens, f
                     per, Ei, ki, logits_stride, c));
             // 32 warps per SM; 16 where the registers of a lane's logits forbid it, and
             // where the warps' sums, added up a few warps at a time, are long: 16384 x
-            // 512 bf16 13.2 us against 15.2 (65536 x 128: 12.9 against 12.0 with 32)
+            // 512 bf16 13.4 us against 15.3, 32768 x 64 fp32 7.4 against 9.2 (65536 x 128
+            // bf16: 14.4 against 11.2 with 32)
             constexpr int NT = l() * v() * n() > 256 || sizeof(Elem) * v() * n() > 32 ? 512 : 1024;
             return launched(launch_kernel(
                 balance_tokens<Elem, NT, l(), v(), n()>, dim3(static_cast<unsigned>(G)),

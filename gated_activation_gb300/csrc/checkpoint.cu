@@ -107,8 +107,8 @@ template <class I> __device__ __forceinline__ I quotient(I n, I d, const FastDiv
 // whatever the alignment; J = ceil(B / kAnyBlocks) such jobs make a row.  Four
 // blocks of two halves are the eight largest magnitudes that one exchange of
 // lanes finds together (put_blocks).  The single bytes and half words that a
-// lane moves make instructions the bound: 16384 x 767 bf16 takes 28.4 us forward
-// (53%) and 30.5 us backward (61%), against 25.2 and 28.7 us at 768, where the
+// lane moves make instructions the bound: 16384 x 767 bf16 takes 28.7 us forward
+// (52%) and 30.5 us backward (61%), against 25.5 and 29.1 us at 768, where the
 // vectors below take 17.2 and 20.7.
 
 constexpr int kAnyBlocks = 4;
@@ -488,11 +488,13 @@ __device__ __forceinline__ float row_mean(float v, float *red, uint32_t other, f
 // ------------------------------------------------------ sparse, any layout
 //
 // One CTA per row, one element per lane: warp w holds the blocks w, w + NT / 32,
-// ..., V of them, in registers.  Instructions and the row's two barriers bound
-// it: 2000 x 4097 bf16 takes 30.9 us forward (31%; 35.2 with registers for 1024
+// ..., V of them, in registers.  Two things bound it: 89 and 105 instructions per
+// element, which keep the issue slots 66 and 62% busy while the CTAs run, and the wait
+// for a row's loads, since nothing of the next row is on its way during a row's sums
+// and barriers.  2000 x 4097 bf16 takes 30.9 us forward (31%; 35.2 with registers for 1024
 // threads per SM instead of 1536) and 37.8 us backward (32%; with 1536: 46.2), 43.3 and
 // 76.6 us with the row read again for each pass, as the next section does.  Rows in
-// vectors take a third: 2000 x 4096 fp16 13.3 and 18.3 us.
+// vectors take half: 2000 x 4096 fp16 13.3 and 17.4 us.
 
 template <class T, int NT, int V>
 __global__ void __launch_bounds__(NT, 1536 / NT)
@@ -650,7 +652,7 @@ sparse_backward_any(T *__restrict__ grad_in, T *__restrict__ out, const T *__res
 constexpr int kWideThreads = 1024, kWideWarps = kWideThreads / 32;
 
 // One CTA per row; the gate is read again (from L1/L2) for each pass.  100 x 40000
-// bf16: 40.1 us forward, 50.7 us backward (256 threads: 115.6 and 166.9): a row's
+// bf16: 41.0 us forward, 50.7 us backward (256 threads: 115.6 and 166.9): a row's
 // latency bounds so few of them.
 template <class T>
 __global__ void __launch_bounds__(kWideThreads)
@@ -744,8 +746,8 @@ sparse_backward_wide(T *__restrict__ grad_in, T *__restrict__ out, const T *__re
 // statistics and its codes, and four neighbouring lanes hold a block.  All
 // loads are issued before the first sum.  The barriers of the statistics, at
 // which a CTA neither reads nor writes, keep it from the copy rate: 4000 x 4096 bf16
-// takes 22.6 us forward (86%) and 32.9 us backward (74%), 500 x 32768 31.9 and
-// 43.2 us, 8 x 8192 fp32 2.7 and 3.9 us (launch and latency).
+// takes 22.6 us forward (86%), 500 x 32768 31.9 forward and 43.3 us backward (61 and
+// 56%), 300 x 32768 fp32 33.9 us forward, 8 x 8192 fp32 2.7 and 3.9 us (launch and latency).
 
 // The output and the codes of the 8 elements at column c of a row (nothing for
 // c >= d, but the lane takes part in its block's largest magnitudes).
@@ -915,8 +917,8 @@ sparse_backward_vec(T *__restrict__ grad_in, T *__restrict__ out, const T *__res
 // reach it through a ring of S shared-memory slots that cp.async fills S - 1
 // rows ahead, so that HBM keeps streaming while a row is summed and written.  A
 // thread copies just the vectors it will read itself: its own wait_group is
-// all the synchronization that the ring needs.  2048 x 16384 bf16: forward 48.5 us
-// (82%), backward 56.3 us (88%); with_ring_cta has the figures without it.
+// all the synchronization that the ring needs.  2048 x 16384 bf16: forward 48.6 us
+// (82%), backward 57.3 us (87%); with_ring_cta has the figures without it.
 
 template <class T, int NT, int V, int S>
 __global__ void __launch_bounds__(NT, 1024 / NT)
@@ -1199,9 +1201,11 @@ dim3 ring_grid(int nt) { return dim3(static_cast<unsigned>(device_sm_count() * (
 //                  8000 x 2048   4000 x 4096   4000 x 8192   2048 x 16384
 //   forward, us    22.8  25.1    23.2  22.5    44.8  50.2    48.5  62.4
 //   backward, us   29.7  31.0    29.9  32.7    55.3  64.4    56.4  76.3
-// The forward pass leaves out its one loss.  It has two slots, with three 2048 x 16384
-// takes 49.0 us; the backward pass three, with two 65.3.  fp32 rows that wide would not
-// leave room for slots to fill ahead, and reach 91 to 94% of the copy rate without.
+// The forward pass leaves out the class of its one loss, which loses at other sizes too
+// (8000 x 2304 35.7 us against 32.8, 4000 x 3328 21.2 against 20.5).  It has two slots,
+// with three 2048 x 16384 takes 49.0 us; the backward pass three, with two 65.3.  fp32
+// rows that wide would not leave room for slots to fill ahead, and reach 91 to 94% of
+// the copy rate without.
 template <bool FORWARD, class F> bool with_ring_cta(int64_t T, int64_t nv, int *rc, F f) {
     if (nv <= 128 || nv > 2048 || (FORWARD && nv > 256 && nv <= 512))
         return false;

@@ -30,8 +30,8 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2 *red) {
 
 // One CTA per row, the row read again (from L1/L2) for each pass, one element per
 // access: rows wider than the rings hold, and rows whose buffers lie at different
-// offsets.  1000 x 12345 fp16 takes 27.8 us forward and 53.1 us backward (rings: 16.8
-// and 33.0), 100 x 40000 bf16 19.9 and 49 us (with 256 threads 59.1 and 104).
+// offsets.  1000 x 12345 fp16 takes 27.0 us forward and 50.8 us backward (rings: 17.1
+// and 33.2), 100 x 40000 bf16 14.8 and 43.3 us (with 256 threads 52.2 and 97.2).
 template <class T, class W, int NT>
 __global__ void __launch_bounds__(NT)
 ln_forward_wide(T *__restrict__ out, float *__restrict__ mean_out, float *__restrict__ rstd_out,
@@ -200,10 +200,10 @@ template <class W> __device__ __forceinline__ Vec8<W> load_params(const W *p) {
 // register.  Rows of one kind of offset go to one CTA (its rows are a multiple
 // of kKinds apart), so that its threads keep their columns.
 //
-// 16384 x 2048 bf16 with fp32 parameters takes 22.7 us (87%), 4004 x 4096 fp32 22.4 us
-// (86%), 2048 x 16384 bf16 26.6 us (74%: the two barriers of a row that fills the
+// 16384 x 2048 bf16 with fp32 parameters takes 22.8 us (87%), 4004 x 4096 fp32 22.8 us
+// (85%), 2048 x 16384 bf16 26.6 us (74%: the two barriers of a row that fills the
 // CTA).  EDGES costs tests and a dependent load per row: aligned rows through it
-// take 29.6 us at 16384 x 2048; 5000 x 2047 bf16 takes 13.1 us (46%).
+// took 29.6 us at 16384 x 2048; 5000 x 2047 bf16 takes 13.0 us (46%).
 
 constexpr int kKinds = 8;      // rows this far apart have the same offset
 
@@ -526,10 +526,10 @@ ln_forward_vec(T *__restrict__ out, float *__restrict__ mean_out, float *__restr
 // of CL CTAs, `chunk` columns each; the row's two sums are then joined through
 // distributed shared memory, after a barrier that every CTA has started.
 //
-// With the second kernel, 16384 x 2048 bf16 with fp32 parameters takes 37.7 us (79%),
-// 4004 x 4096 fp32 33.6 us (86%), 2048 x 16384 bf16 42.9 us (69%), 800 x 32768 bf16
-// 49.5 us over clusters of two (140.0 with the row read again for each pass); 5000 x
-// 2047 bf16 22.8 us.  The shares, one per SM and column, are written and read
+// With the second kernel, 16384 x 2048 bf16 with fp32 parameters takes 37.9 us (78%),
+// 4004 x 4096 fp32 33.6 us (86%), 2048 x 16384 bf16 43.0 us (69%), 800 x 32768 bf16
+// 49.5 us over clusters of two (140.0 with the row read again for each pass), 800 x 16384
+// fp32 40.5 us over clusters of two; 5000 x 2047 bf16 22.7 us.  The shares, one per SM and column, are written and read
 // again: with few rows they are the larger part (16 x 2048: 4.9 us, two launches).
 
 constexpr int kBackThreads = 512;
@@ -754,8 +754,8 @@ template <class F> int with_types(int dtype, int param_dtype, F f) {
 }
 
 // Calls f(integral constant NT): the threads of a row that no ring takes.  1024
-// for wide ones: 100 x 12345 fp16 forward 7.9 us against 19.2 with 256, 1000 of them 27.8
-// against 25.1, backward 53.1 against 57.2.
+// for wide ones: 100 x 12345 fp16 forward 6.4 us against 17.0 with 256 and backward 17.3
+// against 35.1, 1000 of them 27.0 against 24.2 and 50.8 against 54.9.
 template <class F> int with_threads(int64_t d, F f) {
     return d > 8192 ? f(Const<1024>{}) : f(Const<kThreads>{});
 }
@@ -769,7 +769,7 @@ int64_t shares(int64_t T) {
 // Calls f(integral constants NT, V, S) for the forward ring over rows of nv
 // vectors, 1024 threads per SM; false when it holds no such row.  Two slots, one
 // row ahead, are enough: with four 16384 x 2048 bf16 takes 23.5 us against 22.7,
-// 16384 x 512 7.85 against 7.12 (the first rows reach the SM as one burst).
+// 16384 x 512 8.2 against 7.0 (the first rows reach the SM as one burst).
 template <class F> bool with_forward_ring(int64_t nv, int *rc, F f) {
     constexpr int S = 2;
     if (nv <= 32)
@@ -792,9 +792,9 @@ template <class F> bool with_forward_ring(int64_t nv, int *rc, F f) {
 }
 
 // Calls f(integral constants TPR, V, S, CL) for the backward ring.  Two slots are
-// enough here, too: with six, 192 KB, 16384 x 2048 bf16 takes 42.1 us, with four 40.5,
-// with two 39.6 (the second kernel took 2 us more then than now).  At four vectors per thread the CTA holds one row, and three are
-// better: 2048 x 16384 bf16 44.0 us against 44.5 (likewise).
+// enough here, too: with six, 192 KB, 16384 x 2048 bf16 takes 40.0 us, with four 39.6,
+// with two 38.0.  At four vectors per thread the CTA holds one row, and three are
+// better: 2048 x 16384 bf16 43.1 us against 43.9.
 template <int SIZE, class F> bool with_backward_ring(int64_t nv, int *rc, F f) {
     constexpr int S2 = 2;    // slots at two vectors per thread
     constexpr Const<1> one{};

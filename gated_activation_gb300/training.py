@@ -7,6 +7,13 @@ current one by default), with no fallback.  The marshalling itself is native
 belong to the stream that the call launches on, and calls the C ABI.  Inputs
 live on the device, or in page-locked host memory that the kernels read in
 place.
+
+The functions are the two passes of each operator, not nodes of PyTorch's
+graph: what they return requires no gradient, whatever their inputs do.  Under
+autograd, call them in the forward and the backward of a
+``torch.autograd.Function``.  Rows need columns side by side: a gradient that
+was expanded (``sum().backward()`` hands one over) is refused, and goes in as
+``grad.contiguous()``.
 """
 from __future__ import annotations
 
@@ -154,7 +161,7 @@ def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float,
                      live: torch.Tensor | None = None,
                      stream: torch.cuda.Stream | None = None) -> BalanceLoss:
     """The balance loss of a router's ``logits`` ([T, E] bf16, fp16 or fp32) and
-    its choices ``ids`` ([T, k] int32 or int64), with the per-expert counts.
+    its choices ``ids`` ([T, k] int32 or int64, contiguous), with the per-expert counts.
 
     ``live`` ([T] bool or uint8): a token that is not live takes no part.  An
     id outside [0, E) is a dropped choice and is not counted.

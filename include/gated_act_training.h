@@ -90,7 +90,8 @@ int gelu_and_mul_backward(void *grad_in, void *out, const void *grad_out, const 
 
 /*
  * gelu_and_mul_sparse that also writes its checkpoint.
- *   std  [T] fp32: each row's population standard deviation.
+ *   std  [T] fp32: each row's population standard deviation; exactly 0 for a row
+ *        of one value, of which nothing passes the mask.
  *   Other arguments as gelu_and_mul_sparse_typed and above.
  */
 int gelu_and_mul_sparse_checkpoint(void *out, int8_t *codes, uint8_t *scales, float *std,
@@ -104,8 +105,8 @@ int gelu_and_mul_sparse_checkpoint(void *out, int8_t *codes, uint8_t *scales, fl
  *   g_i - mean  = delta_i + z std,
  *   grad_up     = grad_out * gelu_tanh(s).
  * The cutoff's own dependence on the row is the second term.  A row with
- * std = 0 has no derivative of std; the z term is then left out (every h of
- * such a row is 0).  A position with delta <= 0 adds nothing to the sum,
+ * std = 0 has no derivative of std; the z term is then left out (every h of a
+ * row of one value is 0).  A position with delta <= 0 adds nothing to the sum,
  * whatever grad_out and u hold there.
  */
 int gelu_and_mul_sparse_backward(void *grad_in, void *out, const void *grad_out,
@@ -124,6 +125,9 @@ int gated_act_checkpoint_values(void *values, const int8_t *codes, const uint8_t
  * Layer norm over rows of width d:
  *   mean = sum x / d,  rstd = 1 / sqrt(sum (x - mean)^2 / d + eps),
  *   out = (x - mean) rstd * weight + bias.
+ * A row of one value has it as its mean and, with eps > 0, the bias as its output.
+ * Squares of deviations are fp32 numbers: past 1.8e19 they are infinite (rstd =
+ * 0), and below 1e-19 they lose bits.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -192,7 +196,8 @@ int moe_balance_loss(float *loss, int32_t *counts, int32_t *tokens, float *mean_
 /*
  *   grad_logits [T, E] contiguous, of type dtype: grad_loss times the gradient
  *               above; 0 in the rows of tokens that are not live.
- *   grad_loss   [1] fp32, read on the device.
+ *   grad_loss   [1] fp32, read on the device; where it is not finite, the rows
+ *               that are not live are 0 all the same.
  *   counts, tokens  what moe_balance_loss wrote.
  */
 int moe_balance_loss_backward(void *grad_logits, const float *grad_loss, const void *logits,
