@@ -47,6 +47,11 @@ EXPORTED = (
     "gelu_and_mul_sparse_backward", "gated_act_checkpoint_values", "layer_norm",
     "layer_norm_backward", "layer_norm_backward_workspace_bytes", "moe_balance_loss",
     "moe_balance_loss_backward", "moe_balance_loss_workspace_bytes",
+    "linear_and_mul_workspace_bytes", "linear_silu_and_mul", "linear_gelu_and_mul",
+    "linear_and_mul_backward_workspace_bytes", "linear_silu_and_mul_backward",
+    "linear_gelu_and_mul_backward", "linear_cross_entropy_workspace_bytes",
+    "linear_cross_entropy", "linear_cross_entropy_backward_workspace_bytes",
+    "linear_cross_entropy_backward",
 )
 
 
@@ -54,6 +59,22 @@ class GatedActError(RuntimeError):
     def __init__(self, fn: str, status: int, msg: str):
         super().__init__(f"{fn}: status {status}: {msg}")
         self.status = status
+
+
+class LinearOperands(ctypes.Structure):
+    """Mirror of ``gated_act_linear``."""
+    _fields_ = [("in_", ctypes.c_void_p), ("weight", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("E", "T", "k", "d", "in_stride", "in_batch",
+                                      "weight_stride", "weight_batch")] + [
+        ("dtype", ctypes.c_int), ("n_rows", ctypes.c_void_p)]
+
+
+class VocabularyOperands(ctypes.Structure):
+    """Mirror of ``gated_act_vocabulary``."""
+    _fields_ = [("in_", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("targets", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("T", "k", "V", "in_stride", "weight_stride")] + [
+        ("dtype", ctypes.c_int), ("targets64", ctypes.c_int)]
 
 
 class Plan(ctypes.Structure):
@@ -166,7 +187,20 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             ("moe_balance_loss", c_int,
              [vp, vp, vp, vp, cvp, cvp, cvp, i64, i64, i64, i64, c_int, c_int, f64, vp, size, vp]),
             ("moe_balance_loss_backward", c_int,
-             [vp, cvp, cvp, cvp, cvp, cvp, i64, i64, i64, i64, c_int, f64, vp])):
+             [vp, cvp, cvp, cvp, cvp, cvp, i64, i64, i64, i64, c_int, f64, vp]),
+            # the products next to the activations (gated_act_linear.h)
+            ("linear_and_mul_workspace_bytes", size, [cvp]),
+            ("linear_silu_and_mul", c_int, [vp, vp, vp, cvp, vp, size, vp]),
+            ("linear_gelu_and_mul", c_int, [vp, vp, vp, cvp, vp, size, vp]),
+            ("linear_and_mul_backward_workspace_bytes", size, [cvp]),
+            ("linear_silu_and_mul_backward", c_int,
+             [vp, vp, cvp, i64, i64, cvp, cvp, cvp, vp, size, vp]),
+            ("linear_gelu_and_mul_backward", c_int,
+             [vp, vp, cvp, i64, i64, cvp, cvp, cvp, vp, size, vp]),
+            ("linear_cross_entropy_workspace_bytes", size, [cvp]),
+            ("linear_cross_entropy", c_int, [vp, vp, cvp, vp, size, vp]),
+            ("linear_cross_entropy_backward_workspace_bytes", size, [cvp]),
+            ("linear_cross_entropy_backward", c_int, [vp, vp, cvp, cvp, cvp, vp, size, vp])):
         getattr(lib, fn).restype = restype
         getattr(lib, fn).argtypes = argtypes
     if path is None:
@@ -418,8 +452,10 @@ def squared_relu(x: torch.Tensor, out: torch.Tensor | None = None,
 
 from .training import *  # noqa: E402,F401,F403
 from .training import __all__ as _training_all  # noqa: E402
+from .linear import *  # noqa: E402,F401,F403
+from .linear import __all__ as _linear_all  # noqa: E402
 
 __all__ = ["gelu_and_mul_sparse_native", "gelu_and_mul_sparse_native_plan", "silu_and_mul_bounded", "gelu_and_mul", "squared_relu", "gelu_and_mul_sparse", "gelu_and_mul_sparse_plan", "silu_and_mul", "device_status", "noop",
            "load_library",
            "status_string", "GatedActError", "Plan", "EXPORTED", "LIB_PATH", "workspace_bytes",
-           "new_workspace"] + _training_all
+           "new_workspace"] + _training_all + _linear_all

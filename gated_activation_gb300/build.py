@@ -26,7 +26,8 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libgated_act.so")
 BINDING = os.path.join(LIB_DIR, "_training.so")
 SOURCES = ("api.cu", "gelu_and_mul_sparse.cu", "elementwise.cu",
-           "training.cu", "checkpoint.cu", "layer_norm.cu", "balance.cu")
+           "training.cu", "checkpoint.cu", "layer_norm.cu", "balance.cu",
+           "product.cu", "linear_act.cu", "cross_entropy.cu")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

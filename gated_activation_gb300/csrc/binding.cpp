@@ -1,7 +1,8 @@
-// Python binding of the training operators (gated_act_training.h) against
+// Python binding of the training operators (gated_act_training.h) and of the products
+// next to the activations (gated_act_linear.h) against
 // PyTorch's C++ interface: argument checks, output allocation and one call of
-// the C ABI each.  training.py holds the documented functions, which hand
-// their arguments on in order.
+// the C ABI each.  training.py and linear.py hold the documented functions, which
+// hand their arguments on in order.
 //
 // Why not ctypes here: these calls allocate two to five tensors and launch one
 // or two kernels of a few microseconds.  Measured on the GB300's host, a
@@ -10,6 +11,7 @@
 #include <Python.h>
 
 #include <string>
+#include <vector>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
@@ -18,13 +20,14 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include "gated_act_training.h"
+#include "gated_act_linear.h"
 
 namespace {
 
 using at::Tensor;
 
-PyObject *g_checkpoint, *g_balance, *g_check;   // training.Checkpoint, .BalanceLoss, _check
+// training.Checkpoint, .BalanceLoss, _check; linear.LinearCheckpoint, .CrossEntropy
+PyObject *g_checkpoint, *g_balance, *g_check, *g_linear, *g_entropy;
 
 struct Error {   // becomes a Python exception; an empty message: one is set already
     PyObject *type;
@@ -449,6 +452,171 @@ PyObject *balance_backward(PyObject *const *a) {
     return wrap(grad);
 }
 
+// --------------------------------------------------------- gated projections
+
+void on_device(const Tensor &x, const char *what) {
+    if (!x.is_cuda())
+        value_error(std::string(what) + " must be a CUDA tensor");
+}
+
+int product_code(const Tensor &x, const char *what) {
+    const int code = dtype_code(x.scalar_type());
+    if (code != GATED_ACT_BF16 && code != GATED_ACT_F16)
+        type_error(std::string(what) + " must be bfloat16 or float16");
+    on_device(x, what);
+    return code;
+}
+
+// A matrix [m, n] or a batch [E, m, n] with contiguous columns.
+struct Batch {
+    const Tensor &x;
+    int64_t E, m, n, stride, batch;
+    int code;
+    Batch(PyObject *o, const char *what) : x(tensor(o, what)) {
+        const int64_t dim = x.dim();
+        if (dim != 2 && dim != 3)
+            value_error(std::string(what) + " must be 2-D, or 3-D for a batch of experts");
+        code = product_code(x, what);
+        E = dim == 3 ? x.size(0) : 1;
+        m = x.size(dim - 2);
+        n = x.size(dim - 1);
+        if (x.stride(dim - 1) != 1 && n > 1)
+            value_error(std::string(what) + ": columns must be contiguous");
+        stride = m > 1 ? x.stride(dim - 2) : n;
+        batch = E > 1 ? x.stride(0) : 0;
+    }
+};
+
+// The operands of a call; the shapes agree.
+struct Linear {
+    Batch x, w;
+    gated_act_linear a;
+    Linear(PyObject *in, PyObject *weight, PyObject *n_rows) : x(in, "input"), w(weight, "weight") {
+        if (w.x.dim() != x.x.dim() || w.E != x.E || w.n != x.n || w.code != x.code)
+            value_error("weight must be [2d, k] for rows [T, k], or [E, 2d, k] for [E, T, k], "
+                        "of the input's type");
+        if (w.m % 2 || w.m == 0)
+            value_error("weight must have 2d rows");
+        a = {x.x.data_ptr(), w.x.data_ptr(), x.E,      x.m,      x.n,      w.m / 2,
+             x.stride,       x.batch,        w.stride, w.batch,  x.code,   nullptr};
+        if (n_rows != Py_None) {
+            const Tensor &n = tensor(n_rows, "n_rows");
+            on_device(n, "n_rows");
+            a.n_rows = static_cast<const int32_t *>(flat(n, "n_rows", at::kInt, {x.E}));
+        }
+    }
+    // [T, n], or [E, T, n]
+    std::vector<int64_t> shape(int64_t m, int64_t n) const {
+        return x.x.dim() == 3 ? std::vector<int64_t>{x.E, m, n} : std::vector<int64_t>{m, n};
+    }
+    int64_t scales() const { return gated_act_checkpoint_scales(a.d); }
+};
+
+// (x, weight, n_rows, keep, out, stream)
+template <class F> PyObject *linear(const char *fn, F f, PyObject *const *a) {
+    const Linear l(a[0], a[1], a[2]);
+    const bool keep = truth(a[3]);
+    const Launch go(a[5], l.x.x);
+    const Tensor out = go.output(a[4], l.shape(l.a.T, l.a.d), l.x.x.scalar_type());
+    Tensor codes, scales;
+    if (keep) {
+        codes = go.empty(l.shape(l.a.T, 2 * l.a.d), at::kShort);
+        scales = go.empty(l.shape(l.a.T, l.scales()), at::kByte);
+    }
+    const size_t need = linear_and_mul_workspace_bytes(&l.a);
+    const Tensor ws = need ? go.scratch(need) : Tensor();
+    check(fn, f(out.data_ptr(), keep ? ptr<int16_t>(codes) : nullptr,
+                keep ? ptr<uint8_t>(scales) : nullptr, &l.a, need ? ws.data_ptr() : nullptr, need,
+                go.stream));
+    return keep ? pack(nullptr, wrap(out), pack(g_linear, wrap(codes), wrap(scales))) : wrap(out);
+}
+PyObject *linear_silu(PyObject *const *a) { return linear("linear_silu_and_mul", linear_silu_and_mul, a); }
+PyObject *linear_gelu(PyObject *const *a) { return linear("linear_gelu_and_mul", linear_gelu_and_mul, a); }
+
+// (grad_out, x, weight, kept, n_rows, grad_in, stream)
+template <class F> PyObject *linear_backward(const char *fn, F f, PyObject *const *a) {
+    const Batch g(a[0], "grad_out");
+    const Linear l(a[1], a[2], a[4]);
+    const at::ScalarType type = l.x.x.scalar_type();
+    if (g.x.dim() != l.x.x.dim() || g.E != l.x.E || g.m != l.a.T || g.n != l.a.d || g.code != l.x.code)
+        value_error("grad_out must have the output's shape and type");
+    if (!PyTuple_Check(a[3]) || PyTuple_GET_SIZE(a[3]) != 2)
+        type_error("the fourth argument must be a LinearCheckpoint");
+    const void *codes = flat(tensor(PyTuple_GET_ITEM(a[3], 0), "codes"), "codes", at::kShort,
+                             l.shape(l.a.T, 2 * l.a.d));
+    const void *scales = flat(tensor(PyTuple_GET_ITEM(a[3], 1), "scales"), "scales", at::kByte,
+                              l.shape(l.a.T, l.scales()));
+    const Launch go(a[6], l.x.x);
+    const Tensor grad_in = go.output(a[5], l.shape(l.a.T, l.a.k), type);
+    const Tensor grad_weight = go.empty(l.shape(2 * l.a.d, l.a.k), type);
+    const size_t need = linear_and_mul_backward_workspace_bytes(&l.a);
+    const Tensor ws = need ? go.scratch(need) : Tensor();
+    check(fn, f(grad_in.data_ptr(), grad_weight.data_ptr(), g.x.data_ptr(), g.stride, g.batch,
+                static_cast<const int16_t *>(codes), static_cast<const uint8_t *>(scales), &l.a,
+                need ? ws.data_ptr() : nullptr, need, go.stream));
+    return pack(nullptr, wrap(grad_in), wrap(grad_weight));
+}
+PyObject *linear_silu_backward(PyObject *const *a) {
+    return linear_backward("linear_silu_and_mul_backward", linear_silu_and_mul_backward, a);
+}
+PyObject *linear_gelu_backward(PyObject *const *a) {
+    return linear_backward("linear_gelu_and_mul_backward", linear_gelu_and_mul_backward, a);
+}
+
+// ------------------------------------------------------------- cross entropy
+
+struct Vocabulary {
+    Batch x, w;
+    gated_act_vocabulary a;
+    Vocabulary(PyObject *in, PyObject *weight, PyObject *targets)
+        : x(in, "input"), w(weight, "weight") {
+        if (x.x.dim() != 2 || w.x.dim() != 2 || w.n != x.n || w.code != x.code)
+            value_error("input must be [T, k] and weight [V, k], of one type");
+        const Tensor &t = tensor(targets, "targets");
+        const at::ScalarType type = t.scalar_type();
+        if (type != at::kInt && type != at::kLong)
+            type_error("targets must be int32 or int64");
+        on_device(t, "targets");
+        a = {x.x.data_ptr(), w.x.data_ptr(), flat(t, "targets", type, {x.m}),
+             x.m, x.n, w.m, x.stride, w.stride, x.code, type == at::kLong};
+    }
+};
+
+// (x, weight, targets, stream)
+PyObject *entropy(PyObject *const *a) {
+    const Vocabulary v(a[0], a[1], a[2]);
+    const Launch go(a[3], v.x.x);
+    const Tensor loss = go.empty({v.a.T}, at::kFloat), lse = go.empty({v.a.T}, at::kFloat);
+    const size_t need = linear_cross_entropy_workspace_bytes(&v.a);
+    const Tensor ws = need ? go.scratch(need) : Tensor();
+    check("linear_cross_entropy",
+          linear_cross_entropy(ptr<float>(loss), ptr<float>(lse), &v.a,
+                               need ? ws.data_ptr() : nullptr, need, go.stream));
+    return pack(g_entropy, wrap(loss), wrap(lse));
+}
+
+// (grad_loss, x, weight, targets, kept, stream)
+PyObject *entropy_backward(PyObject *const *a) {
+    const Vocabulary v(a[1], a[2], a[3]);
+    const Tensor &g = tensor(a[0], "grad_loss");
+    on_device(g, "grad_loss");
+    const void *grad_loss = flat(g, "grad_loss", at::kFloat, {v.a.T});
+    if (!PyTuple_Check(a[4]) || PyTuple_GET_SIZE(a[4]) != 2)
+        type_error("the fifth argument must be a CrossEntropy");
+    const void *lse = flat(tensor(PyTuple_GET_ITEM(a[4], 1), "lse"), "lse", at::kFloat, {v.a.T});
+    const Launch go(a[5], v.x.x);
+    const at::ScalarType type = v.x.x.scalar_type();
+    const Tensor grad_in = go.empty({v.a.T, v.a.k}, type), grad_weight = go.empty({v.a.V, v.a.k}, type);
+    const size_t need = linear_cross_entropy_backward_workspace_bytes(&v.a);
+    const Tensor ws = need ? go.scratch(need) : Tensor();
+    check("linear_cross_entropy_backward",
+          linear_cross_entropy_backward(grad_in.data_ptr(), grad_weight.data_ptr(),
+                                        static_cast<const float *>(grad_loss),
+                                        static_cast<const float *>(lse), &v.a,
+                                        need ? ws.data_ptr() : nullptr, need, go.stream));
+    return pack(nullptr, wrap(grad_in), wrap(grad_weight));
+}
+
 // -------------------------------------------------------------------- module
 
 // N positional arguments to f; C++ exceptions to Python's.
@@ -475,17 +643,19 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return nullptr;
 }
 
-// (Checkpoint, BalanceLoss, check)
+// (Checkpoint, BalanceLoss, check, LinearCheckpoint, CrossEntropy)
 PyObject *set_up(PyObject *const *a) {
     g_checkpoint = Py_NewRef(a[0]);
     g_balance = Py_NewRef(a[1]);
     g_check = Py_NewRef(a[2]);
+    g_linear = Py_NewRef(a[3]);
+    g_entropy = Py_NewRef(a[4]);
     return none();
 }
 
 #define ENTRY(name, f, n) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {
-    ENTRY("set_up", set_up, 3),
+    ENTRY("set_up", set_up, 5),
     ENTRY("silu_and_mul_checkpoint", silu_checkpoint, 5),
     ENTRY("gelu_and_mul_checkpoint", gelu_checkpoint, 5),
     ENTRY("gelu_and_mul_sparse_checkpoint", sparse_checkpoint, 5),
@@ -497,6 +667,12 @@ PyMethodDef g_methods[] = {
     ENTRY("layer_norm_backward", norm_backward, 7),
     ENTRY("moe_balance_loss", balance, 5),
     ENTRY("moe_balance_loss_backward", balance_backward, 5),
+    ENTRY("linear_silu_and_mul", linear_silu, 6),
+    ENTRY("linear_gelu_and_mul", linear_gelu, 6),
+    ENTRY("linear_silu_and_mul_backward", linear_silu_backward, 7),
+    ENTRY("linear_gelu_and_mul_backward", linear_gelu_backward, 7),
+    ENTRY("linear_cross_entropy", entropy, 4),
+    ENTRY("linear_cross_entropy_backward", entropy_backward, 6),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_training", nullptr, -1, g_methods,

@@ -154,6 +154,10 @@ cudaError_t launch_kernel(void (*kernel)(Exp...), dim3 grid, dim3 block, size_t 
 // Record a CUDA error for gated_act_last_cuda_error() and map it to a status.
 int cuda_status(cudaError_t e);
 
+// Read and clear the status words of the translation units with bounded waits, into *flags.
+cudaError_t take_linear_act_status(unsigned int *flags);
+cudaError_t take_cross_entropy_status(unsigned int *flags);
+
 // The address kernels use for `p`: device (and managed) memory as is;
 // page-locked host memory through its device mapping.  Sets *host when the
 // bytes live in host memory.  Returns GATED_ACT_OK, or GATED_ACT_ERR_HOST for

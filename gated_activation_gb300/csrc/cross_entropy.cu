@@ -1,0 +1,734 @@
+// Cross entropy of in W' over a large vocabulary, the logits never kept.
+//
+//   live_tokens   numbers the tokens that take part; where some do not, copies their
+//                 rows side by side, so that the products run over live rows alone.
+//   forward       one product kernel whose epilogue leaves each row's maximum and sum of
+//                 exponentials over a tile's 256 columns, and the target's logit; a second
+//                 kernel joins them.
+//   backward      for each piece of the vocabulary: the logits again, with y = (p - [target])
+//                 grad_loss as the epilogue; y W added to grad_in's sums; y' in as the
+//                 piece's rows of grad_weight.
+#include "product.cuh"
+
+#include "gated_act_linear.h"
+
+namespace gact {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ------------------------------------------------------------------ live tokens
+
+// What live_tokens writes; `row` counts live tokens.
+struct Tokens {
+    int32_t *count;     // [1] live tokens
+    int32_t *token;     // [T] the token of a row
+    int32_t *goal;      // [T] its target
+    float *shift;       // [T] its lse in powers of two        (backward)
+    float *weight;      // [T] its grad_loss / 2^e             (backward)
+    float *power;       // [1] 2^e                             (backward)
+};
+
+template <class T> struct TokenArgs {
+    const void *targets;
+    const T *in;
+    const float *grad_loss, *lse;   // backward
+    float *loss_out, *lse_out;      // forward: 0 at dead tokens
+    T *grad_in;                     // backward: 0 at dead tokens
+    T *rows;                        // copies of live rows, zeros up to a whole step
+    Tokens t;
+    int64_t in_stride;
+    int n, k, kp, V, segment;
+    bool wide, copy;                // copy: also where every token is live
+};
+
+__device__ __forceinline__ int block_sum_int(int v, int *red) {
+    v = __reduce_add_sync(0xFFFFFFFFu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int s = 0;
+    for (int i = 0; i < 8; ++i)
+        s += red[i];
+    return s;
+}
+
+// Each block numbers a segment of the tokens.  It counts those in front of it itself (the
+// targets are few bytes and stay in L2), so that no block waits for another.
+template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<T> g) {
+    __shared__ int red[8];
+    __shared__ int list[256];
+    pdl_wait();
+    pdl_trigger();
+    const auto target = [&](int i) -> int {
+        const int64_t v = g.wide ? static_cast<const int64_t *>(g.targets)[i]
+                                 : static_cast<const int32_t *>(g.targets)[i];
+        return v >= 0 && v < g.V ? static_cast<int>(v) : -1;
+    };
+    const int begin = blockIdx.x * g.segment, end = min(begin + g.segment, g.n);
+    int before = 0, all = 0;
+    float top = 0.f;
+    for (int i = threadIdx.x; i < g.n; i += 256) {
+        const bool live = target(i) >= 0;
+        all += live;
+        before += live && i < begin;
+        if (g.grad_loss && live)
+            top = fmaxf(top, fabsf(g.grad_loss[i]));
+    }
+    all = block_sum_int(all, red);
+    before = block_sum_int(before, red);
+    float power = 1.f;
+    if (g.grad_loss) {
+        const int bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_int(top));   // top >= 0
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0)
+            red[threadIdx.x >> 5] = bits;
+        __syncthreads();
+        int most = 0;
+        for (int i = 0; i < 8; ++i)
+            most = max(most, red[i]);
+        // the power of two in it, within what has a normal inverse; 1 for 0 and infinity
+        const int e = min(max(most >> 23, 1), 253);
+        power = most == 0 || most >= 0x7F800000 ? 1.f : __int_as_float(e << 23);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *g.t.count = all;
+        if (g.grad_loss)
+            *g.t.power = power;
+    }
+    const bool copy = g.copy || all < g.n;
+    for (int i0 = begin; i0 < end; i0 += 256) {
+        const int i = i0 + threadIdx.x, goal = i < end ? target(i) : -1;
+        const bool live = goal >= 0;
+        // the rank of a live token among this turn's
+        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, live);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0)
+            red[threadIdx.x >> 5] = __popc(votes);
+        list[threadIdx.x] = -1;
+        __syncthreads();
+        int rank = __popc(votes & ((1u << (threadIdx.x & 31)) - 1)), turn = 0;
+        for (int w = 0; w < 8; ++w) {
+            if (w < static_cast<int>(threadIdx.x >> 5))
+                rank += red[w];
+            turn += red[w];
+        }
+        if (live) {
+            const int row = before + rank;
+            list[threadIdx.x] = row;
+            g.t.token[row] = i;
+            g.t.goal[row] = goal;
+            if (g.grad_loss) {
+                g.t.shift[row] = g.lse[i] * kLog2e;
+                g.t.weight[row] = g.grad_loss[i] / power;
+            }
+        } else if (i < end && g.loss_out) {
+            g.loss_out[i] = 0.f;
+            g.lse_out[i] = 0.f;
+        }
+        __syncthreads();
+        // rows: copied where they are packed, zero gradients where they are dead
+        if (copy || g.grad_in)
+            for (int j = threadIdx.x >> 5; j < 256 && i0 + j < end; j += 8) {
+                const int row = list[j];
+                if (row >= 0 && copy) {
+                    const T *from = g.in + (i0 + j) * g.in_stride;
+                    T *to = g.rows + int64_t(row) * g.kp;
+                    if (((reinterpret_cast<uintptr_t>(from) | reinterpret_cast<uintptr_t>(to)) & 15) == 0) {
+                        int c = (threadIdx.x & 31) * 8;
+                        for (; c + 8 <= g.k; c += 256)
+                            st_vec(to + c, ld_stream(from + c));
+                        for (int x = c; x < g.k && x < c + 8; ++x)
+                            to[x] = from[x];
+                    } else {
+                        for (int c = threadIdx.x & 31; c < g.k; c += 32)
+                            to[c] = from[c];
+                    }
+                } else if (row < 0 && g.grad_in) {
+                    T *to = g.grad_in + int64_t(i0 + j) * g.k;
+                    if ((reinterpret_cast<uintptr_t>(to) & 15) == 0) {
+                        int c = (threadIdx.x & 31) * 8;
+                        for (; c + 8 <= g.k; c += 256)
+                            st_vec(to + c, make_uint4(0, 0, 0, 0));
+                        for (int x = c; x < g.k && x < c + 8; ++x)
+                            to[x] = from_float<T>(0.f);
+                    } else {
+                        for (int c = threadIdx.x & 31; c < g.k; c += 32)
+                            to[c] = from_float<T>(0.f);
+                    }
+                }
+            }
+        before += turn;
+        __syncthreads();
+    }
+    // zeros from the live rows to a whole step of a sum over them
+    if (copy && blockIdx.x == 0) {
+        const int64_t from = int64_t(all) * g.kp, to = int64_t((all + kStep - 1) / kStep * kStep) * g.kp;
+        for (int64_t c = from + threadIdx.x; c < to; c += 256)
+            g.rows[c] = from_float<T>(0.f);
+    }
+}
+
+// ------------------------------------------------------------- products of logits
+
+// Copies of the operands of logits [rows, from `first` on]: packed rows where some token is dead.
+template <class G>
+__device__ __forceinline__ void load_logits(const G &g, const Tile &t, int first, int step, uint32_t rank,
+                                            uint32_t a, uint32_t b, uint32_t bar) {
+    load_along(a, t.rows < g.capacity ? &g.other : &g.a, bar, step * kStep,
+               t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
+    load_along(b, &g.b, bar, step * kStep, first + t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, 0);
+}
+
+// Maximum (in powers of two) and sum of exponentials of each row over a tile's columns.
+template <class T> struct Statistics {
+    using Elem = T;
+    static constexpr bool kAAcross = false, kBAcross = false, kLiveRows = true;
+    struct Args {
+        const int32_t *goal;
+        float2 *part;        // [tiles, capacity]: maximum, sum
+        float *at_goal;      // [capacity]
+        int V;
+    };
+    using G = Product<Statistics>;
+    __device__ static int batch_of(int) { return 0; }
+    __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
+                                uint32_t b, uint32_t bar) {
+        load_logits(g, t, 0, step, rank, a, b, bar);
+    }
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
+        const int r = t.m0 + row;
+        const bool mine = r < t.rows;
+        const int first = t.n0 * kTile, goal = mine ? g.j.goal[r] - first : -1;
+        float top = -INFINITY, sum = 0.f;
+        for (int c = 0; c < kTile && first + c < g.j.V; c += 32) {
+            float v[32];
+            sums_load32(sums + c, v);
+            sums_load_wait();
+            if (goal >= c && goal < c + 32) {
+                float at = 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    at = goal - c == i ? v[i] : at;
+                g.j.at_goal[r] = at;
+            }
+            const int n = g.j.V - first - c;
+            if (n < 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    v[i] = i < n ? v[i] : -INFINITY;
+            }
+            float most = top;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                v[i] *= kLog2e;
+                most = fmaxf(most, v[i]);
+            }
+            // a row of -infinity alone has no exponential: its maximum is taken as 0
+            const float base = most == -INFINITY ? 0.f : most;
+            sum *= exp2_fast(top - base);
+            top = most;
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                part[i & 3] += exp2_fast(v[i] - base);
+            sum += (part[0] + part[1]) + (part[2] + part[3]);
+        }
+        if (mine)
+            g.j.part[int64_t(t.n0) * g.capacity + r] = make_float2(top, sum);
+    }
+};
+
+// y = (exp(l - lse) - [target]) weight, times 2^14 in fp16 (whose smallest normal number,
+// 2^-14, a probability in a large vocabulary often falls below; |y| <= 2^15 then).
+template <class T> constexpr float kLift = std::is_same_v<T, f16> ? 16384.f : 1.f;
+
+template <class T> struct Slopes {
+    using Elem = T;
+    static constexpr bool kAAcross = false, kBAcross = false, kLiveRows = true;
+    struct Args {
+        Tokens t;
+        T *y;              // [padded, piece]
+        int V, first, piece;
+    };
+    using G = Product<Slopes>;
+    __device__ static int batch_of(int) { return 0; }
+    __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
+                                uint32_t b, uint32_t bar) {
+        load_logits(g, t, g.j.first, step, rank, a, b, bar);
+    }
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
+        const int r = t.m0 + row;
+        const bool mine = r < t.rows, write = r < (t.rows + kStep - 1) / kStep * kStep;
+        const int first = g.j.first + t.n0 * kTile;
+        const int goal = mine ? g.j.t.goal[r] - first : -1;
+        const float shift = mine ? g.j.t.shift[r] : 0.f;
+        const float weight = mine ? g.j.t.weight[r] * kLift<T> : 0.f;
+        T *y = g.j.y + int64_t(r) * g.j.piece + t.n0 * kTile;
+        for (int c = 0; c < kTile && t.n0 * kTile + c < g.j.piece; c += 32) {
+            float v[32];
+            sums_load32(sums + c, v);
+            sums_load_wait();
+            if (!write)
+                continue;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                v[i] = exp2_fast(fmaf(v[i], kLog2e, -shift));
+            if (goal >= c && goal < c + 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    v[i] -= goal - c == i ? 1.f : 0.f;
+            }
+            const int n = g.j.V - first - c;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                v[i] = mine && i < n ? v[i] * weight : 0.f;
+            store32(y + c, v, 32, true);
+        }
+    }
+};
+
+// grad_in += y W over one piece: A = y along the sum, B = the weight across it.
+template <class T> struct PieceGradIn {
+    using Elem = T;
+    static constexpr bool kAAcross = false, kBAcross = true, kLiveRows = true;
+    struct Args {
+        Tokens t;
+        T *out;              // [T, k]
+        float *sums;         // [rows, k]
+        int k, first;
+        bool begin, end, vec;
+    };
+    using G = Product<PieceGradIn>;
+    __device__ static int batch_of(int) { return 0; }
+    __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
+                                uint32_t b, uint32_t bar) {
+        load_along(a, &g.a, bar, step * kStep, t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
+        load_across(b, &g.b, bar, g.j.first + step * kStep,
+                    t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, 0);
+    }
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
+        const int k = g.j.k, r = t.m0 + row;
+        const bool mine = r < t.rows;
+        const float power = g.j.end ? *g.j.t.power * (1.f / kLift<T>) : 1.f;
+        const int64_t token = mine && g.j.end ? g.j.t.token[r] : 0;
+        for (int c = 0; c < kTile && t.n0 * kTile + c < k; c += 32) {
+            float v[32];
+            sums_load32(sums + c, v);
+            sums_load_wait();
+            if (!mine)
+                continue;
+            const int col = t.n0 * kTile + c, n = k - col;
+            float *held = g.j.sums + int64_t(r) * k + col;
+            if (!g.j.begin) {
+                if (g.j.vec && n >= 32) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 h = *reinterpret_cast<const float4 *>(held + i);
+                        v[i] += h.x;
+                        v[i + 1] += h.y;
+                        v[i + 2] += h.z;
+                        v[i + 3] += h.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] += i < n ? held[i] : 0.f;
+                }
+            }
+            if (g.j.end) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    v[i] *= power;
+                store32(g.j.out + token * k + col, v, n, g.j.vec);
+            } else if (g.j.vec && n >= 32) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<float4 *>(held + i) =
+                        make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i < n)
+                        held[i] = v[i];
+            }
+        }
+    }
+};
+
+// A piece's rows of grad_weight: A = y across the sum over the live rows, B = in across it.
+template <class T> struct PieceGradWeight {
+    using Elem = T;
+    static constexpr bool kAAcross = true, kBAcross = true, kLiveRows = false;
+    struct Args {
+        const float *power;
+        T *out;              // the piece's first row
+        int k;
+        bool vec;
+    };
+    using G = Product<PieceGradWeight>;
+    __device__ static int batch_of(int) { return 0; }
+    __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
+                                uint32_t b, uint32_t bar) {
+        load_across(a, &g.a, bar, step * kStep, t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
+        load_across(b, g.live_of(0) < g.capacity ? &g.other : &g.b, bar, step * kStep,
+                    t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, 0);
+    }
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
+        const int k = g.j.k, r = t.m0 + row;
+        const float power = t.steps ? *g.j.power * (1.f / kLift<T>) : 0.f;
+        for (int c = 0; c < kTile && t.n0 * kTile + c < k; c += 32) {
+            float v[32];
+            sums_load32(sums + c, v);
+            sums_load_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                v[i] = t.steps ? v[i] * power : 0.f;
+            const int col = t.n0 * kTile + c;
+            if (r < t.rows)
+                store32(g.j.out + int64_t(r) * k + col, v, k - col, g.j.vec);
+        }
+    }
+};
+
+// ----------------------------------------------------------------------- the join
+
+struct JoinArgs {
+    const float2 *part;
+    const float *at_goal;
+    const int32_t *count, *token;
+    float *loss, *lse;
+    int capacity, tiles;
+};
+
+// 32 rows per block, a row per lane; the warps take a share of the tiles each.
+__global__ void __launch_bounds__(256) join_statistics(JoinArgs g) {
+    __shared__ float2 share[8][32];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x * 32 + lane;
+    const bool mine = r < *g.count;
+    float top = -INFINITY, sum = 0.f;
+    const auto add = [&](float2 p) {
+        const float most = fmaxf(top, p.x), base = most == -INFINITY ? 0.f : most;
+        sum = sum * exp2_fast(top - base) + p.y * exp2_fast(p.x - base);
+        top = most;
+    };
+    if (mine)
+        for (int i = warp; i < g.tiles; i += 8)
+            add(g.part[int64_t(i) * g.capacity + r]);
+    share[warp][lane] = make_float2(top, sum);
+    __syncthreads();
+    if (warp || !mine)
+        return;
+    for (int i = 1; i < 8; ++i)
+        add(share[i][lane]);
+    const float lse = (top + log2f(sum)) * kLn2;
+    const int i = g.token[r];
+    g.lse[i] = lse;
+    g.loss[i] = lse - g.at_goal[r];
+}
+
+// ------------------------------------------------------------------ host side
+
+int check_sizes(const gated_act_vocabulary &a) {
+    if (a.T < 0 || a.k <= 0 || a.V <= 0)
+        return GATED_ACT_ERR_SIZE;
+    if (a.dtype != GATED_ACT_BF16 && a.dtype != GATED_ACT_F16)
+        return GATED_ACT_ERR_DTYPE;
+    if (a.T > kMaxWidth || a.k > kMaxWidth || a.V > kMaxWidth || a.in_stride > kMaxRows ||
+        a.weight_stride > kMaxRows)
+        return GATED_ACT_ERR_TOO_LARGE;
+    if (a.in_stride < a.k || a.weight_stride < a.k)
+        return GATED_ACT_ERR_STRIDE;
+    const double most = 2147479552.0;   // 32-bit tile numbers
+    const auto tiles = [&](int64_t x, int64_t y) {
+        return static_cast<double>(ceil_div64(x, kTile)) * static_cast<double>(ceil_div64(y, kTile));
+    };
+    if (tiles(a.T, a.V) >= most || tiles(a.T, a.k) >= most || tiles(a.V, a.k) >= most)
+        return GATED_ACT_ERR_TOO_LARGE;
+    return GATED_ACT_OK;
+}
+
+Region in_region(const gated_act_vocabulary &a) {
+    return {a.in, span_bytes(a.T, a.in_stride, a.k, 2), 2, false};
+}
+Region weight_region(const gated_act_vocabulary &a) {
+    return {a.weight, span_bytes(a.V, a.weight_stride, a.k, 2), 2, false};
+}
+Region target_region(const gated_act_vocabulary &a) {
+    const int64_t size = a.targets64 ? 8 : 4;
+    return {a.targets, static_cast<uint64_t>(a.T * size), static_cast<uintptr_t>(size), false};
+}
+
+// Columns of one piece of the vocabulary: y takes about 64 MB, so that the two products that
+// read it find it in L2, but 8192 columns at least, so that adding to grad_in's sums
+// (8 bytes per row and column of it) stays small beside the product.
+int64_t piece_of(const gated_act_vocabulary &a) {
+    const int64_t rows = ceil_div64(a.T, kStep) * kStep;
+    int64_t n = (int64_t(32) << 20) / rows / kTile * kTile;
+    n = n < 8192 ? 8192 : n;
+    const int64_t all = ceil_div64(a.V, kTile) * kTile;
+    return n < all ? n : all;
+}
+
+// The parts of a workspace.
+struct Parts {
+    Layout in, packed, weight;
+    Tokens t = {};
+    float2 *part = nullptr;
+    float *at_goal = nullptr, *sums = nullptr;
+    void *y = nullptr;
+    int64_t kp, padded, piece;
+    bool copy;
+    uint64_t bytes;
+    int rc;
+    Parts(const gated_act_vocabulary &a, bool backward, void *workspace, cudaStream_t stream)
+        : in{a.in, {a.k, a.T, 1, 1}, {1, a.in_stride, 0, 0}},
+          weight{a.weight, {a.k, a.V, 1, 1}, {1, a.weight_stride, 0, 0}} {
+        kp = ceil_div64(a.k, 8) * 8;
+        padded = ceil_div64(a.T, kStep) * kStep;
+        piece = piece_of(a);
+        copy = !tma_addressable(in);
+        Carve ws(workspace);
+        t.count = ws.take<int32_t>(4);
+        t.token = ws.take<int32_t>(4 * a.T);
+        t.goal = ws.take<int32_t>(4 * a.T);
+        packed = {ws.take<void>(2 * padded * kp), {a.k, padded, 1, 1}, {1, kp, 0, 0}};
+        if (backward) {
+            t.shift = ws.take<float>(4 * a.T);
+            t.weight = ws.take<float>(4 * a.T);
+            t.power = ws.take<float>(4);
+            y = ws.take<void>(2 * padded * piece);
+            sums = ws.take<float>(piece < a.V ? 4 * a.T * a.k : 0);
+        } else {
+            part = ws.take<float2>(8 * ceil_div64(a.V, kTile) * a.T);
+            at_goal = ws.take<float>(4 * a.T);
+        }
+        rc = GATED_ACT_OK;
+        if (!tma_addressable(weight)) {
+            const Layout to = packed_layout(weight, ws.take<void>(packed_bytes(weight)));
+            if (workspace)
+                rc = launch_pack(to, weight, stream);
+            weight = to;
+        }
+        bytes = ws.used;
+    }
+};
+
+template <class T>
+int run_live_tokens(const Parts &w, const gated_act_vocabulary &a, const float *grad_loss,
+                    const float *lse, float *loss_out, float *lse_out, void *grad_in,
+                    cudaStream_t stream) {
+    TokenArgs<T> g;
+    g.targets = a.targets;
+    g.in = static_cast<const T *>(a.in);
+    g.grad_loss = grad_loss;
+    g.lse = lse;
+    g.loss_out = loss_out;
+    g.lse_out = lse_out;
+    g.grad_in = static_cast<T *>(grad_in);
+    g.rows = static_cast<T *>(const_cast<void *>(w.packed.data));
+    g.t = w.t;
+    g.in_stride = a.in_stride;
+    g.n = static_cast<int>(a.T);
+    g.k = static_cast<int>(a.k);
+    g.kp = static_cast<int>(w.kp);
+    g.V = static_cast<int>(a.V);
+    g.wide = a.targets64 != 0;
+    g.copy = w.copy;
+    const int64_t segment = ceil_div64(a.T, 1024);   // at most 1024 blocks count the targets
+    g.segment = static_cast<int>(segment < 32 ? 32 : segment);
+    const unsigned grid = static_cast<unsigned>(ceil_div64(a.T, g.segment));
+    return cuda_status(launch_kernel(live_tokens<T>, dim3(grid), dim3(256), 0, stream, 1, g));
+}
+
+template <class J>
+void set_rows(Product<J> *g, const Parts &w, const gated_act_vocabulary &a) {
+    g->live = w.t.count;
+    g->batches = 1;
+    g->capacity = g->rows = static_cast<int>(a.T);
+}
+
+// Maps of the live rows: in place, and packed.
+template <class T> int encode_rows(CUtensorMap *place, CUtensorMap *packed, const Parts &w, int rows) {
+    constexpr bool is_bf16 = std::is_same_v<T, bf16>;
+    const int rc = encode_map(packed, w.packed, rows, is_bf16);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    if (w.copy) {
+        *place = *packed;
+        return rc;
+    }
+    return encode_map(place, w.in, rows, is_bf16);
+}
+
+template <class T>
+int run_forward(float *loss, float *lse, const gated_act_vocabulary &a, void *workspace,
+                cudaStream_t stream) {
+    const Parts w(a, false, workspace, stream);
+    int rc = w.rc;
+    if (rc == GATED_ACT_OK)
+        rc = run_live_tokens<T>(w, a, nullptr, nullptr, loss, lse, nullptr, stream);
+    Product<Statistics<T>> g;
+    if (rc == GATED_ACT_OK)
+        rc = encode_rows<T>(&g.a, &g.other, w, kHalf);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&g.b, w.weight, kHalf, std::is_same_v<T, bf16>);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    set_rows(&g, w, a);
+    g.n_tiles = static_cast<int>(ceil_div64(a.V, kTile));
+    g.steps = static_cast<int>(ceil_div64(a.k, kStep));
+    g.j = {w.t.goal, w.part, w.at_goal, static_cast<int>(a.V)};
+    rc = launch_product(g, ceil_div64(a.T, kTile) * g.n_tiles, stream);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    const JoinArgs j = {w.part, w.at_goal, w.t.count, w.t.token, loss, lse,
+                        static_cast<int>(a.T), g.n_tiles};
+    return cuda_status(launch_kernel(join_statistics, dim3(static_cast<unsigned>(ceil_div64(a.T, 32))),
+                                     dim3(256), 0, stream, 1, j));
+}
+
+template <class T>
+int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const float *lse,
+                 const gated_act_vocabulary &a, void *workspace, cudaStream_t stream) {
+    constexpr bool is_bf16 = std::is_same_v<T, bf16>;
+    const Parts w(a, true, workspace, stream);
+    int rc = w.rc;
+    if (rc == GATED_ACT_OK)
+        rc = run_live_tokens<T>(w, a, grad_loss, lse, nullptr, nullptr, grad_in, stream);
+    const int k = static_cast<int>(a.k);
+    const bool vec = a.k % 8 == 0 && aligned(grad_in, 16) && aligned(grad_weight, 16);
+
+    Product<Slopes<T>> s;
+    Product<PieceGradIn<T>> gi;
+    Product<PieceGradWeight<T>> gw;
+    if (rc == GATED_ACT_OK)
+        rc = encode_rows<T>(&s.a, &s.other, w, kHalf);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&s.b, w.weight, kHalf, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&gi.b, w.weight, kStep, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = encode_rows<T>(&gw.b, &gw.other, w, kStep);
+    for (int64_t first = 0; first < a.V && rc == GATED_ACT_OK; first += w.piece) {
+        const int64_t cols = a.V - first < w.piece ? a.V - first : w.piece;
+        const Layout y = {w.y, {cols, w.padded, 1, 1}, {1, w.piece, 0, 0}};
+        set_rows(&s, w, a);
+        s.n_tiles = static_cast<int>(ceil_div64(cols, kTile));
+        s.steps = static_cast<int>(ceil_div64(a.k, kStep));
+        s.j = {w.t, static_cast<T *>(w.y), static_cast<int>(a.V), static_cast<int>(first),
+               static_cast<int>(w.piece)};
+        rc = launch_product(s, ceil_div64(a.T, kTile) * s.n_tiles, stream);
+
+        if (rc == GATED_ACT_OK)
+            rc = encode_map(&gi.a, y, kHalf, is_bf16);
+        if (rc != GATED_ACT_OK)
+            return rc;
+        gi.other = gi.a;
+        set_rows(&gi, w, a);
+        gi.n_tiles = static_cast<int>(ceil_div64(a.k, kTile));
+        gi.steps = static_cast<int>(ceil_div64(cols, kStep));
+        gi.j = {w.t,   static_cast<T *>(grad_in), w.sums, k, static_cast<int>(first),
+                first == 0, first + cols == a.V,  vec};
+        rc = launch_product(gi, ceil_div64(a.T, kTile) * gi.n_tiles, stream);
+
+        if (rc == GATED_ACT_OK)
+            rc = encode_map(&gw.a, y, kStep, is_bf16);
+        if (rc != GATED_ACT_OK)
+            return rc;
+        set_rows(&gw, w, a);
+        gw.rows = static_cast<int>(cols);
+        gw.n_tiles = gi.n_tiles;
+        gw.steps = 0;
+        gw.j = {w.t.power, static_cast<T *>(grad_weight) + first * a.k, k, vec};
+        rc = launch_product(gw, ceil_div64(cols, kTile) * gw.n_tiles, stream);
+    }
+    return rc;
+}
+
+}  // namespace
+
+cudaError_t take_cross_entropy_status(unsigned int *flags) { return take_product_status(flags); }
+
+}  // namespace gact
+
+using gact::check_sizes;
+using gact::Region;
+
+extern "C" {
+
+size_t linear_cross_entropy_workspace_bytes(const gated_act_vocabulary *a) {
+    if (!a || check_sizes(*a) != GATED_ACT_OK || a->T == 0)
+        return 0;
+    return gact::Parts(*a, false, nullptr, nullptr).bytes;
+}
+
+size_t linear_cross_entropy_backward_workspace_bytes(const gated_act_vocabulary *a) {
+    if (!a || check_sizes(*a) != GATED_ACT_OK || a->T == 0)
+        return 0;
+    return gact::Parts(*a, true, nullptr, nullptr).bytes;
+}
+
+int linear_cross_entropy(float *loss, float *lse, const gated_act_vocabulary *a, void *workspace,
+                         size_t workspace_bytes, cudaStream_t stream) {
+    if (!a)
+        return GATED_ACT_ERR_NULL;
+    int rc = check_sizes(*a);
+    if (rc != GATED_ACT_OK || a->T == 0)
+        return rc;
+    const size_t need = linear_cross_entropy_workspace_bytes(a);
+    if (workspace_bytes < need)
+        return GATED_ACT_ERR_SCRATCH;
+    const uint64_t each = static_cast<uint64_t>(a->T) * 4;
+    Region r[] = {{loss, each, 4, true},     {lse, each, 4, true},
+                  gact::in_region(*a),       gact::weight_region(*a),
+                  gact::target_region(*a),   {workspace, need, 16, true}};
+    rc = gact::check_device_regions(r, 6);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    return a->dtype == GATED_ACT_BF16
+               ? gact::run_forward<gact::bf16>(loss, lse, *a, workspace, stream)
+               : gact::run_forward<gact::f16>(loss, lse, *a, workspace, stream);
+}
+
+int linear_cross_entropy_backward(void *grad_in, void *grad_weight, const float *grad_loss,
+                                  const float *lse, const gated_act_vocabulary *a, void *workspace,
+                                  size_t workspace_bytes, cudaStream_t stream) {
+    if (!a)
+        return GATED_ACT_ERR_NULL;
+    int rc = check_sizes(*a);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    const size_t need = linear_cross_entropy_backward_workspace_bytes(a);
+    if (workspace_bytes < need)
+        return GATED_ACT_ERR_SCRATCH;
+    const uint64_t each = static_cast<uint64_t>(a->T) * 4;
+    const uint64_t weight_bytes = static_cast<uint64_t>(a->V * a->k) * 2;
+    Region r[] = {{grad_in, static_cast<uint64_t>(a->T * a->k) * 2, 2, true},
+                  {grad_weight, weight_bytes, 2, true},
+                  {grad_loss, each, 4, false},
+                  {lse, each, 4, false},
+                  gact::in_region(*a),
+                  gact::weight_region(*a),
+                  gact::target_region(*a),
+                  {workspace, need, 16, true}};
+    rc = gact::check_device_regions(r, 8);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    if (a->T == 0)   // sums over no tokens
+        return gact::cuda_status(cudaMemsetAsync(grad_weight, 0, weight_bytes, stream));
+    return a->dtype == GATED_ACT_BF16
+               ? gact::run_backward<gact::bf16>(grad_in, grad_weight, grad_loss, lse, *a, workspace, stream)
+               : gact::run_backward<gact::f16>(grad_in, grad_weight, grad_loss, lse, *a, workspace, stream);
+}
+
+}  // extern "C"

@@ -2323,6 +2323,10 @@ extern "C" int gated_act_device_status(unsigned int *flags) {
         return gact::cuda_status(e);
     const unsigned int zero = 0;
     e = cudaMemcpyToSymbol(gact::g_device_status, &zero, sizeof zero);
+    if (e == cudaSuccess)
+        e = gact::take_linear_act_status(&v);
+    if (e == cudaSuccess)
+        e = gact::take_cross_entropy_status(&v);
     if (e != cudaSuccess)
         return gact::cuda_status(e);
     *flags = v;

@@ -1,0 +1,588 @@
+// Gated projections: both products of a gated MLP's up half with the activation as
+// their epilogue, and their backward pass.
+//
+//   forward   (g, u) = in (Wg, Wu)',  out = act(g) u: one product kernel.  A pair's tile
+//             holds 128 columns of g and the same 128 of u, so that a thread has both.
+//   backward  dg = grad_out u act'(g), du = grad_out act(g) from the kept g and u (one pass
+//             over memory), then grad_in = (dg, du) W and grad_weight = (dg, du)' in.
+#include "product.cuh"
+
+#include "gated_act_linear.h"
+
+namespace gact {
+namespace {
+
+constexpr int kBlock = 32;   // elements under one scale
+
+// ------------------------------------------------------- 16-bit checkpoints
+
+// The scale byte of a block whose largest magnitude is `top`: 2^(e - 127) is the smallest
+// power of two of which `top` is at most 32767 multiples, after rounding.  Adding 2^8 to
+// the bits carries a mantissa of 2 - 2^-15 or more, which would round to 2^15 multiples,
+// into the exponent.
+__device__ __forceinline__ uint32_t scale_of(float top) {
+    const uint32_t e = (__float_as_uint(top) + 0x100u) >> 23;   // 255: infinity or NaN
+    return e >= 255 ? 255u : e <= 15 ? 1u : e - 14;
+}
+// v / 2^(e - 127) as an int16 (0 under e = 255).
+__device__ __forceinline__ uint32_t code_of(float v, float inverse) {
+    return static_cast<uint32_t>(__float2int_rn(v * inverse)) & 0xFFFFu;
+}
+__device__ __forceinline__ float inverse_scale(uint32_t e) {
+    return e == 255 ? 0.f : __uint_as_float((254u - e) << 23);
+}
+
+// Writes the codes and the scale of n of 32 values.
+__device__ __forceinline__ void keep32(int16_t *codes, uint8_t *scale, const float (&v)[32], int n,
+                                       bool vec) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+        top = max_abs(top, make_float2(v[i], v[i + 1]));
+    const uint32_t e = scale_of(top);
+    const float inverse = inverse_scale(e);
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        w[i] = e == 255 ? 0u
+                        : code_of(v[2 * i], inverse) | code_of(v[2 * i + 1], inverse) << 16;
+    *scale = static_cast<uint8_t>(e);
+    if (vec && n >= 32) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            st_vec_out(codes + 2 * i, make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]));
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i < n)
+            codes[i] = static_cast<int16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
+}
+
+// ------------------------------------------------------------------- products
+
+template <class Act, class T, bool KEEP> struct Forward {
+    using Elem = T;
+    static constexpr bool kAAcross = false, kBAcross = false, kLiveRows = true;
+    struct Args {
+        T *out;
+        int16_t *codes;
+        uint8_t *scales;
+        int d;
+        bool vec;
+    };
+    using G = Product<Forward>;
+    __device__ static int batch_of(int b) { return b; }
+    __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
+                                uint32_t b, uint32_t bar) {
+        load_along(a, &g.a, bar, step * kStep, t.m0 + static_cast<int>(rank) * kHalf, 0, t.b);
+        // the first CTA brings the gate's rows of the weight, the second the up half's
+        load_along(b, &g.b, bar, step * kStep, t.n0 * kHalf, static_cast<int>(rank), t.b);
+    }
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
+        const int d = g.j.d, r = t.m0 + row;
+        const bool mine = r < t.rows;
+        const int64_t at = int64_t(t.b) * g.capacity + r;
+        for (int c = 0; c < kHalf && t.n0 * kHalf + c < d; c += 32) {
+            float gate[32], up[32], y[32];
+            sums_load32(sums + c, gate);
+            sums_load32(sums + kHalf + c, up);
+            sums_load_wait();
+            if (!mine)
+                continue;
+            const int col = t.n0 * kHalf + c, n = d - col;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float2 v = act_mul<Act>({gate[i], gate[i + 1]}, {up[i], up[i + 1]});
+                y[i] = v.x;
+                y[i + 1] = v.y;
+            }
+            store32(g.j.out + at * d + col, y, n, g.j.vec);
+            if (KEEP) {
+                const int blocks = (d + kBlock - 1) / kBlock;
+                int16_t *codes = g.j.codes + at * 2 * d + col;
+                uint8_t *scale = g.j.scales + at * 2 * blocks + col / kBlock;
+                keep32(codes, scale, gate, n, g.j.vec);
+                keep32(codes + d, scale + blocks, up, n, g.j.vec);
+            }
+        }
+    }
+};
+
+// grad_in: A = (dg, du) along the sum over 2d, B = the weight across it.
+template <class T> struct GradIn {
+    using Elem = T;
+    static constexpr bool kAAcross = false, kBAcross = true, kLiveRows = true;
+    struct Args {
+        T *out;
+        int k, half_steps;   // ring steps of one half of the sum
+        bool vec;
+    };
+    using G = Product<GradIn>;
+    __device__ static int batch_of(int b) { return b; }
+    __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
+                                uint32_t b, uint32_t bar) {
+        const int half = step >= g.j.half_steps, x = (step - half * g.j.half_steps) * kStep;
+        load_along(a, &g.a, bar, x, t.m0 + static_cast<int>(rank) * kHalf, half, t.b);
+        load_across(b, &g.b, bar, x, t.n0 * kTile + static_cast<int>(rank) * kHalf, half, t.b);
+    }
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
+        const int k = g.j.k, r = t.m0 + row;
+        const int64_t at = int64_t(t.b) * g.capacity + r;
+        for (int c = 0; c < kTile && t.n0 * kTile + c < k; c += 32) {
+            float v[32];
+            sums_load32(sums + c, v);
+            sums_load_wait();
+            const int col = t.n0 * kTile + c;
+            if (r < t.rows)
+                store32(g.j.out + at * k + col, v, k - col, g.j.vec);
+        }
+    }
+};
+
+// grad_weight: A = (dg, du) across the sum over the rows, B = in across it; batch 2e + half.
+// Past the live rows dg and du are zeros up to a whole step; the last rows of `in` come from
+// a copy with zeros there, as what lies past the live rows may be anything.
+template <class T> struct GradWeight {
+    using Elem = T;
+    static constexpr bool kAAcross = true, kBAcross = true, kLiveRows = false;
+    struct Args {
+        T *out;
+        int k;
+        bool vec;
+    };
+    using G = Product<GradWeight>;
+    __device__ static int batch_of(int b) { return b >> 1; }
+    __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
+                                uint32_t b, uint32_t bar) {
+        const int x = step * kStep, e = t.b >> 1, live = g.live_of(t.b);
+        load_across(a, &g.a, bar, x, t.m0 + static_cast<int>(rank) * kHalf, t.b & 1, e);
+        const bool tail = x + kStep > live && live < g.capacity;
+        load_across(b, tail ? &g.other : &g.b, bar, tail ? 0 : x,
+                    t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, e);
+    }
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
+        const int k = g.j.k, r = t.m0 + row;
+        const int64_t at = int64_t(t.b) * g.rows + r;
+        for (int c = 0; c < kTile && t.n0 * kTile + c < k; c += 32) {
+            float v[32];
+            sums_load32(sums + c, v);
+            sums_load_wait();
+            if (t.steps == 0) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    v[i] = 0.f;
+            }
+            const int col = t.n0 * kTile + c;
+            if (r < t.rows)
+                store32(g.j.out + at * k + col, v, k - col, g.j.vec);
+        }
+    }
+};
+
+// ------------------------------------------------- the gradients of g and u
+
+template <class T> struct GateGradArgs {
+    const T *grad;
+    const int16_t *codes;
+    const uint8_t *scales;
+    const T *in;          // with live counts: its last, partly live, step of rows goes to `tail`
+    T *rows;              // [E, 2, padded, dp]
+    T *tail;              // [E, 64, kp]
+    const int32_t *live;
+    int64_t grad_stride, grad_batch, in_stride, in_batch;
+    int E, T_, d, dp, k, kp, padded;
+    bool vec;             // vectors of grad and codes
+};
+
+// (dg, du) of eight columns of a row per thread, zeros from the live rows to a whole step.
+// One pass: 6 bytes and the scales in, 4 out per pair of elements.
+template <class Act, class T> __global__ void __launch_bounds__(256) gate_gradients(GateGradArgs<T> g) {
+    pdl_wait();
+    pdl_trigger();
+    const int x = (blockIdx.x * 32 + threadIdx.x) * 8;
+    const int blocks = (g.d + kBlock - 1) / kBlock;
+    if (x < g.dp)
+        for (int64_t r = int64_t(blockIdx.y) * 8 + threadIdx.y; r < int64_t(g.E) * g.padded;
+             r += int64_t(gridDim.y) * 8) {
+            const int e = static_cast<int>(r / g.padded), i = static_cast<int>(r - int64_t(e) * g.padded);
+            const int live = g.live ? min(max(g.live[e], 0), g.T_) : g.T_;
+            if (i >= (live + kStep - 1) / kStep * kStep)
+                continue;
+            float2 dg[4], du[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                dg[p] = du[p] = make_float2(0.f, 0.f);
+            if (i < live) {
+                const int64_t at = int64_t(e) * g.T_ + i;
+                const T *grad = g.grad + e * g.grad_batch + i * g.grad_stride + x;
+                const int16_t *gate = g.codes + at * 2 * g.d + x, *up = gate + g.d;
+                const uint8_t *scale = g.scales + at * 2 * blocks + x / kBlock;
+                const float sg = __uint_as_float(uint32_t(scale[0]) << 23),
+                            su = __uint_as_float(uint32_t(scale[blocks]) << 23);
+                float dy[8], a[8], b[8];
+                if (g.vec) {
+                    const uint4 vy = ld_stream(grad), va = ld_stream(gate), vb = ld_stream(up);
+                    const T *py = reinterpret_cast<const T *>(&vy);
+                    const int16_t *pa = reinterpret_cast<const int16_t *>(&va),
+                                  *pb = reinterpret_cast<const int16_t *>(&vb);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        dy[j] = to_float(py[j]);
+                        a[j] = pa[j] * sg;
+                        b[j] = pb[j] * su;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const bool in = x + j < g.d;
+                        dy[j] = in ? to_float(grad[j]) : 0.f;
+                        a[j] = in ? gate[j] * sg : 0.f;
+                        b[j] = in ? up[j] * su : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const GateGrad2 m = act_grad<Act>({a[2 * p], a[2 * p + 1]}, {b[2 * p], b[2 * p + 1]},
+                                                      {dy[2 * p], dy[2 * p + 1]});
+                    dg[p] = m.gate;
+                    du[p] = m.up;
+                }
+            }
+            T *to = g.rows + (int64_t(e) * 2 * g.padded + i) * g.dp + x;
+            st_vec(to, make_uint4(pack2<T>(dg[0]), pack2<T>(dg[1]), pack2<T>(dg[2]), pack2<T>(dg[3])));
+            st_vec(to + int64_t(g.padded) * g.dp,
+                   make_uint4(pack2<T>(du[0]), pack2<T>(du[1]), pack2<T>(du[2]), pack2<T>(du[3])));
+        }
+    if (!g.live)
+        return;
+    // the partly live step of `in`, 256 columns of a row per block and turn
+    const int64_t chunks = (g.k + 255) / 256, turns = int64_t(g.E) * kStep * chunks;
+    const int64_t block = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+    for (int64_t i = block; i < turns; i += int64_t(gridDim.y) * gridDim.x) {
+        const int c = static_cast<int>(i % chunks) * 256 + threadIdx.y * 32 + threadIdx.x;
+        const int row = static_cast<int>(i / chunks % kStep), e = static_cast<int>(i / chunks / kStep);
+        const int live = min(max(g.live[e], 0), g.T_), at = live / kStep * kStep + row;
+        if (c < g.k && live % kStep)
+            g.tail[(int64_t(e) * kStep + row) * g.kp + c] =
+                at < live ? g.in[e * g.in_batch + at * g.in_stride + c] : from_float<T>(0.f);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+struct Operands {
+    Layout in, weight;   // as given
+};
+
+Operands operands(const gated_act_linear &a) {
+    return {{a.in, {a.k, a.T, 1, a.E}, {1, a.in_stride, 0, a.in_batch}},
+            {a.weight,
+             {a.k, a.d, 2, a.E},
+             {1, a.weight_stride, a.d * a.weight_stride, a.weight_batch}}};
+}
+
+int check_sizes(const gated_act_linear &a) {
+    if (a.E < 0 || a.T < 0 || a.d <= 0 || a.k <= 0)
+        return GATED_ACT_ERR_SIZE;
+    if (a.dtype != GATED_ACT_BF16 && a.dtype != GATED_ACT_F16)
+        return GATED_ACT_ERR_DTYPE;
+    if (a.d > kMaxWidth || a.k > kMaxWidth || a.T > kMaxWidth || a.E > GATED_ACT_MAX_EXPERTS ||
+        a.in_stride > kMaxRows || a.in_batch > kMaxRows || a.weight_stride > kMaxRows ||
+        a.weight_batch > kMaxRows)
+        return GATED_ACT_ERR_TOO_LARGE;
+    if (a.in_stride < a.k || a.weight_stride < a.k ||
+        (a.E > 1 && a.T > 0 && a.in_batch < (a.T - 1) * a.in_stride + a.k) ||
+        (a.E > 1 && a.weight_batch < (2 * a.d - 1) * a.weight_stride + a.k))
+        return GATED_ACT_ERR_STRIDE;
+    // 32-bit tile numbers in each of the three products, 63-bit byte counts
+    const int64_t most = (int64_t(1) << 31) - 4096;
+    const auto tiles = [&](int64_t rows, int64_t cols, int64_t width) {
+        return static_cast<double>(a.E) * static_cast<double>(ceil_div64(rows, kTile)) *
+                   static_cast<double>(ceil_div64(cols, width)) <
+               static_cast<double>(most);
+    };
+    if (!tiles(a.T, a.d, kHalf) || !tiles(a.T, a.k, kTile) || !tiles(2 * a.d, a.k, kTile) ||
+        static_cast<double>(a.E) * static_cast<double>(a.T + kStep) *
+                static_cast<double>(2 * a.d + a.k) > 1e17)
+        return GATED_ACT_ERR_TOO_LARGE;
+    return GATED_ACT_OK;
+}
+
+Region in_region(const gated_act_linear &a) {
+    return {a.in, span_bytes(a.E, a.in_batch, span_bytes(a.T, a.in_stride, a.k, 1), 2), 2, false};
+}
+Region weight_region(const gated_act_linear &a) {
+    return {a.weight, span_bytes(a.E, a.weight_batch, span_bytes(2 * a.d, a.weight_stride, a.k, 1), 2),
+            2, false};
+}
+
+// An operand that TMA can address: `t` itself, or a copy in the workspace.
+int addressable(Layout *t, Carve *ws, cudaStream_t stream) {
+    if (tma_addressable(*t))
+        return GATED_ACT_OK;
+    void *copy = ws->take<void>(packed_bytes(*t));
+    if (!ws->start)
+        return GATED_ACT_OK;
+    const Layout to = packed_layout(*t, copy);
+    const int rc = launch_pack(to, *t, stream);
+    *t = to;
+    return rc;
+}
+
+uint64_t forward_bytes(const gated_act_linear &a) {
+    Operands o = operands(a);
+    Carve ws(nullptr);
+    addressable(&o.in, &ws, nullptr);
+    addressable(&o.weight, &ws, nullptr);
+    return ws.used;
+}
+
+template <class Act, class T, bool KEEP>
+int run_forward(void *out, int16_t *codes, uint8_t *scales, const gated_act_linear &a,
+                const int32_t *live, void *workspace, cudaStream_t stream) {
+    constexpr bool is_bf16 = std::is_same_v<T, bf16>;
+    Operands o = operands(a);
+    Carve ws(workspace);
+    int rc = addressable(&o.in, &ws, stream);
+    if (rc == GATED_ACT_OK)
+        rc = addressable(&o.weight, &ws, stream);
+    Product<Forward<Act, T, KEEP>> g;
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&g.a, o.in, kHalf, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&g.b, o.weight, kHalf, is_bf16);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    g.other = g.a;
+    g.live = live;
+    g.batches = static_cast<int>(a.E);
+    g.capacity = g.rows = static_cast<int>(a.T);
+    g.n_tiles = static_cast<int>(ceil_div64(a.d, kHalf));
+    g.steps = static_cast<int>(ceil_div64(a.k, kStep));
+    g.j = {static_cast<T *>(out), codes, scales, static_cast<int>(a.d),
+           a.d % 8 == 0 && aligned(out, 16) && aligned(codes, 16)};
+    return launch_product(g, a.E * ceil_div64(a.T, kTile) * g.n_tiles, stream);
+}
+
+template <class Act>
+int forward(void *out, int16_t *codes, uint8_t *scales, const gated_act_linear *a, void *workspace,
+            size_t workspace_bytes, cudaStream_t stream) {
+    if (!a)
+        return GATED_ACT_ERR_NULL;
+    int rc = check_sizes(*a);
+    if (rc != GATED_ACT_OK || a->T == 0 || a->E == 0)
+        return rc;
+    const uint64_t need = forward_bytes(*a), rows = a->E * a->T;
+    if (workspace_bytes < need)
+        return GATED_ACT_ERR_SCRATCH;
+    if (!codes != !scales)
+        return GATED_ACT_ERR_NULL;
+    Region r[] = {{out, rows * a->d * 2, 2, true},
+                  in_region(*a),
+                  weight_region(*a),
+                  {workspace, need, 16, true},
+                  {codes, codes ? rows * 4 * a->d : 0, 2, true},
+                  {scales, codes ? rows * 2 * ceil_div64(a->d, kBlock) : 0, 1, true},
+                  {a->n_rows, a->n_rows ? uint64_t(a->E) * 4 : 0, 4, false}};
+    rc = check_device_regions(r, 7);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    const auto go = [&](auto type, auto keep) {
+        using T = decltype(type);
+        return run_forward<Act, T, decltype(keep)::value>(out, codes, scales, *a, a->n_rows,
+                                                          workspace, stream);
+    };
+    const auto with_keep = [&](auto type) {
+        return codes ? go(type, std::true_type{}) : go(type, std::false_type{});
+    };
+    return a->dtype == GATED_ACT_BF16 ? with_keep(bf16{}) : with_keep(f16{});
+}
+
+// What the backward pass keeps in its workspace.
+struct BackwardParts {
+    Operands o;
+    int64_t dp, kp, padded;
+    void *rows, *tail;
+    int rc;
+    BackwardParts(const gated_act_linear &a, void *workspace, cudaStream_t stream) : o(operands(a)) {
+        dp = ceil_div64(a.d, 8) * 8;
+        kp = ceil_div64(a.k, 8) * 8;
+        padded = ceil_div64(a.T, kStep) * kStep;
+        Carve ws(workspace);
+        rows = ws.take<void>(uint64_t(a.E) * 2 * padded * dp * 2);
+        tail = ws.take<void>(a.n_rows ? uint64_t(a.E) * kStep * kp * 2 : 0);
+        rc = addressable(&o.in, &ws, stream);
+        if (rc == GATED_ACT_OK)
+            rc = addressable(&o.weight, &ws, stream);
+        bytes = ws.used;
+    }
+    uint64_t bytes;
+};
+
+template <class Act, class T>
+int run_backward(void *grad_in, void *grad_weight, const void *grad_out, int64_t grad_stride,
+                 int64_t grad_batch, const int16_t *codes, const uint8_t *scales,
+                 const gated_act_linear &a, void *workspace, cudaStream_t stream) {
+    constexpr bool is_bf16 = std::is_same_v<T, bf16>;
+    const int E = static_cast<int>(a.E), d = static_cast<int>(a.d), k = static_cast<int>(a.k);
+    const BackwardParts w(a, workspace, stream);
+    if (w.rc != GATED_ACT_OK)
+        return w.rc;
+
+    GateGradArgs<T> e;
+    e.grad = static_cast<const T *>(grad_out);
+    e.codes = codes;
+    e.scales = scales;
+    e.in = static_cast<const T *>(a.in);
+    e.rows = static_cast<T *>(w.rows);
+    e.tail = static_cast<T *>(w.tail);
+    e.live = a.n_rows;
+    e.grad_stride = grad_stride;
+    e.grad_batch = grad_batch;
+    e.in_stride = a.in_stride;
+    e.in_batch = a.in_batch;
+    e.E = E;
+    e.T_ = static_cast<int>(a.T);
+    e.d = d;
+    e.dp = static_cast<int>(w.dp);
+    e.k = k;
+    e.kp = static_cast<int>(w.kp);
+    e.padded = static_cast<int>(w.padded);
+    e.vec = d % 8 == 0 && aligned(grad_out, 16) && aligned(codes, 16) && grad_stride % 8 == 0 &&
+            grad_batch % 8 == 0;
+    const int64_t high = ceil_div64(a.E * w.padded, 8);
+    const dim3 grid(static_cast<unsigned>(ceil_div64(w.dp, 256)),
+                    static_cast<unsigned>(high < 32768 ? high : 32768));
+    int rc = cuda_status(launch_kernel(gate_gradients<Act, T>, grid, dim3(32, 8), 0, stream, 1, e));
+    if (rc != GATED_ACT_OK)
+        return rc;
+
+    const Layout rows = {w.rows,
+                         {a.d, w.padded, 2, a.E},
+                         {1, w.dp, w.padded * w.dp, 2 * w.padded * w.dp}};
+    const Layout tail = {w.tail, {a.k, kStep, 1, a.E}, {1, w.kp, 0, kStep * w.kp}};
+
+    Product<GradIn<T>> gi;
+    rc = encode_map(&gi.a, rows, kHalf, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&gi.b, w.o.weight, kStep, is_bf16);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    gi.other = gi.a;
+    gi.live = a.n_rows;
+    gi.batches = E;
+    gi.capacity = gi.rows = static_cast<int>(a.T);
+    gi.n_tiles = static_cast<int>(ceil_div64(k, kTile));
+    const int half_steps = static_cast<int>(ceil_div64(d, kStep));
+    gi.steps = 2 * half_steps;
+    gi.j = {static_cast<T *>(grad_in), k, half_steps, k % 8 == 0 && aligned(grad_in, 16)};
+    rc = launch_product(gi, a.E * ceil_div64(a.T, kTile) * gi.n_tiles, stream);
+    if (rc != GATED_ACT_OK)
+        return rc;
+
+    Product<GradWeight<T>> gw;
+    rc = encode_map(&gw.a, rows, kStep, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&gw.b, w.o.in, kStep, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = a.n_rows ? encode_map(&gw.other, tail, kStep, is_bf16) : GATED_ACT_OK;
+    if (rc != GATED_ACT_OK)
+        return rc;
+    if (!a.n_rows)
+        gw.other = gw.b;
+    gw.live = a.n_rows;
+    gw.batches = 2 * E;
+    gw.capacity = static_cast<int>(a.T);
+    gw.rows = d;
+    gw.n_tiles = gi.n_tiles;
+    gw.steps = 0;
+    gw.j = {static_cast<T *>(grad_weight), k, k % 8 == 0 && aligned(grad_weight, 16)};
+    return launch_product(gw, 2 * a.E * ceil_div64(d, kTile) * gw.n_tiles, stream);
+}
+
+template <class Act>
+int backward(void *grad_in, void *grad_weight, const void *grad_out, int64_t grad_stride,
+             int64_t grad_batch, const int16_t *codes, const uint8_t *scales,
+             const gated_act_linear *a, void *workspace, size_t workspace_bytes,
+             cudaStream_t stream) {
+    if (!a)
+        return GATED_ACT_ERR_NULL;
+    int rc = check_sizes(*a);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    if (grad_stride > kMaxRows || grad_batch > kMaxRows)
+        return GATED_ACT_ERR_TOO_LARGE;
+    if (grad_stride < a->d ||
+        (a->E > 1 && a->T > 0 && grad_batch < (a->T - 1) * grad_stride + a->d))
+        return GATED_ACT_ERR_STRIDE;
+    if (a->E == 0)
+        return GATED_ACT_OK;
+    const uint64_t need = a->T ? BackwardParts(*a, nullptr, nullptr).bytes : 0, rows = a->E * a->T;
+    if (workspace_bytes < need)
+        return GATED_ACT_ERR_SCRATCH;
+    const uint64_t weight_bytes = uint64_t(a->E) * 4 * a->d * a->k;
+    Region r[] = {{grad_in, rows * a->k * 2, 2, true},
+                  {grad_weight, weight_bytes, 2, true},
+                  {grad_out,
+                   span_bytes(a->E, grad_batch, span_bytes(a->T, grad_stride, a->d, 1), 2), 2, false},
+                  {codes, rows * 4 * a->d, 2, false},
+                  {scales, rows * 2 * ceil_div64(a->d, kBlock), 1, false},
+                  in_region(*a),
+                  weight_region(*a),
+                  {workspace, need, 16, true},
+                  {a->n_rows, a->n_rows ? uint64_t(a->E) * 4 : 0, 4, false}};
+    rc = check_device_regions(r, 9);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    if (a->T == 0)   // sums over no rows
+        return cuda_status(cudaMemsetAsync(grad_weight, 0, weight_bytes, stream));
+    if (a->dtype == GATED_ACT_BF16)
+        return run_backward<Act, bf16>(grad_in, grad_weight, grad_out, grad_stride, grad_batch,
+                                       codes, scales, *a, workspace, stream);
+    return run_backward<Act, f16>(grad_in, grad_weight, grad_out, grad_stride, grad_batch, codes,
+                                  scales, *a, workspace, stream);
+}
+
+}  // namespace
+
+cudaError_t take_linear_act_status(unsigned int *flags) { return take_product_status(flags); }
+
+}  // namespace gact
+
+extern "C" {
+
+size_t linear_and_mul_workspace_bytes(const gated_act_linear *a) {
+    if (!a || gact::check_sizes(*a) != GATED_ACT_OK || a->E == 0 || a->T == 0)
+        return 0;
+    return gact::forward_bytes(*a);
+}
+size_t linear_and_mul_backward_workspace_bytes(const gated_act_linear *a) {
+    if (!a || gact::check_sizes(*a) != GATED_ACT_OK || a->E == 0 || a->T == 0)
+        return 0;
+    return gact::BackwardParts(*a, nullptr, nullptr).bytes;
+}
+int linear_silu_and_mul(void *out, int16_t *codes, uint8_t *scales, const gated_act_linear *a,
+                        void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    return gact::forward<gact::Silu>(out, codes, scales, a, workspace, workspace_bytes, stream);
+}
+int linear_gelu_and_mul(void *out, int16_t *codes, uint8_t *scales, const gated_act_linear *a,
+                        void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    return gact::forward<gact::Gelu>(out, codes, scales, a, workspace, workspace_bytes, stream);
+}
+int linear_silu_and_mul_backward(void *grad_in, void *grad_weight, const void *grad_out,
+                                 int64_t grad_stride, int64_t grad_batch, const int16_t *codes,
+                                 const uint8_t *scales, const gated_act_linear *a, void *workspace,
+                                 size_t workspace_bytes, cudaStream_t stream) {
+    return gact::backward<gact::Silu>(grad_in, grad_weight, grad_out, grad_stride, grad_batch, codes,
+                                      scales, a, workspace, workspace_bytes, stream);
+}
+int linear_gelu_and_mul_backward(void *grad_in, void *grad_weight, const void *grad_out,
+                                 int64_t grad_stride, int64_t grad_batch, const int16_t *codes,
+                                 const uint8_t *scales, const gated_act_linear *a, void *workspace,
+                                 size_t workspace_bytes, cudaStream_t stream) {
+    return gact::backward<gact::Gelu>(grad_in, grad_weight, grad_out, grad_stride, grad_batch, codes,
+                                      scales, a, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,490 @@
+// Matrix products on the tensor cores (tcgen05) with an epilogue of the caller's:
+// the main loop of the linear_* operators.
+//
+// One persistent kernel, one cluster of two CTAs per pair of SMs.  A pair computes
+// tiles of 256 x 256 elements of A B' (fp32 sums), 128 rows per CTA:
+//   warp 0     loads 64 columns of both operands per step into a ring of shared
+//              memory slots (TMA, 128-byte swizzle), in both CTAs;
+//   warp 1     of the pair's first CTA issues the products (tcgen05.mma of the two
+//              CTAs together, 256 x 256 x 16), whose sums lie in tensor memory;
+//   warps 4-7  read finished sums back, a row per thread, and run the epilogue while
+//              the next tile is summed into the other half of the tensor memory.
+// An operand is stored with its rows along the summed dimension (as the activations
+// and weights of a linear layer are in its forward product) or across it (as they are
+// in the products of its gradients); the TMA box and the descriptors differ, no data
+// is transposed.  What lies outside a tensor is read as zeros.
+//
+// Every wait gives up after a second; the kernel then sets its status bit, lets its
+// copies land, frees its tensor memory and returns.
+#pragma once
+
+#include <cuda.h>
+
+#include "training.cuh"
+
+namespace gact {
+
+constexpr int kTile = 256;            // rows and columns of a pair's tile
+constexpr int kHalf = kTile / 2;      // of one CTA's part
+constexpr int kStep = 64;             // summed elements per ring slot: 128 bytes
+constexpr int kSlots = 6;
+constexpr int kOperandBytes = kHalf * kStep * 2;
+constexpr int kSlotBytes = 2 * kOperandBytes;
+constexpr int kMaxBatches = 2048;
+constexpr unsigned long long kProductWaitNs = 1000000000ull;
+
+static __device__ unsigned int g_product_status;   // of this translation unit
+
+// ------------------------------------------------------------- barriers, copies
+
+__device__ __forceinline__ uint32_t smem_address(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// The address of the same variable in the pair's first CTA.
+__device__ __forceinline__ uint32_t in_first_cta(uint32_t a) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void barrier_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// Waits for the phase `parity` of `bar`; false once a wait of this CTA gave up.
+static __device__ __noinline__ bool barrier_wait_slow(uint32_t bar, uint32_t parity,
+                                                      volatile uint32_t *gave_up) {
+    const unsigned long long t0 = now_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (barrier_try(bar, parity))
+            return true;
+        if ((i & 63u) == 0) {
+            if (*gave_up)
+                return false;
+            if (now_ns() - t0 > kProductWaitNs) {
+                *gave_up = 1;
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity,
+                                             volatile uint32_t *gave_up) {
+    return barrier_try(bar, parity) || barrier_wait_slow(bar, parity, gave_up);
+}
+
+// One box of a 4-D tensor into this CTA's shared memory; its bytes count on `bar` of
+// the pair's first CTA.
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x,
+                                         int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+// ------------------------------------------------------------- tensor cores
+
+// Shared memory descriptor of an operand's slot (PTX ISA, "Shared memory descriptor"), 128-byte
+// swizzle.  Rows along the sum: 8 rows of 128 bytes every 1024 bytes.  Rows across it: 8 summed
+// elements every 1024 bytes, 64 rows every 64 summed elements x 128 bytes.
+template <bool ACROSS> __device__ __forceinline__ uint64_t slot_descriptor(uint32_t address) {
+    constexpr uint64_t lead = ACROSS ? (kStep * 128) >> 4 : 1, stride = 1024 >> 4;
+    return (uint64_t((address & 0x3FFFF) >> 4)) | lead << 16 | stride << 32 | uint64_t(1) << 46 |
+           uint64_t(2) << 61;
+}
+// What 16 summed elements add to it.
+template <bool ACROSS> constexpr uint64_t kDescriptorStep = (ACROSS ? 16 * 128 : 16 * 2) >> 4;
+
+// Instruction descriptor (PTX ISA, "Instruction descriptor", kind::f16): fp32 sums of 256 x 256.
+template <class T, bool A_ACROSS, bool B_ACROSS>
+__host__ __device__ constexpr uint32_t product_descriptor() {
+    constexpr uint32_t type = std::is_same_v<T, bf16> ? 1 : 0;
+    return 1u << 4 | type << 7 | type << 10 | uint32_t(A_ACROSS) << 15 | uint32_t(B_ACROSS) << 16 |
+           uint32_t(kTile / 8) << 17 | uint32_t(kTile / 16) << 24;
+}
+__device__ __forceinline__ void product_step(uint32_t sums, uint64_t a, uint64_t b, uint32_t desc,
+                                             bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
+        ::"r"(sums), "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add))
+        : "memory");
+}
+// Arrives on `bar` of both CTAs once the products issued so far are done.
+__device__ __forceinline__ void product_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar), "h"(uint16_t(3))
+        : "memory");
+}
+__device__ __forceinline__ void sums_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void sums_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// 32 columns of the warp's 32 rows: v[i] is column i of the lane's row.
+__device__ __forceinline__ void sums_load32(uint32_t address, float (&v)[32]) {
+    uint32_t r[32];
+    __syncwarp();   // the instruction is the whole warp's
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(address));
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void sums_load_wait() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// ------------------------------------------------------------- the kernel
+
+// One tile of a pair: batch, first row and column, rows of the batch, ring steps.
+struct Tile {
+    int b, m0, n0, rows, steps;
+};
+
+// A job J describes a product and what happens to it:
+//   J::Elem                      bf16 or f16
+//   J::kAAcross, J::kBAcross     operand rows lie across the sum
+//   J::Args                      what its functions read
+//   J::kLiveRows                 live counts bound the rows; else the summed elements
+//   J::batch_of(b)               index of the live count of a batch
+//   J::load(g, tile, step, rank, a, b, bar)   issues the step's copies of one CTA
+//   J::finish(g, tile, row, sums, quarter)    the epilogue of one row (row of the tile
+//                                in [0, 256), sums = tensor memory address of its columns)
+template <class J> struct Product {
+    CUtensorMap a, b, other;
+    const int32_t *live;   // null: `capacity` everywhere
+    int batches, capacity, rows, n_tiles, steps;
+    typename J::Args j;
+
+    __device__ int live_of(int b) const {
+        return live ? min(max(live[J::batch_of(b)], 0), capacity) : capacity;
+    }
+};
+
+struct alignas(8) ProductShared {
+    uint64_t full[kSlots], empty[kSlots], sums_full[2], sums_empty[2];
+    uint32_t sums;             // tensor memory address
+    volatile uint32_t gave_up;
+    int first[kMaxBatches + 1];   // first tile row of each batch
+};
+constexpr size_t kProductShared = kSlots * kSlotBytes + sizeof(ProductShared) + 1024;
+
+constexpr int kTallest = 8;   // tile rows that are walked together, so that the tiles of a wave
+                              // share rows and columns in L2
+
+// The tiles of one pair, in order.
+template <class J> struct Walk {
+    const Product<J> &g;
+    const ProductShared &s;
+    int at, step, b = 0, total;
+    __device__ Walk(const Product<J> &g_, const ProductShared &s_)
+        : g(g_), s(s_), at(blockIdx.x >> 1), step(gridDim.x >> 1), total(s_.first[g_.batches]) {}
+    __device__ bool next(Tile *t) {
+        if (at >= total * g.n_tiles)
+            return false;
+        while (s.first[b + 1] * g.n_tiles <= at)
+            ++b;
+        const int r = at - s.first[b] * g.n_tiles, tall = s.first[b + 1] - s.first[b];
+        const int group = r / (kTallest * g.n_tiles), top = group * kTallest;
+        const int high = min(kTallest, tall - top), rest = r - top * g.n_tiles;
+        t->b = b;
+        t->m0 = (top + rest % high) * kTile;
+        t->n0 = rest / high;
+        if (J::kLiveRows) {
+            t->rows = g.live_of(b);
+            t->steps = g.steps;
+        } else {
+            t->rows = g.rows;
+            t->steps = (g.live_of(b) + kStep - 1) / kStep;
+        }
+        at += step;
+        return true;
+    }
+};
+
+template <class J>
+__global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__ Product<J> g) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_address(raw) + 1023u) & ~1023u;   // the swizzle's period
+    ProductShared &s =
+        *reinterpret_cast<ProductShared *>(raw + (base - smem_address(raw)) + kSlots * kSlotBytes);
+    const uint32_t full = smem_address(s.full), empty = smem_address(s.empty),
+                   sums_full = smem_address(s.sums_full), sums_empty = smem_address(s.sums_empty);
+    const uint32_t rank = cluster_rank();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            barrier_init(full + 8 * i, 1);
+            barrier_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            barrier_init(sums_full + 8 * i, 1);
+            barrier_init(sums_empty + 8 * i, 8);   // four epilogue warps of each CTA
+        }
+        s.gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;"
+                     ::"r"(smem_address(&s.sums))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 3) {
+        int sum = 0;
+        for (int b0 = 0; b0 < g.batches; b0 += 32) {
+            const int b = b0 + lane;
+            int n = 0;
+            if (b < g.batches)
+                n = ((J::kLiveRows ? g.live_of(b) : g.rows) + kTile - 1) / kTile;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xFFFFFFFFu, n, o);
+                if (lane >= o)
+                    n += up;
+            }
+            if (b < g.batches)
+                s.first[b + 1] = sum + n;
+            sum += __shfl_sync(0xFFFFFFFFu, n, 31);
+        }
+        if (lane == 0)
+            s.first[0] = 0;
+    }
+    sums_fence_before();
+    __syncthreads();
+    cluster_barrier();
+    sums_fence_after();
+    const uint32_t sums = s.sums;
+
+    Walk<J> walk(g, s);
+    Tile t;
+    if (warp == 0 && lane == 0) {
+        // the first CTA's barrier counts both CTAs' bytes
+        uint32_t slot = 0, phase = 0;
+        bool ok = true;
+        while (ok && walk.next(&t))
+            for (int k = 0; k < t.steps; ++k) {
+                if (!(ok = barrier_wait(empty + 8 * slot, phase ^ 1, &s.gave_up)))
+                    break;
+                const uint32_t to = base + slot * kSlotBytes;
+                if (rank == 0)
+                    barrier_expect(full + 8 * slot, 2 * kSlotBytes);
+                J::load(g, t, k, rank, to, to + kOperandBytes, in_first_cta(full + 8 * slot));
+                if (++slot == kSlots) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+        // every use of a slot is over (at once for one never used): nothing arrives at this CTA's
+        // barriers after its end
+        for (int i = 0; ok && i < kSlots; ++i) {
+            ok = barrier_wait(empty + 8 * slot, phase ^ 1, &s.gave_up);
+            if (++slot == kSlots) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        constexpr uint32_t desc =
+            product_descriptor<typename J::Elem, J::kAAcross, J::kBAcross>();
+        uint32_t slot = 0, phase = 0, turn = 0;
+        bool ok = true;
+        while (ok && walk.next(&t)) {
+            const uint32_t half = turn & 1, to = sums + half * kTile;
+            if (!(ok = barrier_wait(sums_empty + 8 * half, ((turn >> 1) & 1) ^ 1, &s.gave_up)))
+                break;
+            sums_fence_after();
+            for (int k = 0; k < t.steps; ++k) {
+                if (!(ok = barrier_wait(full + 8 * slot, phase, &s.gave_up)))
+                    break;
+                sums_fence_after();
+                const uint32_t from = base + slot * kSlotBytes;
+                const uint64_t a = slot_descriptor<J::kAAcross>(from),
+                               b = slot_descriptor<J::kBAcross>(from + kOperandBytes);
+#pragma unroll
+                for (int i = 0; i < kStep / 16; ++i)
+                    product_step(to, a + i * kDescriptorStep<J::kAAcross>,
+                                 b + i * kDescriptorStep<J::kBAcross>, desc, k > 0 || i > 0);
+                product_commit(empty + 8 * slot);
+                if (++slot == kSlots) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+            if (ok)
+                product_commit(sums_full + 8 * half);
+            ++turn;
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp & 3;   // the tensor memory lanes that the warp may read
+        uint32_t turn = 0;
+        while (walk.next(&t)) {
+            const uint32_t half = turn & 1;
+            if (!barrier_wait(sums_full + 8 * half, (turn >> 1) & 1, &s.gave_up))
+                break;
+            sums_fence_after();
+            J::finish(g, t, static_cast<int>(rank) * kHalf + quarter * 32 + lane,
+                      sums + half * kTile + (static_cast<uint32_t>(quarter * 32) << 16));
+            sums_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                barrier_arrive_cluster(in_first_cta(sums_empty + 8 * half));
+            ++turn;
+        }
+    }
+    __syncthreads();
+    if (s.gave_up) {
+        // copies in flight land well within this time
+        if (threadIdx.x == 0)
+            atomicOr(&g_product_status, 1u);
+        const unsigned long long t0 = now_ns();
+        for (int i = 0; i < 1000000 && now_ns() - t0 < 5000000ull; ++i)
+            ;
+    }
+    __syncthreads();
+    cluster_barrier();
+    if (warp == 2) {
+        sums_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(sums) : "memory");
+    }
+    __syncthreads();
+    cluster_barrier();
+}
+
+// ------------------------------------------------------------- loads, stores
+
+// 128 operand rows from `row` on, summed elements from `x` on.
+__device__ __forceinline__ void load_along(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                           int x, int row, int z, int w) {
+    box_load(dst, map, bar, x, row, z, w);
+}
+// The same of an operand whose rows lie across the sum.
+__device__ __forceinline__ void load_across(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                            int x, int row, int z, int w) {
+    box_load(dst, map, bar, row, x, z, w);
+    box_load(dst + kStep * 128, map, bar, row + 64, x, z, w);
+}
+
+template <class T> __device__ __forceinline__ uint32_t pack2(float2 v);
+template <> __device__ __forceinline__ uint32_t pack2<bf16>(float2 v) { return pack_bf16x2(v.x, v.y); }
+template <> __device__ __forceinline__ uint32_t pack2<f16>(float2 v) {
+    const __half2 h = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The first n of 32 values, each rounded once, to p; whole rows of 16-byte vectors where `vec`.
+template <class T>
+__device__ __forceinline__ void store32(T *p, const float (&v)[32], int n, bool vec) {
+    if (vec && n >= 32) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+            st_vec_out(p + i, make_uint4(pack2<T>({v[i], v[i + 1]}), pack2<T>({v[i + 2], v[i + 3]}),
+                                         pack2<T>({v[i + 4], v[i + 5]}),
+                                         pack2<T>({v[i + 6], v[i + 7]})));
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i < n)
+            p[i] = from_float<T>(v[i]);
+}
+
+// ------------------------------------------------------------- host side
+
+// A tensor of up to four dimensions, innermost first; strides in elements of two bytes.
+struct Layout {
+    const void *data;
+    int64_t size[4], stride[4];   // stride[0] = 1
+};
+
+// Whether a TMA copy can address it: 16-byte rows, planes and base.
+bool tma_addressable(const Layout &t);
+
+// The tensor map of boxes of 64 x `rows` elements.
+int encode_map(CUtensorMap *map, const Layout &t, int rows, bool is_bf16);
+
+// The layout of a copy of `t` at `data` whose rows are padded to 16 bytes.
+Layout packed_layout(const Layout &t, void *data);
+inline uint64_t packed_bytes(const Layout &t) {
+    return static_cast<uint64_t>(ceil_div64(t.size[0], 8)) * 16 * t.size[1] * t.size[2] * t.size[3];
+}
+// Copies `from` into `to`, a packed_layout of it; the padding is zeros.
+int launch_pack(const Layout &to, const Layout &from, cudaStream_t stream);
+
+// check_regions, and no buffer in host memory.
+int check_device_regions(Region *r, int n);
+
+// Parts of a workspace, each 128-byte aligned from its start; with a null start it
+// only counts.
+struct Carve {
+    uint8_t *start;
+    uint64_t used = 0;
+    explicit Carve(void *p) : start(static_cast<uint8_t *>(p)) {}
+    template <class T> T *take(uint64_t bytes) {
+        T *p = start ? reinterpret_cast<T *>(start + used) : nullptr;
+        used += (bytes + 127) / 128 * 128;
+        return p;
+    }
+};
+
+template <class J> int launch_product(const Product<J> &g, int64_t tiles, cudaStream_t stream) {
+    auto kernel = product_kernel<J>;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), kProductShared);
+    if (e != cudaSuccess)
+        return cuda_status(e);
+    const int pairs = device_sm_count() / 2;
+    const unsigned grid = 2u * static_cast<unsigned>(tiles < pairs ? (tiles < 1 ? 1 : tiles) : pairs);
+    return cuda_status(launch_kernel(kernel, dim3(grid), dim3(256), kProductShared, stream, 2, g));
+}
+
+// Reads and clears this translation unit's status.
+static inline cudaError_t take_product_status(unsigned int *flags) {
+    unsigned int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_product_status, sizeof v);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_product_status, &zero, sizeof zero);
+    *flags |= v;
+    return e;
+}
+
+}  // namespace gact

@@ -63,7 +63,9 @@ def _native():
                                                       _build.BINDING)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        module.set_up(Checkpoint, BalanceLoss, _ga._check)
+        from . import linear
+        module.set_up(Checkpoint, BalanceLoss, _ga._check, linear.LinearCheckpoint,
+                      linear.CrossEntropy)
         _module = module
     return _module
 
