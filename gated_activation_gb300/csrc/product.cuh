@@ -264,7 +264,6 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;"
                      ::"r"(smem_address(&s.sums))
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     pdl_wait();
     pdl_trigger();
@@ -292,6 +291,10 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
     __syncthreads();
     cluster_barrier();
     sums_fence_after();
+    // The pair gives its right to allocate back only here, when both CTAs have allocated: given
+    // back by the first CTA before the second's allocation, that one never returned.
+    if (warp == 2)
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     const uint32_t sums = s.sums;
 
     Walk<J> walk(g, s);

@@ -325,6 +325,17 @@ def test_runs_together(ga):
         assert all(torch.equal(a, b) for a, b in zip(held, result))
 
 
+def test_many_passes_in_a_row(ga):
+    """Kernels of one and two CTAs per SM pair behind each other without a pause, some of them on
+    a part of the SMs: 1500 launches of products."""
+    x, w, dy = _operands(1001, 1101, 2731, F16, 61)
+    for _ in range(500):
+        out, kept = ga.linear_silu_and_mul(x, w, keep=True)
+        grads = ga.linear_silu_and_mul_backward(dy, x, w, kept)
+    torch.cuda.synchronize()
+    _check_gated("silu", x, w, dy, out, grads, F16)
+
+
 def test_two_streams_at_once(ga):
     """Calls that overlap on the GPU have workspaces of their own."""
     x, w, dy = _operands(500, 257, 300, BF16, 41)
