@@ -260,6 +260,10 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
         s.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    // Both CTAs run before either allocates: an allocation for the pair while the other CTA had
+    // not started left that one's own allocation waiting for ever.
+    __syncthreads();
+    cluster_barrier();
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;"
                      ::"r"(smem_address(&s.sums))
@@ -287,14 +291,11 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
         if (lane == 0)
             s.first[0] = 0;
     }
+    // The first CTA's products write the other's tensor memory, but they wait for its copies,
+    // which it issues after this.
     sums_fence_before();
     __syncthreads();
-    cluster_barrier();
     sums_fence_after();
-    // The pair gives its right to allocate back only here, when both CTAs have allocated: given
-    // back by the first CTA before the second's allocation, that one never returned.
-    if (warp == 2)
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     const uint32_t sums = s.sums;
 
     Walk<J> walk(g, s);
@@ -373,6 +374,7 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
             ++turn;
         }
     }
+    __syncwarp();
     __syncthreads();
     if (s.gave_up) {
         // copies in flight land well within this time
@@ -386,6 +388,8 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
     cluster_barrier();
     if (warp == 2) {
         sums_fence_after();
+        // not earlier: the right to allocate is the pair's
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(sums) : "memory");
     }
     __syncthreads();
