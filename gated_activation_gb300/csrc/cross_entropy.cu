@@ -3,11 +3,11 @@
 //   live_tokens   numbers the tokens that take part; where some do not, copies their
 //                 rows side by side, so that the products run over live rows alone.
 //   forward       one product kernel whose epilogue leaves each row's maximum and sum of
-//                 exponentials over a tile's 256 columns, and the target's logit; a second
-//                 kernel joins them.
+//                 exponentials over a tile's 256 columns, the target's column left out; a second
+//                 kernel joins them with the target's logit.
 //   backward      for each piece of the vocabulary: the logits again, with y = (p - [target])
 //                 grad_loss as the epilogue; y W added to grad_in's sums; y' in as the
-//                 piece's rows of grad_weight.
+//                 piece's rows of grad_weight.  Last, grad_in from its sums.
 #include "product.cuh"
 
 #include "gated_act_linear.h"
@@ -20,6 +20,13 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The larger of two, NaN if one is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
 
@@ -193,17 +200,17 @@ template <class T> struct Statistics {
     static constexpr bool kAAcross = false, kBAcross = false, kLiveRows = true;
     struct Args {
         const int32_t *goal;
-        float2 *part;        // [tiles, capacity]: maximum, sum
-        float *at_goal;      // [capacity]
+        float2 *part;        // [capacity, tiles]: maximum, sum
         int V;
     };
     using G = Product<Statistics>;
     __device__ static int batch_of(int) { return 0; }
+    __device__ static int steps_of(const G &g, int) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
         load_logits(g, t, 0, step, rank, a, b, bar);
     }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &) {
         const int r = t.m0 + row;
         const bool mine = r < t.rows;
         const int first = t.n0 * kTile, goal = mine ? g.j.goal[r] - first : -1;
@@ -212,37 +219,31 @@ template <class T> struct Statistics {
             float v[32];
             sums_load32(sums + c, v);
             sums_load_wait();
-            if (goal >= c && goal < c + 32) {
-                float at = 0.f;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    at = goal - c == i ? v[i] : at;
-                g.j.at_goal[r] = at;
-            }
             const int n = g.j.V - first - c;
-            if (n < 32) {
+            if (n < 32 || (goal >= c && goal < c + 32)) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    v[i] = i < n ? v[i] : -INFINITY;
+                    v[i] = i < n && goal - c != i ? v[i] : -INFINITY;
             }
-            float most = top;
+            float most[4] = {top * (1.f / kLog2e), v[0], v[1], v[2]};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                v[i] *= kLog2e;
-                most = fmaxf(most, v[i]);
-            }
+            for (int i = 3; i < 32; ++i)
+                most[i & 3] = max_nan(most[i & 3], v[i]);
+            const float now = max_nan(max_nan(most[0], most[1]), max_nan(most[2], most[3])) * kLog2e;
             // a row of -infinity alone has no exponential: its maximum is taken as 0
-            const float base = most == -INFINITY ? 0.f : most;
-            sum *= exp2_fast(top - base);
-            top = most;
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
+            const float base = now == -INFINITY ? 0.f : now;
+            float2 part[2] = {{sum * exp2_fast(top - base), 0.f}, {0.f, 0.f}};
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                part[i & 3] += exp2_fast(v[i] - base);
-            sum += (part[0] + part[1]) + (part[2] + part[3]);
+            for (int i = 0; i < 32; i += 2) {
+                const float2 y = fma2({v[i], v[i + 1]}, both(kLog2e), both(-base));
+                part[i >> 1 & 1] = add2(part[i >> 1 & 1], {exp2_fast(y.x), exp2_fast(y.y)});
+            }
+            part[0] = add2(part[0], part[1]);
+            sum = part[0].x + part[0].y;
+            top = now;
         }
         if (mine)
-            g.j.part[int64_t(t.n0) * g.capacity + r] = make_float2(top, sum);
+            g.j.part[int64_t(r) * g.n_tiles + t.n0] = make_float2(top, sum);
     }
 };
 
@@ -260,104 +261,92 @@ template <class T> struct Slopes {
     };
     using G = Product<Slopes>;
     __device__ static int batch_of(int) { return 0; }
+    __device__ static int steps_of(const G &g, int) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
         load_logits(g, t, g.j.first, step, rank, a, b, bar);
     }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
         const int r = t.m0 + row;
         const bool mine = r < t.rows, write = r < (t.rows + kStep - 1) / kStep * kStep;
         const int first = g.j.first + t.n0 * kTile;
         const int goal = mine ? g.j.t.goal[r] - first : -1;
         const float shift = mine ? g.j.t.shift[r] : 0.f;
         const float weight = mine ? g.j.t.weight[r] * kLift<T> : 0.f;
-        T *y = g.j.y + int64_t(r) * g.j.piece + t.n0 * kTile;
-        for (int c = 0; c < kTile && t.n0 * kTile + c < g.j.piece; c += 32) {
-            float v[32];
-            sums_load32(sums + c, v);
-            sums_load_wait();
-            if (!write)
-                continue;
+        T *y = write ? g.j.y + int64_t(r) * g.j.piece + t.n0 * kTile : nullptr;
+        for (int c0 = 0; c0 < kTile && t.n0 * kTile + c0 < g.j.piece; c0 += 64) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                v[i] = exp2_fast(fmaf(v[i], kLog2e, -shift));
-            if (goal >= c && goal < c + 32) {
+            for (int half = 0; half < 2; ++half) {
+                const int c = c0 + 32 * half, n = mine ? g.j.V - first - c : 0;
+                float v[32];
+                uint32_t w[16];
+                sums_load32(sums + c, v);
+                sums_load_wait();
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 x = fma2({v[i], v[i + 1]}, both(kLog2e), both(-shift));
+                    v[i] = exp2_fast(x.x);
+                    v[i + 1] = exp2_fast(x.y);
+                }
+                if (goal >= c && goal < c + 32) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] -= goal - c == i ? 1.f : 0.f;
+                }
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    v[i] -= goal - c == i ? 1.f : 0.f;
+                    v[i] = i < n ? v[i] * weight : 0.f;
+                pack32<T>(w, v);
+                stage.put(half, w);
             }
-            const int n = g.j.V - first - c;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                v[i] = mine && i < n ? v[i] * weight : 0.f;
-            store32(y + c, v, 32, true);
+            stage.flush(y ? y + c0 : nullptr, 64, true);
         }
     }
 };
 
-// grad_in += y W over one piece: A = y along the sum, B = the weight across it.
+// grad_in's sums += y W over one piece: A = y along the sum, B = the weight across it; each batch
+// sums a share of the piece's columns.  The sums lie as the threads hold them, 256 x 256 to a tile,
+// column after column: a warp reads and writes 128 bytes at once.
 template <class T> struct PieceGradIn {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = true, kLiveRows = true;
     struct Args {
-        Tokens t;
-        T *out;              // [T, k]
-        float *sums;         // [rows, k]
-        int k, first;
-        bool begin, end, vec;
+        float *sums;
+        int k, first, m_tiles;
+        bool begin;
     };
     using G = Product<PieceGradIn>;
     __device__ static int batch_of(int) { return 0; }
+    // shares of whole steps, as even as they get
+    __device__ static int first_step(const G &g, int b) {
+        return static_cast<int>(int64_t(g.steps) * b / g.batches);
+    }
+    __device__ static int steps_of(const G &g, int b) { return first_step(g, b + 1) - first_step(g, b); }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
-        load_along(a, &g.a, bar, step * kStep, t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
-        load_across(b, &g.b, bar, g.j.first + step * kStep,
-                    t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, 0);
+        const int x = (first_step(g, t.b) + step) * kStep;
+        load_along(a, &g.a, bar, x, t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
+        load_across(b, &g.b, bar, g.j.first + x, t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, 0);
     }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
-        const int k = g.j.k, r = t.m0 + row;
-        const bool mine = r < t.rows;
-        const float power = g.j.end ? *g.j.t.power * (1.f / kLift<T>) : 1.f;
-        const int64_t token = mine && g.j.end ? g.j.t.token[r] : 0;
-        for (int c = 0; c < kTile && t.n0 * kTile + c < k; c += 32) {
-            float v[32];
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &) {
+        const bool mine = t.m0 + row < t.rows;
+        const int64_t tile = (int64_t(t.b) * g.j.m_tiles + t.m0 / kTile) * g.n_tiles + t.n0;
+        float *held = g.j.sums + tile * (kTile * kTile) + row;
+        for (int c = 0; c < kTile && t.n0 * kTile + c < g.j.k; c += 32, held += 32 * kTile) {
+            float v[32], old[32];
+            if (!g.j.begin) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    old[i] = mine ? held[i * kTile] : 0.f;
+            }
             sums_load32(sums + c, v);
             sums_load_wait();
             if (!mine)
                 continue;
-            const int col = t.n0 * kTile + c, n = k - col;
-            float *held = g.j.sums + int64_t(r) * k + col;
-            if (!g.j.begin) {
-                if (g.j.vec && n >= 32) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 h = *reinterpret_cast<const float4 *>(held + i);
-                        v[i] += h.x;
-                        v[i + 1] += h.y;
-                        v[i + 2] += h.z;
-                        v[i + 3] += h.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] += i < n ? held[i] : 0.f;
-                }
-            }
-            if (g.j.end) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    v[i] *= power;
-                store32(g.j.out + token * k + col, v, n, g.j.vec);
-            } else if (g.j.vec && n >= 32) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<float4 *>(held + i) =
-                        make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (i < n)
-                        held[i] = v[i];
+            for (int i = 0; i < 32; ++i) {
+                const float x = t.steps ? v[i] : 0.f;
+                held[i * kTile] = g.j.begin ? x : old[i] + x;
             }
         }
     }
@@ -375,65 +364,138 @@ template <class T> struct PieceGradWeight {
     };
     using G = Product<PieceGradWeight>;
     __device__ static int batch_of(int) { return 0; }
+    __device__ static int steps_of(const G &g, int) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
         load_across(a, &g.a, bar, step * kStep, t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
-        load_across(b, g.live_of(0) < g.capacity ? &g.other : &g.b, bar, step * kStep,
+        load_across(b, t.live < g.capacity ? &g.other : &g.b, bar, step * kStep,
                     t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, 0);
     }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
-        const int k = g.j.k, r = t.m0 + row;
-        const float power = t.steps ? *g.j.power * (1.f / kLift<T>) : 0.f;
-        for (int c = 0; c < kTile && t.n0 * kTile + c < k; c += 32) {
-            float v[32];
-            sums_load32(sums + c, v);
-            sums_load_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                v[i] = t.steps ? v[i] * power : 0.f;
-            const int col = t.n0 * kTile + c;
-            if (r < t.rows)
-                store32(g.j.out + int64_t(r) * k + col, v, k - col, g.j.vec);
-        }
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
+        const int k = g.j.k, r = t.m0 + row, col = t.n0 * kTile;
+        T *mine = r < t.rows ? g.j.out + int64_t(r) * k + col : nullptr;
+        store_tile(sums, stage, mine, k - col, g.j.vec, *g.j.power * (1.f / kLift<T>), t.steps == 0);
     }
 };
 
-// ----------------------------------------------------------------------- the join
+// ---------------------------------------------------------------------- the joins
 
-struct JoinArgs {
+template <class T> struct JoinArgs {
     const float2 *part;
-    const float *at_goal;
-    const int32_t *count, *token;
+    const T *in, *weight;     // as given: rows in_stride and weight_stride apart
+    Tokens t;
     float *loss, *lse;
-    int capacity, tiles;
+    int64_t in_stride, weight_stride;
+    int capacity, tiles, k;
 };
 
-// 32 rows per block, a row per lane; the warps take a share of the tiles each.
-__global__ void __launch_bounds__(256) join_statistics(JoinArgs g) {
-    __shared__ float2 share[8][32];
+// Eight elements at any address of theirs.
+template <class T> __device__ __forceinline__ uint4 eight(const T *p) {
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = ld_stream_u16(reinterpret_cast<const uint16_t *>(p) + i);
+    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+}
+
+// A warp per live row.  The target's logit is summed here in fp32 with rounding: the tensor cores cut
+// sums off, which at k = 2048 left it 1e-6 of its size too small.  With the other columns' sum s of
+// 2^(l - m), loss = log(1 + s 2^(m - l_target)) where the target is above them, so that a confident
+// token's small loss keeps its bits.
+template <class T> __global__ void __launch_bounds__(256) join_statistics(JoinArgs<T> g) {
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x * 32 + lane;
-    const bool mine = r < *g.count;
+    const int lane = threadIdx.x & 31, r = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= *g.t.count)
+        return;
+    const int token = g.t.token[r];
+    const T *x = g.in + token * g.in_stride, *w = g.weight + g.t.goal[r] * g.weight_stride;
+    float2 dot[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+    const int from = g.k & ~7;
+    const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 15) == 0;
+#pragma unroll 2
+    for (int c = lane * 8; c < from; c += 256) {   // in one order, whatever the alignment
+        uint4 vx, vw;
+        if (vec) {
+            vx = ld_stream(x + c);
+            vw = ld_stream(w + c);
+        } else {
+            vx = eight(x + c);
+            vw = eight(w + c);
+        }
+        const T *px = reinterpret_cast<const T *>(&vx), *pw = reinterpret_cast<const T *>(&vw);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            dot[i] = fma2({to_float(px[2 * i]), to_float(px[2 * i + 1])},
+                          {to_float(pw[2 * i]), to_float(pw[2 * i + 1])}, dot[i]);
+    }
+    for (int c = from + lane; c < g.k; c += 32)
+        dot[0].x = fmaf(to_float(x[c]), to_float(w[c]), dot[0].x);
+    dot[0] = add2(add2(dot[0], dot[1]), add2(dot[2], dot[3]));
+    const float at = warp_sum(dot[0].x + dot[0].y), goal = at * kLog2e;
+
     float top = -INFINITY, sum = 0.f;
     const auto add = [&](float2 p) {
-        const float most = fmaxf(top, p.x), base = most == -INFINITY ? 0.f : most;
+        const float most = max_nan(top, p.x), base = most == -INFINITY ? 0.f : most;
         sum = sum * exp2_fast(top - base) + p.y * exp2_fast(p.x - base);
         top = most;
     };
-    if (mine)
-        for (int i = warp; i < g.tiles; i += 8)
-            add(g.part[int64_t(i) * g.capacity + r]);
-    share[warp][lane] = make_float2(top, sum);
-    __syncthreads();
-    if (warp || !mine)
+    for (int i = lane; i < g.tiles; i += 32)
+        add(g.part[int64_t(r) * g.tiles + i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float2 p = {__shfl_xor_sync(0xFFFFFFFFu, top, o), __shfl_xor_sync(0xFFFFFFFFu, sum, o)};
+        add(p);
+    }
+    if (lane)
         return;
-    for (int i = 1; i < 8; ++i)
-        add(share[i][lane]);
-    const float lse = (top + log2f(sum)) * kLn2;
-    const int i = g.token[r];
-    g.lse[i] = lse;
-    g.loss[i] = lse - g.at_goal[r];
+    float lse, loss;
+    if (goal >= top) {
+        loss = goal == INFINITY ? NAN : log1pf(sum * exp2f(top - goal));
+        lse = at + loss;
+    } else {
+        lse = top * kLn2 + logf(sum + exp2f(goal - top));
+        loss = lse - at;
+    }
+    g.lse[token] = lse;
+    g.loss[token] = loss;
+}
+
+template <class T> struct GradInArgs {
+    const float *sums;
+    Tokens t;
+    T *out;
+    int k, shares, m_tiles, n_tiles;
+};
+
+// grad_in's rows from the shares of their sums: a block takes 32 rows x 64 columns of a tile, reads
+// columns and writes rows.
+template <class T> __global__ void __launch_bounds__(256) join_grad_in(GradInArgs<T> g) {
+    __shared__ float held[64][33];
+    pdl_wait();
+    pdl_trigger();
+    const int wide = (g.k + 63) / 64, count = *g.t.count;
+    const int r0 = static_cast<int>(blockIdx.x / wide) * 32, c0 = static_cast<int>(blockIdx.x % wide) * 64;
+    if (r0 >= count)
+        return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t part = int64_t(g.m_tiles) * g.n_tiles * (kTile * kTile);
+    const float *from = g.sums + (int64_t(r0 / kTile) * g.n_tiles + c0 / kTile) * (kTile * kTile) +
+                        (c0 % kTile) * kTile + r0 % kTile + lane;
+    for (int c = warp; c < 64 && c0 + c < g.k; c += 8) {
+        float v = 0.f;
+        if (r0 + lane < count)
+            for (int s = 0; s < g.shares; ++s)
+                v += from[s * part + c * kTile];
+        held[c][lane] = v;
+    }
+    __syncthreads();
+    const float power = *g.t.power * (1.f / kLift<T>);
+    for (int i = warp; i < 32 && r0 + i < count; i += 8) {
+        T *to = g.out + int64_t(g.t.token[r0 + i]) * g.k + c0;
+        for (int c = lane; c < 64 && c0 + c < g.k; c += 32)
+            to[c] = from_float<T>(held[c][i] * power);
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -452,7 +514,7 @@ int check_sizes(const gated_act_vocabulary &a) {
     const auto tiles = [&](int64_t x, int64_t y) {
         return static_cast<double>(ceil_div64(x, kTile)) * static_cast<double>(ceil_div64(y, kTile));
     };
-    if (tiles(a.T, a.V) >= most || tiles(a.T, a.k) >= most || tiles(a.V, a.k) >= most)
+    if (tiles(a.T, a.V) >= most || 32 * tiles(a.T, a.k) >= most || tiles(a.V, a.k) >= most)
         return GATED_ACT_ERR_TOO_LARGE;
     return GATED_ACT_OK;
 }
@@ -479,14 +541,26 @@ int64_t piece_of(const gated_act_vocabulary &a) {
     return n < all ? n : all;
 }
 
+// Shares that grad_in's sums over a piece are split into, so that its tiles occupy the pairs of
+// SMs.  A share costs each piece 8 bytes of traffic per row and column, so that of the counts with
+// equal waves per share the smallest is taken, none leaves fewer than 16 steps, and more than one
+// wave is not split.
+int64_t shares_of(int64_t tiles, int64_t steps) {
+    const int64_t pairs = device_sm_count() / 2;
+    int64_t n = tiles < pairs ? pairs / tiles : 1;
+    if (n > steps / 16)
+        n = steps / 16;
+    return n < 1 ? 1 : n;
+}
+
 // The parts of a workspace.
 struct Parts {
     Layout in, packed, weight;
     Tokens t = {};
     float2 *part = nullptr;
-    float *at_goal = nullptr, *sums = nullptr;
+    float *sums = nullptr;
     void *y = nullptr;
-    int64_t kp, padded, piece;
+    int64_t kp, padded, piece, m_tiles = 0, n_tiles = 0, shares = 0;
     bool copy;
     uint64_t bytes;
     int rc;
@@ -507,10 +581,12 @@ struct Parts {
             t.weight = ws.take<float>(4 * a.T);
             t.power = ws.take<float>(4);
             y = ws.take<void>(2 * padded * piece);
-            sums = ws.take<float>(piece < a.V ? 4 * a.T * a.k : 0);
+            m_tiles = ceil_div64(a.T, kTile);
+            n_tiles = ceil_div64(a.k, kTile);
+            shares = shares_of(m_tiles * n_tiles, ceil_div64(piece, kStep));
+            sums = ws.take<float>(4 * kTile * kTile * shares * m_tiles * n_tiles);
         } else {
             part = ws.take<float2>(8 * ceil_div64(a.V, kTile) * a.T);
-            at_goal = ws.take<float>(4 * a.T);
         }
         rc = GATED_ACT_OK;
         if (!tma_addressable(weight)) {
@@ -587,13 +663,22 @@ int run_forward(float *loss, float *lse, const gated_act_vocabulary &a, void *wo
     set_rows(&g, w, a);
     g.n_tiles = static_cast<int>(ceil_div64(a.V, kTile));
     g.steps = static_cast<int>(ceil_div64(a.k, kStep));
-    g.j = {w.t.goal, w.part, w.at_goal, static_cast<int>(a.V)};
+    g.j = {w.t.goal, w.part, static_cast<int>(a.V)};
     rc = launch_product(g, ceil_div64(a.T, kTile) * g.n_tiles, stream);
     if (rc != GATED_ACT_OK)
         return rc;
-    const JoinArgs j = {w.part, w.at_goal, w.t.count, w.t.token, loss, lse,
-                        static_cast<int>(a.T), g.n_tiles};
-    return cuda_status(launch_kernel(join_statistics, dim3(static_cast<unsigned>(ceil_div64(a.T, 32))),
+    const JoinArgs<T> j = {w.part,
+                           static_cast<const T *>(a.in),
+                           static_cast<const T *>(a.weight),
+                           w.t,
+                           loss,
+                           lse,
+                           a.in_stride,
+                           a.weight_stride,
+                           static_cast<int>(a.T),
+                           g.n_tiles,
+                           static_cast<int>(a.k)};
+    return cuda_status(launch_kernel(join_statistics<T>, dim3(static_cast<unsigned>(ceil_div64(a.T, 8))),
                                      dim3(256), 0, stream, 1, j));
 }
 
@@ -606,7 +691,7 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
     if (rc == GATED_ACT_OK)
         rc = run_live_tokens<T>(w, a, grad_loss, lse, nullptr, nullptr, grad_in, stream);
     const int k = static_cast<int>(a.k);
-    const bool vec = a.k % 8 == 0 && aligned(grad_in, 16) && aligned(grad_weight, 16);
+    const bool vec = a.k % 8 == 0 && aligned(grad_weight, 16);
 
     Product<Slopes<T>> s;
     Product<PieceGradIn<T>> gi;
@@ -635,11 +720,11 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
             return rc;
         gi.other = gi.a;
         set_rows(&gi, w, a);
-        gi.n_tiles = static_cast<int>(ceil_div64(a.k, kTile));
+        gi.batches = static_cast<int>(w.shares);
+        gi.n_tiles = static_cast<int>(w.n_tiles);
         gi.steps = static_cast<int>(ceil_div64(cols, kStep));
-        gi.j = {w.t,   static_cast<T *>(grad_in), w.sums, k, static_cast<int>(first),
-                first == 0, first + cols == a.V,  vec};
-        rc = launch_product(gi, ceil_div64(a.T, kTile) * gi.n_tiles, stream);
+        gi.j = {w.sums, k, static_cast<int>(first), static_cast<int>(w.m_tiles), first == 0};
+        rc = launch_product(gi, w.shares * w.m_tiles * w.n_tiles, stream);
 
         if (rc == GATED_ACT_OK)
             rc = encode_map(&gw.a, y, kStep, is_bf16);
@@ -652,7 +737,13 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
         gw.j = {w.t.power, static_cast<T *>(grad_weight) + first * a.k, k, vec};
         rc = launch_product(gw, ceil_div64(cols, kTile) * gw.n_tiles, stream);
     }
-    return rc;
+    if (rc != GATED_ACT_OK)
+        return rc;
+    const GradInArgs<T> j = {w.sums, w.t, static_cast<T *>(grad_in), k, static_cast<int>(w.shares),
+                             static_cast<int>(w.m_tiles), static_cast<int>(w.n_tiles)};
+    const int64_t blocks = ceil_div64(a.k, 64) * ceil_div64(a.T, 32);
+    return cuda_status(launch_kernel(join_grad_in<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                                     stream, 1, j));
 }
 
 }  // namespace

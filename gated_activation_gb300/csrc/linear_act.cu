@@ -32,31 +32,19 @@ __device__ __forceinline__ float inverse_scale(uint32_t e) {
     return e == 255 ? 0.f : __uint_as_float((254u - e) << 23);
 }
 
-// Writes the codes and the scale of n of 32 values.
-__device__ __forceinline__ void keep32(int16_t *codes, uint8_t *scale, const float (&v)[32], int n,
-                                       bool vec) {
+// The codes of 32 values, two to a word; returns the scale byte.
+__device__ __forceinline__ uint32_t encode32(uint32_t (&w)[16], const float (&v)[32]) {
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; i += 2)
         top = max_abs(top, make_float2(v[i], v[i + 1]));
     const uint32_t e = scale_of(top);
     const float inverse = inverse_scale(e);
-    uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         w[i] = e == 255 ? 0u
                         : code_of(v[2 * i], inverse) | code_of(v[2 * i + 1], inverse) << 16;
-    *scale = static_cast<uint8_t>(e);
-    if (vec && n >= 32) {
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-            st_vec_out(codes + 2 * i, make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]));
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (i < n)
-            codes[i] = static_cast<int16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
+    return e;
 }
 
 // ------------------------------------------------------------------- products
@@ -79,32 +67,42 @@ template <class Act, class T, bool KEEP> struct Forward {
         // the first CTA brings the gate's rows of the weight, the second the up half's
         load_along(b, &g.b, bar, step * kStep, t.n0 * kHalf, static_cast<int>(rank), t.b);
     }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
-        const int d = g.j.d, r = t.m0 + row;
+    __device__ static int steps_of(const G &g, int) { return g.steps; }
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
+        const int d = g.j.d, r = t.m0 + row, blocks = (d + kBlock - 1) / kBlock;
         const bool mine = r < t.rows;
         const int64_t at = int64_t(t.b) * g.capacity + r;
-        for (int c = 0; c < kHalf && t.n0 * kHalf + c < d; c += 32) {
-            float gate[32], up[32], y[32];
-            sums_load32(sums + c, gate);
-            sums_load32(sums + kHalf + c, up);
-            sums_load_wait();
-            if (!mine)
-                continue;
+        for (int c = 0; c < kHalf && t.n0 * kHalf + c < d; c += 64) {
             const int col = t.n0 * kHalf + c, n = d - col;
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                const float2 v = act_mul<Act>({gate[i], gate[i + 1]}, {up[i], up[i + 1]});
-                y[i] = v.x;
-                y[i + 1] = v.y;
+            for (int half = 0; half < 2; ++half) {
+                float gate[32], up[32];
+                sums_load32(sums + c + 32 * half, gate);
+                sums_load32(sums + kHalf + c + 32 * half, up);
+                sums_load_wait();
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    w[i] = pack2<T>(act_mul<Act>({gate[2 * i], gate[2 * i + 1]}, {up[2 * i], up[2 * i + 1]}));
+                stage.put(half, w);
             }
-            store32(g.j.out + at * d + col, y, n, g.j.vec);
-            if (KEEP) {
-                const int blocks = (d + kBlock - 1) / kBlock;
-                int16_t *codes = g.j.codes + at * 2 * d + col;
-                uint8_t *scale = g.j.scales + at * 2 * blocks + col / kBlock;
-                keep32(codes, scale, gate, n, g.j.vec);
-                keep32(codes + d, scale + blocks, up, n, g.j.vec);
-            }
+            stage.flush(mine ? g.j.out + at * d + col : nullptr, n, g.j.vec);
+            if (KEEP)
+                for (int part = 0; part < 2; ++part) {   // gate, up
+                    uint8_t *scale = g.j.scales + (at * 2 + part) * blocks + col / kBlock;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float v[32];
+                        uint32_t w[16];
+                        sums_load32(sums + part * kHalf + c + 32 * half, v);
+                        sums_load_wait();
+                        const uint32_t e = encode32(w, v);
+                        if (mine && col + 32 * half < d)
+                            scale[half] = static_cast<uint8_t>(e);
+                        stage.put(half, w);
+                    }
+                    stage.flush(mine ? g.j.codes + (at * 2 + part) * d + col : nullptr, n, g.j.vec);
+                }
         }
     }
 };
@@ -126,17 +124,11 @@ template <class T> struct GradIn {
         load_along(a, &g.a, bar, x, t.m0 + static_cast<int>(rank) * kHalf, half, t.b);
         load_across(b, &g.b, bar, x, t.n0 * kTile + static_cast<int>(rank) * kHalf, half, t.b);
     }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
-        const int k = g.j.k, r = t.m0 + row;
-        const int64_t at = int64_t(t.b) * g.capacity + r;
-        for (int c = 0; c < kTile && t.n0 * kTile + c < k; c += 32) {
-            float v[32];
-            sums_load32(sums + c, v);
-            sums_load_wait();
-            const int col = t.n0 * kTile + c;
-            if (r < t.rows)
-                store32(g.j.out + at * k + col, v, k - col, g.j.vec);
-        }
+    __device__ static int steps_of(const G &g, int) { return g.steps; }
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
+        const int k = g.j.k, r = t.m0 + row, col = t.n0 * kTile;
+        T *mine = r < t.rows ? g.j.out + (int64_t(t.b) * g.capacity + r) * k + col : nullptr;
+        store_tile(sums, stage, mine, k - col, g.j.vec, 1.f, false);
     }
 };
 
@@ -155,28 +147,16 @@ template <class T> struct GradWeight {
     __device__ static int batch_of(int b) { return b >> 1; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
-        const int x = step * kStep, e = t.b >> 1, live = g.live_of(t.b);
+        const int x = step * kStep, e = t.b >> 1;
         load_across(a, &g.a, bar, x, t.m0 + static_cast<int>(rank) * kHalf, t.b & 1, e);
-        const bool tail = x + kStep > live && live < g.capacity;
+        const bool tail = x + kStep > t.live && t.live < g.capacity;
         load_across(b, tail ? &g.other : &g.b, bar, tail ? 0 : x,
                     t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, e);
     }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums) {
-        const int k = g.j.k, r = t.m0 + row;
-        const int64_t at = int64_t(t.b) * g.rows + r;
-        for (int c = 0; c < kTile && t.n0 * kTile + c < k; c += 32) {
-            float v[32];
-            sums_load32(sums + c, v);
-            sums_load_wait();
-            if (t.steps == 0) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    v[i] = 0.f;
-            }
-            const int col = t.n0 * kTile + c;
-            if (r < t.rows)
-                store32(g.j.out + at * k + col, v, k - col, g.j.vec);
-        }
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
+        const int k = g.j.k, r = t.m0 + row, col = t.n0 * kTile;
+        T *mine = r < t.rows ? g.j.out + (int64_t(t.b) * g.rows + r) * k + col : nullptr;
+        store_tile(sums, stage, mine, k - col, g.j.vec, 1.f, t.steps == 0);
     }
 };
 
@@ -191,82 +171,98 @@ template <class T> struct GateGradArgs {
     T *tail;              // [E, 64, kp]
     const int32_t *live;
     int64_t grad_stride, grad_batch, in_stride, in_batch;
-    int E, T_, d, dp, k, kp, padded;
-    bool vec;             // vectors of grad and codes
+    int T_, d, dp, k, kp, padded;
 };
 
-// (dg, du) of eight columns of a row per thread, zeros from the live rows to a whole step.
+// Eight columns of a row: what the gradients there are computed from.
+template <class T> struct GateGradIn {
+    uint4 dy, gate, up;
+    float sg, su;
+};
+
+constexpr int kGradRows = 4;   // rows of a thread: twelve 16-byte loads on their way
+
+// (dg, du) of eight columns of four rows per thread, zeros from the live rows to a whole step.
 // One pass: 6 bytes and the scales in, 4 out per pair of elements.
-template <class Act, class T> __global__ void __launch_bounds__(256) gate_gradients(GateGradArgs<T> g) {
+template <class Act, class T, bool VEC>
+__global__ void __launch_bounds__(256) gate_gradients(GateGradArgs<T> g) {
     pdl_wait();
     pdl_trigger();
     const int x = (blockIdx.x * 32 + threadIdx.x) * 8;
     const int blocks = (g.d + kBlock - 1) / kBlock;
-    if (x < g.dp)
-        for (int64_t r = int64_t(blockIdx.y) * 8 + threadIdx.y; r < int64_t(g.E) * g.padded;
-             r += int64_t(gridDim.y) * 8) {
-            const int e = static_cast<int>(r / g.padded), i = static_cast<int>(r - int64_t(e) * g.padded);
-            const int live = g.live ? min(max(g.live[e], 0), g.T_) : g.T_;
-            if (i >= (live + kStep - 1) / kStep * kStep)
+    const int e = blockIdx.z, live = g.live ? min(max(g.live[e], 0), g.T_) : g.T_;
+    const int end = (live + kStep - 1) / kStep * kStep;
+    for (int i0 = (blockIdx.y * kGradRows) * 8 + threadIdx.y; i0 < end && x < g.dp;
+         i0 += gridDim.y * kGradRows * 8) {
+        GateGradIn<T> in[kGradRows];
+#pragma unroll
+        for (int j = 0; j < kGradRows; ++j) {
+            const int i = i0 + 8 * j;
+            in[j].dy = in[j].gate = in[j].up = make_uint4(0, 0, 0, 0);
+            in[j].sg = in[j].su = 0.f;
+            if (i >= live)
                 continue;
-            float2 dg[4], du[4];
+            const int64_t at = int64_t(e) * g.T_ + i;
+            const T *grad = g.grad + e * g.grad_batch + i * g.grad_stride + x;
+            const int16_t *gate = g.codes + at * 2 * g.d + x, *up = gate + g.d;
+            const uint8_t *scale = g.scales + at * 2 * blocks + x / kBlock;
+            if (VEC) {
+                in[j].dy = ld_stream(grad);
+                in[j].gate = ld_stream(gate);
+                in[j].up = ld_stream(up);
+            } else {
+                uint32_t v[3][8];
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
-                dg[p] = du[p] = make_float2(0.f, 0.f);
-            if (i < live) {
-                const int64_t at = int64_t(e) * g.T_ + i;
-                const T *grad = g.grad + e * g.grad_batch + i * g.grad_stride + x;
-                const int16_t *gate = g.codes + at * 2 * g.d + x, *up = gate + g.d;
-                const uint8_t *scale = g.scales + at * 2 * blocks + x / kBlock;
-                const float sg = __uint_as_float(uint32_t(scale[0]) << 23),
-                            su = __uint_as_float(uint32_t(scale[blocks]) << 23);
-                float dy[8], a[8], b[8];
-                if (g.vec) {
-                    const uint4 vy = ld_stream(grad), va = ld_stream(gate), vb = ld_stream(up);
-                    const T *py = reinterpret_cast<const T *>(&vy);
-                    const int16_t *pa = reinterpret_cast<const int16_t *>(&va),
-                                  *pb = reinterpret_cast<const int16_t *>(&vb);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        dy[j] = to_float(py[j]);
-                        a[j] = pa[j] * sg;
-                        b[j] = pb[j] * su;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const bool in = x + j < g.d;
-                        dy[j] = in ? to_float(grad[j]) : 0.f;
-                        a[j] = in ? gate[j] * sg : 0.f;
-                        b[j] = in ? up[j] * su : 0.f;
-                    }
+                for (int c = 0; c < 8; ++c) {
+                    const bool here = x + c < g.d;
+                    v[0][c] = here ? ld_stream_u16(reinterpret_cast<const uint16_t *>(grad) + c) : 0;
+                    v[1][c] = here ? ld_stream_u16(reinterpret_cast<const uint16_t *>(gate) + c) : 0;
+                    v[2][c] = here ? ld_stream_u16(reinterpret_cast<const uint16_t *>(up) + c) : 0;
                 }
+                const auto join = [](const uint32_t (&u)[8]) {
+                    return make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16,
+                                      u[6] | u[7] << 16);
+                };
+                in[j].dy = join(v[0]);
+                in[j].gate = join(v[1]);
+                in[j].up = join(v[2]);
+            }
+            in[j].sg = __uint_as_float(uint32_t(scale[0]) << 23);
+            in[j].su = __uint_as_float(uint32_t(scale[blocks]) << 23);
+        }
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const GateGrad2 m = act_grad<Act>({a[2 * p], a[2 * p + 1]}, {b[2 * p], b[2 * p + 1]},
-                                                      {dy[2 * p], dy[2 * p + 1]});
-                    dg[p] = m.gate;
-                    du[p] = m.up;
-                }
+        for (int j = 0; j < kGradRows; ++j) {
+            const int i = i0 + 8 * j;
+            if (i >= end)
+                break;
+            const T *dy = reinterpret_cast<const T *>(&in[j].dy);
+            const int16_t *a = reinterpret_cast<const int16_t *>(&in[j].gate),
+                          *b = reinterpret_cast<const int16_t *>(&in[j].up);
+            uint32_t dg[4], du[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const GateGrad2 m = act_grad<Act>(
+                    {a[2 * p] * in[j].sg, a[2 * p + 1] * in[j].sg},
+                    {b[2 * p] * in[j].su, b[2 * p + 1] * in[j].su},
+                    {to_float(dy[2 * p]), to_float(dy[2 * p + 1])});
+                dg[p] = i < live ? pack2<T>(m.gate) : 0;
+                du[p] = i < live ? pack2<T>(m.up) : 0;
             }
             T *to = g.rows + (int64_t(e) * 2 * g.padded + i) * g.dp + x;
-            st_vec(to, make_uint4(pack2<T>(dg[0]), pack2<T>(dg[1]), pack2<T>(dg[2]), pack2<T>(dg[3])));
-            st_vec(to + int64_t(g.padded) * g.dp,
-                   make_uint4(pack2<T>(du[0]), pack2<T>(du[1]), pack2<T>(du[2]), pack2<T>(du[3])));
+            st_vec(to, make_uint4(dg[0], dg[1], dg[2], dg[3]));
+            st_vec(to + int64_t(g.padded) * g.dp, make_uint4(du[0], du[1], du[2], du[3]));
         }
+    }
     if (!g.live)
         return;
-    // the partly live step of `in`, 256 columns of a row per block and turn
-    const int64_t chunks = (g.k + 255) / 256, turns = int64_t(g.E) * kStep * chunks;
-    const int64_t block = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
-    for (int64_t i = block; i < turns; i += int64_t(gridDim.y) * gridDim.x) {
-        const int c = static_cast<int>(i % chunks) * 256 + threadIdx.y * 32 + threadIdx.x;
-        const int row = static_cast<int>(i / chunks % kStep), e = static_cast<int>(i / chunks / kStep);
-        const int live = min(max(g.live[e], 0), g.T_), at = live / kStep * kStep + row;
-        if (c < g.k && live % kStep)
-            g.tail[(int64_t(e) * kStep + row) * g.kp + c] =
-                at < live ? g.in[e * g.in_batch + at * g.in_stride + c] : from_float<T>(0.f);
-    }
+    // the partly live step of `in`
+    const int row = blockIdx.y * 8 + threadIdx.y;
+    if (row >= kStep || live % kStep == 0)
+        return;
+    const int from = live / kStep * kStep + row;
+    for (int c = blockIdx.x * 32 + threadIdx.x; c < g.k; c += gridDim.x * 32)
+        g.tail[(int64_t(e) * kStep + row) * g.kp + c] =
+            from < live ? g.in[e * g.in_batch + from * g.in_stride + c] : from_float<T>(0.f);
 }
 
 // ------------------------------------------------------------------ host side
@@ -442,19 +438,21 @@ int run_backward(void *grad_in, void *grad_weight, const void *grad_out, int64_t
     e.grad_batch = grad_batch;
     e.in_stride = a.in_stride;
     e.in_batch = a.in_batch;
-    e.E = E;
     e.T_ = static_cast<int>(a.T);
     e.d = d;
     e.dp = static_cast<int>(w.dp);
     e.k = k;
     e.kp = static_cast<int>(w.kp);
     e.padded = static_cast<int>(w.padded);
-    e.vec = d % 8 == 0 && aligned(grad_out, 16) && aligned(codes, 16) && grad_stride % 8 == 0 &&
-            grad_batch % 8 == 0;
-    const int64_t high = ceil_div64(a.E * w.padded, 8);
+    const bool vec = d % 8 == 0 && aligned(grad_out, 16) && aligned(codes, 16) &&
+                     grad_stride % 8 == 0 && grad_batch % 8 == 0;
+    // eight blocks of rows at least: they share the 64 rows of the tail
+    const int64_t high = ceil_div64(w.padded, 8 * kGradRows);
     const dim3 grid(static_cast<unsigned>(ceil_div64(w.dp, 256)),
-                    static_cast<unsigned>(high < 32768 ? high : 32768));
-    int rc = cuda_status(launch_kernel(gate_gradients<Act, T>, grid, dim3(32, 8), 0, stream, 1, e));
+                    static_cast<unsigned>(high < 8 ? 8 : high < 32768 ? high : 32768),
+                    static_cast<unsigned>(E));
+    auto kernel = vec ? gate_gradients<Act, T, true> : gate_gradients<Act, T, false>;
+    int rc = cuda_status(launch_kernel(kernel, grid, dim3(32, 8), 0, stream, 1, e));
     if (rc != GATED_ACT_OK)
         return rc;
 

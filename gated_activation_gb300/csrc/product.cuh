@@ -171,9 +171,10 @@ __device__ __forceinline__ void sums_load_wait() {
 
 // ------------------------------------------------------------- the kernel
 
-// One tile of a pair: batch, first row and column, rows of the batch, ring steps.
+// One tile of a pair: batch, first row, number of the column tile, rows of the batch, ring steps,
+// live count of the batch (not read again for each step: that stalled the copies).
 struct Tile {
-    int b, m0, n0, rows, steps;
+    int b, m0, n0, rows, steps, live;
 };
 
 // A job J describes a product and what happens to it:
@@ -182,9 +183,11 @@ struct Tile {
 //   J::Args                      what its functions read
 //   J::kLiveRows                 live counts bound the rows; else the summed elements
 //   J::batch_of(b)               index of the live count of a batch
+//   J::steps_of(g, b)            with kLiveRows: ring steps of a batch
 //   J::load(g, tile, step, rank, a, b, bar)   issues the step's copies of one CTA
-//   J::finish(g, tile, row, sums, quarter)    the epilogue of one row (row of the tile
-//                                in [0, 256), sums = tensor memory address of its columns)
+//   J::finish(g, tile, row, sums, stage)      the epilogue of a warp's 32 rows: `row` is the
+//                                lane's (of the tile, in [0, 256)), `sums` the tensor memory
+//                                address of its columns, `stage` the warp's shared memory
 template <class J> struct Product {
     CUtensorMap a, b, other;
     const int32_t *live;   // null: `capacity` everywhere
@@ -196,7 +199,51 @@ template <class J> struct Product {
     }
 };
 
-struct alignas(8) ProductShared {
+// Where a warp turns 64 columns of its 32 rows, a row per thread, into row segments; rows are 144
+// bytes apart, so that neither side has bank conflicts.
+constexpr int kStageRow = 64 * 2 + 16;
+struct Stage {
+    uint8_t *p;
+    // half (0, 1) of the 64 columns of the lane's row, two elements to a word
+    __device__ __forceinline__ void put(int half, const uint32_t (&w)[16]) const {
+        uint4 *to = reinterpret_cast<uint4 *>(p + (threadIdx.x & 31) * kStageRow + half * 64);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            to[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    // Writes n columns (of 64) of every row to its address, the lane's own being `mine` (null:
+    // not written).  `vec`: addresses and n are multiples of 16 bytes; a warp then writes four rows'
+    // 128 bytes at a time, else 64 bytes of one row.
+    __device__ __forceinline__ void flush(void *mine, int n, bool vec) const {
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = 4 * i + (lane >> 3), c = (lane & 7) * 8;
+                uint16_t *to = reinterpret_cast<uint16_t *>(
+                    __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), row));
+                if (to && c < n)
+                    st_vec_out(to + c, *reinterpret_cast<const uint4 *>(p + row * kStageRow + 2 * c));
+            }
+        } else {
+#pragma unroll 8
+            for (int row = 0; row < 32; ++row) {
+                uint16_t *to = reinterpret_cast<uint16_t *>(
+                    __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), row));
+                const uint16_t *from = reinterpret_cast<const uint16_t *>(p + row * kStageRow);
+                if (to && lane < n)
+                    to[lane] = from[lane];
+                if (to && lane + 32 < n)
+                    to[lane + 32] = from[lane + 32];
+            }
+        }
+        __syncwarp();
+    }
+};
+
+struct alignas(16) ProductShared {
+    uint8_t stage[4][32 * kStageRow];
     uint64_t full[kSlots], empty[kSlots], sums_full[2], sums_empty[2];
     uint32_t sums;             // tensor memory address
     volatile uint32_t gave_up;
@@ -225,12 +272,13 @@ template <class J> struct Walk {
         t->b = b;
         t->m0 = (top + rest % high) * kTile;
         t->n0 = rest / high;
-        if (J::kLiveRows) {
-            t->rows = g.live_of(b);
-            t->steps = g.steps;
+        t->live = g.live_of(b);
+        if constexpr (J::kLiveRows) {
+            t->rows = t->live;
+            t->steps = J::steps_of(g, b);
         } else {
             t->rows = g.rows;
-            t->steps = (g.live_of(b) + kStep - 1) / kStep;
+            t->steps = (t->live + kStep - 1) / kStep;
         }
         at += step;
         return true;
@@ -366,7 +414,8 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
                 break;
             sums_fence_after();
             J::finish(g, t, static_cast<int>(rank) * kHalf + quarter * 32 + lane,
-                      sums + half * kTile + (static_cast<uint32_t>(quarter * 32) << 16));
+                      sums + half * kTile + (static_cast<uint32_t>(quarter * 32) << 16),
+                      Stage{s.stage[quarter]});
             sums_fence_before();
             __syncwarp();
             if (lane == 0)
@@ -417,21 +466,33 @@ template <> __device__ __forceinline__ uint32_t pack2<f16>(float2 v) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// The first n of 32 values, each rounded once, to p; whole rows of 16-byte vectors where `vec`.
+// 32 values, each rounded once, as words for a Stage.
+template <class T> __device__ __forceinline__ void pack32(uint32_t (&w)[16], const float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        w[i] = pack2<T>({v[2 * i], v[2 * i + 1]});
+}
+
+// The epilogue of a plain product: every column of the tile below `columns`, times `scale`, rounded
+// to T, into the lane's row at `mine` (null: none).  A sum without terms is 0 whatever tensor memory holds.
 template <class T>
-__device__ __forceinline__ void store32(T *p, const float (&v)[32], int n, bool vec) {
-    if (vec && n >= 32) {
+__device__ __forceinline__ void store_tile(uint32_t sums, const Stage &stage, T *mine, int columns,
+                                           bool vec, float scale, bool zero) {
+    for (int c = 0; c < kTile && c < columns; c += 64) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
-            st_vec_out(p + i, make_uint4(pack2<T>({v[i], v[i + 1]}), pack2<T>({v[i + 2], v[i + 3]}),
-                                         pack2<T>({v[i + 4], v[i + 5]}),
-                                         pack2<T>({v[i + 6], v[i + 7]})));
-        return;
+        for (int half = 0; half < 2; ++half) {
+            float v[32];
+            uint32_t w[16];
+            sums_load32(sums + c + 32 * half, v);
+            sums_load_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                v[i] = zero ? 0.f : v[i] * scale;
+            pack32<T>(w, v);
+            stage.put(half, w);
+        }
+        stage.flush(mine ? mine + c : nullptr, columns - c, vec);
     }
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (i < n)
-            p[i] = from_float<T>(v[i]);
 }
 
 // ------------------------------------------------------------- host side
