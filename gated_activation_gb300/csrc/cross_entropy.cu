@@ -82,6 +82,7 @@ template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<
     const int begin = blockIdx.x * g.segment, end = min(begin + g.segment, g.n);
     int before = 0, all = 0;
     float top = 0.f;
+#pragma unroll 8
     for (int i = threadIdx.x; i < g.n; i += 256) {
         const bool live = target(i) >= 0;
         all += live;
@@ -333,12 +334,7 @@ template <class T> struct PieceGradIn {
         const int64_t tile = (int64_t(t.b) * g.j.m_tiles + t.m0 / kTile) * g.n_tiles + t.n0;
         float *held = g.j.sums + tile * (kTile * kTile) + row;
         for (int c = 0; c < kTile && t.n0 * kTile + c < g.j.k; c += 32, held += 32 * kTile) {
-            float v[32], old[32];
-            if (!g.j.begin) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    old[i] = mine ? held[i * kTile] : 0.f;
-            }
+            float v[32];
             sums_load32(sums + c, v);
             sums_load_wait();
             if (!mine)
@@ -346,7 +342,11 @@ template <class T> struct PieceGradIn {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 const float x = t.steps ? v[i] : 0.f;
-                held[i * kTile] = g.j.begin ? x : old[i] + x;
+                if (g.j.begin)
+                    held[i * kTile] = x;
+                else   // one addition per element and launch: no order to depend on, no load to wait for
+                    asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(held + i * kTile), "f"(x)
+                                 : "memory");
             }
         }
     }
@@ -621,7 +621,7 @@ int run_live_tokens(const Parts &w, const gated_act_vocabulary &a, const float *
     g.wide = a.targets64 != 0;
     g.copy = w.copy;
     const int64_t segment = ceil_div64(a.T, 1024);   // at most 1024 blocks count the targets
-    g.segment = static_cast<int>(segment < 32 ? 32 : segment);
+    g.segment = static_cast<int>(segment < 8 ? 8 : segment);
     const unsigned grid = static_cast<unsigned>(ceil_div64(a.T, g.segment));
     return cuda_status(launch_kernel(live_tokens<T>, dim3(grid), dim3(256), 0, stream, 1, g));
 }

@@ -5,7 +5,7 @@
 //             holds 128 columns of g and the same 128 of u, so that a thread has both.
 //   backward  dg = grad_out u act'(g), du = grad_out act(g) from the kept g and u (one pass
 //             over memory), then grad_in = (dg, du) W and grad_weight = (dg, du)' in.
-#include "product.cuh"
+#include "few_rows.cuh"
 
 #include "gated_act_linear.h"
 
@@ -30,6 +30,15 @@ __device__ __forceinline__ uint32_t code_of(float v, float inverse) {
 }
 __device__ __forceinline__ float inverse_scale(uint32_t e) {
     return e == 255 ? 0.f : __uint_as_float((254u - e) << 23);
+}
+
+// Two codes of a word.  2^23 + 2^15 + q has q + 2^15 in its last mantissa bits, so that no
+// conversion is needed (those run at a quarter of the exponentials' already small rate, in the same unit).
+__device__ __forceinline__ float2 decode2(uint32_t w) {
+    const uint32_t u = w ^ 0x80008000u;
+    return sub2({__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7610)),
+                 __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7632))},
+                both(8388608.f + 32768.f));
 }
 
 // The codes of 32 values, two to a word; returns the scale byte.
@@ -236,15 +245,13 @@ __global__ void __launch_bounds__(256) gate_gradients(GateGradArgs<T> g) {
             if (i >= end)
                 break;
             const T *dy = reinterpret_cast<const T *>(&in[j].dy);
-            const int16_t *a = reinterpret_cast<const int16_t *>(&in[j].gate),
-                          *b = reinterpret_cast<const int16_t *>(&in[j].up);
+            const uint32_t *a = &in[j].gate.x, *b = &in[j].up.x;
             uint32_t dg[4], du[4];
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-                const GateGrad2 m = act_grad<Act>(
-                    {a[2 * p] * in[j].sg, a[2 * p + 1] * in[j].sg},
-                    {b[2 * p] * in[j].su, b[2 * p + 1] * in[j].su},
-                    {to_float(dy[2 * p]), to_float(dy[2 * p + 1])});
+                const GateGrad2 m = act_grad<Act>(mul2(decode2(a[p]), both(in[j].sg)),
+                                                  mul2(decode2(b[p]), both(in[j].su)),
+                                                  {to_float(dy[2 * p]), to_float(dy[2 * p + 1])});
                 dg[p] = i < live ? pack2<T>(m.gate) : 0;
                 du[p] = i < live ? pack2<T>(m.up) : 0;
             }
@@ -326,7 +333,12 @@ int addressable(Layout *t, Carve *ws, cudaStream_t stream) {
     return rc;
 }
 
-uint64_t forward_bytes(const gated_act_linear &a) {
+// Few rows without a checkpoint have a kernel of their own, which reads any layout in place.
+bool few(const gated_act_linear &a, bool keep) { return a.T <= kFewRows && !keep; }
+
+uint64_t forward_bytes(const gated_act_linear &a, bool keep) {
+    if (few(a, keep))
+        return 0;
     Operands o = operands(a);
     Carve ws(nullptr);
     addressable(&o.in, &ws, nullptr);
@@ -339,6 +351,12 @@ int run_forward(void *out, int16_t *codes, uint8_t *scales, const gated_act_line
                 const int32_t *live, void *workspace, cudaStream_t stream) {
     constexpr bool is_bf16 = std::is_same_v<T, bf16>;
     Operands o = operands(a);
+    if (few(a, KEEP))
+        return launch_few_rows<Act, T>(
+            {static_cast<const T *>(a.in), static_cast<const T *>(a.weight), static_cast<T *>(out), live,
+             a.in_stride, a.in_batch, a.weight_stride, a.weight_batch, static_cast<int>(a.T),
+             static_cast<int>(a.k), static_cast<int>(a.d), 1},
+            a.E, tma_addressable(o.in) && tma_addressable(o.weight), stream);
     Carve ws(workspace);
     int rc = addressable(&o.in, &ws, stream);
     if (rc == GATED_ACT_OK)
@@ -369,7 +387,7 @@ int forward(void *out, int16_t *codes, uint8_t *scales, const gated_act_linear *
     int rc = check_sizes(*a);
     if (rc != GATED_ACT_OK || a->T == 0 || a->E == 0)
         return rc;
-    const uint64_t need = forward_bytes(*a), rows = a->E * a->T;
+    const uint64_t need = forward_bytes(*a, codes != nullptr), rows = a->E * a->T;
     if (workspace_bytes < need)
         return GATED_ACT_ERR_SCRATCH;
     if (!codes != !scales)
@@ -553,7 +571,7 @@ extern "C" {
 size_t linear_and_mul_workspace_bytes(const gated_act_linear *a) {
     if (!a || gact::check_sizes(*a) != GATED_ACT_OK || a->E == 0 || a->T == 0)
         return 0;
-    return gact::forward_bytes(*a);
+    return gact::forward_bytes(*a, true);
 }
 size_t linear_and_mul_backward_workspace_bytes(const gated_act_linear *a) {
     if (!a || gact::check_sizes(*a) != GATED_ACT_OK || a->E == 0 || a->T == 0)

@@ -79,8 +79,8 @@ def _check_gated(name, x, w, dy, out, grads, dtype):
 def test_gated(ga, name, m, k, d, dtype):
     x, w, dy = _operands(m, k, d, dtype, m + k + d)
     forward, backward = _ops(ga, name)
+    _check_gated(name, x, w, dy, forward(x, w), None, dtype)
     out, kept = forward(x, w, keep=True)
-    assert torch.equal(out, forward(x, w))
     _check_gated(name, x, w, dy, out, backward(dy, x, w, kept), dtype)
 
 
