@@ -30,6 +30,15 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 
+// Eight elements at any address of theirs.
+template <class T> __device__ __forceinline__ uint4 eight(const T *p) {
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = ld_stream_u16(reinterpret_cast<const uint16_t *>(p) + i);
+    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+}
+
 // ------------------------------------------------------------------ live tokens
 
 // What live_tokens writes; `row` counts live tokens.
@@ -149,16 +158,13 @@ template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<
                 if (row >= 0 && copy) {
                     const T *from = g.in + (i0 + j) * g.in_stride;
                     T *to = g.rows + int64_t(row) * g.kp;
-                    if (((reinterpret_cast<uintptr_t>(from) | reinterpret_cast<uintptr_t>(to)) & 15) == 0) {
-                        int c = (threadIdx.x & 31) * 8;
-                        for (; c + 8 <= g.k; c += 256)
-                            st_vec(to + c, ld_stream(from + c));
-                        for (int x = c; x < g.k && x < c + 8; ++x)
-                            to[x] = from[x];
-                    } else {
-                        for (int c = threadIdx.x & 31; c < g.k; c += 32)
-                            to[c] = from[c];
-                    }
+                    const bool vec = (reinterpret_cast<uintptr_t>(from) & 15) == 0;
+                    int c = (threadIdx.x & 31) * 8;
+#pragma unroll 2
+                    for (; c + 8 <= g.k; c += 256)
+                        st_vec(to + c, vec ? ld_stream(from + c) : eight(from + c));
+                    for (int x = c; x < g.k && x < c + 8; ++x)
+                        to[x] = from[x];
                 } else if (row < 0 && g.grad_in) {
                     T *to = g.grad_in + int64_t(i0 + j) * g.k;
                     if ((reinterpret_cast<uintptr_t>(to) & 15) == 0) {
@@ -198,7 +204,9 @@ __device__ __forceinline__ void load_logits(const G &g, const Tile &t, int first
 // Maximum (in powers of two) and sum of exponentials of each row over a tile's columns.
 template <class T> struct Statistics {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = false, kLiveRows = true;
+    static constexpr bool kAAcross = false, kBAcross = false;
+    static constexpr int kN = kTile, kRows = kTile;
+    static constexpr Live kLive = Live::Rows;
     struct Args {
         const int32_t *goal;
         float2 *part;        // [capacity, tiles]: maximum, sum
@@ -206,7 +214,8 @@ template <class T> struct Statistics {
     };
     using G = Product<Statistics>;
     __device__ static int batch_of(int) { return 0; }
-    __device__ static int steps_of(const G &g, int) { return g.steps; }
+    __device__ static int batches(const G &g) { return g.batches; }
+    __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
         load_logits(g, t, 0, step, rank, a, b, bar);
@@ -254,7 +263,9 @@ template <class T> constexpr float kLift = std::is_same_v<T, f16> ? 16384.f : 1.
 
 template <class T> struct Slopes {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = false, kLiveRows = true;
+    static constexpr bool kAAcross = false, kBAcross = false;
+    static constexpr int kN = kTile, kRows = kTile;
+    static constexpr Live kLive = Live::Rows;
     struct Args {
         Tokens t;
         T *y;              // [padded, piece]
@@ -262,7 +273,8 @@ template <class T> struct Slopes {
     };
     using G = Product<Slopes>;
     __device__ static int batch_of(int) { return 0; }
-    __device__ static int steps_of(const G &g, int) { return g.steps; }
+    __device__ static int batches(const G &g) { return g.batches; }
+    __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
         load_logits(g, t, g.j.first, step, rank, a, b, bar);
@@ -305,33 +317,58 @@ template <class T> struct Slopes {
     }
 };
 
+// Shares that the sums over a piece (`steps` ring steps) are split into: of up to 8 the number that
+// takes the fewest turns of the pairs of SMs, counted in whole sums.  A share more costs its additions
+// in L2, a fiftieth of a sum.  It follows from the live rows, so that it is taken on the device.
+constexpr int kShares = 8;
+__host__ __device__ inline int shares_of(int tiles, int steps, int pairs) {
+    int best = 1;
+    float least = 1e30f;
+    for (int n = 1; n <= kShares && n * 8 <= (steps < 8 ? 8 : steps); ++n) {
+        const float turns = static_cast<float>((int64_t(tiles) * n + pairs - 1) / pairs) / n + 0.02f * n;
+        if (turns < least) {
+            least = turns;
+            best = n;
+        }
+    }
+    return best;
+}
+
 // grad_in's sums += y W over one piece: A = y along the sum, B = the weight across it; each batch
 // sums a share of the piece's columns.  The sums lie as the threads hold them, 256 x 256 to a tile,
 // column after column: a warp reads and writes 128 bytes at once.
 template <class T> struct PieceGradIn {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = true, kLiveRows = true;
+    static constexpr bool kAAcross = false, kBAcross = true;
+    static constexpr int kN = kTile, kRows = kTile;
+    static constexpr Live kLive = Live::Rows;
     struct Args {
         float *sums;
-        int k, first, m_tiles;
+        int k, first, piece_steps, pairs;
         bool begin;
     };
     using G = Product<PieceGradIn>;
     __device__ static int batch_of(int) { return 0; }
-    // shares of whole steps, as even as they get
-    __device__ static int first_step(const G &g, int b) {
-        return static_cast<int>(int64_t(g.steps) * b / g.batches);
+    __device__ static int batches(const G &g) {
+        return shares_of((g.live_of(0) + kTile - 1) / kTile * g.n_tiles, g.j.piece_steps, g.j.pairs);
     }
-    __device__ static int steps_of(const G &g, int b) { return first_step(g, b + 1) - first_step(g, b); }
+    // shares of whole steps, as even as they get
+    __device__ static int first_step(const G &g, const Tile &t, int b) {
+        return static_cast<int>(int64_t(g.steps) * b / t.batches);
+    }
+    __device__ static int steps_of(const G &g, const Tile &t) {
+        return first_step(g, t, t.b + 1) - first_step(g, t, t.b);
+    }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
-        const int x = (first_step(g, t.b) + step) * kStep;
+        const int x = (first_step(g, t, t.b) + step) * kStep;
         load_along(a, &g.a, bar, x, t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
         load_across(b, &g.b, bar, g.j.first + x, t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, 0);
     }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &) {
         const bool mine = t.m0 + row < t.rows;
-        const int64_t tile = (int64_t(t.b) * g.j.m_tiles + t.m0 / kTile) * g.n_tiles + t.n0;
+        const int64_t m_tiles = (t.live + kTile - 1) / kTile;
+        const int64_t tile = (t.b * m_tiles + t.m0 / kTile) * g.n_tiles + t.n0;
         float *held = g.j.sums + tile * (kTile * kTile) + row;
         for (int c = 0; c < kTile && t.n0 * kTile + c < g.j.k; c += 32, held += 32 * kTile) {
             float v[32];
@@ -355,7 +392,9 @@ template <class T> struct PieceGradIn {
 // A piece's rows of grad_weight: A = y across the sum over the live rows, B = in across it.
 template <class T> struct PieceGradWeight {
     using Elem = T;
-    static constexpr bool kAAcross = true, kBAcross = true, kLiveRows = false;
+    static constexpr bool kAAcross = true, kBAcross = true;
+    static constexpr int kN = kTile, kRows = kTile;
+    static constexpr Live kLive = Live::Sum;
     struct Args {
         const float *power;
         T *out;              // the piece's first row
@@ -364,7 +403,8 @@ template <class T> struct PieceGradWeight {
     };
     using G = Product<PieceGradWeight>;
     __device__ static int batch_of(int) { return 0; }
-    __device__ static int steps_of(const G &g, int) { return g.steps; }
+    __device__ static int batches(const G &g) { return g.batches; }
+    __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
         load_across(a, &g.a, bar, step * kStep, t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
@@ -374,7 +414,7 @@ template <class T> struct PieceGradWeight {
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
         const int k = g.j.k, r = t.m0 + row, col = t.n0 * kTile;
         T *mine = r < t.rows ? g.j.out + int64_t(r) * k + col : nullptr;
-        store_tile(sums, stage, mine, k - col, g.j.vec, *g.j.power * (1.f / kLift<T>), t.steps == 0);
+        store_tile<kTile>(sums, stage, mine, k - col, g.j.vec, *g.j.power * (1.f / kLift<T>), t.steps == 0);
     }
 };
 
@@ -388,15 +428,6 @@ template <class T> struct JoinArgs {
     int64_t in_stride, weight_stride;
     int capacity, tiles, k;
 };
-
-// Eight elements at any address of theirs.
-template <class T> __device__ __forceinline__ uint4 eight(const T *p) {
-    uint32_t v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = ld_stream_u16(reinterpret_cast<const uint16_t *>(p) + i);
-    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-}
 
 // A warp per live row.  The target's logit is summed here in fp32 with rounding: the tensor cores cut
 // sums off, which at k = 2048 left it 1e-6 of its size too small.  With the other columns' sum s of
@@ -465,7 +496,7 @@ template <class T> struct GradInArgs {
     const float *sums;
     Tokens t;
     T *out;
-    int k, shares, m_tiles, n_tiles;
+    int k, n_tiles, piece_steps, pairs;
 };
 
 // grad_in's rows from the shares of their sums: a block takes 32 rows x 64 columns of a tile, reads
@@ -479,13 +510,15 @@ template <class T> __global__ void __launch_bounds__(256) join_grad_in(GradInArg
     if (r0 >= count)
         return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t part = int64_t(g.m_tiles) * g.n_tiles * (kTile * kTile);
+    const int tiles = (count + kTile - 1) / kTile * g.n_tiles;
+    const int shares = shares_of(tiles, g.piece_steps, g.pairs);
+    const int64_t part = int64_t(tiles) * (kTile * kTile);
     const float *from = g.sums + (int64_t(r0 / kTile) * g.n_tiles + c0 / kTile) * (kTile * kTile) +
                         (c0 % kTile) * kTile + r0 % kTile + lane;
     for (int c = warp; c < 64 && c0 + c < g.k; c += 8) {
         float v = 0.f;
         if (r0 + lane < count)
-            for (int s = 0; s < g.shares; ++s)
+            for (int s = 0; s < shares; ++s)
                 v += from[s * part + c * kTile];
         held[c][lane] = v;
     }
@@ -541,18 +574,6 @@ int64_t piece_of(const gated_act_vocabulary &a) {
     return n < all ? n : all;
 }
 
-// Shares that grad_in's sums over a piece are split into, so that its tiles occupy the pairs of
-// SMs.  A share costs each piece 8 bytes of traffic per row and column, so that of the counts with
-// equal waves per share the smallest is taken, none leaves fewer than 16 steps, and more than one
-// wave is not split.
-int64_t shares_of(int64_t tiles, int64_t steps) {
-    const int64_t pairs = device_sm_count() / 2;
-    int64_t n = tiles < pairs ? pairs / tiles : 1;
-    if (n > steps / 16)
-        n = steps / 16;
-    return n < 1 ? 1 : n;
-}
-
 // The parts of a workspace.
 struct Parts {
     Layout in, packed, weight;
@@ -560,7 +581,8 @@ struct Parts {
     float2 *part = nullptr;
     float *sums = nullptr;
     void *y = nullptr;
-    int64_t kp, padded, piece, m_tiles = 0, n_tiles = 0, shares = 0;
+    int64_t kp, padded, piece, m_tiles = 0, n_tiles = 0, piece_steps = 0;
+    int pairs = 0;
     bool copy;
     uint64_t bytes;
     int rc;
@@ -583,8 +605,20 @@ struct Parts {
             y = ws.take<void>(2 * padded * piece);
             m_tiles = ceil_div64(a.T, kTile);
             n_tiles = ceil_div64(a.k, kTile);
-            shares = shares_of(m_tiles * n_tiles, ceil_div64(piece, kStep));
-            sums = ws.take<float>(4 * kTile * kTile * shares * m_tiles * n_tiles);
+            piece_steps = ceil_div64(piece < a.V ? piece : a.V, kStep);
+            pairs = device_sm_count() / 2;
+            // the most that any number of live rows takes
+            int64_t most = 0;
+            for (int64_t m = 1; m <= m_tiles; ++m) {
+                const int64_t n = m * n_tiles;
+                const int64_t s = n >= kShares * pairs
+                                      ? kShares
+                                      : shares_of(static_cast<int>(n), static_cast<int>(piece_steps), pairs);
+                most = n * s > most ? n * s : most;
+                if (n >= kShares * pairs)
+                    m = m_tiles - 1 > m ? m_tiles - 1 : m;
+            }
+            sums = ws.take<float>(4 * kTile * kTile * most);
         } else {
             part = ws.take<float2>(8 * ceil_div64(a.V, kTile) * a.T);
         }
@@ -720,11 +754,11 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
             return rc;
         gi.other = gi.a;
         set_rows(&gi, w, a);
-        gi.batches = static_cast<int>(w.shares);
+        gi.batches = kShares;
         gi.n_tiles = static_cast<int>(w.n_tiles);
         gi.steps = static_cast<int>(ceil_div64(cols, kStep));
-        gi.j = {w.sums, k, static_cast<int>(first), static_cast<int>(w.m_tiles), first == 0};
-        rc = launch_product(gi, w.shares * w.m_tiles * w.n_tiles, stream);
+        gi.j = {w.sums, k, static_cast<int>(first), static_cast<int>(w.piece_steps), w.pairs, first == 0};
+        rc = launch_product(gi, kShares * w.m_tiles * w.n_tiles, stream);
 
         if (rc == GATED_ACT_OK)
             rc = encode_map(&gw.a, y, kStep, is_bf16);
@@ -739,8 +773,8 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
     }
     if (rc != GATED_ACT_OK)
         return rc;
-    const GradInArgs<T> j = {w.sums, w.t, static_cast<T *>(grad_in), k, static_cast<int>(w.shares),
-                             static_cast<int>(w.m_tiles), static_cast<int>(w.n_tiles)};
+    const GradInArgs<T> j = {w.sums, w.t, static_cast<T *>(grad_in), k, static_cast<int>(w.n_tiles),
+                             static_cast<int>(w.piece_steps), w.pairs};
     const int64_t blocks = ceil_div64(a.k, 64) * ceil_div64(a.T, 32);
     return cuda_status(launch_kernel(join_grad_in<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
                                      stream, 1, j));

@@ -58,9 +58,11 @@ __device__ __forceinline__ uint32_t encode32(uint32_t (&w)[16], const float (&v)
 
 // ------------------------------------------------------------------- products
 
-template <class Act, class T, bool KEEP> struct Forward {
+template <class Act, class T, int N, bool KEEP> struct Forward {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = false, kLiveRows = true;
+    static constexpr bool kAAcross = false, kBAcross = false;
+    static constexpr int kN = N, kRows = kTile;
+    static constexpr Live kLive = Live::Rows;
     struct Args {
         T *out;
         int16_t *codes;
@@ -70,24 +72,25 @@ template <class Act, class T, bool KEEP> struct Forward {
     };
     using G = Product<Forward>;
     __device__ static int batch_of(int b) { return b; }
+    __device__ static int batches(const G &g) { return g.batches; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
         load_along(a, &g.a, bar, step * kStep, t.m0 + static_cast<int>(rank) * kHalf, 0, t.b);
         // the first CTA brings the gate's rows of the weight, the second the up half's
-        load_along(b, &g.b, bar, step * kStep, t.n0 * kHalf, static_cast<int>(rank), t.b);
+        load_along(b, &g.b, bar, step * kStep, t.n0 * (N / 2), static_cast<int>(rank), t.b);
     }
-    __device__ static int steps_of(const G &g, int) { return g.steps; }
+    __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
         const int d = g.j.d, r = t.m0 + row, blocks = (d + kBlock - 1) / kBlock;
         const bool mine = r < t.rows;
         const int64_t at = int64_t(t.b) * g.capacity + r;
-        for (int c = 0; c < kHalf && t.n0 * kHalf + c < d; c += 64) {
-            const int col = t.n0 * kHalf + c, n = d - col;
+        for (int c = 0; c < N / 2 && t.n0 * (N / 2) + c < d; c += 64) {
+            const int col = t.n0 * (N / 2) + c, n = d - col;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 float gate[32], up[32];
                 sums_load32(sums + c + 32 * half, gate);
-                sums_load32(sums + kHalf + c + 32 * half, up);
+                sums_load32(sums + N / 2 + c + 32 * half, up);
                 sums_load_wait();
                 uint32_t w[16];
 #pragma unroll
@@ -103,7 +106,7 @@ template <class Act, class T, bool KEEP> struct Forward {
                     for (int half = 0; half < 2; ++half) {
                         float v[32];
                         uint32_t w[16];
-                        sums_load32(sums + part * kHalf + c + 32 * half, v);
+                        sums_load32(sums + part * (N / 2) + c + 32 * half, v);
                         sums_load_wait();
                         const uint32_t e = encode32(w, v);
                         if (mine && col + 32 * half < d)
@@ -116,10 +119,75 @@ template <class Act, class T, bool KEEP> struct Forward {
     }
 };
 
-// grad_in: A = (dg, du) along the sum over 2d, B = the weight across it.
-template <class T> struct GradIn {
+// The same product with the roles turned round, for up to N rows that would leave most of a
+// 256-row tile empty: the weight's rows are the tile's (64 of g and the same 64 of u per CTA), the
+// input's its columns.  Warps 0 and 1 of the epilogue hold g, warps 2 and 3 the u of the same columns,
+// which they hand over through shared memory.
+template <class Act, class T, int N> struct Swapped {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = true, kLiveRows = true;
+    static constexpr bool kAAcross = false, kBAcross = false;
+    static constexpr int kN = N, kRows = kHalf;
+    static constexpr Live kLive = Live::Columns;
+    struct Args {
+        T *out;
+    };
+    using G = Product<Swapped>;
+    __device__ static int batch_of(int b) { return b; }
+    __device__ static int batches(const G &g) { return g.batches; }
+    __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
+    __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
+                                uint32_t b, uint32_t bar) {
+        const int col = t.m0 + static_cast<int>(rank) * 64;
+        load_along(a, &g.a, bar, step * kStep, col, 0, t.b);
+        load_along(a + kRowBytes / 2, &g.a, bar, step * kStep, col, 1, t.b);
+        load_along(b, &g.b, bar, step * kStep, static_cast<int>(rank) * (N / 2), 0, t.b);
+    }
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
+        float *held = reinterpret_cast<float *>(stage.s.stage[0]);   // [32 rows, 64 columns]
+        const uint32_t full = smem_address(&stage.s.swap_full), empty = smem_address(&stage.s.swap_empty);
+        const int lane = threadIdx.x & 31, at = row & 63;
+        const bool up = row & 64;
+        const int col = t.m0 + (row >> 7) * 64 + at, d = g.rows;
+        T *out = g.j.out + int64_t(t.b) * g.capacity * d + col;
+        for (int c = 0; c < N && c < t.live; c += 32) {
+            const uint32_t use = stage.uses++;
+            float v[32];
+            sums_load32(sums + c, v);
+            sums_load_wait();
+            if (up) {
+                if (!barrier_wait(empty, (use & 1) ^ 1, &stage.s.gave_up))
+                    return;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    held[i * 64 + at] = v[i];
+                __syncwarp();
+                if (lane == 0)
+                    barrier_arrive(full);
+                continue;
+            }
+            if (!barrier_wait(full, use & 1, &stage.s.gave_up))
+                return;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float2 y = act_mul<Act>({v[i], v[i + 1]}, {held[i * 64 + at], held[i * 64 + 64 + at]});
+                if (col < d && c + i < t.live)
+                    out[int64_t(c + i) * d] = from_float<T>(y.x);
+                if (col < d && c + i + 1 < t.live)
+                    out[int64_t(c + i + 1) * d] = from_float<T>(y.y);
+            }
+            __syncwarp();
+            if (lane == 0)
+                barrier_arrive(empty);
+        }
+    }
+};
+
+// grad_in: A = (dg, du) along the sum over 2d, B = the weight across it.
+template <class T, int N> struct GradIn {
+    using Elem = T;
+    static constexpr bool kAAcross = false, kBAcross = true;
+    static constexpr int kN = N, kRows = kTile;
+    static constexpr Live kLive = Live::Rows;
     struct Args {
         T *out;
         int k, half_steps;   // ring steps of one half of the sum
@@ -127,26 +195,29 @@ template <class T> struct GradIn {
     };
     using G = Product<GradIn>;
     __device__ static int batch_of(int b) { return b; }
+    __device__ static int batches(const G &g) { return g.batches; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
         const int half = step >= g.j.half_steps, x = (step - half * g.j.half_steps) * kStep;
         load_along(a, &g.a, bar, x, t.m0 + static_cast<int>(rank) * kHalf, half, t.b);
-        load_across(b, &g.b, bar, x, t.n0 * kTile + static_cast<int>(rank) * kHalf, half, t.b);
+        load_across<N / 2>(b, &g.b, bar, x, t.n0 * N + static_cast<int>(rank) * (N / 2), half, t.b);
     }
-    __device__ static int steps_of(const G &g, int) { return g.steps; }
+    __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
-        const int k = g.j.k, r = t.m0 + row, col = t.n0 * kTile;
+        const int k = g.j.k, r = t.m0 + row, col = t.n0 * N;
         T *mine = r < t.rows ? g.j.out + (int64_t(t.b) * g.capacity + r) * k + col : nullptr;
-        store_tile(sums, stage, mine, k - col, g.j.vec, 1.f, false);
+        store_tile<N>(sums, stage, mine, k - col, g.j.vec, 1.f, false);
     }
 };
 
 // grad_weight: A = (dg, du) across the sum over the rows, B = in across it; batch 2e + half.
 // Past the live rows dg and du are zeros up to a whole step; the last rows of `in` come from
 // a copy with zeros there, as what lies past the live rows may be anything.
-template <class T> struct GradWeight {
+template <class T, int N> struct GradWeight {
     using Elem = T;
-    static constexpr bool kAAcross = true, kBAcross = true, kLiveRows = false;
+    static constexpr bool kAAcross = true, kBAcross = true;
+    static constexpr int kN = N, kRows = kTile;
+    static constexpr Live kLive = Live::Sum;
     struct Args {
         T *out;
         int k;
@@ -154,18 +225,19 @@ template <class T> struct GradWeight {
     };
     using G = Product<GradWeight>;
     __device__ static int batch_of(int b) { return b >> 1; }
+    __device__ static int batches(const G &g) { return g.batches; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
         const int x = step * kStep, e = t.b >> 1;
         load_across(a, &g.a, bar, x, t.m0 + static_cast<int>(rank) * kHalf, t.b & 1, e);
         const bool tail = x + kStep > t.live && t.live < g.capacity;
-        load_across(b, tail ? &g.other : &g.b, bar, tail ? 0 : x,
-                    t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, e);
+        load_across<N / 2>(b, tail ? &g.other : &g.b, bar, tail ? 0 : x,
+                           t.n0 * N + static_cast<int>(rank) * (N / 2), 0, e);
     }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
-        const int k = g.j.k, r = t.m0 + row, col = t.n0 * kTile;
+        const int k = g.j.k, r = t.m0 + row, col = t.n0 * N;
         T *mine = r < t.rows ? g.j.out + (int64_t(t.b) * g.rows + r) * k + col : nullptr;
-        store_tile(sums, stage, mine, k - col, g.j.vec, 1.f, t.steps == 0);
+        store_tile<N>(sums, stage, mine, k - col, g.j.vec, 1.f, t.steps == 0);
     }
 };
 
@@ -189,12 +261,12 @@ template <class T> struct GateGradIn {
     float sg, su;
 };
 
-constexpr int kGradRows = 4;   // rows of a thread: twelve 16-byte loads on their way
+constexpr int kGradRows = 2;   // rows of a thread: six 16-byte loads on their way
 
 // (dg, du) of eight columns of four rows per thread, zeros from the live rows to a whole step.
 // One pass: 6 bytes and the scales in, 4 out per pair of elements.
 template <class Act, class T, bool VEC>
-__global__ void __launch_bounds__(256) gate_gradients(GateGradArgs<T> g) {
+__global__ void __launch_bounds__(256, 4) gate_gradients(GateGradArgs<T> g) {
     pdl_wait();
     pdl_trigger();
     const int x = (blockIdx.x * 32 + threadIdx.x) * 8;
@@ -305,7 +377,7 @@ int check_sizes(const gated_act_linear &a) {
                    static_cast<double>(ceil_div64(cols, width)) <
                static_cast<double>(most);
     };
-    if (!tiles(a.T, a.d, kHalf) || !tiles(a.T, a.k, kTile) || !tiles(2 * a.d, a.k, kTile) ||
+    if (!tiles(a.T, a.d, 64) || !tiles(a.T, a.k, 128) || !tiles(2 * a.d, a.k, 128) ||
         static_cast<double>(a.E) * static_cast<double>(a.T + kStep) *
                 static_cast<double>(2 * a.d + a.k) > 1e17)
         return GATED_ACT_ERR_TOO_LARGE;
@@ -333,8 +405,12 @@ int addressable(Layout *t, Carve *ws, cudaStream_t stream) {
     return rc;
 }
 
-// Few rows without a checkpoint have a kernel of their own, which reads any layout in place.
-bool few(const gated_act_linear &a, bool keep) { return a.T <= kFewRows && !keep; }
+// Rows without a checkpoint have other kernels where they are few: with up to 32 that leave pairs of
+// SMs without one of the turned tiles, the one that streams the weight through registers; else, with
+// up to 128, the turned product.
+bool few(const gated_act_linear &a, bool keep) {
+    return !keep && a.T <= kFewRows && a.E * ceil_div64(a.d, kHalf) < device_sm_count() / 2;
+}
 
 uint64_t forward_bytes(const gated_act_linear &a, bool keep) {
     if (few(a, keep))
@@ -346,37 +422,77 @@ uint64_t forward_bytes(const gated_act_linear &a, bool keep) {
     return ws.used;
 }
 
+// The parts of a forward product that its jobs share.
+template <class J> int set_forward(Product<J> *g, const gated_act_linear &a, const int32_t *live) {
+    g->other = g->a;
+    g->live = live;
+    g->batches = static_cast<int>(a.E);
+    g->capacity = static_cast<int>(a.T);
+    g->steps = static_cast<int>(ceil_div64(a.k, kStep));
+    return GATED_ACT_OK;
+}
+
+template <class Act, class T, int N, bool KEEP>
+int run_product(void *out, int16_t *codes, uint8_t *scales, const gated_act_linear &a, const Operands &o,
+                const int32_t *live, cudaStream_t stream) {
+    constexpr bool is_bf16 = std::is_same_v<T, bf16>;
+    Product<Forward<Act, T, N, KEEP>> g;
+    int rc = encode_map(&g.a, o.in, kHalf, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&g.b, o.weight, N / 2, is_bf16);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    set_forward(&g, a, live);
+    g.rows = static_cast<int>(a.T);
+    g.n_tiles = static_cast<int>(ceil_div64(a.d, N / 2));
+    g.j = {static_cast<T *>(out), codes, scales, static_cast<int>(a.d),
+           a.d % 8 == 0 && aligned(out, 16) && aligned(codes, 16)};
+    return launch_product(g, a.E * ceil_div64(a.T, kTile) * g.n_tiles, stream);
+}
+
+template <class Act, class T, int N>
+int run_swapped(void *out, const gated_act_linear &a, const Operands &o, const int32_t *live,
+                cudaStream_t stream) {
+    constexpr bool is_bf16 = std::is_same_v<T, bf16>;
+    Product<Swapped<Act, T, N>> g;
+    int rc = encode_map(&g.a, o.weight, 64, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&g.b, o.in, N / 2, is_bf16);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    set_forward(&g, a, live);
+    g.rows = static_cast<int>(a.d);
+    g.n_tiles = 1;
+    g.j = {static_cast<T *>(out)};
+    return launch_product(g, a.E * ceil_div64(a.d, kHalf), stream);
+}
+
 template <class Act, class T, bool KEEP>
 int run_forward(void *out, int16_t *codes, uint8_t *scales, const gated_act_linear &a,
                 const int32_t *live, void *workspace, cudaStream_t stream) {
-    constexpr bool is_bf16 = std::is_same_v<T, bf16>;
     Operands o = operands(a);
-    if (few(a, KEEP))
-        return launch_few_rows<Act, T>(
-            {static_cast<const T *>(a.in), static_cast<const T *>(a.weight), static_cast<T *>(out), live,
-             a.in_stride, a.in_batch, a.weight_stride, a.weight_batch, static_cast<int>(a.T),
-             static_cast<int>(a.k), static_cast<int>(a.d), 1},
-            a.E, tma_addressable(o.in) && tma_addressable(o.weight), stream);
+    if constexpr (!KEEP)
+        if (few(a, KEEP))
+            return launch_few_rows<Act, T>(
+                {static_cast<const T *>(a.in), static_cast<const T *>(a.weight), static_cast<T *>(out),
+                 live, a.in_stride, a.in_batch, a.weight_stride, a.weight_batch, static_cast<int>(a.T),
+                 static_cast<int>(a.k), static_cast<int>(a.d), 1},
+                a.E, tma_addressable(o.in) && tma_addressable(o.weight), stream);
     Carve ws(workspace);
     int rc = addressable(&o.in, &ws, stream);
     if (rc == GATED_ACT_OK)
         rc = addressable(&o.weight, &ws, stream);
-    Product<Forward<Act, T, KEEP>> g;
-    if (rc == GATED_ACT_OK)
-        rc = encode_map(&g.a, o.in, kHalf, is_bf16);
-    if (rc == GATED_ACT_OK)
-        rc = encode_map(&g.b, o.weight, kHalf, is_bf16);
     if (rc != GATED_ACT_OK)
         return rc;
-    g.other = g.a;
-    g.live = live;
-    g.batches = static_cast<int>(a.E);
-    g.capacity = g.rows = static_cast<int>(a.T);
-    g.n_tiles = static_cast<int>(ceil_div64(a.d, kHalf));
-    g.steps = static_cast<int>(ceil_div64(a.k, kStep));
-    g.j = {static_cast<T *>(out), codes, scales, static_cast<int>(a.d),
-           a.d % 8 == 0 && aligned(out, 16) && aligned(codes, 16)};
-    return launch_product(g, a.E * ceil_div64(a.T, kTile) * g.n_tiles, stream);
+    if constexpr (!KEEP) {
+        if (a.T <= 32)
+            return run_swapped<Act, T, 32>(out, a, o, live, stream);
+        if (a.T <= 128)
+            return run_swapped<Act, T, 128>(out, a, o, live, stream);
+    }
+    return tile_columns(a.E * ceil_div64(a.T, kTile), 2 * a.d) == 256
+               ? run_product<Act, T, 256, KEEP>(out, codes, scales, a, o, live, stream)
+               : run_product<Act, T, 128, KEEP>(out, codes, scales, a, o, live, stream);
 }
 
 template <class Act>
@@ -434,11 +550,54 @@ struct BackwardParts {
     uint64_t bytes;
 };
 
+template <class T, int N>
+int run_grad_in(void *grad_in, const gated_act_linear &a, const Layout &rows, const Layout &weight,
+                cudaStream_t stream) {
+    constexpr bool is_bf16 = std::is_same_v<T, bf16>;
+    Product<GradIn<T, N>> g;
+    int rc = encode_map(&g.a, rows, kHalf, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&g.b, weight, kStep, is_bf16);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    g.other = g.a;
+    g.live = a.n_rows;
+    g.batches = static_cast<int>(a.E);
+    g.capacity = g.rows = static_cast<int>(a.T);
+    g.n_tiles = static_cast<int>(ceil_div64(a.k, N));
+    const int half_steps = static_cast<int>(ceil_div64(a.d, kStep));
+    g.steps = 2 * half_steps;
+    g.j = {static_cast<T *>(grad_in), static_cast<int>(a.k), half_steps,
+           a.k % 8 == 0 && aligned(grad_in, 16)};
+    return launch_product(g, a.E * ceil_div64(a.T, kTile) * g.n_tiles, stream);
+}
+
+template <class T, int N>
+int run_grad_weight(void *grad_weight, const gated_act_linear &a, const Layout &rows, const Layout &in,
+                    const Layout &tail, cudaStream_t stream) {
+    constexpr bool is_bf16 = std::is_same_v<T, bf16>;
+    Product<GradWeight<T, N>> g;
+    int rc = encode_map(&g.a, rows, kStep, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&g.b, in, kStep, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&g.other, a.n_rows ? tail : in, kStep, is_bf16);
+    if (rc != GATED_ACT_OK)
+        return rc;
+    g.live = a.n_rows;
+    g.batches = static_cast<int>(2 * a.E);
+    g.capacity = static_cast<int>(a.T);
+    g.rows = static_cast<int>(a.d);
+    g.n_tiles = static_cast<int>(ceil_div64(a.k, N));
+    g.steps = 0;
+    g.j = {static_cast<T *>(grad_weight), static_cast<int>(a.k), a.k % 8 == 0 && aligned(grad_weight, 16)};
+    return launch_product(g, 2 * a.E * ceil_div64(a.d, kTile) * g.n_tiles, stream);
+}
+
 template <class Act, class T>
 int run_backward(void *grad_in, void *grad_weight, const void *grad_out, int64_t grad_stride,
                  int64_t grad_batch, const int16_t *codes, const uint8_t *scales,
                  const gated_act_linear &a, void *workspace, cudaStream_t stream) {
-    constexpr bool is_bf16 = std::is_same_v<T, bf16>;
     const int E = static_cast<int>(a.E), d = static_cast<int>(a.d), k = static_cast<int>(a.k);
     const BackwardParts w(a, workspace, stream);
     if (w.rc != GATED_ACT_OK)
@@ -479,42 +638,14 @@ int run_backward(void *grad_in, void *grad_weight, const void *grad_out, int64_t
                          {1, w.dp, w.padded * w.dp, 2 * w.padded * w.dp}};
     const Layout tail = {w.tail, {a.k, kStep, 1, a.E}, {1, w.kp, 0, kStep * w.kp}};
 
-    Product<GradIn<T>> gi;
-    rc = encode_map(&gi.a, rows, kHalf, is_bf16);
-    if (rc == GATED_ACT_OK)
-        rc = encode_map(&gi.b, w.o.weight, kStep, is_bf16);
+    const int64_t m_tiles = a.E * ceil_div64(a.T, kTile), w_tiles = 2 * a.E * ceil_div64(a.d, kTile);
+    rc = tile_columns(m_tiles, a.k) == 256 ? run_grad_in<T, 256>(grad_in, a, rows, w.o.weight, stream)
+                                           : run_grad_in<T, 128>(grad_in, a, rows, w.o.weight, stream);
     if (rc != GATED_ACT_OK)
         return rc;
-    gi.other = gi.a;
-    gi.live = a.n_rows;
-    gi.batches = E;
-    gi.capacity = gi.rows = static_cast<int>(a.T);
-    gi.n_tiles = static_cast<int>(ceil_div64(k, kTile));
-    const int half_steps = static_cast<int>(ceil_div64(d, kStep));
-    gi.steps = 2 * half_steps;
-    gi.j = {static_cast<T *>(grad_in), k, half_steps, k % 8 == 0 && aligned(grad_in, 16)};
-    rc = launch_product(gi, a.E * ceil_div64(a.T, kTile) * gi.n_tiles, stream);
-    if (rc != GATED_ACT_OK)
-        return rc;
-
-    Product<GradWeight<T>> gw;
-    rc = encode_map(&gw.a, rows, kStep, is_bf16);
-    if (rc == GATED_ACT_OK)
-        rc = encode_map(&gw.b, w.o.in, kStep, is_bf16);
-    if (rc == GATED_ACT_OK)
-        rc = a.n_rows ? encode_map(&gw.other, tail, kStep, is_bf16) : GATED_ACT_OK;
-    if (rc != GATED_ACT_OK)
-        return rc;
-    if (!a.n_rows)
-        gw.other = gw.b;
-    gw.live = a.n_rows;
-    gw.batches = 2 * E;
-    gw.capacity = static_cast<int>(a.T);
-    gw.rows = d;
-    gw.n_tiles = gi.n_tiles;
-    gw.steps = 0;
-    gw.j = {static_cast<T *>(grad_weight), k, k % 8 == 0 && aligned(grad_weight, 16)};
-    return launch_product(gw, 2 * a.E * ceil_div64(d, kTile) * gw.n_tiles, stream);
+    return tile_columns(w_tiles, a.k) == 256
+               ? run_grad_weight<T, 256>(grad_weight, a, rows, w.o.in, tail, stream)
+               : run_grad_weight<T, 128>(grad_weight, a, rows, w.o.in, tail, stream);
 }
 
 template <class Act>

@@ -76,8 +76,31 @@ Layout packed_layout(const Layout &t, void *data) {
     return p;
 }
 
-// Eight elements per thread, loaded one by one (consecutive lanes read consecutive
-// addresses, through L1) and stored as a vector.
+// Eight elements from an address off a 16-byte boundary, out of the two vectors that hold them.
+__device__ __forceinline__ uint4 shifted8(const uint16_t *p) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint4 *v = reinterpret_cast<const uint4 *>(at & ~uintptr_t(15));
+    const uint4 lo = __ldg(v), hi = __ldg(v + 1);
+    const uint32_t off = static_cast<uint32_t>(at & 15), bits = (off & 3) * 8;
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t r[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {   // words from off / 4 on
+        const uint32_t a = off & 8 ? w[i + 2] : w[i];
+        const uint32_t b = off & 8 ? w[i + 3] : w[i + 1];
+        r[i] = off & 4 ? b : a;
+    }
+    uint4 y;
+    y.x = __funnelshift_r(r[0], r[1], bits);
+    y.y = __funnelshift_r(r[1], r[2], bits);
+    y.z = __funnelshift_r(r[2], r[3], bits);
+    y.w = __funnelshift_r(r[3], r[4], bits);
+    return y;
+}
+
+// Eight elements and a 16-byte store per thread and row.  Rows off 16-byte boundaries are read as the
+// aligned vectors that hold them (consecutive lanes share these through L1); where one of the two
+// would reach past the tensor's own bytes, and at a row's end, element by element.
 __global__ void __launch_bounds__(256) pack_rows(Layout to, Layout from) {
     pdl_wait();
     pdl_trigger();
@@ -85,17 +108,27 @@ __global__ void __launch_bounds__(256) pack_rows(Layout to, Layout from) {
     if (x >= to.size[0])
         return;
     const int64_t rows = to.size[1] * to.size[2] * to.size[3];
+    const uintptr_t first = reinterpret_cast<uintptr_t>(from.data);
+    const uintptr_t last = first + 2 * static_cast<uintptr_t>(
+        (from.size[1] - 1) * from.stride[1] + (from.size[2] - 1) * from.stride[2] +
+        (from.size[3] - 1) * from.stride[3] + from.size[0]);
+#pragma unroll 2
     for (int64_t r = int64_t(blockIdx.y) * 8 + threadIdx.y; r < rows; r += int64_t(gridDim.y) * 8) {
         const int64_t y = r % to.size[1], zw = r / to.size[1], z = zw % to.size[2], w = zw / to.size[2];
         const uint16_t *p = static_cast<const uint16_t *>(from.data) + y * from.stride[1] +
                             z * from.stride[2] + w * from.stride[3] + x;
-        uint32_t v[8];
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
+        uint4 v;
+        if (x + 8 <= to.size[0] && at >= first && at + 32 <= last) {
+            v = shifted8(p);
+        } else {
+            uint32_t e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = x + i < to.size[0] ? ld_stream_u16(p + i) : 0;
-        st_vec(static_cast<uint16_t *>(const_cast<void *>(to.data)) + r * to.stride[1] + x,
-               make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
-                          v[6] | v[7] << 16));
+            for (int i = 0; i < 8; ++i)
+                e[i] = x + i < to.size[0] ? ld_stream_u16(p + i) : 0;
+            v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+        }
+        st_vec(static_cast<uint16_t *>(const_cast<void *>(to.data)) + r * to.stride[1] + x, v);
     }
 }
 

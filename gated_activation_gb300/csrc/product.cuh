@@ -24,13 +24,18 @@
 
 namespace gact {
 
-constexpr int kTile = 256;            // rows and columns of a pair's tile
-constexpr int kHalf = kTile / 2;      // of one CTA's part
+constexpr int kTile = 256;            // rows of a pair's tile, and most columns
+constexpr int kHalf = kTile / 2;      // rows of one CTA's part
 constexpr int kStep = 64;             // summed elements per ring slot: 128 bytes
-constexpr int kSlots = 6;
-constexpr int kOperandBytes = kHalf * kStep * 2;
-constexpr int kSlotBytes = 2 * kOperandBytes;
+constexpr int kRowBytes = kHalf * kStep * 2;   // of the first operand in a slot
+constexpr int kRingBytes = 6 * 2 * kRowBytes;
+constexpr int kMostSlots = 10;
 constexpr int kMaxBatches = 2048;
+
+// A slot of a job with N columns per tile: each CTA brings half of the second operand's rows.
+template <int N> constexpr int kSlotBytes = kRowBytes + N / 2 * kStep * 2;
+template <int N> constexpr int kSlots =
+    kRingBytes / kSlotBytes<N> < kMostSlots ? kRingBytes / kSlotBytes<N> : kMostSlots;
 constexpr unsigned long long kProductWaitNs = 1000000000ull;
 
 static __device__ unsigned int g_product_status;   // of this translation unit
@@ -52,6 +57,9 @@ __device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void barrier_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
@@ -119,12 +127,12 @@ template <bool ACROSS> __device__ __forceinline__ uint64_t slot_descriptor(uint3
 // What 16 summed elements add to it.
 template <bool ACROSS> constexpr uint64_t kDescriptorStep = (ACROSS ? 16 * 128 : 16 * 2) >> 4;
 
-// Instruction descriptor (PTX ISA, "Instruction descriptor", kind::f16): fp32 sums of 256 x 256.
-template <class T, bool A_ACROSS, bool B_ACROSS>
+// Instruction descriptor (PTX ISA, "Instruction descriptor", kind::f16): fp32 sums of 256 x N.
+template <class T, int N, bool A_ACROSS, bool B_ACROSS>
 __host__ __device__ constexpr uint32_t product_descriptor() {
     constexpr uint32_t type = std::is_same_v<T, bf16> ? 1 : 0;
     return 1u << 4 | type << 7 | type << 10 | uint32_t(A_ACROSS) << 15 | uint32_t(B_ACROSS) << 16 |
-           uint32_t(kTile / 8) << 17 | uint32_t(kTile / 16) << 24;
+           uint32_t(N / 8) << 17 | uint32_t(kTile / 16) << 24;
 }
 __device__ __forceinline__ void product_step(uint32_t sums, uint64_t a, uint64_t b, uint32_t desc,
                                              bool add) {
@@ -172,22 +180,27 @@ __device__ __forceinline__ void sums_load_wait() {
 // ------------------------------------------------------------- the kernel
 
 // One tile of a pair: batch, first row, number of the column tile, rows of the batch, ring steps,
-// live count of the batch (not read again for each step: that stalled the copies).
+// live count of the batch (not read again for each step: that stalled the copies), batches.
 struct Tile {
-    int b, m0, n0, rows, steps, live;
+    int b, m0, n0, rows, steps, live, batches;
 };
 
 // A job J describes a product and what happens to it:
 //   J::Elem                      bf16 or f16
 //   J::kAAcross, J::kBAcross     operand rows lie across the sum
+//   J::kN                        columns of a tile
+//   J::kRows                     rows that a tile counts for
 //   J::Args                      what its functions read
-//   J::kLiveRows                 live counts bound the rows; else the summed elements
+//   J::kLive                     what the live counts bound
 //   J::batch_of(b)               index of the live count of a batch
-//   J::steps_of(g, b)            with kLiveRows: ring steps of a batch
+//   J::batches(g)                how many there are, of at most g.batches
+//   J::steps_of(g, tile)         ring steps of a tile, where live counts do not bound them
 //   J::load(g, tile, step, rank, a, b, bar)   issues the step's copies of one CTA
 //   J::finish(g, tile, row, sums, stage)      the epilogue of a warp's 32 rows: `row` is the
 //                                lane's (of the tile, in [0, 256)), `sums` the tensor memory
 //                                address of its columns, `stage` the warp's shared memory
+enum class Live { Rows, Sum, Columns };
+
 template <class J> struct Product {
     CUtensorMap a, b, other;
     const int32_t *live;   // null: `capacity` everywhere
@@ -202,8 +215,11 @@ template <class J> struct Product {
 // Where a warp turns 64 columns of its 32 rows, a row per thread, into row segments; rows are 144
 // bytes apart, so that neither side has bank conflicts.
 constexpr int kStageRow = 64 * 2 + 16;
+struct ProductShared;
 struct Stage {
     uint8_t *p;
+    ProductShared &s;
+    uint32_t &uses;   // of the whole block's stage memory, for swap_full and swap_empty
     // half (0, 1) of the 64 columns of the lane's row, two elements to a word
     __device__ __forceinline__ void put(int half, const uint32_t (&w)[16]) const {
         uint4 *to = reinterpret_cast<uint4 *>(p + (threadIdx.x & 31) * kStageRow + half * 64);
@@ -244,12 +260,12 @@ struct Stage {
 
 struct alignas(16) ProductShared {
     uint8_t stage[4][32 * kStageRow];
-    uint64_t full[kSlots], empty[kSlots], sums_full[2], sums_empty[2];
+    uint64_t full[kMostSlots], empty[kMostSlots], sums_full[2], sums_empty[2], swap_full, swap_empty;
     uint32_t sums;             // tensor memory address
     volatile uint32_t gave_up;
     int first[kMaxBatches + 1];   // first tile row of each batch
 };
-constexpr size_t kProductShared = kSlots * kSlotBytes + sizeof(ProductShared) + 1024;
+constexpr size_t kProductShared = kRingBytes + sizeof(ProductShared) + 1024;
 
 constexpr int kTallest = 8;   // tile rows that are walked together, so that the tiles of a wave
                               // share rows and columns in L2
@@ -258,9 +274,10 @@ constexpr int kTallest = 8;   // tile rows that are walked together, so that the
 template <class J> struct Walk {
     const Product<J> &g;
     const ProductShared &s;
-    int at, step, b = 0, total;
+    int at, step, b = 0, batches, total;
     __device__ Walk(const Product<J> &g_, const ProductShared &s_)
-        : g(g_), s(s_), at(blockIdx.x >> 1), step(gridDim.x >> 1), total(s_.first[g_.batches]) {}
+        : g(g_), s(s_), at(blockIdx.x >> 1), step(gridDim.x >> 1), batches(J::batches(g_)),
+          total(s_.first[batches]) {}
     __device__ bool next(Tile *t) {
         if (at >= total * g.n_tiles)
             return false;
@@ -270,16 +287,15 @@ template <class J> struct Walk {
         const int group = r / (kTallest * g.n_tiles), top = group * kTallest;
         const int high = min(kTallest, tall - top), rest = r - top * g.n_tiles;
         t->b = b;
-        t->m0 = (top + rest % high) * kTile;
+        t->batches = batches;
+        t->m0 = (top + rest % high) * J::kRows;
         t->n0 = rest / high;
         t->live = g.live_of(b);
-        if constexpr (J::kLiveRows) {
-            t->rows = t->live;
-            t->steps = J::steps_of(g, b);
-        } else {
-            t->rows = g.rows;
+        t->rows = J::kLive == Live::Rows ? t->live : g.rows;
+        if constexpr (J::kLive == Live::Sum)
             t->steps = (t->live + kStep - 1) / kStep;
-        }
+        else
+            t->steps = J::steps_of(g, *t);
         at += step;
         return true;
     }
@@ -289,15 +305,16 @@ template <class J>
 __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__ Product<J> g) {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_address(raw) + 1023u) & ~1023u;   // the swizzle's period
+    constexpr int SLOTS = kSlots<J::kN>, SLOT = kSlotBytes<J::kN>;
     ProductShared &s =
-        *reinterpret_cast<ProductShared *>(raw + (base - smem_address(raw)) + kSlots * kSlotBytes);
+        *reinterpret_cast<ProductShared *>(raw + (base - smem_address(raw)) + kRingBytes);
     const uint32_t full = smem_address(s.full), empty = smem_address(s.empty),
                    sums_full = smem_address(s.sums_full), sums_empty = smem_address(s.sums_empty);
     const uint32_t rank = cluster_rank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
+        for (int i = 0; i < SLOTS; ++i) {
             barrier_init(full + 8 * i, 1);
             barrier_init(empty + 8 * i, 1);
         }
@@ -305,6 +322,8 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
             barrier_init(sums_full + 8 * i, 1);
             barrier_init(sums_empty + 8 * i, 8);   // four epilogue warps of each CTA
         }
+        barrier_init(smem_address(&s.swap_full), 2);
+        barrier_init(smem_address(&s.swap_empty), 2);
         s.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -321,18 +340,21 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
     pdl_trigger();
     if (warp == 3) {
         int sum = 0;
-        for (int b0 = 0; b0 < g.batches; b0 += 32) {
+        const int batches = J::batches(g);
+        for (int b0 = 0; b0 < batches; b0 += 32) {
             const int b = b0 + lane;
             int n = 0;
-            if (b < g.batches)
-                n = ((J::kLiveRows ? g.live_of(b) : g.rows) + kTile - 1) / kTile;
+            if (b < batches)
+                n = ((J::kLive == Live::Rows ? g.live_of(b)
+                      : J::kLive == Live::Columns && g.live_of(b) == 0 ? 0 : g.rows) +
+                     J::kRows - 1) / J::kRows;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int up = __shfl_up_sync(0xFFFFFFFFu, n, o);
                 if (lane >= o)
                     n += up;
             }
-            if (b < g.batches)
+            if (b < batches)
                 s.first[b + 1] = sum + n;
             sum += __shfl_sync(0xFFFFFFFFu, n, 31);
         }
@@ -356,27 +378,27 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
             for (int k = 0; k < t.steps; ++k) {
                 if (!(ok = barrier_wait(empty + 8 * slot, phase ^ 1, &s.gave_up)))
                     break;
-                const uint32_t to = base + slot * kSlotBytes;
+                const uint32_t to = base + slot * SLOT;
                 if (rank == 0)
-                    barrier_expect(full + 8 * slot, 2 * kSlotBytes);
-                J::load(g, t, k, rank, to, to + kOperandBytes, in_first_cta(full + 8 * slot));
-                if (++slot == kSlots) {
+                    barrier_expect(full + 8 * slot, 2 * SLOT);
+                J::load(g, t, k, rank, to, to + kRowBytes, in_first_cta(full + 8 * slot));
+                if (++slot == SLOTS) {
                     slot = 0;
                     phase ^= 1;
                 }
             }
         // every use of a slot is over (at once for one never used): nothing arrives at this CTA's
         // barriers after its end
-        for (int i = 0; ok && i < kSlots; ++i) {
+        for (int i = 0; ok && i < SLOTS; ++i) {
             ok = barrier_wait(empty + 8 * slot, phase ^ 1, &s.gave_up);
-            if (++slot == kSlots) {
+            if (++slot == SLOTS) {
                 slot = 0;
                 phase ^= 1;
             }
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {
         constexpr uint32_t desc =
-            product_descriptor<typename J::Elem, J::kAAcross, J::kBAcross>();
+            product_descriptor<typename J::Elem, J::kN, J::kAAcross, J::kBAcross>();
         uint32_t slot = 0, phase = 0, turn = 0;
         bool ok = true;
         while (ok && walk.next(&t)) {
@@ -388,15 +410,15 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
                 if (!(ok = barrier_wait(full + 8 * slot, phase, &s.gave_up)))
                     break;
                 sums_fence_after();
-                const uint32_t from = base + slot * kSlotBytes;
+                const uint32_t from = base + slot * SLOT;
                 const uint64_t a = slot_descriptor<J::kAAcross>(from),
-                               b = slot_descriptor<J::kBAcross>(from + kOperandBytes);
+                               b = slot_descriptor<J::kBAcross>(from + kRowBytes);
 #pragma unroll
                 for (int i = 0; i < kStep / 16; ++i)
                     product_step(to, a + i * kDescriptorStep<J::kAAcross>,
                                  b + i * kDescriptorStep<J::kBAcross>, desc, k > 0 || i > 0);
                 product_commit(empty + 8 * slot);
-                if (++slot == kSlots) {
+                if (++slot == SLOTS) {
                     slot = 0;
                     phase ^= 1;
                 }
@@ -407,7 +429,7 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
         }
     } else if (warp >= 4) {
         const int quarter = warp & 3;   // the tensor memory lanes that the warp may read
-        uint32_t turn = 0;
+        uint32_t turn = 0, uses = 0;
         while (walk.next(&t)) {
             const uint32_t half = turn & 1;
             if (!barrier_wait(sums_full + 8 * half, (turn >> 1) & 1, &s.gave_up))
@@ -415,7 +437,7 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
             sums_fence_after();
             J::finish(g, t, static_cast<int>(rank) * kHalf + quarter * 32 + lane,
                       sums + half * kTile + (static_cast<uint32_t>(quarter * 32) << 16),
-                      Stage{s.stage[quarter]});
+                      Stage{s.stage[quarter], s, uses});
             sums_fence_before();
             __syncwarp();
             if (lane == 0)
@@ -447,16 +469,19 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
 
 // ------------------------------------------------------------- loads, stores
 
-// 128 operand rows from `row` on, summed elements from `x` on.
+// The box's operand rows from `row` on, summed elements from `x` on.
 __device__ __forceinline__ void load_along(uint32_t dst, const CUtensorMap *map, uint32_t bar,
                                            int x, int row, int z, int w) {
     box_load(dst, map, bar, x, row, z, w);
 }
-// The same of an operand whose rows lie across the sum.
+// The same of `rows` (64 or 128) of an operand whose rows lie across the sum.
+template <int ROWS = kHalf>
 __device__ __forceinline__ void load_across(uint32_t dst, const CUtensorMap *map, uint32_t bar,
                                             int x, int row, int z, int w) {
+    static_assert(ROWS == 64 || ROWS == 128);
     box_load(dst, map, bar, row, x, z, w);
-    box_load(dst + kStep * 128, map, bar, row + 64, x, z, w);
+    if (ROWS == 128)
+        box_load(dst + kStep * 128, map, bar, row + 64, x, z, w);
 }
 
 template <class T> __device__ __forceinline__ uint32_t pack2(float2 v);
@@ -475,10 +500,10 @@ template <class T> __device__ __forceinline__ void pack32(uint32_t (&w)[16], con
 
 // The epilogue of a plain product: every column of the tile below `columns`, times `scale`, rounded
 // to T, into the lane's row at `mine` (null: none).  A sum without terms is 0 whatever tensor memory holds.
-template <class T>
+template <int N, class T>
 __device__ __forceinline__ void store_tile(uint32_t sums, const Stage &stage, T *mine, int columns,
                                            bool vec, float scale, bool zero) {
-    for (int c = 0; c < kTile && c < columns; c += 64) {
+    for (int c = 0; c < N && c < columns; c += 64) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float v[32];
@@ -541,6 +566,14 @@ template <class J> int launch_product(const Product<J> &g, int64_t tiles, cudaSt
     const int pairs = device_sm_count() / 2;
     const unsigned grid = 2u * static_cast<unsigned>(tiles < pairs ? (tiles < 1 ? 1 : tiles) : pairs);
     return cuda_status(launch_kernel(kernel, dim3(grid), dim3(256), kProductShared, stream, 2, g));
+}
+
+// Columns of a tile, 256 or 128, for `rows` tile rows and `cols` columns: those that take the SM
+// pairs fewer turns.  A tile of 128 takes 0.6 of the time of one of 256.
+inline int tile_columns(int64_t rows, int64_t cols) {
+    const int64_t pairs = device_sm_count() / 2;
+    const auto turns = [&](int64_t n) { return ceil_div64(rows * ceil_div64(cols, n), pairs); };
+    return 0.6 * static_cast<double>(turns(128)) < static_cast<double>(turns(256)) ? 128 : 256;
 }
 
 // Reads and clears this translation unit's status.

@@ -125,6 +125,35 @@ def test_experts(ga, name, m, k, d, counts, dtype):
         _check_gated(name, x[i, :n], w[i], dy[i, :n], out[i, :n], (gi[i, :n], gw[i]), dtype)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+@pytest.mark.parametrize("m,k,d,counts", [
+    (1, 64, 96, [1, 0, 1]), (8, 130, 33, [8, 0, 3]), (16, 2048, 40, [16, 9, 0, 1]),
+    (32, 72, 136, [0, 32, 17]), (32, 256, 40, [i % 33 for i in range(100)]),
+    (20, 33, 130, [i % 21 for i in range(50)]), (100, 200, 72, [100, 0, 33, 64, 1, 96]),
+    (128, 64, 300, [128, 5, 65] * 40), (129, 64, 40, [129, 0, 7])])
+def test_experts_without_checkpoint(ga, name, m, k, d, counts, dtype):
+    """The kernels for few rows: those that stream the weight, and the turned products."""
+    x, w, _ = _operands(m, k, d, dtype, m + k, len(counts))
+    for i, n in enumerate(counts):
+        x[i, n:] = float("nan")
+    out = torch.full((len(counts), m, d), -7.0, dtype=dtype, device="cuda")
+    _ops(ga, name)[0](x, w, n_rows=torch.tensor(counts, dtype=torch.int32, device="cuda"), out=out)
+    for i, n in enumerate(counts):
+        assert (out[i, n:] == -7).all()
+        _check_gated(name, x[i, :n], w[i], None, out[i, :n], None, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,k,d", [(1, 264, 9800), (16, 72, 10001), (32, 1030, 9728), (33, 520, 200),
+                                   (64, 2000, 700), (128, 96, 9900), (100, 77, 333), (7, 8200, 24)])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 8), (3, 1)])
+def test_few_rows(ga, m, k, d, pad, shift, dtype):
+    x, w, _ = _operands(m, k, d, dtype, m + k)
+    out = ga.linear_gelu_and_mul(_strided(x, pad, shift), _strided(w, pad, shift))
+    _check_gated("gelu", x, w, None, out, None, dtype)
+
+
 def test_gated_special_values(ga):
     """An infinity or a NaN reaches what it is multiplied into, and nothing else."""
     x, w, dy = _operands(70, 64, 40, BF16, 11)
