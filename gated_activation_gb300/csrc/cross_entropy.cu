@@ -204,7 +204,7 @@ __device__ __forceinline__ void load_logits(const G &g, const Tile &t, int first
 // Maximum (in powers of two) and sum of exponentials of each row over a tile's columns.
 template <class T> struct Statistics {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = false;
+    static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
     static constexpr int kN = kTile, kRows = kTile;
     static constexpr Live kLive = Live::Rows;
     struct Args {
@@ -213,7 +213,7 @@ template <class T> struct Statistics {
         int V;
     };
     using G = Product<Statistics>;
-    __device__ static int batch_of(int) { return 0; }
+    __device__ static int batch_of(int, bool) { return 0; }
     __device__ static int batches(const G &g) { return g.batches; }
     __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
@@ -263,7 +263,7 @@ template <class T> constexpr float kLift = std::is_same_v<T, f16> ? 16384.f : 1.
 
 template <class T> struct Slopes {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = false;
+    static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
     static constexpr int kN = kTile, kRows = kTile;
     static constexpr Live kLive = Live::Rows;
     struct Args {
@@ -272,7 +272,7 @@ template <class T> struct Slopes {
         int V, first, piece;
     };
     using G = Product<Slopes>;
-    __device__ static int batch_of(int) { return 0; }
+    __device__ static int batch_of(int, bool) { return 0; }
     __device__ static int batches(const G &g) { return g.batches; }
     __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
@@ -317,41 +317,42 @@ template <class T> struct Slopes {
     }
 };
 
-// Shares that the sums over a piece (`steps` ring steps) are split into: of up to 8 the number that
-// takes the fewest turns of the pairs of SMs, counted in whole sums.  A share more costs its additions
-// in L2, a fiftieth of a sum.  It follows from the live rows, so that it is taken on the device.
-constexpr int kShares = 8;
-__host__ __device__ inline int shares_of(int tiles, int steps, int pairs) {
-    int best = 1;
-    float least = 1e30f;
-    for (int n = 1; n <= kShares && n * 8 <= (steps < 8 ? 8 : steps); ++n) {
-        const float turns = static_cast<float>((int64_t(tiles) * n + pairs - 1) / pairs) / n + 0.02f * n;
-        if (turns < least) {
-            least = turns;
-            best = n;
-        }
+// Shares that grad_in's sums over a piece are split into, so that the longest tile is at most half of
+// what each pair of SMs has to do.  The number follows from the live rows: it is taken on the device,
+// and from the numbers of a whole piece, so that it is the same for all.
+constexpr int kShares = 32;
+struct Shares {
+    int n_tiles, piece_steps, w_tiles, pairs;   // column tiles of grad_in; the piece's steps; tiles of grad_weight
+    __host__ __device__ int operator()(int64_t live) const {
+        const int64_t tiles = (live + kTile - 1) / kTile * n_tiles, w_steps = (live + kStep - 1) / kStep;
+        const int64_t each = (tiles * piece_steps + w_tiles * w_steps) / pairs + 1;
+        int64_t n = (2 * piece_steps + each - 1) / each;
+        n = n < piece_steps / 8 ? n : piece_steps / 8;
+        return n < 1 ? 1 : n > kShares ? kShares : static_cast<int>(n);
     }
-    return best;
-}
+};
 
 // grad_in's sums += y W over one piece: A = y along the sum, B = the weight across it; each batch
 // sums a share of the piece's columns.  The sums lie as the threads hold them, 256 x 256 to a tile,
-// column after column: a warp reads and writes 128 bytes at once.
-template <class T> struct PieceGradIn {
+// column after column: a warp writes 128 bytes at once.
+// Second, the piece's rows of grad_weight: A = y across the sum over the live rows, B = in across it.
+template <class T> struct PieceGradients {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = true;
+    static constexpr bool kAAcross = false, kBAcross = true, kSecond = true;
     static constexpr int kN = kTile, kRows = kTile;
     static constexpr Live kLive = Live::Rows;
     struct Args {
+        CUtensorMap y, in, packed;   // of the second product
         float *sums;
-        int k, first, piece_steps, pairs;
-        bool begin;
+        const float *power;
+        T *grad_weight;              // the piece's first row
+        Shares shares;
+        int k, first;
+        bool begin, vec;
     };
-    using G = Product<PieceGradIn>;
-    __device__ static int batch_of(int) { return 0; }
-    __device__ static int batches(const G &g) {
-        return shares_of((g.live_of(0) + kTile - 1) / kTile * g.n_tiles, g.j.piece_steps, g.j.pairs);
-    }
+    using G = Product<PieceGradients>;
+    __device__ static int batch_of(int, bool) { return 0; }
+    __device__ static int batches(const G &g) { return g.j.shares(g.live_of(0)); }
     // shares of whole steps, as even as they get
     __device__ static int first_step(const G &g, const Tile &t, int b) {
         return static_cast<int>(int64_t(g.steps) * b / t.batches);
@@ -361,16 +362,29 @@ template <class T> struct PieceGradIn {
     }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
-        const int x = (first_step(g, t, t.b) + step) * kStep;
-        load_along(a, &g.a, bar, x, t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
-        load_across(b, &g.b, bar, g.j.first + x, t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, 0);
+        const int row = t.m0 + static_cast<int>(rank) * kHalf;
+        const int col = t.n0 * kTile + static_cast<int>(rank) * kHalf;
+        if (!t.second) {
+            const int x = (first_step(g, t, t.b) + step) * kStep;
+            load_along(a, &g.a, bar, x, row, 0, 0);
+            load_across(b, &g.b, bar, g.j.first + x, col, 0, 0);
+            return;
+        }
+        load_across(a, &g.j.y, bar, step * kStep, row, 0, 0);
+        load_across(b, t.live < g.capacity ? &g.j.packed : &g.j.in, bar, step * kStep, col, 0, 0);
     }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &) {
-        const bool mine = t.m0 + row < t.rows;
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
+        const int k = g.j.k, r = t.m0 + row, col = t.n0 * kTile;
+        const bool mine = r < t.rows;
+        if (t.second) {
+            store_tile<kTile>(sums, stage, mine ? g.j.grad_weight + int64_t(r) * k + col : nullptr, k - col,
+                              g.j.vec, *g.j.power * (1.f / kLift<T>), t.steps == 0);
+            return;
+        }
         const int64_t m_tiles = (t.live + kTile - 1) / kTile;
         const int64_t tile = (t.b * m_tiles + t.m0 / kTile) * g.n_tiles + t.n0;
         float *held = g.j.sums + tile * (kTile * kTile) + row;
-        for (int c = 0; c < kTile && t.n0 * kTile + c < g.j.k; c += 32, held += 32 * kTile) {
+        for (int c = 0; c < kTile && col + c < k; c += 32, held += 32 * kTile) {
             float v[32];
             sums_load32(sums + c, v);
             sums_load_wait();
@@ -386,35 +400,6 @@ template <class T> struct PieceGradIn {
                                  : "memory");
             }
         }
-    }
-};
-
-// A piece's rows of grad_weight: A = y across the sum over the live rows, B = in across it.
-template <class T> struct PieceGradWeight {
-    using Elem = T;
-    static constexpr bool kAAcross = true, kBAcross = true;
-    static constexpr int kN = kTile, kRows = kTile;
-    static constexpr Live kLive = Live::Sum;
-    struct Args {
-        const float *power;
-        T *out;              // the piece's first row
-        int k;
-        bool vec;
-    };
-    using G = Product<PieceGradWeight>;
-    __device__ static int batch_of(int) { return 0; }
-    __device__ static int batches(const G &g) { return g.batches; }
-    __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
-    __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
-                                uint32_t b, uint32_t bar) {
-        load_across(a, &g.a, bar, step * kStep, t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
-        load_across(b, t.live < g.capacity ? &g.other : &g.b, bar, step * kStep,
-                    t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, 0);
-    }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
-        const int k = g.j.k, r = t.m0 + row, col = t.n0 * kTile;
-        T *mine = r < t.rows ? g.j.out + int64_t(r) * k + col : nullptr;
-        store_tile<kTile>(sums, stage, mine, k - col, g.j.vec, *g.j.power * (1.f / kLift<T>), t.steps == 0);
     }
 };
 
@@ -496,11 +481,12 @@ template <class T> struct GradInArgs {
     const float *sums;
     Tokens t;
     T *out;
-    int k, n_tiles, piece_steps, pairs;
+    Shares shares;
+    int k;
 };
 
 // grad_in's rows from the shares of their sums: a block takes 32 rows x 64 columns of a tile, reads
-// columns and writes rows.
+// columns (eight loads on their way per thread) and writes rows.
 template <class T> __global__ void __launch_bounds__(256) join_grad_in(GradInArgs<T> g) {
     __shared__ float held[64][33];
     pdl_wait();
@@ -510,18 +496,24 @@ template <class T> __global__ void __launch_bounds__(256) join_grad_in(GradInArg
     if (r0 >= count)
         return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int tiles = (count + kTile - 1) / kTile * g.n_tiles;
-    const int shares = shares_of(tiles, g.piece_steps, g.pairs);
-    const int64_t part = int64_t(tiles) * (kTile * kTile);
-    const float *from = g.sums + (int64_t(r0 / kTile) * g.n_tiles + c0 / kTile) * (kTile * kTile) +
+    const int shares = g.shares(count);
+    const int64_t part = int64_t((count + kTile - 1) / kTile) * g.shares.n_tiles * (kTile * kTile);
+    const float *from = g.sums + (int64_t(r0 / kTile) * g.shares.n_tiles + c0 / kTile) * (kTile * kTile) +
                         (c0 % kTile) * kTile + r0 % kTile + lane;
-    for (int c = warp; c < 64 && c0 + c < g.k; c += 8) {
-        float v = 0.f;
-        if (r0 + lane < count)
-            for (int s = 0; s < shares; ++s)
-                v += from[s * part + c * kTile];
-        held[c][lane] = v;
-    }
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = 0.f;
+    for (int s = 0; s < shares; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = warp + 8 * i;
+            if (r0 + lane < count && c0 + c < g.k)
+                v[i] += from[s * part + c * kTile];
+        }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        held[warp + 8 * i][lane] = v[i];
     __syncthreads();
     const float power = *g.t.power * (1.f / kLift<T>);
     for (int i = warp; i < 32 && r0 + i < count; i += 8) {
@@ -581,8 +573,8 @@ struct Parts {
     float2 *part = nullptr;
     float *sums = nullptr;
     void *y = nullptr;
-    int64_t kp, padded, piece, m_tiles = 0, n_tiles = 0, piece_steps = 0;
-    int pairs = 0;
+    int64_t kp, padded, piece;
+    Shares shares = {};
     bool copy;
     uint64_t bytes;
     int rc;
@@ -603,20 +595,21 @@ struct Parts {
             t.weight = ws.take<float>(4 * a.T);
             t.power = ws.take<float>(4);
             y = ws.take<void>(2 * padded * piece);
-            m_tiles = ceil_div64(a.T, kTile);
-            n_tiles = ceil_div64(a.k, kTile);
-            piece_steps = ceil_div64(piece < a.V ? piece : a.V, kStep);
-            pairs = device_sm_count() / 2;
-            // the most that any number of live rows takes
+            shares = {static_cast<int>(ceil_div64(a.k, kTile)),
+                      static_cast<int>(ceil_div64(piece < a.V ? piece : a.V, kStep)),
+                      static_cast<int>(ceil_div64(piece < a.V ? piece : a.V, kTile) * ceil_div64(a.k, kTile)),
+                      device_sm_count() / 2};
+            // the most tiles of sums that any number of live rows takes: with more rows there are
+            // more tiles and no more shares, and past kShares x pairs tiles the last count has the most
             int64_t most = 0;
+            const int64_t m_tiles = ceil_div64(a.T, kTile);
             for (int64_t m = 1; m <= m_tiles; ++m) {
-                const int64_t n = m * n_tiles;
-                const int64_t s = n >= kShares * pairs
-                                      ? kShares
-                                      : shares_of(static_cast<int>(n), static_cast<int>(piece_steps), pairs);
-                most = n * s > most ? n * s : most;
-                if (n >= kShares * pairs)
-                    m = m_tiles - 1 > m ? m_tiles - 1 : m;
+                const int64_t n = m * shares.n_tiles;
+                if (n > int64_t(kShares) * shares.pairs)
+                    m = m_tiles;
+                // fewer rows of the last tile mean fewer steps of grad_weight, and more shares
+                const int64_t s = shares((m - 1) * kTile + 1);
+                most = m * shares.n_tiles * s > most ? m * shares.n_tiles * s : most;
             }
             sums = ws.take<float>(4 * kTile * kTile * most);
         } else {
@@ -654,7 +647,7 @@ int run_live_tokens(const Parts &w, const gated_act_vocabulary &a, const float *
     g.V = static_cast<int>(a.V);
     g.wide = a.targets64 != 0;
     g.copy = w.copy;
-    const int64_t segment = ceil_div64(a.T, 1024);   // at most 1024 blocks count the targets
+    const int64_t segment = ceil_div64(a.T, 304);   // two blocks per SM count the targets
     g.segment = static_cast<int>(segment < 8 ? 8 : segment);
     const unsigned grid = static_cast<unsigned>(ceil_div64(a.T, g.segment));
     return cuda_status(launch_kernel(live_tokens<T>, dim3(grid), dim3(256), 0, stream, 1, g));
@@ -728,16 +721,15 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
     const bool vec = a.k % 8 == 0 && aligned(grad_weight, 16);
 
     Product<Slopes<T>> s;
-    Product<PieceGradIn<T>> gi;
-    Product<PieceGradWeight<T>> gw;
+    Product<PieceGradients<T>> g;
     if (rc == GATED_ACT_OK)
         rc = encode_rows<T>(&s.a, &s.other, w, kHalf);
     if (rc == GATED_ACT_OK)
         rc = encode_map(&s.b, w.weight, kHalf, is_bf16);
     if (rc == GATED_ACT_OK)
-        rc = encode_map(&gi.b, w.weight, kStep, is_bf16);
+        rc = encode_map(&g.b, w.weight, kStep, is_bf16);
     if (rc == GATED_ACT_OK)
-        rc = encode_rows<T>(&gw.b, &gw.other, w, kStep);
+        rc = encode_rows<T>(&g.j.in, &g.j.packed, w, kStep);
     for (int64_t first = 0; first < a.V && rc == GATED_ACT_OK; first += w.piece) {
         const int64_t cols = a.V - first < w.piece ? a.V - first : w.piece;
         const Layout y = {w.y, {cols, w.padded, 1, 1}, {1, w.piece, 0, 0}};
@@ -747,34 +739,34 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
         s.j = {w.t, static_cast<T *>(w.y), static_cast<int>(a.V), static_cast<int>(first),
                static_cast<int>(w.piece)};
         rc = launch_product(s, ceil_div64(a.T, kTile) * s.n_tiles, stream);
-
         if (rc == GATED_ACT_OK)
-            rc = encode_map(&gi.a, y, kHalf, is_bf16);
+            rc = encode_map(&g.a, y, kHalf, is_bf16);
+        if (rc == GATED_ACT_OK)
+            rc = encode_map(&g.j.y, y, kStep, is_bf16);
         if (rc != GATED_ACT_OK)
             return rc;
-        gi.other = gi.a;
-        set_rows(&gi, w, a);
-        gi.batches = kShares;
-        gi.n_tiles = static_cast<int>(w.n_tiles);
-        gi.steps = static_cast<int>(ceil_div64(cols, kStep));
-        gi.j = {w.sums, k, static_cast<int>(first), static_cast<int>(w.piece_steps), w.pairs, first == 0};
-        rc = launch_product(gi, kShares * w.m_tiles * w.n_tiles, stream);
-
-        if (rc == GATED_ACT_OK)
-            rc = encode_map(&gw.a, y, kStep, is_bf16);
-        if (rc != GATED_ACT_OK)
-            return rc;
-        set_rows(&gw, w, a);
-        gw.rows = static_cast<int>(cols);
-        gw.n_tiles = gi.n_tiles;
-        gw.steps = 0;
-        gw.j = {w.t.power, static_cast<T *>(grad_weight) + first * a.k, k, vec};
-        rc = launch_product(gw, ceil_div64(cols, kTile) * gw.n_tiles, stream);
+        g.other = g.a;
+        set_rows(&g, w, a);
+        g.batches = kShares;
+        g.n_tiles = w.shares.n_tiles;
+        g.steps = static_cast<int>(ceil_div64(cols, kStep));
+        g.second.batches = 1;
+        g.second.m_tiles = static_cast<int>(ceil_div64(cols, kTile));
+        g.second.n_tiles = g.n_tiles;
+        g.second.rows = static_cast<int>(cols);
+        g.j.sums = w.sums;
+        g.j.power = w.t.power;
+        g.j.grad_weight = static_cast<T *>(grad_weight) + first * a.k;
+        g.j.shares = w.shares;
+        g.j.k = k;
+        g.j.first = static_cast<int>(first);
+        g.j.begin = first == 0;
+        g.j.vec = vec;
+        rc = launch_product(g, (ceil_div64(a.T, kTile) + g.second.m_tiles) * g.n_tiles, stream);
     }
     if (rc != GATED_ACT_OK)
         return rc;
-    const GradInArgs<T> j = {w.sums, w.t, static_cast<T *>(grad_in), k, static_cast<int>(w.n_tiles),
-                             static_cast<int>(w.piece_steps), w.pairs};
+    const GradInArgs<T> j = {w.sums, w.t, static_cast<T *>(grad_in), w.shares, k};
     const int64_t blocks = ceil_div64(a.k, 64) * ceil_div64(a.T, 32);
     return cuda_status(launch_kernel(join_grad_in<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
                                      stream, 1, j));

@@ -60,7 +60,7 @@ __device__ __forceinline__ uint32_t encode32(uint32_t (&w)[16], const float (&v)
 
 template <class Act, class T, int N, bool KEEP> struct Forward {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = false;
+    static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
     static constexpr int kN = N, kRows = kTile;
     static constexpr Live kLive = Live::Rows;
     struct Args {
@@ -71,7 +71,7 @@ template <class Act, class T, int N, bool KEEP> struct Forward {
         bool vec;
     };
     using G = Product<Forward>;
-    __device__ static int batch_of(int b) { return b; }
+    __device__ static int batch_of(int b, bool) { return b; }
     __device__ static int batches(const G &g) { return g.batches; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
@@ -125,14 +125,14 @@ template <class Act, class T, int N, bool KEEP> struct Forward {
 // which they hand over through shared memory.
 template <class Act, class T, int N> struct Swapped {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = false;
+    static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
     static constexpr int kN = N, kRows = kHalf;
     static constexpr Live kLive = Live::Columns;
     struct Args {
         T *out;
     };
     using G = Product<Swapped>;
-    __device__ static int batch_of(int b) { return b; }
+    __device__ static int batch_of(int b, bool) { return b; }
     __device__ static int batches(const G &g) { return g.batches; }
     __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
@@ -183,61 +183,44 @@ template <class Act, class T, int N> struct Swapped {
 };
 
 // grad_in: A = (dg, du) along the sum over 2d, B = the weight across it.
-template <class T, int N> struct GradIn {
+// Second, grad_weight: A = (dg, du) across the sum over the rows, B = in across it; batch 2e + half.
+// Past the live rows dg and du are zeros up to a whole step; the last rows of `in` come from
+// a copy with zeros there, as what lies past the live rows may be anything.
+template <class T, int N> struct Gradients {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = true;
+    static constexpr bool kAAcross = false, kBAcross = true, kSecond = true;
     static constexpr int kN = N, kRows = kTile;
     static constexpr Live kLive = Live::Rows;
     struct Args {
-        T *out;
-        int k, half_steps;   // ring steps of one half of the sum
-        bool vec;
+        CUtensorMap rows, in, tail;   // of the second product
+        T *grad_in, *grad_weight;
+        int k, half_steps;            // ring steps of one half of the first sum
+        bool vec_in, vec_weight;
     };
-    using G = Product<GradIn>;
-    __device__ static int batch_of(int b) { return b; }
+    using G = Product<Gradients>;
+    __device__ static int batch_of(int b, bool second) { return second ? b >> 1 : b; }
     __device__ static int batches(const G &g) { return g.batches; }
-    __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
-                                uint32_t b, uint32_t bar) {
-        const int half = step >= g.j.half_steps, x = (step - half * g.j.half_steps) * kStep;
-        load_along(a, &g.a, bar, x, t.m0 + static_cast<int>(rank) * kHalf, half, t.b);
-        load_across<N / 2>(b, &g.b, bar, x, t.n0 * N + static_cast<int>(rank) * (N / 2), half, t.b);
-    }
     __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
-        const int k = g.j.k, r = t.m0 + row, col = t.n0 * N;
-        T *mine = r < t.rows ? g.j.out + (int64_t(t.b) * g.capacity + r) * k + col : nullptr;
-        store_tile<N>(sums, stage, mine, k - col, g.j.vec, 1.f, false);
-    }
-};
-
-// grad_weight: A = (dg, du) across the sum over the rows, B = in across it; batch 2e + half.
-// Past the live rows dg and du are zeros up to a whole step; the last rows of `in` come from
-// a copy with zeros there, as what lies past the live rows may be anything.
-template <class T, int N> struct GradWeight {
-    using Elem = T;
-    static constexpr bool kAAcross = true, kBAcross = true;
-    static constexpr int kN = N, kRows = kTile;
-    static constexpr Live kLive = Live::Sum;
-    struct Args {
-        T *out;
-        int k;
-        bool vec;
-    };
-    using G = Product<GradWeight>;
-    __device__ static int batch_of(int b) { return b >> 1; }
-    __device__ static int batches(const G &g) { return g.batches; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
+        const int row = t.m0 + static_cast<int>(rank) * kHalf, col = t.n0 * N + static_cast<int>(rank) * (N / 2);
+        if (!t.second) {
+            const int half = step >= g.j.half_steps, x = (step - half * g.j.half_steps) * kStep;
+            load_along(a, &g.a, bar, x, row, half, t.b);
+            load_across<N / 2>(b, &g.b, bar, x, col, half, t.b);
+            return;
+        }
         const int x = step * kStep, e = t.b >> 1;
-        load_across(a, &g.a, bar, x, t.m0 + static_cast<int>(rank) * kHalf, t.b & 1, e);
+        load_across(a, &g.j.rows, bar, x, row, t.b & 1, e);
         const bool tail = x + kStep > t.live && t.live < g.capacity;
-        load_across<N / 2>(b, tail ? &g.other : &g.b, bar, tail ? 0 : x,
-                           t.n0 * N + static_cast<int>(rank) * (N / 2), 0, e);
+        load_across<N / 2>(b, tail ? &g.j.tail : &g.j.in, bar, tail ? 0 : x, col, 0, e);
     }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
         const int k = g.j.k, r = t.m0 + row, col = t.n0 * N;
-        T *mine = r < t.rows ? g.j.out + (int64_t(t.b) * g.rows + r) * k + col : nullptr;
-        store_tile<N>(sums, stage, mine, k - col, g.j.vec, 1.f, t.steps == 0);
+        T *to = t.second ? g.j.grad_weight + (int64_t(t.b) * g.second.rows + r) * k + col
+                         : g.j.grad_in + (int64_t(t.b) * g.capacity + r) * k + col;
+        store_tile<N>(sums, stage, r < t.rows ? to : nullptr, k - col,
+                      t.second ? g.j.vec_weight : g.j.vec_in, 1.f, t.steps == 0);
     }
 };
 
@@ -377,7 +360,7 @@ int check_sizes(const gated_act_linear &a) {
                    static_cast<double>(ceil_div64(cols, width)) <
                static_cast<double>(most);
     };
-    if (!tiles(a.T, a.d, 64) || !tiles(a.T, a.k, 128) || !tiles(2 * a.d, a.k, 128) ||
+    if (!tiles(a.T, a.d, 64) || !tiles(a.T + 2 * a.d + kTile, a.k, 128) ||
         static_cast<double>(a.E) * static_cast<double>(a.T + kStep) *
                 static_cast<double>(2 * a.d + a.k) > 1e17)
         return GATED_ACT_ERR_TOO_LARGE;
@@ -551,13 +534,19 @@ struct BackwardParts {
 };
 
 template <class T, int N>
-int run_grad_in(void *grad_in, const gated_act_linear &a, const Layout &rows, const Layout &weight,
-                cudaStream_t stream) {
+int run_gradients(void *grad_in, void *grad_weight, const gated_act_linear &a, const Layout &rows,
+                  const Operands &o, const Layout &tail, cudaStream_t stream) {
     constexpr bool is_bf16 = std::is_same_v<T, bf16>;
-    Product<GradIn<T, N>> g;
+    Product<Gradients<T, N>> g;
     int rc = encode_map(&g.a, rows, kHalf, is_bf16);
     if (rc == GATED_ACT_OK)
-        rc = encode_map(&g.b, weight, kStep, is_bf16);
+        rc = encode_map(&g.b, o.weight, kStep, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&g.j.rows, rows, kStep, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&g.j.in, o.in, kStep, is_bf16);
+    if (rc == GATED_ACT_OK)
+        rc = encode_map(&g.j.tail, a.n_rows ? tail : o.in, kStep, is_bf16);
     if (rc != GATED_ACT_OK)
         return rc;
     g.other = g.a;
@@ -565,33 +554,41 @@ int run_grad_in(void *grad_in, const gated_act_linear &a, const Layout &rows, co
     g.batches = static_cast<int>(a.E);
     g.capacity = g.rows = static_cast<int>(a.T);
     g.n_tiles = static_cast<int>(ceil_div64(a.k, N));
-    const int half_steps = static_cast<int>(ceil_div64(a.d, kStep));
-    g.steps = 2 * half_steps;
-    g.j = {static_cast<T *>(grad_in), static_cast<int>(a.k), half_steps,
-           a.k % 8 == 0 && aligned(grad_in, 16)};
-    return launch_product(g, a.E * ceil_div64(a.T, kTile) * g.n_tiles, stream);
+    g.j.half_steps = static_cast<int>(ceil_div64(a.d, kStep));
+    g.steps = 2 * g.j.half_steps;
+    g.second.batches = static_cast<int>(2 * a.E);
+    g.second.m_tiles = static_cast<int>(ceil_div64(a.d, kTile));
+    g.second.n_tiles = g.n_tiles;
+    g.second.rows = static_cast<int>(a.d);
+    g.j.grad_in = static_cast<T *>(grad_in);
+    g.j.grad_weight = static_cast<T *>(grad_weight);
+    g.j.k = static_cast<int>(a.k);
+    g.j.vec_in = a.k % 8 == 0 && aligned(grad_in, 16);
+    g.j.vec_weight = a.k % 8 == 0 && aligned(grad_weight, 16);
+    return launch_product(g, a.E * (ceil_div64(a.T, kTile) + 2 * g.second.m_tiles) * g.n_tiles, stream);
 }
 
-template <class T, int N>
-int run_grad_weight(void *grad_weight, const gated_act_linear &a, const Layout &rows, const Layout &in,
-                    const Layout &tail, cudaStream_t stream) {
-    constexpr bool is_bf16 = std::is_same_v<T, bf16>;
-    Product<GradWeight<T, N>> g;
-    int rc = encode_map(&g.a, rows, kStep, is_bf16);
-    if (rc == GATED_ACT_OK)
-        rc = encode_map(&g.b, in, kStep, is_bf16);
-    if (rc == GATED_ACT_OK)
-        rc = encode_map(&g.other, a.n_rows ? tail : in, kStep, is_bf16);
-    if (rc != GATED_ACT_OK)
-        return rc;
-    g.live = a.n_rows;
-    g.batches = static_cast<int>(2 * a.E);
-    g.capacity = static_cast<int>(a.T);
-    g.rows = static_cast<int>(a.d);
-    g.n_tiles = static_cast<int>(ceil_div64(a.k, N));
-    g.steps = 0;
-    g.j = {static_cast<T *>(grad_weight), static_cast<int>(a.k), a.k % 8 == 0 && aligned(grad_weight, 16)};
-    return launch_product(g, 2 * a.E * ceil_div64(a.d, kTile) * g.n_tiles, stream);
+// Columns of a tile for both products: those for which the busiest pair of SMs has fewer ring steps,
+// a step of 128 columns being 0.6 of one of 256.  Tiles go round the pairs in order, the first product's
+// in front.
+int gradient_columns(int64_t in_tiles, int64_t in_steps, int64_t w_tiles, int64_t w_steps, int64_t k) {
+    const int64_t pairs = device_sm_count() / 2;
+    const auto busiest = [&](int64_t n) {
+        const int64_t in = in_tiles * ceil_div64(k, n), w = w_tiles * ceil_div64(k, n);
+        const int64_t left = in % pairs, turns = in / pairs;   // pairs with one first tile more
+        // second tiles of a pair that has a first tile more, and of one that has not
+        const int64_t all = in + w;
+        int64_t most = 0;
+        for (const int64_t p : {int64_t(0), left ? left - 1 : 0, left, pairs - 1}) {
+            if (p >= pairs)
+                continue;
+            const int64_t mine = turns + (p < left), total = all / pairs + (p < all % pairs);
+            const int64_t steps = mine * in_steps + (total - mine) * w_steps;
+            most = steps > most ? steps : most;
+        }
+        return most;
+    };
+    return 0.6 * static_cast<double>(busiest(128)) < static_cast<double>(busiest(256)) ? 128 : 256;
 }
 
 template <class Act, class T>
@@ -638,14 +635,13 @@ int run_backward(void *grad_in, void *grad_weight, const void *grad_out, int64_t
                          {1, w.dp, w.padded * w.dp, 2 * w.padded * w.dp}};
     const Layout tail = {w.tail, {a.k, kStep, 1, a.E}, {1, w.kp, 0, kStep * w.kp}};
 
-    const int64_t m_tiles = a.E * ceil_div64(a.T, kTile), w_tiles = 2 * a.E * ceil_div64(a.d, kTile);
-    rc = tile_columns(m_tiles, a.k) == 256 ? run_grad_in<T, 256>(grad_in, a, rows, w.o.weight, stream)
-                                           : run_grad_in<T, 128>(grad_in, a, rows, w.o.weight, stream);
-    if (rc != GATED_ACT_OK)
-        return rc;
-    return tile_columns(w_tiles, a.k) == 256
-               ? run_grad_weight<T, 256>(grad_weight, a, rows, w.o.in, tail, stream)
-               : run_grad_weight<T, 128>(grad_weight, a, rows, w.o.in, tail, stream);
+    // Both products in one launch: its turns are those of the shorter tiles, unless the longer, of
+    // which there are few where the rows are few, last longer than all of them.
+    const int64_t in_tiles = a.E * ceil_div64(a.T, kTile), in_steps = 2 * ceil_div64(a.d, kStep),
+                  w_tiles = 2 * a.E * ceil_div64(a.d, kTile), w_steps = ceil_div64(a.T, kStep);
+    return gradient_columns(in_tiles, in_steps, w_tiles, w_steps, a.k) == 256
+               ? run_gradients<T, 256>(grad_in, grad_weight, a, rows, w.o, tail, stream)
+               : run_gradients<T, 128>(grad_in, grad_weight, a, rows, w.o, tail, stream);
 }
 
 template <class Act>

@@ -107,16 +107,18 @@ __global__ void __launch_bounds__(256) pack_rows(Layout to, Layout from) {
     const int64_t x = (int64_t(blockIdx.x) * 32 + threadIdx.x) * 8;
     if (x >= to.size[0])
         return;
-    const int64_t rows = to.size[1] * to.size[2] * to.size[3];
+    const int64_t z = blockIdx.z % to.size[2], w = blockIdx.z / to.size[2];
+    const uint16_t *plane = static_cast<const uint16_t *>(from.data) + z * from.stride[2] +
+                            w * from.stride[3] + x;
+    uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(to.data)) +
+                    blockIdx.z * to.size[1] * to.stride[1] + x;
     const uintptr_t first = reinterpret_cast<uintptr_t>(from.data);
     const uintptr_t last = first + 2 * static_cast<uintptr_t>(
         (from.size[1] - 1) * from.stride[1] + (from.size[2] - 1) * from.stride[2] +
         (from.size[3] - 1) * from.stride[3] + from.size[0]);
 #pragma unroll 2
-    for (int64_t r = int64_t(blockIdx.y) * 8 + threadIdx.y; r < rows; r += int64_t(gridDim.y) * 8) {
-        const int64_t y = r % to.size[1], zw = r / to.size[1], z = zw % to.size[2], w = zw / to.size[2];
-        const uint16_t *p = static_cast<const uint16_t *>(from.data) + y * from.stride[1] +
-                            z * from.stride[2] + w * from.stride[3] + x;
+    for (int64_t r = int64_t(blockIdx.y) * 8 + threadIdx.y; r < to.size[1]; r += int64_t(gridDim.y) * 8) {
+        const uint16_t *p = plane + r * from.stride[1];
         const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
         uint4 v;
         if (x + 8 <= to.size[0] && at >= first && at + 32 <= last) {
@@ -128,16 +130,16 @@ __global__ void __launch_bounds__(256) pack_rows(Layout to, Layout from) {
                 e[i] = x + i < to.size[0] ? ld_stream_u16(p + i) : 0;
             v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
         }
-        st_vec(static_cast<uint16_t *>(const_cast<void *>(to.data)) + r * to.stride[1] + x, v);
+        st_vec(out + r * to.stride[1], v);
     }
 }
 
 int launch_pack(const Layout &to, const Layout &from, cudaStream_t stream) {
-    const int64_t rows = to.size[1] * to.size[2] * to.size[3], blocks = ceil_div64(rows, 8);
-    if (rows == 0)
+    const int64_t planes = to.size[2] * to.size[3], blocks = ceil_div64(to.size[1], 16);
+    if (to.size[1] * planes == 0)
         return GATED_ACT_OK;
     const dim3 grid(static_cast<unsigned>(ceil_div64(to.size[0], 256)),
-                    static_cast<unsigned>(blocks < 16384 ? blocks : 16384));
+                    static_cast<unsigned>(blocks < 32768 ? blocks : 32768), static_cast<unsigned>(planes));
     return cuda_status(launch_kernel(pack_rows, grid, dim3(32, 8), 0, stream, 1, to, from));
 }
 

@@ -183,6 +183,12 @@ __device__ __forceinline__ void sums_load_wait() {
 // live count of the batch (not read again for each step: that stalled the copies), batches.
 struct Tile {
     int b, m0, n0, rows, steps, live, batches;
+    bool second;   // of the job's second product
+};
+
+// A second product of a job: its first operand's rows lie across the sum, over the live counts.
+struct Second {
+    int batches = 0, m_tiles = 0, n_tiles = 0, rows = 0;
 };
 
 // A job J describes a product and what happens to it:
@@ -192,7 +198,9 @@ struct Tile {
 //   J::kRows                     rows that a tile counts for
 //   J::Args                      what its functions read
 //   J::kLive                     what the live counts bound
-//   J::batch_of(b)               index of the live count of a batch
+//   J::kSecond                   whether there is a second product (Second), whose tiles follow the
+//                                first's: in one launch the SM pairs share both out more evenly
+//   J::batch_of(b, second)       index of the live count of a batch
 //   J::batches(g)                how many there are, of at most g.batches
 //   J::steps_of(g, tile)         ring steps of a tile, where live counts do not bound them
 //   J::load(g, tile, step, rank, a, b, bar)   issues the step's copies of one CTA
@@ -205,10 +213,11 @@ template <class J> struct Product {
     CUtensorMap a, b, other;
     const int32_t *live;   // null: `capacity` everywhere
     int batches, capacity, rows, n_tiles, steps;
+    Second second;
     typename J::Args j;
 
     __device__ int live_of(int b) const {
-        return live ? min(max(live[J::batch_of(b)], 0), capacity) : capacity;
+        return live ? min(max(live[b], 0), capacity) : capacity;
     }
 };
 
@@ -278,26 +287,44 @@ template <class J> struct Walk {
     __device__ Walk(const Product<J> &g_, const ProductShared &s_)
         : g(g_), s(s_), at(blockIdx.x >> 1), step(gridDim.x >> 1), batches(J::batches(g_)),
           total(s_.first[batches]) {}
-    __device__ bool next(Tile *t) {
-        if (at >= total * g.n_tiles)
-            return false;
-        while (s.first[b + 1] * g.n_tiles <= at)
-            ++b;
-        const int r = at - s.first[b] * g.n_tiles, tall = s.first[b + 1] - s.first[b];
-        const int group = r / (kTallest * g.n_tiles), top = group * kTallest;
-        const int high = min(kTallest, tall - top), rest = r - top * g.n_tiles;
-        t->b = b;
-        t->batches = batches;
+    // The r-th tile of a batch `tall` tiles high.
+    __device__ void place(Tile *t, int r, int tall, int n_tiles) const {
+        const int group = r / (kTallest * n_tiles), top = group * kTallest;
+        const int high = min(kTallest, tall - top), rest = r - top * n_tiles;
         t->m0 = (top + rest % high) * J::kRows;
         t->n0 = rest / high;
-        t->live = g.live_of(b);
-        t->rows = J::kLive == Live::Rows ? t->live : g.rows;
-        if constexpr (J::kLive == Live::Sum)
+    }
+    __device__ bool next(Tile *t) {
+        t->batches = batches;
+        t->second = false;
+        if (at < total * g.n_tiles) {
+            while (s.first[b + 1] * g.n_tiles <= at)
+                ++b;
+            t->b = b;
+            place(t, at - s.first[b] * g.n_tiles, s.first[b + 1] - s.first[b], g.n_tiles);
+            t->live = g.live_of(J::batch_of(b, false));
+            t->rows = J::kLive == Live::Rows ? t->live : g.rows;
+            if constexpr (J::kLive == Live::Sum)
+                t->steps = (t->live + kStep - 1) / kStep;
+            else
+                t->steps = J::steps_of(g, *t);
+            at += step;
+            return true;
+        }
+        if constexpr (J::kSecond) {
+            const int r = at - total * g.n_tiles, each = g.second.m_tiles * g.second.n_tiles;
+            if (r >= g.second.batches * each)
+                return false;
+            t->second = true;
+            t->b = r / each;
+            place(t, r % each, g.second.m_tiles, g.second.n_tiles);
+            t->live = g.live_of(J::batch_of(t->b, true));
+            t->rows = g.second.rows;
             t->steps = (t->live + kStep - 1) / kStep;
-        else
-            t->steps = J::steps_of(g, *t);
-        at += step;
-        return true;
+            at += step;
+            return true;
+        }
+        return false;
     }
 };
 
@@ -345,8 +372,8 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
             const int b = b0 + lane;
             int n = 0;
             if (b < batches)
-                n = ((J::kLive == Live::Rows ? g.live_of(b)
-                      : J::kLive == Live::Columns && g.live_of(b) == 0 ? 0 : g.rows) +
+                n = ((J::kLive == Live::Rows ? g.live_of(J::batch_of(b, false))
+                      : J::kLive == Live::Columns && g.live_of(J::batch_of(b, false)) == 0 ? 0 : g.rows) +
                      J::kRows - 1) / J::kRows;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -397,8 +424,8 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
             }
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {
-        constexpr uint32_t desc =
-            product_descriptor<typename J::Elem, J::kN, J::kAAcross, J::kBAcross>();
+        constexpr uint32_t first = product_descriptor<typename J::Elem, J::kN, J::kAAcross, J::kBAcross>();
+        constexpr uint32_t second = product_descriptor<typename J::Elem, J::kN, true, J::kBAcross>();
         uint32_t slot = 0, phase = 0, turn = 0;
         bool ok = true;
         while (ok && walk.next(&t)) {
@@ -411,12 +438,14 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
                     break;
                 sums_fence_after();
                 const uint32_t from = base + slot * SLOT;
-                const uint64_t a = slot_descriptor<J::kAAcross>(from),
+                const bool across = J::kAAcross || (J::kSecond && t.second);
+                const uint64_t a = across ? slot_descriptor<true>(from) : slot_descriptor<false>(from),
+                               turn16 = across ? kDescriptorStep<true> : kDescriptorStep<false>,
                                b = slot_descriptor<J::kBAcross>(from + kRowBytes);
 #pragma unroll
                 for (int i = 0; i < kStep / 16; ++i)
-                    product_step(to, a + i * kDescriptorStep<J::kAAcross>,
-                                 b + i * kDescriptorStep<J::kBAcross>, desc, k > 0 || i > 0);
+                    product_step(to, a + i * turn16,
+                                 b + i * kDescriptorStep<J::kBAcross>, across ? second : first, k > 0 || i > 0);
                 product_commit(empty + 8 * slot);
                 if (++slot == SLOTS) {
                     slot = 0;
