@@ -281,12 +281,13 @@ template <class T> struct Slopes {
     }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
         const int r = t.m0 + row;
-        const bool mine = r < t.rows, write = r < (t.rows + kStep - 1) / kStep * kStep;
+        const bool mine = r < t.rows;
         const int first = g.j.first + t.n0 * kTile;
         const int goal = mine ? g.j.t.goal[r] - first : -1;
         const float shift = mine ? g.j.t.shift[r] : 0.f;
         const float weight = mine ? g.j.t.weight[r] * kLift<T> : 0.f;
-        T *y = write ? g.j.y + int64_t(r) * g.j.piece + t.n0 * kTile : nullptr;
+        const int top = t.m0 + (row & ~31), whole = (t.rows + kStep - 1) / kStep * kStep;
+        T *y = g.j.y + int64_t(top) * g.j.piece + t.n0 * kTile;   // the warp's first row
         for (int c0 = 0; c0 < kTile && t.n0 * kTile + c0 < g.j.piece; c0 += 64) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -312,7 +313,7 @@ template <class T> struct Slopes {
                 pack32<T>(w, v);
                 stage.put(half, w);
             }
-            stage.flush(y ? y + c0 : nullptr, 64, true);
+            stage.flush(y + c0, g.j.piece, whole - top, 64, true);
         }
     }
 };
@@ -377,7 +378,8 @@ template <class T> struct PieceGradients {
         const int k = g.j.k, r = t.m0 + row, col = t.n0 * kTile;
         const bool mine = r < t.rows;
         if (t.second) {
-            store_tile<kTile>(sums, stage, mine ? g.j.grad_weight + int64_t(r) * k + col : nullptr, k - col,
+            const int top = t.m0 + (row & ~31);
+            store_tile<kTile>(sums, stage, g.j.grad_weight + int64_t(top) * k + col, k, t.rows - top, k - col,
                               g.j.vec, *g.j.power * (1.f / kLift<T>), t.steps == 0);
             return;
         }

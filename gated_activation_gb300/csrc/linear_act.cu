@@ -83,7 +83,8 @@ template <class Act, class T, int N, bool KEEP> struct Forward {
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
         const int d = g.j.d, r = t.m0 + row, blocks = (d + kBlock - 1) / kBlock;
         const bool mine = r < t.rows;
-        const int64_t at = int64_t(t.b) * g.capacity + r;
+        const int lane = threadIdx.x & 31, rows = t.rows - (r - lane);   // of the warp
+        const int64_t at = int64_t(t.b) * g.capacity + r, top = at - lane;
         for (int c = 0; c < N / 2 && t.n0 * (N / 2) + c < d; c += 64) {
             const int col = t.n0 * (N / 2) + c, n = d - col;
 #pragma unroll
@@ -98,7 +99,7 @@ template <class Act, class T, int N, bool KEEP> struct Forward {
                     w[i] = pack2<T>(act_mul<Act>({gate[2 * i], gate[2 * i + 1]}, {up[2 * i], up[2 * i + 1]}));
                 stage.put(half, w);
             }
-            stage.flush(mine ? g.j.out + at * d + col : nullptr, n, g.j.vec);
+            stage.flush(g.j.out + top * d + col, d, rows, n, g.j.vec);
             if (KEEP)
                 for (int part = 0; part < 2; ++part) {   // gate, up
                     uint8_t *scale = g.j.scales + (at * 2 + part) * blocks + col / kBlock;
@@ -113,7 +114,7 @@ template <class Act, class T, int N, bool KEEP> struct Forward {
                             scale[half] = static_cast<uint8_t>(e);
                         stage.put(half, w);
                     }
-                    stage.flush(mine ? g.j.codes + (at * 2 + part) * d + col : nullptr, n, g.j.vec);
+                    stage.flush(g.j.codes + (top * 2 + part) * d + col, 2 * int64_t(d), rows, n, g.j.vec);
                 }
         }
     }
@@ -216,11 +217,11 @@ template <class T, int N> struct Gradients {
         load_across<N / 2>(b, tail ? &g.j.tail : &g.j.in, bar, tail ? 0 : x, col, 0, e);
     }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
-        const int k = g.j.k, r = t.m0 + row, col = t.n0 * N;
-        T *to = t.second ? g.j.grad_weight + (int64_t(t.b) * g.second.rows + r) * k + col
-                         : g.j.grad_in + (int64_t(t.b) * g.capacity + r) * k + col;
-        store_tile<N>(sums, stage, r < t.rows ? to : nullptr, k - col,
-                      t.second ? g.j.vec_weight : g.j.vec_in, 1.f, t.steps == 0);
+        const int k = g.j.k, top = t.m0 + (row & ~31), col = t.n0 * N;   // the warp's first row
+        T *to = t.second ? g.j.grad_weight + (int64_t(t.b) * g.second.rows + top) * k + col
+                         : g.j.grad_in + (int64_t(t.b) * g.capacity + top) * k + col;
+        store_tile<N>(sums, stage, to, k, t.rows - top, k - col, t.second ? g.j.vec_weight : g.j.vec_in,
+                      1.f, t.steps == 0);
     }
 };
 

@@ -236,31 +236,40 @@ struct Stage {
         for (int i = 0; i < 4; ++i)
             to[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
-    // Writes n columns (of 64) of every row to its address, the lane's own being `mine` (null:
-    // not written).  `vec`: addresses and n are multiples of 16 bytes; a warp then writes four rows'
-    // 128 bytes at a time, else 64 bytes of one row.
-    __device__ __forceinline__ void flush(void *mine, int n, bool vec) const {
+    // Writes n columns (of 64) of the first `rows` of the 32 rows to `to`, `stride` elements apart.
+    // `vec`: addresses, strides and n are multiples of 16 bytes; a warp then writes four rows' 128 bytes
+    // at a time.  Else 64 bytes of a row at a time, element by element.
+    __device__ __forceinline__ void flush(void *to, int64_t stride, int rows, int n, bool vec) const {
         const int lane = threadIdx.x & 31;
+        uint16_t *out = static_cast<uint16_t *>(to);
         __syncwarp();
         if (vec) {
+            const int c = (lane & 7) * 8;
+            out += (lane >> 3) * stride + c;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = 4 * i + (lane >> 3), c = (lane & 7) * 8;
-                uint16_t *to = reinterpret_cast<uint16_t *>(
-                    __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), row));
-                if (to && c < n)
-                    st_vec_out(to + c, *reinterpret_cast<const uint4 *>(p + row * kStageRow + 2 * c));
+            for (int i = 0; i < 8; ++i, out += 4 * stride) {
+                const int row = 4 * i + (lane >> 3);
+                if (row < rows && c < n)
+                    st_vec_out(out, *reinterpret_cast<const uint4 *>(p + row * kStageRow + 2 * c));
             }
         } else {
-#pragma unroll 8
-            for (int row = 0; row < 32; ++row) {
-                uint16_t *to = reinterpret_cast<uint16_t *>(
-                    __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), row));
-                const uint16_t *from = reinterpret_cast<const uint16_t *>(p + row * kStageRow);
-                if (to && lane < n)
-                    to[lane] = from[lane];
-                if (to && lane + 32 < n)
-                    to[lane + 32] = from[lane + 32];
+            // sixteen reads on their way before the first write, which they cannot pass
+            out += lane;
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += 8) {
+                uint16_t v[8][2];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        v[i][half] = *reinterpret_cast<const uint16_t *>(p + (r0 + i) * kStageRow + 2 * lane + 64 * half);
+#pragma unroll
+                for (int i = 0; i < 8; ++i, out += stride) {
+                    if (r0 + i < rows && lane < n)
+                        out[0] = v[i][0];
+                    if (r0 + i < rows && lane + 32 < n)
+                        out[32] = v[i][1];
+                }
             }
         }
         __syncwarp();
@@ -283,7 +292,7 @@ constexpr int kTallest = 8;   // tile rows that are walked together, so that the
 template <class J> struct Walk {
     const Product<J> &g;
     const ProductShared &s;
-    int at, step, b = 0, batches, total;
+    int at, step, b = 0, batches, total, turn = 0;
     __device__ Walk(const Product<J> &g_, const ProductShared &s_)
         : g(g_), s(s_), at(blockIdx.x >> 1), step(gridDim.x >> 1), batches(J::batches(g_)),
           total(s_.first[batches]) {}
@@ -312,7 +321,26 @@ template <class J> struct Walk {
             return true;
         }
         if constexpr (J::kSecond) {
-            const int r = at - total * g.n_tiles, each = g.second.m_tiles * g.second.n_tiles;
+            // Where some pairs have a first tile more than others, the others take second tiles for it
+            // before all go on in turns.
+            const int left = total * g.n_tiles % step, mine = blockIdx.x >> 1;
+            const int others = left ? step - left : 0, each = g.second.m_tiles * g.second.n_tiles;
+            const int live = J::kLive == Live::Rows ? total * J::kRows / max(batches, 1) : 0;
+            int ahead = 0;   // second tiles for a first one
+            if (others) {
+                Tile f = *t;
+                f.b = 0;
+                f.live = live;
+                ahead = J::steps_of(g, f) / max((min(live, g.capacity) + kStep - 1) / kStep, 1);
+            }
+            const bool other = mine >= left && others;
+            int r;
+            if (other && turn < ahead)
+                r = mine - left + turn * others;
+            else
+                r = ahead * others + (mine >= left ? mine - left : mine + step - left) +
+                    (turn - (other ? ahead : 0)) * step;
+            ++turn;
             if (r >= g.second.batches * each)
                 return false;
             t->second = true;
@@ -321,7 +349,6 @@ template <class J> struct Walk {
             t->live = g.live_of(J::batch_of(t->b, true));
             t->rows = g.second.rows;
             t->steps = (t->live + kStep - 1) / kStep;
-            at += step;
             return true;
         }
         return false;
@@ -528,10 +555,11 @@ template <class T> __device__ __forceinline__ void pack32(uint32_t (&w)[16], con
 }
 
 // The epilogue of a plain product: every column of the tile below `columns`, times `scale`, rounded
-// to T, into the lane's row at `mine` (null: none).  A sum without terms is 0 whatever tensor memory holds.
+// to T, into the warp's first `rows` rows at `to`, `stride` apart.  A sum without terms is 0 whatever
+// tensor memory holds.
 template <int N, class T>
-__device__ __forceinline__ void store_tile(uint32_t sums, const Stage &stage, T *mine, int columns,
-                                           bool vec, float scale, bool zero) {
+__device__ __forceinline__ void store_tile(uint32_t sums, const Stage &stage, T *to, int64_t stride, int rows,
+                                           int columns, bool vec, float scale, bool zero) {
     for (int c = 0; c < N && c < columns; c += 64) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -545,7 +573,7 @@ __device__ __forceinline__ void store_tile(uint32_t sums, const Stage &stage, T 
             pack32<T>(w, v);
             stage.put(half, w);
         }
-        stage.flush(mine ? mine + c : nullptr, columns - c, vec);
+        stage.flush(to + c, stride, rows, columns - c, vec);
     }
 }
 
