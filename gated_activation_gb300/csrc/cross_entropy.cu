@@ -209,7 +209,7 @@ template <class T> struct Statistics {
     static constexpr Live kLive = Live::Rows;
     struct Args {
         const int32_t *goal;
-        float2 *part;        // [capacity, tiles]: maximum, sum
+        float2 *part;        // [capacity, 2 tiles]: maximum, sum of each warp's columns
         int V;
     };
     using G = Product<Statistics>;
@@ -220,12 +220,12 @@ template <class T> struct Statistics {
                                 uint32_t b, uint32_t bar) {
         load_logits(g, t, 0, step, rank, a, b, bar);
     }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &) {
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
         const int r = t.m0 + row;
         const bool mine = r < t.rows;
         const int first = t.n0 * kTile, goal = mine ? g.j.goal[r] - first : -1;
         float top = -INFINITY, sum = 0.f;
-        for (int c = 0; c < kTile && first + c < g.j.V; c += 32) {
+        for (int c = 32 * stage.part; c < kTile && first + c < g.j.V; c += 64) {
             float v[32];
             sums_load32(sums + c, v);
             sums_load_wait();
@@ -253,7 +253,7 @@ template <class T> struct Statistics {
             top = now;
         }
         if (mine)
-            g.j.part[int64_t(r) * g.n_tiles + t.n0] = make_float2(top, sum);
+            g.j.part[int64_t(r) * 2 * g.n_tiles + 2 * t.n0 + stage.part] = make_float2(top, sum);
     }
 };
 
@@ -288,32 +288,28 @@ template <class T> struct Slopes {
         const float weight = mine ? g.j.t.weight[r] * kLift<T> : 0.f;
         const int top = t.m0 + (row & ~31), whole = (t.rows + kStep - 1) / kStep * kStep;
         T *y = g.j.y + int64_t(top) * g.j.piece + t.n0 * kTile;   // the warp's first row
-        for (int c0 = 0; c0 < kTile && t.n0 * kTile + c0 < g.j.piece; c0 += 64) {
+        for (int c = 32 * stage.part; c < kTile && t.n0 * kTile + c < g.j.piece; c += 64) {
+            const int n = mine ? g.j.V - first - c : 0;
+            float v[32];
+            uint32_t w[16];
+            sums_load32(sums + c, v);
+            sums_load_wait();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int c = c0 + 32 * half, n = mine ? g.j.V - first - c : 0;
-                float v[32];
-                uint32_t w[16];
-                sums_load32(sums + c, v);
-                sums_load_wait();
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float2 x = fma2({v[i], v[i + 1]}, both(kLog2e), both(-shift));
-                    v[i] = exp2_fast(x.x);
-                    v[i + 1] = exp2_fast(x.y);
-                }
-                if (goal >= c && goal < c + 32) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] -= goal - c == i ? 1.f : 0.f;
-                }
+            for (int i = 0; i < 32; i += 2) {
+                const float2 x = fma2({v[i], v[i + 1]}, both(kLog2e), both(-shift));
+                v[i] = exp2_fast(x.x);
+                v[i + 1] = exp2_fast(x.y);
+            }
+            if (goal >= c && goal < c + 32) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    v[i] = i < n ? v[i] * weight : 0.f;
-                pack32<T>(w, v);
-                stage.put(half, w);
+                    v[i] -= goal - c == i ? 1.f : 0.f;
             }
-            stage.flush(y + c0, g.j.piece, whole - top, 64, true);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                v[i] = i < n ? v[i] * weight : 0.f;
+            pack32<T>(w, v);
+            stage.flush(w, y + c, g.j.piece, whole - top, 32, true);
         }
     }
 };
@@ -385,8 +381,8 @@ template <class T> struct PieceGradients {
         }
         const int64_t m_tiles = (t.live + kTile - 1) / kTile;
         const int64_t tile = (t.b * m_tiles + t.m0 / kTile) * g.n_tiles + t.n0;
-        float *held = g.j.sums + tile * (kTile * kTile) + row;
-        for (int c = 0; c < kTile && col + c < k; c += 32, held += 32 * kTile) {
+        float *held = g.j.sums + tile * (kTile * kTile) + 32 * stage.part * kTile + row;
+        for (int c = 32 * stage.part; c < kTile && col + c < k; c += 64, held += 64 * kTile) {
             float v[32];
             sums_load32(sums + c, v);
             sums_load_wait();
@@ -615,7 +611,7 @@ struct Parts {
             }
             sums = ws.take<float>(4 * kTile * kTile * most);
         } else {
-            part = ws.take<float2>(8 * ceil_div64(a.V, kTile) * a.T);
+            part = ws.take<float2>(16 * ceil_div64(a.V, kTile) * a.T);
         }
         rc = GATED_ACT_OK;
         if (!tma_addressable(weight)) {
@@ -705,7 +701,7 @@ int run_forward(float *loss, float *lse, const gated_act_vocabulary &a, void *wo
                            a.in_stride,
                            a.weight_stride,
                            static_cast<int>(a.T),
-                           g.n_tiles,
+                           2 * g.n_tiles,
                            static_cast<int>(a.k)};
     return cuda_status(launch_kernel(join_statistics<T>, dim3(static_cast<unsigned>(ceil_div64(a.T, 8))),
                                      dim3(256), 0, stream, 1, j));

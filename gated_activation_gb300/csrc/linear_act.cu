@@ -85,45 +85,37 @@ template <class Act, class T, int N, bool KEEP> struct Forward {
         const bool mine = r < t.rows;
         const int lane = threadIdx.x & 31, rows = t.rows - (r - lane);   // of the warp
         const int64_t at = int64_t(t.b) * g.capacity + r, top = at - lane;
-        for (int c = 0; c < N / 2 && t.n0 * (N / 2) + c < d; c += 64) {
+        for (int c = 32 * stage.part; c < N / 2 && t.n0 * (N / 2) + c < d; c += 64) {
             const int col = t.n0 * (N / 2) + c, n = d - col;
+            float gate[32], up[32];
+            sums_load32(sums + c, gate);
+            sums_load32(sums + N / 2 + c, up);
+            sums_load_wait();
+            uint32_t w[16];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float gate[32], up[32];
-                sums_load32(sums + c + 32 * half, gate);
-                sums_load32(sums + N / 2 + c + 32 * half, up);
-                sums_load_wait();
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    w[i] = pack2<T>(act_mul<Act>({gate[2 * i], gate[2 * i + 1]}, {up[2 * i], up[2 * i + 1]}));
-                stage.put(half, w);
+            for (int i = 0; i < 16; ++i)
+                w[i] = pack2<T>(act_mul<Act>({gate[2 * i], gate[2 * i + 1]}, {up[2 * i], up[2 * i + 1]}));
+            stage.flush(w, g.j.out + top * d + col, d, rows, n, g.j.vec);
+            if (KEEP) {
+                uint8_t *scale = g.j.scales + at * 2 * blocks + col / kBlock;
+                int16_t *codes = g.j.codes + top * 2 * d + col;
+                uint32_t e = encode32(w, gate);
+                if (mine)
+                    scale[0] = static_cast<uint8_t>(e);
+                stage.flush(w, codes, 2 * int64_t(d), rows, n, g.j.vec);
+                e = encode32(w, up);
+                if (mine)
+                    scale[blocks] = static_cast<uint8_t>(e);
+                stage.flush(w, codes + d, 2 * int64_t(d), rows, n, g.j.vec);
             }
-            stage.flush(g.j.out + top * d + col, d, rows, n, g.j.vec);
-            if (KEEP)
-                for (int part = 0; part < 2; ++part) {   // gate, up
-                    uint8_t *scale = g.j.scales + (at * 2 + part) * blocks + col / kBlock;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float v[32];
-                        uint32_t w[16];
-                        sums_load32(sums + part * (N / 2) + c + 32 * half, v);
-                        sums_load_wait();
-                        const uint32_t e = encode32(w, v);
-                        if (mine && col + 32 * half < d)
-                            scale[half] = static_cast<uint8_t>(e);
-                        stage.put(half, w);
-                    }
-                    stage.flush(g.j.codes + (top * 2 + part) * d + col, 2 * int64_t(d), rows, n, g.j.vec);
-                }
         }
     }
 };
 
 // The same product with the roles turned round, for up to N rows that would leave most of a
 // 256-row tile empty: the weight's rows are the tile's (64 of g and the same 64 of u per CTA), the
-// input's its columns.  Warps 0 and 1 of the epilogue hold g, warps 2 and 3 the u of the same columns,
-// which they hand over through shared memory.
+// input's its columns.  Of four epilogue warps two hold g and two the u of the same columns, which
+// they hand over through shared memory.
 template <class Act, class T, int N> struct Swapped {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
@@ -144,13 +136,15 @@ template <class Act, class T, int N> struct Swapped {
         load_along(b, &g.b, bar, step * kStep, static_cast<int>(rank) * (N / 2), 0, t.b);
     }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
-        float *held = reinterpret_cast<float *>(stage.s.stage[0]);   // [32 rows, 64 columns]
-        const uint32_t full = smem_address(&stage.s.swap_full), empty = smem_address(&stage.s.swap_empty);
+        // [32 rows, 64 columns] of each part
+        float *held = reinterpret_cast<float *>(stage.s.stage[4 * stage.part]);
+        const uint32_t full = smem_address(&stage.s.swap_full[stage.part]),
+                       empty = smem_address(&stage.s.swap_empty[stage.part]);
         const int lane = threadIdx.x & 31, at = row & 63;
         const bool up = row & 64;
         const int col = t.m0 + (row >> 7) * 64 + at, d = g.rows;
         T *out = g.j.out + int64_t(t.b) * g.capacity * d + col;
-        for (int c = 0; c < N && c < t.live; c += 32) {
+        for (int c = 32 * stage.part; c < N && c < t.live; c += 64) {
             const uint32_t use = stage.uses++;
             float v[32];
             sums_load32(sums + c, v);

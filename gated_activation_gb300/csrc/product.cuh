@@ -7,8 +7,9 @@
 //              memory slots (TMA, 128-byte swizzle), in both CTAs;
 //   warp 1     of the pair's first CTA issues the products (tcgen05.mma of the two
 //              CTAs together, 256 x 256 x 16), whose sums lie in tensor memory;
-//   warps 4-7  read finished sums back, a row per thread, and run the epilogue while
-//              the next tile is summed into the other half of the tensor memory.
+//   warps 4-11 read finished sums back, a row per thread and every second 32 columns, and
+//              run the epilogue while the next tile is summed into the other half of the
+//              tensor memory.
 // An operand is stored with its rows along the summed dimension (as the activations
 // and weights of a linear layer are in its forward product) or across it (as they are
 // in the products of its gradients); the TMA box and the descriptors differ, no data
@@ -31,6 +32,7 @@ constexpr int kRowBytes = kHalf * kStep * 2;   // of the first operand in a slot
 constexpr int kRingBytes = 6 * 2 * kRowBytes;
 constexpr int kMostSlots = 10;
 constexpr int kMaxBatches = 2048;
+constexpr int kProductThreads = 384;
 
 // A slot of a job with N columns per tile: each CTA brings half of the second operand's rows.
 template <int N> constexpr int kSlotBytes = kRowBytes + N / 2 * kStep * 2;
@@ -62,14 +64,14 @@ __device__ __forceinline__ void barrier_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void barrier_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
 }
 __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -221,34 +223,33 @@ template <class J> struct Product {
     }
 };
 
-// Where a warp turns 64 columns of its 32 rows, a row per thread, into row segments; rows are 144
+// Where a warp turns 32 columns of its 32 rows, a row per thread, into row segments; rows are 80
 // bytes apart, so that neither side has bank conflicts.
-constexpr int kStageRow = 64 * 2 + 16;
+constexpr int kStageRow = 32 * 2 + 16;
 struct ProductShared;
 struct Stage {
     uint8_t *p;
     ProductShared &s;
-    uint32_t &uses;   // of the whole block's stage memory, for swap_full and swap_empty
-    // half (0, 1) of the 64 columns of the lane's row, two elements to a word
-    __device__ __forceinline__ void put(int half, const uint32_t (&w)[16]) const {
-        uint4 *to = reinterpret_cast<uint4 *>(p + (threadIdx.x & 31) * kStageRow + half * 64);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            to[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    }
-    // Writes n columns (of 64) of the first `rows` of the 32 rows to `to`, `stride` elements apart.
-    // `vec`: addresses, strides and n are multiples of 16 bytes; a warp then writes four rows' 128 bytes
-    // at a time.  Else 64 bytes of a row at a time, element by element.
-    __device__ __forceinline__ void flush(void *to, int64_t stride, int rows, int n, bool vec) const {
+    int part;         // which of the tile's 32 columns the warp takes: every second, from this one on
+    uint32_t &uses;   // of the part's hand-over buffer
+    // Writes n columns (of 32), two to a word of the lane's row, of the first `rows` of the 32 rows to
+    // `to`, `stride` elements apart.  `vec`: addresses, strides and n are multiples of 16 bytes; a warp then
+    // writes eight rows' 64 bytes at a time.  Else a row's at a time, element by element.
+    __device__ __forceinline__ void flush(const uint32_t (&w)[16], void *to, int64_t stride, int rows, int n,
+                                          bool vec) const {
         const int lane = threadIdx.x & 31;
         uint16_t *out = static_cast<uint16_t *>(to);
+        uint4 *mine = reinterpret_cast<uint4 *>(p + lane * kStageRow);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mine[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         __syncwarp();
         if (vec) {
-            const int c = (lane & 7) * 8;
-            out += (lane >> 3) * stride + c;
+            const int c = (lane & 3) * 8;
+            out += (lane >> 2) * stride + c;
 #pragma unroll
-            for (int i = 0; i < 8; ++i, out += 4 * stride) {
-                const int row = 4 * i + (lane >> 3);
+            for (int i = 0; i < 4; ++i, out += 8 * stride) {
+                const int row = 8 * i + (lane >> 2);
                 if (row < rows && c < n)
                     st_vec_out(out, *reinterpret_cast<const uint4 *>(p + row * kStageRow + 2 * c));
             }
@@ -256,20 +257,15 @@ struct Stage {
             // sixteen reads on their way before the first write, which they cannot pass
             out += lane;
 #pragma unroll
-            for (int r0 = 0; r0 < 32; r0 += 8) {
-                uint16_t v[8][2];
+            for (int r0 = 0; r0 < 32; r0 += 16) {
+                uint16_t v[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < 16; ++i)
+                    v[i] = *reinterpret_cast<const uint16_t *>(p + (r0 + i) * kStageRow + 2 * lane);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half)
-                        v[i][half] = *reinterpret_cast<const uint16_t *>(p + (r0 + i) * kStageRow + 2 * lane + 64 * half);
-#pragma unroll
-                for (int i = 0; i < 8; ++i, out += stride) {
+                for (int i = 0; i < 16; ++i, out += stride)
                     if (r0 + i < rows && lane < n)
-                        out[0] = v[i][0];
-                    if (r0 + i < rows && lane + 32 < n)
-                        out[32] = v[i][1];
-                }
+                        out[0] = v[i];
             }
         }
         __syncwarp();
@@ -277,8 +273,8 @@ struct Stage {
 };
 
 struct alignas(16) ProductShared {
-    uint8_t stage[4][32 * kStageRow];
-    uint64_t full[kMostSlots], empty[kMostSlots], sums_full[2], sums_empty[2], swap_full, swap_empty;
+    uint8_t stage[8][32 * kStageRow];
+    uint64_t full[kMostSlots], empty[kMostSlots], sums_full[2], sums_empty[2], swap_full[2], swap_empty[2];
     uint32_t sums;             // tensor memory address
     volatile uint32_t gave_up;
     int first[kMaxBatches + 1];   // first tile row of each batch
@@ -356,7 +352,7 @@ template <class J> struct Walk {
 };
 
 template <class J>
-__global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__ Product<J> g) {
+__global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ Product<J> g) {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_address(raw) + 1023u) & ~1023u;   // the swizzle's period
     constexpr int SLOTS = kSlots<J::kN>, SLOT = kSlotBytes<J::kN>;
@@ -374,10 +370,10 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
         }
         for (int i = 0; i < 2; ++i) {
             barrier_init(sums_full + 8 * i, 1);
-            barrier_init(sums_empty + 8 * i, 8);   // four epilogue warps of each CTA
+            barrier_init(sums_empty + 8 * i, 16);   // eight epilogue warps of each CTA
+            barrier_init(smem_address(&s.swap_full[i]), 2);
+            barrier_init(smem_address(&s.swap_empty[i]), 2);
         }
-        barrier_init(smem_address(&s.swap_full), 2);
-        barrier_init(smem_address(&s.swap_empty), 2);
         s.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -493,7 +489,7 @@ __global__ void __launch_bounds__(256, 1) product_kernel(const __grid_constant__
             sums_fence_after();
             J::finish(g, t, static_cast<int>(rank) * kHalf + quarter * 32 + lane,
                       sums + half * kTile + (static_cast<uint32_t>(quarter * 32) << 16),
-                      Stage{s.stage[quarter], s, uses});
+                      Stage{s.stage[warp - 4], s, (warp >> 2) - 1, uses});
             sums_fence_before();
             __syncwarp();
             if (lane == 0)
@@ -560,20 +556,16 @@ template <class T> __device__ __forceinline__ void pack32(uint32_t (&w)[16], con
 template <int N, class T>
 __device__ __forceinline__ void store_tile(uint32_t sums, const Stage &stage, T *to, int64_t stride, int rows,
                                            int columns, bool vec, float scale, bool zero) {
-    for (int c = 0; c < N && c < columns; c += 64) {
+    for (int c = 32 * stage.part; c < N && c < columns; c += 64) {
+        float v[32];
+        uint32_t w[16];
+        sums_load32(sums + c, v);
+        sums_load_wait();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float v[32];
-            uint32_t w[16];
-            sums_load32(sums + c + 32 * half, v);
-            sums_load_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                v[i] = zero ? 0.f : v[i] * scale;
-            pack32<T>(w, v);
-            stage.put(half, w);
-        }
-        stage.flush(to + c, stride, rows, columns - c, vec);
+        for (int i = 0; i < 32; ++i)
+            v[i] = zero ? 0.f : v[i] * scale;
+        pack32<T>(w, v);
+        stage.flush(w, to + c, stride, rows, columns - c, vec);
     }
 }
 
@@ -622,7 +614,7 @@ template <class J> int launch_product(const Product<J> &g, int64_t tiles, cudaSt
         return cuda_status(e);
     const int pairs = device_sm_count() / 2;
     const unsigned grid = 2u * static_cast<unsigned>(tiles < pairs ? (tiles < 1 ? 1 : tiles) : pairs);
-    return cuda_status(launch_kernel(kernel, dim3(grid), dim3(256), kProductShared, stream, 2, g));
+    return cuda_status(launch_kernel(kernel, dim3(grid), dim3(kProductThreads), kProductShared, stream, 2, g));
 }
 
 // Columns of a tile, 256 or 128, for `rows` tile rows and `cols` columns: those that take the SM
