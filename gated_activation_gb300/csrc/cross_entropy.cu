@@ -185,8 +185,8 @@ template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<
     // zeros from the live rows to a whole step of a sum over them
     if (copy && blockIdx.x == 0) {
         const int64_t from = int64_t(all) * g.kp, to = int64_t((all + kStep - 1) / kStep * kStep) * g.kp;
-        for (int64_t c = from + threadIdx.x; c < to; c += 256)
-            g.rows[c] = from_float<T>(0.f);
+        for (int64_t c = from + 8 * threadIdx.x; c < to; c += 8 * 256)
+            st_vec(g.rows + c, make_uint4(0, 0, 0, 0));
     }
 }
 
@@ -254,6 +254,67 @@ template <class T> struct Statistics {
         }
         if (mine)
             g.j.part[int64_t(r) * 2 * g.n_tiles + 2 * t.n0 + stage.part] = make_float2(top, sum);
+    }
+};
+
+// The same for up to N tokens, which would leave most of a 256-row tile empty, with the roles turned
+// round: the vocabulary's rows are the tile's, the tokens its columns.  A warp turns its 32 rows of 16
+// tokens in shared memory; two lanes then take half of the rows of a token each.
+template <class T, int N> struct TurnedStatistics {
+    using Elem = T;
+    static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
+    static constexpr int kN = N, kRows = kTile;
+    static constexpr Live kLive = Live::Columns;
+    struct Args {
+        const int32_t *goal;
+        float2 *part;        // [capacity, 8 tiles]: maximum, sum of 32 columns
+        int tiles;
+    };
+    using G = Product<TurnedStatistics>;
+    __device__ static int batch_of(int, bool) { return 0; }
+    __device__ static int batches(const G &g) { return g.batches; }
+    __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
+    __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
+                                uint32_t b, uint32_t bar) {
+        load_along(a, &g.a, bar, step * kStep, t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
+        load_along(b, t.live < g.capacity ? &g.other : &g.b, bar, step * kStep,
+                   static_cast<int>(rank) * (N / 2), 0, 0);
+    }
+    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
+        static_assert(32 * 17 * 4 <= 32 * kStageRow);
+        float *held = reinterpret_cast<float *>(stage.p);   // [32 rows, 16 tokens], 17 apart
+        const int lane = threadIdx.x & 31, first = t.m0 + (row & ~31), from = (lane >> 4) * 16;
+        for (int c = 32 * stage.part; c < N && c < t.live; c += 64) {
+            float v[32];
+            sums_load32(sums + c, v);
+            sums_load_wait();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    held[lane * 17 + i] = t.m0 + row < t.rows ? v[16 * half + i] : -INFINITY;
+                __syncwarp();
+                const int token = c + 16 * half + (lane & 15);
+                const bool mine = token < t.live;
+                const int goal = mine ? g.j.goal[token] - first - from : -1;
+                float x[16], top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    x[i] = held[(from + i) * 17 + (lane & 15)] * kLog2e;
+                    x[i] = goal == i ? -INFINITY : x[i];
+                    top = max_nan(top, x[i]);
+                }
+                top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+                const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    sum += exp2_fast(x[i] - base);
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+                if (mine && lane < 16)
+                    g.j.part[int64_t(token) * 8 * g.j.tiles + (first >> 5)] = make_float2(top, sum);
+                __syncwarp();
+            }
+        }
     }
 };
 
@@ -409,17 +470,19 @@ template <class T> struct JoinArgs {
     Tokens t;
     float *loss, *lse;
     int64_t in_stride, weight_stride;
-    int capacity, tiles, k;
+    int parts, k;
 };
 
-// A warp per live row.  The target's logit is summed here in fp32 with rounding: the tensor cores cut
+// WARPS warps per live row: one, or eight where there are few.  The target's logit is summed here in fp32 with rounding: the tensor cores cut
 // sums off, which at k = 2048 left it 1e-6 of its size too small.  With the other columns' sum s of
 // 2^(l - m), loss = log(1 + s 2^(m - l_target)) where the target is above them, so that a confident
 // token's small loss keeps its bits.
-template <class T> __global__ void __launch_bounds__(256) join_statistics(JoinArgs<T> g) {
+template <class T, int WARPS> __global__ void __launch_bounds__(256) join_statistics(JoinArgs<T> g) {
+    __shared__ float share[3][8];
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, r = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = (blockIdx.x * 8 + warp) / WARPS;
+    const int thread = warp % WARPS * 32 + lane;
     if (r >= *g.t.count)
         return;
     const int token = g.t.token[r];
@@ -428,7 +491,7 @@ template <class T> __global__ void __launch_bounds__(256) join_statistics(JoinAr
     const int from = g.k & ~7;
     const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 15) == 0;
 #pragma unroll 2
-    for (int c = lane * 8; c < from; c += 256) {   // in one order, whatever the alignment
+    for (int c = thread * 8; c < from; c += 256 * WARPS) {   // in one order, whatever the alignment
         uint4 vx, vw;
         if (vec) {
             vx = ld_stream(x + c);
@@ -443,10 +506,10 @@ template <class T> __global__ void __launch_bounds__(256) join_statistics(JoinAr
             dot[i] = fma2({to_float(px[2 * i]), to_float(px[2 * i + 1])},
                           {to_float(pw[2 * i]), to_float(pw[2 * i + 1])}, dot[i]);
     }
-    for (int c = from + lane; c < g.k; c += 32)
+    for (int c = from + thread; c < g.k; c += 32 * WARPS)
         dot[0].x = fmaf(to_float(x[c]), to_float(w[c]), dot[0].x);
     dot[0] = add2(add2(dot[0], dot[1]), add2(dot[2], dot[3]));
-    const float at = warp_sum(dot[0].x + dot[0].y), goal = at * kLog2e;
+    float at = warp_sum(dot[0].x + dot[0].y);
 
     float top = -INFINITY, sum = 0.f;
     const auto add = [&](float2 p) {
@@ -454,15 +517,30 @@ template <class T> __global__ void __launch_bounds__(256) join_statistics(JoinAr
         sum = sum * exp2_fast(top - base) + p.y * exp2_fast(p.x - base);
         top = most;
     };
-    for (int i = lane; i < g.tiles; i += 32)
-        add(g.part[int64_t(r) * g.tiles + i]);
+#pragma unroll 4
+    for (int i = thread; i < g.parts; i += 32 * WARPS)
+        add(g.part[int64_t(r) * g.parts + i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float2 p = {__shfl_xor_sync(0xFFFFFFFFu, top, o), __shfl_xor_sync(0xFFFFFFFFu, sum, o)};
         add(p);
     }
-    if (lane)
+    if (WARPS > 1) {   // a block is one row
+        if (lane == 0) {
+            share[0][warp] = at;
+            share[1][warp] = top;
+            share[2][warp] = sum;
+        }
+        __syncthreads();
+        if (thread == 0)
+            for (int i = 1; i < WARPS; ++i) {
+                at += share[0][i];
+                add({share[1][i], share[2][i]});
+            }
+    }
+    if (thread)
         return;
+    const float goal = at * kLog2e;
     float lse, loss;
     if (goal >= top) {
         loss = goal == INFINITY ? NAN : log1pf(sum * exp2f(top - goal));
@@ -553,15 +631,28 @@ Region target_region(const gated_act_vocabulary &a) {
     return {a.targets, static_cast<uint64_t>(a.T * size), static_cast<uintptr_t>(size), false};
 }
 
-// Columns of one piece of the vocabulary: y takes about 64 MB, so that the two products that
-// read it find it in L2, but 8192 columns at least, so that adding to grad_in's sums
-// (8 bytes per row and column of it) stays small beside the product.
+// Columns of one piece of the vocabulary: as many as give y 256 MB (of which the products that read
+// it find half in L2), but at least 8192, so that adding to grad_in's sums (8 bytes per row and column of it)
+// stays small beside the products; of those a quarter fewer to a quarter more, the number whose tiles come
+// nearest to a whole number of turns of the SM pairs.  (Pieces of 48 MB, which L2 holds, measured a
+// third slower at 4096 x 65536 x 1024, 40% live: 945 us against 710 with 64 MB.)
 int64_t piece_of(const gated_act_vocabulary &a) {
-    const int64_t rows = ceil_div64(a.T, kStep) * kStep;
-    int64_t n = (int64_t(32) << 20) / rows / kTile * kTile;
-    n = n < 8192 ? 8192 : n;
-    const int64_t all = ceil_div64(a.V, kTile) * kTile;
-    return n < all ? n : all;
+    const int64_t rows = ceil_div64(a.T, kStep) * kStep, m = ceil_div64(a.T, kTile);
+    const int64_t pairs = device_sm_count() / 2, all = ceil_div64(a.V, kTile);
+    int64_t n = (int64_t(128) << 20) / rows / kTile;
+    n = n < 32 ? 32 : n;
+    if (n >= all)
+        return all * kTile;
+    int64_t best = n;
+    double most = 0;
+    for (int64_t i = n - n / 4; i <= n + n / 4; ++i) {
+        const double full = static_cast<double>(m * i) / static_cast<double>(ceil_div64(m * i, pairs) * pairs);
+        if (full >= most) {
+            most = full;
+            best = i;
+        }
+    }
+    return (best < all ? best : all) * kTile;
 }
 
 // The parts of a workspace.
@@ -611,7 +702,8 @@ struct Parts {
             }
             sums = ws.take<float>(4 * kTile * kTile * most);
         } else {
-            part = ws.take<float2>(16 * ceil_div64(a.V, kTile) * a.T);
+            // two warps' shares of a tile's columns, or eight of the turned form's
+            part = ws.take<float2>((a.T <= 128 ? 64 : 16) * ceil_div64(a.V, kTile) * a.T);
         }
         rc = GATED_ACT_OK;
         if (!tma_addressable(weight)) {
@@ -671,6 +763,37 @@ template <class T> int encode_rows(CUtensorMap *place, CUtensorMap *packed, cons
     return encode_map(place, w.in, rows, is_bf16);
 }
 
+// The two forms of the statistics' product.
+template <class T> struct Upright {
+    static int set(Product<Statistics<T>> *g, const Parts &w, const gated_act_vocabulary &a) {
+        g->n_tiles = static_cast<int>(ceil_div64(a.V, kTile));
+        g->j = {w.t.goal, w.part, static_cast<int>(a.V)};
+        const int rc = encode_rows<T>(&g->a, &g->other, w, kHalf);
+        return rc == GATED_ACT_OK ? encode_map(&g->b, w.weight, kHalf, std::is_same_v<T, bf16>) : rc;
+    }
+    using Job = Statistics<T>;
+    static int64_t tiles(const gated_act_vocabulary &a) { return ceil_div64(a.T, kTile) * ceil_div64(a.V, kTile); }
+};
+template <class T, int N> struct Turned {
+    static int set(Product<TurnedStatistics<T, N>> *g, const Parts &w, const gated_act_vocabulary &a) {
+        g->n_tiles = 1;
+        g->rows = static_cast<int>(a.V);
+        g->j = {w.t.goal, w.part, static_cast<int>(ceil_div64(a.V, kTile))};
+        const int rc = encode_rows<T>(&g->b, &g->other, w, N / 2);
+        return rc == GATED_ACT_OK ? encode_map(&g->a, w.weight, kHalf, std::is_same_v<T, bf16>) : rc;
+    }
+    using Job = TurnedStatistics<T, N>;
+    static int64_t tiles(const gated_act_vocabulary &a) { return ceil_div64(a.V, kTile); }
+};
+template <class Form>
+int run_statistics(Form, const Parts &w, const gated_act_vocabulary &a, cudaStream_t stream) {
+    Product<typename Form::Job> g;
+    set_rows(&g, w, a);
+    g.steps = static_cast<int>(ceil_div64(a.k, kStep));
+    const int rc = Form::set(&g, w, a);
+    return rc == GATED_ACT_OK ? launch_product(g, Form::tiles(a), stream) : rc;
+}
+
 template <class T>
 int run_forward(float *loss, float *lse, const gated_act_vocabulary &a, void *workspace,
                 cudaStream_t stream) {
@@ -678,33 +801,22 @@ int run_forward(float *loss, float *lse, const gated_act_vocabulary &a, void *wo
     int rc = w.rc;
     if (rc == GATED_ACT_OK)
         rc = run_live_tokens<T>(w, a, nullptr, nullptr, loss, lse, nullptr, stream);
-    Product<Statistics<T>> g;
-    if (rc == GATED_ACT_OK)
-        rc = encode_rows<T>(&g.a, &g.other, w, kHalf);
-    if (rc == GATED_ACT_OK)
-        rc = encode_map(&g.b, w.weight, kHalf, std::is_same_v<T, bf16>);
     if (rc != GATED_ACT_OK)
         return rc;
-    set_rows(&g, w, a);
-    g.n_tiles = static_cast<int>(ceil_div64(a.V, kTile));
-    g.steps = static_cast<int>(ceil_div64(a.k, kStep));
-    g.j = {w.t.goal, w.part, static_cast<int>(a.V)};
-    rc = launch_product(g, ceil_div64(a.T, kTile) * g.n_tiles, stream);
+    const bool turned = a.T <= 128;
+    rc = a.T <= 32 ? run_statistics(Turned<T, 32>{}, w, a, stream)
+         : turned  ? run_statistics(Turned<T, 128>{}, w, a, stream)
+                   : run_statistics(Upright<T>{}, w, a, stream);
     if (rc != GATED_ACT_OK)
         return rc;
-    const JoinArgs<T> j = {w.part,
-                           static_cast<const T *>(a.in),
-                           static_cast<const T *>(a.weight),
-                           w.t,
-                           loss,
-                           lse,
-                           a.in_stride,
-                           a.weight_stride,
-                           static_cast<int>(a.T),
-                           2 * g.n_tiles,
-                           static_cast<int>(a.k)};
-    return cuda_status(launch_kernel(join_statistics<T>, dim3(static_cast<unsigned>(ceil_div64(a.T, 8))),
-                                     dim3(256), 0, stream, 1, j));
+    const int parts = static_cast<int>((turned ? 8 : 2) * ceil_div64(a.V, kTile));
+    const JoinArgs<T> j = {w.part, static_cast<const T *>(a.in), static_cast<const T *>(a.weight), w.t,
+                           loss,   lse, a.in_stride, a.weight_stride, parts, static_cast<int>(a.k)};
+    // with up to 1024 rows, a block each fills the SMs no better with a warp each
+    const bool wide = a.T <= 1024;
+    return cuda_status(launch_kernel(wide ? join_statistics<T, 8> : join_statistics<T, 1>,
+                                     dim3(static_cast<unsigned>(wide ? a.T : ceil_div64(a.T, 8))), dim3(256),
+                                     0, stream, 1, j));
 }
 
 template <class T>

@@ -17,7 +17,7 @@ GATED = [(1, 1, 1), (1, 64, 128), (3, 7, 5), (2, 72, 40), (17, 130, 33), (64, 64
          (9, 4096, 512), (1100, 264, 1032), (2304, 128, 2304)]
 # tokens, k, vocabulary
 ENTROPY = [(1, 1, 1), (1, 64, 256), (2, 8, 3), (5, 7, 31), (33, 72, 300), (64, 128, 1000),
-           (257, 200, 777), (300, 1001, 4099), (511, 256, 16384), (40, 64, 40001), (700, 136, 8200)]
+           (128, 96, 5000), (129, 40, 700), (257, 200, 777), (300, 1001, 4099), (511, 256, 16384), (40, 64, 40001), (700, 136, 8200)]
 
 
 @pytest.fixture(scope="module")
