@@ -111,8 +111,8 @@ template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<
         int most = 0;
         for (int i = 0; i < 8; ++i)
             most = max(most, red[i]);
-        // the power of two in it, within what has a normal inverse; 1 for 0 and infinity
-        const int e = min(max(most >> 23, 1), 253);
+        // the power of two in it, a normal number; 1 for 0 and infinity
+        const int e = min(max(most >> 23, 1), 254);
         power = most == 0 || most >= 0x7F800000 ? 1.f : __int_as_float(e << 23);
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -638,7 +638,7 @@ Region target_region(const gated_act_vocabulary &a) {
 // third slower at 4096 x 65536 x 1024, 40% live: 945 us against 710 with 64 MB.)
 int64_t piece_of(const gated_act_vocabulary &a) {
     const int64_t rows = ceil_div64(a.T, kStep) * kStep, m = ceil_div64(a.T, kTile);
-    const int64_t pairs = device_sm_count() / 2, all = ceil_div64(a.V, kTile);
+    const int64_t pairs = sm_pairs(), all = ceil_div64(a.V, kTile);
     int64_t n = (int64_t(128) << 20) / rows / kTile;
     n = n < 32 ? 32 : n;
     if (n >= all)
@@ -687,7 +687,7 @@ struct Parts {
             shares = {static_cast<int>(ceil_div64(a.k, kTile)),
                       static_cast<int>(ceil_div64(piece < a.V ? piece : a.V, kStep)),
                       static_cast<int>(ceil_div64(piece < a.V ? piece : a.V, kTile) * ceil_div64(a.k, kTile)),
-                      device_sm_count() / 2};
+                      sm_pairs()};
             // the most tiles of sums that any number of live rows takes: with more rows there are
             // more tiles and no more shares, and past kShares x pairs tiles the last count has the most
             int64_t most = 0;

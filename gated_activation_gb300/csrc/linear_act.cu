@@ -387,7 +387,7 @@ int addressable(Layout *t, Carve *ws, cudaStream_t stream) {
 // SMs without one of the turned tiles, the one that streams the weight through registers; else, with
 // up to 128, the turned product.
 bool few(const gated_act_linear &a, bool keep) {
-    return !keep && a.T <= kFewRows && a.E * ceil_div64(a.d, kHalf) < device_sm_count() / 2;
+    return !keep && a.T <= kFewRows && a.E * ceil_div64(a.d, kHalf) < sm_pairs();
 }
 
 uint64_t forward_bytes(const gated_act_linear &a, bool keep) {
@@ -567,7 +567,7 @@ int run_gradients(void *grad_in, void *grad_weight, const gated_act_linear &a, c
 // a step of 128 columns being 0.6 of one of 256.  Tiles go round the pairs in order, the first product's
 // in front.
 int gradient_columns(int64_t in_tiles, int64_t in_steps, int64_t w_tiles, int64_t w_steps, int64_t k) {
-    const int64_t pairs = device_sm_count() / 2;
+    const int64_t pairs = sm_pairs();
     const auto busiest = [&](int64_t n) {
         const int64_t in = in_tiles * ceil_div64(k, n), w = w_tiles * ceil_div64(k, n);
         const int64_t left = in % pairs, turns = in / pairs;   // pairs with one first tile more

@@ -6,8 +6,8 @@ namespace gact {
 bool tma_addressable(const Layout &t) {
     if (!aligned(t.data, 16))
         return false;
-    for (int i = 1; i < 4; ++i)
-        if (t.size[i] > 1 && t.stride[i] % 8)
+    for (int i = 1; i < 4; ++i)   // whole 16 bytes, below 2^40 bytes
+        if (t.size[i] > 1 && (t.stride[i] % 8 || t.stride[i] >= int64_t(1) << 39))
             return false;
     return true;
 }
@@ -76,31 +76,29 @@ Layout packed_layout(const Layout &t, void *data) {
     return p;
 }
 
-// Eight elements from an address off a 16-byte boundary, out of the two vectors that hold them.
-__device__ __forceinline__ uint4 shifted8(const uint16_t *p) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    const uint4 *v = reinterpret_cast<const uint4 *>(at & ~uintptr_t(15));
-    const uint4 lo = __ldg(v), hi = __ldg(v + 1);
-    const uint32_t off = static_cast<uint32_t>(at & 15), bits = (off & 3) * 8;
-    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    uint32_t r[5];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) {   // words from off / 4 on
-        const uint32_t a = off & 8 ? w[i + 2] : w[i];
-        const uint32_t b = off & 8 ? w[i + 3] : w[i + 1];
-        r[i] = off & 4 ? b : a;
+// The eight elements that start `off` bytes (even, below 16; the same in a warp) into two vectors.
+__device__ __forceinline__ uint4 shifted8(uint4 lo, uint4 hi, uint32_t off) {
+    const uint32_t pick = off & 2 ? 0x5432u : 0x3210u;
+    switch (off >> 2) {
+    case 0:
+        return make_uint4(__byte_perm(lo.x, lo.y, pick), __byte_perm(lo.y, lo.z, pick),
+                          __byte_perm(lo.z, lo.w, pick), __byte_perm(lo.w, hi.x, pick));
+    case 1:
+        return make_uint4(__byte_perm(lo.y, lo.z, pick), __byte_perm(lo.z, lo.w, pick),
+                          __byte_perm(lo.w, hi.x, pick), __byte_perm(hi.x, hi.y, pick));
+    case 2:
+        return make_uint4(__byte_perm(lo.z, lo.w, pick), __byte_perm(lo.w, hi.x, pick),
+                          __byte_perm(hi.x, hi.y, pick), __byte_perm(hi.y, hi.z, pick));
+    default:
+        return make_uint4(__byte_perm(lo.w, hi.x, pick), __byte_perm(hi.x, hi.y, pick),
+                          __byte_perm(hi.y, hi.z, pick), __byte_perm(hi.z, hi.w, pick));
     }
-    uint4 y;
-    y.x = __funnelshift_r(r[0], r[1], bits);
-    y.y = __funnelshift_r(r[1], r[2], bits);
-    y.z = __funnelshift_r(r[2], r[3], bits);
-    y.w = __funnelshift_r(r[3], r[4], bits);
-    return y;
 }
 
-// Eight elements and a 16-byte store per thread and row.  Rows off 16-byte boundaries are read as the
-// aligned vectors that hold them (consecutive lanes share these through L1); where one of the two
-// would reach past the tensor's own bytes, and at a row's end, element by element.
+// Eight elements and a 16-byte store per thread and row, a row's 256 elements per warp.  Rows off
+// 16-byte boundaries are read as the aligned vectors that hold them (consecutive lanes share these
+// through L1); where one of the two would reach past the tensor's own bytes, and at a row's end, element
+// by element.  Bound by its instructions before the shift was made the warp's (50001 x 1001: 56 us).
 __global__ void __launch_bounds__(256) pack_rows(Layout to, Layout from) {
     pdl_wait();
     pdl_trigger();
@@ -108,29 +106,32 @@ __global__ void __launch_bounds__(256) pack_rows(Layout to, Layout from) {
     if (x >= to.size[0])
         return;
     const int64_t z = blockIdx.z % to.size[2], w = blockIdx.z / to.size[2];
-    const uint16_t *plane = static_cast<const uint16_t *>(from.data) + z * from.stride[2] +
-                            w * from.stride[3] + x;
-    uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(to.data)) +
-                    blockIdx.z * to.size[1] * to.stride[1] + x;
     const uintptr_t first = reinterpret_cast<uintptr_t>(from.data);
     const uintptr_t last = first + 2 * static_cast<uintptr_t>(
         (from.size[1] - 1) * from.stride[1] + (from.size[2] - 1) * from.stride[2] +
-        (from.size[3] - 1) * from.stride[3] + from.size[0]);
+        (from.size[3] - 1) * from.stride[3] + from.size[0]) - 32;
+    const bool whole = x + 8 <= to.size[0];
+    int64_t r = int64_t(blockIdx.y) * 8 + threadIdx.y;
+    const int64_t step = int64_t(gridDim.y) * 8;
+    const uint16_t *p = static_cast<const uint16_t *>(from.data) + z * from.stride[2] +
+                        w * from.stride[3] + r * from.stride[1] + x;
+    uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(to.data)) +
+                    (blockIdx.z * to.size[1] + r) * to.stride[1] + x;
 #pragma unroll 2
-    for (int64_t r = int64_t(blockIdx.y) * 8 + threadIdx.y; r < to.size[1]; r += int64_t(gridDim.y) * 8) {
-        const uint16_t *p = plane + r * from.stride[1];
+    for (; r < to.size[1]; r += step, p += step * from.stride[1], out += step * to.stride[1]) {
         const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
         uint4 v;
-        if (x + 8 <= to.size[0] && at >= first && at + 32 <= last) {
-            v = shifted8(p);
+        if (whole && at >= first && at <= last) {
+            const uint4 *vec = reinterpret_cast<const uint4 *>(at);
+            v = shifted8(__ldg(vec), __ldg(vec + 1), static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15));
         } else {
             uint32_t e[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                e[i] = x + i < to.size[0] ? ld_stream_u16(p + i) : 0;
+            for (int c = 0; c < 8; ++c)
+                e[c] = x + c < to.size[0] ? ld_stream_u16(p + c) : 0;
             v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
         }
-        st_vec(out + r * to.stride[1], v);
+        st_vec_out(out, v);
     }
 }
 

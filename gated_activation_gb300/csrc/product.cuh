@@ -31,7 +31,7 @@ constexpr int kStep = 64;             // summed elements per ring slot: 128 byte
 constexpr int kRowBytes = kHalf * kStep * 2;   // of the first operand in a slot
 constexpr int kRingBytes = 6 * 2 * kRowBytes;
 constexpr int kMostSlots = 10;
-constexpr int kMaxBatches = 2048;
+constexpr int kMaxBatches = 1024;
 constexpr int kProductThreads = 384;
 
 // A slot of a job with N columns per tile: each CTA brings half of the second operand's rows.
@@ -607,12 +607,14 @@ struct Carve {
     }
 };
 
+inline int sm_pairs() { return device_sm_count() > 1 ? device_sm_count() / 2 : 1; }
+
 template <class J> int launch_product(const Product<J> &g, int64_t tiles, cudaStream_t stream) {
     auto kernel = product_kernel<J>;
     const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), kProductShared);
     if (e != cudaSuccess)
         return cuda_status(e);
-    const int pairs = device_sm_count() / 2;
+    const int pairs = sm_pairs();
     const unsigned grid = 2u * static_cast<unsigned>(tiles < pairs ? (tiles < 1 ? 1 : tiles) : pairs);
     return cuda_status(launch_kernel(kernel, dim3(grid), dim3(kProductThreads), kProductShared, stream, 2, g));
 }
@@ -620,7 +622,7 @@ template <class J> int launch_product(const Product<J> &g, int64_t tiles, cudaSt
 // Columns of a tile, 256 or 128, for `rows` tile rows and `cols` columns: those that take the SM
 // pairs fewer turns.  A tile of 128 takes 0.6 of the time of one of 256.
 inline int tile_columns(int64_t rows, int64_t cols) {
-    const int64_t pairs = device_sm_count() / 2;
+    const int64_t pairs = sm_pairs();
     const auto turns = [&](int64_t n) { return ceil_div64(rows * ceil_div64(cols, n), pairs); };
     return 0.6 * static_cast<double>(turns(128)) < static_cast<double>(turns(256)) ? 128 : 256;
 }
