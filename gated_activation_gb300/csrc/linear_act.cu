@@ -58,10 +58,10 @@ __device__ __forceinline__ uint32_t encode32(uint32_t (&w)[16], const float (&v)
 
 // ------------------------------------------------------------------- products
 
-template <class Act, class T, int N, bool KEEP> struct Forward {
+template <class Act, class T, bool KEEP> struct Forward {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
-    static constexpr int kN = N, kRows = kTile;
+    static constexpr int kN = kTile, kRows = kTile;
     static constexpr Live kLive = Live::Rows;
     struct Args {
         T *out;
@@ -77,7 +77,7 @@ template <class Act, class T, int N, bool KEEP> struct Forward {
                                 uint32_t b, uint32_t bar) {
         load_along(a, &g.a, bar, step * kStep, t.m0 + static_cast<int>(rank) * kHalf, 0, t.b);
         // the first CTA brings the gate's rows of the weight, the second the up half's
-        load_along(b, &g.b, bar, step * kStep, t.n0 * (N / 2), static_cast<int>(rank), t.b);
+        load_along(b, &g.b, bar, step * kStep, t.n0 * kHalf, static_cast<int>(rank), t.b);
     }
     __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
@@ -85,11 +85,11 @@ template <class Act, class T, int N, bool KEEP> struct Forward {
         const bool mine = r < t.rows;
         const int lane = threadIdx.x & 31, rows = t.rows - (r - lane);   // of the warp
         const int64_t at = int64_t(t.b) * g.capacity + r, top = at - lane;
-        for (int c = 32 * stage.part; c < N / 2 && t.n0 * (N / 2) + c < d; c += 64) {
-            const int col = t.n0 * (N / 2) + c, n = d - col;
+        for (int c = 32 * stage.part; c < kHalf && t.n0 * kHalf + c < d; c += 64) {
+            const int col = t.n0 * kHalf + c, n = d - col;
             float gate[32], up[32];
             sums_load32(sums + c, gate);
-            sums_load32(sums + N / 2 + c, up);
+            sums_load32(sums + kHalf + c, up);
             sums_load_wait();
             uint32_t w[16];
 #pragma unroll
@@ -181,10 +181,10 @@ template <class Act, class T, int N> struct Swapped {
 // Second, grad_weight: A = (dg, du) across the sum over the rows, B = in across it; batch 2e + half.
 // Past the live rows dg and du are zeros up to a whole step; the last rows of `in` come from
 // a copy with zeros there, as what lies past the live rows may be anything.
-template <class T, int N> struct Gradients {
+template <class T> struct Gradients {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = true, kSecond = true;
-    static constexpr int kN = N, kRows = kTile;
+    static constexpr int kN = kTile, kRows = kTile;
     static constexpr Live kLive = Live::Rows;
     struct Args {
         CUtensorMap rows, in, tail;   // of the second product
@@ -198,24 +198,24 @@ template <class T, int N> struct Gradients {
     __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
-        const int row = t.m0 + static_cast<int>(rank) * kHalf, col = t.n0 * N + static_cast<int>(rank) * (N / 2);
+        const int row = t.m0 + static_cast<int>(rank) * kHalf, col = t.n0 * kTile + static_cast<int>(rank) * kHalf;
         if (!t.second) {
             const int half = step >= g.j.half_steps, x = (step - half * g.j.half_steps) * kStep;
             load_along(a, &g.a, bar, x, row, half, t.b);
-            load_across<N / 2>(b, &g.b, bar, x, col, half, t.b);
+            load_across(b, &g.b, bar, x, col, half, t.b);
             return;
         }
         const int x = step * kStep, e = t.b >> 1;
         load_across(a, &g.j.rows, bar, x, row, t.b & 1, e);
         const bool tail = x + kStep > t.live && t.live < g.capacity;
-        load_across<N / 2>(b, tail ? &g.j.tail : &g.j.in, bar, tail ? 0 : x, col, 0, e);
+        load_across(b, tail ? &g.j.tail : &g.j.in, bar, tail ? 0 : x, col, 0, e);
     }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
-        const int k = g.j.k, top = t.m0 + (row & ~31), col = t.n0 * N;   // the warp's first row
+        const int k = g.j.k, top = t.m0 + (row & ~31), col = t.n0 * kTile;   // the warp's first row
         T *to = t.second ? g.j.grad_weight + (int64_t(t.b) * g.second.rows + top) * k + col
                          : g.j.grad_in + (int64_t(t.b) * g.capacity + top) * k + col;
-        store_tile<N>(sums, stage, to, k, t.rows - top, k - col, t.second ? g.j.vec_weight : g.j.vec_in,
-                      1.f, t.steps == 0);
+        store_tile(sums, stage, to, k, t.rows - top, k - col, t.second ? g.j.vec_weight : g.j.vec_in,
+                   1.f, t.steps == 0);
     }
 };
 
@@ -355,7 +355,7 @@ int check_sizes(const gated_act_linear &a) {
                    static_cast<double>(ceil_div64(cols, width)) <
                static_cast<double>(most);
     };
-    if (!tiles(a.T, a.d, 64) || !tiles(a.T + 2 * a.d + kTile, a.k, 128) ||
+    if (!tiles(a.T, a.d, kHalf) || !tiles(a.T + 2 * a.d + kTile, a.k, kTile) ||
         static_cast<double>(a.E) * static_cast<double>(a.T + kStep) *
                 static_cast<double>(2 * a.d + a.k) > 1e17)
         return GATED_ACT_ERR_TOO_LARGE;
@@ -410,19 +410,19 @@ template <class J> int set_forward(Product<J> *g, const gated_act_linear &a, con
     return GATED_ACT_OK;
 }
 
-template <class Act, class T, int N, bool KEEP>
+template <class Act, class T, bool KEEP>
 int run_product(void *out, int16_t *codes, uint8_t *scales, const gated_act_linear &a, const Operands &o,
                 const int32_t *live, cudaStream_t stream) {
     constexpr bool is_bf16 = std::is_same_v<T, bf16>;
-    Product<Forward<Act, T, N, KEEP>> g;
+    Product<Forward<Act, T, KEEP>> g;
     int rc = encode_map(&g.a, o.in, kHalf, is_bf16);
     if (rc == GATED_ACT_OK)
-        rc = encode_map(&g.b, o.weight, N / 2, is_bf16);
+        rc = encode_map(&g.b, o.weight, kHalf, is_bf16);
     if (rc != GATED_ACT_OK)
         return rc;
     set_forward(&g, a, live);
     g.rows = static_cast<int>(a.T);
-    g.n_tiles = static_cast<int>(ceil_div64(a.d, N / 2));
+    g.n_tiles = static_cast<int>(ceil_div64(a.d, kHalf));
     g.j = {static_cast<T *>(out), codes, scales, static_cast<int>(a.d),
            a.d % 8 == 0 && aligned(out, 16) && aligned(codes, 16)};
     return launch_product(g, a.E * ceil_div64(a.T, kTile) * g.n_tiles, stream);
@@ -468,9 +468,7 @@ int run_forward(void *out, int16_t *codes, uint8_t *scales, const gated_act_line
         if (a.T <= 128)
             return run_swapped<Act, T, 128>(out, a, o, live, stream);
     }
-    return tile_columns(a.E * ceil_div64(a.T, kTile), 2 * a.d) == 256
-               ? run_product<Act, T, 256, KEEP>(out, codes, scales, a, o, live, stream)
-               : run_product<Act, T, 128, KEEP>(out, codes, scales, a, o, live, stream);
+    return run_product<Act, T, KEEP>(out, codes, scales, a, o, live, stream);
 }
 
 template <class Act>
@@ -528,11 +526,11 @@ struct BackwardParts {
     uint64_t bytes;
 };
 
-template <class T, int N>
+template <class T>
 int run_gradients(void *grad_in, void *grad_weight, const gated_act_linear &a, const Layout &rows,
                   const Operands &o, const Layout &tail, cudaStream_t stream) {
     constexpr bool is_bf16 = std::is_same_v<T, bf16>;
-    Product<Gradients<T, N>> g;
+    Product<Gradients<T>> g;
     int rc = encode_map(&g.a, rows, kHalf, is_bf16);
     if (rc == GATED_ACT_OK)
         rc = encode_map(&g.b, o.weight, kStep, is_bf16);
@@ -548,7 +546,7 @@ int run_gradients(void *grad_in, void *grad_weight, const gated_act_linear &a, c
     g.live = a.n_rows;
     g.batches = static_cast<int>(a.E);
     g.capacity = g.rows = static_cast<int>(a.T);
-    g.n_tiles = static_cast<int>(ceil_div64(a.k, N));
+    g.n_tiles = static_cast<int>(ceil_div64(a.k, kTile));
     g.j.half_steps = static_cast<int>(ceil_div64(a.d, kStep));
     g.steps = 2 * g.j.half_steps;
     g.second.batches = static_cast<int>(2 * a.E);
@@ -561,29 +559,6 @@ int run_gradients(void *grad_in, void *grad_weight, const gated_act_linear &a, c
     g.j.vec_in = a.k % 8 == 0 && aligned(grad_in, 16);
     g.j.vec_weight = a.k % 8 == 0 && aligned(grad_weight, 16);
     return launch_product(g, a.E * (ceil_div64(a.T, kTile) + 2 * g.second.m_tiles) * g.n_tiles, stream);
-}
-
-// Columns of a tile for both products: those for which the busiest pair of SMs has fewer ring steps,
-// a step of 128 columns being 0.6 of one of 256.  Tiles go round the pairs in order, the first product's
-// in front.
-int gradient_columns(int64_t in_tiles, int64_t in_steps, int64_t w_tiles, int64_t w_steps, int64_t k) {
-    const int64_t pairs = sm_pairs();
-    const auto busiest = [&](int64_t n) {
-        const int64_t in = in_tiles * ceil_div64(k, n), w = w_tiles * ceil_div64(k, n);
-        const int64_t left = in % pairs, turns = in / pairs;   // pairs with one first tile more
-        // second tiles of a pair that has a first tile more, and of one that has not
-        const int64_t all = in + w;
-        int64_t most = 0;
-        for (const int64_t p : {int64_t(0), left ? left - 1 : 0, left, pairs - 1}) {
-            if (p >= pairs)
-                continue;
-            const int64_t mine = turns + (p < left), total = all / pairs + (p < all % pairs);
-            const int64_t steps = mine * in_steps + (total - mine) * w_steps;
-            most = steps > most ? steps : most;
-        }
-        return most;
-    };
-    return 0.6 * static_cast<double>(busiest(128)) < static_cast<double>(busiest(256)) ? 128 : 256;
 }
 
 template <class Act, class T>
@@ -630,13 +605,7 @@ int run_backward(void *grad_in, void *grad_weight, const void *grad_out, int64_t
                          {1, w.dp, w.padded * w.dp, 2 * w.padded * w.dp}};
     const Layout tail = {w.tail, {a.k, kStep, 1, a.E}, {1, w.kp, 0, kStep * w.kp}};
 
-    // Both products in one launch: its turns are those of the shorter tiles, unless the longer, of
-    // which there are few where the rows are few, last longer than all of them.
-    const int64_t in_tiles = a.E * ceil_div64(a.T, kTile), in_steps = 2 * ceil_div64(a.d, kStep),
-                  w_tiles = 2 * a.E * ceil_div64(a.d, kTile), w_steps = ceil_div64(a.T, kStep);
-    return gradient_columns(in_tiles, in_steps, w_tiles, w_steps, a.k) == 256
-               ? run_gradients<T, 256>(grad_in, grad_weight, a, rows, w.o, tail, stream)
-               : run_gradients<T, 128>(grad_in, grad_weight, a, rows, w.o, tail, stream);
+    return run_gradients<T>(grad_in, grad_weight, a, rows, w.o, tail, stream);
 }
 
 template <class Act>

@@ -57,12 +57,9 @@ int check_device_regions(Region *r, int n) {
     const int rc = check_regions(r, n);
     if (rc != GATED_ACT_OK)
         return rc;
-    for (int i = 0; i < n; ++i) {
-        const void *dev = nullptr;
-        bool host = false;
-        if (r[i].bytes && (resolve_ptr(r[i].p, &dev, &host) != GATED_ACT_OK || host))
+    for (int i = 0; i < n; ++i)
+        if (r[i].host)
             return GATED_ACT_ERR_HOST;
-    }
     return GATED_ACT_OK;
 }
 

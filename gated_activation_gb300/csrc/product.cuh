@@ -526,14 +526,11 @@ __device__ __forceinline__ void load_along(uint32_t dst, const CUtensorMap *map,
                                            int x, int row, int z, int w) {
     box_load(dst, map, bar, x, row, z, w);
 }
-// The same of `rows` (64 or 128) of an operand whose rows lie across the sum.
-template <int ROWS = kHalf>
+// The same of 128 rows of an operand whose rows lie across the sum.
 __device__ __forceinline__ void load_across(uint32_t dst, const CUtensorMap *map, uint32_t bar,
                                             int x, int row, int z, int w) {
-    static_assert(ROWS == 64 || ROWS == 128);
     box_load(dst, map, bar, row, x, z, w);
-    if (ROWS == 128)
-        box_load(dst + kStep * 128, map, bar, row + 64, x, z, w);
+    box_load(dst + kStep * 128, map, bar, row + 64, x, z, w);
 }
 
 template <class T> __device__ __forceinline__ uint32_t pack2(float2 v);
@@ -553,10 +550,10 @@ template <class T> __device__ __forceinline__ void pack32(uint32_t (&w)[16], con
 // The epilogue of a plain product: every column of the tile below `columns`, times `scale`, rounded
 // to T, into the warp's first `rows` rows at `to`, `stride` apart.  A sum without terms is 0 whatever
 // tensor memory holds.
-template <int N, class T>
+template <class T>
 __device__ __forceinline__ void store_tile(uint32_t sums, const Stage &stage, T *to, int64_t stride, int rows,
                                            int columns, bool vec, float scale, bool zero) {
-    for (int c = 32 * stage.part; c < N && c < columns; c += 64) {
+    for (int c = 32 * stage.part; c < kTile && c < columns; c += 64) {
         float v[32];
         uint32_t w[16];
         sums_load32(sums + c, v);
@@ -617,14 +614,6 @@ template <class J> int launch_product(const Product<J> &g, int64_t tiles, cudaSt
     const int pairs = sm_pairs();
     const unsigned grid = 2u * static_cast<unsigned>(tiles < pairs ? (tiles < 1 ? 1 : tiles) : pairs);
     return cuda_status(launch_kernel(kernel, dim3(grid), dim3(kProductThreads), kProductShared, stream, 2, g));
-}
-
-// Columns of a tile, 256 or 128, for `rows` tile rows and `cols` columns: those that take the SM
-// pairs fewer turns.  A tile of 128 takes 0.6 of the time of one of 256.
-inline int tile_columns(int64_t rows, int64_t cols) {
-    const int64_t pairs = sm_pairs();
-    const auto turns = [&](int64_t n) { return ceil_div64(rows * ceil_div64(cols, n), pairs); };
-    return 0.6 * static_cast<double>(turns(128)) < static_cast<double>(turns(256)) ? 128 : 256;
 }
 
 // Reads and clears this translation unit's status.

@@ -16,11 +16,11 @@ int check_regions(Region *r, int n) {
                 ranges_overlap(r[i].p, r[i].bytes, r[j].p, r[j].bytes))
                 return GATED_ACT_ERR_OVERLAP;
     for (int i = 0; i < n; ++i) {
-        bool host = false;
         r[i].dev = nullptr;
+        r[i].host = false;
         if (!r[i].bytes)
             continue;
-        const int rc = resolve_ptr(r[i].p, &r[i].dev, &host);
+        const int rc = resolve_ptr(r[i].p, &r[i].dev, &r[i].host);
         if (rc != GATED_ACT_OK)
             return rc;
     }

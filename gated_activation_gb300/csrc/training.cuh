@@ -444,6 +444,7 @@ struct Region {
     uintptr_t align;
     bool write;
     const void *dev = nullptr;
+    bool host = false;   // set by check_regions: page-locked host memory
 };
 
 // Null, alignment, overlap (of two buffers of which one is written) and

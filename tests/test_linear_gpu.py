@@ -154,6 +154,59 @@ def test_few_rows(ga, m, k, d, pad, shift, dtype):
     _check_gated("gelu", x, w, None, out, None, dtype)
 
 
+def _values(codes, scales):
+    """What a LinearCheckpoint's codes [n, 2d] stand for, from the format's definition."""
+    d, b = codes.shape[1] // 2, scales.shape[1] // 2
+    step = 2.0 ** (scales.double() - 127)
+    step = torch.where(scales == 255, torch.full_like(step, float("nan")), step)
+    step = torch.cat([step[:, :b].repeat_interleave(32, 1)[:, :d],
+                      step[:, b:].repeat_interleave(32, 1)[:, :d]], 1)
+    return codes.double() * step, step
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,k,d", [(5, 64, 32), (40, 72, 33), (300, 100, 200)])
+def test_checkpoint_values(ga, m, k, d, dtype):
+    """Codes are the nearest multiples of the smallest step that holds their block."""
+    x, w, _ = _operands(m, k, d, dtype, m)
+    x[::3] *= 2.0 ** -9
+    _, kept = ga.linear_silu_and_mul(x, w, keep=True)
+    _, _, g, u, og, ou = R.forward("silu", x.double(), w.double(), dtype)
+    ref, off = torch.cat([g, u], 1), torch.cat([og, ou], 1)
+    values, step = _values(kept.codes, kept.scales)
+    assert ((values - ref).abs() <= off + step / 2).all()
+    top = torch.cat([R.block_top(g), R.block_top(u)], 1)
+    worst = torch.cat([R.block_top(og), R.block_top(ou)], 1)
+    assert ((top - worst) / step <= 32767.5).all() and ((top + worst) / step >= 16383.75).all()
+
+
+def test_checkpoint_largest_code(ga):
+    """Magnitudes just below a power of two, where the next step is taken once the largest code
+    would round to 2^15: exact sums 2 - 2^-15 + t 2^-18 of three weights, alone in their blocks."""
+    t = torch.arange(-16, 17, dtype=torch.float64)
+    d = 32 * len(t)
+    w = torch.zeros(2 * d, 8, dtype=torch.float64)
+    rows = torch.arange(len(t)) * 32
+    for base in (0, d):
+        w[base + rows, 0] = 2 - 2.0 ** -7
+        w[base + rows, 1] = 2.0 ** -7 - 2.0 ** -15
+        w[base + rows, 2] = t * 2.0 ** -18
+    exact = (w[:, 0] + w[:, 1] + w[:, 2])[rows]
+    w = w.to(BF16)
+    assert torch.equal(w.double().sum(1)[rows], exact)
+    x = torch.ones(1, 8, dtype=BF16, device="cuda")
+    out, kept = ga.linear_silu_and_mul(x, w.cuda(), keep=True)
+    for part, base in ((0, 0), (1, d)):
+        codes = kept.codes[0, base + rows.cuda()].cpu().double()
+        scales = kept.scales[0].view(2, -1)[part].cpu().double()
+        low = (exact * 2.0 ** 14).round() <= 32767          # ties to even: 32767.5 gives 32768
+        assert torch.equal(scales, torch.where(low, 127.0 - 14, 127.0 - 13).double())
+        assert torch.equal(codes, (exact / 2.0 ** (scales - 127)).round())
+    dy = torch.ones(1, d, dtype=BF16, device="cuda")
+    grads = ga.linear_silu_and_mul_backward(dy, x, w.cuda(), kept)
+    _check_gated("silu", x, w.cuda(), dy, out, grads, BF16)
+
+
 def test_gated_special_values(ga):
     """An infinity or a NaN reaches what it is multiplied into, and nothing else."""
     x, w, dy = _operands(70, 64, 40, BF16, 11)
@@ -306,6 +359,99 @@ def test_entropy_zero_tokens(ga):
     assert kept.loss.shape == (0,) and gi.shape == (0, 64) and (gw == 0).all()
 
 
+def test_entropy_gradients_against_differences(ga):
+    """The kernels' gradients against differences of the 64-bit form."""
+    x, w, goal, gl = _tokens(7, 16, 40, F16, 12, 0.8)
+    kept = ga.linear_cross_entropy(x, w, goal)
+    gi, gw = ga.linear_cross_entropy_backward(gl, x, w, goal, kept)
+    live = goal >= 0
+    loss = lambda x, w: (R.entropy(x[live], w, goal[live])[0] * gl[live].double()).sum()  # noqa: E731
+    (_, bounds_in), (_, bounds_w) = R.entropy_backward(gl[live].double(), x[live].double(), w.double(),
+                                                       goal[live], F16)
+    full = torch.zeros_like(x, dtype=torch.float64)
+    full[live] = bounds_in
+    for t, grad, bound, which in ((x, gi, full, 0), (w, gw, bounds_w, 1)):
+        for i in range(0, t.numel(), 13):
+            move = torch.zeros(t.numel(), dtype=torch.float64, device="cuda")
+            move[i] = 1e-5
+            at = [x.double(), w.double()]
+            up, down = list(at), list(at)
+            up[which] = at[which] + move.view(t.shape)
+            down[which] = at[which] - move.view(t.shape)
+            diff = (loss(*up) - loss(*down)) / 2e-5
+            # the differences' own error: a third derivative times 1e-10, and cancellation
+            assert abs(grad.reshape(-1)[i].item() - diff.item()) <= bound.reshape(-1)[i].item() + 1e-6
+
+
+# ------------------------------------------------------------------ many sizes
+
+def test_random_sizes(ga):
+    import random
+    rng = random.Random(20)
+    for i in range(40):
+        dtype, name = rng.choice(DTYPES), rng.choice(["silu", "gelu"])
+        m, k, d = (int(2 ** rng.uniform(0, hi)) for hi in (9.5, 9, 9))
+        if rng.random() < 0.5:
+            x, w, dy = _operands(m, k, d, dtype, i)
+            out, kept = _ops(ga, name)[0](x, w, keep=True)
+            _check_gated(name, x, w, dy, out, _ops(ga, name)[1](dy, x, w, kept), dtype)
+            _check_gated(name, x, w, None, _ops(ga, name)[0](x, w), None, dtype)
+        else:
+            v = int(2 ** rng.uniform(0, 13))
+            x, w, goal, gl = _tokens(m, k, v, dtype, i, rng.choice([1.0, 0.7]))
+            kept = ga.linear_cross_entropy(x, w, goal)
+            _check_entropy(x, w, goal, gl, kept,
+                           ga.linear_cross_entropy_backward(gl, x, w, goal, kept), dtype)
+
+
+def test_offsets_past_32_bits_gated(ga):
+    """Outputs, codes and gradients of more than 2^31 elements."""
+    m, k, d = 70000, 64, 32768
+    x, w, _ = _operands(m, k, d, BF16, 81)
+    out, kept = ga.linear_silu_and_mul(x, w, keep=True)
+    dy = torch.empty(m, d, dtype=BF16, device="cuda")
+    rows = torch.tensor([0, 255, 32767, 65535, 65536, 69999], device="cuda")
+    dy.zero_()
+    dy[rows] = _randn(len(rows), d, seed=82).to(BF16)
+    _check_gated("silu", x[rows], w, None, out[rows], None, BF16)
+    gi, gw = ga.linear_silu_and_mul_backward(dy, x, w, kept)
+    # the other rows add nothing
+    (ri, bi), (rw, bw) = R.backward("silu", dy[rows].double(), x[rows].double(), w.double(), BF16)
+    R.check(gi[rows], ri, bi, "grad_in")
+    R.check(gw, rw, bw, "grad_weight")
+
+
+def test_offsets_past_32_bits_entropy(ga):
+    """A weight of more than 2^31 elements."""
+    t, k, v = 40, 8200, 270000
+    w = torch.empty(v, k, dtype=BF16, device="cuda")
+    for i in range(0, v, 30000):
+        w[i:i + 30000] = _randn(30000, k, seed=i, scale=2 * k ** -0.5).to(BF16)
+    x = _randn(t, k, seed=1).to(BF16)
+    goal = torch.randint(v, (t,), generator=_gen(2), device="cuda")
+    goal[0], goal[1] = v - 1, 0
+    gl = torch.rand(t, generator=_gen(3), device="cuda")
+    kept = ga.linear_cross_entropy(x, w, goal)
+    gi, gw = ga.linear_cross_entropy_backward(gl, x, w, goal, kept)
+    # the logits in 64 bits, in parts; then a part of the vocabulary's gradient
+    logits = torch.cat([x.double() @ w[i:i + 30000].double().T for i in range(0, v, 30000)], 1)
+    lse = torch.logsumexp(logits, 1)
+    at = logits.gather(1, goal[:, None])[:, 0]
+    off = R.acc(k) * (x.double().abs().sum(1) * w.abs().max().item())
+    assert ((kept.lse - lse).abs() <= off + 1e-4).all() and ((kept.loss - (lse - at)).abs() <= 2 * off + 1e-4).all()
+    y = torch.exp(logits - lse[:, None])
+    y[torch.arange(t, device="cuda"), goal] -= 1
+    y *= gl.double()[:, None]
+    for part in (slice(0, 300), slice(261000, 262500), slice(v - 300, v)):
+        ref = y[:, part].T @ x.double()
+        # half a step of y and of the result, and y's own error: off of exp's argument, at most
+        loose = (y[:, part].abs() * (2.0 ** -8 + 3 * off[:, None] + 1e-4)).T @ x.double().abs()
+        R.check(gw[part], ref, loose + R.half_step(ref, BF16) + 1e-30, "grad_weight")
+    ref = sum(y[:, i:i + 30000] @ w[i:i + 30000].double() for i in range(0, v, 30000))
+    # row by row in norm: y's roundings are independent of each other and of the weight
+    assert ((gi.double() - ref).norm(dim=1) <= 2 * 2.0 ** -8 * ref.norm(dim=1)).all()
+
+
 # ------------------------------------------------------- streams, graphs, order
 
 def test_runs_together(ga):
@@ -380,6 +526,35 @@ def test_two_streams_at_once(ga):
     torch.cuda.synchronize()
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, (want, *grads)))
+
+
+def test_two_graphs(ga):
+    """Two captured graphs, replayed in turn and on two streams at once."""
+    sets = [_operands(300, 200, 130, BF16, 90 + i) for i in range(2)]
+    goals = [torch.randint(200, (300,), generator=_gen(i), device="cuda") for i in range(2)]
+    gl = torch.full((300,), 1 / 300, device="cuda")
+
+    def work(i):
+        x, w, dy = sets[i]
+        out, kept = ga.linear_gelu_and_mul(x, w, keep=True)
+        ce = ga.linear_cross_entropy(x, w, goals[i])
+        return (out, *ga.linear_gelu_and_mul_backward(dy, x, w, kept), ce.loss,
+                *ga.linear_cross_entropy_backward(gl, x, w, goals[i], ce))
+
+    want = [work(0), work(1)]
+    torch.cuda.synchronize()
+    graphs, held = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for i, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            held.append(work(i))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for got, ref in zip(held, want):
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
 
 
 def test_autograd_function(ga):
