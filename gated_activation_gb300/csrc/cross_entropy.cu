@@ -17,6 +17,17 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// What logits of k terms are multiplied with to be powers of two.  The tensor cores cut their fp32 sums
+// off towards 0 after every instruction (16 terms), half a unit in the last place on average: a sum of k
+// terms, whose partial sums are half of it on average, loses a share of it that grows as k.  (Expected,
+// with 24 bits: k / 16 cuts x 2^-24 x 0.72, the mean of 1 / m over mantissas m in [1, 2), x 1/2 = 1.3e-9 k.
+// Measured on GB300, 65536 sums of N(0, 16) each: 0.93e-9 to 0.97e-9 k in bf16 and 1.03e-9 to 1.12e-9 k in
+// fp16 for k from 1024 to 8192.)  The mean of it is given back here: it would be most of the error of a loss,
+// 9e-7 of it at k = 2048.
+inline float powers_of(int64_t k) {
+    return static_cast<float>(1.4426950408889634 * (1.0 + 1.0e-9 * static_cast<double>(k)));
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -211,6 +222,7 @@ template <class T> struct Statistics {
         const int32_t *goal;
         float2 *part;        // [capacity, 2 tiles]: maximum, sum of each warp's columns
         int V;
+        float powers;
     };
     using G = Product<Statistics>;
     __device__ static int batch_of(int, bool) { return 0; }
@@ -235,17 +247,18 @@ template <class T> struct Statistics {
                 for (int i = 0; i < 32; ++i)
                     v[i] = i < n && goal - c != i ? v[i] : -INFINITY;
             }
-            float most[4] = {top * (1.f / kLog2e), v[0], v[1], v[2]};
+            float most[4] = {-INFINITY, v[0], v[1], v[2]};
 #pragma unroll
             for (int i = 3; i < 32; ++i)
                 most[i & 3] = max_nan(most[i & 3], v[i]);
-            const float now = max_nan(max_nan(most[0], most[1]), max_nan(most[2], most[3])) * kLog2e;
+            const float here = max_nan(max_nan(most[0], most[1]), max_nan(most[2], most[3]));
+            const float now = max_nan(top, here * g.j.powers);
             // a row of -infinity alone has no exponential: its maximum is taken as 0
             const float base = now == -INFINITY ? 0.f : now;
             float2 part[2] = {{sum * exp2_fast(top - base), 0.f}, {0.f, 0.f}};
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-                const float2 y = fma2({v[i], v[i + 1]}, both(kLog2e), both(-base));
+                const float2 y = fma2({v[i], v[i + 1]}, both(g.j.powers), both(-base));
                 part[i >> 1 & 1] = add2(part[i >> 1 & 1], {exp2_fast(y.x), exp2_fast(y.y)});
             }
             part[0] = add2(part[0], part[1]);
@@ -269,6 +282,7 @@ template <class T, int N> struct TurnedStatistics {
         const int32_t *goal;
         float2 *part;        // [capacity, 8 tiles]: maximum, sum of 32 columns
         int tiles;
+        float powers;
     };
     using G = Product<TurnedStatistics>;
     __device__ static int batch_of(int, bool) { return 0; }
@@ -300,7 +314,7 @@ template <class T, int N> struct TurnedStatistics {
                 float x[16], top = -INFINITY, sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    x[i] = held[(from + i) * 17 + (lane & 15)] * kLog2e;
+                    x[i] = held[(from + i) * 17 + (lane & 15)] * g.j.powers;
                     x[i] = goal == i ? -INFINITY : x[i];
                     top = max_nan(top, x[i]);
                 }
@@ -331,6 +345,7 @@ template <class T> struct Slopes {
         Tokens t;
         T *y;              // [padded, piece]
         int V, first, piece;
+        float powers;
     };
     using G = Product<Slopes>;
     __device__ static int batch_of(int, bool) { return 0; }
@@ -357,7 +372,7 @@ template <class T> struct Slopes {
             sums_load_wait();
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-                const float2 x = fma2({v[i], v[i + 1]}, both(kLog2e), both(-shift));
+                const float2 x = fma2({v[i], v[i + 1]}, both(g.j.powers), both(-shift));
                 v[i] = exp2_fast(x.x);
                 v[i + 1] = exp2_fast(x.y);
             }
@@ -767,7 +782,7 @@ template <class T> int encode_rows(CUtensorMap *place, CUtensorMap *packed, cons
 template <class T> struct Upright {
     static int set(Product<Statistics<T>> *g, const Parts &w, const gated_act_vocabulary &a) {
         g->n_tiles = static_cast<int>(ceil_div64(a.V, kTile));
-        g->j = {w.t.goal, w.part, static_cast<int>(a.V)};
+        g->j = {w.t.goal, w.part, static_cast<int>(a.V), powers_of(a.k)};
         const int rc = encode_rows<T>(&g->a, &g->other, w, kHalf);
         return rc == GATED_ACT_OK ? encode_map(&g->b, w.weight, kHalf, std::is_same_v<T, bf16>) : rc;
     }
@@ -778,7 +793,7 @@ template <class T, int N> struct Turned {
     static int set(Product<TurnedStatistics<T, N>> *g, const Parts &w, const gated_act_vocabulary &a) {
         g->n_tiles = 1;
         g->rows = static_cast<int>(a.V);
-        g->j = {w.t.goal, w.part, static_cast<int>(ceil_div64(a.V, kTile))};
+        g->j = {w.t.goal, w.part, static_cast<int>(ceil_div64(a.V, kTile)), powers_of(a.k)};
         const int rc = encode_rows<T>(&g->b, &g->other, w, N / 2);
         return rc == GATED_ACT_OK ? encode_map(&g->a, w.weight, kHalf, std::is_same_v<T, bf16>) : rc;
     }
@@ -847,7 +862,7 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
         s.n_tiles = static_cast<int>(ceil_div64(cols, kTile));
         s.steps = static_cast<int>(ceil_div64(a.k, kStep));
         s.j = {w.t, static_cast<T *>(w.y), static_cast<int>(a.V), static_cast<int>(first),
-               static_cast<int>(w.piece)};
+               static_cast<int>(w.piece), powers_of(a.k)};
         rc = launch_product(s, ceil_div64(a.T, kTile) * s.n_tiles, stream);
         if (rc == GATED_ACT_OK)
             rc = encode_map(&g.a, y, kHalf, is_bf16);
