@@ -53,6 +53,14 @@ __device__ __forceinline__ uint32_t in_first_cta(uint32_t a) {
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
     return r;
 }
+// True in one lane of a converged warp, always the same.  (The compiler knows of this form that one
+// lane is left, and keeps the operands of the copies and products in uniform registers; under
+// `lane == 0` each took a loop over the lanes, 500 cycles for a step's instructions.)
+__device__ __forceinline__ bool elected() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
@@ -420,8 +428,9 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
 
     Walk<J> walk(g, s);
     Tile t;
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // the first CTA's barrier counts both CTAs' bytes
+        const uint32_t first_full = in_first_cta(full);
         uint32_t slot = 0, phase = 0;
         bool ok = true;
         while (ok && walk.next(&t))
@@ -429,9 +438,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                 if (!(ok = barrier_wait(empty + 8 * slot, phase ^ 1, &s.gave_up)))
                     break;
                 const uint32_t to = base + slot * SLOT;
-                if (rank == 0)
-                    barrier_expect(full + 8 * slot, 2 * SLOT);
-                J::load(g, t, k, rank, to, to + kRowBytes, in_first_cta(full + 8 * slot));
+                if (elected()) {
+                    if (rank == 0)
+                        barrier_expect(full + 8 * slot, 2 * SLOT);
+                    J::load(g, t, k, rank, to, to + kRowBytes, first_full + 8 * slot);
+                }
+                __syncwarp();
                 if (++slot == SLOTS) {
                     slot = 0;
                     phase ^= 1;
@@ -446,7 +458,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                 phase ^= 1;
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
         constexpr uint32_t first = product_descriptor<typename J::Elem, J::kN, J::kAAcross, J::kBAcross>();
         constexpr uint32_t second = product_descriptor<typename J::Elem, J::kN, true, J::kBAcross>();
         uint32_t slot = 0, phase = 0, turn = 0;
@@ -456,27 +468,32 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
             if (!(ok = barrier_wait(sums_empty + 8 * half, ((turn >> 1) & 1) ^ 1, &s.gave_up)))
                 break;
             sums_fence_after();
+            const bool across = J::kAAcross || (J::kSecond && t.second);
+            const uint64_t a0 = across ? slot_descriptor<true>(base) : slot_descriptor<false>(base),
+                           b0 = slot_descriptor<J::kBAcross>(base + kRowBytes),
+                           turn16 = across ? kDescriptorStep<true> : kDescriptorStep<false>;
+            const uint32_t desc = across ? second : first;
             for (int k = 0; k < t.steps; ++k) {
                 if (!(ok = barrier_wait(full + 8 * slot, phase, &s.gave_up)))
                     break;
                 sums_fence_after();
-                const uint32_t from = base + slot * SLOT;
-                const bool across = J::kAAcross || (J::kSecond && t.second);
-                const uint64_t a = across ? slot_descriptor<true>(from) : slot_descriptor<false>(from),
-                               turn16 = across ? kDescriptorStep<true> : kDescriptorStep<false>,
-                               b = slot_descriptor<J::kBAcross>(from + kRowBytes);
+                if (elected()) {
+                    const uint64_t at = slot * (SLOT >> 4);
 #pragma unroll
-                for (int i = 0; i < kStep / 16; ++i)
-                    product_step(to, a + i * turn16,
-                                 b + i * kDescriptorStep<J::kBAcross>, across ? second : first, k > 0 || i > 0);
-                product_commit(empty + 8 * slot);
+                    for (int i = 0; i < kStep / 16; ++i)
+                        product_step(to, a0 + at + i * turn16, b0 + at + i * kDescriptorStep<J::kBAcross>,
+                                     desc, k > 0 || i > 0);
+                    product_commit(empty + 8 * slot);
+                }
+                __syncwarp();
                 if (++slot == SLOTS) {
                     slot = 0;
                     phase ^= 1;
                 }
             }
-            if (ok)
+            if (ok && elected())
                 product_commit(sums_full + 8 * half);
+            __syncwarp();
             ++turn;
         }
     } else if (warp >= 4) {
