@@ -24,10 +24,6 @@ __device__ __forceinline__ uint32_t scale_of(float top) {
     const uint32_t e = (__float_as_uint(top) + 0x100u) >> 23;   // 255: infinity or NaN
     return e >= 255 ? 255u : e <= 15 ? 1u : e - 14;
 }
-// v / 2^(e - 127) as an int16 (0 under e = 255).
-__device__ __forceinline__ uint32_t code_of(float v, float inverse) {
-    return static_cast<uint32_t>(__float2int_rn(v * inverse)) & 0xFFFFu;
-}
 __device__ __forceinline__ float inverse_scale(uint32_t e) {
     return e == 255 ? 0.f : __uint_as_float((254u - e) << 23);
 }
@@ -50,9 +46,12 @@ __device__ __forceinline__ uint32_t encode32(uint32_t (&w)[16], const float (&v)
     const uint32_t e = scale_of(top);
     const float inverse = inverse_scale(e);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        w[i] = e == 255 ? 0u
-                        : code_of(v[2 * i], inverse) | code_of(v[2 * i + 1], inverse) << 16;
+    for (int i = 0; i < 16; ++i) {
+        // 1.5 2^23 + x is rounded to whole numbers, ties to even, and x's 16 bits are its last ones:
+        // no conversion, as in decode2
+        const float2 x = fma2({v[2 * i], v[2 * i + 1]}, both(inverse), both(12582912.f));
+        w[i] = e == 255 ? 0u : __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x5410);
+    }
     return e;
 }
 

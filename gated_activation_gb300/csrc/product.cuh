@@ -53,9 +53,9 @@ __device__ __forceinline__ uint32_t in_first_cta(uint32_t a) {
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
     return r;
 }
-// True in one lane of a converged warp, always the same.  (The compiler knows of this form that one
-// lane is left, and keeps the operands of the copies and products in uniform registers; under
-// `lane == 0` each took a loop over the lanes, 500 cycles for a step's instructions.)
+// True in one lane of a converged warp.  (Of this form the compiler knows that one lane is left, and
+// keeps the operands of the copies and products in uniform registers; under `lane == 0` each took a loop
+// over the lanes, and a step's instructions 500 cycles, as long as its products.)
 __device__ __forceinline__ bool elected() {
     uint32_t p;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
 
     Walk<J> walk(g, s);
     Tile t;
-    if (warp == 0) {
+    if (warp == 0 && elected()) {
         // the first CTA's barrier counts both CTAs' bytes
         const uint32_t first_full = in_first_cta(full);
         uint32_t slot = 0, phase = 0;
@@ -438,12 +438,9 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                 if (!(ok = barrier_wait(empty + 8 * slot, phase ^ 1, &s.gave_up)))
                     break;
                 const uint32_t to = base + slot * SLOT;
-                if (elected()) {
-                    if (rank == 0)
-                        barrier_expect(full + 8 * slot, 2 * SLOT);
-                    J::load(g, t, k, rank, to, to + kRowBytes, first_full + 8 * slot);
-                }
-                __syncwarp();
+                if (rank == 0)
+                    barrier_expect(full + 8 * slot, 2 * SLOT);
+                J::load(g, t, k, rank, to, to + kRowBytes, first_full + 8 * slot);
                 if (++slot == SLOTS) {
                     slot = 0;
                     phase ^= 1;
@@ -458,7 +455,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                 phase ^= 1;
             }
         }
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp == 1 && rank == 0 && elected()) {
         constexpr uint32_t first = product_descriptor<typename J::Elem, J::kN, J::kAAcross, J::kBAcross>();
         constexpr uint32_t second = product_descriptor<typename J::Elem, J::kN, true, J::kBAcross>();
         uint32_t slot = 0, phase = 0, turn = 0;
@@ -477,23 +474,19 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                 if (!(ok = barrier_wait(full + 8 * slot, phase, &s.gave_up)))
                     break;
                 sums_fence_after();
-                if (elected()) {
-                    const uint64_t at = slot * (SLOT >> 4);
+                const uint64_t at = slot * (SLOT >> 4);
 #pragma unroll
-                    for (int i = 0; i < kStep / 16; ++i)
-                        product_step(to, a0 + at + i * turn16, b0 + at + i * kDescriptorStep<J::kBAcross>,
-                                     desc, k > 0 || i > 0);
-                    product_commit(empty + 8 * slot);
-                }
-                __syncwarp();
+                for (int i = 0; i < kStep / 16; ++i)
+                    product_step(to, a0 + at + i * turn16, b0 + at + i * kDescriptorStep<J::kBAcross>, desc,
+                                 k > 0 || i > 0);
+                product_commit(empty + 8 * slot);
                 if (++slot == SLOTS) {
                     slot = 0;
                     phase ^= 1;
                 }
             }
-            if (ok && elected())
+            if (ok)
                 product_commit(sums_full + 8 * half);
-            __syncwarp();
             ++turn;
         }
     } else if (warp >= 4) {
