@@ -102,13 +102,21 @@ template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<
     const int begin = blockIdx.x * g.segment, end = min(begin + g.segment, g.n);
     int before = 0, all = 0;
     float top = 0.f;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < g.n; i += 256) {
-        const bool live = target(i) >= 0;
-        all += live;
-        before += live && i < begin;
-        if (g.grad_loss && live)
-            top = fmaxf(top, fabsf(g.grad_loss[i]));
+    for (int i0 = threadIdx.x; i0 < g.n; i0 += 8 * 256) {   // sixteen loads on their way
+        int goal[8];
+        float weight[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + 256 * j;
+            goal[j] = i < g.n ? target(i) : -1;
+            weight[j] = g.grad_loss && i < g.n ? g.grad_loss[i] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            all += goal[j] >= 0;
+            before += goal[j] >= 0 && i0 + 256 * j < begin;
+            top = goal[j] >= 0 ? fmaxf(top, fabsf(weight[j])) : top;
+        }
     }
     all = block_sum_int(all, red);
     before = block_sum_int(before, red);
