@@ -220,7 +220,9 @@ __device__ __forceinline__ void load_logits(const G &g, const Tile &t, int first
     load_along(b, &g.b, bar, step * kStep, first + t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, 0);
 }
 
-// Maximum (in powers of two) and sum of exponentials of each row over a tile's columns.
+// Maximum (in powers of two) and sum of exponentials of each row over a tile's columns.  2 T V k operations,
+// bound by the tensor cores: 8192 x 65536 x 2048 in 1.09 ms alone (2.0 PFLOP/s), 1.28 ms in a stream of such
+// calls (the power limit).  A tile's exponentials take 1.7 us, hidden from k = 384 on.
 template <class T> struct Statistics {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
@@ -279,7 +281,7 @@ template <class T> struct Statistics {
 };
 
 // The same for up to N tokens, which would leave most of a 256-row tile empty, with the roles turned
-// round: the vocabulary's rows are the tile's, the tokens its columns.  A warp turns its 32 rows of 16
+// round: the vocabulary's rows are the tile's, the tokens its columns (64 x 32000 x 1024: 12.6 us, upright 17.3).  A warp turns its 32 rows of 16
 // tokens in shared memory; two lanes then take half of the rows of a token each.
 template <class T, int N> struct TurnedStatistics {
     using Elem = T;
@@ -344,6 +346,9 @@ template <class T, int N> struct TurnedStatistics {
 // 2^-14, a probability in a large vocabulary often falls below; |y| <= 2^15 then).
 template <class T> constexpr float kLift = std::is_same_v<T, f16> ? 16384.f : 1.f;
 
+//
+// The product again, y written as the operand that the next one reads along the sum and across it: 4096 x
+// 38912 x 2048 in 337 us (1.94 PFLOP/s).
 template <class T> struct Slopes {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
@@ -417,6 +422,7 @@ struct Shares {
 // sums a share of the piece's columns.  The sums lie as the threads hold them, 256 x 256 to a tile,
 // column after column: a warp writes 128 bytes at once.
 // Second, the piece's rows of grad_weight: A = y across the sum over the live rows, B = in across it.
+// 4096 x 38912 x 2048 in 665 us (1.96 PFLOP/s); 4096 x 8192 x 2048 in 168 us, as two launches 182.
 template <class T> struct PieceGradients {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = true, kSecond = true;

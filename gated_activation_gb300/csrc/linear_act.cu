@@ -57,6 +57,10 @@ __device__ __forceinline__ uint32_t encode32(uint32_t (&w)[16], const float (&v)
 
 // ------------------------------------------------------------------- products
 
+// The forward product.  4 T k d operations; bound by the tensor cores where k is long (2048 x 4096 -> 16384:
+// 280 us alone, 94% of cuBLAS's rate and more), by the epilogue where it is short: per element one exponential, one
+// reciprocal and, for the checkpoint, a maximum, a product and three rounds through shared memory, 4 to
+// 5 us for a tile of 128 x 128 per CTA (8 warps), against 5 ns per summed element in the main loop.
 template <class Act, class T, bool KEEP> struct Forward {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
@@ -114,7 +118,9 @@ template <class Act, class T, bool KEEP> struct Forward {
 // The same product with the roles turned round, for up to N rows that would leave most of a
 // 256-row tile empty: the weight's rows are the tile's (64 of g and the same 64 of u per CTA), the
 // input's its columns.  Of four epilogue warps two hold g and two the u of the same columns, which
-// they hand over through shared memory.
+// they hand over through shared memory.  Bound by reading the weight: 16 rows of 4096 -> 16384 43.5 us (268 MB, 91%
+// of the copy rate; upright 51 us), 128 experts of 2048 -> 768 with 0 to 4 rows 104 us (the copy rate;
+// upright 117 us).
 template <class Act, class T, int N> struct Swapped {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
@@ -180,6 +186,8 @@ template <class Act, class T, int N> struct Swapped {
 // Second, grad_weight: A = (dg, du) across the sum over the rows, B = in across it; batch 2e + half.
 // Past the live rows dg and du are zeros up to a whole step; the last rows of `in` come from
 // a copy with zeros there, as what lies past the live rows may be anything.
+// 8 T k d operations in one launch: 4096 rows of 4096 -> 8192 in 560 us alone (1.96 PFLOP/s; two launches 620),
+// 32 experts of 2048 -> 768, 70% of 1024 rows, 167 us (1.73 PFLOP/s of the live rows).
 template <class T> struct Gradients {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = true, kSecond = true;
@@ -241,7 +249,8 @@ template <class T> struct GateGradIn {
 constexpr int kGradRows = 2;   // rows of a thread: six 16-byte loads on their way
 
 // (dg, du) of eight columns of four rows per thread, zeros from the live rows to a whole step.
-// One pass: 6 bytes and the scales in, 4 out per pair of elements.
+// One pass: 6 bytes and the scales in, 4 out per pair of elements; 4096 x 8192 in 55 us, 90% of the copy
+// rate (four rows a thread in 128 registers: 71 us; two in 64, twice the warps).
 template <class Act, class T, bool VEC>
 __global__ void __launch_bounds__(256, 4) gate_gradients(GateGradArgs<T> g) {
     pdl_wait();

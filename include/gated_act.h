@@ -37,8 +37,9 @@
  *     launch only on `stream` (0 = the legacy default stream), so every call
  *     is asynchronous and can be captured in a CUDA graph.  The library keeps
  *     three pieces of device state per GPU, all in its own static device
- *     memory: a status word that the bulk-copy kernels set when a bounded
- *     wait gives up (gated_act_device_status), the 256-byte scratch array of
+ *     memory: status words that the bulk-copy kernels and the products of
+ *     gated_act_linear.h set when a bounded wait gives up
+ *     (gated_act_device_status), the 256-byte scratch array of
  *     gelu_and_mul_sparse_ws_static, and the native mode's 64 KB tables (see
  *     gelu_and_mul_sparse_native).  No other device state outlives a call.
  *   - The launch geometry depends only on the arguments, the pointers'
@@ -177,8 +178,9 @@ int gated_act_last_cuda_error(void);
 /*
  * Device-side status of the library's kernels on the current device since
  * the last call, then cleared.  *flags bit 0: a kernel's bounded wait (1 s)
- * for one of its own bulk copies gave up; the rows that CTA had not finished
- * were left unwritten.  No other bit is used.  Synchronizes the device
+ * for one of its own bulk copies (or, in the products of gated_act_linear.h,
+ * for copies, products or its own warps) gave up; the rows or tiles that CTA had
+ * not finished were left unwritten.  No other bit is used.  Synchronizes the device
  * (it copies a status word), so call it outside stream capture.
  */
 int gated_act_device_status(unsigned int *flags);
