@@ -250,7 +250,7 @@ template <class T> struct Statistics {
         for (int c = 32 * stage.part; c < kTile && first + c < g.j.V; c += 64) {
             float v[32];
             sums_load32(sums + c, v);
-            sums_load_wait();
+            sums_ready(v);
             const int n = g.j.V - first - c;
             if (n < 32 || (goal >= c && goal < c + 32)) {
 #pragma unroll
@@ -311,7 +311,7 @@ template <class T, int N> struct TurnedStatistics {
         for (int c = 32 * stage.part; c < N && c < t.live; c += 64) {
             float v[32];
             sums_load32(sums + c, v);
-            sums_load_wait();
+            sums_ready(v);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -382,7 +382,7 @@ template <class T> struct Slopes {
             float v[32];
             uint32_t w[16];
             sums_load32(sums + c, v);
-            sums_load_wait();
+            sums_ready(v);
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
                 const float2 x = fma2({v[i], v[i + 1]}, both(g.j.powers), both(-shift));
@@ -475,7 +475,7 @@ template <class T> struct PieceGradients {
         for (int c = 32 * stage.part; c < kTile && col + c < k; c += 64, held += 64 * kTile) {
             float v[32];
             sums_load32(sums + c, v);
-            sums_load_wait();
+            sums_ready(v);
             if (!mine)
                 continue;
 #pragma unroll

@@ -93,7 +93,8 @@ template <class Act, class T, bool KEEP> struct Forward {
             float gate[32], up[32];
             sums_load32(sums + c, gate);
             sums_load32(sums + kHalf + c, up);
-            sums_load_wait();
+            sums_ready(gate);
+            sums_ready(up);
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -153,7 +154,7 @@ template <class Act, class T, int N> struct Swapped {
             const uint32_t use = stage.uses++;
             float v[32];
             sums_load32(sums + c, v);
-            sums_load_wait();
+            sums_ready(v);
             if (up) {
                 if (!barrier_wait(empty, (use & 1) ^ 1, &stage.s.gave_up))
                     return;

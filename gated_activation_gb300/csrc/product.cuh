@@ -23,7 +23,7 @@
 // Small products are bound by what is not overlapped: launch and allocation (2.5 us), the first copies, the
 // last tile's epilogue (1 to 5 us).
 //
-// Every wait gives up after a second; the kernel then sets its status bit, lets its
+// Every wait gives up after a second (that for a sum's end later, by the sum's length); the kernel then sets its status bit, lets its
 // copies land, frees its tensor memory and returns.
 #pragma once
 
@@ -99,9 +99,10 @@ __device__ __forceinline__ unsigned long long now_ns() {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
-// Waits for the phase `parity` of `bar`; false once a wait of this CTA gave up.
+// Waits for the phase `parity` of `bar`; false once a wait of this CTA gave up, after a second and 20 us
+// for each of `steps` ring steps that it may have to wait for (0.3 us is what one takes).
 static __device__ __noinline__ bool barrier_wait_slow(uint32_t bar, uint32_t parity,
-                                                      volatile uint32_t *gave_up) {
+                                                      volatile uint32_t *gave_up, int steps) {
     const unsigned long long t0 = now_ns();
     for (uint32_t i = 1;; ++i) {
         if (barrier_try(bar, parity))
@@ -109,7 +110,7 @@ static __device__ __noinline__ bool barrier_wait_slow(uint32_t bar, uint32_t par
         if ((i & 63u) == 0) {
             if (*gave_up)
                 return false;
-            if (now_ns() - t0 > kProductWaitNs) {
+            if (now_ns() - t0 > kProductWaitNs + 20000ull * static_cast<uint32_t>(steps)) {
                 *gave_up = 1;
                 return false;
             }
@@ -117,8 +118,8 @@ static __device__ __noinline__ bool barrier_wait_slow(uint32_t bar, uint32_t par
     }
 }
 __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity,
-                                             volatile uint32_t *gave_up) {
-    return barrier_try(bar, parity) || barrier_wait_slow(bar, parity, gave_up);
+                                             volatile uint32_t *gave_up, int steps = 0) {
+    return barrier_try(bar, parity) || barrier_wait_slow(bar, parity, gave_up, steps);
 }
 
 // One box of a 4-D tensor into this CTA's shared memory; its bytes count on `bar` of
@@ -191,8 +192,17 @@ __device__ __forceinline__ void sums_load32(uint32_t address, float (&v)[32]) {
     for (int i = 0; i < 32; ++i)
         v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void sums_load_wait() {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// Waits for the loads; `v`, what one of them gave, is not used before.
+__device__ __forceinline__ void sums_ready(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                   "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]),
+                   "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+                   "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                   "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29])
+                 :
+                 : "memory");
+    asm volatile("" : "+f"(v[30]), "+f"(v[31]));
 }
 
 // ------------------------------------------------------------- the kernel
@@ -344,6 +354,7 @@ template <class J> struct Walk {
                 f.b = 0;
                 f.live = live;
                 ahead = J::steps_of(g, f) / max((min(live, g.capacity) + kStep - 1) / kStep, 1);
+                ahead = min(ahead, g.second.batches * each / others + 1);
             }
             const bool other = mine >= left && others;
             int r;
@@ -439,6 +450,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
     if (warp == 0 && elected()) {
         // the first CTA's barrier counts both CTAs' bytes
         const uint32_t first_full = in_first_cta(full);
+        // what the kernels before wrote, to the copies of this one
+        asm volatile("fence.proxy.async.global;" ::: "memory");
         uint32_t slot = 0, phase = 0;
         bool ok = true;
         while (ok && walk.next(&t))
@@ -502,7 +515,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
         uint32_t turn = 0, uses = 0;
         while (walk.next(&t)) {
             const uint32_t half = turn & 1;
-            if (!barrier_wait(sums_full + 8 * half, (turn >> 1) & 1, &s.gave_up))
+            if (!barrier_wait(sums_full + 8 * half, (turn >> 1) & 1, &s.gave_up, t.steps))
                 break;
             sums_fence_after();
             J::finish(g, t, static_cast<int>(rank) * kHalf + quarter * 32 + lane,
@@ -575,7 +588,7 @@ __device__ __forceinline__ void store_tile(uint32_t sums, const Stage &stage, T 
         float v[32];
         uint32_t w[16];
         sums_load32(sums + c, v);
-        sums_load_wait();
+        sums_ready(v);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
             v[i] = zero ? 0.f : v[i] * scale;

@@ -232,6 +232,14 @@ def test_gated_wide_range(ga, dtype):
     _check_gated("gelu", x, w, dy, out, ga.linear_gelu_and_mul_backward(dy, x, w, kept), dtype)
 
 
+@pytest.mark.parametrize("keep", [False, True])
+def test_gated_long_sum(ga, keep):
+    """A sum of 2^20 terms."""
+    x, w, _ = _operands(3, 1 << 20, 8, BF16, 71)
+    out = ga.linear_silu_and_mul(x, w, keep=keep)
+    _check_gated("silu", x, w, None, out[0] if keep else out, None, BF16)
+
+
 def test_gated_zero_sizes(ga):
     x, w, dy = _operands(0, 64, 32, BF16, 0)
     out, kept = ga.linear_silu_and_mul(x, w, keep=True)
