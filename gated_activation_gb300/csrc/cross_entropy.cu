@@ -50,6 +50,17 @@ template <class T> __device__ __forceinline__ uint4 eight(const T *p) {
     return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
 }
 
+// The targets as given: a token's, or -1 where it lies outside the vocabulary.
+struct Targets {
+    const void *data;
+    bool wide;
+    int V;
+    __device__ __forceinline__ int operator[](int i) const {
+        const int64_t v = wide ? static_cast<const int64_t *>(data)[i] : static_cast<const int32_t *>(data)[i];
+        return v >= 0 && v < V ? static_cast<int>(v) : -1;
+    }
+};
+
 // ------------------------------------------------------------------ live tokens
 
 // What live_tokens writes; `row` counts live tokens.
@@ -63,7 +74,7 @@ struct Tokens {
 };
 
 template <class T> struct TokenArgs {
-    const void *targets;
+    Targets target;
     const T *in;
     const float *grad_loss, *lse;   // backward
     float *loss_out, *lse_out;      // forward: 0 at dead tokens
@@ -71,8 +82,8 @@ template <class T> struct TokenArgs {
     T *rows;                        // copies of live rows, zeros up to a whole step
     Tokens t;
     int64_t in_stride;
-    int n, k, kp, V, segment;
-    bool wide, copy;                // copy: also where every token is live
+    int n, k, kp, segment;
+    bool copy;                      // also where every token is live
 };
 
 __device__ __forceinline__ int block_sum_int(int v, int *red) {
@@ -94,11 +105,7 @@ template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<
     __shared__ int list[256];
     pdl_wait();
     pdl_trigger();
-    const auto target = [&](int i) -> int {
-        const int64_t v = g.wide ? static_cast<const int64_t *>(g.targets)[i]
-                                 : static_cast<const int32_t *>(g.targets)[i];
-        return v >= 0 && v < g.V ? static_cast<int>(v) : -1;
-    };
+    const Targets &target = g.target;
     const int begin = blockIdx.x * g.segment, end = min(begin + g.segment, g.n);
     int before = 0, all = 0;
     float top = 0.f;
@@ -108,7 +115,7 @@ template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int i = i0 + 256 * j;
-            goal[j] = i < g.n ? target(i) : -1;
+            goal[j] = i < g.n ? target[i] : -1;
             weight[j] = g.grad_loss && i < g.n ? g.grad_loss[i] : 0.f;
         }
 #pragma unroll
@@ -141,7 +148,7 @@ template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<
     }
     const bool copy = g.copy || all < g.n;
     for (int i0 = begin; i0 < end; i0 += 256) {
-        const int i = i0 + threadIdx.x, goal = i < end ? target(i) : -1;
+        const int i = i0 + threadIdx.x, goal = i < end ? target[i] : -1;
         const bool live = goal >= 0;
         // the rank of a live token among this turn's
         const uint32_t votes = __ballot_sync(0xFFFFFFFFu, live);
@@ -289,7 +296,7 @@ template <class T, int N> struct TurnedStatistics {
     static constexpr int kN = N, kRows = kTile;
     static constexpr Live kLive = Live::Columns;
     struct Args {
-        const int32_t *goal;
+        Targets target;
         float2 *part;        // [capacity, 8 tiles]: maximum, sum of 32 columns
         int tiles;
         float powers;
@@ -301,8 +308,7 @@ template <class T, int N> struct TurnedStatistics {
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
         load_along(a, &g.a, bar, step * kStep, t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
-        load_along(b, t.live < g.capacity ? &g.other : &g.b, bar, step * kStep,
-                   static_cast<int>(rank) * (N / 2), 0, 0);
+        load_along(b, &g.b, bar, step * kStep, static_cast<int>(rank) * (N / 2), 0, 0);
     }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
         static_assert(32 * 17 * 4 <= 32 * kStageRow);
@@ -320,7 +326,7 @@ template <class T, int N> struct TurnedStatistics {
                 __syncwarp();
                 const int token = c + 16 * half + (lane & 15);
                 const bool mine = token < t.live;
-                const int goal = mine ? g.j.goal[token] - first - from : -1;
+                const int goal = (mine ? g.j.target[token] : -1) - first - from;
                 float x[16], top = -INFINITY, sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -496,7 +502,8 @@ template <class T> struct PieceGradients {
 template <class T> struct JoinArgs {
     const float2 *part;
     const T *in, *weight;     // as given: rows in_stride and weight_stride apart
-    Tokens t;
+    Tokens t;                 // count null: every token has a row
+    Targets target;
     float *loss, *lse;
     int64_t in_stride, weight_stride;
     int parts, k;
@@ -512,10 +519,15 @@ template <class T, int WARPS> __global__ void __launch_bounds__(256) join_statis
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = (blockIdx.x * 8 + warp) / WARPS;
     const int thread = warp % WARPS * 32 + lane;
-    if (r >= *g.t.count)
+    if (g.t.count && r >= *g.t.count)
         return;
-    const int token = g.t.token[r];
-    const T *x = g.in + token * g.in_stride, *w = g.weight + g.t.goal[r] * g.weight_stride;
+    const int token = g.t.count ? g.t.token[r] : r, target = g.t.count ? g.t.goal[r] : g.target[r];
+    if (target < 0) {
+        if (thread == 0)
+            g.loss[token] = g.lse[token] = 0.f;
+        return;
+    }
+    const T *x = g.in + token * g.in_stride, *w = g.weight + target * g.weight_stride;
     float2 dot[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
     const int from = g.k & ~7;
     const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 15) == 0;
@@ -660,6 +672,14 @@ Region target_region(const gated_act_vocabulary &a) {
     return {a.targets, static_cast<uint64_t>(a.T * size), static_cast<uintptr_t>(size), false};
 }
 
+Targets targets_of(const gated_act_vocabulary &a) {
+    return {a.targets, a.targets64 != 0, static_cast<int>(a.V)};
+}
+
+// Up to 128 tokens are few: the forward product is turned round, and dead tokens, columns of their own, are
+// left in (nothing of theirs reaches another), so that no kernel has to count them first.
+bool few(const gated_act_vocabulary &a) { return a.T <= 128; }
+
 // Columns of one piece of the vocabulary: as many as give y 256 MB (of which the products that read
 // it find half in L2), but at least 8192, so that adding to grad_in's sums (8 bytes per row and column of it)
 // stays small beside the products; of those a quarter fewer to a quarter more, the number whose tiles come
@@ -732,7 +752,7 @@ struct Parts {
             sums = ws.take<float>(4 * kTile * kTile * most);
         } else {
             // two warps' shares of a tile's columns, or eight of the turned form's
-            part = ws.take<float2>((a.T <= 128 ? 64 : 16) * ceil_div64(a.V, kTile) * a.T);
+            part = ws.take<float2>((few(a) ? 64 : 16) * ceil_div64(a.V, kTile) * a.T);
         }
         rc = GATED_ACT_OK;
         if (!tma_addressable(weight)) {
@@ -750,7 +770,7 @@ int run_live_tokens(const Parts &w, const gated_act_vocabulary &a, const float *
                     const float *lse, float *loss_out, float *lse_out, void *grad_in,
                     cudaStream_t stream) {
     TokenArgs<T> g;
-    g.targets = a.targets;
+    g.target = targets_of(a);
     g.in = static_cast<const T *>(a.in);
     g.grad_loss = grad_loss;
     g.lse = lse;
@@ -763,8 +783,6 @@ int run_live_tokens(const Parts &w, const gated_act_vocabulary &a, const float *
     g.n = static_cast<int>(a.T);
     g.k = static_cast<int>(a.k);
     g.kp = static_cast<int>(w.kp);
-    g.V = static_cast<int>(a.V);
-    g.wide = a.targets64 != 0;
     g.copy = w.copy;
     const int64_t segment = ceil_div64(a.T, 304);   // two blocks per SM count the targets
     g.segment = static_cast<int>(segment < 8 ? 8 : segment);
@@ -805,10 +823,12 @@ template <class T> struct Upright {
 };
 template <class T, int N> struct Turned {
     static int set(Product<TurnedStatistics<T, N>> *g, const Parts &w, const gated_act_vocabulary &a) {
+        g->live = nullptr;
         g->n_tiles = 1;
         g->rows = static_cast<int>(a.V);
-        g->j = {w.t.goal, w.part, static_cast<int>(ceil_div64(a.V, kTile)), powers_of(a.k)};
-        const int rc = encode_rows<T>(&g->b, &g->other, w, N / 2);
+        g->j = {targets_of(a), w.part, static_cast<int>(ceil_div64(a.V, kTile)), powers_of(a.k)};
+        const int rc = encode_map(&g->b, w.copy ? w.packed : w.in, N / 2, std::is_same_v<T, bf16>);
+        g->other = g->b;
         return rc == GATED_ACT_OK ? encode_map(&g->a, w.weight, kHalf, std::is_same_v<T, bf16>) : rc;
     }
     using Job = TurnedStatistics<T, N>;
@@ -828,19 +848,22 @@ int run_forward(float *loss, float *lse, const gated_act_vocabulary &a, void *wo
                 cudaStream_t stream) {
     const Parts w(a, false, workspace, stream);
     int rc = w.rc;
-    if (rc == GATED_ACT_OK)
+    const bool turned = few(a);
+    if (rc == GATED_ACT_OK && !turned)
         rc = run_live_tokens<T>(w, a, nullptr, nullptr, loss, lse, nullptr, stream);
+    if (rc == GATED_ACT_OK && turned && w.copy)
+        rc = launch_pack(packed_layout(w.in, const_cast<void *>(w.packed.data)), w.in, stream);
     if (rc != GATED_ACT_OK)
         return rc;
-    const bool turned = a.T <= 128;
     rc = a.T <= 32 ? run_statistics(Turned<T, 32>{}, w, a, stream)
          : turned  ? run_statistics(Turned<T, 128>{}, w, a, stream)
                    : run_statistics(Upright<T>{}, w, a, stream);
     if (rc != GATED_ACT_OK)
         return rc;
     const int parts = static_cast<int>((turned ? 8 : 2) * ceil_div64(a.V, kTile));
-    const JoinArgs<T> j = {w.part, static_cast<const T *>(a.in), static_cast<const T *>(a.weight), w.t,
-                           loss,   lse, a.in_stride, a.weight_stride, parts, static_cast<int>(a.k)};
+    const JoinArgs<T> j = {w.part, static_cast<const T *>(a.in), static_cast<const T *>(a.weight),
+                           turned ? Tokens{} : w.t, targets_of(a), loss, lse, a.in_stride,
+                           a.weight_stride, parts, static_cast<int>(a.k)};
     // with up to 1024 rows, a block each fills the SMs no better with a warp each
     const bool wide = a.T <= 1024;
     return cuda_status(launch_kernel(wide ? join_statistics<T, 8> : join_statistics<T, 1>,

@@ -379,17 +379,20 @@ Region weight_region(const gated_act_linear &a) {
             2, false};
 }
 
-// An operand that TMA can address: `t` itself, or a copy in the workspace.
-int addressable(Layout *t, Carve *ws, cudaStream_t stream) {
-    if (tma_addressable(*t))
-        return GATED_ACT_OK;
-    void *copy = ws->take<void>(packed_bytes(*t));
-    if (!ws->start)
-        return GATED_ACT_OK;
-    const Layout to = packed_layout(*t, copy);
-    const int rc = launch_pack(to, *t, stream);
-    *t = to;
-    return rc;
+// Operands that TMA can address: as they are, or copies in the workspace.
+int addressable(Operands *o, Carve *ws, cudaStream_t stream) {
+    const bool in = !tma_addressable(o->in), weight = !tma_addressable(o->weight);
+    const Layout none = {};
+    Layout to[2] = {none, none}, from[2] = {none, none};
+    int n = 0;
+    for (Layout *t : {in ? &o->in : nullptr, weight ? &o->weight : nullptr}) {
+        if (!t)
+            continue;
+        from[n] = *t;
+        to[n] = packed_layout(*t, ws->take<void>(packed_bytes(*t)));
+        *t = to[n++];
+    }
+    return n && ws->start ? launch_pack(to[0], from[0], to[1], from[1], stream) : GATED_ACT_OK;
 }
 
 // Rows without a checkpoint have other kernels where they are few: with up to 32 that leave pairs of
@@ -404,8 +407,7 @@ uint64_t forward_bytes(const gated_act_linear &a, bool keep) {
         return 0;
     Operands o = operands(a);
     Carve ws(nullptr);
-    addressable(&o.in, &ws, nullptr);
-    addressable(&o.weight, &ws, nullptr);
+    addressable(&o, &ws, nullptr);
     return ws.used;
 }
 
@@ -466,9 +468,7 @@ int run_forward(void *out, int16_t *codes, uint8_t *scales, const gated_act_line
                  static_cast<int>(a.k), static_cast<int>(a.d), 1},
                 a.E, tma_addressable(o.in) && tma_addressable(o.weight), stream);
     Carve ws(workspace);
-    int rc = addressable(&o.in, &ws, stream);
-    if (rc == GATED_ACT_OK)
-        rc = addressable(&o.weight, &ws, stream);
+    const int rc = addressable(&o, &ws, stream);
     if (rc != GATED_ACT_OK)
         return rc;
     if constexpr (!KEEP) {
@@ -527,9 +527,7 @@ struct BackwardParts {
         Carve ws(workspace);
         rows = ws.take<void>(uint64_t(a.E) * 2 * padded * dp * 2);
         tail = ws.take<void>(a.n_rows ? uint64_t(a.E) * kStep * kp * 2 : 0);
-        rc = addressable(&o.in, &ws, stream);
-        if (rc == GATED_ACT_OK)
-            rc = addressable(&o.weight, &ws, stream);
+        rc = addressable(&o, &ws, stream);
         bytes = ws.used;
     }
     uint64_t bytes;

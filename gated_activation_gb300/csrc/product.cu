@@ -96,13 +96,18 @@ __device__ __forceinline__ uint4 shifted8(uint4 lo, uint4 hi, uint32_t off) {
 // 16-byte boundaries are read as the aligned vectors that hold them (consecutive lanes share these
 // through L1); where one of the two would reach past the tensor's own bytes, and at a row's end, element
 // by element.  Bound by its instructions before the shift was made the warp's (50001 x 1001: 56 us).
-__global__ void __launch_bounds__(256) pack_rows(Layout to, Layout from) {
+// Two tensors share a launch: planes of the grid from `split` on are the second's.
+__global__ void __launch_bounds__(256) pack_rows(Layout to0, Layout from0, Layout to1, Layout from1,
+                                                 int split) {
     pdl_wait();
     pdl_trigger();
+    const bool second = static_cast<int>(blockIdx.z) >= split;
+    const Layout &to = second ? to1 : to0, &from = second ? from1 : from0;
+    const int64_t plane = blockIdx.z - (second ? split : 0);
     const int64_t x = (int64_t(blockIdx.x) * 32 + threadIdx.x) * 8;
     if (x >= to.size[0])
         return;
-    const int64_t z = blockIdx.z % to.size[2], w = blockIdx.z / to.size[2];
+    const int64_t z = plane % to.size[2], w = plane / to.size[2];
     const uintptr_t first = reinterpret_cast<uintptr_t>(from.data);
     const uintptr_t last = first + 2 * static_cast<uintptr_t>(
         (from.size[1] - 1) * from.stride[1] + (from.size[2] - 1) * from.stride[2] +
@@ -113,7 +118,7 @@ __global__ void __launch_bounds__(256) pack_rows(Layout to, Layout from) {
     const uint16_t *p = static_cast<const uint16_t *>(from.data) + z * from.stride[2] +
                         w * from.stride[3] + r * from.stride[1] + x;
     uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(to.data)) +
-                    (blockIdx.z * to.size[1] + r) * to.stride[1] + x;
+                    (plane * to.size[1] + r) * to.stride[1] + x;
 #pragma unroll 2
     for (; r < to.size[1]; r += step, p += step * from.stride[1], out += step * to.stride[1]) {
         const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
@@ -132,13 +137,23 @@ __global__ void __launch_bounds__(256) pack_rows(Layout to, Layout from) {
     }
 }
 
-int launch_pack(const Layout &to, const Layout &from, cudaStream_t stream) {
-    const int64_t planes = to.size[2] * to.size[3], blocks = ceil_div64(to.size[1], 16);
-    if (to.size[1] * planes == 0)
+int launch_pack(const Layout &to0, const Layout &from0, const Layout &to1, const Layout &from1,
+                cudaStream_t stream) {
+    const auto planes = [](const Layout &t) { return t.size[1] ? t.size[2] * t.size[3] : 0; };
+    const int64_t n0 = planes(to0), n1 = planes(to1);
+    const int64_t wide = to0.size[0] > to1.size[0] ? to0.size[0] : to1.size[0];
+    const int64_t high = ceil_div64(to0.size[1] > to1.size[1] ? to0.size[1] : to1.size[1], 16);
+    if (n0 + n1 == 0)
         return GATED_ACT_OK;
-    const dim3 grid(static_cast<unsigned>(ceil_div64(to.size[0], 256)),
-                    static_cast<unsigned>(blocks < 32768 ? blocks : 32768), static_cast<unsigned>(planes));
-    return cuda_status(launch_kernel(pack_rows, grid, dim3(32, 8), 0, stream, 1, to, from));
+    const dim3 grid(static_cast<unsigned>(ceil_div64(wide, 256)),
+                    static_cast<unsigned>(high < 32768 ? high : 32768), static_cast<unsigned>(n0 + n1));
+    return cuda_status(launch_kernel(pack_rows, grid, dim3(32, 8), 0, stream, 1, to0, from0, to1, from1,
+                                     static_cast<int>(n0)));
+}
+
+int launch_pack(const Layout &to, const Layout &from, cudaStream_t stream) {
+    const Layout none = {};
+    return launch_pack(to, from, none, none, stream);
 }
 
 }  // namespace gact

@@ -616,8 +616,10 @@ Layout packed_layout(const Layout &t, void *data);
 inline uint64_t packed_bytes(const Layout &t) {
     return static_cast<uint64_t>(ceil_div64(t.size[0], 8)) * 16 * t.size[1] * t.size[2] * t.size[3];
 }
-// Copies `from` into `to`, a packed_layout of it; the padding is zeros.
+// Copies `from` into `to`, a packed_layout of it (and a second pair in the same launch); the padding is zeros.
 int launch_pack(const Layout &to, const Layout &from, cudaStream_t stream);
+int launch_pack(const Layout &to0, const Layout &from0, const Layout &to1, const Layout &from1,
+                cudaStream_t stream);
 
 // check_regions, and no buffer in host memory.
 int check_device_regions(Region *r, int n);
