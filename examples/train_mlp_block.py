@@ -1,10 +1,12 @@
 """Training steps of a mixture-of-experts MLP block on the library's operators.
 
-    python examples/train_mlp_block.py [--steps 20] [--activation silu|gelu|sparse]
+    python examples/train_mlp_block.py [--steps 20] [--activation silu|gelu|sparse|fused]
 
 Layer norm, a router with its balance loss, and experts whose gated activation keeps its
 input in 8 bits: the block's forward pass, its backward pass written out, and a plain
-gradient step.  The matrix products are PyTorch's.  What the forward pass keeps of each
+gradient step.  The matrix products are PyTorch's, but for those of ``fused``: there the
+up projections of all experts, their silu gates and the live row counts are one call of
+linear_silu_and_mul, and their gradients one of its backward pass.  What the forward pass keeps of each
 expert's activation is the 8-bit checkpoint alone: the activation's output, which the down
 projection's weight gradient reads, is computed from it again by the backward pass.  An
 expert's rows lie in a buffer of fixed capacity, and the balance loss's per-expert counts
@@ -51,7 +53,9 @@ class Block:
             "norm_weight": torch.ones(w, device=device),
             "norm_bias": torch.zeros(w, device=device),
             "router": normal(w, e, scale=w ** -0.5),
-            "up": normal(e, w, 2 * d, scale=w ** -0.5),
+            # as a linear layer has it, rows of outputs, for the fused products
+            "up": normal(e, 2 * d, w, scale=w ** -0.5) if activation == "fused"
+            else normal(e, w, 2 * d, scale=w ** -0.5),
             "down": normal(e, d, w, scale=d ** -0.5),
         }
 
@@ -84,12 +88,17 @@ class Block:
         token = torch.arange(s.tokens, device=x.device)[:, None].expand_as(ids)
         rows[ids, place] = normed[token]
 
-        hidden = torch.bmm(rows, p["up"])
-        kept, moved = [], x.new_zeros(s.experts, s.tokens, s.width)
-        for e in range(s.experts):
-            out, checkpoint = self._activate(hidden[e], balance.counts[e:e + 1])
-            kept.append(checkpoint)
-            moved[e] = self._live(out, balance, e) @ p["down"][e]
+        if self.activation == "fused":
+            out, checkpoint = ga.linear_silu_and_mul(rows, p["up"], n_rows=balance.counts, keep=True,
+                                                     out=x.new_zeros(s.experts, s.tokens, s.d))
+            kept, moved = (out, checkpoint), torch.bmm(out, p["down"])
+        else:
+            hidden = torch.bmm(rows, p["up"])
+            kept, moved = [], x.new_zeros(s.experts, s.tokens, s.width)
+            for e in range(s.experts):
+                out, checkpoint = self._activate(hidden[e], balance.counts[e:e + 1])
+                kept.append(checkpoint)
+                moved[e] = self._live(out, balance, e) @ p["down"][e]
         y = x + (moved[ids, place].float() * share[..., None]).sum(1).to(x.dtype)
         return y, balance.loss, (x, normed, mean, rstd, logits, ids, balance, share, place, token,
                                  rows, moved, kept)
@@ -112,8 +121,14 @@ class Block:
         grad_moved[ids, place] = (per_choice * share[..., None]).to(x.dtype)
 
         # the experts
-        grad_rows = torch.empty_like(rows)
-        for e in range(s.experts):
+        grad_rows = torch.zeros_like(rows)
+        if self.activation == "fused":
+            out, checkpoint = kept
+            grads["down"] = torch.bmm(out.mT, grad_moved)
+            grad_rows, grads["up"] = ga.linear_silu_and_mul_backward(
+                torch.bmm(grad_moved, p["down"].mT), rows, p["up"], checkpoint,
+                n_rows=balance.counts, grad_in=grad_rows)
+        for e in range(0 if self.activation == "fused" else s.experts):
             n = balance.counts[e:e + 1]
             grad_hidden, again = self._activate_backward(grad_moved[e] @ p["down"][e].T, kept[e], n)
             grads["down"][e] = self._live(again, balance, e).T @ grad_moved[e]
@@ -161,6 +176,6 @@ def train(steps: int = 20, activation: str = "silu", shape: Shape = Shape(), lr:
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=20)
-    ap.add_argument("--activation", choices=("silu", "gelu", "sparse"), default="silu")
+    ap.add_argument("--activation", choices=("silu", "gelu", "sparse", "fused"), default="silu")
     args = ap.parse_args()
     train(args.steps, args.activation, report=print)

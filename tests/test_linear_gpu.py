@@ -508,6 +508,44 @@ def test_runs_together(ga):
         assert all(torch.equal(a, b) for a, b in zip(held, result))
 
 
+def test_block_of_experts(ga):
+    """examples/train_mlp_block.py with its experts' products fused: gradients against autograd of
+    the same block in 64 bits, and a few training steps."""
+    import importlib
+    example = importlib.import_module("examples.train_mlp_block")
+    s = example.Shape(tokens=96, width=64, d=48, experts=4, k=2)
+    block = example.Block(s, "fused", seed=3)
+    x = _randn(s.tokens, s.width, seed=5).to(BF16)
+    grad_y = _randn(s.tokens, s.width, seed=6).to(BF16)
+    y, loss, saved = block.forward(x)
+    grad_x, grads = block.backward(grad_y, torch.full((1,), 2.0, device="cuda"), saved)
+
+    p = {k: v.double().requires_grad_() for k, v in block.params.items()}
+    xr, ids = x.double().requires_grad_(), saved[5]
+    normed = torch.nn.functional.layer_norm(xr, (s.width,), p["norm_weight"], p["norm_bias"], 1e-5)
+    full = torch.softmax(normed @ p["router"], 1)
+    ref = xr
+    for j in range(s.k):
+        e = ids[:, j]
+        h = torch.einsum("tw,tdw->td", normed, p["up"][e])
+        a = torch.nn.functional.silu(h[:, :s.d]) * h[:, s.d:]
+        ref = ref + full.gather(1, e[:, None]) * torch.einsum("td,tdw->tw", a, p["down"][e])
+    counts = torch.bincount(ids.reshape(-1), minlength=s.experts).double()
+    balance = s.coef * s.experts * (counts / (s.tokens * s.k) * full.mean(0)).sum()
+    ((ref * grad_y.double()).sum() + 2 * balance).backward()
+
+    def off(a, b):
+        return ((a.double() - b).norm() / b.norm()).item()
+
+    # eight bf16 roundings of half a step lie on the way of a gradient through the block (its input,
+    # the products and their operands), in norm at most 8 x 2^-8 with none of them cancelled
+    assert off(y, ref.detach()) < 8 * 2.0 ** -8 and off(loss, balance.detach().view(1)) < 0.01
+    assert off(grad_x, xr.grad) < 8 * 2.0 ** -8
+    for name, value in p.items():
+        assert off(grads[name], value.grad) < 8 * 2.0 ** -8, name
+    assert len(example.train(steps=3, activation="fused", shape=s)) == 3
+
+
 def test_many_passes_in_a_row(ga):
     """Kernels of one and two CTAs per SM pair behind each other without a pause, some of them on
     a part of the SMs: 1500 launches of products."""
