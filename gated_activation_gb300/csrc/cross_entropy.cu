@@ -471,7 +471,7 @@ template <class T> struct PieceGradients {
         const bool mine = r < t.rows;
         if (t.second) {
             const int top = t.m0 + (row & ~31);
-            store_tile(sums, stage, g.j.grad_weight + int64_t(top) * k + col, k, t.rows - top, k - col,
+            store_tile<kTile>(sums, stage, g.j.grad_weight + int64_t(top) * k + col, k, t.rows - top, k - col,
                               g.j.vec, *g.j.power * (1.f / kLift<T>), t.steps == 0);
             return;
         }

@@ -61,10 +61,10 @@ __device__ __forceinline__ uint32_t encode32(uint32_t (&w)[16], const float (&v)
 // 280 us alone, 94% of cuBLAS's rate and more), by the epilogue where it is short: per element one exponential, one
 // reciprocal and, for the checkpoint, a maximum, a product and three rounds through shared memory, 4 to
 // 5 us for a tile of 128 x 128 per CTA (8 warps), against 5 ns per summed element in the main loop.
-template <class Act, class T, bool KEEP> struct Forward {
+template <class Act, class T, int N, bool KEEP> struct Forward {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
-    static constexpr int kN = kTile, kRows = kTile;
+    static constexpr int kN = N, kRows = kTile;
     static constexpr Live kLive = Live::Rows;
     struct Args {
         T *out;
@@ -80,7 +80,7 @@ template <class Act, class T, bool KEEP> struct Forward {
                                 uint32_t b, uint32_t bar) {
         load_along(a, &g.a, bar, step * kStep, t.m0 + static_cast<int>(rank) * kHalf, 0, t.b);
         // the first CTA brings the gate's rows of the weight, the second the up half's
-        load_along(b, &g.b, bar, step * kStep, t.n0 * kHalf, static_cast<int>(rank), t.b);
+        load_along(b, &g.b, bar, step * kStep, t.n0 * (N / 2), static_cast<int>(rank), t.b);
     }
     __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
@@ -88,11 +88,11 @@ template <class Act, class T, bool KEEP> struct Forward {
         const bool mine = r < t.rows;
         const int lane = threadIdx.x & 31, rows = t.rows - (r - lane);   // of the warp
         const int64_t at = int64_t(t.b) * g.capacity + r, top = at - lane;
-        for (int c = 32 * stage.part; c < kHalf && t.n0 * kHalf + c < d; c += 64) {
-            const int col = t.n0 * kHalf + c, n = d - col;
+        for (int c = 32 * stage.part; c < N / 2 && t.n0 * (N / 2) + c < d; c += 64) {
+            const int col = t.n0 * (N / 2) + c, n = d - col;
             float gate[32], up[32];
             sums_load32(sums + c, gate);
-            sums_load32(sums + kHalf + c, up);
+            sums_load32(sums + N / 2 + c, up);
             sums_ready(gate);
             sums_ready(up);
             uint32_t w[16];
@@ -189,10 +189,10 @@ template <class Act, class T, int N> struct Swapped {
 // a copy with zeros there, as what lies past the live rows may be anything.
 // 8 T k d operations in one launch: 4096 rows of 4096 -> 8192 in 560 us alone (1.96 PFLOP/s; two launches 620),
 // 32 experts of 2048 -> 768, 70% of 1024 rows, 167 us (1.73 PFLOP/s of the live rows).
-template <class T> struct Gradients {
+template <class T, int N> struct Gradients {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = true, kSecond = true;
-    static constexpr int kN = kTile, kRows = kTile;
+    static constexpr int kN = N, kRows = kTile;
     static constexpr Live kLive = Live::Rows;
     struct Args {
         CUtensorMap rows, in, tail;   // of the second product
@@ -206,23 +206,23 @@ template <class T> struct Gradients {
     __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
-        const int row = t.m0 + static_cast<int>(rank) * kHalf, col = t.n0 * kTile + static_cast<int>(rank) * kHalf;
+        const int row = t.m0 + static_cast<int>(rank) * kHalf, col = t.n0 * N + static_cast<int>(rank) * (N / 2);
         if (!t.second) {
             const int half = step >= g.j.half_steps, x = (step - half * g.j.half_steps) * kStep;
             load_along(a, &g.a, bar, x, row, half, t.b);
-            load_across(b, &g.b, bar, x, col, half, t.b);
+            load_across<N / 2>(b, &g.b, bar, x, col, half, t.b);
             return;
         }
         const int x = step * kStep, e = t.b >> 1;
         load_across(a, &g.j.rows, bar, x, row, t.b & 1, e);
         const bool tail = x + kStep > t.live && t.live < g.capacity;
-        load_across(b, tail ? &g.j.tail : &g.j.in, bar, tail ? 0 : x, col, 0, e);
+        load_across<N / 2>(b, tail ? &g.j.tail : &g.j.in, bar, tail ? 0 : x, col, 0, e);
     }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
-        const int k = g.j.k, top = t.m0 + (row & ~31), col = t.n0 * kTile;   // the warp's first row
+        const int k = g.j.k, top = t.m0 + (row & ~31), col = t.n0 * N;   // the warp's first row
         T *to = t.second ? g.j.grad_weight + (int64_t(t.b) * g.second.rows + top) * k + col
                          : g.j.grad_in + (int64_t(t.b) * g.capacity + top) * k + col;
-        store_tile(sums, stage, to, k, t.rows - top, k - col, t.second ? g.j.vec_weight : g.j.vec_in,
+        store_tile<N>(sums, stage, to, k, t.rows - top, k - col, t.second ? g.j.vec_weight : g.j.vec_in,
                    1.f, t.steps == 0);
     }
 };
@@ -365,7 +365,7 @@ int check_sizes(const gated_act_linear &a) {
                    static_cast<double>(ceil_div64(cols, width)) <
                static_cast<double>(most);
     };
-    if (!tiles(a.T, a.d, kHalf) || !tiles(a.T + 2 * a.d + kTile, a.k, kTile) ||
+    if (!tiles(a.T, a.d, 64) || !tiles(a.T + 2 * a.d + kTile, a.k, kHalf) ||
         static_cast<double>(a.E) * static_cast<double>(a.T + kStep) *
                 static_cast<double>(2 * a.d + a.k) > 1e17)
         return GATED_ACT_ERR_TOO_LARGE;
@@ -412,6 +412,52 @@ uint64_t forward_bytes(const gated_act_linear &a, bool keep) {
     return ws.used;
 }
 
+// Columns of a tile, 256 or 128: those for which the pair of SMs with the most work has less of it.  Work is
+// counted in ring steps of 256 columns (0.30 us); a step of 128 is 0.59 of one in the forward product and
+// 0.68 in the gradients', both operands of which lie across the sum (2048 x 4096 -> 16384: 274 and 323 us
+// forward, 560 and 780 backward).  A tile is not done before the one in front of it has left through
+// its epilogue: 11 steps of 256 columns (with the checkpoint 21, a gradient 9), 7.4 (11, 6) of 128.
+// Measured where it decides: 512 x 4096 -> 2048 forward 23.2 us with 256 columns and 14.8 with 128, 256 x 2048 -> 9728
+// 16.5 and 17.5, backward 98.5 and 70.6, 512 x 4096 -> 2048 backward 29.2 and 40.8.
+double tile_steps(int64_t steps, double share, double epilogue) {
+    const double n = share * static_cast<double>(steps);
+    return n < epilogue ? epilogue : n;
+}
+
+int forward_columns(const gated_act_linear &a, bool keep) {
+    const int64_t tall = a.E * ceil_div64(a.T, kTile), steps = ceil_div64(a.k, kStep), pairs = sm_pairs();
+    const auto turns = [&](int64_t n) {
+        return static_cast<double>(ceil_div64(tall * ceil_div64(2 * a.d, n), pairs));
+    };
+    return turns(128) * tile_steps(steps, 0.59, keep ? 11 : 7.4) < turns(256) * tile_steps(steps, 1, keep ? 21 : 11)
+               ? 128
+               : 256;
+}
+
+int gradient_columns(const gated_act_linear &a) {
+    const int64_t pairs = sm_pairs(), in_steps = 2 * ceil_div64(a.d, kStep), w_steps = ceil_div64(a.T, kStep);
+    // the walk's own division of the two products' tiles among the pairs
+    const auto busiest = [&](int64_t n, double share, double epilogue) {
+        const int64_t wide = ceil_div64(a.k, n), first = a.E * ceil_div64(a.T, kTile) * wide;
+        const int64_t second = 2 * a.E * ceil_div64(a.d, kTile) * wide;
+        const int64_t left = first % pairs, others = left ? pairs - left : 0, ahead = in_steps / w_steps;
+        const int64_t taken = second < ahead * others ? second : ahead * others, rest = second - taken;
+        const double f = tile_steps(in_steps, share, epilogue), w = tile_steps(w_steps, share, epilogue);
+        // the pairs in the order in which they take the rest: those with fewer first tiles in front
+        const auto load = [&](int64_t firsts, int64_t place, int64_t before) {
+            return static_cast<double>(firsts) * f +
+                   static_cast<double>(before + rest / pairs + (place < rest % pairs)) * w;
+        };
+        double most = load(first / pairs, 0, others ? ceil_div64(taken, others) : 0);
+        if (left) {
+            const double more = load(first / pairs + 1, others, 0);
+            most = more > most ? more : most;
+        }
+        return most;
+    };
+    return busiest(128, 0.68, 6) < busiest(256, 1, 9) ? 128 : 256;
+}
+
 // The parts of a forward product that its jobs share.
 template <class J> int set_forward(Product<J> *g, const gated_act_linear &a, const int32_t *live) {
     g->other = g->a;
@@ -422,19 +468,19 @@ template <class J> int set_forward(Product<J> *g, const gated_act_linear &a, con
     return GATED_ACT_OK;
 }
 
-template <class Act, class T, bool KEEP>
+template <class Act, class T, int N, bool KEEP>
 int run_product(void *out, int16_t *codes, uint8_t *scales, const gated_act_linear &a, const Operands &o,
                 const int32_t *live, cudaStream_t stream) {
     constexpr bool is_bf16 = std::is_same_v<T, bf16>;
-    Product<Forward<Act, T, KEEP>> g;
+    Product<Forward<Act, T, N, KEEP>> g;
     int rc = encode_map(&g.a, o.in, kHalf, is_bf16);
     if (rc == GATED_ACT_OK)
-        rc = encode_map(&g.b, o.weight, kHalf, is_bf16);
+        rc = encode_map(&g.b, o.weight, N / 2, is_bf16);
     if (rc != GATED_ACT_OK)
         return rc;
     set_forward(&g, a, live);
     g.rows = static_cast<int>(a.T);
-    g.n_tiles = static_cast<int>(ceil_div64(a.d, kHalf));
+    g.n_tiles = static_cast<int>(ceil_div64(a.d, N / 2));
     g.j = {static_cast<T *>(out), codes, scales, static_cast<int>(a.d),
            a.d % 8 == 0 && aligned(out, 16) && aligned(codes, 16)};
     return launch_product(g, a.E * ceil_div64(a.T, kTile) * g.n_tiles, stream);
@@ -478,7 +524,9 @@ int run_forward(void *out, int16_t *codes, uint8_t *scales, const gated_act_line
         if (a.T <= 128)
             return run_swapped<Act, T, 128>(out, a, o, live, stream);
     }
-    return run_product<Act, T, KEEP>(out, codes, scales, a, o, live, stream);
+    return forward_columns(a, KEEP) == 256
+               ? run_product<Act, T, 256, KEEP>(out, codes, scales, a, o, live, stream)
+               : run_product<Act, T, 128, KEEP>(out, codes, scales, a, o, live, stream);
 }
 
 template <class Act>
@@ -534,11 +582,11 @@ struct BackwardParts {
     uint64_t bytes;
 };
 
-template <class T>
+template <class T, int N>
 int run_gradients(void *grad_in, void *grad_weight, const gated_act_linear &a, const Layout &rows,
                   const Operands &o, const Layout &tail, cudaStream_t stream) {
     constexpr bool is_bf16 = std::is_same_v<T, bf16>;
-    Product<Gradients<T>> g;
+    Product<Gradients<T, N>> g;
     int rc = encode_map(&g.a, rows, kHalf, is_bf16);
     if (rc == GATED_ACT_OK)
         rc = encode_map(&g.b, o.weight, kStep, is_bf16);
@@ -554,7 +602,7 @@ int run_gradients(void *grad_in, void *grad_weight, const gated_act_linear &a, c
     g.live = a.n_rows;
     g.batches = static_cast<int>(a.E);
     g.capacity = g.rows = static_cast<int>(a.T);
-    g.n_tiles = static_cast<int>(ceil_div64(a.k, kTile));
+    g.n_tiles = static_cast<int>(ceil_div64(a.k, N));
     g.j.half_steps = static_cast<int>(ceil_div64(a.d, kStep));
     g.steps = 2 * g.j.half_steps;
     g.second.batches = static_cast<int>(2 * a.E);
@@ -615,7 +663,9 @@ int run_backward(void *grad_in, void *grad_weight, const void *grad_out, int64_t
                          {1, w.dp, w.padded * w.dp, 2 * w.padded * w.dp}};
     const Layout tail = {w.tail, {a.k, kStep, 1, a.E}, {1, w.kp, 0, kStep * w.kp}};
 
-    return run_gradients<T>(grad_in, grad_weight, a, rows, w.o, tail, stream);
+    return gradient_columns(a) == 256
+               ? run_gradients<T, 256>(grad_in, grad_weight, a, rows, w.o, tail, stream)
+               : run_gradients<T, 128>(grad_in, grad_weight, a, rows, w.o, tail, stream);
 }
 
 template <class Act>

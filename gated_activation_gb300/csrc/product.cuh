@@ -557,11 +557,14 @@ __device__ __forceinline__ void load_along(uint32_t dst, const CUtensorMap *map,
                                            int x, int row, int z, int w) {
     box_load(dst, map, bar, x, row, z, w);
 }
-// The same of 128 rows of an operand whose rows lie across the sum.
+// The same of `ROWS` (64 or 128) rows of an operand whose rows lie across the sum.
+template <int ROWS = kHalf>
 __device__ __forceinline__ void load_across(uint32_t dst, const CUtensorMap *map, uint32_t bar,
                                             int x, int row, int z, int w) {
+    static_assert(ROWS == 64 || ROWS == 128);
     box_load(dst, map, bar, row, x, z, w);
-    box_load(dst + kStep * 128, map, bar, row + 64, x, z, w);
+    if (ROWS == 128)
+        box_load(dst + kStep * 128, map, bar, row + 64, x, z, w);
 }
 
 template <class T> __device__ __forceinline__ uint32_t pack2(float2 v);
@@ -581,10 +584,10 @@ template <class T> __device__ __forceinline__ void pack32(uint32_t (&w)[16], con
 // The epilogue of a plain product: every column of the tile below `columns`, times `scale`, rounded
 // to T, into the warp's first `rows` rows at `to`, `stride` apart.  A sum without terms is 0 whatever
 // tensor memory holds.
-template <class T>
+template <int N, class T>
 __device__ __forceinline__ void store_tile(uint32_t sums, const Stage &stage, T *to, int64_t stride, int rows,
                                            int columns, bool vec, float scale, bool zero) {
-    for (int c = 32 * stage.part; c < kTile && c < columns; c += 64) {
+    for (int c = 32 * stage.part; c < N && c < columns; c += 64) {
         float v[32];
         uint32_t w[16];
         sums_load32(sums + c, v);

@@ -574,6 +574,40 @@ def test_two_streams_at_once(ga):
         assert all(torch.equal(a, b) for a, b in zip(g, (want, *grads)))
 
 
+def test_threads(ga):
+    """Calls from three threads at once, each on a stream of its own."""
+    import threading
+    x, w, dy = _operands(200, 130, 96, BF16, 65)
+    goal = torch.randint(192, (200,), generator=_gen(66), device="cuda")
+    gl = torch.ones(200, device="cuda")
+
+    def work():
+        out, kept = ga.linear_silu_and_mul(x, w, keep=True)
+        ce = ga.linear_cross_entropy(x, w, goal)
+        return (out, *ga.linear_silu_and_mul_backward(dy, x, w, kept), ce.loss,
+                *ga.linear_cross_entropy_backward(gl, x, w, goal, ce))
+
+    want, got = work(), []
+    torch.cuda.synchronize()
+
+    def run():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(50):
+                result = work()
+        stream.synchronize()
+        got.append(result)
+
+    threads = [threading.Thread(target=run) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(got) == 3
+    for result in got:
+        assert all(torch.equal(a, b) for a, b in zip(result, want))
+
+
 def test_two_graphs(ga):
     """Two captured graphs, replayed in turn and on two streams at once."""
     sets = [_operands(300, 200, 130, BF16, 90 + i) for i in range(2)]
