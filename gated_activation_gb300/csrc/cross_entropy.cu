@@ -242,7 +242,7 @@ template <class T> struct Statistics {
         float powers;
     };
     using G = Product<Statistics>;
-    __device__ static int batch_of(int, bool) { return 0; }
+    __device__ static int batch_of(const G &, int, bool) { return 0; }
     __device__ static int batches(const G &g) { return g.batches; }
     __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
@@ -302,7 +302,7 @@ template <class T, int N> struct TurnedStatistics {
         float powers;
     };
     using G = Product<TurnedStatistics>;
-    __device__ static int batch_of(int, bool) { return 0; }
+    __device__ static int batch_of(const G &, int, bool) { return 0; }
     __device__ static int batches(const G &g) { return g.batches; }
     __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
@@ -367,7 +367,7 @@ template <class T> struct Slopes {
         float powers;
     };
     using G = Product<Slopes>;
-    __device__ static int batch_of(int, bool) { return 0; }
+    __device__ static int batch_of(const G &, int, bool) { return 0; }
     __device__ static int batches(const G &g) { return g.batches; }
     __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
@@ -444,7 +444,7 @@ template <class T> struct PieceGradients {
         bool begin, vec;
     };
     using G = Product<PieceGradients>;
-    __device__ static int batch_of(int, bool) { return 0; }
+    __device__ static int batch_of(const G &, int, bool) { return 0; }
     __device__ static int batches(const G &g) { return g.j.shares(g.live_of(0)); }
     // shares of whole steps, as even as they get
     __device__ static int first_step(const G &g, const Tile &t, int b) {
@@ -603,7 +603,7 @@ template <class T> struct GradInArgs {
 };
 
 // grad_in's rows from the shares of their sums: a block takes 32 rows x 64 columns of a tile, reads
-// columns (eight loads on their way per thread) and writes rows.
+// columns (32 loads on their way per thread) and writes rows.
 template <class T> __global__ void __launch_bounds__(256) join_grad_in(GradInArgs<T> g) {
     __shared__ float held[64][33];
     pdl_wait();
@@ -621,6 +621,7 @@ template <class T> __global__ void __launch_bounds__(256) join_grad_in(GradInArg
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         v[i] = 0.f;
+#pragma unroll 4
     for (int s = 0; s < shares; ++s)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {

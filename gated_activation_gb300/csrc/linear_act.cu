@@ -74,7 +74,7 @@ template <class Act, class T, int N, bool KEEP> struct Forward {
         bool vec;
     };
     using G = Product<Forward>;
-    __device__ static int batch_of(int b, bool) { return b; }
+    __device__ static int batch_of(const G &, int b, bool) { return b; }
     __device__ static int batches(const G &g) { return g.batches; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
@@ -131,7 +131,7 @@ template <class Act, class T, int N> struct Swapped {
         T *out;
     };
     using G = Product<Swapped>;
-    __device__ static int batch_of(int b, bool) { return b; }
+    __device__ static int batch_of(const G &, int b, bool) { return b; }
     __device__ static int batches(const G &g) { return g.batches; }
     __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
@@ -187,9 +187,11 @@ template <class Act, class T, int N> struct Swapped {
 // Second, grad_weight: A = (dg, du) across the sum over the rows, B = in across it; batch 2e + half.
 // Past the live rows dg and du are zeros up to a whole step; the last rows of `in` come from
 // a copy with zeros there, as what lies past the live rows may be anything.
+// SPLIT: the first product's sums are divided into shares, fp32 tiles as the threads hold them (256 x 256,
+// column after column), which join_shares adds up.
 // 8 T k d operations in one launch: 4096 rows of 4096 -> 8192 in 560 us alone (1.96 PFLOP/s; two launches 620),
 // 32 experts of 2048 -> 768, 70% of 1024 rows, 167 us (1.73 PFLOP/s of the live rows).
-template <class T, int N> struct Gradients {
+template <class T, int N, bool SPLIT> struct Gradients {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = true, kSecond = true;
     static constexpr int kN = N, kRows = kTile;
@@ -197,20 +199,31 @@ template <class T, int N> struct Gradients {
     struct Args {
         CUtensorMap rows, in, tail;   // of the second product
         T *grad_in, *grad_weight;
-        int k, half_steps;            // ring steps of one half of the first sum
+        float *sums;                  // SPLIT: [E, shares, tile rows, tile columns, 256, 256]
+        int k, half_steps, shares;    // ring steps of one half of the first sum
         bool vec_in, vec_weight;
     };
     using G = Product<Gradients>;
-    __device__ static int batch_of(int b, bool second) { return second ? b >> 1 : b; }
+    __device__ static int batch_of(const G &g, int b, bool second) {
+        return second ? b >> 1 : SPLIT ? b / g.j.shares : b;
+    }
     __device__ static int batches(const G &g) { return g.batches; }
-    __device__ static int steps_of(const G &g, const Tile &) { return g.steps; }
+    // shares of whole steps, as even as they get
+    __device__ static int first_step(const G &g, int b) {
+        return SPLIT ? static_cast<int>(int64_t(g.steps) * (b % g.j.shares) / g.j.shares) : 0;
+    }
+    __device__ static int steps_of(const G &g, const Tile &t) {
+        return SPLIT ? (t.b % g.j.shares == g.j.shares - 1 ? g.steps : first_step(g, t.b + 1)) - first_step(g, t.b)
+                     : g.steps;
+    }
     __device__ static void load(const G &g, const Tile &t, int step, uint32_t rank, uint32_t a,
                                 uint32_t b, uint32_t bar) {
         const int row = t.m0 + static_cast<int>(rank) * kHalf, col = t.n0 * N + static_cast<int>(rank) * (N / 2);
         if (!t.second) {
-            const int half = step >= g.j.half_steps, x = (step - half * g.j.half_steps) * kStep;
-            load_along(a, &g.a, bar, x, row, half, t.b);
-            load_across<N / 2>(b, &g.b, bar, x, col, half, t.b);
+            const int at = first_step(g, t.b) + step, e = batch_of(g, t.b, false);
+            const int half = at >= g.j.half_steps, x = (at - half * g.j.half_steps) * kStep;
+            load_along(a, &g.a, bar, x, row, half, e);
+            load_across<N / 2>(b, &g.b, bar, x, col, half, e);
             return;
         }
         const int x = step * kStep, e = t.b >> 1;
@@ -220,12 +233,75 @@ template <class T, int N> struct Gradients {
     }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
         const int k = g.j.k, top = t.m0 + (row & ~31), col = t.n0 * N;   // the warp's first row
+        if (SPLIT && !t.second) {
+            const int64_t tall = (g.capacity + kTile - 1) / kTile;
+            const int64_t tile = (t.b * tall + t.m0 / kTile) * g.n_tiles + t.n0;
+            float *held = g.j.sums + tile * (kTile * kTile) + 32 * stage.part * kTile + row;
+            for (int c = 32 * stage.part; c < kTile && col + c < k; c += 64, held += 64 * kTile) {
+                float v[32];
+                sums_load32(sums + c, v);
+                sums_ready(v);
+                if (t.m0 + row < t.rows)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        held[i * kTile] = v[i];
+            }
+            return;
+        }
         T *to = t.second ? g.j.grad_weight + (int64_t(t.b) * g.second.rows + top) * k + col
                          : g.j.grad_in + (int64_t(t.b) * g.capacity + top) * k + col;
         store_tile<N>(sums, stage, to, k, t.rows - top, k - col, t.second ? g.j.vec_weight : g.j.vec_in,
                    1.f, t.steps == 0);
     }
 };
+
+template <class T> struct ShareArgs {
+    const float *sums;
+    T *out;
+    const int32_t *live;
+    int capacity, k, shares;
+};
+
+// grad_in's rows from the shares of their sums: a block takes 32 rows x 64 columns of a tile, reads columns
+// (32 loads on their way per thread) and writes rows.
+template <class T> __global__ void __launch_bounds__(256) join_shares(ShareArgs<T> g) {
+    __shared__ float held[64][33];
+    pdl_wait();
+    pdl_trigger();
+    const int wide = (g.k + 63) / 64, high = (g.capacity + 31) / 32;
+    const int e = static_cast<int>(blockIdx.x / (wide * high)), at = static_cast<int>(blockIdx.x % (wide * high));
+    const int r0 = at / wide * 32, c0 = at % wide * 64;
+    const int live = g.live ? min(max(g.live[e], 0), g.capacity) : g.capacity;
+    if (r0 >= live)
+        return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tall = (g.capacity + kTile - 1) / kTile, tiles = tall * ((g.k + kTile - 1) / kTile);
+    const int64_t part = int64_t(tiles) * (kTile * kTile);
+    const float *from = g.sums + e * g.shares * part +
+                        (int64_t(r0 / kTile) * ((g.k + kTile - 1) / kTile) + c0 / kTile) * (kTile * kTile) +
+                        (c0 % kTile) * kTile + r0 % kTile + lane;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < g.shares; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = warp + 8 * i;
+            if (r0 + lane < live && c0 + c < g.k)
+                v[i] += from[s * part + c * kTile];
+        }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        held[warp + 8 * i][lane] = v[i];
+    __syncthreads();
+    for (int i = warp; i < 32 && r0 + i < live; i += 8) {
+        T *to = g.out + (int64_t(e) * g.capacity + r0 + i) * g.k + c0;
+        for (int c = lane; c < 64 && c0 + c < g.k; c += 32)
+            to[c] = from_float<T>(held[c][i]);
+    }
+}
 
 // ------------------------------------------------- the gradients of g and u
 
@@ -434,15 +510,21 @@ int forward_columns(const gated_act_linear &a, bool keep) {
                : 256;
 }
 
-int gradient_columns(const gated_act_linear &a) {
+// How the gradients' products are divided: the columns of a tile, and shares of the first one's sums.
+// A few long sums (2d terms, over the tiles of few rows) are as slow as their longest; shares of them cost
+// their way through L2 as fp32 (a tile 0.4 of a step, on all pairs) and a second kernel (8 steps).
+struct Division {
+    int columns, shares;
+};
+Division division_of(const gated_act_linear &a) {
     const int64_t pairs = sm_pairs(), in_steps = 2 * ceil_div64(a.d, kStep), w_steps = ceil_div64(a.T, kStep);
     // the walk's own division of the two products' tiles among the pairs
-    const auto busiest = [&](int64_t n, double share, double epilogue) {
-        const int64_t wide = ceil_div64(a.k, n), first = a.E * ceil_div64(a.T, kTile) * wide;
-        const int64_t second = 2 * a.E * ceil_div64(a.d, kTile) * wide;
-        const int64_t left = first % pairs, others = left ? pairs - left : 0, ahead = in_steps / w_steps;
+    const auto busiest = [&](int64_t n, int64_t shares, double share, double epilogue) {
+        const int64_t wide = ceil_div64(a.k, n), first = a.E * shares * ceil_div64(a.T, kTile) * wide;
+        const int64_t second = 2 * a.E * ceil_div64(a.d, kTile) * wide, steps = ceil_div64(in_steps, shares);
+        const int64_t left = first % pairs, others = left ? pairs - left : 0, ahead = steps / w_steps;
         const int64_t taken = second < ahead * others ? second : ahead * others, rest = second - taken;
-        const double f = tile_steps(in_steps, share, epilogue), w = tile_steps(w_steps, share, epilogue);
+        const double f = tile_steps(steps, share, epilogue), w = tile_steps(w_steps, share, epilogue);
         // the pairs in the order in which they take the rest: those with fewer first tiles in front
         const auto load = [&](int64_t firsts, int64_t place, int64_t before) {
             return static_cast<double>(firsts) * f +
@@ -453,9 +535,17 @@ int gradient_columns(const gated_act_linear &a) {
             const double more = load(first / pairs + 1, others, 0);
             most = more > most ? more : most;
         }
-        return most;
+        return most + (shares > 1 ? 8 + 0.4 * static_cast<double>(first) / static_cast<double>(pairs) : 0);
     };
-    return busiest(128, 0.68, 6) < busiest(256, 1, 9) ? 128 : 256;
+    const double narrow = busiest(128, 1, 0.68, 6), wide = busiest(256, 1, 1, 9);
+    Division best = {narrow < wide ? 128 : 256, 1};
+    double least = 0.85 * (narrow < wide ? narrow : wide);
+    for (const int n : {2, 3, 4, 6, 8, 12, 16, 24, 32})
+        if (n * 8 <= in_steps && n * a.E <= kMaxBatches && busiest(256, n, 1, 9) < least) {
+            least = busiest(256, n, 1, 9);
+            best = {256, n};
+        }
+    return best;
 }
 
 // The parts of a forward product that its jobs share.
@@ -568,6 +658,8 @@ struct BackwardParts {
     Operands o;
     int64_t dp, kp, padded;
     void *rows, *tail;
+    Division division;
+    float *sums;
     int rc;
     BackwardParts(const gated_act_linear &a, void *workspace, cudaStream_t stream) : o(operands(a)) {
         dp = ceil_div64(a.d, 8) * 8;
@@ -576,17 +668,23 @@ struct BackwardParts {
         Carve ws(workspace);
         rows = ws.take<void>(uint64_t(a.E) * 2 * padded * dp * 2);
         tail = ws.take<void>(a.n_rows ? uint64_t(a.E) * kStep * kp * 2 : 0);
+        division = division_of(a);
+        sums = ws.take<float>(division.shares > 1 ? uint64_t(4) * kTile * kTile * a.E * division.shares *
+                                                        ceil_div64(a.T, kTile) * ceil_div64(a.k, kTile)
+                                                  : 0);
         rc = addressable(&o, &ws, stream);
         bytes = ws.used;
     }
     uint64_t bytes;
 };
 
-template <class T, int N>
+template <class T, int N, bool SPLIT>
 int run_gradients(void *grad_in, void *grad_weight, const gated_act_linear &a, const Layout &rows,
-                  const Operands &o, const Layout &tail, cudaStream_t stream) {
+                  const BackwardParts &w, const Layout &tail, cudaStream_t stream) {
     constexpr bool is_bf16 = std::is_same_v<T, bf16>;
-    Product<Gradients<T, N>> g;
+    const Operands &o = w.o;
+    const int shares = w.division.shares;
+    Product<Gradients<T, N, SPLIT>> g;
     int rc = encode_map(&g.a, rows, kHalf, is_bf16);
     if (rc == GATED_ACT_OK)
         rc = encode_map(&g.b, o.weight, kStep, is_bf16);
@@ -600,7 +698,7 @@ int run_gradients(void *grad_in, void *grad_weight, const gated_act_linear &a, c
         return rc;
     g.other = g.a;
     g.live = a.n_rows;
-    g.batches = static_cast<int>(a.E);
+    g.batches = static_cast<int>(a.E) * shares;
     g.capacity = g.rows = static_cast<int>(a.T);
     g.n_tiles = static_cast<int>(ceil_div64(a.k, N));
     g.j.half_steps = static_cast<int>(ceil_div64(a.d, kStep));
@@ -611,10 +709,19 @@ int run_gradients(void *grad_in, void *grad_weight, const gated_act_linear &a, c
     g.second.rows = static_cast<int>(a.d);
     g.j.grad_in = static_cast<T *>(grad_in);
     g.j.grad_weight = static_cast<T *>(grad_weight);
+    g.j.sums = w.sums;
+    g.j.shares = shares;
     g.j.k = static_cast<int>(a.k);
     g.j.vec_in = a.k % 8 == 0 && aligned(grad_in, 16);
     g.j.vec_weight = a.k % 8 == 0 && aligned(grad_weight, 16);
-    return launch_product(g, a.E * (ceil_div64(a.T, kTile) + 2 * g.second.m_tiles) * g.n_tiles, stream);
+    rc = launch_product(g, a.E * (shares * ceil_div64(a.T, kTile) + 2 * g.second.m_tiles) * g.n_tiles, stream);
+    if (!SPLIT || rc != GATED_ACT_OK)
+        return rc;
+    const ShareArgs<T> j = {w.sums, static_cast<T *>(grad_in), a.n_rows, static_cast<int>(a.T),
+                            static_cast<int>(a.k), shares};
+    const int64_t blocks = a.E * ceil_div64(a.T, 32) * ceil_div64(a.k, 64);
+    return cuda_status(launch_kernel(join_shares<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                                     stream, 1, j));
 }
 
 template <class Act, class T>
@@ -663,9 +770,11 @@ int run_backward(void *grad_in, void *grad_weight, const void *grad_out, int64_t
                          {1, w.dp, w.padded * w.dp, 2 * w.padded * w.dp}};
     const Layout tail = {w.tail, {a.k, kStep, 1, a.E}, {1, w.kp, 0, kStep * w.kp}};
 
-    return gradient_columns(a) == 256
-               ? run_gradients<T, 256>(grad_in, grad_weight, a, rows, w.o, tail, stream)
-               : run_gradients<T, 128>(grad_in, grad_weight, a, rows, w.o, tail, stream);
+    return w.division.shares > 1
+               ? run_gradients<T, 256, true>(grad_in, grad_weight, a, rows, w, tail, stream)
+           : w.division.columns == 256
+               ? run_gradients<T, 256, false>(grad_in, grad_weight, a, rows, w, tail, stream)
+               : run_gradients<T, 128, false>(grad_in, grad_weight, a, rows, w, tail, stream);
 }
 
 template <class Act>

@@ -228,7 +228,7 @@ struct Second {
 //   J::kLive                     what the live counts bound
 //   J::kSecond                   whether there is a second product (Second), whose tiles follow the
 //                                first's: in one launch the SM pairs share both out more evenly
-//   J::batch_of(b, second)       index of the live count of a batch
+//   J::batch_of(g, b, second)    index of the live count of a batch
 //   J::batches(g)                how many there are, of at most g.batches
 //   J::steps_of(g, tile)         ring steps of a tile, where live counts do not bound them
 //   J::load(g, tile, step, rank, a, b, bar)   issues the step's copies of one CTA
@@ -333,7 +333,7 @@ template <class J> struct Walk {
                 ++b;
             t->b = b;
             place(t, at - s.first[b] * g.n_tiles, s.first[b + 1] - s.first[b], g.n_tiles);
-            t->live = g.live_of(J::batch_of(b, false));
+            t->live = g.live_of(J::batch_of(g, b, false));
             t->rows = J::kLive == Live::Rows ? t->live : g.rows;
             if constexpr (J::kLive == Live::Sum)
                 t->steps = (t->live + kStep - 1) / kStep;
@@ -369,7 +369,7 @@ template <class J> struct Walk {
             t->second = true;
             t->b = r / each;
             place(t, r % each, g.second.m_tiles, g.second.n_tiles);
-            t->live = g.live_of(J::batch_of(t->b, true));
+            t->live = g.live_of(J::batch_of(g, t->b, true));
             t->rows = g.second.rows;
             t->steps = (t->live + kStep - 1) / kStep;
             return true;
@@ -422,8 +422,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
             const int b = b0 + lane;
             int n = 0;
             if (b < batches)
-                n = ((J::kLive == Live::Rows ? g.live_of(J::batch_of(b, false))
-                      : J::kLive == Live::Columns && g.live_of(J::batch_of(b, false)) == 0 ? 0 : g.rows) +
+                n = ((J::kLive == Live::Rows ? g.live_of(J::batch_of(g, b, false))
+                      : J::kLive == Live::Columns && g.live_of(J::batch_of(g, b, false)) == 0 ? 0 : g.rows) +
                      J::kRows - 1) / J::kRows;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {

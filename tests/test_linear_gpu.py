@@ -11,10 +11,12 @@ pytestmark = pytest.mark.gpu
 BF16, F16 = torch.bfloat16, torch.float16
 DTYPES = [BF16, F16]
 # rows, k, d: one of everything, below and above a ring step and a tile, rows off 16-byte
-# boundaries (k or d not a multiple of 8), several tiles, more tiles than pairs of SMs
+# boundaries (k or d not a multiple of 8), several tiles, more tiles than pairs of SMs, sums of 2d long
+# enough to be split
 GATED = [(1, 1, 1), (1, 64, 128), (3, 7, 5), (2, 72, 40), (17, 130, 33), (64, 64, 256),
          (127, 200, 129), (256, 512, 384), (257, 1101, 271), (300, 96, 2000), (1, 2048, 768),
-         (9, 4096, 512), (1100, 264, 1032), (2304, 128, 2304)]
+         (9, 4096, 512), (1100, 264, 1032), (2304, 128, 2304),
+         (100, 72, 9001), (30, 200, 4096), (300, 520, 5000)]
 # tokens, k, vocabulary
 ENTROPY = [(1, 1, 1), (1, 64, 256), (2, 8, 3), (5, 7, 31), (33, 72, 300), (64, 128, 1000),
            (128, 96, 5000), (129, 40, 700), (257, 200, 777), (300, 1001, 4099), (511, 256, 16384), (40, 64, 40001), (700, 136, 8200)]
@@ -103,7 +105,7 @@ def test_gated_strides(ga, pad, shift, dtype, experts):
 @pytest.mark.parametrize("name", ["silu", "gelu"])
 @pytest.mark.parametrize("m,k,d,counts", [
     (40, 64, 96, [40, 0, 1, 17]), (300, 72, 136, [300, 64, 0, 0, 257, 1, 63, 65]),
-    (8, 128, 40, [0, 0, 0]), (64, 33, 7, [64, 5]), (100, 64, 64, [-3, 1000, 50]),
+    (60, 72, 5000, [60, 0, 33]), (8, 128, 40, [0, 0, 0]), (64, 33, 7, [64, 5]), (100, 64, 64, [-3, 1000, 50]),
     (2, 64, 32, [1 + i % 2 for i in range(200)])])
 def test_experts(ga, name, m, k, d, counts, dtype):
     e = len(counts)
