@@ -200,7 +200,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             ("linear_cross_entropy_workspace_bytes", size, [cvp]),
             ("linear_cross_entropy", c_int, [vp, vp, cvp, vp, size, vp]),
             ("linear_cross_entropy_backward_workspace_bytes", size, [cvp]),
-            ("linear_cross_entropy_backward", c_int, [vp, vp, cvp, cvp, cvp, vp, size, vp])):
+            ("linear_cross_entropy_backward", c_int, [vp, vp, cvp, cvp, cvp, cvp, vp, size, vp])):
         getattr(lib, fn).restype = restype
         getattr(lib, fn).argtypes = argtypes
     if path is None:

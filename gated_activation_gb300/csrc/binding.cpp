@@ -603,6 +603,7 @@ PyObject *entropy_backward(PyObject *const *a) {
     const void *grad_loss = flat(g, "grad_loss", at::kFloat, {v.a.T});
     if (!PyTuple_Check(a[4]) || PyTuple_GET_SIZE(a[4]) != 2)
         type_error("the fifth argument must be a CrossEntropy");
+    const void *loss = flat(tensor(PyTuple_GET_ITEM(a[4], 0), "loss"), "loss", at::kFloat, {v.a.T});
     const void *lse = flat(tensor(PyTuple_GET_ITEM(a[4], 1), "lse"), "lse", at::kFloat, {v.a.T});
     const Launch go(a[5], v.x.x);
     const at::ScalarType type = v.x.x.scalar_type();
@@ -612,6 +613,7 @@ PyObject *entropy_backward(PyObject *const *a) {
     check("linear_cross_entropy_backward",
           linear_cross_entropy_backward(grad_in.data_ptr(), grad_weight.data_ptr(),
                                         static_cast<const float *>(grad_loss),
+                                        static_cast<const float *>(loss),
                                         static_cast<const float *>(lse), &v.a,
                                         need ? ws.data_ptr() : nullptr, need, go.stream));
     return pack(nullptr, wrap(grad_in), wrap(grad_weight));

@@ -5,9 +5,9 @@
 //   forward       one product kernel whose epilogue leaves each row's maximum and sum of
 //                 exponentials over a tile's 256 columns, the target's column left out; a second
 //                 kernel joins them with the target's logit.
-//   backward      for each piece of the vocabulary: the logits again, with y = (p - [target])
-//                 grad_loss as the epilogue; y W added to grad_in's sums; y' in as the
-//                 piece's rows of grad_weight.  Last, grad_in from its sums.
+//   backward      for each piece of the vocabulary: the logits again, with y = (p - [target]) /
+//                 (1 - p_target) as the epilogue; y W added to grad_in's sums; y' and the rows times
+//                 their slopes as the piece's rows of grad_weight.  Last, grad_in from its sums.
 #include "product.cuh"
 
 #include "gated_act_linear.h"
@@ -68,18 +68,21 @@ struct Tokens {
     int32_t *count;     // [1] live tokens
     int32_t *token;     // [T] the token of a row
     int32_t *goal;      // [T] its target
-    float *shift;       // [T] its lse in powers of two        (backward)
-    float *weight;      // [T] its grad_loss / 2^e             (backward)
-    float *power;       // [1] 2^e                             (backward)
+    // backward: with c = 1 - p_target = -expm1(-loss) and f = grad_loss c,
+    float *shift;       // [T] lse and log c, in powers of two
+    float *factor;      // [T] f
+    float *power;       // [1] 2^e, above every |f|
 };
 
 template <class T> struct TokenArgs {
     Targets target;
     const T *in;
-    const float *grad_loss, *lse;   // backward
+    const float *grad_loss, *loss, *lse;   // backward
     float *loss_out, *lse_out;      // forward: 0 at dead tokens
     T *grad_in;                     // backward: 0 at dead tokens
     T *rows;                        // copies of live rows, zeros up to a whole step
+    T *scaled;                      // backward: the same, times f / 2^e
+    int64_t low;                    // where what that rounded off lies behind it; 0: nowhere
     Tokens t;
     int64_t in_stride;
     int n, k, kp, segment;
@@ -103,6 +106,7 @@ __device__ __forceinline__ int block_sum_int(int v, int *red) {
 template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<T> g) {
     __shared__ int red[8];
     __shared__ int list[256];
+    __shared__ float times[256];
     pdl_wait();
     pdl_trigger();
     const Targets &target = g.target;
@@ -116,7 +120,7 @@ template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<
         for (int j = 0; j < 8; ++j) {
             const int i = i0 + 256 * j;
             goal[j] = i < g.n ? target[i] : -1;
-            weight[j] = g.grad_loss && i < g.n ? g.grad_loss[i] : 0.f;
+            weight[j] = g.grad_loss && i < g.n ? g.grad_loss[i] * -expm1f(-g.loss[i]) : 0.f;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -137,8 +141,8 @@ template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<
         int most = 0;
         for (int i = 0; i < 8; ++i)
             most = max(most, red[i]);
-        // the power of two in it, a normal number; 1 for 0 and infinity
-        const int e = min(max(most >> 23, 1), 254);
+        // the next power of two, a normal number; 1 for 0 and infinity
+        const int e = min((most >> 23) + 1, 254);
         power = most == 0 || most >= 0x7F800000 ? 1.f : __int_as_float(e << 23);
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -169,8 +173,11 @@ template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<
             g.t.token[row] = i;
             g.t.goal[row] = goal;
             if (g.grad_loss) {
-                g.t.shift[row] = g.lse[i] * kLog2e;
-                g.t.weight[row] = g.grad_loss[i] / power;
+                const float c = -expm1f(-g.loss[i]), f = g.grad_loss[i] * c;
+                // c = 0: no slope; infinity makes every y 0 but the target's, and f is 0
+                g.t.shift[row] = c > 0.f ? fmaf(g.lse[i], kLog2e, log2f(c)) : INFINITY;
+                g.t.factor[row] = f;
+                times[threadIdx.x] = f / power;
             }
         } else if (i < end && g.loss_out) {
             g.loss_out[i] = 0.f;
@@ -181,16 +188,42 @@ template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<
         if (copy || g.grad_in)
             for (int j = threadIdx.x >> 5; j < 256 && i0 + j < end; j += 8) {
                 const int row = list[j];
-                if (row >= 0 && copy) {
+                if (row >= 0) {
                     const T *from = g.in + (i0 + j) * g.in_stride;
-                    T *to = g.rows + int64_t(row) * g.kp;
+                    T *to = g.rows + int64_t(row) * g.kp, *scaled = g.scaled + int64_t(row) * g.kp;
+                    const float f = times[j];
                     const bool vec = (reinterpret_cast<uintptr_t>(from) & 15) == 0;
                     int c = (threadIdx.x & 31) * 8;
 #pragma unroll 2
-                    for (; c + 8 <= g.k; c += 256)
-                        st_vec(to + c, vec ? ld_stream(from + c) : eight(from + c));
-                    for (int x = c; x < g.k && x < c + 8; ++x)
-                        to[x] = from[x];
+                    for (; c + 8 <= g.k; c += 256) {
+                        const uint4 v = vec ? ld_stream(from + c) : eight(from + c);
+                        if (copy)
+                            st_vec_out(to + c, v);
+                        if (g.scaled) {
+                            const T *x = reinterpret_cast<const T *>(&v);
+                            uint32_t w[4], rest[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 y = {to_float(x[2 * i]) * f, to_float(x[2 * i + 1]) * f};
+                                w[i] = pack2<T>(y);
+                                const T *high = reinterpret_cast<const T *>(&w[i]);
+                                rest[i] = pack2<T>({y.x - to_float(high[0]), y.y - to_float(high[1])});
+                            }
+                            st_vec_out(scaled + c, make_uint4(w[0], w[1], w[2], w[3]));
+                            if (g.low)
+                                st_vec_out(scaled + g.low + c, make_uint4(rest[0], rest[1], rest[2], rest[3]));
+                        }
+                    }
+                    for (int x = c; x < g.k && x < c + 8; ++x) {
+                        if (copy)
+                            to[x] = from[x];
+                        if (g.scaled) {
+                            const float y = to_float(from[x]) * f;
+                            scaled[x] = from_float<T>(y);
+                            if (g.low)
+                                scaled[g.low + x] = from_float<T>(y - to_float(from_float<T>(y)));
+                        }
+                    }
                 } else if (row < 0 && g.grad_in) {
                     T *to = g.grad_in + int64_t(i0 + j) * g.k;
                     if ((reinterpret_cast<uintptr_t>(to) & 15) == 0) {
@@ -209,10 +242,16 @@ template <class T> __global__ void __launch_bounds__(256) live_tokens(TokenArgs<
         __syncthreads();
     }
     // zeros from the live rows to a whole step of a sum over them
-    if (copy && blockIdx.x == 0) {
+    if (blockIdx.x == 0) {
         const int64_t from = int64_t(all) * g.kp, to = int64_t((all + kStep - 1) / kStep * kStep) * g.kp;
-        for (int64_t c = from + 8 * threadIdx.x; c < to; c += 8 * 256)
-            st_vec(g.rows + c, make_uint4(0, 0, 0, 0));
+        for (int64_t c = from + 8 * threadIdx.x; c < to; c += 8 * 256) {
+            if (copy)
+                st_vec(g.rows + c, make_uint4(0, 0, 0, 0));
+            if (g.scaled)
+                st_vec(g.scaled + c, make_uint4(0, 0, 0, 0));
+            if (g.scaled && g.low)
+                st_vec(g.scaled + g.low + c, make_uint4(0, 0, 0, 0));
+        }
     }
 }
 
@@ -348,11 +387,13 @@ template <class T, int N> struct TurnedStatistics {
     }
 };
 
-// y = (exp(l - lse) - [target]) weight, times 2^14 in fp16 (whose smallest normal number,
-// 2^-14, a probability in a large vocabulary often falls below; |y| <= 2^15 then).
+// y = (p - [target]) / c, c = 1 - p_target: the target's is -1, exactly, and the others' sum is 1.  A token's slope
+// f = grad_loss c stands outside: grad_in = f (y W) in fp32, grad_weight = y' (f in).  (With the slope inside, the rounding
+// of the target's y, half of a row's gradient in one number, was in all of the row: with a few dozen
+// tokens the error could be 1.5 of the results' own.)  Times 2^14 in fp16, whose smallest normal number, 2^-14, a
+// probability in a large vocabulary often falls below.
 template <class T> constexpr float kLift = std::is_same_v<T, f16> ? 16384.f : 1.f;
 
-//
 // The product again, y written as the operand that the next one reads along the sum and across it: 4096 x
 // 38912 x 2048 in 337 us (1.94 PFLOP/s).
 template <class T> struct Slopes {
@@ -380,7 +421,6 @@ template <class T> struct Slopes {
         const int first = g.j.first + t.n0 * kTile;
         const int goal = mine ? g.j.t.goal[r] - first : -1;
         const float shift = mine ? g.j.t.shift[r] : 0.f;
-        const float weight = mine ? g.j.t.weight[r] * kLift<T> : 0.f;
         const int top = t.m0 + (row & ~31), whole = (t.rows + kStep - 1) / kStep * kStep;
         T *y = g.j.y + int64_t(top) * g.j.piece + t.n0 * kTile;   // the warp's first row
         for (int c = 32 * stage.part; c < kTile && t.n0 * kTile + c < g.j.piece; c += 64) {
@@ -398,11 +438,11 @@ template <class T> struct Slopes {
             if (goal >= c && goal < c + 32) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    v[i] -= goal - c == i ? 1.f : 0.f;
+                    v[i] = goal - c == i ? -1.f : v[i];
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                v[i] = i < n ? v[i] * weight : 0.f;
+                v[i] = i < n ? v[i] * kLift<T> : 0.f;
             pack32<T>(w, v);
             stage.flush(w, y + c, g.j.piece, whole - top, 32, true);
         }
@@ -435,15 +475,18 @@ template <class T> struct PieceGradients {
     static constexpr int kN = kTile, kRows = kTile;
     static constexpr Live kLive = Live::Rows;
     struct Args {
-        CUtensorMap y, in, packed;   // of the second product
+        CUtensorMap y, scaled;       // of the second product
         float *sums;
         const float *power;
         T *grad_weight;              // the piece's first row
         Shares shares;
-        int k, first;
+        int k, first, low;           // rows from a scaled row to what it rounded off; 0: not kept
         bool begin, vec;
     };
     using G = Product<PieceGradients>;
+    __device__ static int second_steps(const G &g, int live) {
+        return (live + kStep - 1) / kStep * (g.j.low ? 2 : 1);
+    }
     __device__ static int batch_of(const G &, int, bool) { return 0; }
     __device__ static int batches(const G &g) { return g.j.shares(g.live_of(0)); }
     // shares of whole steps, as even as they get
@@ -463,8 +506,10 @@ template <class T> struct PieceGradients {
             load_across(b, &g.b, bar, g.j.first + x, col, 0, 0);
             return;
         }
-        load_across(a, &g.j.y, bar, step * kStep, row, 0, 0);
-        load_across(b, t.live < g.capacity ? &g.j.packed : &g.j.in, bar, step * kStep, col, 0, 0);
+        const int whole = (t.live + kStep - 1) / kStep, low = step >= whole;
+        const int x = (step - low * whole) * kStep;
+        load_across(a, &g.j.y, bar, x, row, 0, 0);
+        load_across(b, &g.j.scaled, bar, x + low * g.j.low, col, 0, 0);
     }
     __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
         const int k = g.j.k, r = t.m0 + row, col = t.n0 * kTile;
@@ -633,8 +678,8 @@ template <class T> __global__ void __launch_bounds__(256) join_grad_in(GradInArg
     for (int i = 0; i < 8; ++i)
         held[warp + 8 * i][lane] = v[i];
     __syncthreads();
-    const float power = *g.t.power * (1.f / kLift<T>);
     for (int i = warp; i < 32 && r0 + i < count; i += 8) {
+        const float power = g.t.factor[r0 + i] * (1.f / kLift<T>);
         T *to = g.out + int64_t(g.t.token[r0 + i]) * g.k + c0;
         for (int c = lane; c < 64 && c0 + c < g.k; c += 32)
             to[c] = from_float<T>(held[c][i] * power);
@@ -707,12 +752,12 @@ int64_t piece_of(const gated_act_vocabulary &a) {
 
 // The parts of a workspace.
 struct Parts {
-    Layout in, packed, weight;
+    Layout in, packed, scaled = {}, weight;
     Tokens t = {};
     float2 *part = nullptr;
     float *sums = nullptr;
     void *y = nullptr;
-    int64_t kp, padded, piece;
+    int64_t kp, padded, piece, low = 0;
     Shares shares = {};
     bool copy;
     uint64_t bytes;
@@ -731,8 +776,14 @@ struct Parts {
         packed = {ws.take<void>(2 * padded * kp), {a.k, padded, 1, 1}, {1, kp, 0, 0}};
         if (backward) {
             t.shift = ws.take<float>(4 * a.T);
-            t.weight = ws.take<float>(4 * a.T);
+            t.factor = ws.take<float>(4 * a.T);
             t.power = ws.take<float>(4);
+            // With a few dozen tokens there is no average over the roundings of f in: what they take off is
+            // kept, a second operand of the same size.
+            low = a.T <= 256 ? padded : 0;
+            scaled = packed;
+            scaled.size[1] += low;
+            scaled.data = ws.take<void>(2 * (padded + low) * kp);
             y = ws.take<void>(2 * padded * piece);
             shares = {static_cast<int>(ceil_div64(a.k, kTile)),
                       static_cast<int>(ceil_div64(piece < a.V ? piece : a.V, kStep)),
@@ -768,17 +819,20 @@ struct Parts {
 
 template <class T>
 int run_live_tokens(const Parts &w, const gated_act_vocabulary &a, const float *grad_loss,
-                    const float *lse, float *loss_out, float *lse_out, void *grad_in,
+                    const float *loss, const float *lse, float *loss_out, float *lse_out, void *grad_in,
                     cudaStream_t stream) {
     TokenArgs<T> g;
     g.target = targets_of(a);
     g.in = static_cast<const T *>(a.in);
     g.grad_loss = grad_loss;
+    g.loss = loss;
     g.lse = lse;
     g.loss_out = loss_out;
     g.lse_out = lse_out;
     g.grad_in = static_cast<T *>(grad_in);
     g.rows = static_cast<T *>(const_cast<void *>(w.packed.data));
+    g.scaled = static_cast<T *>(const_cast<void *>(w.scaled.data));
+    g.low = w.low * w.kp;
     g.t = w.t;
     g.in_stride = a.in_stride;
     g.n = static_cast<int>(a.T);
@@ -851,7 +905,7 @@ int run_forward(float *loss, float *lse, const gated_act_vocabulary &a, void *wo
     int rc = w.rc;
     const bool turned = few(a);
     if (rc == GATED_ACT_OK && !turned)
-        rc = run_live_tokens<T>(w, a, nullptr, nullptr, loss, lse, nullptr, stream);
+        rc = run_live_tokens<T>(w, a, nullptr, nullptr, nullptr, loss, lse, nullptr, stream);
     if (rc == GATED_ACT_OK && turned && w.copy)
         rc = launch_pack(packed_layout(w.in, const_cast<void *>(w.packed.data)), w.in, stream);
     if (rc != GATED_ACT_OK)
@@ -873,13 +927,13 @@ int run_forward(float *loss, float *lse, const gated_act_vocabulary &a, void *wo
 }
 
 template <class T>
-int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const float *lse,
-                 const gated_act_vocabulary &a, void *workspace, cudaStream_t stream) {
+int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const float *loss,
+                 const float *lse, const gated_act_vocabulary &a, void *workspace, cudaStream_t stream) {
     constexpr bool is_bf16 = std::is_same_v<T, bf16>;
     const Parts w(a, true, workspace, stream);
     int rc = w.rc;
     if (rc == GATED_ACT_OK)
-        rc = run_live_tokens<T>(w, a, grad_loss, lse, nullptr, nullptr, grad_in, stream);
+        rc = run_live_tokens<T>(w, a, grad_loss, loss, lse, nullptr, nullptr, grad_in, stream);
     const int k = static_cast<int>(a.k);
     const bool vec = a.k % 8 == 0 && aligned(grad_weight, 16);
 
@@ -892,7 +946,7 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
     if (rc == GATED_ACT_OK)
         rc = encode_map(&g.b, w.weight, kStep, is_bf16);
     if (rc == GATED_ACT_OK)
-        rc = encode_rows<T>(&g.j.in, &g.j.packed, w, kStep);
+        rc = encode_map(&g.j.scaled, w.scaled, kStep, is_bf16);
     for (int64_t first = 0; first < a.V && rc == GATED_ACT_OK; first += w.piece) {
         const int64_t cols = a.V - first < w.piece ? a.V - first : w.piece;
         const Layout y = {w.y, {cols, w.padded, 1, 1}, {1, w.piece, 0, 0}};
@@ -923,6 +977,7 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
         g.j.shares = w.shares;
         g.j.k = k;
         g.j.first = static_cast<int>(first);
+        g.j.low = static_cast<int>(w.low);
         g.j.begin = first == 0;
         g.j.vec = vec;
         rc = launch_product(g, (ceil_div64(a.T, kTile) + g.second.m_tiles) * g.n_tiles, stream);
@@ -981,8 +1036,8 @@ int linear_cross_entropy(float *loss, float *lse, const gated_act_vocabulary *a,
 }
 
 int linear_cross_entropy_backward(void *grad_in, void *grad_weight, const float *grad_loss,
-                                  const float *lse, const gated_act_vocabulary *a, void *workspace,
-                                  size_t workspace_bytes, cudaStream_t stream) {
+                                  const float *loss, const float *lse, const gated_act_vocabulary *a,
+                                  void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (!a)
         return GATED_ACT_ERR_NULL;
     int rc = check_sizes(*a);
@@ -996,19 +1051,20 @@ int linear_cross_entropy_backward(void *grad_in, void *grad_weight, const float 
     Region r[] = {{grad_in, static_cast<uint64_t>(a->T * a->k) * 2, 2, true},
                   {grad_weight, weight_bytes, 2, true},
                   {grad_loss, each, 4, false},
+                  {loss, each, 4, false},
                   {lse, each, 4, false},
                   gact::in_region(*a),
                   gact::weight_region(*a),
                   gact::target_region(*a),
                   {workspace, need, 16, true}};
-    rc = gact::check_device_regions(r, 8);
+    rc = gact::check_device_regions(r, 9);
     if (rc != GATED_ACT_OK)
         return rc;
     if (a->T == 0)   // sums over no tokens
         return gact::cuda_status(cudaMemsetAsync(grad_weight, 0, weight_bytes, stream));
     return a->dtype == GATED_ACT_BF16
-               ? gact::run_backward<gact::bf16>(grad_in, grad_weight, grad_loss, lse, *a, workspace, stream)
-               : gact::run_backward<gact::f16>(grad_in, grad_weight, grad_loss, lse, *a, workspace, stream);
+               ? gact::run_backward<gact::bf16>(grad_in, grad_weight, grad_loss, loss, lse, *a, workspace, stream)
+               : gact::run_backward<gact::f16>(grad_in, grad_weight, grad_loss, loss, lse, *a, workspace, stream);
 }
 
 }  // extern "C"

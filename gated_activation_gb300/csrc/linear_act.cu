@@ -208,6 +208,7 @@ template <class T, int N, bool SPLIT> struct Gradients {
         return second ? b >> 1 : SPLIT ? b / g.j.shares : b;
     }
     __device__ static int batches(const G &g) { return g.batches; }
+    __device__ static int second_steps(const G &, int live) { return (live + kStep - 1) / kStep; }
     // shares of whole steps, as even as they get
     __device__ static int first_step(const G &g, int b) {
         return SPLIT ? static_cast<int>(int64_t(g.steps) * (b % g.j.shares) / g.j.shares) : 0;

@@ -231,6 +231,7 @@ struct Second {
 //   J::batch_of(g, b, second)    index of the live count of a batch
 //   J::batches(g)                how many there are, of at most g.batches
 //   J::steps_of(g, tile)         ring steps of a tile, where live counts do not bound them
+//   J::second_steps(g, live)     with kSecond: those of a second tile
 //   J::load(g, tile, step, rank, a, b, bar)   issues the step's copies of one CTA
 //   J::finish(g, tile, row, sums, stage)      the epilogue of a warp's 32 rows: `row` is the
 //                                lane's (of the tile, in [0, 256)), `sums` the tensor memory
@@ -353,7 +354,7 @@ template <class J> struct Walk {
                 Tile f = *t;
                 f.b = 0;
                 f.live = live;
-                ahead = J::steps_of(g, f) / max((min(live, g.capacity) + kStep - 1) / kStep, 1);
+                ahead = J::steps_of(g, f) / max(J::second_steps(g, min(live, g.capacity)), 1);
                 ahead = min(ahead, g.second.batches * each / others + 1);
             }
             const bool other = mine >= left && others;
@@ -371,7 +372,7 @@ template <class J> struct Walk {
             place(t, r % each, g.second.m_tiles, g.second.n_tiles);
             t->live = g.live_of(J::batch_of(g, t->b, true));
             t->rows = g.second.rows;
-            t->steps = (t->live + kStep - 1) / kStep;
+            t->steps = J::second_steps(g, t->live);
             return true;
         }
         return false;

@@ -120,18 +120,19 @@ int linear_cross_entropy(float *loss, float *lse, const gated_act_vocabulary *a,
 size_t linear_cross_entropy_backward_workspace_bytes(const gated_act_vocabulary *a);
 
 /*
- * With p = exp(l - lse) and y = p - [v = target], rounded once to the element type after
- * multiplication with grad_loss (by the largest power of two in the batch's largest |grad_loss|,
- * which the sums are multiplied with at their end):
- *   grad_in      = grad_loss y W             [T, k] contiguous, of type dtype;
- *   grad_weight  = sum_t grad_loss_t y_t' in_t   [V, k] contiguous, of type dtype.
+ * With p = exp(l - lse), c = 1 - p_target (from the loss) and a token's slope f = grad_loss c,
+ *   grad_in      = f y W                     [T, k] contiguous, of type dtype;
+ *   grad_weight  = sum_t y_t' (f_t in_t)     [V, k] contiguous, of type dtype,
+ * where y = (p - [v = target]) / c, and f in (by a power of two above the batch's largest |f|, which the
+ * sums are multiplied with at their end), are each rounded once to the element type as
+ * operands of the products.  In fp16 a token whose slope is below 2^-14 of the largest loses bits.
  *   grad_loss    [T] fp32, read on the device; not used at tokens that take no part.
- *   lse          what linear_cross_entropy wrote.
+ *   loss, lse    what linear_cross_entropy wrote.
  * The logits are computed again, in pieces of the vocabulary.
  */
 int linear_cross_entropy_backward(void *grad_in, void *grad_weight, const float *grad_loss,
-                                  const float *lse, const gated_act_vocabulary *a, void *workspace,
-                                  size_t workspace_bytes, cudaStream_t stream);
+                                  const float *loss, const float *lse, const gated_act_vocabulary *a,
+                                  void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

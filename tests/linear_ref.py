@@ -115,16 +115,23 @@ def entropy_backward(gl, x, w, goal, dtype):
     p = torch.exp(logits - lse[:, None])
     y = p.clone()
     y[torch.arange(n, device=y.device), goal] -= 1
-    # y before it is rounded, then its rounding: in fp16 y stands 2^14 above, beside the largest
-    # power of two of the gradients, and half a subnormal step is 2^-25
-    oy = MORE * p * (off + olse[:, None] + ARITH * (1 + logits.abs())) + 2.0 ** -23 * (p + y.abs())
-    weight = gl[:, None].abs()
-    power = 2.0 ** torch.floor(torch.log2(gl.abs().max())) if n and gl.abs().max() > 0 else 1.0
-    tiny = 2.0 ** -25 * 2.0 ** -14 * power if dtype == torch.float16 else 0.0
-    off = weight * (oy + torch.finfo(dtype).eps / 2 * MORE * y.abs()) + tiny
+    # y / c, c = 1 - p_target, is an operand (the target's -1 exact), f = gl c stands outside, and f x is the other
+    # operand.  y's own error, in units of y: the logits' and the loss's; then the roundings, half a step each:
+    # y's of all but the target's column, and f x's.  c is within the loss's error of its own value.
+    oy = MORE * p * (off + 2 * olse[:, None] + ARITH * (1 + logits.abs())) + 2.0 ** -21 * (p + y.abs())
+    oy = oy + y.abs() * (2 * olse[:, None] + ARITH)
+    weight, half = gl[:, None].abs(), torch.finfo(dtype).eps / 2 * MORE
+    c = 1 - torch.exp(logits.gather(1, goal[:, None]) - lse[:, None])
+    f = gl.abs()[:, None] * c
+    power = 2.0 ** (torch.floor(torch.log2(f.max())) + 1) if n and f.max() > 0 else 1.0
+    # fp16: half a subnormal step, of y under its 2^14 and of f x under the power of two above every f
+    tiny = 2.0 ** -25 if dtype == torch.float16 else 0.0
+    off_in = weight * (oy + half * p) + f * tiny * 2.0 ** -14
+    off_w = weight * (oy + half * (p + y.abs())) + f * tiny * 2.0 ** -14
     rows = gl[:, None] * y
     gi, gw = rows @ w, rows.T @ x
     # sums over pieces of the vocabulary add fp32 roundings
-    bi = MORE * (off @ w.abs()) + (acc(v) + 2.0 ** -18) * (rows.abs() @ w.abs()) + half_step(gi, dtype)
-    bw = MORE * (off.T @ x.abs()) + acc(n) * (rows.abs().T @ x.abs()) + half_step(gw, dtype)
+    bi = MORE * (off_in @ w.abs()) + (acc(v) + 2.0 ** -18) * (rows.abs() @ w.abs()) + half_step(gi, dtype)
+    bw = MORE * (off_w.T @ x.abs()) + acc(n) * (rows.abs().T @ x.abs()) + half_step(gw, dtype) \
+        + (tiny * power * (y.abs() / c.clamp(min=1e-30)).sum(0)[:, None] if n else 0.0)
     return (gi, bi + 1e-30), (gw, bw + 1e-30)

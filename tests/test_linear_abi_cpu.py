@@ -97,16 +97,16 @@ def test_entropy_refusals(lib):
 
 
 def test_entropy_backward_refusals(lib):
-    def f(gi=D, gw=E, gl=F, lse=G, work=W, size=1 << 30, **a):
-        return lib.linear_cross_entropy_backward(gi, gw, gl, lse, _vocabulary(**a), work, size, None)
+    def f(gi=D, gw=E, gl=F, loss=F + 4096, lse=G, work=W, size=1 << 30, **a):
+        return lib.linear_cross_entropy_backward(gi, gw, gl, loss, lse, _vocabulary(**a), work, size, None)
 
-    assert lib.linear_cross_entropy_backward(D, E, F, G, None, W, 0, None) == ga.ERR_NULL
+    assert lib.linear_cross_entropy_backward(D, E, F, F + 4096, G, None, W, 0, None) == ga.ERR_NULL
     assert f(t=-1) == f(v=-1) == ga.ERR_SIZE and f(dtype=ga.F32) == ga.ERR_DTYPE
     need = lib.linear_cross_entropy_backward_workspace_bytes(_vocabulary())
     assert need > 0 and f(size=need - 1) == ga.ERR_SCRATCH
     # rows off 16-byte boundaries: the weight's copy is added, 32 padded rows
     assert lib.linear_cross_entropy_backward_workspace_bytes(_vocabulary(w=B + 2)) == need + 32 * 16 * 2
-    for missing in ("gi", "gw", "gl", "lse", "x", "w", "goal", "work"):
+    for missing in ("gi", "gw", "gl", "loss", "lse", "x", "w", "goal", "work"):
         assert f(**{missing: None}) == ga.ERR_NULL
     assert f(gi=D + 1) == f(gl=F + 2) == f(goal=C + 2, wide=0) == ga.ERR_ALIGN
-    assert f(gi=A) == f(gw=B) == f(gw=F) == f(gi=G) == f(gi=C) == ga.ERR_OVERLAP
+    assert f(gi=A) == f(gw=B) == f(gw=F) == f(gi=G) == f(gi=C) == f(gi=F + 4096) == ga.ERR_OVERLAP
