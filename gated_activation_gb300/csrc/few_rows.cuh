@@ -10,7 +10,7 @@
 //
 // `split` warps of a block share the sum; they add up through shared memory, in a fixed order.
 //
-// Measured: 1 row of 2048 -> 768 in 4.5 us a call (5.3 us alone; the turned product 13.6 us), of which the 6 MB are
+// Measured: 1 row of 2048 -> 768 in 4.5 us a call (5.3 us alone; the big tiles took 13.6), of which the 6 MB are
 // 0.9 us and the rest launch, one chain of loads and the host.  For weights with a turned tile for every pair
 // of SMs it is not used: 16 rows of 4096 -> 16384 took 80 us here, as every warp reads the rows' 128 KB through
 // L1 again, and 44 us there.

@@ -58,7 +58,7 @@ __device__ __forceinline__ uint32_t encode32(uint32_t (&w)[16], const float (&v)
 // ------------------------------------------------------------------- products
 
 // The forward product.  4 T k d operations; bound by the tensor cores where k is long (2048 x 4096 -> 16384:
-// 280 us alone, 94% of cuBLAS's rate and more), by the epilogue where it is short: per element one exponential, one
+// 275 us alone, cuBLAS's rate and more), by the epilogue where it is short: per element one exponential, one
 // reciprocal and, for the checkpoint, a maximum, a product and three rounds through shared memory, 4 to
 // 5 us for a tile of 128 x 128 per CTA (8 warps), against 5 ns per summed element in the main loop.
 template <class Act, class T, int N, bool KEEP> struct Forward {

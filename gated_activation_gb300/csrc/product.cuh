@@ -16,10 +16,10 @@
 // is transposed.  What lies outside a tensor is read as zeros.
 //
 // Why these sizes: a pair's step of 64 (256 x 256 x 64) takes 512 cycles of its tensor cores and 64 KB of
-// copies, 64 bytes per cycle and SM from L2; a tile of 128 columns takes 48 KB for half the products, and
-// measured 0.86 of the time.  The ring's six slots are 3000 cycles, twice a copy's latency under load.
+// copies, 64 bytes per cycle and SM from L2; a step of 128 columns takes 48 KB for half the products, and
+// measured 0.59 to 0.68 of the time.  The ring's six slots are 3000 cycles, twice a copy's latency under load.
 // Measured on GB300 (cuBLAS: 1.88 PFLOP/s in short runs, 1.72 under the power limit): 2048 x 32768 x 4096 in
-// 280 us alone (1.96 PFLOP/s), 316 us in a stream of such calls; tensor cores active 85% of the cycles.
+// 275 us alone (2.0 PFLOP/s), 318 us in a stream of such calls; tensor cores active 91% of the cycles.
 // Small products are bound by what is not overlapped: launch and allocation (2.5 us), the first copies, the
 // last tile's epilogue (1 to 5 us).
 //
