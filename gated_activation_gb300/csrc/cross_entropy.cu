@@ -570,7 +570,7 @@ template <class T, int WARPS> __global__ void __launch_bounds__(256) join_statis
     float2 dot[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
     const int from = g.k & ~7;
     const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 15) == 0;
-#pragma unroll 2
+#pragma unroll 4
     for (int c = thread * 8; c < from; c += 256 * WARPS) {   // in one order, whatever the alignment
         const uint4 vx = eight(x + c, 8, vec), vw = eight(w + c, 8, vec);
         const T *px = reinterpret_cast<const T *>(&vx), *pw = reinterpret_cast<const T *>(&vw);
@@ -590,9 +590,25 @@ template <class T, int WARPS> __global__ void __launch_bounds__(256) join_statis
         sum = sum * exp2_fast(top - base) + p.y * exp2_fast(p.x - base);
         top = most;
     };
-#pragma unroll 4
-    for (int i = thread; i < g.parts; i += 32 * WARPS)
-        add(g.part[int64_t(r) * g.parts + i]);
+    constexpr int kAhead = 8;   // of a thread's parts on their way; one exponential each
+    for (int i0 = thread; i0 < g.parts; i0 += kAhead * 32 * WARPS) {
+        float2 p[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * 32 * WARPS;
+            p[j] = i < g.parts ? g.part[int64_t(r) * g.parts + i] : make_float2(-INFINITY, 0.f);
+        }
+        float most = top;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            most = max_nan(most, p[j].x);
+        const float base = most == -INFINITY ? 0.f : most;
+        sum *= exp2_fast(top - base);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            sum = fmaf(p[j].y, exp2_fast(p[j].x - base), sum);
+        top = most;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float2 p = {__shfl_xor_sync(0xFFFFFFFFu, top, o), __shfl_xor_sync(0xFFFFFFFFu, sum, o)};
@@ -645,6 +661,9 @@ template <class T> __global__ void __launch_bounds__(256) join_grad_in(GradInArg
     if (r0 >= count)
         return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool mine = r0 + lane < count;   // the lane's row: its place and slope, for the end
+    const int token = mine ? g.t.token[r0 + lane] : 0;
+    const float slope = mine ? g.t.factor[r0 + lane] * (1.f / kLift<T>) : 0.f;
     const int shares = g.shares(count);
     const int64_t part = int64_t((count + kTile - 1) / kTile) * g.shares.n_tiles * (kTile * kTile);
     const float *from = g.sums + (int64_t(r0 / kTile) * g.shares.n_tiles + c0 / kTile) * (kTile * kTile) +
@@ -658,7 +677,7 @@ template <class T> __global__ void __launch_bounds__(256) join_grad_in(GradInArg
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int c = warp + 8 * i;
-            if (r0 + lane < count && c0 + c < g.k)
+            if (mine && c0 + c < g.k)
                 v[i] += from[s * part + c * kTile];
         }
 #pragma unroll
@@ -666,10 +685,10 @@ template <class T> __global__ void __launch_bounds__(256) join_grad_in(GradInArg
         held[warp + 8 * i][lane] = v[i];
     __syncthreads();
     for (int i = warp; i < 32 && r0 + i < count; i += 8) {
-        const float power = g.t.factor[r0 + i] * (1.f / kLift<T>);
-        T *to = g.out + int64_t(g.t.token[r0 + i]) * g.k + c0;
+        const float f = __shfl_sync(0xFFFFFFFFu, slope, i);
+        T *to = g.out + int64_t(__shfl_sync(0xFFFFFFFFu, token, i)) * g.k + c0;
         for (int c = lane; c < 64 && c0 + c < g.k; c += 32)
-            to[c] = from_float<T>(held[c][i] * power);
+            to[c] = from_float<T>(held[c][i] * f);
     }
 }
 
