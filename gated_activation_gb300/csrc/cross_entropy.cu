@@ -41,17 +41,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 
-// Eight elements at any address of theirs (with `vec` one of 16 bytes), zeros from the n-th on.
-template <class T> __device__ __forceinline__ uint4 eight(const T *p, int n, bool vec) {
-    if (vec && n >= 8)
-        return ld_stream(p);
-    uint32_t v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = i < n ? ld_stream_u16(reinterpret_cast<const uint16_t *>(p) + i) : 0;
-    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-}
-
 // The targets as given: a token's, or -1 where it lies outside the vocabulary.
 struct Targets {
     const void *data;

@@ -568,6 +568,17 @@ __device__ __forceinline__ void load_across(uint32_t dst, const CUtensorMap *map
         box_load(dst + kStep * 128, map, bar, row + 64, x, z, w);
 }
 
+// Eight elements at any address of theirs (with `vec` one of 16 bytes), zeros from the n-th on.
+template <class T> __device__ __forceinline__ uint4 eight(const T *p, int n, bool vec) {
+    if (vec && n >= 8)
+        return ld_stream(p);
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = i < n ? ld_stream_u16(reinterpret_cast<const uint16_t *>(p) + i) : 0;
+    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+}
+
 template <class T> __device__ __forceinline__ uint32_t pack2(float2 v);
 template <> __device__ __forceinline__ uint32_t pack2<bf16>(float2 v) { return pack_bf16x2(v.x, v.y); }
 template <> __device__ __forceinline__ uint32_t pack2<f16>(float2 v) {
