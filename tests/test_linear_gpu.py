@@ -101,6 +101,22 @@ def test_gated_strides(ga, pad, shift, dtype, experts):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("pad,shift", [(8, 8), (3, 5)])
+def test_experts_strides(ga, pad, shift):
+    """Rows apart, on 16-byte boundaries and off them, of which the last step is partly live."""
+    x, w, dy = _operands(200, 104, 40, BF16, 77, 3)
+    counts = torch.tensor([200, 70, 129], dtype=torch.int32, device="cuda")
+    xs, ws, dys = _strided(x, pad, shift), _strided(w, pad, shift), _strided(dy, pad, shift)
+    want, kept = ga.linear_silu_and_mul(x, w, n_rows=counts, keep=True)
+    grads = ga.linear_silu_and_mul_backward(dy, x, w, kept, n_rows=counts)
+    got, again = ga.linear_silu_and_mul(xs, ws, n_rows=counts, keep=True)
+    others = ga.linear_silu_and_mul_backward(dys, xs, ws, again, n_rows=counts)
+    assert torch.equal(grads[1], others[1])
+    for i, n in enumerate(counts.tolist()):
+        assert torch.equal(want[i, :n], got[i, :n]) and torch.equal(grads[0][i, :n], others[0][i, :n])
+        _check_gated("silu", x[i, :n], w[i], dy[i, :n], want[i, :n], (grads[0][i, :n], grads[1][i]), BF16)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("name", ["silu", "gelu"])
 @pytest.mark.parametrize("m,k,d,counts", [
@@ -330,6 +346,15 @@ def test_entropy_dead_tokens(ga, dtype):
     kept = ga.linear_cross_entropy(x, w, goal)
     gi, gw = ga.linear_cross_entropy_backward(gl, x, w, goal, kept)
     assert not any(t.any() for t in (kept.loss, kept.lse, gi, gw))
+
+
+@pytest.mark.parametrize("k", [40, 1100])
+def test_entropy_many_tokens(ga, k):
+    """More tokens than all SMs number in one turn, and rows of more than one piece."""
+    x, w, goal, gl = _tokens(170001 if k < 100 else 5000, k, 50, BF16, k, 0.6)
+    kept = ga.linear_cross_entropy(x, w, goal)
+    grads = ga.linear_cross_entropy_backward(gl, x, w, goal, kept)
+    _check_entropy(x, w, goal, gl, kept, grads, BF16)
 
 
 @pytest.mark.parametrize("pad,shift", [(8, 0), (1, 0), (3, 5), (0, 1)])
