@@ -326,7 +326,7 @@ template <class T> struct GateGradIn {
 
 constexpr int kGradRows = 2;   // rows of a thread: six 16-byte loads on their way
 
-// (dg, du) of eight columns of four rows per thread, zeros from the live rows to a whole step.
+// (dg, du) of eight columns of two rows per thread, zeros from the live rows to a whole step.
 // One pass: 6 bytes and the scales in, 4 out per pair of elements; 4096 x 8192 in 53.5 us, 93% of the copy
 // rate (four rows a thread in 128 registers: 71 us; two in 64, twice the warps).
 template <class Act, class T, bool VEC>
