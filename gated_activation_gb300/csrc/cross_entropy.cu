@@ -17,16 +17,17 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// What logits of k terms are multiplied with to be powers of two.  The tensor cores cut their fp32 sums
-// off towards 0 after every instruction (16 terms), half a unit in the last place on average: a sum of k
-// terms, whose partial sums are half of it on average, loses a share of it that grows as k.  (Expected,
-// with 24 bits: k / 16 cuts x 2^-24 x 0.72, the mean of 1 / m over mantissas m in [1, 2), x 1/2 = 1.3e-9 k.
-// Measured on GB300, 65536 sums of N(0, 16) each: 0.93e-9 to 0.97e-9 k in bf16 and 1.03e-9 to 1.12e-9 k in
-// fp16 for k from 1024 to 8192.)  The mean of it is given back here: it would be most of the error of a loss,
-// 9e-7 of it at k = 2048.
-inline float powers_of(int64_t k) {
-    return static_cast<float>(1.4426950408889634 * (1.0 + 1.0e-9 * static_cast<double>(k)));
-}
+// Ring steps (64 terms each) after which the sum of a logit is closed.  The tensor cores cut their fp32 sums off
+// towards 0 after every instruction (16 terms), half a unit in the last place on average: a sum of k dense terms,
+// whose partial sums are half of it on average, loses a share of it that grows as k.  (Expected, with 24 bits:
+// k / 16 cuts x 2^-24 x 0.72, the mean of 1 / m over mantissas m in [1, 2), x 1/2 = 1.3e-9 k.  Measured on GB300,
+// 65536 sums of N(0, 16) each: 0.93e-9 to 0.97e-9 k in bf16 and 1.03e-9 to 1.12e-9 k in fp16 for k from 1024 to
+// 8192.)  Closed sums lose the share of their own terms alone, 5e-7, and are added with rounding; a sum that fp32
+// holds exactly stays exact.  For the gradients, which are rounded to 16 bits, twice as many.
+// What it costs, 4096 tokens over 32768: k = 640 102 us for 93 (the epilogue no longer hides), 1024 167 for 165,
+// 2048 and 8192 nothing; sums closed after 4 steps cost 8% at every k.  Up to 8 (16) steps a kernel without closed
+// sums is taken: with them k = 256 took 77 us for 57, as 128 registers of sums leave few for the exponentials.
+constexpr int kLossSteps = 8, kSlopeSteps = 16;
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -252,16 +253,15 @@ __device__ __forceinline__ void load_logits(const G &g, const Tile &t, int first
 // Maximum (in powers of two) and sum of exponentials of each row over a tile's columns.  2 T V k operations,
 // bound by the tensor cores: 8192 x 65536 x 2048 in 1.09 ms alone (2.0 PFLOP/s), 1.28 ms in a stream of such
 // calls (the power limit).  A tile's exponentials take 1.7 us, hidden from k = 384 on.
-template <class T> struct Statistics {
+template <class T, int CLOSED> struct Statistics {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
-    static constexpr int kN = kTile, kRows = kTile;
+    static constexpr int kN = kTile, kRows = kTile, kClosed = CLOSED;
     static constexpr Live kLive = Live::Rows;
     struct Args {
         const int32_t *goal;
         float2 *part;        // [capacity, 2 tiles]: maximum, sum of each warp's columns
         int V;
-        float powers;
     };
     using G = Product<Statistics>;
     __device__ static int batch_of(const G &, int, bool) { return 0; }
@@ -271,15 +271,13 @@ template <class T> struct Statistics {
                                 uint32_t b, uint32_t bar) {
         load_logits(g, t, 0, step, rank, a, b, bar);
     }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
+    __device__ static void finish(const G &g, const Tile &t, int row, Sums<CLOSED, kN> &sums,
+                                  const Stage &stage) {
         const int r = t.m0 + row;
         const bool mine = r < t.rows;
         const int first = t.n0 * kTile, goal = mine ? g.j.goal[r] - first : -1;
         float top = -INFINITY, sum = 0.f;
-        for (int c = 32 * stage.part; c < kTile && first + c < g.j.V; c += 64) {
-            float v[32];
-            sums_load32(sums + c, v);
-            sums_ready(v);
+        for_columns<CLOSED, kN>(sums, stage.part, g.j.V - first, [&](int c, float (&v)[32]) {
             const int n = g.j.V - first - c;
             if (n < 32 || (goal >= c && goal < c + 32)) {
 #pragma unroll
@@ -291,19 +289,19 @@ template <class T> struct Statistics {
             for (int i = 3; i < 32; ++i)
                 most[i & 3] = max_nan(most[i & 3], v[i]);
             const float here = max_nan(max_nan(most[0], most[1]), max_nan(most[2], most[3]));
-            const float now = max_nan(top, here * g.j.powers);
+            const float now = max_nan(top, here * kLog2e);
             // a row of -infinity alone has no exponential: its maximum is taken as 0
             const float base = now == -INFINITY ? 0.f : now;
             float2 part[2] = {{sum * exp2_fast(top - base), 0.f}, {0.f, 0.f}};
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-                const float2 y = fma2({v[i], v[i + 1]}, both(g.j.powers), both(-base));
+                const float2 y = fma2({v[i], v[i + 1]}, both(kLog2e), both(-base));
                 part[i >> 1 & 1] = add2(part[i >> 1 & 1], {exp2_fast(y.x), exp2_fast(y.y)});
             }
             part[0] = add2(part[0], part[1]);
             sum = part[0].x + part[0].y;
             top = now;
-        }
+        });
         if (mine)
             g.j.part[int64_t(r) * 2 * g.n_tiles + 2 * t.n0 + stage.part] = make_float2(top, sum);
     }
@@ -312,16 +310,15 @@ template <class T> struct Statistics {
 // The same for up to N tokens, which would leave most of a 256-row tile empty, with the roles turned
 // round: the vocabulary's rows are the tile's, the tokens its columns (64 x 32000 x 1024: 12.6 us, upright 17.3).  A warp turns its 32 rows of 16
 // tokens in shared memory; two lanes then take half of the rows of a token each.
-template <class T, int N> struct TurnedStatistics {
+template <class T, int N, int CLOSED> struct TurnedStatistics {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
-    static constexpr int kN = N, kRows = kTile;
+    static constexpr int kN = N, kRows = kTile, kClosed = CLOSED;
     static constexpr Live kLive = Live::Columns;
     struct Args {
         Targets target;
         float2 *part;        // [capacity, 8 tiles]: maximum, sum of 32 columns
         int tiles;
-        float powers;
     };
     using G = Product<TurnedStatistics>;
     __device__ static int batch_of(const G &, int, bool) { return 0; }
@@ -332,14 +329,12 @@ template <class T, int N> struct TurnedStatistics {
         load_along(a, &g.a, bar, step * kStep, t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
         load_along(b, &g.b, bar, step * kStep, static_cast<int>(rank) * (N / 2), 0, 0);
     }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
+    __device__ static void finish(const G &g, const Tile &t, int row, Sums<CLOSED, N> &sums,
+                                  const Stage &stage) {
         static_assert(32 * 17 * 4 <= 32 * kStageRow);
         float *held = reinterpret_cast<float *>(stage.p);   // [32 rows, 16 tokens], 17 apart
         const int lane = threadIdx.x & 31, first = t.m0 + (row & ~31), from = (lane >> 4) * 16;
-        for (int c = 32 * stage.part; c < N && c < t.live; c += 64) {
-            float v[32];
-            sums_load32(sums + c, v);
-            sums_ready(v);
+        for_columns<CLOSED, N>(sums, stage.part, t.live, [&](int c, float (&v)[32]) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -352,7 +347,7 @@ template <class T, int N> struct TurnedStatistics {
                 float x[16], top = -INFINITY, sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    x[i] = held[(from + i) * 17 + (lane & 15)] * g.j.powers;
+                    x[i] = held[(from + i) * 17 + (lane & 15)] * kLog2e;
                     x[i] = goal == i ? -INFINITY : x[i];
                     top = max_nan(top, x[i]);
                 }
@@ -366,7 +361,7 @@ template <class T, int N> struct TurnedStatistics {
                     g.j.part[int64_t(token) * 8 * g.j.tiles + (first >> 5)] = make_float2(top, sum);
                 __syncwarp();
             }
-        }
+        });
     }
 };
 
@@ -379,16 +374,15 @@ template <class T> constexpr float kLift = std::is_same_v<T, f16> ? 16384.f : 1.
 
 // The product again, y written as the operand that the next one reads along the sum and across it: 4096 x
 // 38912 x 2048 in 337 us (1.94 PFLOP/s).
-template <class T> struct Slopes {
+template <class T, int CLOSED> struct Slopes {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
-    static constexpr int kN = kTile, kRows = kTile;
+    static constexpr int kN = kTile, kRows = kTile, kClosed = CLOSED;
     static constexpr Live kLive = Live::Rows;
     struct Args {
         Tokens t;
         T *y;              // [padded, piece]
         int V, first, piece;
-        float powers;
     };
     using G = Product<Slopes>;
     __device__ static int batch_of(const G &, int, bool) { return 0; }
@@ -398,7 +392,8 @@ template <class T> struct Slopes {
                                 uint32_t b, uint32_t bar) {
         load_logits(g, t, g.j.first, step, rank, a, b, bar);
     }
-    __device__ static void finish(const G &g, const Tile &t, int row, uint32_t sums, const Stage &stage) {
+    __device__ static void finish(const G &g, const Tile &t, int row, Sums<CLOSED, kN> &sums,
+                                  const Stage &stage) {
         const int r = t.m0 + row;
         const bool mine = r < t.rows;
         const int first = g.j.first + t.n0 * kTile;
@@ -406,15 +401,12 @@ template <class T> struct Slopes {
         const float shift = mine ? g.j.t.shift[r] : 0.f;
         const int top = t.m0 + (row & ~31), whole = (t.rows + kStep - 1) / kStep * kStep;
         T *y = g.j.y + int64_t(top) * g.j.piece + t.n0 * kTile;   // the warp's first row
-        for (int c = 32 * stage.part; c < kTile && t.n0 * kTile + c < g.j.piece; c += 64) {
+        for_columns<CLOSED, kN>(sums, stage.part, g.j.piece - t.n0 * kTile, [&](int c, float (&v)[32]) {
             const int n = mine ? g.j.V - first - c : 0;
-            float v[32];
             uint32_t w[16];
-            sums_load32(sums + c, v);
-            sums_ready(v);
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-                const float2 x = fma2({v[i], v[i + 1]}, both(g.j.powers), both(-shift));
+                const float2 x = fma2({v[i], v[i + 1]}, both(kLog2e), both(-shift));
                 v[i] = exp2_fast(x.x);
                 v[i + 1] = exp2_fast(x.y);
             }
@@ -428,7 +420,7 @@ template <class T> struct Slopes {
                 v[i] = i < n ? v[i] * kLift<T> : 0.f;
             pack32<T>(w, v);
             stage.flush(w, y + c, g.j.piece, whole - top, 32, true);
-        }
+        });
     }
 };
 
@@ -455,7 +447,7 @@ struct Shares {
 template <class T> struct PieceGradients {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = true, kSecond = true;
-    static constexpr int kN = kTile, kRows = kTile;
+    static constexpr int kN = kTile, kRows = kTile, kClosed = 0;
     static constexpr Live kLive = Live::Rows;
     struct Args {
         CUtensorMap y, scaled;       // of the second product
@@ -861,27 +853,27 @@ template <class T> int encode_rows(CUtensorMap *place, CUtensorMap *packed, cons
 }
 
 // The two forms of the statistics' product.
-template <class T> struct Upright {
-    static int set(Product<Statistics<T>> *g, const Parts &w, const gated_act_vocabulary &a) {
+template <class T, int CLOSED> struct Upright {
+    static int set(Product<Statistics<T, CLOSED>> *g, const Parts &w, const gated_act_vocabulary &a) {
         g->n_tiles = static_cast<int>(ceil_div64(a.V, kTile));
-        g->j = {w.t.goal, w.part, static_cast<int>(a.V), powers_of(a.k)};
+        g->j = {w.t.goal, w.part, static_cast<int>(a.V)};
         const int rc = encode_rows<T>(&g->a, &g->other, w, kHalf);
         return rc == GATED_ACT_OK ? encode_map(&g->b, w.weight, kHalf, std::is_same_v<T, bf16>) : rc;
     }
-    using Job = Statistics<T>;
+    using Job = Statistics<T, CLOSED>;
     static int64_t tiles(const gated_act_vocabulary &a) { return ceil_div64(a.T, kTile) * ceil_div64(a.V, kTile); }
 };
-template <class T, int N> struct Turned {
-    static int set(Product<TurnedStatistics<T, N>> *g, const Parts &w, const gated_act_vocabulary &a) {
+template <class T, int N, int CLOSED> struct Turned {
+    static int set(Product<TurnedStatistics<T, N, CLOSED>> *g, const Parts &w, const gated_act_vocabulary &a) {
         g->live = nullptr;
         g->n_tiles = 1;
         g->rows = static_cast<int>(a.V);
-        g->j = {targets_of(a), w.part, static_cast<int>(ceil_div64(a.V, kTile)), powers_of(a.k)};
+        g->j = {targets_of(a), w.part, static_cast<int>(ceil_div64(a.V, kTile))};
         const int rc = encode_map(&g->b, w.copy ? w.packed : w.in, N / 2, std::is_same_v<T, bf16>);
         g->other = g->b;
         return rc == GATED_ACT_OK ? encode_map(&g->a, w.weight, kHalf, std::is_same_v<T, bf16>) : rc;
     }
-    using Job = TurnedStatistics<T, N>;
+    using Job = TurnedStatistics<T, N, CLOSED>;
     static int64_t tiles(const gated_act_vocabulary &a) { return ceil_div64(a.V, kTile); }
 };
 template <class Form>
@@ -905,9 +897,13 @@ int run_forward(float *loss, float *lse, const gated_act_vocabulary &a, void *wo
         rc = launch_pack(packed_layout(w.in, const_cast<void *>(w.packed.data)), w.in, stream);
     if (rc != GATED_ACT_OK)
         return rc;
-    rc = a.T <= 32 ? run_statistics(Turned<T, 32>{}, w, a, stream)
-         : turned  ? run_statistics(Turned<T, 128>{}, w, a, stream)
-                   : run_statistics(Upright<T>{}, w, a, stream);
+    const auto statistics = [&](auto closed) {
+        constexpr int CLOSED = decltype(closed)::value;
+        return a.T <= 32 ? run_statistics(Turned<T, 32, CLOSED>{}, w, a, stream)
+               : turned  ? run_statistics(Turned<T, 128, CLOSED>{}, w, a, stream)
+                         : run_statistics(Upright<T, CLOSED>{}, w, a, stream);
+    };
+    rc = a.k > kLossSteps * kStep ? statistics(Const<kLossSteps>{}) : statistics(Const<0>{});
     if (rc != GATED_ACT_OK)
         return rc;
     const int parts = static_cast<int>((turned ? 8 : 2) * ceil_div64(a.V, kTile));
@@ -921,7 +917,7 @@ int run_forward(float *loss, float *lse, const gated_act_vocabulary &a, void *wo
                                      0, stream, 1, j));
 }
 
-template <class T>
+template <class T, int CLOSED>
 int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const float *loss,
                  const float *lse, const gated_act_vocabulary &a, void *workspace, cudaStream_t stream) {
     constexpr bool is_bf16 = std::is_same_v<T, bf16>;
@@ -932,7 +928,7 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
     const int k = static_cast<int>(a.k);
     const bool vec = a.k % 8 == 0 && aligned(grad_weight, 16);
 
-    Product<Slopes<T>> s;
+    Product<Slopes<T, CLOSED>> s;
     Product<PieceGradients<T>> g;
     if (rc == GATED_ACT_OK)
         rc = encode_rows<T>(&s.a, &s.other, w, kHalf);
@@ -949,7 +945,7 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
         s.n_tiles = static_cast<int>(ceil_div64(cols, kTile));
         s.steps = static_cast<int>(ceil_div64(a.k, kStep));
         s.j = {w.t, static_cast<T *>(w.y), static_cast<int>(a.V), static_cast<int>(first),
-               static_cast<int>(w.piece), powers_of(a.k)};
+               static_cast<int>(w.piece)};
         rc = launch_product(s, ceil_div64(a.T, kTile) * s.n_tiles, stream);
         if (rc == GATED_ACT_OK)
             rc = encode_map(&g.a, y, kHalf, is_bf16);
@@ -1057,9 +1053,13 @@ int linear_cross_entropy_backward(void *grad_in, void *grad_weight, const float 
         return rc;
     if (a->T == 0)   // sums over no tokens
         return gact::cuda_status(cudaMemsetAsync(grad_weight, 0, weight_bytes, stream));
-    return a->dtype == GATED_ACT_BF16
-               ? gact::run_backward<gact::bf16>(grad_in, grad_weight, grad_loss, loss, lse, *a, workspace, stream)
-               : gact::run_backward<gact::f16>(grad_in, grad_weight, grad_loss, loss, lse, *a, workspace, stream);
+    const auto go = [&](auto type) {
+        using T = decltype(type);
+        return a->k > gact::kSlopeSteps * gact::kStep
+                   ? gact::run_backward<T, gact::kSlopeSteps>(grad_in, grad_weight, grad_loss, loss, lse, *a, workspace, stream)
+                   : gact::run_backward<T, 0>(grad_in, grad_weight, grad_loss, loss, lse, *a, workspace, stream);
+    };
+    return a->dtype == GATED_ACT_BF16 ? go(gact::bf16{}) : go(gact::f16{});
 }
 
 }  // extern "C"

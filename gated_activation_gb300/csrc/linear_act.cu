@@ -65,6 +65,7 @@ template <class Act, class T, int N, bool KEEP> struct Forward {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
     static constexpr int kN = N, kRows = kTile;
+    static constexpr int kClosed = 0;
     static constexpr Live kLive = Live::Rows;
     struct Args {
         T *out;
@@ -126,6 +127,7 @@ template <class Act, class T, int N> struct Swapped {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
     static constexpr int kN = N, kRows = kHalf;
+    static constexpr int kClosed = 0;
     static constexpr Live kLive = Live::Columns;
     struct Args {
         T *out;
@@ -195,6 +197,7 @@ template <class T, int N, bool SPLIT> struct Gradients {
     using Elem = T;
     static constexpr bool kAAcross = false, kBAcross = true, kSecond = true;
     static constexpr int kN = N, kRows = kTile;
+    static constexpr int kClosed = 0;
     static constexpr Live kLive = Live::Rows;
     struct Args {
         CUtensorMap rows, in, tail;   // of the second product

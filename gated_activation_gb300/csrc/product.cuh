@@ -204,6 +204,46 @@ __device__ __forceinline__ void sums_ready(float (&v)[32]) {
                  : "memory");
     asm volatile("" : "+f"(v[30]), "+f"(v[31]));
 }
+// G times 32 columns, 64 apart, added to v: 16 columns are on their way while the 16 before are added.
+__device__ __forceinline__ void sums_load16(uint32_t address, float (&v)[16]) {
+    uint32_t r[16];
+    __syncwarp();
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(address));
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void sums_ready(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                   "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]),
+                   "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :
+                 : "memory");
+}
+template <int G> __device__ __forceinline__ void sums_add(uint32_t address, float (&v)[G][32]) {
+    float x[2][16];
+    sums_load16(address, x[0]);
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) {
+        sums_ready(x[i & 1]);
+        if (i + 1 < 2 * G)
+            sums_load16(address + (i + 1) / 2 * 64 + (i + 1) % 2 * 16, x[(i + 1) & 1]);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            float *to = v[i / 2] + i % 2 * 16 + j;
+            const float2 y = add2({to[0], to[1]}, {x[i & 1][j], x[i & 1][j + 1]});
+            to[0] = y.x;
+            to[1] = y.y;
+        }
+    }
+}
 
 // ------------------------------------------------------------- the kernel
 
@@ -236,6 +276,9 @@ struct Second {
 //   J::finish(g, tile, row, sums, stage)      the epilogue of a warp's 32 rows: `row` is the
 //                                lane's (of the tile, in [0, 256)), `sums` the tensor memory
 //                                address of its columns, `stage` the warp's shared memory
+//   J::kClosed                   ring steps after which a sum is closed: the tensor cores begin the next one at 0,
+//                                and the epilogue's threads add them up, with rounding; `sums` are then the results,
+//                                [i][...] those of 32 columns from 32 part + 64 i on.  0: sums are never closed
 enum class Live { Rows, Sum, Columns };
 
 template <class J> struct Product {
@@ -483,50 +526,75 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
         uint32_t slot = 0, phase = 0, turn = 0;
         bool ok = true;
         while (ok && walk.next(&t)) {
-            const uint32_t half = turn & 1, to = sums + half * kTile;
-            if (!(ok = barrier_wait(sums_empty + 8 * half, ((turn >> 1) & 1) ^ 1, &s.gave_up)))
-                break;
-            sums_fence_after();
             const bool across = J::kAAcross || (J::kSecond && t.second);
             const uint64_t a0 = across ? slot_descriptor<true>(base) : slot_descriptor<false>(base),
                            b0 = slot_descriptor<J::kBAcross>(base + kRowBytes),
                            turn16 = across ? kDescriptorStep<true> : kDescriptorStep<false>;
             const uint32_t desc = across ? second : first;
-            for (int k = 0; k < t.steps; ++k) {
-                if (!(ok = barrier_wait(full + 8 * slot, phase, &s.gave_up)))
+            int k = 0;
+            do {
+                const uint32_t half = turn++ & 1, to = sums + half * kTile;
+                if (!(ok = barrier_wait(sums_empty + 8 * half, ((turn - 1) >> 1 & 1) ^ 1, &s.gave_up)))
                     break;
                 sums_fence_after();
-                const uint64_t at = slot * (SLOT >> 4);
+                const int begin = k, end = J::kClosed ? min(k + J::kClosed, t.steps) : t.steps;
+                for (; k < end; ++k) {
+                    if (!(ok = barrier_wait(full + 8 * slot, phase, &s.gave_up)))
+                        break;
+                    sums_fence_after();
+                    const uint64_t at = slot * (SLOT >> 4);
 #pragma unroll
-                for (int i = 0; i < kStep / 16; ++i)
-                    product_step(to, a0 + at + i * turn16, b0 + at + i * kDescriptorStep<J::kBAcross>, desc,
-                                 k > 0 || i > 0);
-                product_commit(empty + 8 * slot);
-                if (++slot == SLOTS) {
-                    slot = 0;
-                    phase ^= 1;
+                    for (int i = 0; i < kStep / 16; ++i)
+                        product_step(to, a0 + at + i * turn16, b0 + at + i * kDescriptorStep<J::kBAcross>,
+                                     desc, k > begin || i > 0);
+                    product_commit(empty + 8 * slot);
+                    if (++slot == SLOTS) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
                 }
-            }
-            if (ok)
-                product_commit(sums_full + 8 * half);
-            ++turn;
+                if (ok)
+                    product_commit(sums_full + 8 * half);
+            } while (ok && k < t.steps);
         }
     } else if (warp >= 4) {
         const int quarter = warp & 3;   // the tensor memory lanes that the warp may read
         uint32_t turn = 0, uses = 0;
-        while (walk.next(&t)) {
-            const uint32_t half = turn & 1;
-            if (!barrier_wait(sums_full + 8 * half, (turn >> 1) & 1, &s.gave_up, t.steps))
-                break;
-            sums_fence_after();
-            J::finish(g, t, static_cast<int>(rank) * kHalf + quarter * 32 + lane,
-                      sums + half * kTile + (static_cast<uint32_t>(quarter * 32) << 16),
-                      Stage{s.stage[warp - 4], s, (warp >> 2) - 1, uses});
+        const int row = static_cast<int>(rank) * kHalf + quarter * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const Stage stage{s.stage[warp - 4], s, (warp >> 2) - 1, uses};
+        const auto taken = [&](uint32_t half) {   // the sums are read
             sums_fence_before();
             __syncwarp();
             if (lane == 0)
                 barrier_arrive_cluster(in_first_cta(sums_empty + 8 * half));
             ++turn;
+        };
+        while (walk.next(&t)) {
+            if constexpr (J::kClosed > 0) {
+                constexpr int groups = (J::kN + 63) / 64;
+                float v[groups][32] = {};
+                bool ok = true;
+                for (int k = 0; k < t.steps; k += J::kClosed) {
+                    const uint32_t half = turn & 1;
+                    if (!(ok = barrier_wait(sums_full + 8 * half, (turn >> 1) & 1, &s.gave_up, J::kClosed)))
+                        break;
+                    sums_fence_after();
+                    if (32 * stage.part < J::kN)
+                        sums_add<groups>(sums + half * kTile + lanes + 32 * stage.part, v);
+                    taken(half);
+                }
+                if (!ok)
+                    break;
+                J::finish(g, t, row, v, stage);
+            } else {
+                const uint32_t half = turn & 1;
+                if (!barrier_wait(sums_full + 8 * half, (turn >> 1) & 1, &s.gave_up, t.steps))
+                    break;
+                sums_fence_after();
+                J::finish(g, t, row, sums + half * kTile + lanes, stage);
+                taken(half);
+            }
         }
     }
     __syncwarp();
@@ -549,6 +617,41 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
     }
     __syncthreads();
     cluster_barrier();
+}
+
+// What an epilogue is given: its sums' address, or closed sums.
+template <int CLOSED, int N>
+using Sums = std::conditional_t<CLOSED == 0, const uint32_t, float[(N + 63) / 64][32]>;
+
+// f(c, v) for the warp's groups of 32 columns c that begin below n (at most N).
+template <int CLOSED, int N, class F>
+__device__ __forceinline__ void for_columns(Sums<CLOSED, N> &sums, int part, int n, F f) {
+    if constexpr (CLOSED == 0) {
+        for (int c = 32 * part; c < N && c < n; c += 64) {
+            float v[32];
+            sums_load32(sums + c, v);
+            sums_ready(v);
+            f(c, v);
+        }
+    } else if constexpr (N <= kHalf) {
+        // not unrolled, the groups move up instead: a short call waits for its instructions (64 x 32000 x 1024
+        // 12.9 us, unrolled 14.8)
+#pragma unroll 1
+        for (int c = 32 * part; c < N && c < n; c += 64) {
+            f(c, sums[0]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                for (int group = 1; group < (N + 63) / 64; ++group)
+                    sums[group - 1][i] = sums[group][i];
+        }
+    } else {
+#pragma unroll
+        for (int group = 0; group < N / 64; ++group) {
+            const int c = 32 * part + 64 * group;
+            if (c < n)
+                f(c, sums[group]);
+        }
+    }
 }
 
 // ------------------------------------------------------------- loads, stores

@@ -1,0 +1,161 @@
+"""How exact the products' results are, where the elementwise bounds of tests/linear_ref.py are too
+wide to tell: exact logits, small losses, errors in norm, small and large values in fp16.
+
+The errors in norm are held to what rounding the 64-bit result to its type takes off (``own``).  A rounded
+operand of a product adds an error of the same relative size, independent of it: a root of two."""
+import math
+
+import pytest
+import torch
+
+from tests import linear_ref as R
+from tests.gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16 = torch.bfloat16, torch.float16
+DTYPES = [BF16, F16]
+
+
+@pytest.fixture(scope="module")
+def ga():
+    return require_gpu()
+
+
+@pytest.fixture(autouse=True)
+def no_wait_gave_up(ga):
+    yield
+    assert ga.device_status() == 0
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(*shape, seed, scale=1.0):
+    return scale * torch.randn(shape, generator=_gen(seed), device="cuda")
+
+
+def _whole(lo, hi, *shape, seed):
+    return torch.randint(lo, hi + 1, shape, generator=_gen(seed), device="cuda").float()
+
+
+def _rms(x):
+    return x.double().square().mean().sqrt().item()
+
+
+def _own(ref, dtype):
+    """What rounding to the type takes off, in norm."""
+    return (ref.to(dtype).double() - ref).norm().item()
+
+
+def _off(got, ref):
+    return (got.double() - ref).norm().item()
+
+
+def _losses(x, w, goal):
+    """(loss, lse, largest magnitude of a logit) of each token, in 64 bits."""
+    logits = x.double() @ w.double().T
+    lse = torch.logsumexp(logits, 1)
+    return lse - logits.gather(1, goal[:, None])[:, 0], lse, logits.abs().amax(1)
+
+
+# ----------------------------------------------------------------- exact logits
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens", [20, 90, 300])
+@pytest.mark.parametrize("k", [64, 1000, 4096, 16384])
+@pytest.mark.parametrize("kind", ["one-hot", "zeros", "whole"])
+def test_exact_logits(ga, kind, k, tokens, dtype):
+    """Logits that fp32 sums hold exactly, in any order: loss and lse are off by fp32's roundings alone."""
+    v = 700
+    if kind == "one-hot":
+        x = torch.zeros(tokens, k, device="cuda")
+        x[torch.arange(tokens), torch.randint(k, (tokens,), generator=_gen(1), device="cuda")] = 30
+        w = _whole(-64, 64, v, k, seed=2) / 64
+    elif kind == "zeros":          # all but the first 32 columns of a row
+        x = torch.zeros(tokens, k, device="cuda")
+        x[:, :32] = _whole(-3, 3, tokens, 32, seed=1)
+        w = _whole(-8, 8, v, k, seed=2) / 8
+    else:                          # multiples of 1/8 below 2^15
+        x = _whole(-2, 2, tokens, k, seed=1) / 8
+        w = _whole(-2, 2, v, k, seed=2)
+    x, w = x.to(dtype), w.to(dtype)
+    w[1] = w[0]                    # two rows alike: a target and its equal
+    goal = torch.randint(v, (tokens,), generator=_gen(3), device="cuda")
+    goal[0] = 0
+    kept = ga.linear_cross_entropy(x, w, goal)
+    loss, lse, most = _losses(x, w, goal)
+    # A logit l in powers of two is rounded three times at most on its way (the constant, the product, the
+    # difference to the row's maximum), 2^-24 of it each; so are the maximum and what is taken back from it.
+    # The sum of exponentials is within R.ARITH of its terms.
+    bound = most * 2.0 ** -21 + R.ARITH
+    assert ((kept.lse - lse).abs() <= bound).all()
+    assert ((kept.loss - loss).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens", [64, 320])
+@pytest.mark.parametrize("k", [64, 4096])
+def test_small_losses_keep_their_bits(ga, k, tokens, dtype):
+    """Confident tokens: losses from 1e-1 down to 1e-12, to a relative error."""
+    v = 256
+    at = torch.arange(tokens, device="cuda") % 64
+    x = torch.zeros(tokens, k, device="cuda")
+    x[torch.arange(tokens), at] = 8
+    w = _whole(-8, 8, v, k, seed=1) / 64                     # logits within 1
+    top = torch.floor(64 + 190 * torch.arange(64, device="cuda") / 63) / 64
+    w[torch.arange(64), torch.arange(64)] = top              # but the targets', 8 to 31.75
+    x, w = x.to(dtype), w.to(dtype)
+    kept = ga.linear_cross_entropy(x, w, at)
+    others = x.double() @ w.double().T
+    goal = others.gather(1, at[:, None])
+    others.scatter_(1, at[:, None], -math.inf)
+    loss = torch.log1p(torch.exp(others - goal).sum(1))
+    assert loss.max() < 0.5 and loss.min() < 1e-11
+    # loss = log1p(s 2^(m - t)): t is rounded to 2^-23 of it (constant and product), a relative error of the
+    # power; s and the functions within R.ARITH
+    assert ((kept.loss - loss).abs() <= loss * (2.0 ** -22 * goal[:, 0] + R.ARITH)).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens", [60, 500])
+@pytest.mark.parametrize("k", [64, 500, 1000, 2048, 4096, 10000])
+def test_losses_in_norm(ga, k, tokens, dtype):
+    """Dense rows.  The tensor cores cut fp32 sums off towards 0 after every 16 terms, half a unit of
+    the sum on average: over k terms 1.3e-9 k of a logit (24 bits, sums half of the last one on average,
+    0.72 for the mantissas' mean inverse).  Sums closed after 512 terms lose 6.6e-7 of theirs, and
+    their additions round to 2^-25 each on average, a random walk."""
+    v = 2000
+    w = _randn(v, k, seed=k, scale=2 * k ** -0.5).to(dtype)
+    goal = torch.randint(v, (tokens,), generator=_gen(k + 1), device="cuda")
+    x = _randn(tokens, k, seed=k + 2)
+    x += 3 * torch.rand(tokens, 1, generator=_gen(k + 3), device="cuda") * w[goal].float()
+    x = x.to(dtype)
+    kept = ga.linear_cross_entropy(x, w, goal)
+    loss, lse, most = _losses(x, w, goal)
+    bound = _rms(most) * (1.3e-9 * min(k, 512) + 2.0 ** -25 * (k / 512 + 1) ** 0.5 + 2.0 ** -24)
+    assert _rms(kept.lse - lse) <= bound
+    assert _rms(kept.loss - loss) <= bound
+
+
+# ------------------------------------------------------- gradients of the loss
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens", [30, 64, 200, 256, 400, 1000])
+def test_loss_gradients_in_norm(ga, tokens, dtype):
+    """Up to 256 tokens nothing but the results' own rounding is seen; past that the weight's
+    gradient has its rows' rounding too."""
+    k, v = 200, 3000
+    x = _randn(tokens, k, seed=tokens).to(dtype)
+    w = _randn(v, k, seed=1, scale=2 * k ** -0.5).to(dtype)
+    goal = torch.randint(v, (tokens,), generator=_gen(2), device="cuda")
+    gl = 16 * (0.25 + torch.rand(tokens, generator=_gen(3), device="cuda"))
+    kept = ga.linear_cross_entropy(x, w, goal)
+    gi, gw = ga.linear_cross_entropy_backward(gl, x, w, goal, kept)
+    y = torch.softmax(x.double() @ w.double().T, 1)
+    y[torch.arange(tokens), goal] -= 1
+    y *= gl.double()[:, None]
+    ref_in, ref_w = y @ w.double(), y.T @ x.double()
+    assert _off(gi, ref_in) <= 1.1 * _own(ref_in, dtype)
+    assert _off(gw, ref_w) <= (1.1 if tokens <= 256 else 1.5) * _own(ref_w, dtype)
