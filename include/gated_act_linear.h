@@ -123,10 +123,11 @@ size_t linear_cross_entropy_backward_workspace_bytes(const gated_act_vocabulary 
  * With p = exp(l - lse), c = 1 - p_target (from the loss) and a token's slope f = grad_loss c,
  *   grad_in      = f y W                     [T, k] contiguous, of type dtype;
  *   grad_weight  = sum_t y_t' (f_t in_t)     [V, k] contiguous, of type dtype,
- * where y = (p - [v = target]) / c and f in (by a power of two above the batch's largest |f|, which the
- * sums are multiplied with at their end) are each rounded once to the element type as operands of the
- * products; with T <= 256 what the second rounding takes off is an operand too.  In fp16, past that, a
- * token whose slope is below 2^-14 of the largest loses bits.
+ * where y = (p - [v = target]) / c and f in (by a power of two from the batch's largest: of |f| in bf16; of |f in| in fp16,
+ * whose upper end it is put to; the sums are multiplied with it at their end) are each rounded once to the element type
+ * as operands of the products; with T <= 256 what the second rounding takes off is an operand too.  In fp16 a product
+ * f in below 2^-29 of the batch's largest loses bits (the second operand, with T <= 256, below 2^-18 of it), and so does
+ * a y below 2^-28.
  *   grad_loss    [T] fp32, read on the device; not used at tokens that take no part.
  *   loss, lse    what linear_cross_entropy wrote.
  * The logits are computed again, in pieces of the vocabulary.

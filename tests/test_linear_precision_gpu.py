@@ -159,3 +159,50 @@ def test_loss_gradients_in_norm(ga, tokens, dtype):
     ref_in, ref_w = y @ w.double(), y.T @ x.double()
     assert _off(gi, ref_in) <= 1.1 * _own(ref_in, dtype)
     assert _off(gw, ref_w) <= (1.1 if tokens <= 256 else 1.5) * _own(ref_w, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens", [64, 256, 257, 700])
+def test_small_slopes_beside_large_ones(ga, tokens, dtype):
+    """Slopes over 20 powers of two in one batch.  Every token has its likely token in row 0 and a target
+    of its own, whose row of the weight's gradient is its slope times its row, all else below 2^-40
+    of the largest slope: each of these rows is right to its own rounding."""
+    k, v = 96, 1000
+    x = _randn(tokens, k, seed=5)
+    x[:, 0] = 8
+    w = _randn(v, k, seed=6, scale=0.5 * k ** -0.5)
+    w[:, 0] = 0
+    w[0] = 0
+    w[0, 0] = 4
+    x, w = x.to(dtype), w.to(dtype)
+    goal = 1 + torch.arange(tokens, device="cuda")
+    gl = 4096 * 2.0 ** (-20 * torch.arange(tokens, device="cuda") / tokens)
+    kept = ga.linear_cross_entropy(x, w, goal)
+    gi, gw = ga.linear_cross_entropy_backward(gl, x, w, goal, kept)
+    y = torch.softmax(x.double() @ w.double().T, 1)
+    y[torch.arange(tokens), goal] -= 1
+    y *= gl.double()[:, None]
+    ref_in, ref_w = y @ w.double(), y.T @ x.double()
+    for ref, got, rows in ((ref_w, gw, goal), (ref_in, gi, slice(None))):
+        off = (got.double() - ref)[rows].norm(dim=1)
+        own = (ref.to(dtype).double() - ref)[rows].norm(dim=1)
+        # y's own error is that of logits of 32, rounded to 2^-22 of it on their way
+        assert (off <= 1.1 * own + 32 * 2.0 ** -22 * ref[rows].norm(dim=1)).all()
+
+
+@pytest.mark.parametrize("tokens", [64, 700])
+@pytest.mark.parametrize("scale", [2.0 ** -30, 1.0, 2.0 ** 12])
+@pytest.mark.parametrize("size", [2.0 ** -12, 1.0, 2.0 ** 9])
+def test_sizes_of_rows_and_gradients_in_fp16(ga, size, scale, tokens):
+    """The elementwise bounds at rows of all sizes and gradients of all sizes in fp16."""
+    k, v = 72, 500
+    x = _randn(tokens, k, seed=7, scale=size).to(F16)
+    w = (_randn(v, k, seed=8, scale=2 * k ** -0.5) / size).to(F16)
+    x[1] = 0                                                  # a row of zeros, whatever its slope
+    goal = torch.randint(v, (tokens,), generator=_gen(9), device="cuda")
+    gl = scale * (0.25 + torch.rand(tokens, generator=_gen(10), device="cuda"))
+    kept = ga.linear_cross_entropy(x, w, goal)
+    gi, gw = ga.linear_cross_entropy_backward(gl, x, w, goal, kept)
+    (ri, bi), (rw, bw) = R.entropy_backward(gl.double(), x.double(), w.double(), goal, F16)
+    R.check(gi, ri, bi, "grad_in")
+    R.check(gw, rw, bw, "grad_weight")
