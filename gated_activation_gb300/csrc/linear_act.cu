@@ -4,7 +4,9 @@
 //   forward   (g, u) = in (Wg, Wu)',  out = act(g) u: one product kernel.  A pair's tile
 //             holds 128 columns of g and the same 128 of u, so that a thread has both.
 //   backward  dg = grad_out u act'(g), du = grad_out act(g) from the kept g and u (one pass
-//             over memory), then grad_in = (dg, du) W and grad_weight = (dg, du)' in.
+//             over memory; in fp16 under a power of two, from a pass before), then grad_in = (dg, du) W and grad_weight = (dg, du)' in.
+#include <cfloat>
+
 #include "few_rows.cuh"
 
 #include "gated_act_linear.h"
@@ -203,6 +205,7 @@ template <class T, int N, bool SPLIT> struct Gradients {
         CUtensorMap rows, in, tail;   // of the second product
         T *grad_in, *grad_weight;
         float *sums;                  // SPLIT: [E, shares, tile rows, tile columns, 256, 256]
+        const float *power;           // fp16: [E] what dg and du were divided by
         int k, half_steps, shares;    // ring steps of one half of the first sum
         bool vec_in, vec_weight;
     };
@@ -254,13 +257,14 @@ template <class T, int N, bool SPLIT> struct Gradients {
         }
         T *to = t.second ? g.j.grad_weight + (int64_t(t.b) * g.second.rows + top) * k + col
                          : g.j.grad_in + (int64_t(t.b) * g.capacity + top) * k + col;
+        const float power = std::is_same_v<T, f16> ? g.j.power[t.second ? t.b >> 1 : t.b] : 1.f;
         store_tile<N>(sums, stage, to, k, t.rows - top, k - col, t.second ? g.j.vec_weight : g.j.vec_in,
-                   1.f, t.steps == 0);
+                      power, t.steps == 0);
     }
 };
 
 template <class T> struct ShareArgs {
-    const float *sums;
+    const float *sums, *power;   // power: fp16
     T *out;
     const int32_t *live;
     int capacity, k, shares;
@@ -300,10 +304,11 @@ template <class T> __global__ void __launch_bounds__(256) join_shares(ShareArgs<
     for (int i = 0; i < 8; ++i)
         held[warp + 8 * i][lane] = v[i];
     __syncthreads();
+    const float power = std::is_same_v<T, f16> ? g.power[e] : 1.f;
     for (int i = warp; i < 32 && r0 + i < live; i += 8) {
         T *to = g.out + (int64_t(e) * g.capacity + r0 + i) * g.k + c0;
         for (int c = lane; c < 64 && c0 + c < g.k; c += 32)
-            to[c] = from_float<T>(held[c][i]);
+            to[c] = from_float<T>(held[c][i] * power);
     }
 }
 
@@ -317,9 +322,93 @@ template <class T> struct GateGradArgs {
     T *rows;              // [E, 2, padded, dp]
     T *tail;              // [E, 64, kp]
     const int32_t *live;
+    float *tops, *power;  // fp16: [E, n_tops] the blocks' shares of gradient_tops, [E] what dg and du are divided by
     int64_t grad_stride, grad_batch, in_stride, in_batch;
-    int T_, d, dp, k, kp, padded;
+    int T_, d, dp, k, kp, padded, n_tops, top_pieces;
 };
+
+// fp16's range is too short for dg and du as they come: they lost bits below 2^-14 and were infinite past 65504, where
+// the gradients, sums of products with them, need do neither.  So they are divided by a power of two per expert that puts
+// the largest just below 2^15.  A bound is enough for it: |act(g)| <= |g| and |act'(g)| < 1.13, and the scales bound g and
+// u by 2^15 steps.  (They are 2^14 at least in a block's largest element, so that the bound is a few times the
+// largest product; fp16's normal numbers reach 2^-29 of it.)  One pass over grad_out alone, whose rows are read as the
+// aligned vectors that hold them, four of a lane on their way; the columns of one may lie in two blocks (1001 x 2731
+// 5.3 us, element by element 12; 4096 x 8192 22 us, of which the bytes are 10).
+constexpr int kTops = 1024, kTopVectors = 4 * 32;   // blocks of an expert; vectors of a warp's piece of a row
+__global__ void __launch_bounds__(256) gradient_tops(GateGradArgs<f16> g) {
+    __shared__ float red[8];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = (g.d + kBlock - 1) / kBlock;
+    const int e = blockIdx.y, live = g.live ? min(max(g.live[e], 0), g.T_) : g.T_;
+    const int pieces = g.top_pieces;
+    const int64_t items = int64_t(live) * pieces;
+    float top = 0.f;
+    for (int64_t item = blockIdx.x * 8 + warp; item < items; item += gridDim.x * 8) {
+        const int i = static_cast<int>(item / pieces), piece = static_cast<int>(item - int64_t(i) * pieces);
+        const f16 *grad = g.grad + e * g.grad_batch + i * g.grad_stride;
+        const int before = static_cast<int>(reinterpret_cast<uintptr_t>(grad) & 15) / 2;
+        const uint8_t *scale = g.scales + (int64_t(e) * g.T_ + i) * 2 * blocks;
+        uint4 v[4];
+        float step[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = (piece * kTopVectors + 32 * j + lane) * 8 - before;   // of the vector's first element
+            v[j] = make_uint4(0, 0, 0, 0);
+            step[j] = 0.f;
+            if (c >= g.d || c + 8 <= 0)
+                continue;
+            const int first = max(c, 0), last = min(c + 8, g.d) - 1;
+            v[j] = c >= 0 && c + 8 <= g.d ? ld_stream(grad + c) : eight(grad + first, last + 1 - first, false);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {   // a NaN's block is NaN whatever it is divided by
+                const int b = (q ? last : first) / kBlock;
+                const uint32_t sg = scale[b], su = scale[blocks + b];
+                step[j] = fmaxf(step[j], fmaxf(sg == 255 ? 0.f : __uint_as_float(sg << 23),
+                                               su == 255 ? 0.f : 1.13f * __uint_as_float(su << 23)));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t most = 0;   // magnitudes of one type order as their bits; infinities and NaN stay what they are
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t lo = (&v[j].x)[q] & 0x7FFFu, hi = (&v[j].x)[q] >> 16 & 0x7FFFu;
+                most = max(most, max(lo < 0x7C00u ? lo : 0u, hi < 0x7C00u ? hi : 0u));
+            }
+            const float dy = __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
+            top = fmaxf(top, fminf(dy * step[j] * 32768.f, FLT_MAX));
+        }
+    }
+    const int bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_int(top));   // top >= 0
+    if (lane == 0)
+        red[warp] = __int_as_float(bits);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 8; ++i)
+            top = fmaxf(top, red[i]);
+        g.tops[e * g.n_tops + blockIdx.x] = top;
+    }
+}
+// The power of two of an expert, for all threads of a block of 8 warps.
+__device__ __forceinline__ float gradient_power(const GateGradArgs<f16> &g, int e) {
+    __shared__ int red[8];
+    const int thread = threadIdx.y * 32 + threadIdx.x;
+    int top = 0;
+#pragma unroll
+    for (int i = 0; i < kTops / 256; ++i)
+        if (thread + 256 * i < g.n_tops)
+            top = max(top, __float_as_int(g.tops[e * g.n_tops + thread + 256 * i]));
+    const int warps = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (threadIdx.x == 0)
+        red[threadIdx.y] = warps;
+    __syncthreads();
+    const int most = __reduce_max_sync(0xFFFFFFFFu, red[threadIdx.x & 7]);
+    const float power = most ? __int_as_float(max((most >> 23) + 1 - 15, 1) << 23) : 1.f;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && thread == 0)
+        g.power[e] = power;
+    return power;
+}
 
 // Eight columns of a row: what the gradients there are computed from.
 template <class T> struct GateGradIn {
@@ -340,6 +429,9 @@ __global__ void __launch_bounds__(256, 4) gate_gradients(GateGradArgs<T> g) {
     const int blocks = (g.d + kBlock - 1) / kBlock;
     const int e = blockIdx.z, live = g.live ? min(max(g.live[e], 0), g.T_) : g.T_;
     const int end = (live + kStep - 1) / kStep * kStep;
+    float inverse = 1.f;   // exact
+    if constexpr (std::is_same_v<T, f16>)
+        inverse = 1.f / gradient_power(g, e);
     // the partly live step of `in`, eight elements at a time over all of the expert's threads (32 experts of 717 x
     // 768 with k = 2048: 26 us; with an element at a time in the blocks of its rows 36.5)
     if (g.live && live % kStep) {
@@ -401,9 +493,13 @@ __global__ void __launch_bounds__(256, 4) gate_gradients(GateGradArgs<T> g) {
             uint32_t dg[4], du[4];
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-                const GateGrad2 m = act_grad<Act>(mul2(decode2(a[p]), both(in[j].sg)),
-                                                  mul2(decode2(b[p]), both(in[j].su)),
-                                                  {to_float(dy[2 * p]), to_float(dy[2 * p + 1])});
+                GateGrad2 m = act_grad<Act>(mul2(decode2(a[p]), both(in[j].sg)),
+                                            mul2(decode2(b[p]), both(in[j].su)),
+                                            {to_float(dy[2 * p]), to_float(dy[2 * p + 1])});
+                if constexpr (std::is_same_v<T, f16>) {
+                    m.gate = mul2(m.gate, both(inverse));
+                    m.up = mul2(m.up, both(inverse));
+                }
                 dg[p] = i < live ? pack2<T>(m.gate) : 0;
                 du[p] = i < live ? pack2<T>(m.up) : 0;
             }
@@ -665,7 +761,7 @@ struct BackwardParts {
     int64_t dp, kp, padded;
     void *rows, *tail;
     Division division;
-    float *sums;
+    float *sums, *tops, *power;
     int rc;
     BackwardParts(const gated_act_linear &a, void *workspace, cudaStream_t stream) : o(operands(a)) {
         dp = ceil_div64(a.d, 8) * 8;
@@ -678,6 +774,9 @@ struct BackwardParts {
         sums = ws.take<float>(division.shares > 1 ? uint64_t(4) * kTile * kTile * a.E * division.shares *
                                                         ceil_div64(a.T, kTile) * ceil_div64(a.k, kTile)
                                                   : 0);
+        const bool lifted = a.dtype == GATED_ACT_F16;
+        tops = ws.take<float>(lifted ? uint64_t(4) * kTops * a.E : 0);
+        power = ws.take<float>(lifted ? uint64_t(4) * a.E : 0);
         rc = addressable(&o, &ws, stream);
         bytes = ws.used;
     }
@@ -716,6 +815,7 @@ int run_gradients(void *grad_in, void *grad_weight, const gated_act_linear &a, c
     g.j.grad_in = static_cast<T *>(grad_in);
     g.j.grad_weight = static_cast<T *>(grad_weight);
     g.j.sums = w.sums;
+    g.j.power = w.power;
     g.j.shares = shares;
     g.j.k = static_cast<int>(a.k);
     g.j.vec_in = a.k % 8 == 0 && aligned(grad_in, 16);
@@ -723,7 +823,7 @@ int run_gradients(void *grad_in, void *grad_weight, const gated_act_linear &a, c
     rc = launch_product(g, a.E * (shares * ceil_div64(a.T, kTile) + 2 * g.second.m_tiles) * g.n_tiles, stream);
     if (!SPLIT || rc != GATED_ACT_OK)
         return rc;
-    const ShareArgs<T> j = {w.sums, static_cast<T *>(grad_in), a.n_rows, static_cast<int>(a.T),
+    const ShareArgs<T> j = {w.sums, w.power, static_cast<T *>(grad_in), a.n_rows, static_cast<int>(a.T),
                             static_cast<int>(a.k), shares};
     const int64_t blocks = a.E * ceil_div64(a.T, 32) * ceil_div64(a.k, 64);
     return cuda_status(launch_kernel(join_shares<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
@@ -757,6 +857,21 @@ int run_backward(void *grad_in, void *grad_weight, const void *grad_out, int64_t
     e.k = k;
     e.kp = static_cast<int>(w.kp);
     e.padded = static_cast<int>(w.padded);
+    e.tops = w.tops;
+    e.power = w.power;
+    e.n_tops = e.top_pieces = 0;
+    if constexpr (std::is_same_v<T, f16>) {
+        // rows off 16-byte boundaries begin up to seven elements into their first vector
+        const bool whole = aligned(grad_out, 16) && grad_stride % 8 == 0 && grad_batch % 8 == 0;
+        e.top_pieces = static_cast<int>(ceil_div64(a.d + (whole ? 0 : 7), 8 * kTopVectors));
+        const int64_t want = ceil_div64(int64_t(8) * device_sm_count(), E), most = ceil_div64(a.T * e.top_pieces, 8);
+        const int64_t blocks = want < most ? want : most;
+        e.n_tops = static_cast<int>(blocks < kTops ? blocks : kTops);
+        const int rc = cuda_status(launch_kernel(gradient_tops, dim3(static_cast<unsigned>(e.n_tops), static_cast<unsigned>(E)),
+                                                 dim3(256), 0, stream, 1, e));
+        if (rc != GATED_ACT_OK)
+            return rc;
+    }
     const bool vec = d % 8 == 0 && aligned(grad_out, 16) && aligned(codes, 16) &&
                      grad_stride % 8 == 0 && grad_batch % 8 == 0;
     const int64_t wide = ceil_div64(w.dp, 256), most = ceil_div64(w.padded, 8 * kGradRows);

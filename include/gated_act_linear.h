@@ -79,7 +79,9 @@ size_t linear_and_mul_backward_workspace_bytes(const gated_act_linear *a);
 
 /*
  * With dg = grad_out u act'(g) and du = grad_out act(g) at the kept g and u, each rounded once
- * to the element type as an operand of the products:
+ * to the element type as an operand of the products (in fp16 under a power of two per expert, so
+ * that neither small nor large ones leave the type's range; below 2^-25 of an expert's largest
+ * they lose bits):
  *   grad_in      = dg Wg + du Wu            [E, T, k] contiguous, of type dtype;
  *   grad_weight  = (dg' in, du' in)         [E, 2d, k] contiguous, of type dtype: sums over
  *                  the live rows (zeros for an expert without any).

@@ -206,3 +206,140 @@ def test_sizes_of_rows_and_gradients_in_fp16(ga, size, scale, tokens):
     (ri, bi), (rw, bw) = R.entropy_backward(gl.double(), x.double(), w.double(), goal, F16)
     R.check(gi, ri, bi, "grad_in")
     R.check(gw, rw, bw, "grad_weight")
+
+
+# ------------------------------------------------- gradients of the projections
+
+def _gated(ga, name, x, w, dy, n_rows=None):
+    forward, backward = ((ga.linear_silu_and_mul, ga.linear_silu_and_mul_backward) if name == "silu" else
+                         (ga.linear_gelu_and_mul, ga.linear_gelu_and_mul_backward))
+    _, kept = forward(x, w, n_rows=n_rows, keep=True)
+    return backward(dy, x, w, kept, n_rows=n_rows)
+
+
+def _exact(name, x, w, dy):
+    """(grad_in, grad_weight) in 64 bits."""
+    x, w, dy = x.double(), w.double(), dy.double()
+    d = w.shape[0] // 2
+    h = x @ w.T
+    a, slope, _ = R.act(name, h[:, :d])
+    rows = torch.cat([dy * h[:, d:] * slope, dy * a], 1)
+    return rows @ w, rows.T @ x
+
+
+# rows, k, d: whole sums, and grad_in's few long ones in shares
+SIZES = [(64, 256, 96), (700, 200, 300), (60, 72, 5000)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+@pytest.mark.parametrize("m,k,d", SIZES)
+def test_projection_gradients_in_norm(ga, m, k, d, name, dtype):
+    """The results' rounding and that of dg and du."""
+    x = _randn(m, k, seed=1).to(dtype)
+    w = _randn(2 * d, k, seed=2, scale=1.2 * k ** -0.5).to(dtype)
+    dy = _randn(m, d, seed=3).to(dtype)
+    for got, ref in zip(_gated(ga, name, x, w, dy), _exact(name, x, w, dy)):
+        assert _off(got, ref) <= 1.5 * _own(ref, dtype)
+
+
+@pytest.mark.parametrize("m,k,d", SIZES)
+def test_small_gradients_in_fp16(ga, m, k, d):
+    """dg and du around 2^-18, below fp16's normal numbers, where the gradients are normal numbers."""
+    dy = _randn(m, d, seed=3, scale=2.0 ** -14).to(F16)
+    # u of 2^-4, a weight of 8 for grad_in; u of 2^-2, rows of 8 for grad_weight
+    for which, size in ((0, 2.0 ** -4 / 8), (1, 8.0)):
+        x = _randn(m, k, seed=1, scale=size * (k ** -0.5 if which == 0 else 1)).to(F16)
+        w = _randn(2 * d, k, seed=2, scale=8 if which == 0 else 2.0 ** -5 * k ** -0.5).to(F16)
+        ref = _exact("silu", x, w, dy)[which]
+        assert _own(ref, F16) <= 2.0 ** -11 * ref.norm()      # the type holds the result
+        assert _off(_gated(ga, "silu", x, w, dy)[which], ref) <= 1.5 * _own(ref, F16)
+
+
+@pytest.mark.parametrize("k,d", [(256, 96), (72, 5000)])
+def test_large_gradients_in_fp16(ga, k, d):
+    """dg and du past 65504, where the weight's gradient is not."""
+    x = _randn(4, k, seed=1, scale=0.004).to(F16)
+    w = _randn(2 * d, k, seed=2, scale=5 / 0.004 * k ** -0.5).to(F16)
+    dy = _randn(4, d, seed=3, scale=32000).clamp(-60000, 60000).to(F16)
+    gi, gw = _gated(ga, "silu", x, w, dy)
+    ref_in, ref = _exact("silu", x, w, dy)
+    h = x.double() @ w.double().T
+    assert (dy.double() * h[:, d:]).abs().max() > 2 * 65504 and ref.abs().max() < 60000
+    # Four rows of products of normals: a few large terms are most of a norm, and it matters where their mantissas m
+    # in [1, 2) lie.  A rounding is off by 2^-11 / (sqrt(3) m) of the value, root mean square: dg's and du's by up to
+    # twice the result's own, together up to sqrt(1 + 4) = 2.24 times it.  (This kernel and its arithmetic in 64 bits
+    # with dg and du rounded agree to 1e-3 of that: 1.38 to 1.54 for eight seeds.)
+    assert _off(gw, ref) <= 2.25 * _own(ref, F16)
+    assert not torch.isnan(gi).any()
+    far = ref_in.abs() > 70000
+    assert (gi[far].double().sign() == ref_in[far].sign()).all() and torch.isinf(gi[far]).all()
+    near = ref_in.abs() < 60000
+    assert torch.isfinite(gi[near]).all()
+
+
+def test_experts_of_different_sizes_in_fp16(ga):
+    """Each expert's gradients to their own rounding, beside others 2^20 times as large; what lies behind
+    the live rows, and an expert without any, have no part in it."""
+    sizes, counts = [2.0 ** -14, 1.0, 2.0 ** 6, 2.0 ** -7, 1.0], [70, 100, 33, 64, 0]
+    e, m, k, d = len(sizes), 100, 128, 72
+    x = _randn(e, m, k, seed=1).to(F16)
+    w = _randn(e, 2 * d, k, seed=2, scale=1.2 * k ** -0.5).to(F16)
+    dy = _randn(e, m, d, seed=3)
+    for i, s in enumerate(sizes):
+        dy[i] *= s
+    dy = dy.to(F16)
+    for i, n in enumerate(counts):
+        x[i, n:] = float("nan")
+        dy[i, n:] = 60000
+    n_rows = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    gi, gw = _gated(ga, "gelu", x, w, dy, n_rows)
+    for i, n in enumerate(counts):
+        ri, rw = _exact("gelu", x[i, :n], w[i], dy[i, :n])
+        assert _off(gi[i, :n], ri) <= 1.5 * _own(ri, F16), i
+        assert _off(gw[i], rw) <= 1.5 * _own(rw, F16), i
+
+
+def test_special_gradients_in_fp16(ga):
+    """An infinity or a NaN in grad_out reaches its own row of grad_in and its own columns' rows of grad_weight, and
+    no others; rows of zeros have gradients of zeros."""
+    x = _randn(80, 64, seed=1).to(F16)
+    w = _randn(2 * 40, 64, seed=2, scale=0.1).to(F16)
+    dy = _randn(80, 40, seed=3).to(F16)
+    dy[20] = 0
+    clean = _gated(ga, "silu", x, w, dy)
+    dy[3, 7], dy[70, 11] = float("inf"), float("nan")
+    gi, gw = _gated(ga, "silu", x, w, dy)
+    rows = torch.ones(80, dtype=torch.bool, device="cuda")
+    rows[[3, 70]] = False
+    cols = torch.ones(80, dtype=torch.bool, device="cuda")
+    cols[[7, 11, 47, 51]] = False
+    assert (gi[20] == 0).all()
+    assert not torch.isfinite(gi[~rows]).any() and not torch.isfinite(gw[~cols]).any()
+    # the power of two under which dg and du are rounded may follow their largest one, which changes no bit
+    # of a normal number
+    for got, want, keep in ((gi, clean[0], rows), (gw, clean[1], cols)):
+        assert (got[keep] - want[keep]).abs().max() <= 2.0 ** -10 * want[keep].abs().max()
+    zero = _gated(ga, "silu", x, w, torch.zeros_like(dy))
+    assert not zero[0].any() and not zero[1].any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_an_outlier_among_32_columns(ga, dtype):
+    """The projections are kept under one scale for 32 columns: beside one of 1000 times their size the other 31
+    keep 2^-16 of its size, 1.5% of theirs, in the factors of their gradients, and no more is off."""
+    m, k, d = 300, 128, 96
+    x = _randn(m, k, seed=1).to(dtype)
+    w = _randn(2 * d, k, seed=2, scale=k ** -0.5)
+    w[[5, d + 40]] *= 1000
+    w = w.to(dtype)
+    dy = _randn(m, d, seed=3, scale=1 if dtype == BF16 else 2.0 ** -6).to(dtype)
+    got, want = _gated(ga, "silu", x, w, dy), R.backward("silu", dy.double(), x.double(), w.double(), dtype)
+    R.check(got[0], *want[0], "grad_in")
+    R.check(got[1], *want[1], "grad_weight")
+    ref = _exact("silu", x, w, dy)[1]
+    off = (got[1].double() - ref).norm(dim=1) / ref.norm(dim=1)
+    # columns of blocks without an outlier: half a step of the result and of dg or du
+    far = [i for i in range(d) if i // 32 not in (0, 1)]
+    assert (off[far + [d + i for i in far]] <= 2 * torch.finfo(dtype).eps / 2).all()
+    assert (off <= 0.03 + torch.finfo(dtype).eps).all()
