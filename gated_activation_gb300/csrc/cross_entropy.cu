@@ -296,7 +296,7 @@ template <class T> __global__ void __launch_bounds__(kTokenThreads) live_tokens(
 template <class G>
 __device__ __forceinline__ void load_logits(const G &g, const Tile &t, int first, int step, uint32_t rank,
                                             uint32_t a, uint32_t b, uint32_t bar) {
-    load_along(a, t.rows < g.capacity ? &g.other : &g.a, bar, step * kStep,
+    load_along(a, t.rows < g.capacity ? &g.j.packed : &g.a, bar, step * kStep,
                t.m0 + static_cast<int>(rank) * kHalf, 0, 0);
     load_along(b, &g.b, bar, step * kStep, first + t.n0 * kTile + static_cast<int>(rank) * kHalf, 0, 0);
 }
@@ -306,10 +306,11 @@ __device__ __forceinline__ void load_logits(const G &g, const Tile &t, int first
 // calls (the power limit).  A tile's exponentials take 1.7 us, hidden from k = 384 on.
 template <class T, int CLOSED> struct Statistics {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
+    static constexpr bool kBAcross = false, kSecond = false;
     static constexpr int kN = kTile, kRows = kTile, kClosed = CLOSED;
     static constexpr Live kLive = Live::Rows;
     struct Args {
+        CUtensorMap packed;  // the live rows, where some token is dead
         const int32_t *goal;
         float2 *part;        // [capacity, 2 tiles]: maximum, sum of each warp's columns
         int V;
@@ -363,7 +364,7 @@ template <class T, int CLOSED> struct Statistics {
 // tokens in shared memory; two lanes then take half of the rows of a token each.
 template <class T, int N, int CLOSED> struct TurnedStatistics {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
+    static constexpr bool kBAcross = false, kSecond = false;
     static constexpr int kN = N, kRows = kTile, kClosed = CLOSED;
     static constexpr Live kLive = Live::Columns;
     struct Args {
@@ -427,10 +428,11 @@ template <class T> constexpr float kLift = std::is_same_v<T, f16> ? 16384.f : 1.
 // 38912 x 2048 in 337 us (1.94 PFLOP/s).
 template <class T, int CLOSED> struct Slopes {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
+    static constexpr bool kBAcross = false, kSecond = false;
     static constexpr int kN = kTile, kRows = kTile, kClosed = CLOSED;
     static constexpr Live kLive = Live::Rows;
     struct Args {
+        CUtensorMap packed;
         Tokens t;
         T *y;              // [padded, piece]
         int V, first, piece;
@@ -497,7 +499,7 @@ struct Shares {
 // 4096 x 38912 x 2048 in 665 us (1.96 PFLOP/s); 4096 x 8192 x 2048 in 168 us, as two launches 182.
 template <class T> struct PieceGradients {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = true, kSecond = true;
+    static constexpr bool kBAcross = true, kSecond = true;
     static constexpr int kN = kTile, kRows = kTile, kClosed = 0;
     static constexpr Live kLive = Live::Rows;
     struct Args {
@@ -920,8 +922,10 @@ template <class T> int encode_rows(CUtensorMap *place, CUtensorMap *packed, cons
 template <class T, int CLOSED> struct Upright {
     static int set(Product<Statistics<T, CLOSED>> *g, const Parts &w, const gated_act_vocabulary &a) {
         g->n_tiles = static_cast<int>(ceil_div64(a.V, kTile));
-        g->j = {w.t.goal, w.part, static_cast<int>(a.V)};
-        const int rc = encode_rows<T>(&g->a, &g->other, w, kHalf);
+        g->j.goal = w.t.goal;
+        g->j.part = w.part;
+        g->j.V = static_cast<int>(a.V);
+        const int rc = encode_rows<T>(&g->a, &g->j.packed, w, kHalf);
         return rc == GATED_ACT_OK ? encode_map(&g->b, w.weight, kHalf, std::is_same_v<T, bf16>) : rc;
     }
     using Job = Statistics<T, CLOSED>;
@@ -934,7 +938,6 @@ template <class T, int N, int CLOSED> struct Turned {
         g->rows = static_cast<int>(a.V);
         g->j = {targets_of(a), w.part, static_cast<int>(ceil_div64(a.V, kTile))};
         const int rc = encode_map(&g->b, w.copy ? w.packed : w.in, N / 2, std::is_same_v<T, bf16>);
-        g->other = g->b;
         return rc == GATED_ACT_OK ? encode_map(&g->a, w.weight, kHalf, std::is_same_v<T, bf16>) : rc;
     }
     using Job = TurnedStatistics<T, N, CLOSED>;
@@ -995,7 +998,7 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
     Product<Slopes<T, CLOSED>> s;
     Product<PieceGradients<T>> g;
     if (rc == GATED_ACT_OK)
-        rc = encode_rows<T>(&s.a, &s.other, w, kHalf);
+        rc = encode_rows<T>(&s.a, &s.j.packed, w, kHalf);
     if (rc == GATED_ACT_OK)
         rc = encode_map(&s.b, w.weight, kHalf, is_bf16);
     if (rc == GATED_ACT_OK)
@@ -1008,8 +1011,11 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
         set_rows(&s, w, a);
         s.n_tiles = static_cast<int>(ceil_div64(cols, kTile));
         s.steps = static_cast<int>(ceil_div64(a.k, kStep));
-        s.j = {w.t, static_cast<T *>(w.y), static_cast<int>(a.V), static_cast<int>(first),
-               static_cast<int>(w.piece)};
+        s.j.t = w.t;
+        s.j.y = static_cast<T *>(w.y);
+        s.j.V = static_cast<int>(a.V);
+        s.j.first = static_cast<int>(first);
+        s.j.piece = static_cast<int>(w.piece);
         rc = launch_product(s, ceil_div64(a.T, kTile) * s.n_tiles, stream);
         if (rc == GATED_ACT_OK)
             rc = encode_map(&g.a, y, kHalf, is_bf16);
@@ -1017,7 +1023,6 @@ int run_backward(void *grad_in, void *grad_weight, const float *grad_loss, const
             rc = encode_map(&g.j.y, y, kStep, is_bf16);
         if (rc != GATED_ACT_OK)
             return rc;
-        g.other = g.a;
         set_rows(&g, w, a);
         g.batches = kShares;
         g.n_tiles = w.shares.n_tiles;

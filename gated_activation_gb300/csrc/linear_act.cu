@@ -65,7 +65,7 @@ __device__ __forceinline__ uint32_t encode32(uint32_t (&w)[16], const float (&v)
 // 5 us for a tile of 128 x 128 per CTA (8 warps), against 5 ns per summed element in the main loop.
 template <class Act, class T, int N, bool KEEP> struct Forward {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
+    static constexpr bool kBAcross = false, kSecond = false;
     static constexpr int kN = N, kRows = kTile;
     static constexpr int kClosed = 0;
     static constexpr Live kLive = Live::Rows;
@@ -127,7 +127,7 @@ template <class Act, class T, int N, bool KEEP> struct Forward {
 // upright 117 us).
 template <class Act, class T, int N> struct Swapped {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = false, kSecond = false;
+    static constexpr bool kBAcross = false, kSecond = false;
     static constexpr int kN = N, kRows = kHalf;
     static constexpr int kClosed = 0;
     static constexpr Live kLive = Live::Columns;
@@ -197,7 +197,7 @@ template <class Act, class T, int N> struct Swapped {
 // 32 experts of 2048 -> 768, 70% of 1024 rows, 167 us (1.73 PFLOP/s of the live rows).
 template <class T, int N, bool SPLIT> struct Gradients {
     using Elem = T;
-    static constexpr bool kAAcross = false, kBAcross = true, kSecond = true;
+    static constexpr bool kBAcross = true, kSecond = true;
     static constexpr int kN = N, kRows = kTile;
     static constexpr int kClosed = 0;
     static constexpr Live kLive = Live::Rows;
@@ -651,13 +651,11 @@ Division division_of(const gated_act_linear &a) {
 }
 
 // The parts of a forward product that its jobs share.
-template <class J> int set_forward(Product<J> *g, const gated_act_linear &a, const int32_t *live) {
-    g->other = g->a;
+template <class J> void set_forward(Product<J> *g, const gated_act_linear &a, const int32_t *live) {
     g->live = live;
     g->batches = static_cast<int>(a.E);
     g->capacity = static_cast<int>(a.T);
     g->steps = static_cast<int>(ceil_div64(a.k, kStep));
-    return GATED_ACT_OK;
 }
 
 template <class Act, class T, int N, bool KEEP>
@@ -801,7 +799,6 @@ int run_gradients(void *grad_in, void *grad_weight, const gated_act_linear &a, c
         rc = encode_map(&g.j.tail, a.n_rows ? tail : o.in, kStep, is_bf16);
     if (rc != GATED_ACT_OK)
         return rc;
-    g.other = g.a;
     g.live = a.n_rows;
     g.batches = static_cast<int>(a.E) * shares;
     g.capacity = g.rows = static_cast<int>(a.T);

@@ -261,7 +261,7 @@ struct Second {
 
 // A job J describes a product and what happens to it:
 //   J::Elem                      bf16 or f16
-//   J::kAAcross, J::kBAcross     operand rows lie across the sum
+//   J::kBAcross                  the second operand's rows lie across the sum (the first product's first ones along it)
 //   J::kN                        columns of a tile
 //   J::kRows                     rows that a tile counts for
 //   J::Args                      what its functions read
@@ -270,7 +270,7 @@ struct Second {
 //                                first's: in one launch the SM pairs share both out more evenly
 //   J::batch_of(g, b, second)    index of the live count of a batch
 //   J::batches(g)                how many there are, of at most g.batches
-//   J::steps_of(g, tile)         ring steps of a tile, where live counts do not bound them
+//   J::steps_of(g, tile)         ring steps of a tile of the first product
 //   J::second_steps(g, live)     with kSecond: those of a second tile
 //   J::load(g, tile, step, rank, a, b, bar)   issues the step's copies of one CTA
 //   J::finish(g, tile, row, sums, stage)      the epilogue of a warp's 32 rows: `row` is the
@@ -279,10 +279,10 @@ struct Second {
 //   J::kClosed                   ring steps after which a sum is closed: the tensor cores begin the next one at 0,
 //                                and the epilogue's threads add them up, with rounding; `sums` are then the results,
 //                                [i][...] those of 32 columns from 32 part + 64 i on.  0: sums are never closed
-enum class Live { Rows, Sum, Columns };
+enum class Live { Rows, Columns };
 
 template <class J> struct Product {
-    CUtensorMap a, b, other;
+    CUtensorMap a, b;
     const int32_t *live;   // null: `capacity` everywhere
     int batches, capacity, rows, n_tiles, steps;
     Second second;
@@ -379,10 +379,7 @@ template <class J> struct Walk {
             place(t, at - s.first[b] * g.n_tiles, s.first[b + 1] - s.first[b], g.n_tiles);
             t->live = g.live_of(J::batch_of(g, b, false));
             t->rows = J::kLive == Live::Rows ? t->live : g.rows;
-            if constexpr (J::kLive == Live::Sum)
-                t->steps = (t->live + kStep - 1) / kStep;
-            else
-                t->steps = J::steps_of(g, *t);
+            t->steps = J::steps_of(g, *t);
             at += step;
             return true;
         }
@@ -521,12 +518,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
             }
         }
     } else if (warp == 1 && rank == 0 && elected()) {
-        constexpr uint32_t first = product_descriptor<typename J::Elem, J::kN, J::kAAcross, J::kBAcross>();
+        constexpr uint32_t first = product_descriptor<typename J::Elem, J::kN, false, J::kBAcross>();
         constexpr uint32_t second = product_descriptor<typename J::Elem, J::kN, true, J::kBAcross>();
         uint32_t slot = 0, phase = 0, turn = 0;
         bool ok = true;
         while (ok && walk.next(&t)) {
-            const bool across = J::kAAcross || (J::kSecond && t.second);
+            const bool across = J::kSecond && t.second;
             const uint64_t a0 = across ? slot_descriptor<true>(base) : slot_descriptor<false>(base),
                            b0 = slot_descriptor<J::kBAcross>(base + kRowBytes),
                            turn16 = across ? kDescriptorStep<true> : kDescriptorStep<false>;
