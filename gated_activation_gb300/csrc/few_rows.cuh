@@ -1,4 +1,4 @@
-// Gated projections of a few rows (up to 32): reading the weight is all the time there is.
+// Gated projections of a few rows (up to 16): reading the weight is all the time there is.
 //
 // A warp holds the sums of 8 columns, gate and up, for every row: the tensor cores' 16 x 8 x 16
 // product (mma.sync) takes 8 gate rows of the weight as its first eight rows and the same 8 up rows
@@ -11,16 +11,16 @@
 // `split` warps of a block share the sum; they add up through shared memory, in a fixed order.
 //
 // Measured: 1 row of 2048 -> 768 in 4.5 us a call (5.3 us alone; the big tiles took 13.6), of which the 6 MB are
-// 0.9 us and the rest launch, one chain of loads and the host.  For weights with a turned tile for every pair
-// of SMs it is not used: 16 rows of 4096 -> 16384 took 80 us here, as every warp reads the rows' 128 KB through
-// L1 again, and 44 us there.
+// 0.9 us and the rest launch, one chain of loads and the host.  It stands back where there are more rows or turned tiles
+// (`few` in linear_act.cu has the figures): every warp reads the rows through L1 again, at 16 rows as many bytes as of
+// its weight, and 16 rows of 4096 -> 16384 took 80 us here and 44 us there.
 #pragma once
 
 #include "product.cuh"
 
 namespace gact {
 
-constexpr int kFewRows = 32;
+constexpr int kFewRows = 16;
 constexpr int kFewUnroll = 4;   // 16-byte loads of a row on their way per thread: 256 bytes a warp
 
 template <class T> struct FewArgs {
@@ -151,7 +151,7 @@ int launch_few_rows(const FewArgs<T> &args, int64_t E, bool vec, cudaStream_t st
         auto kernel = vec ? few_rows<Act, T, NT, true> : few_rows<Act, T, NT, false>;
         return cuda_status(launch_kernel(kernel, grid, dim3(256), 0, stream, 1, g));
     };
-    return g.rows <= 8 ? go(Const<1>{}) : g.rows <= 16 ? go(Const<2>{}) : go(Const<4>{});
+    return g.rows <= 8 ? go(Const<1>{}) : go(Const<2>{});
 }
 
 }  // namespace gact

@@ -574,11 +574,26 @@ int addressable(Operands *o, Carve *ws, cudaStream_t stream) {
     return n && ws->start ? launch_pack(to[0], from[0], to[1], from[1], stream) : GATED_ACT_OK;
 }
 
-// Rows without a checkpoint have other kernels where they are few: with up to 32 that leave pairs of
-// SMs without one of the turned tiles, the one that streams the weight through registers; else, with
-// up to 128, the turned product.
+// Rows without a checkpoint have other kernels where they are few: up to 16 of a weight of few turned tiles the one
+// that streams it through registers, else up to 128 the turned product.  A turned tile is one long chain of copies, and a
+// pair of SMs without a tile idles; the streaming kernel has warps on every SM, but its time grows with the
+// rows, and in steps with its rounds of blocks: up to 25 tiles, a third of the pairs, are one round.  Weights off 16-byte
+// boundaries are read in place there and copied first for the turned product: any number of tiles below the pairs'.
+// Measured in us for 8, 16 and 32 rows (the streaming kernel's third figure is of a form that was not kept):
+//                 tiles  floor  streaming         turned
+//   256  -> 1024      8    0.2   2.5  3.4  5.1     4.3  4.3  4.4
+//   2048 -> 768       6    0.9   4.7  6.4  9.9     8.3  8.3  8.4
+//   2048 -> 2048     16    2.5   6.3  8.0 11.4     8.4  8.5  8.5
+//   4096 -> 2560     20    6.2  11.8 15.4 36.2    13.0 13.0 13.1
+//   2048 -> 4096     32    5.0  11.6 15.0 21.0     9.6  9.7  9.7
+//   4096 -> 8192     64   19.8  32.4 42.5 74.4    23.5 23.7 23.7
+//   2049 -> 2045     16    2.5  13.5 16.4 19.8    18.8 19.1 19.2   (off 16-byte boundaries)
+//   4097 -> 4093     32    9.9  39.0 50.7 69.2    46.4 46.9 47.0
 bool few(const gated_act_linear &a, bool keep) {
-    return !keep && a.T <= kFewRows && a.E * ceil_div64(a.d, kHalf) < sm_pairs();
+    const Operands o = operands(a);
+    const int64_t tiles = a.E * ceil_div64(a.d, kHalf);
+    const bool in_place = tma_addressable(o.in) && tma_addressable(o.weight);
+    return !keep && a.T <= kFewRows && (in_place ? tiles <= sm_pairs() / 3 : tiles < sm_pairs());
 }
 
 uint64_t forward_bytes(const gated_act_linear &a, bool keep) {

@@ -208,6 +208,23 @@ def test_sizes_of_rows_and_gradients_in_fp16(ga, size, scale, tokens):
     R.check(gw, rw, bw, "grad_weight")
 
 
+# ------------------------------------------------------- kernels for few rows
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,k,d,experts", [
+    (16, 72, 3200, 1), (16, 72, 3201, 1), (17, 72, 3200, 1), (8, 72, 3200, 1), (9, 1000, 128, 25), (16, 64, 100, 26),
+    (16, 71, 3200, 1), (16, 71, 3329, 1), (17, 71, 500, 1), (3, 71, 9700, 1), (3, 71, 9800, 1), (5, 33, 64, 75),
+    (5, 33, 64, 76), (20, 1024, 300, 1), (32, 257, 700, 1)])
+def test_borders_between_kernels_of_few_rows(ga, m, k, d, experts, dtype):
+    """Both sides of the borders, in rows and in tiles, on 16-byte boundaries (k = 72, 1000, 64, 1024) and off them."""
+    x = _randn(experts, m, k, seed=m + k).to(dtype)
+    w = _randn(experts, 2 * d, k, seed=d, scale=1.3 * k ** -0.5).to(dtype)
+    out = ga.linear_silu_and_mul(x, w)
+    for i in range(0, experts, 5):
+        ref, bound, *_ = R.forward("silu", x[i].double(), w[i].double(), dtype)
+        R.check(out[i], ref, bound, "out")
+
+
 # ------------------------------------------------- gradients of the projections
 
 def _gated(ga, name, x, w, dy, n_rows=None):
