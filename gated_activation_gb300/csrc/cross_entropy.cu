@@ -302,7 +302,7 @@ __device__ __forceinline__ void load_logits(const G &g, const Tile &t, int first
 }
 
 // Maximum (in powers of two) and sum of exponentials of each row over a tile's columns.  2 T V k operations,
-// bound by the tensor cores: 8192 x 65536 x 2048 in 1.09 ms alone (2.0 PFLOP/s), 1.28 ms in a stream of such
+// bound by the tensor cores: 8192 x 65536 x 2048 in 1.11 ms alone (1.98 PFLOP/s), 1.25 ms in a stream of such
 // calls (the power limit).  A tile's exponentials take 1.7 us, hidden from k = 384 on.
 template <class T, int CLOSED> struct Statistics {
     using Elem = T;
@@ -360,7 +360,7 @@ template <class T, int CLOSED> struct Statistics {
 };
 
 // The same for up to N tokens, which would leave most of a 256-row tile empty, with the roles turned
-// round: the vocabulary's rows are the tile's, the tokens its columns (64 x 32000 x 1024: 12.6 us, upright 17.3).  A warp turns its 32 rows of 16
+// round: the vocabulary's rows are the tile's, the tokens its columns (64 x 32000 x 1024: 12.9 us, upright 17.3).  A warp turns its 32 rows of 16
 // tokens in shared memory; two lanes then take half of the rows of a token each.
 template <class T, int N, int CLOSED> struct TurnedStatistics {
     using Elem = T;
@@ -583,7 +583,7 @@ template <class T> struct JoinArgs {
 };
 
 // WARPS warps per live row: one, or eight where there are few.  The target's logit is summed here in fp32 with rounding: the tensor cores cut
-// sums off, which at k = 2048 left it 1e-6 of its size too small.  With the other columns' sum s of
+// sums off, 5e-7 of its size even where they are closed.  With the other columns' sum s of
 // 2^(l - m), loss = log(1 + s 2^(m - l_target)) where the target is above them, so that a confident
 // token's small loss keeps its bits.
 template <class T, int WARPS> __global__ void __launch_bounds__(256) join_statistics(JoinArgs<T> g) {

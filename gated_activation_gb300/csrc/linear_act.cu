@@ -60,7 +60,7 @@ __device__ __forceinline__ uint32_t encode32(uint32_t (&w)[16], const float (&v)
 // ------------------------------------------------------------------- products
 
 // The forward product.  4 T k d operations; bound by the tensor cores where k is long (2048 x 4096 -> 16384:
-// 275 us alone, cuBLAS's rate and more), by the epilogue where it is short: per element one exponential, one
+// 285 us alone, cuBLAS's rate and more), by the epilogue where it is short: per element one exponential, one
 // reciprocal and, for the checkpoint, a maximum, a product and three rounds through shared memory, 4 to
 // 5 us for a tile of 128 x 128 per CTA (8 warps), against 5 ns per summed element in the main loop.
 template <class Act, class T, int N, bool KEEP> struct Forward {
@@ -193,7 +193,7 @@ template <class Act, class T, int N> struct Swapped {
 // a copy with zeros there, as what lies past the live rows may be anything.
 // SPLIT: the first product's sums are divided into shares, fp32 tiles as the threads hold them (256 x 256,
 // column after column), which join_shares adds up.
-// 8 T k d operations in one launch: 4096 rows of 4096 -> 8192 in 560 us alone (1.96 PFLOP/s; two launches 620),
+// 8 T k d operations in one launch: 4096 rows of 4096 -> 8192 in 566 us alone (1.94 PFLOP/s; two launches 620),
 // 32 experts of 2048 -> 768, 70% of 1024 rows, 167 us (1.73 PFLOP/s of the live rows).
 template <class T, int N, bool SPLIT> struct Gradients {
     using Elem = T;
@@ -607,8 +607,8 @@ uint64_t forward_bytes(const gated_act_linear &a, bool keep) {
 
 // Columns of a tile, 256 or 128: those for which the pair of SMs with the most work has less of it.  Work is
 // counted in ring steps of 256 columns (0.30 us); a step of 128 is 0.59 of one in the forward product and
-// 0.68 in the gradients', both operands of which lie across the sum (2048 x 4096 -> 16384: 274 and 323 us
-// forward, 560 and 780 backward).  A tile is not done before the one in front of it has left through
+// 0.68 in the gradients', both operands of which lie across the sum (2048 x 4096 -> 16384, both in one
+// session: 274 and 323 us forward, 560 and 780 backward).  A tile is not done before the one in front of it has left through
 // its epilogue: 11 steps of 256 columns (with the checkpoint 21, a gradient 9), 7.4 (11, 6) of 128.
 // Measured where it decides: 512 x 4096 -> 2048 forward 23.2 us with 256 columns and 14.8 with 128, 256 x 2048 -> 9728
 // 16.5 and 17.5, backward 98.5 and 70.6, 512 x 4096 -> 2048 backward 29.2 and 40.8.

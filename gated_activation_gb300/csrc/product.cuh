@@ -7,9 +7,9 @@
 //              memory slots (TMA, 128-byte swizzle), in both CTAs;
 //   warp 1     of the pair's first CTA issues the products (tcgen05.mma of the two
 //              CTAs together, 256 x 256 x 16), whose sums lie in tensor memory;
-//   warps 4-11 read finished sums back, a row per thread and every second 32 columns, and
-//              run the epilogue while the next tile is summed into the other half of the
-//              tensor memory.
+//   warps 4-11 read finished sums back (of some jobs in parts, which they add up), a row
+//              per thread and every second 32 columns, and run the epilogue while the
+//              next tile is summed into the other half of the tensor memory.
 // An operand is stored with its rows along the summed dimension (as the activations
 // and weights of a linear layer are in its forward product) or across it (as they are
 // in the products of its gradients); the TMA box and the descriptors differ, no data
@@ -19,12 +19,14 @@
 // copies, 64 bytes per cycle and SM from L2; a step of 128 columns takes 48 KB for half the products, and
 // measured 0.59 to 0.68 of the time.  The ring's six slots are 3000 cycles, twice a copy's latency under load.
 // Measured on GB300 (cuBLAS: 1.88 PFLOP/s in short runs, 1.72 under the power limit): 2048 x 32768 x 4096 in
-// 275 us alone (2.0 PFLOP/s), 318 us in a stream of such calls; tensor cores active 91% of the cycles.
+// 285 us alone (1.93 PFLOP/s), 314 us in a stream of such calls; tensor cores active 89% of the cycles.
 // Small products are bound by what is not overlapped: launch and allocation (2.5 us), the first copies, the
 // last tile's epilogue (1 to 5 us).
 //
-// Every wait gives up after a second (that for a sum's end later, by the sum's length); the kernel then sets its status bit, lets its
-// copies land, frees its tensor memory and returns.
+// Every wait on an mbarrier gives up after a second (that for a sum's end later, by the sum's length); the kernel then
+// sets its status bit, lets its copies land, frees its tensor memory and returns.  The allocation of tensor memory, which
+// waits for earlier kernels on the SM, and the barriers of the pair have no form with a limit: what keeps the pair
+// together there is that each CTA reaches all of them, since its other waits end.
 #pragma once
 
 #include <cuda.h>

@@ -178,9 +178,9 @@ int gated_act_last_cuda_error(void);
 /*
  * Device-side status of the library's kernels on the current device since
  * the last call, then cleared.  *flags bit 0: a kernel's bounded wait (1 s)
- * for one of its own bulk copies (or, in the products of gated_act_linear.h,
- * for copies, products or its own warps) gave up; the rows or tiles that CTA had
- * not finished were left unwritten.  No other bit is used.  Synchronizes the device
+ * for one of its own bulk copies (or, in the products of gated_act_linear.h, which
+ * say how long, for copies, products or its own warps) gave up; the rows or tiles
+ * that CTA had not finished were left unwritten.  No other bit is used.  Synchronizes the device
  * (it copies a status word), so call it outside stream capture.
  */
 int gated_act_device_status(unsigned int *flags);

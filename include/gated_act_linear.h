@@ -16,8 +16,13 @@
  *     GATED_ACT_ERR_HOST): the operands are read many times;
  *   - rows whose base and strides are multiples of 16 bytes are read in place; others
  *     are first copied into the workspace, whose size depends on that.
- * A wait inside a kernel that does not end within a second sets bit 0 of
- * gated_act_device_status, and the call's outputs are then undefined.
+ * The kernels wait inside for copies, products and their own warps.  Such a wait gives up
+ * after a second by the clock (for the end of a sum of n terms after n x 0.3 us more); the kernel
+ * then sets bit 0 of gated_act_device_status and ends, and the outputs of the call, which returned
+ * GATED_ACT_OK long before, and of what was computed from them are undefined.  A kernel that
+ * something else holds up for that long (pages of managed memory on their way, another process's
+ * time slice) gives up as well.  Two waits have no limit: for tensor memory, until the kernels that
+ * hold it on the same SM have ended, and those of a pair of blocks for each other.
  */
 #ifndef GATED_ACT_LINEAR_H
 #define GATED_ACT_LINEAR_H
@@ -37,7 +42,8 @@ typedef struct gated_act_linear {
     const void *weight;     /* [E, 2d, k], gate rows [0, d), up rows [d, 2d)           */
     int64_t E, T, k, d;
     int64_t in_stride;      /* >= k                                                    */
-    int64_t in_batch;       /* >= (T - 1) in_stride + k, where E > 1                   */
+    int64_t in_batch;       /* >= (T - 1) in_stride + k, where E > 1: rows that all experts
+                               share (0) are refused, GATED_ACT_ERR_STRIDE; so is a shared weight */
     int64_t weight_stride;  /* >= k                                                    */
     int64_t weight_batch;   /* >= (2d - 1) weight_stride + k, where E > 1              */
     int dtype;
@@ -57,6 +63,10 @@ typedef struct gated_act_linear {
  * rint(|v| 2^-k) <= 32767.  A block that holds an infinity or a NaN has e = 255 and
  * q = 0 and stands for NaN.  (Why not the element type: bf16's 8 bits would add an error
  * of the gradients' own rounding to each factor that they are computed from.)
+ * What one scale for 32 means: a code is off by up to 2^-15 of its block's largest magnitude.  An
+ * element r times smaller than that is off by up to r 2^-15 of itself, past r = 128 more than in
+ * bf16: one of the 32 that is 1000 times the others leaves these up to 3% off, in the factors of
+ * the gradients of their own columns alone.
  * ------------------------------------------------------------------------ */
 
 /* Bytes of workspace that the forward pass needs. */
@@ -74,7 +84,8 @@ int linear_silu_and_mul(void *out, int16_t *codes, uint8_t *scales, const gated_
 int linear_gelu_and_mul(void *out, int16_t *codes, uint8_t *scales, const gated_act_linear *a,
                         void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
-/* Bytes of workspace that the backward pass needs. */
+/* Bytes of workspace that the backward pass needs: dg and du (4 E T d), where n_rows are given 64 rows of k
+ * for each expert, where few long sums of grad_in are split these in fp32, and the copies of operands. */
 size_t linear_and_mul_backward_workspace_bytes(const gated_act_linear *a);
 
 /*
@@ -113,12 +124,19 @@ typedef struct gated_act_vocabulary {
     int targets64;          /* 0: int32 targets, else int64             */
 } gated_act_vocabulary;
 
+/* Bytes of workspace that the forward pass needs: T V / 16 (up to 128 tokens T V / 4), the live rows (2 T k), and
+ * the copy of a weight that is not read in place. */
 size_t linear_cross_entropy_workspace_bytes(const gated_act_vocabulary *a);
 
 /*   loss, lse  [T] fp32. */
 int linear_cross_entropy(float *loss, float *lse, const gated_act_vocabulary *a, void *workspace,
                          size_t workspace_bytes, cudaStream_t stream);
 
+/* Bytes of workspace that the backward pass needs: grad_in's sums in fp32 (4 T k; few rows, up to 32 times that), the
+ * rows with and without their slopes (4 T k), a piece of the vocabulary's y, and the copy of a weight that is
+ * not read in place.  A piece's y takes about 256 MB up to 16384 tokens; past that a piece keeps 8192
+ * columns (a quarter more at most), and y grows with the tokens as the other parts do, 16 KB a token: 1 GB at
+ * 65536 of them. */
 size_t linear_cross_entropy_backward_workspace_bytes(const gated_act_vocabulary *a);
 
 /*
