@@ -120,7 +120,7 @@ def test_small_losses_keep_their_bits(ga, k, tokens, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("tokens", [60, 500])
-@pytest.mark.parametrize("k", [64, 500, 1000, 2048, 4096, 10000])
+@pytest.mark.parametrize("k", [64, 500, 1000, 2048, 4096, 10000, 100001])
 def test_losses_in_norm(ga, k, tokens, dtype):
     """Dense rows.  The tensor cores cut fp32 sums off towards 0 after every 16 terms, half a unit of
     the sum on average: over k terms 1.3e-9 k of a logit (24 bits, sums half of the last one on average,
@@ -360,3 +360,71 @@ def test_an_outlier_among_32_columns(ga, dtype):
     far = [i for i in range(d) if i // 32 not in (0, 1)]
     assert (off[far + [d + i for i in far]] <= 2 * torch.finfo(dtype).eps / 2).all()
     assert (off <= 0.03 + torch.finfo(dtype).eps).all()
+
+
+# ------------------------------------------------------------ fp16, used as one
+
+def _step(ga, x, w, head, goal, gl):
+    """A gated block, its loss and all gradients."""
+    y, kept = ga.linear_gelu_and_mul(x, w, keep=True)
+    ce = ga.linear_cross_entropy(y, head, goal)
+    gy, ghead = ga.linear_cross_entropy_backward(gl, y, head, goal, ce)
+    return (y, ce.loss, ghead) + ga.linear_gelu_and_mul_backward(gy, x, w, kept)
+
+
+def test_captured_and_overlapping_in_fp16(ga):
+    """The passes that find the powers of two, in a graph replayed with larger and smaller inputs than it was captured
+    with, and in calls on two streams at once."""
+    x = _randn(300, 700, seed=1).to(F16)
+    w = _randn(2 * 90, 700, seed=2, scale=700 ** -0.5).to(F16)
+    head = _randn(500, 90, seed=3, scale=0.5).to(F16)
+    goal = torch.randint(500, (300,), generator=_gen(4), device="cuda")
+    goal[::7] = -100
+    gl = torch.full((300,), 4.0, device="cuda")
+    inputs = [x, (x * 2.0 ** -6), (x * 8)]
+    now = x.clone()
+    want = []
+    for v in inputs:
+        now.copy_(v)
+        want.append([t.clone() for t in _step(ga, now, w, head, goal, gl)])
+    now.copy_(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = _step(ga, now, w, head, goal, gl)
+    for i in (1, 2, 0, 1):
+        now.copy_(inputs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want[i])), i
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i, _step(ga, inputs[i], w, head, goal, gl)))
+    torch.cuda.synchronize()
+    for i, result in got:
+        assert all(torch.equal(a, b) for a, b in zip(result, want[i]))
+
+
+def test_many_tokens_in_fp16(ga):
+    """More tokens than the first pass has warps, and experts more than SMs."""
+    x = _randn(20001, 40, seed=1).to(F16)
+    w = _randn(50, 40, seed=2, scale=0.3).to(F16)
+    goal = torch.randint(-20, 50, (20001,), generator=_gen(3), device="cuda")
+    gl = 64 * torch.rand(20001, generator=_gen(4), device="cuda")
+    live = goal >= 0
+    kept = ga.linear_cross_entropy(x, w, goal)
+    gi, gw = ga.linear_cross_entropy_backward(gl, x, w, goal, kept)
+    (ri, bi), (rw, bw) = R.entropy_backward(gl[live].double(), x[live].double(), w.double(), goal[live], F16)
+    R.check(gi[live], ri, bi, "grad_in")
+    R.check(gw, rw, bw, "grad_weight")
+    e, m, k, d = 400, 5, 24, 41
+    x, w, dy = (_randn(*n, seed=i).to(F16) for i, n in enumerate(((e, m, k), (e, 2 * d, k), (e, m, d))))
+    n_rows = torch.arange(e, dtype=torch.int32, device="cuda") % 6
+    gi, gw = _gated(ga, "silu", x, w, dy, n_rows)
+    for i in range(0, e, 7):
+        n = i % 6
+        for got, (ref, bound) in zip((gi[i, :n], gw[i]),
+                                     R.backward("silu", dy[i, :n].double(), x[i, :n].double(), w[i].double(), F16)):
+            R.check(got, ref, bound, f"expert {i}")
