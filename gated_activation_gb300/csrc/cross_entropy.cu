@@ -99,8 +99,8 @@ __device__ __forceinline__ int block_sum_int(int v, int *red) {
 
 // fp16: the largest finite |f x| of the live tokens, one of each block.  Below a power of two above every |f| alone, f x
 // left fp16's upper binades empty, and a token whose slope is 2^-14 of the largest lost bits to the type's lower end
-// (its remainder all of them); next to the largest |f x|, 2^-29.  bf16 has fp32's range.  One pass over the rows
-// (a step of 777 tokens of 1001 over 50001 takes 343 us with it and without).
+// (its remainder all of them); next to the largest |f x|, 2^-29.  bf16 has fp32's range.  One pass over the rows,
+// read as the aligned vectors that hold them (a step of 777 tokens of 1001 over 50001 takes 4.4 us more with it, 348).
 constexpr int kTops = 1024;
 __global__ void __launch_bounds__(256) slope_tops(TokenArgs<f16> g, float *tops) {
     __shared__ float red[8];
@@ -115,20 +115,14 @@ __global__ void __launch_bounds__(256) slope_tops(TokenArgs<f16> g, float *tops)
         if (!(f < INFINITY))   // an infinity or a NaN, whatever it is divided by
             continue;
         const f16 *row = g.in + i * g.in_stride;
-        const bool vec = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
-        uint32_t most = 0;   // magnitudes of one type order as their bits
+        float most = 0.f;
+        const int before = before_row(row);
 #pragma unroll 4
-        for (int c = lane * 8; c < g.k; c += 256) {
-            const uint4 v = eight(row + c, g.k - c, vec);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t lo = (&v.x)[q] & 0x7FFFu, hi = (&v.x)[q] >> 16 & 0x7FFFu;
-                most = max(most, max(lo < 0x7C00u ? lo : 0u, hi < 0x7C00u ? hi : 0u));
-            }
-        }
-        most = __reduce_max_sync(0xFFFFFFFFu, most);
-        top = fmaxf(top, fminf(f * __half2float(__ushort_as_half(static_cast<unsigned short>(most))), FLT_MAX));
+        for (int c = lane * 8 - before; c < g.k; c += 256)
+            most = fmaxf(most, top_of_eight(eight_around(row, c, g.k)));
+        top = fmaxf(top, fminf(f * most, FLT_MAX));
     }
+    top = __int_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_int(top)));   // top >= 0
     if (lane == 0)
         red[warp] = top;
     __syncthreads();

@@ -347,19 +347,18 @@ __global__ void __launch_bounds__(256) gradient_tops(GateGradArgs<f16> g) {
     for (int64_t item = blockIdx.x * 8 + warp; item < items; item += gridDim.x * 8) {
         const int i = static_cast<int>(item / pieces), piece = static_cast<int>(item - int64_t(i) * pieces);
         const f16 *grad = g.grad + e * g.grad_batch + i * g.grad_stride;
-        const int before = static_cast<int>(reinterpret_cast<uintptr_t>(grad) & 15) / 2;
+        const int before = before_row(grad);
         const uint8_t *scale = g.scales + (int64_t(e) * g.T_ + i) * 2 * blocks;
         uint4 v[4];
         float step[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = (piece * kTopVectors + 32 * j + lane) * 8 - before;   // of the vector's first element
-            v[j] = make_uint4(0, 0, 0, 0);
+            v[j] = eight_around(grad, c, g.d);
             step[j] = 0.f;
             if (c >= g.d || c + 8 <= 0)
                 continue;
             const int first = max(c, 0), last = min(c + 8, g.d) - 1;
-            v[j] = c >= 0 && c + 8 <= g.d ? ld_stream(grad + c) : eight(grad + first, last + 1 - first, false);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {   // a NaN's block is NaN whatever it is divided by
                 const int b = (q ? last : first) / kBlock;
@@ -369,16 +368,8 @@ __global__ void __launch_bounds__(256) gradient_tops(GateGradArgs<f16> g) {
             }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t most = 0;   // magnitudes of one type order as their bits; infinities and NaN stay what they are
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t lo = (&v[j].x)[q] & 0x7FFFu, hi = (&v[j].x)[q] >> 16 & 0x7FFFu;
-                most = max(most, max(lo < 0x7C00u ? lo : 0u, hi < 0x7C00u ? hi : 0u));
-            }
-            const float dy = __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
-            top = fmaxf(top, fminf(dy * step[j] * 32768.f, FLT_MAX));
-        }
+        for (int j = 0; j < 4; ++j)   // infinities and NaN stay what they are
+            top = fmaxf(top, fminf(top_of_eight(v[j]) * step[j] * 32768.f, FLT_MAX));
     }
     const int bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_int(top));   // top >= 0
     if (lane == 0)

@@ -681,6 +681,28 @@ template <class T> __device__ __forceinline__ uint4 eight(const T *p, int n, boo
     return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
 }
 
+// The same of columns [c, c + 8) of a row of n, where `row + c` is a multiple of 16 bytes: zeros outside of the row.
+template <class T> __device__ __forceinline__ uint4 eight_around(const T *row, int c, int n) {
+    if (c >= 0 && c + 8 <= n)
+        return ld_stream(row + c);
+    const int first = max(c, 0), last = min(c + 8, n);
+    return first < last ? eight(row + first, last - first, false) : make_uint4(0, 0, 0, 0);
+}
+// The elements of a row's first such vector that lie in front of the row.
+template <class T> __device__ __forceinline__ int before_row(const T *row) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15) / static_cast<int>(sizeof(T));
+}
+// The largest finite magnitude of eight fp16 elements.  Magnitudes of one type order as their bits.
+__device__ __forceinline__ float top_of_eight(uint4 v) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t lo = (&v.x)[q] & 0x7FFFu, hi = (&v.x)[q] >> 16 & 0x7FFFu;
+        most = max(most, max(lo < 0x7C00u ? lo : 0u, hi < 0x7C00u ? hi : 0u));
+    }
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
+}
+
 template <class T> __device__ __forceinline__ uint32_t pack2(float2 v);
 template <> __device__ __forceinline__ uint32_t pack2<bf16>(float2 v) { return pack_bf16x2(v.x, v.y); }
 template <> __device__ __forceinline__ uint32_t pack2<f16>(float2 v) {
